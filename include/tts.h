@@ -48,7 +48,7 @@ typedef enum {
   TTS_ERR_WORKSPACE = 6       /* workspace missing or smaller than required */
 } tts_status;
 
-typedef enum { TTS_BF16 = 0, TTS_F32 = 1 } tts_dtype;
+typedef enum { TTS_BF16 = 0, TTS_F32 = 1, TTS_E4M3 = 2 /* KV caches only */ } tts_dtype;
 
 /* Bits a kernel ORs into *dev_status. */
 #define TTS_DEV_INDEX_RANGE 0x1u
@@ -324,6 +324,120 @@ tts_status tts_attn_fwd_varlen_fp8(const void* q8, const float* q_scale, const v
                                    int32_t causal, float scale, float* out, float* lse,
                                    void* workspace, size_t workspace_bytes,
                                    uint32_t* dev_status, void* stream);
+
+/*
+ * Grouped-query KV cache: append of new tokens, the position rotation applied on the way.
+ *
+ * The write path of the serving loop around the prefill above: "从 SGLang Kernel源码到 GPU
+ * Trace" rotates q and k from a precomputed cos/sin table (section 3.3) and keeps the keys
+ * and values in a page-table-managed cache (section 2.2, PagedKVCache); "AMD
+ * MI250部署DeepSeek-V4-Flash" quantizes by blocks (section 5.3). The pages fix neither the
+ * cache's layout nor its 8-bit format; the reading taken:
+ *
+ *   k_cache, v_cache  device [num_pages, num_heads_kv, page_size, head_dim], bf16 or e4m3
+ *                     codes (one byte); page_size 16, 32, 64 or 128
+ *   k_scale, v_scale  device fp32 [num_pages, num_heads_kv], e4m3 caches only: a cached value
+ *                     is code * scale of its page and head. Scales written here are powers of
+ *                     two: the smallest s >= 2^-60 with |x| <= 448 s for all rows of the page.
+ *
+ * Request r appends n_r = cu_new[r+1] - cu_new[r] tokens behind its past_lens[r] cached ones:
+ * token i has position past_lens[r] + i, lands in page page_tables[r, pos / page_size] at
+ * slot pos % page_size, and is rotated as in tts_qkv_rope (pairs (j, j + head_dim / 2),
+ * cos_sin[pos]; in fp32, each product and sum rounded; cos_sin NULL: no rotation).
+ *   q_out[t] = bf16(R q[t])    k_out[t] = bf16(R k[t])    k row = R k[t]    v row = v[t]
+ * A bf16 cache takes the rows rounded to nearest even. An e4m3 cache takes e4m3(x / s)
+ * (nearest even, saturating; s ignores non-finite x). A page whose first slot is written by
+ * this call takes s from the new rows alone (what it held before is forgotten); a page that
+ * already holds rows of the request keeps its s if the new rows fit and else grows it, and the
+ * codes of its earlier rows become e4m3(code * s_old / s_new). Slots behind the last appended
+ * token keep their bytes; they are past the end.
+ *
+ * q, k, v     device bf16, token t's heads at q + t * q_stride (in values; head h at + h *
+ *             head_dim), so they may be views of one packed projection. q may be NULL (then
+ *             q_out, num_heads_q and q_stride are not looked at).
+ * total_new   rows of q / k / v; max_new: host upper bound of n_r (it chooses the kernel; a
+ *             longer request is flagged TTS_DEV_BAD_ARG and skipped, like entries of cu_new
+ *             that decrease or leave [0, total_new])
+ * cu_new      device int32 [batch + 1];  past_lens device int32 [batch]
+ * cos_sin     device fp32 [max_pos, head_dim / 2, 2] of tts_rope_cache, or NULL
+ * page_tables device int32 [batch, max_pages]
+ * q_out       device bf16 [total_new, num_heads_q, head_dim];  k_out device bf16
+ *             [total_new, num_heads_kv, head_dim] or NULL (the rotated keys for the prefill's
+ *             attention). Neither may overlap q, k or v.
+ * A request whose positions do not fit [0, max_pages * page_size) (or max_pos with a table)
+ * is not cached, its q_out / k_out rows are zeros, and TTS_DEV_INDEX_RANGE is set; a page
+ * outside [0, num_pages) takes no rows and sets the same bit. A partly filled page whose scale
+ * is not a positive finite number is treated as new and sets TTS_DEV_BAD_ARG. Two requests
+ * of one call must not append to the same page (what it then holds is unspecified). Rows
+ * of q_out / k_out outside every request are left as they were.
+ *
+ * cache_dtype TTS_BF16 or TTS_E4M3; head_dim 64 or 128, other page sizes or head_dims:
+ * TTS_ERR_UNSUPPORTED. Strides are multiples of 8 and at least heads * head_dim; q, k, v,
+ * the caches, q_out, k_out and cos_sin are 16-byte aligned. One launch, nothing allocated.
+ */
+tts_status tts_rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads_q, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride,
+                              int64_t total_new, const int32_t* cu_new, const int32_t* past_lens,
+                              int32_t batch, int32_t max_new, int32_t num_heads_kv,
+                              int32_t head_dim, const float* cos_sin, int32_t max_pos,
+                              const int32_t* page_tables, int32_t max_pages, void* k_cache,
+                              void* v_cache, float* k_scale, float* v_scale,
+                              tts_dtype cache_dtype, int32_t num_pages, int32_t page_size,
+                              void* q_out, void* k_out, uint32_t* dev_status, void* stream);
+
+/*
+ * Attention of each request's newest tokens over the cache of tts_rope_kv_append: the decode
+ * step (one token per request) and steps of a few tokens (drafts to verify), with an optional
+ * sliding window and first tokens that stay visible.
+ *
+ * Same sequences and statistics as tts_attn_fwd_varlen (FP32 softmax and accumulation), read
+ * through page tables as in tts_sparse_attn_decode, dense. Request r's n_r query tokens
+ * (rows cu_seqlens_q[r] .. of q; cu_seqlens_q NULL: row r) are its last ones: with L =
+ * kv_lens[r] cached tokens, token i sits at position P = L - n_r + i and sees key j iff
+ *   j <= P  and  (window = 0  or  j > P - window  or  j < sinks).
+ *   s_j = scale * k_scale[page(j), g] * q[i, h, :] . k_code[j, g, :],   g = h / (Hq / Hkv)
+ *   out[i, h, :] = sum_j softmax(s)_j v_scale[page(j), g] v_code[j, g, :]
+ *   lse[i, h] = ln sum_j e^{s_j}
+ * A row that sees no key gets out = 0, lse = -inf. Products are fp16 x fp16 for e4m3 codes
+ * (codes exact; q exact after a power-of-two row scaling, down to 2^-22 of the row's largest
+ * value; weights rounded to 11 bits) and bf16 x bf16 for a bf16 cache (weights rounded to
+ * bf16), accumulated in fp32. Cached values that some new token of the request sees must be
+ * finite; what the page holds behind the last token or outside the window is never used,
+ * and pages without a visible key are not read (their table entries may be anything).
+ *
+ * q           device bf16 [total_q, num_heads_q, head_dim]; rows outside every request are
+ *             not read, and their out / lse rows are left as they were
+ * max_seqlen_q  host upper bound of n_r, 1 .. 64 (longer: TTS_ERR_UNSUPPORTED; prompts go
+ *             through tts_attn_fwd_varlen_window); a longer request is flagged and skipped
+ * k_cache .. page_size, page_tables, max_pages: as tts_rope_kv_append. k_scale / v_scale may
+ *             hold any positive finite values (others: TTS_DEV_BAD_ARG, the page's keys are
+ *             skipped); NULL for a bf16 cache.
+ * kv_lens     device int32 [batch], the new tokens included; an entry outside
+ *             [0, max_pages * page_size] reads as 0 and sets TTS_DEV_INDEX_RANGE, and so
+ *             does a page outside [0, num_pages) with visible keys, which are skipped
+ * window >= 0, sinks >= 0 (not looked at when window = 0)
+ * out         device fp32 or bf16 (out_dtype) [total_q, num_heads_q, head_dim]; lse device
+ *             fp32 [total_q, num_heads_q] or NULL
+ * workspace   device scratch of at least tts_attn_decode_workspace_bytes(...) bytes, 16-byte
+ *             aligned, owned by the caller, not shared by calls that may overlap; nothing in
+ *             it needs to be initialised. Missing or smaller: TTS_ERR_WORKSPACE.
+ * head_dim 64 or 128, page_size 16, 32, 64 or 128 (else TTS_ERR_UNSUPPORTED); q, caches and out
+ * 16-byte aligned. Results are bitwise reproducible, but the split of the keys over CTAs, and
+ * so the rounding of a request's result, depends on the whole batch's lengths.
+ */
+size_t tts_attn_decode_workspace_bytes(int32_t max_seqlen_q, int32_t num_heads_q,
+                                       int32_t num_heads_kv, int32_t head_dim);
+
+tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* cu_seqlens_q,
+                                 int32_t batch, int32_t max_seqlen_q, int32_t num_heads_q,
+                                 int32_t num_heads_kv, int32_t head_dim, const void* k_cache,
+                                 const void* v_cache, const float* k_scale, const float* v_scale,
+                                 tts_dtype cache_dtype, int32_t num_pages, int32_t page_size,
+                                 const int32_t* page_tables, int32_t max_pages,
+                                 const int32_t* kv_lens, int32_t window, int32_t sinks,
+                                 float scale, void* out, tts_dtype out_dtype, float* lse,
+                                 void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                 void* stream);
 
 /*
  * cos/sin table of rotary position embedding, built once and read by tts_qkv_rope.

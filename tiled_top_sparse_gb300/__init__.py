@@ -13,6 +13,12 @@ no fallback: if the library is missing or fails to load, calls raise.
     attn_fwd_varlen_fp8(q8, q_scale, k8, k_scale, v, cu_seqlens_q, cu_seqlens_k,
                         max_seqlen_q, max_seqlen_k, causal, scale, out=None, lse=None,
                         workspace=None, status=None)
+    rope_kv_append(k, v, k_cache, v_cache, page_tables, past_lens, cu_new, max_new,
+                   k_scale=None, v_scale=None, cos_sin=None, q=None, q_out=None, k_out=None,
+                   status=None)
+    attn_decode_paged(q, k_cache, v_cache, page_tables, kv_lens, scale, cu_seqlens_q=None,
+                      max_seqlen_q=1, k_scale=None, v_scale=None, window=0, sinks=0, out=None,
+                      lse=None, workspace=None, status=None)
     rope_cache(max_pos, rot_dim, base=10000.0, out=None, device=None)
     qkv_rope(x, w, bias, positions, cos_sin, num_heads, q=None, k=None, v=None,
              status=None)
@@ -40,6 +46,7 @@ TTS_ERR_DEVICE_TIMEOUT = 5
 TTS_ERR_WORKSPACE = 6
 TTS_BF16 = 0
 TTS_F32 = 1
+TTS_E4M3 = 2
 TTS_DEV_INDEX_RANGE = 0x1
 TTS_DEV_TIMEOUT = 0x2
 TTS_DEV_BAD_ARG = 0x4
@@ -59,6 +66,9 @@ EXPORTED = (
     "tts_paged_kv_write",
     "tts_quantize_fp8_prefill",
     "tts_attn_fwd_varlen_fp8",
+    "tts_rope_kv_append",
+    "tts_attn_decode_workspace_bytes",
+    "tts_attn_decode_paged",
     "tts_rope_cache",
     "tts_qkv_rope",
     "tts_attn_fwd_varlen_f32_noalloc",
@@ -116,6 +126,15 @@ def lib() -> ctypes.CDLL:
     L.tts_attn_fwd_varlen_fp8.argtypes = [P, P, P, P, P, i64, i64, P, P, i32, i32, i32, i32,
                                           i32, i32, i32, f32, P, P, P, ctypes.c_size_t, P, P]
     L.tts_attn_fwd_varlen_fp8.restype = ctypes.c_int
+    L.tts_rope_kv_append.argtypes = [P, i64, i32, P, i64, P, i64, i64, P, P, i32, i32, i32, i32, P,
+                                     i32, P, i32, P, P, P, P, ctypes.c_int, i32, i32, P, P, P, P]
+    L.tts_rope_kv_append.restype = ctypes.c_int
+    L.tts_attn_decode_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.tts_attn_decode_workspace_bytes.restype = ctypes.c_size_t
+    L.tts_attn_decode_paged.argtypes = [P, i64, P, i32, i32, i32, i32, i32, P, P, P, P,
+                                        ctypes.c_int, i32, i32, P, i32, P, i32, i32, f32, P,
+                                        ctypes.c_int, P, P, ctypes.c_size_t, P, P]
+    L.tts_attn_decode_paged.restype = ctypes.c_int
     L.tts_rope_cache.argtypes = [i32, i32, f32, P, P]
     L.tts_rope_cache.restype = ctypes.c_int
     L.tts_qkv_rope.argtypes = [P, i64, i32, P, P, P, P, i32, i32, i32, P, P, P, P, P]
@@ -478,4 +497,137 @@ def attn_fwd_varlen_fp8(q8, q_scale, k8, k_scale, v, cu_seqlens_q, cu_seqlens_k,
         hkv, d, int(bool(causal)), float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(status), _stream(q8.device))
     _check(code, "tts_attn_fwd_varlen_fp8")
+    return out, lse
+
+
+def _token_rows(t, name):
+    """[tokens, heads, head_dim] bf16 whose heads are contiguous; returns the token stride.
+    Views of a packed projection pass without a copy."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3,
+          f"{name} must be a CUDA bf16 tensor [tokens, heads, head_dim]")
+    s = t.stride()
+    _need(s[2] == 1 and (s[1] == t.shape[2] or t.shape[1] == 1),
+          f"{name}: the heads of a token must be contiguous")
+    return s[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks a grouped-query cache and returns its dtype code."""
+    f8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _cuda_contig(t, n)
+        _need(t.dim() == 4 and t.dtype == k_cache.dtype and (f8 or t.dtype == torch.bfloat16),
+              f"{n} must be [pages, heads_kv, page_size, head_dim] in bf16, or uint8 / "
+              "float8_e4m3fn codes")
+    _need(k_cache.shape == v_cache.shape, "k_cache and v_cache must have the same shape")
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need((t is not None) == f8, f"{n} goes with an e4m3 cache")
+        if f8:
+            _cuda_contig(t, n, torch.float32)
+            _need(tuple(t.shape) == tuple(k_cache.shape[:2]), f"{n} must be [pages, heads_kv]")
+    return TTS_E4M3 if f8 else TTS_BF16
+
+
+def rope_kv_append(k, v, k_cache, v_cache, page_tables, past_lens, cu_new, max_new, k_scale=None,
+                   v_scale=None, cos_sin=None, q=None, q_out=None, k_out=None, status=None,
+                   want_k=False):
+    """Append new tokens to a paged grouped-query cache, rotating q and k (tts_rope_kv_append).
+
+    k, v bf16 [tokens, Hkv, d] and q [tokens, Hq, d] or None (views of a packed projection are
+    taken as they are), caches [pages, Hkv, page_size, d] in bf16 or e4m3 codes (uint8 or
+    float8_e4m3fn) with scales fp32 [pages, Hkv], page_tables int32 [batch, max_pages], past_lens
+    int32 [batch], cu_new int32 [batch + 1], cos_sin of rope_cache or None (no rotation). The
+    caches and scales are written in place. Returns (q_out bf16 [tokens, Hq, d] or None, k_out
+    bf16 [tokens, Hkv, d]; k_out is None unless given or asked for with want_k)."""
+    code = _cache(k_cache, v_cache, k_scale, v_scale)
+    pages, hkv, ps, d = k_cache.shape
+    ks, vs = _token_rows(k, "k"), _token_rows(v, "v")
+    total = k.shape[0]
+    _need(k.shape == v.shape and tuple(k.shape[1:]) == (hkv, d), "k, v [tokens, Hkv, d]")
+    _cuda_contig(page_tables, "page_tables", torch.int32)
+    _cuda_contig(past_lens, "past_lens", torch.int32)
+    _cuda_contig(cu_new, "cu_new", torch.int32)
+    batch = past_lens.numel()
+    _need(page_tables.dim() == 2 and page_tables.shape[0] == batch and
+          cu_new.numel() == batch + 1, "page_tables [batch, max_pages], cu_new [batch + 1]")
+    max_pos = 0
+    if cos_sin is not None:
+        _cuda_contig(cos_sin, "cos_sin", torch.float32)
+        _need(cos_sin.dim() == 3 and tuple(cos_sin.shape[1:]) == (d // 2, 2),
+              "cos_sin must be [max_pos, head_dim/2, 2]")
+        max_pos = cos_sin.shape[0]
+    hq, qs = 0, 0
+    if q is not None:
+        qs = _token_rows(q, "q")
+        hq = q.shape[1]
+        _need(q.shape[0] == total and q.shape[2] == d, "q [tokens, Hq, d]")
+        if q_out is None:
+            q_out = torch.empty((total, hq, d), dtype=torch.bfloat16, device=q.device)
+        _cuda_contig(q_out, "q_out", torch.bfloat16)
+        _need(q_out.shape == q.shape, "q_out shape")
+    else:
+        _need(q_out is None, "q_out goes with q")
+    if k_out is None and want_k:
+        k_out = torch.empty((total, hkv, d), dtype=torch.bfloat16, device=k.device)
+    if k_out is not None:
+        _cuda_contig(k_out, "k_out", torch.bfloat16)
+        _need(k_out.shape == k.shape, "k_out shape")
+    _check(lib().tts_rope_kv_append(
+        _ptr(q), qs, hq, _ptr(k), ks, _ptr(v), vs, total, _ptr(cu_new), _ptr(past_lens), batch,
+        int(max_new), hkv, d, _ptr(cos_sin), max_pos, _ptr(page_tables), page_tables.shape[1],
+        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code, pages, ps, _ptr(q_out),
+        _ptr(k_out), _ptr(status), _stream(k.device)), "tts_rope_kv_append")
+    return q_out, k_out
+
+
+def attn_decode_workspace_bytes(max_seqlen_q, num_heads_q, num_heads_kv, head_dim) -> int:
+    return int(lib().tts_attn_decode_workspace_bytes(int(max_seqlen_q), int(num_heads_q),
+                                                     int(num_heads_kv), int(head_dim)))
+
+
+def attn_decode_paged(q, k_cache, v_cache, page_tables, kv_lens, scale, cu_seqlens_q=None,
+                      max_seqlen_q=1, k_scale=None, v_scale=None, window=0, sinks=0, out=None,
+                      lse=None, workspace=None, status=None, want_lse=True,
+                      out_dtype=torch.float32):
+    """Attention of each request's newest tokens over a paged grouped-query cache
+    (tts_attn_decode_paged).
+
+    q bf16 [tokens, Hq, d] (one token per request without cu_seqlens_q), the cache as in
+    rope_kv_append, kv_lens int32 [batch] with the new tokens counted. window > 0: a token sees
+    the last `window` positions up to its own and the first `sinks`. Returns (out [tokens, Hq, d]
+    in out_dtype, or in out's dtype: fp32 or bf16; lse fp32 [tokens, Hq])."""
+    code = _cache(k_cache, v_cache, k_scale, v_scale)
+    pages, hkv, ps, d = k_cache.shape
+    _cuda_contig(q, "q", torch.bfloat16)
+    _need(q.dim() == 3 and q.shape[2] == d, "q [tokens, Hq, d]")
+    total, hq = q.shape[:2]
+    _cuda_contig(page_tables, "page_tables", torch.int32)
+    _cuda_contig(kv_lens, "kv_lens", torch.int32)
+    batch = kv_lens.numel()
+    _need(page_tables.dim() == 2 and page_tables.shape[0] == batch, "page_tables [batch, max_pages]")
+    if cu_seqlens_q is not None:
+        _cuda_contig(cu_seqlens_q, "cu_seqlens_q", torch.int32)
+        _need(cu_seqlens_q.numel() == batch + 1, "cu_seqlens_q [batch + 1]")
+    else:
+        _need(total == batch, "q has one token per request without cu_seqlens_q")
+    if out is None:
+        out = torch.empty((total, hq, d), dtype=out_dtype, device=q.device)
+    _cuda_contig(out, "out")
+    _need(out.dtype in (torch.float32, torch.bfloat16) and out.shape == q.shape,
+          "out must be fp32 or bf16 [tokens, Hq, d]")
+    if lse is None and want_lse:
+        lse = torch.empty((total, hq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _cuda_contig(lse, "lse", torch.float32)
+        _need(tuple(lse.shape) == (total, hq), "lse shape")
+    need = attn_decode_workspace_bytes(max_seqlen_q, hq, hkv, d)
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _check(lib().tts_attn_decode_paged(
+        _ptr(q), total, _ptr(cu_seqlens_q), batch, int(max_seqlen_q), hq, hkv, d, _ptr(k_cache),
+        _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code, pages, ps, _ptr(page_tables),
+        page_tables.shape[1], _ptr(kv_lens), int(window), int(sinks), float(scale), _ptr(out),
+        TTS_BF16 if out.dtype == torch.bfloat16 else TTS_F32, _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(status), _stream(q.device)),
+        "tts_attn_decode_paged")
     return out, lse

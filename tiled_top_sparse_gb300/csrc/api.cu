@@ -60,6 +60,18 @@ inline tts_status from_cuda(cudaError_t e) {
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 constexpr size_t kCounterBytes = 256;  // attention workspace: work-item counter
+constexpr int kDecodeMaxQ = 64;        // new tokens per request of tts_attn_decode_paged
+
+// Shapes of the grouped-query cache that the append and decode kernels are built for; a
+// request's positions and the cache's rows stay below 2^30, so that sums of a position, a
+// window and a tile stay in 32 bits.
+inline bool cache_shape_built(int32_t d, int32_t page_size, int32_t num_pages, int32_t max_pages,
+                              int32_t hkv) {
+  return (d == 64 || d == 128) &&
+         (page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128) &&
+         (int64_t)max_pages * page_size <= (int64_t(1) << 30) &&
+         (int64_t)num_pages * hkv <= 0x7FFFFFFFLL;
+}
 
 }  // namespace
 
@@ -391,6 +403,155 @@ tts_status tts_attn_fwd_varlen_fp8(const void* q8, const float* q_scale, const v
   a.dev_status = dev_status;
   int drv = 0;
   cudaError_t e = launch_attn_fwd(a, &drv, static_cast<cudaStream_t>(stream));
+  if (drv != 0) return TTS_ERR_CUDA;
+  return from_cuda(e);
+}
+
+tts_status tts_rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads_q, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride,
+                              int64_t total_new, const int32_t* cu_new, const int32_t* past_lens,
+                              int32_t batch, int32_t max_new, int32_t num_heads_kv,
+                              int32_t head_dim, const float* cos_sin, int32_t max_pos,
+                              const int32_t* page_tables, int32_t max_pages, void* k_cache,
+                              void* v_cache, float* k_scale, float* v_scale,
+                              tts_dtype cache_dtype, int32_t num_pages, int32_t page_size,
+                              void* q_out, void* k_out, uint32_t* dev_status, void* stream) {
+  if (total_new < 0 || batch < 1 || max_new < 0 || num_heads_kv < 1 || head_dim < 1 ||
+      max_pages < 1 || num_pages < 1 || page_size < 1)
+    return TTS_ERR_INVALID_ARG;
+  if (cache_dtype != TTS_BF16 && cache_dtype != TTS_E4M3) return TTS_ERR_INVALID_ARG;
+  if (!cache_shape_built(head_dim, page_size, num_pages, max_pages, num_heads_kv))
+    return TTS_ERR_UNSUPPORTED;
+  if (total_new > 0x7FFFFF00LL || (int64_t)num_heads_kv * head_dim > 0x7FFFFFFFLL)
+    return TTS_ERR_UNSUPPORTED;
+  if (total_new == 0 || max_new == 0) return TTS_OK;  // nothing to append
+  if (k == nullptr || v == nullptr || cu_new == nullptr || past_lens == nullptr ||
+      page_tables == nullptr || k_cache == nullptr || v_cache == nullptr)
+    return TTS_ERR_INVALID_ARG;
+  const int64_t kv_row = (int64_t)num_heads_kv * head_dim;
+  if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return TTS_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      (k_out != nullptr && !aligned16(k_out)))
+    return TTS_ERR_INVALID_ARG;
+  if (cache_dtype == TTS_E4M3 && (k_scale == nullptr || v_scale == nullptr))
+    return TTS_ERR_INVALID_ARG;
+  if (cos_sin != nullptr && (max_pos < 1 || !aligned16(cos_sin))) return TTS_ERR_INVALID_ARG;
+  if (q != nullptr) {
+    if (num_heads_q < 1 || q_out == nullptr || !aligned16(q) || !aligned16(q_out) ||
+        q_stride % 8 != 0 || q_stride < (int64_t)num_heads_q * head_dim)
+      return TTS_ERR_INVALID_ARG;
+  }
+  KvAppendArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.total_new = total_new;
+  a.cu_new = cu_new;
+  a.past_lens = past_lens;
+  a.batch = batch;
+  a.max_new = max_new;
+  a.hq = q != nullptr ? num_heads_q : 0;
+  a.hkv = num_heads_kv;
+  a.d = head_dim;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.page_tables = page_tables;
+  a.max_pages = max_pages;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.f8 = cache_dtype == TTS_E4M3;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.dev_status = dev_status;
+  return from_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t tts_attn_decode_workspace_bytes(int32_t max_seqlen_q, int32_t num_heads_q,
+                                       int32_t num_heads_kv, int32_t head_dim) {
+  if (max_seqlen_q < 1 || max_seqlen_q > kDecodeMaxQ || num_heads_q < 1 || num_heads_kv < 1 ||
+      num_heads_q % num_heads_kv != 0 || (head_dim != 64 && head_dim != 128))
+    return 0;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();  // no device
+    return 0;
+  }
+  return attn_decode_workspace_bytes(max_seqlen_q, num_heads_q, num_heads_kv, head_dim, sms);
+}
+
+tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* cu_seqlens_q,
+                                 int32_t batch, int32_t max_seqlen_q, int32_t num_heads_q,
+                                 int32_t num_heads_kv, int32_t head_dim, const void* k_cache,
+                                 const void* v_cache, const float* k_scale, const float* v_scale,
+                                 tts_dtype cache_dtype, int32_t num_pages, int32_t page_size,
+                                 const int32_t* page_tables, int32_t max_pages,
+                                 const int32_t* kv_lens, int32_t window, int32_t sinks,
+                                 float scale, void* out, tts_dtype out_dtype, float* lse,
+                                 void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                 void* stream) {
+  if (total_q < 0 || batch < 1 || max_seqlen_q < 1 || num_heads_q < 1 || num_heads_kv < 1 ||
+      head_dim < 1 || num_pages < 1 || page_size < 1 || max_pages < 1 || window < 0 || sinks < 0)
+    return TTS_ERR_INVALID_ARG;
+  if (num_heads_q % num_heads_kv != 0) return TTS_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return TTS_ERR_INVALID_ARG;
+  if (cache_dtype != TTS_BF16 && cache_dtype != TTS_E4M3) return TTS_ERR_INVALID_ARG;
+  if (out_dtype != TTS_BF16 && out_dtype != TTS_F32) return TTS_ERR_INVALID_ARG;
+  if (!cache_shape_built(head_dim, page_size, num_pages, max_pages, num_heads_kv) ||
+      max_seqlen_q > kDecodeMaxQ || total_q > 0x7FFFFF00LL ||
+      (int64_t)max_seqlen_q * num_heads_q > 0x7FFFFFFFLL)
+    return TTS_ERR_UNSUPPORTED;
+  if (total_q == 0) return TTS_OK;  // nothing to compute
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || page_tables == nullptr ||
+      kv_lens == nullptr || out == nullptr)
+    return TTS_ERR_INVALID_ARG;
+  if (cache_dtype == TTS_E4M3 && (k_scale == nullptr || v_scale == nullptr))
+    return TTS_ERR_INVALID_ARG;
+  if (cu_seqlens_q == nullptr && total_q < batch) return TTS_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return TTS_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned16(workspace) ||
+      workspace_bytes < tts_attn_decode_workspace_bytes(max_seqlen_q, num_heads_q, num_heads_kv,
+                                                        head_dim))
+    return TTS_ERR_WORKSPACE;
+  AttnDecodeArgs a;
+  a.q = q;
+  a.total_q = total_q;
+  a.cu_q = cu_seqlens_q;
+  a.batch = batch;
+  a.max_q = max_seqlen_q;
+  a.hq = num_heads_q;
+  a.hkv = num_heads_kv;
+  a.d = head_dim;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.f8 = cache_dtype == TTS_E4M3;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.page_tables = page_tables;
+  a.max_pages = max_pages;
+  a.kv_lens = kv_lens;
+  // a window no key can leave is no window
+  a.window = window >= 1 << 30 ? 0 : window;
+  a.sinks = sinks;
+  a.scale = scale;
+  a.out = out;
+  a.out_bf16 = out_dtype == TTS_BF16;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.dev_status = dev_status;
+  int drv = 0;
+  const cudaError_t e = launch_attn_decode(a, &drv, static_cast<cudaStream_t>(stream));
   if (drv != 0) return TTS_ERR_CUDA;
   return from_cuda(e);
 }

@@ -1,0 +1,975 @@
+// Attention of the newest tokens of each request over a paged grouped-query KV cache held in
+// e4m3 (a scale per page and KV head) or bf16, with an optional sliding window and first
+// tokens that stay visible.
+//
+// For KV head g the q rows of its group (token-major: row = token * G + head in the group)
+// are tiles of 8 NT rows; a unit is (request, g, row tile) and a tile is kTK consecutive keys.
+// With x_j = scale log2(e) sK[page(j)] q.k_j (q.k over codes), y_j = x_j + log2 sV[page(j)]:
+//   out = sum_j 2^(y_j - m) v_j / sum_j 2^(y_j - m) / sV[page(j)],  lse = ln 2 (m + log2 of the
+// denominator): the value scale rides in the exponent, so weights of pages with different
+// scales share one fp16 product with the codes, and the running maximum m is taken over y.
+//
+// Bound: HBM (each cached byte is used by 8 NT rows only). All tiles of all units form one
+// list, cut into equal runs, one per CTA (two CTAs per SM), so ragged batches, one request and
+// many requests all fill the GPU; a unit cut by a run's border leaves unnormalised partial
+// sums, joined in a fixed order by a second launch. In a CTA one warp brings tiles by TMA
+// (pages through the table, 128-byte swizzle) into a ring of kStages slots, and each of four
+// warps takes every fourth tile for itself, with its own running maximum, sum and
+// accumulators, joined through shared memory at the end of the unit: no barrier inside a unit.
+//
+// S^T = K Q^T and O^T = V^T P^T run on m16n8k16 tensor-core products with keys (then d) as
+// the 16 rows and q rows as the 8 columns: a group of 4 to 8 heads fills the columns, where a
+// 128-row tcgen05 tile would be 3 to 6 % used and would need the codes widened in shared
+// memory. e4m3 codes become fp16 (exactly) in registers; q is fp16 after a power-of-two
+// scaling of its row (exact for every element within 2^-22 of the row's largest), and P is
+// fp16 with its reference kept so that 2^-25 of the maximum still has all 11 bits. bf16
+// caches use bf16 products throughout. Sums and softmax statistics are fp32.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace tts {
+namespace {
+
+constexpr int kNW = 4;                        // consumer warps
+constexpr int kThreads = (kNW + 1) * 32;      // and one producer warp
+constexpr int kCtasPerSm = 2;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <bool F8, int D, int NT>
+struct Cfg {
+  static constexpr int kRowBytes = D * (F8 ? 1 : 2);
+  static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;  // one swizzled TMA box row
+  static constexpr int kPanels = kRowBytes / kPanelBytes;
+  static constexpr int kTK = kRowBytes == 256 ? 32 : 64;  // keys per tile
+  static constexpr int kMT = kTK / 16;
+  static constexpr int kKBytes = kTK * kRowBytes;  // K (or V) of one tile
+  static constexpr int kStageBytes = 2 * kKBytes;
+  static constexpr int kR = 8 * NT;        // q rows per unit
+  static constexpr int kKS = D / 16;       // k steps of the first product, m tiles of the second
+  static constexpr int kMQ = kKS / kNW;    // m tiles each warp finishes when a unit ends
+  static constexpr int kJoinBytes = kNW * (kNW - 1) * NT * kMQ * 4 * 32 * 4;
+  // Two CTAs per SM: 113 KB each, less 1 KB to align the ring and 1 KB of barriers.
+  static constexpr int kStagesFit = (113 * 1024 - 2048 - kJoinBytes) / kStageBytes;
+  static constexpr int kStages = kStagesFit < 12 ? kStagesFit : 12;
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kJoinBytes;
+};
+
+struct Params {
+  const uint16_t* q;
+  const int32_t* cu_q;  // null: one token per request
+  const int32_t* page_tables;
+  const int32_t* kv_lens;
+  const float* k_scale;
+  const float* v_scale;
+  void* out;
+  float* lse;
+  float* parts;  // [2 * CTAs][kR * (D + 2)]
+  int4* jobs;    // [CTAs]: {first CTA of the unit (-1: none), request, g, row tile}
+  uint32_t* dev_status;
+  int64_t total_q;
+  int batch, max_q, hq, hkv, group, num_pages, max_pages, page_size, page_shift, window, sinks;
+  float scale_log2;
+  int out_bf16, ctas;
+};
+
+// A request as the kernel sees it: its tokens, its visible keys as two runs of tiles (first
+// tokens, window) and the number of units per head.
+struct Req {
+  int n, L, lo, sinks;  // new tokens, keys, first key of the window (0: none), kept first keys
+  int st, lt, nt, rt;   // tiles of the first keys, first tile of the window, tiles, row tiles
+  int64_t q0;           // first q row
+};
+template <int TK, int R>
+__device__ __forceinline__ Req load_req(const Params& p, int b, uint32_t* bad) {
+  Req r;
+  int64_t q0 = b, q1 = b + 1;
+  if (p.cu_q != nullptr) {
+    q0 = p.cu_q[b];
+    q1 = p.cu_q[b + 1];
+  }
+  int L = p.kv_lens[b];
+  r.n = 0;
+  r.q0 = q0;
+  if (q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.max_q)
+    *bad |= kDevBadArg;
+  else
+    r.n = (int)(q1 - q0);
+  if (L < 0 || (int64_t)L > (int64_t)p.max_pages * p.page_size) {
+    *bad |= kDevIndexRange;
+    L = 0;  // its rows see no key
+  }
+  r.L = L;
+  r.lo = 0;
+  if (p.window > 0) {
+    const int64_t lo = (int64_t)L - r.n + 1 - p.window;
+    r.lo = lo > 0 ? (int)(lo < L ? lo : L) : 0;
+  }
+  r.sinks = p.sinks < r.lo ? p.sinks : r.lo;
+  r.lt = r.lo / TK;
+  r.st = (r.sinks + TK - 1) / TK;
+  if (r.st > r.lt) r.st = r.lt;
+  r.nt = r.st + (L + TK - 1) / TK - r.lt;
+  if (r.nt < 1) r.nt = 1;  // an empty tile: the unit writes zeros
+  r.rt = (r.n * p.group + R - 1) / R;
+  return r;
+}
+__device__ __forceinline__ int64_t req_tiles(const Params& p, const Req& r) {
+  return (int64_t)p.hkv * r.rt * r.nt;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool F8>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (F8)
+    mma_f16(d, a, b0, b1);
+  else
+    mma_bf16(d, a, b0, b1);
+}
+// 8x8 transpose of 16-bit values across the warp.
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// The two e4m3 codes in the low / high half of w as two fp16 values (exact).
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+
+// Shared-memory address of 16-byte chunk c of row `row` of a K or V tile, as TMA's swizzle
+// places it (128-byte rows: chunk ^ row mod 8; 64-byte rows: chunk ^ row / 2 mod 4).
+template <int TK, int PB>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row, int c) {
+  if constexpr (PB == 128)
+    return base + (c >> 3) * (TK * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+  else
+    return base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+}
+
+struct Meta {  // of a ring slot, written by the producer
+  uint32_t ok;   // bit i: piece i of the tile (a page, or the tile if pages are larger) is there
+  float ks[4];   // scale of its keys
+  float vl[4];   // log2 of the scale of its values
+  float vi[4];   // 1 / that scale
+};
+
+template <bool F8, int D, int NT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    attn_decode_kernel(const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const Params p) {
+  using C = Cfg<F8, D, NT>;
+  constexpr int TK = C::kTK, MT = C::kMT, S = C::kStages, R = C::kR, KS = C::kKS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[S], bar_empty[S];
+  __shared__ Meta s_meta[S];
+  __shared__ float2 s_ml[kNW][R];  // each warp's reference and sum of every row
+  __shared__ int64_t s_scan[kThreads / 32], s_off;
+  __shared__ int s_b, s_abort, s_issued;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  float* join = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S * C::kStageBytes);
+  volatile int* abort_flag = &s_abort;
+  volatile int* issued_tiles = &s_issued;
+
+  // ---- this CTA's run [t0, t1) of the list of tiles, and the request it begins in
+  uint32_t bad = 0;
+  auto block_scan = [&](int64_t v, int64_t* total) -> int64_t {  // inclusive
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int64_t before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += s_scan[w];
+      sum += s_scan[w];
+    }
+    *total = sum;
+    return x + before;
+  };
+  auto tiles_of = [&](int b) -> int64_t {
+    return b < p.batch ? req_tiles(p, load_req<TK, R>(p, b, &bad)) : 0;
+  };
+  if (tid == 0) {
+    s_abort = s_issued = 0;
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&bar_full[i]), 1);
+      mbar_init(smem_u32(&bar_empty[i]), 1);
+    }
+    fence_mbar_init();
+  }
+  int64_t total = 0, v0 = 0, incl0 = 0;
+  for (int base = 0; base < p.batch; base += kThreads) {
+    const int64_t v = tiles_of(base + tid);
+    int64_t sum;
+    const int64_t incl = block_scan(v, &sum);
+    if (base == 0) {
+      v0 = v;
+      incl0 = incl;
+    }
+    total += sum;
+  }
+  if (blockIdx.x == 0 && bad && p.dev_status != nullptr) atomicOr(p.dev_status, bad);
+  const int64_t runs = total < p.ctas ? total : p.ctas;  // runs with at least one tile each
+  if (tid == 0) p.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if ((int64_t)blockIdx.x >= runs) return;
+  const int64_t t0 = total * blockIdx.x / runs, t1 = total * (blockIdx.x + 1) / runs;
+  {
+    int64_t carry = 0;
+    for (int base = 0; base < p.batch; base += kThreads) {
+      int64_t v = v0, incl = incl0, sum = 0;
+      if (p.batch > kThreads) {
+        v = tiles_of(base + tid);
+        incl = block_scan(v, &sum);
+      }
+      if (carry + incl > t0 && carry + incl - v <= t0) {
+        s_b = base + tid;
+        s_off = t0 - (carry + incl - v);
+      }
+      carry += sum;
+    }
+  }
+  __syncthreads();
+
+  int b = s_b;
+  int64_t off = s_off, left = t1 - t0;
+  int it = 0;  // tiles of this run so far
+  Req r = load_req<TK, R>(p, b, &bad);
+  // The next unit's part in this run: head, row tile, tiles [x0, x1) of nt.
+  auto next_seg = [&](int& g, int& rt, int& x0, int& x1) {
+    while (off >= req_tiles(p, r)) {  // requests without tiles are stepped over
+      ++b;
+      off = 0;
+      r = load_req<TK, R>(p, b, &bad);
+    }
+    const int u = (int)(off / r.nt);
+    x0 = (int)(off - (int64_t)u * r.nt);
+    g = u / r.rt;
+    rt = u - g * r.rt;
+    x1 = (int)(r.nt - x0 < left ? r.nt : x0 + left);
+    off += x1 - x0;
+    left -= x1 - x0;
+  };
+  const int piece = p.page_size < TK ? p.page_size : TK;  // keys per TMA box
+  const int n_pieces = TK / piece;
+
+  if (warp == kNW) {
+    // ------------------------------------------------------------------ producer
+    constexpr uint32_t kBox = C::kPanelBytes;
+    int cache_b = -1, cache_at = 0, cache_g = -1, page = -1;
+    float ks = 1.f, vs = 1.f;
+    bool ok = true;
+    while (ok && left > 0) {
+      int g, rt, x0, x1;
+      next_seg(g, rt, x0, x1);
+      for (int x = x0; ok && x < x1; ++x, ++it) {
+        const int key0 = (x < r.st ? x : r.lt + x - r.st) * TK;
+        const int st = it % S;
+        const int pg0 = key0 >> p.page_shift;
+        if (cache_b != b || pg0 < cache_at || pg0 + n_pieces > cache_at + 32) {
+          cache_b = b;
+          cache_at = pg0;
+          cache_g = -1;
+          const int lp = pg0 + lane;
+          page = lp < p.max_pages ? p.page_tables[(int64_t)b * p.max_pages + lp] : -1;
+        }
+        if (F8 && cache_g != g) {
+          cache_g = g;
+          ks = vs = 1.f;
+          if (page >= 0 && page < p.num_pages) {
+            ks = p.k_scale[(int64_t)page * p.hkv + g];
+            vs = p.v_scale[(int64_t)page * p.hkv + g];
+          }
+        }
+        if (it >= S)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bar_empty[st]), ((it / S) - 1) & 1,
+                                                 abort_flag, p.dev_status));
+        if (!ok) break;
+        const int at = pg0 - cache_at + (lane < n_pieces ? lane : 0);
+        const int pg = __shfl_sync(0xFFFFFFFFu, page, at);
+        const int a = key0 + lane * piece;  // this lane's piece: keys [a, a + piece)
+        const bool seen = lane < n_pieces && a < r.L && (a + piece > r.lo || a < r.sinks);
+        bool good = seen && pg >= 0 && pg < p.num_pages;
+        uint32_t flag = seen && !good ? kDevIndexRange : 0u;
+        if (good) {
+          const uint32_t dst = ring + st * C::kStageBytes + lane * piece * kBox;
+          const int row = key0 & (p.page_size - 1);  // 0 unless the tile is inside a page
+          const int slab = pg * p.hkv + g;
+          const uint32_t bar = smem_u32(&bar_full[st]);
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn) {
+            tma_load_3d(dst + pn * TK * kBox, &map_k, bar, pn * 64, row, slab);
+            tma_load_3d(dst + C::kKBytes + pn * TK * kBox, &map_v, bar, pn * 64, row, slab);
+          }
+        }
+        const uint32_t sent = __ballot_sync(0xFFFFFFFFu, good);
+        if constexpr (F8) {
+          const float pks = __shfl_sync(0xFFFFFFFFu, ks, at), pvs = __shfl_sync(0xFFFFFFFFu, vs, at);
+          if (good && !(pks > 0.f && pks < INFINITY && pvs > 0.f && pvs < INFINITY)) {
+            good = false;  // no scale a cache page can have: its keys are skipped
+            flag |= kDevBadArg;
+          }
+          if (lane < n_pieces) {
+            s_meta[st].ks[lane] = pks;
+            s_meta[st].vl[lane] = good ? log2f(pvs) : 0.f;
+            s_meta[st].vi[lane] = good ? 1.f / pvs : 0.f;
+          }
+        }
+        if (flag && p.dev_status != nullptr) atomicOr(p.dev_status, flag);
+        const uint32_t use = __ballot_sync(0xFFFFFFFFu, good);
+        if (lane == 0) {
+          s_meta[st].ok = use;
+        }
+        __syncwarp();
+        if (lane == 0)
+          mbar_arrive_expect_tx(smem_u32(&bar_full[st]),
+                                __popc(sent) * piece * C::kRowBytes * 2);
+        if (lane == 0) {
+          __threadfence_block();
+          *issued_tiles = it + 1;
+        }
+      }
+    }
+    if (!ok) {  // copies in flight must land before the CTA can exit
+      for (int i = it > S ? it - S : 0; i < it; ++i)
+        mbar_wait(smem_u32(&bar_full[i % S]), (i / S) & 1, nullptr, nullptr);
+    }
+  } else {
+    // ------------------------------------------------------------------ consumers
+    constexpr float kThr = F8 ? 4.f : 8.f;    // the reference moves when exceeded by 2^kThr
+    constexpr float kBias = F8 ? 11.f : 0.f;  // P is held times 2^kBias: at most 2^15 in fp16
+    const int g8 = lane >> 2, t4 = lane & 3;
+    const int piece_shift = 31 - __clz(piece >> 4);  // 16-key m tile -> piece
+    // Bounded wait until the producer has issued tile i (usually long ago).
+    auto issued = [&](int i) -> bool {
+      bool ok = *issued_tiles > i;
+      if (!ok) {
+        const uint64_t since = globaltimer();
+        while (!(ok = *issued_tiles > i) && !*abort_flag) {
+          if (globaltimer() - since > kWaitLimitNs) {
+            if (p.dev_status != nullptr) atomicOr(p.dev_status, kDevTimeout);
+            *abort_flag = 1;
+          }
+        }
+      }
+      return __all_sync(0xFFFFFFFFu, ok);
+    };
+    while (left > 0) {
+      int g, rt, x0, x1;
+      next_seg(g, rt, x0, x1);
+      const bool whole_l = x0 == 0, whole_r = x1 == r.nt;
+      const int rows = r.n * p.group - rt * R;  // rows of this tile: min(rows, R)
+
+      // q fragments of column g8 of every n tile: step i takes elements e0(i) .. e0(i) + 3
+      uint32_t qf[NT][KS][2];
+      float f0[NT], f1[NT];      // factor of the scores of columns 2 t4 and 2 t4 + 1
+      int pos0[NT], pos1[NT];    // positions of the two rows
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int rr = rt * R + j * 8 + g8;
+        const bool in = j * 8 + g8 < rows;
+        const int tok = in ? rr / p.group : 0;
+        const int h = in ? g * p.group + (rr - tok * p.group) : 0;
+        const uint16_t* src = p.q + ((r.q0 + tok) * p.hq + h) * (int64_t)D;
+        uint32_t w[KS][2];
+#pragma unroll
+        for (int i = 0; i < KS; i += 2) {
+          const int e0 = F8 ? (D / 4) * t4 + 4 * i : 64 * (i / 4) + 16 * t4 + 4 * (i % 4);
+          const uint4 v = in ? *reinterpret_cast<const uint4*>(src + e0) : make_uint4(0, 0, 0, 0);
+          w[i][0] = v.x;
+          w[i][1] = v.y;
+          w[i + 1][0] = v.z;
+          w[i + 1][1] = v.w;
+        }
+        float fac = p.scale_log2;
+        if constexpr (F8) {
+          uint32_t top = 0;  // largest |q| of the row, as bf16 bits
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t m = w[i][k] & 0x7FFF7FFFu;
+              top = max(top, max(m & 0xFFFFu, m >> 16));
+            }
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          const int e = max((int)(top >> 7), 27);  // biased exponent; q' = q 2^(8 - e) < 2^9
+          const float up = __uint_as_float((uint32_t)(262 - e < 1 ? 1 : 262 - e) << 23);
+          fac *= __uint_as_float((uint32_t)(e < 9 ? 1 : e - 8) << 23);
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              qf[j][i][k] = pack_f16x2(__uint_as_float(w[i][k] << 16) * up,
+                                       __uint_as_float(w[i][k] & 0xFFFF0000u) * up);
+        } else {
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            qf[j][i][0] = w[i][0];
+            qf[j][i][1] = w[i][1];
+          }
+        }
+        const int pos = r.L - r.n + tok;
+        f0[j] = __shfl_sync(0xFFFFFFFFu, fac, (2 * t4) * 4);
+        f1[j] = __shfl_sync(0xFFFFFFFFu, fac, (2 * t4 + 1) * 4);
+        pos0[j] = __shfl_sync(0xFFFFFFFFu, pos, (2 * t4) * 4);
+        pos1[j] = __shfl_sync(0xFFFFFFFFu, pos, (2 * t4 + 1) * 4);
+      }
+      // every row sees keys [max_lo, min_end) (and the first sinks)
+      const int last_row = rt * R + (rows < R ? rows : R) - 1;
+      const int min_end = r.L - r.n + rt * R / p.group + 1;
+      const int max_pos = r.L - r.n + last_row / p.group;
+      const int max_lo = p.window > 0 ? max_pos + 1 - p.window : 0;
+
+      float o[NT][KS][4];
+      float m0[NT], m1[NT], l0[NT], l1[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        m0[j] = m1[j] = -INFINITY;
+        l0[j] = l1[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[j][i][k] = 0.f;
+      }
+
+      for (int x = x0; x < x1; ++x, ++it) {
+        if (it % kNW != warp) continue;
+        const int st = it % S;
+        // A parity wait is only unambiguous against the phase in progress. The slot's previous
+        // tile is another warp's (kNW need not divide kStages) and copies may land out of
+        // order, so the tile must have been issued first: that tells that the slot's earlier
+        // phases are complete.
+        if (!issued(it) ||
+            !warp_wait(smem_u32(&bar_full[st]), (it / S) & 1, abort_flag, p.dev_status))
+          continue;  // the run is lost; the barriers below still need every warp
+        const int key0 = (x < r.st ? x : r.lt + x - r.st) * TK;
+        const uint32_t sk = ring + st * C::kStageBytes, sv = sk + C::kKBytes;
+        const uint32_t okp = s_meta[st].ok;
+        const bool all_pieces = okp == (1u << n_pieces) - 1u;
+        // rows of the tile that some new token sees all lie in pieces that are there
+        if (okp != 0) {
+          // ---- S^T = K Q^T
+          float s[NT][MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s[j][mt][k] = 0.f;
+            const int ra = mt * 16 + g8, rb = ra + 8;
+            if constexpr (F8) {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c) {
+                const uint4 va = lds128(chunk_at<TK, C::kPanelBytes>(sk, ra, (D / 64) * t4 + c));
+                const uint4 vb = lds128(chunk_at<TK, C::kPanelBytes>(sk, rb, (D / 64) * t4 + c));
+                const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t a[4] = {e4m3_lo(wa[k]), e4m3_lo(wb[k]), e4m3_hi(wa[k]),
+                                         e4m3_hi(wb[k])};
+#pragma unroll
+                  for (int j = 0; j < NT; ++j)
+                    mma16<F8>(s[j][mt], a, qf[j][c * 4 + k][0], qf[j][c * 4 + k][1]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {  // panel c / 2, chunk 2 t4 + c % 2
+                const int ch = (c / 2) * 8 + 2 * t4 + (c & 1);
+                const uint4 va = lds128(chunk_at<TK, C::kPanelBytes>(sk, ra, ch));
+                const uint4 vb = lds128(chunk_at<TK, C::kPanelBytes>(sk, rb, ch));
+                const uint32_t a0[4] = {va.x, vb.x, va.y, vb.y}, a1[4] = {va.z, vb.z, va.w, vb.w};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                  mma16<F8>(s[j][mt], a0, qf[j][2 * c][0], qf[j][2 * c][1]);
+                  mma16<F8>(s[j][mt], a1, qf[j][2 * c + 1][0], qf[j][2 * c + 1][1]);
+                }
+              }
+            }
+          }
+          // ---- scores in the exp2 domain, masks, running reference
+          const bool clear = all_pieces && key0 + TK <= min_end &&
+                             (p.window == 0 || key0 >= max_lo || key0 + TK <= p.sinks);
+          float t0m[NT], t1m[NT];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) t0m[j] = t1m[j] = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float ks = 1.f, vl = 0.f;
+            if constexpr (F8) {
+              ks = s_meta[st].ks[mt >> piece_shift];
+              vl = s_meta[st].vl[mt >> piece_shift];
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const float a0 = f0[j] * ks, a1 = f1[j] * ks;
+              float(&v)[4] = s[j][mt];
+              v[0] = fmaf(v[0], a0, vl);
+              v[1] = fmaf(v[1], a1, vl);
+              v[2] = fmaf(v[2], a0, vl);
+              v[3] = fmaf(v[3], a1, vl);
+              if (!clear) {
+                const bool here = (okp >> (mt >> piece_shift)) & 1u;
+                const int ka = key0 + mt * 16 + g8, kb = ka + 8;
+                auto sees = [&](int key, int pos) {
+                  return here && key <= pos &&
+                         (p.window == 0 || key > pos - p.window || key < p.sinks);
+                };
+                if (!sees(ka, pos0[j])) v[0] = -INFINITY;
+                if (!sees(ka, pos1[j])) v[1] = -INFINITY;
+                if (!sees(kb, pos0[j])) v[2] = -INFINITY;
+                if (!sees(kb, pos1[j])) v[3] = -INFINITY;
+              }
+              t0m[j] = fmax3(t0m[j], v[0], v[2]);
+              t1m[j] = fmax3(t1m[j], v[1], v[3]);
+            }
+          }
+          bool move = false;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            move = move || t0m[j] > m0[j] + kThr || t1m[j] > m1[j] + kThr;
+          if (__any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) {
+                t0m[j] = fmaxf(t0m[j], __shfl_xor_sync(0xFFFFFFFFu, t0m[j], d));
+                t1m[j] = fmaxf(t1m[j], __shfl_xor_sync(0xFFFFFFFFu, t1m[j], d));
+              }
+              const float n0 = fmaxf(m0[j], t0m[j]), n1 = fmaxf(m1[j], t1m[j]);
+              const float al0 = n0 == -INFINITY ? 1.f : ex2_approx(m0[j] - n0);
+              const float al1 = n1 == -INFINITY ? 1.f : ex2_approx(m1[j] - n1);
+              m0[j] = n0;
+              m1[j] = n1;
+              l0[j] *= al0;
+              l1[j] *= al1;
+#pragma unroll
+              for (int i = 0; i < KS; ++i) {
+                o[j][i][0] *= al0;
+                o[j][i][1] *= al1;
+                o[j][i][2] *= al0;
+                o[j][i][3] *= al1;
+              }
+            }
+          }
+          // ---- values of keys nobody sees must not meet a weight of zero as NaN
+          if (!(all_pieces && key0 + TK <= r.L && (key0 >= r.lo || key0 + TK <= r.sinks))) {
+            for (int row = lane / 4; row < TK; row += 8) {
+              const int key = key0 + row;
+              const bool seen = ((okp >> ((row >> 4) >> piece_shift)) & 1u) && key < r.L &&
+                                (key >= r.lo || key < r.sinks);
+              if (!seen)
+                for (int c = lane & 3; c < C::kRowBytes / 16; c += 4) {
+                  const uint32_t at = chunk_at<TK, C::kPanelBytes>(sv, row, c);
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0)
+                               : "memory");
+                }
+            }
+            fence_proxy_async_smem();  // before the slot is handed back to TMA
+            __syncwarp();
+          }
+          // ---- P and O^T += V^T P^T
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float vi = 1.f;
+            if constexpr (F8) vi = s_meta[st].vi[mt >> piece_shift];
+            uint32_t b0[NT], b1[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const float e0 = m0[j] == -INFINITY ? 0.f : m0[j] - kBias;
+              const float e1 = m1[j] == -INFINITY ? 0.f : m1[j] - kBias;
+              float pr[4];
+              pr[0] = ex2_approx(s[j][mt][0] - e0);
+              pr[1] = ex2_approx(s[j][mt][1] - e1);
+              pr[2] = ex2_approx(s[j][mt][2] - e0);
+              pr[3] = ex2_approx(s[j][mt][3] - e1);
+              l0[j] = fmaf(pr[0] + pr[2], vi, l0[j]);
+              l1[j] = fmaf(pr[1] + pr[3], vi, l1[j]);
+              b0[j] = movm(F8 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
+              b1[j] = movm(F8 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
+            }
+            if constexpr (F8) {
+              // words of rows 2t, 2t + 1, 2t + 8, 2t + 9; d = (D/8) g8 + ...
+              constexpr int kWords = D / 32;  // 4-byte words per lane and row
+              uint32_t w[4][kWords];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int row = mt * 16 + 2 * t4 + (k & 1) + (k >> 1) * 8;
+                if constexpr (kWords == 4) {
+                  const uint4 v = lds128(chunk_at<TK, C::kPanelBytes>(sv, row, g8));
+                  w[k][0] = v.x;
+                  w[k][1] = v.y;
+                  w[k][2] = v.z;
+                  w[k][3] = v.w;
+                } else {
+                  const uint2 v =
+                      lds64(chunk_at<TK, C::kPanelBytes>(sv, row, g8 >> 1) + (g8 & 1) * 8);
+                  w[k][0] = v.x;
+                  w[k][1] = v.y;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < kWords; ++i) {
+                const uint32_t xa = __byte_perm(w[0][i], w[1][i], 0x5140),
+                               xb = __byte_perm(w[0][i], w[1][i], 0x7362),
+                               ya = __byte_perm(w[2][i], w[3][i], 0x5140),
+                               yb = __byte_perm(w[2][i], w[3][i], 0x7362);
+                const uint32_t a0[4] = {e4m3_lo(xa), e4m3_hi(xa), e4m3_lo(ya), e4m3_hi(ya)};
+                const uint32_t a1[4] = {e4m3_lo(xb), e4m3_hi(xb), e4m3_lo(yb), e4m3_hi(yb)};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                  mma16<F8>(o[j][2 * i], a0, b0[j], b1[j]);
+                  mma16<F8>(o[j][2 * i + 1], a1, b0[j], b1[j]);
+                }
+              }
+            } else {
+              const int row = mt * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+              for (int i = 0; i < KS; ++i) {
+                uint32_t a[4];
+                ldsm_x4_trans(a, chunk_at<TK, C::kPanelBytes>(sv, row, 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma16<F8>(o[j][i], a, b0[j], b1[j]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_empty[st]));
+      }
+
+      // ---- join the four warps: warp w finishes m tiles [w kMQ, (w + 1) kMQ)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          l0[j] += __shfl_xor_sync(0xFFFFFFFFu, l0[j], d);
+          l1[j] += __shfl_xor_sync(0xFFFFFFFFu, l1[j], d);
+        }
+        if (g8 == 0) {
+          s_ml[warp][j * 8 + 2 * t4] = make_float2(m0[j], l0[j]);
+          s_ml[warp][j * 8 + 2 * t4 + 1] = make_float2(m1[j], l1[j]);
+        }
+      }
+      // slot of (finishing warp, source warp): sources other than the finisher, in order
+      auto join_at = [&](int dst, int src) -> float* {
+        const int k = src < dst ? src : src - 1;
+        return join + (size_t)(dst * (kNW - 1) + k) * (NT * C::kMQ * 4 * 32) + lane;
+      };
+#pragma unroll
+      for (int dst = 0; dst < kNW; ++dst) {
+        if (dst == warp) continue;
+        float* to = join_at(dst, warp);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < C::kMQ; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              to[((j * C::kMQ + i) * 4 + k) * 32] = o[j][dst * C::kMQ + i][k];
+      }
+      named_barrier_sync(1, kNW * 32);
+      const bool final = whole_l && whole_r;
+      float* part = p.parts + (size_t)(2 * blockIdx.x + (whole_l ? 1 : 0)) * (R * (D + 2));
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, fw[kNW][2];
+#pragma unroll
+        for (int w = 0; w < kNW; ++w)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) top[k] = fmaxf(top[k], s_ml[w][j * 8 + 2 * t4 + k].x);
+#pragma unroll
+        for (int w = 0; w < kNW; ++w)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 ml = s_ml[w][j * 8 + 2 * t4 + k];
+            fw[w][k] = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top[k]);
+            sum[k] = fmaf(ml.y, fw[w][k], sum[k]);
+          }
+        float acc[C::kMQ][4];
+#pragma unroll
+        for (int i = 0; i < C::kMQ; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kNW; ++w) {
+          const float* from = join_at(warp, w == warp ? (warp == 0 ? 1 : 0) : w);
+#pragma unroll
+          for (int i = 0; i < C::kMQ; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float v = from[((j * C::kMQ + i) * 4 + k) * 32];
+              if (w == warp) {
+#pragma unroll
+                for (int d = 0; d < kNW; ++d)
+                  if (d == warp) v = o[j][d * C::kMQ + i][k];
+              }
+              acc[i][k] = fmaf(v, fw[w][k & 1], acc[i][k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // column 2 t4 + k: one q row
+          const int row = j * 8 + 2 * t4 + k;
+          float v[2 * C::kMQ];
+#pragma unroll
+          for (int i = 0; i < C::kMQ; ++i) {
+            v[2 * i] = acc[i][k];
+            v[2 * i + 1] = acc[i][k + 2];
+          }
+          // v[2 i], v[2 i + 1] are elements d of m tile w kMQ + i: for e4m3 (D/8) g8 +
+          // 2 (w kMQ + i) + {0, 1}; for bf16 16 (w kMQ + i) + g8 + {0, 8}
+          if (final) {
+            if (row < rows) {
+              const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;
+              const int rr = rt * R + row, tok = rr / p.group;
+              const int64_t at = (r.q0 + tok) * p.hq + g * p.group + (rr - tok * p.group);
+#pragma unroll
+              for (int i = 0; i < 2 * C::kMQ; ++i) {
+                const int m = warp * C::kMQ + i / 2;
+                const int d = F8 ? (D / 8) * g8 + 2 * m + (i & 1) : 16 * m + g8 + 8 * (i & 1);
+                if (p.out_bf16)
+                  static_cast<__nv_bfloat16*>(p.out)[at * D + d] = __float2bfloat16_rn(v[i] * inv);
+                else
+                  static_cast<float*>(p.out)[at * D + d] = v[i] * inv;
+              }
+              if (p.lse != nullptr && warp == 0 && g8 == 0)
+                p.lse[at] = sum[k] > 0.f ? (top[k] - kBias + log2f(sum[k])) * kLn2 : -INFINITY;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2 * C::kMQ; ++i) {
+              const int m = warp * C::kMQ + i / 2;
+              const int d = F8 ? (D / 8) * g8 + 2 * m + (i & 1) : 16 * m + g8 + 8 * (i & 1);
+              part[row * D + d] = v[i];
+            }
+            if (warp == 0 && g8 == 0) {
+              part[R * D + 2 * row] = top[k];
+              part[R * D + 2 * row + 1] = sum[k];
+            }
+          }
+        }
+      }
+      if (!whole_l && whole_r && tid == 0) {
+        // the unit ends here: tell the second launch where it began
+        const int64_t begin = t1 - left - x1;  // list index of the unit's first tile
+        p.jobs[blockIdx.x] =
+            make_int4((int)(((begin + 1) * runs - 1) / total), b, g, rt);
+      }
+      named_barrier_sync(1, kNW * 32);
+    }
+  }
+}
+
+// Joins the parts of the units that CTA borders cut: block (c, row) for the unit that ended in
+// CTA c, parts in list order within each of eight warps, then the warps in order.
+template <bool F8, int D, int NT>
+__global__ void __launch_bounds__(256) attn_decode_join_kernel(const Params p) {
+  using C = Cfg<F8, D, NT>;
+  constexpr int R = C::kR;
+  constexpr float kBias = F8 ? 11.f : 0.f;
+  __shared__ float2 s_ml[8];
+  __shared__ float4 s_acc[8][D / 4];
+  const int c1 = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 job = p.jobs[c1];
+  if (job.x < 0) return;
+  uint32_t bad = 0;
+  const Req r = load_req<C::kTK, R>(p, job.y, &bad);
+  const int rr = job.w * R + row;
+  if (rr >= r.n * p.group) return;
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int c = job.x + warp; c <= c1; c += 8) {
+    const float* part = p.parts + (size_t)(2 * c + (c == job.x ? 1 : 0)) * (R * (D + 2));
+    const float m = part[R * D + 2 * row], l = part[R * D + 2 * row + 1];
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lane < D / 4) v = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
+    const float n = fmaxf(top, m);
+    const float fa = top == -INFINITY ? 0.f : ex2_approx(top - n);
+    const float fb = m == -INFINITY ? 0.f : ex2_approx(m - n);
+    top = n;
+    sum = sum * fa + l * fb;
+    acc.x = acc.x * fa + v.x * fb;
+    acc.y = acc.y * fa + v.y * fb;
+    acc.z = acc.z * fa + v.z * fb;
+    acc.w = acc.w * fa + v.w * fb;
+  }
+  if (lane == 0) s_ml[warp] = make_float2(top, sum);
+  if (lane < D / 4) s_acc[warp][lane] = acc;
+  __syncthreads();
+  if (warp != 0) return;
+  top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, s_ml[w].x);
+  sum = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float f = s_ml[w].x == -INFINITY ? 0.f : ex2_approx(s_ml[w].x - top);
+    sum = fmaf(s_ml[w].y, f, sum);
+    if (lane < D / 4) {
+      const float4 v = s_acc[w][lane];
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
+    }
+  }
+  const int tok = rr / p.group;
+  const int64_t at = (r.q0 + tok) * p.hq + job.z * p.group + (rr - tok * p.group);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  if (lane < D / 4) {
+    if (p.out_bf16) {
+      uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane;
+      *o = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    } else {
+      reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[lane] =
+          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    }
+  }
+  if (p.lse != nullptr && lane == 0)
+    p.lse[at] = sum > 0.f ? (top - kBias + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+int rows_of(int max_q, int group) { return max_q * group <= 8 ? 8 : 16; }
+
+template <bool F8, int D, int NT>
+cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t stream) {
+  using C = Cfg<F8, D, NT>;
+  Params p;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.cu_q = a.cu_q;
+  p.page_tables = a.page_tables;
+  p.kv_lens = a.kv_lens;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.dev_status = a.dev_status;
+  p.total_q = a.total_q;
+  p.batch = a.batch;
+  p.max_q = a.max_q;
+  p.hq = a.hq;
+  p.hkv = a.hkv;
+  p.group = a.hq / a.hkv;
+  p.num_pages = a.num_pages;
+  p.max_pages = a.max_pages;
+  p.page_size = a.page_size;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.scale_log2 = a.scale * kLog2e;
+  p.out_bf16 = a.out_bf16 ? 1 : 0;
+  p.ctas = kCtasPerSm * sms;
+  p.jobs = static_cast<int4*>(a.workspace);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
+                                     ((size_t)p.ctas * sizeof(int4) + 255) / 256 * 256);
+  CUtensorMap mk, mv;
+  auto make = [&](CUtensorMap* m, void* base) -> bool {
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.page_size, (uint64_t)a.num_pages * a.hkv};
+    const uint64_t strides[2] = {(uint64_t)C::kRowBytes, (uint64_t)C::kRowBytes * a.page_size};
+    const uint32_t box[3] = {(uint32_t)(F8 ? D : 64),
+                             (uint32_t)(a.page_size < C::kTK ? a.page_size : C::kTK), 1};
+    const CUresult e = encode_tensor_map(
+        m, F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims,
+        strides, box, C::kPanelBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+    if (e != CUDA_SUCCESS) *drv_err = (int)e;
+    return e == CUDA_SUCCESS;
+  };
+  if (!make(&mk, const_cast<void*>(a.k_cache)) || !make(&mv, const_cast<void*>(a.v_cache)))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<F8, D, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  attn_decode_kernel<F8, D, NT><<<p.ctas, kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  attn_decode_join_kernel<F8, D, NT><<<dim3(p.ctas, C::kR), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <bool F8, int D>
+cudaError_t launch_nt(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t stream) {
+  return rows_of(a.max_q, a.hq / a.hkv) == 8 ? launch<F8, D, 1>(a, sms, drv_err, stream)
+                                             : launch<F8, D, 2>(a, sms, drv_err, stream);
+}
+
+}  // namespace
+
+size_t attn_decode_workspace_bytes(int max_q, int hq, int hkv, int d, int sms) {
+  const size_t ctas = (size_t)kCtasPerSm * sms, rows = rows_of(max_q, hq / hkv);
+  return (ctas * sizeof(int4) + 255) / 256 * 256 + ctas * 2 * rows * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_attn_decode(const AttnDecodeArgs& a, int* drv_err, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  if (a.d == 64)
+    return a.f8 ? launch_nt<true, 64>(a, sms, drv_err, stream)
+                : launch_nt<false, 64>(a, sms, drv_err, stream);
+  if (a.d == 128)
+    return a.f8 ? launch_nt<true, 128>(a, sms, drv_err, stream)
+                : launch_nt<false, 128>(a, sms, drv_err, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace tts

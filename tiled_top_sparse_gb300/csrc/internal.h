@@ -25,6 +25,58 @@ cudaError_t launch_paged_kv_write(const void* kv_new, int64_t ntok, int32_t dim,
                                   void* kv_cache, int32_t num_pages, int32_t page_size,
                                   uint32_t* dev_status, cudaStream_t stream);
 
+// ---- grouped-query KV cache: append with rotation
+struct KvAppendArgs {
+  const void* q;  // bf16, may be null
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;  // values from one token to the next
+  int64_t total_new;
+  const int32_t* cu_new;
+  const int32_t* past_lens;
+  int batch, max_new, hq, hkv, d;
+  const float* cos_sin;  // [max_pos, d / 2, 2] or null (no rotation)
+  int max_pos;
+  const int32_t* page_tables;
+  int max_pages;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  bool f8;  // e4m3 cache with scales, else bf16
+  int num_pages, page_size;
+  void* q_out;
+  void* k_out;  // may be null
+  uint32_t* dev_status;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
+
+// ---- attention of a few new tokens over that cache
+struct AttnDecodeArgs {
+  const void* q;  // bf16 [total_q, hq, d]
+  int64_t total_q;
+  const int32_t* cu_q;  // null: one token per request
+  int batch, max_q, hq, hkv, d;
+  const void* k_cache;  // [num_pages, hkv, page_size, d] bf16 or e4m3
+  const void* v_cache;
+  const float* k_scale;  // [num_pages, hkv] (e4m3)
+  const float* v_scale;
+  bool f8;
+  int num_pages, page_size;
+  const int32_t* page_tables;
+  int max_pages;
+  const int32_t* kv_lens;
+  int window, sinks;  // window 0: all keys
+  float scale;
+  void* out;
+  bool out_bf16;
+  float* lse;
+  void* workspace;
+  uint32_t* dev_status;
+};
+size_t attn_decode_workspace_bytes(int max_q, int hq, int hkv, int d, int sms);
+cudaError_t launch_attn_decode(const AttnDecodeArgs& a, int* drv_err, cudaStream_t stream);
+
 // ---- dense attention
 struct AttnArgs {
   const void* q;  // bf16
