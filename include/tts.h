@@ -112,6 +112,30 @@ tts_status tts_attn_fwd_varlen(const void* q, const void* k, const void* v, tts_
                                uint32_t* dev_status, void* stream);
 
 /*
+ * Dense attention forward with a causal sliding window and first tokens that stay visible.
+ *
+ * As tts_attn_fwd_varlen with causal = 1 (same sequences, layouts, types, workspace, device
+ * checks and errors), except that row i of a sequence, at position P = i + (Lk - Lq), sees
+ * key j iff
+ *   j < Lk  and  j <= P  and  (j > P - window  or  j < sinks),
+ * and that out is fp32 or bf16 (out_dtype; bf16: the fp32 result rounded to nearest even).
+ * Key tiles that no row of a query tile sees are not read. The prefill of a model whose
+ * decode steps call tts_attn_decode_paged with the same window and sinks.
+ *
+ * window >= 1 (larger than the sequence: plain causal attention), sinks >= 0. k and v must be
+ * finite for every key a row's 128-key tile shares with it; rows behind a sequence's last key
+ * (another sequence's, or padding) may hold anything.
+ */
+tts_status tts_attn_fwd_varlen_window(const void* q, const void* k, const void* v,
+                                      tts_dtype in_dtype, int64_t total_q, int64_t total_k,
+                                      const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                      int32_t batch, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                      int32_t num_heads_q, int32_t num_heads_kv, int32_t head_dim,
+                                      int32_t window, int32_t sinks, float scale, void* out,
+                                      tts_dtype out_dtype, float* lse, void* workspace,
+                                      size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
  * Deterministic top-k selection over per-row indexer logits.
  *
  * Follows "推理引擎的蝴蝶效应 -- 从V32 模型的输出不一致说起" (section 实验方法和

@@ -150,3 +150,37 @@ def rope_table(max_pos, d):
     a = np.arange(max_pos, dtype=np.float64)[:, None] * 10000.0 ** (
         -np.arange(0, d, 2, dtype=np.float64) / d)
     return np.stack([np.cos(a), np.sin(a)], -1).astype(np.float32)
+
+
+def attend_packed(q, k, v, cu_q, cu_k, scale, window, sinks, w_half):
+    """Windowed causal attention over packed sequences in 64 bits (bottom-right aligned), with
+    the bounds of attend()."""
+    T, hq, d = q.shape
+    G = hq // k.shape[1]
+    out = np.zeros((T, hq, d))
+    lse = np.full((T, hq), -np.inf)
+    tol, tol_l = np.zeros((T, hq, d)), np.full((T, hq), 1e-6)
+    for r in range(len(cu_q) - 1):
+        n, L = int(cu_q[r + 1] - cu_q[r]), int(cu_k[r + 1] - cu_k[r])
+        if n == 0 or L == 0:
+            continue
+        pos = np.arange(n)[:, None] + L - n
+        j = np.arange(L)[None]
+        see = (j <= pos) & ((j > pos - window) | (j < sinks))
+        some = see.any(1)
+        rows = slice(cu_q[r], cu_q[r + 1])
+        for h in range(hq):
+            qq = q[rows, h].astype(np.float64)
+            kk = k[cu_k[r]:cu_k[r + 1], h // G].astype(np.float64)
+            vv = v[cu_k[r]:cu_k[r + 1], h // G].astype(np.float64)
+            x = np.where(see, scale * (qq @ kk.T), -np.inf)
+            size = np.where(see, scale * (np.abs(qq) @ np.abs(kk).T), 0).max(1)
+            m = np.where(some, x.max(1), 0)
+            p = np.exp(x - m[:, None])
+            l = np.where(some, p.sum(1), 1)
+            dx = (d + 16) * 2.0 ** -24 * size + 2.0 ** -18
+            out[rows, h] = p @ vv / l[:, None]
+            lse[rows, h] = np.where(some, m + np.log(l), -np.inf)
+            tol[rows, h] = (p @ np.abs(vv) / l[:, None]) * (w_half * 1.01 + 2.5 * dx)[:, None]
+            tol_l[rows, h] = 2 * dx + 2.0 ** -22 * np.abs(np.where(some, lse[rows, h], 0))
+    return out, lse, tol, tol_l

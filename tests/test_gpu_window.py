@@ -1,0 +1,172 @@
+"""GPU parity for tts_attn_fwd_varlen_window: sliding-window prefill with first tokens that stay
+visible against 64-bit attention, row by row, and against the plain causal entry point where
+the window holds every key."""
+import numpy as np
+import pytest
+import torch
+
+import gqa_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16_HALF = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def tts():
+    import tiled_top_sparse_gb300 as m
+    m.lib()
+    return m
+
+
+def cum(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+
+
+def inputs(seed, lq, lk, hq, hkv, d, dtype, tail=0):
+    """q, k, v on the device; `tail` rows behind the last sequence hold NaN."""
+    g = torch.Generator("cpu")
+    g.manual_seed(seed)
+    t = [torch.randn(int(sum(n)) + tail, h, d, generator=g) for n, h in ((lq, hq), (lk, hkv),
+                                                                         (lk, hkv))]
+    for x in t:
+        if tail:
+            x[-tail:] = float("nan")
+    return [x.to(dtype).cuda() for x in t]
+
+
+def check(tts, seed, lq, lk, hq, hkv, d, window, sinks, dtype=torch.bfloat16,
+          out_dtype=torch.float32, tail=5):
+    lk = lq if lk is None else lk
+    q, k, v = inputs(seed, lq, lk, hq, hkv, d, dtype, tail)
+    cq, ck = cum(lq), cum(lk)
+    T = int(cq[-1])
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, 7.0, dtype=out_dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+
+    def call():
+        return tts.attn_fwd_varlen_window(q, k, v, torch.tensor(cq).cuda(), torch.tensor(ck).cuda(),
+                                          max(lq), max(lk), window, sinks, d ** -0.5, out=out,
+                                          lse=lse, status=st)
+
+    call()
+    tts.check_status(st)
+    h = [x.to(torch.bfloat16).float().cpu().numpy() for x in (q, k, v)]
+    ro, rl, tol, tol_l = ref.attend_packed(h[0][:T], h[1], h[2], cq, ck, d ** -0.5, window, sinks,
+                                           BF16_HALF)
+    if out_dtype == torch.bfloat16:
+        tol = tol + (np.abs(ro) + tol) * BF16_HALF
+    o, l = out.float().cpu().numpy(), lse.cpu().numpy()
+    assert np.array_equal(np.isneginf(l[:T]), np.isneginf(rl))
+    fin = np.isfinite(rl)
+    assert np.all(np.abs(l[:T][fin] - rl[fin]) <= tol_l[fin])
+    err = np.abs(o[:T] - ro)
+    assert np.all(err <= tol), (err - tol).max()
+    assert (o[T:] == 7).all() and (l[T:] == 7).all()
+    a, b = out.clone(), lse.clone()
+    call()
+    assert torch.equal(a, out) and torch.equal(b, lse)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("lq,lk,hq,hkv,window,sinks", [
+    ([700], None, 4, 2, 256, 4),
+    ([1, 129, 385, 256], None, 2, 1, 100, 0),          # ragged; a window inside a tile
+    ([1000], None, 2, 2, 1, 1),                        # only itself and the first
+    ([900, 300], None, 3, 1, 300, 130),                # sinks over a tile border
+    ([640], None, 2, 1, 128, 300),                     # sinks meet the window
+    ([257], None, 2, 1, 10 ** 9, 0),                   # no key ever leaves
+    ([100, 260], [700, 900], 4, 1, 200, 5),            # new tokens behind cached keys
+    ([300, 200], [120, 1], 2, 1, 64, 2),               # more rows than keys: rows that see none
+    ([0, 200, 0], [5, 200, 0], 2, 2, 50, 3),           # empty sequences
+])
+def test_window_parity(tts, d, lq, lk, hq, hkv, window, sinks):
+    check(tts, sum(lq) + d, lq, lk, hq, hkv, d, window, sinks)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_bf16_out_and_fp32_in(tts, d):
+    check(tts, 5, [333, 70], None, 4, 2, d, 96, 4, out_dtype=torch.bfloat16)
+    check(tts, 6, [333, 70], None, 4, 2, d, 96, 4, dtype=torch.float32)
+
+
+def test_many_items_per_cta(tts):
+    """More items than CTAs: the ring, the Q tiles and the accumulators are reused."""
+    check(tts, 7, [1500, 700, 1100], None, 16, 4, 128, 300, 4)
+    check(tts, 8, [1200, 900], None, 32, 8, 64, 200, 130)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_wide_window_equals_causal(tts, d):
+    """A window that holds every key takes the same tiles in the same order as the plain causal
+    call: the same bits."""
+    lens = [500, 129, 1, 300]
+    q, k, v = inputs(9, lens, lens, 4, 2, d, torch.bfloat16)
+    cu = torch.tensor(cum(lens)).cuda()
+    a = tts.attn_fwd_varlen_window(q, k, v, cu, cu, 500, 500, 500, 3, d ** -0.5)
+    b = tts.attn_fwd_varlen(q, k, v, cu, cu, 500, 500, True, d ** -0.5)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_bad_sequences_are_reported(tts):
+    q, k, v = inputs(10, [100, 100], [100, 100], 2, 1, 64, torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 100, 201], dtype=torch.int32, device="cuda")  # past the end
+    out = torch.full(q.shape, 7.0, device="cuda")
+    tts.attn_fwd_varlen_window(q, k, v, cu, cu, 101, 101, 30, 2, 0.125, out=out, status=st)
+    assert int(st.item()) == tts.TTS_DEV_BAD_ARG
+    assert bool((out[100:] == 7).all()) and not bool((out[:100] == 7).all())
+
+
+@pytest.mark.parametrize("f8", [True, False])
+def test_prefill_then_decode(tts, f8):
+    """A prompt through append and windowed prefill, then decode steps over the cache: the
+    prefill's rows equal 64-bit attention over its rotated keys, the steps' rows over the cache."""
+    hq, hkv, d, ps, window, sinks = 8, 2, 128, 64, 200, 4
+    lens, steps = [500, 77, 260], 3
+    pages = sum(-(-(n + steps) // ps) for n in lens)
+    tables = torch.full((3, 10), -1, dtype=torch.int32)
+    perm = torch.randperm(pages, generator=torch.Generator("cpu").manual_seed(1)).int()
+    at = 0
+    for r, n in enumerate(lens):
+        m = -(-(n + steps) // ps)
+        tables[r, :m] = perm[at:at + m]
+        at += m
+    dt = torch.uint8 if f8 else torch.bfloat16
+    kc, vc = (torch.zeros(pages, hkv, ps, d, dtype=dt, device="cuda") for _ in range(2))
+    ks, vs = ((torch.zeros(pages, hkv, device="cuda") for _ in range(2)) if f8 else (None, None))
+    cs = tts.rope_cache(600, d)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = torch.Generator("cpu")
+    g.manual_seed(2)
+    past = [0, 0, 0]
+    for step in range(steps + 1):
+        new = lens if step == 0 else [1, 1, 1]
+        cu = cum(new)
+        qkv = torch.randn(int(cu[-1]), hq + 2 * hkv, d, generator=g).to(torch.bfloat16).cuda()
+        v = qkv[:, hq + hkv:]
+        q, k = tts.rope_kv_append(qkv[:, hq:hq + hkv], v, kc, vc, tables.cuda(),
+                                  torch.tensor(past, dtype=torch.int32).cuda(),
+                                  torch.tensor(cu).cuda(), max(new), k_scale=ks, v_scale=vs,
+                                  cos_sin=cs, q=qkv[:, :hq], want_k=step == 0, status=st)
+        past = [a + b for a, b in zip(past, new)]
+        if step == 0:
+            c = torch.tensor(cu).cuda()
+            out, lse = tts.attn_fwd_varlen_window(q, k, v.contiguous(), c, c, max(new), max(new),
+                                                  window, sinks, d ** -0.5, status=st)
+            want = ref.attend_packed(q.float().cpu().numpy(), k.float().cpu().numpy(),
+                                     v.float().cpu().numpy(), cu, cu, d ** -0.5, window, sinks,
+                                     BF16_HALF)
+        else:
+            out, lse = tts.attn_decode_paged(q, kc, vc, tables.cuda(),
+                                             torch.tensor(past, dtype=torch.int32).cuda(),
+                                             d ** -0.5, k_scale=ks, v_scale=vs, window=window,
+                                             sinks=sinks, status=st)
+            want = ref.attend(q.float().cpu().numpy(), ref.codes_of(kc), ref.codes_of(vc),
+                              None if ks is None else ks.cpu().numpy(),
+                              None if vs is None else vs.cpu().numpy(), tables.numpy(), past, cu,
+                              d ** -0.5, window, sinks, 2.0 ** -11 if f8 else BF16_HALF)
+        tts.check_status(st)
+        assert np.all(np.abs(out.cpu().numpy() - want[0]) <= want[2]), step
+        assert np.all(np.abs(lse.cpu().numpy() - want[1]) <= want[3]), step

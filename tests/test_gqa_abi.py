@@ -111,3 +111,26 @@ def test_visible_keys_brute_force():
                 for j in range(10):
                     want = j <= pos and (w == 0 or j > pos - w or j < s)
                     assert got[j] == want
+
+
+def test_window_refusals(L):
+    import tiled_top_sparse_gb300 as tts
+
+    def window(**kw):
+        a = dict(q=A, k=A, v=A, dt=0, tq=256, tk=256, cq=A, ck=A, b=1, mq=256, mk=256, hq=2,
+                 hkv=1, d=64, window=100, sinks=4, scale=0.125, out=A, odt=0, lse=NUL, ws=A,
+                 wsb=1 << 30, st=NUL, stream=NUL)
+        assert set(kw) <= set(a)
+        a.update(kw)
+        return L.tts_attn_fwd_varlen_window(*a.values())
+
+    for n in ("q", "k", "v", "cq", "ck", "out"):
+        assert window(**{n: NUL}) == tts.TTS_ERR_INVALID_ARG, n
+    for n in ("q", "k", "v", "out"):
+        assert window(**{n: B}) == tts.TTS_ERR_INVALID_ARG, n
+    for kw in (dict(window=0), dict(window=-1), dict(sinks=-1), dict(dt=2), dict(odt=2),
+               dict(hq=3, hkv=2), dict(scale=-1.0), dict(b=0)):
+        assert window(**kw) == tts.TTS_ERR_INVALID_ARG, kw
+    assert window(d=96) == tts.TTS_ERR_UNSUPPORTED
+    assert window(ws=NUL) == tts.TTS_ERR_WORKSPACE
+    assert window(tq=0) == tts.TTS_OK

@@ -6,6 +6,8 @@ no fallback: if the library is missing or fails to load, calls raise.
 
     attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                     causal, scale, out=None, lse=None, workspace=None, status=None)
+    attn_fwd_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                           window, sinks, scale, out=None, lse=None, workspace=None, status=None)
     topk_select(logits, row_starts, row_lens, k, idx=None, status=None)
     sparse_attn_paged(q, kv_cache, page_table, idx, kv_len, scale, dv=512,
                       out=None, lse=None, status=None)
@@ -57,6 +59,7 @@ EXPORTED = (
     "tts_version",
     "tts_attn_workspace_bytes",
     "tts_attn_fwd_varlen",
+    "tts_attn_fwd_varlen_window",
     "tts_topk_select",
     "tts_topk_long_workspace_bytes",
     "tts_topk_select_long",
@@ -105,6 +108,10 @@ def lib() -> ctypes.CDLL:
     L.tts_attn_fwd_varlen.argtypes = [P, P, P, ctypes.c_int, i64, i64, P, P, i32, i32, i32, i32,
                                       i32, i32, i32, f32, P, P, P, ctypes.c_size_t, P, P]
     L.tts_attn_fwd_varlen.restype = ctypes.c_int
+    L.tts_attn_fwd_varlen_window.argtypes = [P, P, P, ctypes.c_int, i64, i64, P, P, i32, i32, i32,
+                                             i32, i32, i32, i32, i32, f32, P, ctypes.c_int, P, P,
+                                             ctypes.c_size_t, P, P]
+    L.tts_attn_fwd_varlen_window.restype = ctypes.c_int
     L.tts_topk_select.argtypes = [P, i64, i32, P, P, i32, P, P, P]
     L.tts_topk_select.restype = ctypes.c_int
     L.tts_topk_long_workspace_bytes.argtypes = [i32, i64, i32]
@@ -234,6 +241,51 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqle
         batch, int(max_seqlen_q), int(max_seqlen_k), hq, hkv, d, int(bool(causal)), float(scale),
         _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _ptr(status), _stream(q.device))
     _check(code, "tts_attn_fwd_varlen")
+    return out, lse
+
+
+def attn_fwd_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, window,
+                           sinks, scale, out=None, lse=None, workspace=None, status=None,
+                           want_lse=True, out_dtype=torch.float32):
+    """Causal sliding-window attention with first tokens that stay visible
+    (tts_attn_fwd_varlen_window): a row sees the last `window` keys up to its own position and
+    the first `sinks`.
+
+    Arguments as attn_fwd_varlen; returns (out [total_q, Hq, d] in out_dtype, or in out's dtype:
+    fp32 or bf16; lse fp32 [total_q, Hq])."""
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _cuda_contig(t, n)
+        _need(t.dim() == 3, f"{n} must be [tokens, heads, head_dim]")
+    _need(q.dtype == k.dtype == v.dtype and q.dtype in (torch.bfloat16, torch.float32),
+          "q, k, v must share dtype bf16 or fp32")
+    _need(k.shape == v.shape, "k and v must have the same shape")
+    _cuda_contig(cu_seqlens_q, "cu_seqlens_q", torch.int32)
+    _cuda_contig(cu_seqlens_k, "cu_seqlens_k", torch.int32)
+    total_q, hq, d = q.shape
+    total_k, hkv, d2 = k.shape
+    _need(d == d2, "head_dim mismatch")
+    batch = cu_seqlens_q.numel() - 1
+    _need(batch >= 1 and cu_seqlens_k.numel() == batch + 1, "cu_seqlens sizes must be batch+1")
+    if out is None:
+        out = torch.empty((total_q, hq, d), dtype=out_dtype, device=q.device)
+    _cuda_contig(out, "out")
+    _need(out.dtype in (torch.float32, torch.bfloat16) and out.shape == q.shape,
+          "out must be fp32 or bf16 [total_q, Hq, d]")
+    if lse is None and want_lse:
+        lse = torch.empty((total_q, hq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _cuda_contig(lse, "lse", torch.float32)
+        _need(tuple(lse.shape) == (total_q, hq), "lse shape")
+    need = attn_workspace_bytes(total_q, total_k, hq, hkv, d, q.dtype)
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(lib().tts_attn_fwd_varlen_window(
+        _ptr(q), _ptr(k), _ptr(v), TTS_F32 if q.dtype == torch.float32 else TTS_BF16, total_q,
+        total_k, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), batch, int(max_seqlen_q),
+        int(max_seqlen_k), hq, hkv, d, int(window), int(sinks), float(scale), _ptr(out),
+        TTS_BF16 if out.dtype == torch.bfloat16 else TTS_F32, _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(status), _stream(q.device)),
+        "tts_attn_fwd_varlen_window")
     return out, lse
 
 

@@ -73,50 +73,14 @@ inline bool cache_shape_built(int32_t d, int32_t page_size, int32_t num_pages, i
          (int64_t)num_pages * hkv <= 0x7FFFFFFFLL;
 }
 
-}  // namespace
-
-extern "C" {
-
-const char* tts_status_string(int status) {
-  switch (status) {
-    case TTS_OK: return "ok";
-    case TTS_ERR_INVALID_ARG: return "invalid argument";
-    case TTS_ERR_UNSUPPORTED: return "unsupported shape or option";
-    case TTS_ERR_CUDA: return "CUDA error";
-    case TTS_ERR_INDEX_RANGE: return "device reported an out-of-range index (entry skipped)";
-    case TTS_ERR_DEVICE_TIMEOUT: return "device reported an expired bounded wait";
-    case TTS_ERR_WORKSPACE: return "workspace missing or too small";
-    default: return "unknown status";
-  }
-}
-
-int tts_status_from_device(uint32_t dev_status) {
-  if (dev_status & TTS_DEV_TIMEOUT) return TTS_ERR_DEVICE_TIMEOUT;
-  if (dev_status & TTS_DEV_BAD_ARG) return TTS_ERR_INVALID_ARG;
-  if (dev_status & TTS_DEV_INDEX_RANGE) return TTS_ERR_INDEX_RANGE;
-  return TTS_OK;
-}
-
-int tts_version(void) { return 100; }
-
-size_t tts_attn_workspace_bytes(int64_t total_q, int64_t total_k, int32_t num_heads_q,
-                                int32_t num_heads_kv, int32_t head_dim, tts_dtype in_dtype) {
-  if (total_q < 0 || total_k < 0 || num_heads_q < 1 || num_heads_kv < 1 || head_dim < 1) return 0;
-  // 256 bytes for the work-item counter of the persistent kernel, then (fp32 inputs)
-  // the bf16 copies of q, k and v.
-  if (in_dtype != TTS_F32) return kCounterBytes;
-  const size_t nq = (size_t)total_q * num_heads_q * head_dim * 2;
-  const size_t nk = (size_t)total_k * num_heads_kv * head_dim * 2;
-  return kCounterBytes + align_up(nq, 256) + 2 * align_up(nk, 256);
-}
-
-tts_status tts_attn_fwd_varlen(const void* q, const void* k, const void* v, tts_dtype in_dtype,
-                               int64_t total_q, int64_t total_k, const int32_t* cu_seqlens_q,
-                               const int32_t* cu_seqlens_k, int32_t batch, int32_t max_seqlen_q,
-                               int32_t max_seqlen_k, int32_t num_heads_q, int32_t num_heads_kv,
-                               int32_t head_dim, int32_t causal, float scale, float* out,
-                               float* lse, void* workspace, size_t workspace_bytes,
-                               uint32_t* dev_status, void* stream) {
+// tts_attn_fwd_varlen and (window > 0) tts_attn_fwd_varlen_window.
+tts_status attn_varlen(const void* q, const void* k, const void* v, tts_dtype in_dtype,
+                       int64_t total_q, int64_t total_k, const int32_t* cu_seqlens_q,
+                       const int32_t* cu_seqlens_k, int32_t batch, int32_t max_seqlen_q,
+                       int32_t max_seqlen_k, int32_t num_heads_q, int32_t num_heads_kv,
+                       int32_t head_dim, int32_t causal, int32_t window, int32_t sinks,
+                       float scale, void* out, tts_dtype out_dtype, float* lse, void* workspace,
+                       size_t workspace_bytes, uint32_t* dev_status, void* stream) {
   if (q == nullptr || k == nullptr || v == nullptr || cu_seqlens_q == nullptr ||
       cu_seqlens_k == nullptr || out == nullptr)
     return TTS_ERR_INVALID_ARG;
@@ -170,13 +134,82 @@ tts_status tts_attn_fwd_varlen(const void* q, const void* k, const void* v, tts_
   a.d = head_dim;
   a.causal = causal;
   a.scale = scale;
-  a.out = out;
+  a.window = window;
+  a.sinks = sinks;
+  a.out_bf16 = out_dtype == TTS_BF16;
+  a.out = static_cast<float*>(out);
   a.lse = lse;
   a.dev_status = dev_status;
   int drv = 0;
   cudaError_t e = launch_attn_fwd(a, &drv, st);
   if (drv != 0) return TTS_ERR_CUDA;
   return from_cuda(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+const char* tts_status_string(int status) {
+  switch (status) {
+    case TTS_OK: return "ok";
+    case TTS_ERR_INVALID_ARG: return "invalid argument";
+    case TTS_ERR_UNSUPPORTED: return "unsupported shape or option";
+    case TTS_ERR_CUDA: return "CUDA error";
+    case TTS_ERR_INDEX_RANGE: return "device reported an out-of-range index (entry skipped)";
+    case TTS_ERR_DEVICE_TIMEOUT: return "device reported an expired bounded wait";
+    case TTS_ERR_WORKSPACE: return "workspace missing or too small";
+    default: return "unknown status";
+  }
+}
+
+int tts_status_from_device(uint32_t dev_status) {
+  if (dev_status & TTS_DEV_TIMEOUT) return TTS_ERR_DEVICE_TIMEOUT;
+  if (dev_status & TTS_DEV_BAD_ARG) return TTS_ERR_INVALID_ARG;
+  if (dev_status & TTS_DEV_INDEX_RANGE) return TTS_ERR_INDEX_RANGE;
+  return TTS_OK;
+}
+
+int tts_version(void) { return 100; }
+
+size_t tts_attn_workspace_bytes(int64_t total_q, int64_t total_k, int32_t num_heads_q,
+                                int32_t num_heads_kv, int32_t head_dim, tts_dtype in_dtype) {
+  if (total_q < 0 || total_k < 0 || num_heads_q < 1 || num_heads_kv < 1 || head_dim < 1) return 0;
+  // 256 bytes for the work-item counter of the persistent kernel, then (fp32 inputs)
+  // the bf16 copies of q, k and v.
+  if (in_dtype != TTS_F32) return kCounterBytes;
+  const size_t nq = (size_t)total_q * num_heads_q * head_dim * 2;
+  const size_t nk = (size_t)total_k * num_heads_kv * head_dim * 2;
+  return kCounterBytes + align_up(nq, 256) + 2 * align_up(nk, 256);
+}
+
+tts_status tts_attn_fwd_varlen(const void* q, const void* k, const void* v, tts_dtype in_dtype,
+                               int64_t total_q, int64_t total_k, const int32_t* cu_seqlens_q,
+                               const int32_t* cu_seqlens_k, int32_t batch, int32_t max_seqlen_q,
+                               int32_t max_seqlen_k, int32_t num_heads_q, int32_t num_heads_kv,
+                               int32_t head_dim, int32_t causal, float scale, float* out,
+                               float* lse, void* workspace, size_t workspace_bytes,
+                               uint32_t* dev_status, void* stream) {
+  return attn_varlen(q, k, v, in_dtype, total_q, total_k, cu_seqlens_q, cu_seqlens_k, batch,
+                     max_seqlen_q, max_seqlen_k, num_heads_q, num_heads_kv, head_dim, causal, 0, 0,
+                     scale, out, TTS_F32, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
+tts_status tts_attn_fwd_varlen_window(const void* q, const void* k, const void* v,
+                                      tts_dtype in_dtype, int64_t total_q, int64_t total_k,
+                                      const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                      int32_t batch, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                      int32_t num_heads_q, int32_t num_heads_kv, int32_t head_dim,
+                                      int32_t window, int32_t sinks, float scale, void* out,
+                                      tts_dtype out_dtype, float* lse, void* workspace,
+                                      size_t workspace_bytes, uint32_t* dev_status,
+                                      void* stream) {
+  if (window < 1 || sinks < 0) return TTS_ERR_INVALID_ARG;
+  if (out_dtype != TTS_F32 && out_dtype != TTS_BF16) return TTS_ERR_INVALID_ARG;
+  return attn_varlen(q, k, v, in_dtype, total_q, total_k, cu_seqlens_q, cu_seqlens_k, batch,
+                     max_seqlen_q, max_seqlen_k, num_heads_q, num_heads_kv, head_dim, 1, window,
+                     sinks, scale, out, out_dtype, lse, workspace, workspace_bytes, dev_status,
+                     stream);
 }
 
 tts_status tts_topk_select(const float* logits, int64_t row_stride, int32_t rows,

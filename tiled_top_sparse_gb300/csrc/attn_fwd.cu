@@ -29,7 +29,16 @@
 // 256 and is exact in real arithmetic (the final O / l cancels the offset).
 // No S or P matrix ever touches global memory, so there is no piece buffer
 // to index (the q0*N overflow of the vision write-up cannot happen here).
+//
+// With a sliding window (kWin, causal): row i at position P = i + Lk - Lq sees keys
+// (P - window, P] and the first `sinks`, so an item streams only the tiles that one of its
+// rows sees: the sinks' tiles, then the window's. The work per row is then 4 d min(P + 1,
+// window + sinks) whatever the prompt's length. Rows of a last tile behind the sequence's
+// end (another sequence's, or padding) are cleared in V before the product, so that what
+// they hold cannot reach a row through a weight of zero.
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -105,6 +114,12 @@ struct AttnParams {
   const float* q_scale;  // e4m3 path: [total_q, hq] per (token, head)
   const float* k_scale;  // e4m3 path: [hkv] per KV head
 };
+struct WindowParams : AttnParams {
+  int window, sinks;  // keys up to a row's own, first keys that stay visible
+  int out_bf16;       // out is bf16
+};
+template <bool kWin>
+using ParamsFor = std::conditional_t<kWin, WindowParams, AttnParams>;
 
 // Load one 128-row tile (all boxes) of a [tokens, heads, D] tensor (F8: of e4m3 q / k).
 template <int D, bool F8 = false>
@@ -164,8 +179,16 @@ struct Item {
   int64_t q_start, k_start, Lq, Lk, q_lo;
   int h, g, n_tiles;  // n_tiles: K/V tiles streamed = max(n0, n1)
   int n0, n1;         // tiles each warpgroup needs (0: no rows, or no visible key)
+  int n_sink, win0;   // kWin: streamed tiles are [0, n_sink), then win0, win0 + 1, ...
 };
-__device__ __forceinline__ bool decode_item(const AttnParams& p, int it, Item& w, bool* bad) {
+// Key tile that an item streams as its j-th.
+template <bool kWin>
+__device__ __forceinline__ int key_tile(const Item& w, int j) {
+  if constexpr (kWin) return j < w.n_sink ? j : w.win0 + (j - w.n_sink);
+  return j;
+}
+template <bool kWin>
+__device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, Item& w, bool* bad) {
   const int h = it % p.hq;
   const int t = it / p.hq;
   const int b = t % p.batch;
@@ -207,6 +230,21 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int it, Item& w
   w.n_tiles = (int)((kv_end + kBlockN - 1) / kBlockN);
   w.n0 = (int)((kv_end0 + kBlockN - 1) / kBlockN);
   w.n1 = (int)((kv_end1 + kBlockN - 1) / kBlockN);
+  if constexpr (kWin) {
+    // First key inside the window of the first row that sees any (a later row's starts later).
+    const int64_t off = Lk - Lq;
+    const int64_t row = kv_end0 > 0 ? (q_lo > 0 ? q_lo : 0) : q_lo + kBlockM;
+    const int64_t lo = row + off + 1 - p.window;
+    const int64_t lo1 = q_lo + kBlockM + off + 1 - p.window;  // of the second warpgroup
+    w.win0 = lo > 0 ? (int)(lo / kBlockN) : 0;
+    const int64_t sinks = p.sinks < lo1 ? p.sinks : lo1;  // more are inside every window
+    const int64_t ns = sinks > 0 ? (sinks + kBlockN - 1) / kBlockN : 0;
+    w.n_sink = (int)(ns < w.win0 ? ns : w.win0);
+    const int skip = w.win0 - w.n_sink;  // tiles in between that no row sees
+    w.n_tiles = w.n_tiles > 0 ? w.n_tiles - skip : 0;
+    w.n0 = w.n0 > 0 ? w.n0 - skip : 0;
+    w.n1 = w.n1 > 0 ? w.n1 - skip : 0;
+  }
   return true;
 }
 
@@ -214,9 +252,9 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int it, Item& w
 // Per CTA, items flow through a two-slot ring (producer -> MMA warp + softmax warps);
 // barrier phases run on counters that continue across items: gt = K/V tiles so far
 // (ring slots, S / P phases), nq = items with at least one tile (Q, O phases).
-template <int D, bool F8 = false>
+template <int D, bool F8 = false, bool kWin = false>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const AttnParams p) {
+    attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const ParamsFor<kWin> p) {
   using C = AttnCfg<D, F8>;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -294,7 +332,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (gj >= NS && !mbar_wait(smem_u32(kOneKV ? &bar_kv_empty[st] : &bar_k_empty[st]),
                                    empty_ph, abort_flag, p.dev_status))
           return false;
-        const int tok = (int)(w.k_start + (int64_t)j * kBlockN);
+        const int tok = (int)(w.k_start + (int64_t)key_tile<kWin>(w, j) * kBlockN);
         const uint32_t bk = smem_u32(&bar_k[st]);
         mbar_arrive_expect_tx(bk, kOneKV ? C::kTileBytes + C::kVTileBytes : C::kTileBytes);
         load_tile<D, F8>(sK(st), &maps.k, &maps.k_t, bk, w.g, tok);
@@ -310,7 +348,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             return false;
           mbar_arrive_expect_tx(bv, C::kVTileBytes);
         }
-        const int tok = (int)(w.k_start + (int64_t)j * kBlockN);
+        const int tok = (int)(w.k_start + (int64_t)key_tile<kWin>(w, j) * kBlockN);
         if constexpr (C::kTail != 0) {
 #pragma unroll
           for (int b = 0; b < C::kVBoxes; ++b)
@@ -332,7 +370,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             break;
           }
           bool bad;
-          if (decode_item(p, it, w, &bad)) break;
+          if (decode_item<kWin>(p, it, w, &bad)) break;
           if (bad && p.dev_status) atomicOr(p.dev_status, kDevBadArg);
         }
         const int slot = ni & 1;
@@ -413,7 +451,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (it < 0) break;
       Item w;
       bool bad;
-      decode_item(p, it, w, &bad);
+      decode_item<kWin>(p, it, w, &bad);
       const int n = w.n_tiles, n0 = w.n0, n1 = w.n1;
       if (n == 0) continue;
       const int st0 = gt % NS;
@@ -552,6 +590,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t O_row = tmem + 256 + wg * 128 + lane_off;
     float4* stage = reinterpret_cast<float4*>(stage_base + (warp - 4) * 4096);
     int ni = 0, nq = 0, gt = 0;
+    int ring = 0;  // kWin: K/V tiles streamed before this item
     bool ok = true;
     while (ok) {
       const int slot = ni & 1;
@@ -565,7 +604,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (it < 0) break;
       Item w;
       bool bad;
-      decode_item(p, it, w, &bad);
+      decode_item<kWin>(p, it, w, &bad);
       const int n_tiles = wg == 0 ? w.n0 : w.n1;  // tiles this warpgroup's rows can see
       const int64_t Lq = w.Lq, Lk = w.Lk;
       const int64_t i = w.q_lo + wg * kBlockM + row;  // query row within the sequence
@@ -583,6 +622,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         c *= f;
         sc *= f;
       }
+      // kWin: keys [win_lo, limit) and [0, sinks) are visible to this row
+      int64_t win_lo = 0;
+      if constexpr (kWin) win_lo = i + (Lk - Lq) + 1 - p.window;
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < n_tiles; ++j) {
         const int gj = gt + j;
@@ -599,9 +641,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               tmem_ld32_max(S_row + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[q4 * 32]));
         tmem_ld_wait();
         float* s = reinterpret_cast<float*>(sr);
-        const int64_t kv0 = (int64_t)j * kBlockN;
+        const int64_t kv0 = (int64_t)key_tile<kWin>(w, j) * kBlockN;
         float tile_max = fmaxf(fmax3(part_max[0], part_max[1], part_max[2]), part_max[3]);
-        if (kv0 + kBlockN > limit) {  // masked columns must not count in the max
+        if constexpr (kWin) {
+          if (kv0 + kBlockN > limit || (kv0 < win_lo && kv0 + kBlockN > p.sinks)) {
+            // visible columns of the tile: [0, sk) and [lo, lim)
+            const int64_t span = limit - kv0, first = win_lo - kv0, kept = p.sinks - kv0;
+            const int lim = span < 128 ? (int)(span < 0 ? 0 : span) : 128;
+            const int lo = first > 0 ? (int)(first < 128 ? first : 128) : 0;
+            const int sk = kept > 0 ? (int)(kept < 128 ? kept : 128) : 0;
+  #pragma unroll
+            for (int cc = 0; cc < 128; ++cc)
+              if (cc >= lim || (cc < lo && cc >= sk)) s[cc] = -INFINITY;
+            tile_max = row_max<128>(s);
+          }
+          if (kv0 + kBlockN > Lk) {  // rows behind the sequence: cleared once V has landed
+            const int gr = ring + j, st = gr % NS;
+            const bool landed = mbar_wait(smem_u32(kOneKV ? &bar_k[st] : &bar_v[st]),
+                                          (gr / NS) & 1, abort_flag, p.dev_status);
+            ok = __all_sync(0xFFFFFFFFu, landed);
+            if (!ok) break;
+            if (row >= Lk - kv0) {
+              constexpr int kRow = C::kVBoxBytes / kBlockN;  // bytes of a row in one box
+  #pragma unroll 1
+              for (int b = 0; b < C::kVBoxes; ++b)
+  #pragma unroll 1
+                for (int o = 0; o < kRow; o += 16)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                   sV(st) + b * C::kVBoxBytes + row * kRow + o),
+                               "r"(0)
+                               : "memory");
+            }
+            fence_proxy_async_smem();
+          }
+        } else if (kv0 + kBlockN > limit) {  // masked columns must not count in the max
           const int64_t lim = limit - kv0;
   #pragma unroll
           for (int cc = 0; cc < 128; ++cc)
@@ -659,6 +732,54 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // Rows leave TMEM one per thread; this warp's 4 KB staging slice turns them into
       // whole 128-byte row segments, so each store instruction writes full lines.
       const int64_t row0 = w.q_lo + wg * kBlockM + (warp & 3) * 32;  // this warp's first row
+      bool rounded = false;
+      if constexpr (kWin) rounded = p.out_bf16 != 0;
+      if (rounded) {
+        // 64 columns at a time, rounded to bf16 (nearest even): 128-byte row segments again
+        // (32 for the d = 80 tail)
+        uint4* stage16 = reinterpret_cast<uint4*>(stage);
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 64) {
+          const int cw = (D - c0 < 64) ? D - c0 : 64;  // 64, or 16 for the d = 80 tail
+#pragma unroll
+          for (int h = 0; h < 64; h += 32) {
+            if (h >= cw) continue;
+            uint32_t o[32];
+            if (n_tiles > 0) {
+              if (cw - h >= 32)
+                tmem_ld32(O_row + c0 + h, o);
+              else
+                tmem_ld16(O_row + c0 + h, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) o[q] = 0u;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (h + 8 * q < cw) {
+                uint32_t v[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                  v[z] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * z]) * inv_l,
+                                     __uint_as_float(o[8 * q + 2 * z + 1]) * inv_l);
+                stage16[lane * 8 + ((h / 8 + q) ^ (lane & 7))] = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+          }
+          __syncwarp();
+          const int lpr = cw / 8;  // lanes per row segment
+          for (int rr = 0; rr < 32; rr += 32 / lpr) {
+            const int r = rr + lane / lpr, q = lane % lpr;
+            const uint4 v = stage16[r * 8 + (q ^ (r & 7))];
+            const int64_t ii = row0 + r;
+            if (ii >= 0 && ii < Lq)
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) +
+                                        ((w.q_start + ii) * p.hq + w.h) * (int64_t)D + c0 + 8 * q) =
+                  v;
+          }
+          __syncwarp();
+        }
+      } else {
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
         constexpr int kW = 32;
@@ -693,10 +814,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         __syncwarp();
       }
+      }
       if (i >= 0 && i < Lq && p.lse != nullptr)
         p.lse[(w.q_start + i) * p.hq + w.h] =
             (l > 0.f) ? m_ref * sc + log2f(l) * 0.69314718055994531f : -INFINITY;
       gt += n_tiles;
+      if constexpr (kWin) ring += w.n_tiles;
       if (n_tiles > 0) ++nq;
     }
   }
@@ -718,7 +841,7 @@ __global__ void f32_to_bf16_kernel(const float4* __restrict__ in, uint2* __restr
   }
 }
 
-template <int D, bool F8 = false>
+template <int D, bool F8 = false, bool kWin = false>
 cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
   using C = AttnCfg<D, F8>;
   AttnMaps maps;
@@ -753,7 +876,7 @@ cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
     maps.k_t = maps.k;
     maps.v_t = maps.v;
   }
-  AttnParams p;
+  ParamsFor<kWin> p;
   p.cu_q = a.cu_q;
   p.cu_k = a.cu_k;
   p.out = a.out;
@@ -772,6 +895,11 @@ cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.q_scale = a.q_scale;
   p.k_scale = a.k_scale;
+  if constexpr (kWin) {
+    p.window = a.window;
+    p.sinks = a.sinks;
+    p.out_bf16 = a.out_bf16 ? 1 : 0;
+  }
   const int64_t items = (int64_t)a.batch * p.pairs_max * a.hq;
   if (items == 0) return cudaSuccess;
   if (items > 0x7FFFFFFF || a.work_counter == nullptr) return cudaErrorInvalidConfiguration;
@@ -783,18 +911,27 @@ cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // One persistent CTA per SM (the kernel's shared memory and TMEM allow one).
   const int grid = (int)(items < sms ? items : sms);
-  e = cudaFuncSetAttribute(attn_fwd_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(attn_fwd_kernel<D, F8, kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmemBytes);
   if (e != cudaSuccess) return e;
   e = cudaMemsetAsync(a.work_counter, 0, sizeof(uint32_t), stream);
   if (e != cudaSuccess) return e;
-  attn_fwd_kernel<D, F8><<<grid, kAttnThreads, C::kSmemBytes, stream>>>(maps, p);
+  attn_fwd_kernel<D, F8, kWin><<<grid, kAttnThreads, C::kSmemBytes, stream>>>(maps, p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_attn_fwd(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
+  if (a.window > 0) {
+    if (a.fp8) return cudaErrorInvalidValue;
+    switch (a.d) {
+      case 64: return launch_d<64, false, true>(a, drv_err, stream);
+      case 80: return launch_d<80, false, true>(a, drv_err, stream);
+      case 128: return launch_d<128, false, true>(a, drv_err, stream);
+      default: return cudaErrorInvalidValue;
+    }
+  }
   switch (a.d) {
     case 64: return a.fp8 ? cudaErrorInvalidValue : launch_d<64>(a, drv_err, stream);
     case 80: return a.fp8 ? cudaErrorInvalidValue : launch_d<80>(a, drv_err, stream);

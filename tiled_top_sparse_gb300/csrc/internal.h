@@ -94,6 +94,8 @@ struct AttnArgs {
   bool fp8 = false;        // q, k are e4m3 codes with the scales below (head_dim 128)
   const float* q_scale = nullptr;  // [total_q, hq]
   const float* k_scale = nullptr;  // [hkv]
+  int window = 0, sinks = 0;       // window > 0: the sliding-window kernel (causal)
+  bool out_bf16 = false;           // with a window: out is bf16 instead of fp32
 };
 // Returns cudaSuccess or the first error; *drv_err receives a CUresult from tensor-map encoding.
 cudaError_t launch_attn_fwd(const AttnArgs& a, int* drv_err, cudaStream_t stream);
