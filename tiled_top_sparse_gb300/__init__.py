@@ -253,39 +253,43 @@ def attn_fwd_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, ma
 
     Arguments as attn_fwd_varlen; returns (out [total_q, Hq, d] in out_dtype, or in out's dtype:
     fp32 or bf16; lse fp32 [total_q, Hq])."""
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _cuda_contig(t, n)
-        _need(t.dim() == 3, f"{n} must be [tokens, heads, head_dim]")
-    _need(q.dtype == k.dtype == v.dtype and q.dtype in (torch.bfloat16, torch.float32),
-          "q, k, v must share dtype bf16 or fp32")
-    _need(k.shape == v.shape, "k and v must have the same shape")
-    _cuda_contig(cu_seqlens_q, "cu_seqlens_q", torch.int32)
-    _cuda_contig(cu_seqlens_k, "cu_seqlens_k", torch.int32)
-    total_q, hq, d = q.shape
-    total_k, hkv, d2 = k.shape
-    _need(d == d2, "head_dim mismatch")
+    dev = _device_of(q, "q")
+    dt, qshape, kshape = q.dtype, q.shape, k.shape
+    if dt != torch.bfloat16 and dt != torch.float32:
+        _refuse("q, k, v must share dtype bf16 or fp32")
+    if len(qshape) != 3 or len(kshape) != 3 or v.shape != kshape or qshape[2] != kshape[2]:
+        _refuse("q, k, v must be [tokens, heads, head_dim], k and v of the same shape")
+    total_q, hq, d = qshape
+    total_k, hkv = kshape[0], kshape[1]
     batch = cu_seqlens_q.numel() - 1
-    _need(batch >= 1 and cu_seqlens_k.numel() == batch + 1, "cu_seqlens sizes must be batch+1")
+    if batch < 1 or cu_seqlens_k.numel() != batch + 1:
+        _refuse("cu_seqlens sizes must be batch+1")
     if out is None:
-        out = torch.empty((total_q, hq, d), dtype=out_dtype, device=q.device)
-    _cuda_contig(out, "out")
-    _need(out.dtype in (torch.float32, torch.bfloat16) and out.shape == q.shape,
-          "out must be fp32 or bf16 [total_q, Hq, d]")
+        out = torch.empty(qshape, dtype=out_dtype, device=q.device)
+    odt = out.dtype
+    if out.shape != qshape or (odt != torch.bfloat16 and odt != torch.float32):
+        _refuse("out must be fp32 or bf16 [total_q, Hq, head_dim]")
     if lse is None and want_lse:
         lse = torch.empty((total_q, hq), dtype=torch.float32, device=q.device)
+    lp = None
     if lse is not None:
-        _cuda_contig(lse, "lse", torch.float32)
-        _need(tuple(lse.shape) == (total_q, hq), "lse shape")
-    need = attn_workspace_bytes(total_q, total_k, hq, hkv, d, q.dtype)
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        if lse.shape != qshape[:2]:
+            _refuse("lse must be [total_q, Hq]")
+        lp = _arg(lse, "lse", dev, torch.float32)
+    need = attn_workspace_bytes(total_q, total_k, hq, hkv, d, dt)
+    have = 0 if workspace is None else workspace.nbytes
+    if have < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(lib().tts_attn_fwd_varlen_window(
-        _ptr(q), _ptr(k), _ptr(v), TTS_F32 if q.dtype == torch.float32 else TTS_BF16, total_q,
-        total_k, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), batch, int(max_seqlen_q),
-        int(max_seqlen_k), hq, hkv, d, int(window), int(sinks), float(scale), _ptr(out),
-        TTS_BF16 if out.dtype == torch.bfloat16 else TTS_F32, _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(status), _stream(q.device)),
-        "tts_attn_fwd_varlen_window")
+        have = need
+    wp = _arg(workspace, "workspace", dev, workspace.dtype) if have else None
+    _call((_lib or lib()).tts_attn_fwd_varlen_window, "tts_attn_fwd_varlen_window", dev,
+          _arg(q, "q", dev, dt), _arg(k, "k", dev, dt), _arg(v, "v", dev, dt),
+          TTS_F32 if dt == torch.float32 else TTS_BF16, total_q, total_k,
+          _arg(cu_seqlens_q, "cu_seqlens_q", dev, torch.int32),
+          _arg(cu_seqlens_k, "cu_seqlens_k", dev, torch.int32), batch, int(max_seqlen_q),
+          int(max_seqlen_k), hq, hkv, d, int(window), int(sinks), float(scale),
+          _arg(out, "out", dev, odt), TTS_BF16 if odt == torch.bfloat16 else TTS_F32, lp, wp, have,
+          None if status is None else _arg(status, "status", dev, torch.int32))
     return out, lse
 
 
@@ -552,32 +556,70 @@ def attn_fwd_varlen_fp8(q8, q_scale, k8, k_scale, v, cu_seqlens_q, cu_seqlens_k,
     return out, lse
 
 
-def _token_rows(t, name):
-    """[tokens, heads, head_dim] bf16 whose heads are contiguous; returns the token stride.
-    Views of a packed projection pass without a copy."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3,
-          f"{name} must be a CUDA bf16 tensor [tokens, heads, head_dim]")
-    s = t.stride()
-    _need(s[2] == 1 and (s[1] == t.shape[2] or t.shape[1] == 1),
-          f"{name}: the heads of a token must be contiguous")
-    return s[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+# The calls of a decode step are short on the GPU, so their bindings look at each tensor once:
+# `_arg` checks one and returns its address.
+def _arg(t, name, dev, dtype):
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        _cuda_contig(t, name, dtype)
+        raise ValueError(f"{name} must be on cuda:{dev} like the call's other tensors")
+    return t.data_ptr()
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale):
-    """Checks a grouped-query cache and returns its dtype code."""
-    f8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _cuda_contig(t, n)
-        _need(t.dim() == 4 and t.dtype == k_cache.dtype and (f8 or t.dtype == torch.bfloat16),
-              f"{n} must be [pages, heads_kv, page_size, head_dim] in bf16, or uint8 / "
-              "float8_e4m3fn codes")
-    _need(k_cache.shape == v_cache.shape, "k_cache and v_cache must have the same shape")
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _need((t is not None) == f8, f"{n} goes with an e4m3 cache")
-        if f8:
-            _cuda_contig(t, n, torch.float32)
-            _need(tuple(t.shape) == tuple(k_cache.shape[:2]), f"{n} must be [pages, heads_kv]")
-    return TTS_E4M3 if f8 else TTS_BF16
+def _refuse(msg):
+    raise ValueError(msg)
+
+
+def _device_of(t, name):
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        _refuse(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _call(fn, what, dev, *args):
+    """Call fn on `dev`'s current stream, with that device current for the call."""
+    if dev == torch.cuda.current_device():
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if code != TTS_OK:
+        raise TTSError(code, what)
+
+
+def _token_rows(t, name, dev, heads, d):
+    """Address and token stride of [tokens, heads, d] bf16 whose heads are contiguous: views of
+    a packed projection pass without a copy."""
+    s0, s1, s2 = t.stride()
+    if t.dtype != torch.bfloat16 or t.get_device() != dev or s2 != 1 or (s1 != d and heads != 1):
+        _refuse(f"{name} must be bf16 [tokens, heads, head_dim] on cuda:{dev}, the heads of a token "
+                "contiguous")
+    return t.data_ptr(), (s0 if t.shape[0] > 1 else heads * d)
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, dev):
+    """Checks a grouped-query cache; returns its dtype code, shape and the four addresses."""
+    dt = k_cache.dtype
+    shape = k_cache.shape
+    f8 = dt in _CODES
+    if len(shape) != 4 or not (f8 or dt == torch.bfloat16):
+        _refuse("k_cache must be [pages, heads_kv, page_size, head_dim] in bf16, or uint8 / "
+                "float8_e4m3fn codes")
+    if v_cache.shape != shape:
+        _refuse("k_cache and v_cache must have the same shape")
+    if f8 != (k_scale is not None) or f8 != (v_scale is not None):
+        _refuse("k_scale and v_scale go with an e4m3 cache")
+    ks = vs = None
+    if f8:
+        if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+            _refuse("k_scale and v_scale must be [pages, heads_kv]")
+        ks = _arg(k_scale, "k_scale", dev, torch.float32)
+        vs = _arg(v_scale, "v_scale", dev, torch.float32)
+    return (TTS_E4M3 if f8 else TTS_BF16, shape, _arg(k_cache, "k_cache", dev, dt),
+            _arg(v_cache, "v_cache", dev, dt), ks, vs)
 
 
 def rope_kv_append(k, v, k_cache, v_cache, page_tables, past_lens, cu_new, max_new, k_scale=None,
@@ -591,50 +633,59 @@ def rope_kv_append(k, v, k_cache, v_cache, page_tables, past_lens, cu_new, max_n
     int32 [batch], cu_new int32 [batch + 1], cos_sin of rope_cache or None (no rotation). The
     caches and scales are written in place. Returns (q_out bf16 [tokens, Hq, d] or None, k_out
     bf16 [tokens, Hkv, d]; k_out is None unless given or asked for with want_k)."""
-    code = _cache(k_cache, v_cache, k_scale, v_scale)
-    pages, hkv, ps, d = k_cache.shape
-    ks, vs = _token_rows(k, "k"), _token_rows(v, "v")
-    total = k.shape[0]
-    _need(k.shape == v.shape and tuple(k.shape[1:]) == (hkv, d), "k, v [tokens, Hkv, d]")
-    _cuda_contig(page_tables, "page_tables", torch.int32)
-    _cuda_contig(past_lens, "past_lens", torch.int32)
-    _cuda_contig(cu_new, "cu_new", torch.int32)
+    dev = _device_of(k, "k")
+    code, (pages, hkv, ps, d), kc, vc, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    kshape = k.shape
+    if len(kshape) != 3 or kshape[1] != hkv or kshape[2] != d or v.shape != kshape:
+        _refuse("k, v must be [tokens, Hkv, head_dim] with the cache's heads")
+    total = kshape[0]
+    kp, k_stride = _token_rows(k, "k", dev, hkv, d)
+    vp, v_stride = _token_rows(v, "v", dev, hkv, d)
     batch = past_lens.numel()
-    _need(page_tables.dim() == 2 and page_tables.shape[0] == batch and
-          cu_new.numel() == batch + 1, "page_tables [batch, max_pages], cu_new [batch + 1]")
-    max_pos = 0
+    tshape = page_tables.shape
+    if len(tshape) != 2 or tshape[0] != batch or cu_new.numel() != batch + 1:
+        _refuse("page_tables must be [batch, max_pages], past_lens [batch], cu_new [batch + 1]")
+    csp, max_pos = None, 0
     if cos_sin is not None:
-        _cuda_contig(cos_sin, "cos_sin", torch.float32)
-        _need(cos_sin.dim() == 3 and tuple(cos_sin.shape[1:]) == (d // 2, 2),
-              "cos_sin must be [max_pos, head_dim/2, 2]")
-        max_pos = cos_sin.shape[0]
-    hq, qs = 0, 0
+        cshape = cos_sin.shape
+        if len(cshape) != 3 or cshape[1] != d // 2 or cshape[2] != 2:
+            _refuse("cos_sin must be [max_pos, head_dim/2, 2]")
+        csp, max_pos = _arg(cos_sin, "cos_sin", dev, torch.float32), cshape[0]
+    qp, q_stride, hq, qop, kop = None, 0, 0, None, None
     if q is not None:
-        qs = _token_rows(q, "q")
-        hq = q.shape[1]
-        _need(q.shape[0] == total and q.shape[2] == d, "q [tokens, Hq, d]")
+        qshape = q.shape
+        if len(qshape) != 3 or qshape[0] != total or qshape[2] != d:
+            _refuse("q must be [tokens, Hq, head_dim]")
+        hq = qshape[1]
+        qp, q_stride = _token_rows(q, "q", dev, hq, d)
         if q_out is None:
-            q_out = torch.empty((total, hq, d), dtype=torch.bfloat16, device=q.device)
-        _cuda_contig(q_out, "q_out", torch.bfloat16)
-        _need(q_out.shape == q.shape, "q_out shape")
-    else:
-        _need(q_out is None, "q_out goes with q")
+            q_out = torch.empty(qshape, dtype=torch.bfloat16, device=k.device)
+        elif q_out.shape != qshape:
+            _refuse("q_out must have q's shape")
+        qop = _arg(q_out, "q_out", dev, torch.bfloat16)
+    elif q_out is not None:
+        _refuse("q_out goes with q")
     if k_out is None and want_k:
-        k_out = torch.empty((total, hkv, d), dtype=torch.bfloat16, device=k.device)
+        k_out = torch.empty(kshape, dtype=torch.bfloat16, device=k.device)
     if k_out is not None:
-        _cuda_contig(k_out, "k_out", torch.bfloat16)
-        _need(k_out.shape == k.shape, "k_out shape")
-    _check(lib().tts_rope_kv_append(
-        _ptr(q), qs, hq, _ptr(k), ks, _ptr(v), vs, total, _ptr(cu_new), _ptr(past_lens), batch,
-        int(max_new), hkv, d, _ptr(cos_sin), max_pos, _ptr(page_tables), page_tables.shape[1],
-        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code, pages, ps, _ptr(q_out),
-        _ptr(k_out), _ptr(status), _stream(k.device)), "tts_rope_kv_append")
+        if k_out.shape != kshape:
+            _refuse("k_out must have k's shape")
+        kop = _arg(k_out, "k_out", dev, torch.bfloat16)
+    _call((_lib or lib()).tts_rope_kv_append, "tts_rope_kv_append", dev, qp, q_stride, hq, kp,
+          k_stride, vp, v_stride, total, _arg(cu_new, "cu_new", dev, torch.int32),
+          _arg(past_lens, "past_lens", dev, torch.int32), batch, int(max_new), hkv, d, csp, max_pos,
+          _arg(page_tables, "page_tables", dev, torch.int32), tshape[1], kc, vc, ks, vs, code,
+          pages, ps, qop, kop,
+          None if status is None else _arg(status, "status", dev, torch.int32))
     return q_out, k_out
 
 
 def attn_decode_workspace_bytes(max_seqlen_q, num_heads_q, num_heads_kv, head_dim) -> int:
     return int(lib().tts_attn_decode_workspace_bytes(int(max_seqlen_q), int(num_heads_q),
                                                      int(num_heads_kv), int(head_dim)))
+
+
+_decode_workspace = {}  # (device, max_seqlen_q, Hq, Hkv, d): bytes
 
 
 def attn_decode_paged(q, k_cache, v_cache, page_tables, kv_lens, scale, cu_seqlens_q=None,
@@ -648,38 +699,50 @@ def attn_decode_paged(q, k_cache, v_cache, page_tables, kv_lens, scale, cu_seqle
     rope_kv_append, kv_lens int32 [batch] with the new tokens counted. window > 0: a token sees
     the last `window` positions up to its own and the first `sinks`. Returns (out [tokens, Hq, d]
     in out_dtype, or in out's dtype: fp32 or bf16; lse fp32 [tokens, Hq])."""
-    code = _cache(k_cache, v_cache, k_scale, v_scale)
-    pages, hkv, ps, d = k_cache.shape
-    _cuda_contig(q, "q", torch.bfloat16)
-    _need(q.dim() == 3 and q.shape[2] == d, "q [tokens, Hq, d]")
-    total, hq = q.shape[:2]
-    _cuda_contig(page_tables, "page_tables", torch.int32)
-    _cuda_contig(kv_lens, "kv_lens", torch.int32)
+    dev = _device_of(q, "q")
+    code, (pages, hkv, ps, d), kc, vc, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d:
+        _refuse("q must be [tokens, Hq, head_dim]")
+    total, hq = shape[0], shape[1]
     batch = kv_lens.numel()
-    _need(page_tables.dim() == 2 and page_tables.shape[0] == batch, "page_tables [batch, max_pages]")
+    tshape = page_tables.shape
+    if len(tshape) != 2 or tshape[0] != batch:
+        _refuse("page_tables must be [batch, max_pages], kv_lens [batch]")
+    cup = None
     if cu_seqlens_q is not None:
-        _cuda_contig(cu_seqlens_q, "cu_seqlens_q", torch.int32)
-        _need(cu_seqlens_q.numel() == batch + 1, "cu_seqlens_q [batch + 1]")
-    else:
-        _need(total == batch, "q has one token per request without cu_seqlens_q")
+        if cu_seqlens_q.numel() != batch + 1:
+            _refuse("cu_seqlens_q must be [batch + 1]")
+        cup = _arg(cu_seqlens_q, "cu_seqlens_q", dev, torch.int32)
+    elif total != batch:
+        _refuse("q has one token per request without cu_seqlens_q")
     if out is None:
-        out = torch.empty((total, hq, d), dtype=out_dtype, device=q.device)
-    _cuda_contig(out, "out")
-    _need(out.dtype in (torch.float32, torch.bfloat16) and out.shape == q.shape,
-          "out must be fp32 or bf16 [tokens, Hq, d]")
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    odt = out.dtype
+    if out.shape != shape or (odt != torch.bfloat16 and odt != torch.float32):
+        _refuse("out must be fp32 or bf16 [tokens, Hq, head_dim]")
     if lse is None and want_lse:
         lse = torch.empty((total, hq), dtype=torch.float32, device=q.device)
+    lp = None
     if lse is not None:
-        _cuda_contig(lse, "lse", torch.float32)
-        _need(tuple(lse.shape) == (total, hq), "lse shape")
-    need = attn_decode_workspace_bytes(max_seqlen_q, hq, hkv, d)
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    _check(lib().tts_attn_decode_paged(
-        _ptr(q), total, _ptr(cu_seqlens_q), batch, int(max_seqlen_q), hq, hkv, d, _ptr(k_cache),
-        _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code, pages, ps, _ptr(page_tables),
-        page_tables.shape[1], _ptr(kv_lens), int(window), int(sinks), float(scale), _ptr(out),
-        TTS_BF16 if out.dtype == torch.bfloat16 else TTS_F32, _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(status), _stream(q.device)),
-        "tts_attn_decode_paged")
+        if lse.shape != shape[:2]:
+            _refuse("lse must be [tokens, Hq]")
+        lp = _arg(lse, "lse", dev, torch.float32)
+    key = (dev, max_seqlen_q, hq, hkv, d)
+    need = _decode_workspace.get(key)
+    if need is None:
+        with torch.cuda.device(dev):
+            need = _decode_workspace[key] = attn_decode_workspace_bytes(*key[1:])
+    have = 0 if workspace is None else workspace.nbytes
+    if have < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        have = need
+    wp = _arg(workspace, "workspace", dev, workspace.dtype) if have else None
+    _call((_lib or lib()).tts_attn_decode_paged, "tts_attn_decode_paged", dev,
+          _arg(q, "q", dev, torch.bfloat16), total, cup, batch, int(max_seqlen_q), hq, hkv, d, kc,
+          vc, ks, vs, code, pages, ps, _arg(page_tables, "page_tables", dev, torch.int32),
+          tshape[1], _arg(kv_lens, "kv_lens", dev, torch.int32), int(window), int(sinks),
+          float(scale), _arg(out, "out", dev, odt),
+          TTS_BF16 if odt == torch.bfloat16 else TTS_F32, lp, wp, have,
+          None if status is None else _arg(status, "status", dev, torch.int32))
     return out, lse

@@ -68,7 +68,10 @@ struct Params {
   void* out;
   float* lse;
   float* parts;  // [2 * CTAs][kR * (D + 2)]
-  int4* jobs;    // [CTAs]: {first CTA of the unit (-1: none), request, g, row tile}
+  // [CTAs], of the unit that was begun in an earlier CTA and ended in this one: {first CTA
+  // (-1: no such unit), rows, first row within the request, g}
+  int4* jobs;
+  int64_t* job_q0;  // and the request's first q row
   uint32_t* dev_status;
   int64_t total_q;
   int batch, max_q, hq, hkv, group, num_pages, max_pages, page_size, page_shift, window, sinks;
@@ -215,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   __shared__ int64_t s_scan[kThreads / 32], s_off;
   __shared__ int s_b, s_abort, s_issued;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   float* join = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S * C::kStageBytes);
@@ -809,85 +813,90 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // the unit ends here: tell the second launch where it began
         const int64_t begin = t1 - left - x1;  // list index of the unit's first tile
         p.jobs[blockIdx.x] =
-            make_int4((int)(((begin + 1) * runs - 1) / total), b, g, rt);
+            make_int4((int)(((begin + 1) * runs - 1) / total), rows < R ? rows : R, rt * R, g);
+        p.job_q0[blockIdx.x] = r.q0;
       }
       named_barrier_sync(1, kNW * 32);
     }
   }
 }
 
-// Joins the parts of the units that CTA borders cut: block (c, row) for the unit that ended in
-// CTA c, parts in list order within each of eight warps, then the warps in order.
+// Joins the parts of the units that CTA borders cut: block c for the unit that ended in CTA c,
+// eight warps over (row, piece of the parts): with R rows each warp takes one row of eight, all
+// parts in list order, four loads at a time.
 template <bool F8, int D, int NT>
 __global__ void __launch_bounds__(256) attn_decode_join_kernel(const Params p) {
   using C = Cfg<F8, D, NT>;
   constexpr int R = C::kR;
   constexpr float kBias = F8 ? 11.f : 0.f;
-  __shared__ float2 s_ml[8];
-  __shared__ float4 s_acc[8][D / 4];
-  const int c1 = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kBatch = 4;  // parts whose loads are in flight together
+  const int c1 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the first launch is complete and its writes visible from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 job = p.jobs[c1];
+  const int64_t q0 = p.job_q0[c1];
   if (job.x < 0) return;
-  uint32_t bad = 0;
-  const Req r = load_req<C::kTK, R>(p, job.y, &bad);
-  const int rr = job.w * R + row;
-  if (rr >= r.n * p.group) return;
-  float top = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int c = job.x + warp; c <= c1; c += 8) {
-    const float* part = p.parts + (size_t)(2 * c + (c == job.x ? 1 : 0)) * (R * (D + 2));
-    const float m = part[R * D + 2 * row], l = part[R * D + 2 * row + 1];
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (lane < D / 4) v = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
-    const float n = fmaxf(top, m);
-    const float fa = top == -INFINITY ? 0.f : ex2_approx(top - n);
-    const float fb = m == -INFINITY ? 0.f : ex2_approx(m - n);
-    top = n;
-    sum = sum * fa + l * fb;
-    acc.x = acc.x * fa + v.x * fb;
-    acc.y = acc.y * fa + v.y * fb;
-    acc.z = acc.z * fa + v.z * fb;
-    acc.w = acc.w * fa + v.w * fb;
-  }
-  if (lane == 0) s_ml[warp] = make_float2(top, sum);
-  if (lane < D / 4) s_acc[warp][lane] = acc;
-  __syncthreads();
-  if (warp != 0) return;
-  top = -INFINITY;
+  for (int row = warp; row < job.y; row += 8) {
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = job.x; c <= c1; c += kBatch) {
+      float m[kBatch], l[kBatch];
+      float4 v[kBatch];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, s_ml[w].x);
-  sum = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < kBatch; ++i) {
+        const int cc = c + i;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (cc <= c1) {
+          const float* part = p.parts + (size_t)(2 * cc + (cc == job.x ? 1 : 0)) * (R * (D + 2));
+          const float2 ml = *reinterpret_cast<const float2*>(part + R * D + 2 * row);
+          m[i] = ml.x;
+          l[i] = ml.y;
+          if (lane < D / 4) v[i] = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
+        }
+      }
+      float n = top;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const float f = s_ml[w].x == -INFINITY ? 0.f : ex2_approx(s_ml[w].x - top);
-    sum = fmaf(s_ml[w].y, f, sum);
+      for (int i = 0; i < kBatch; ++i) n = fmaxf(n, m[i]);
+      const float f = top == -INFINITY ? 0.f : ex2_approx(top - n);
+      top = n;
+      sum *= f;
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float fi = m[i] == -INFINITY ? 0.f : ex2_approx(m[i] - n);
+        sum = fmaf(l[i], fi, sum);
+        acc.x = fmaf(v[i].x, fi, acc.x);
+        acc.y = fmaf(v[i].y, fi, acc.y);
+        acc.z = fmaf(v[i].z, fi, acc.z);
+        acc.w = fmaf(v[i].w, fi, acc.w);
+      }
+    }
+    const int rr = job.z + row, tok = rr / p.group;
+    const int64_t at = (q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
     if (lane < D / 4) {
-      const float4 v = s_acc[w][lane];
-      acc.x = fmaf(v.x, f, acc.x);
-      acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z);
-      acc.w = fmaf(v.w, f, acc.w);
+      if (p.out_bf16) {
+        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane;
+        *o = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      } else {
+        reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[lane] =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      }
     }
+    if (p.lse != nullptr && lane == 0)
+      p.lse[at] = sum > 0.f ? (top - kBias + log2f(sum)) * kLn2 : -INFINITY;
   }
-  const int tok = rr / p.group;
-  const int64_t at = (r.q0 + tok) * p.hq + job.z * p.group + (rr - tok * p.group);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (lane < D / 4) {
-    if (p.out_bf16) {
-      uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane;
-      *o = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    } else {
-      reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[lane] =
-          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    }
-  }
-  if (p.lse != nullptr && lane == 0)
-    p.lse[at] = sum > 0.f ? (top - kBias + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 int rows_of(int max_q, int group) { return max_q * group <= 8 ? 8 : 16; }
+size_t job_bytes(size_t ctas) {
+  return (ctas * (sizeof(int4) + sizeof(int64_t)) + 255) / 256 * 256;
+}
 
 template <bool F8, int D, int NT>
 cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t stream) {
@@ -919,8 +928,9 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   p.out_bf16 = a.out_bf16 ? 1 : 0;
   p.ctas = kCtasPerSm * sms;
   p.jobs = static_cast<int4*>(a.workspace);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
-                                     ((size_t)p.ctas * sizeof(int4) + 255) / 256 * 256);
+  p.job_q0 = reinterpret_cast<int64_t*>(p.jobs + p.ctas);
+  p.parts =
+      reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + job_bytes((size_t)p.ctas));
   CUtensorMap mk, mv;
   auto make = [&](CUtensorMap* m, void* base) -> bool {
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.page_size, (uint64_t)a.num_pages * a.hkv};
@@ -941,8 +951,17 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   attn_decode_kernel<F8, D, NT><<<p.ctas, kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_decode_join_kernel<F8, D, NT><<<dim3(p.ctas, C::kR), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  // The second launch may be set up while the first runs; it waits for its end itself.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ctas);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<F8, D, NT>, p);
 }
 
 template <bool F8, int D>
@@ -955,7 +974,7 @@ cudaError_t launch_nt(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream
 
 size_t attn_decode_workspace_bytes(int max_q, int hq, int hkv, int d, int sms) {
   const size_t ctas = (size_t)kCtasPerSm * sms, rows = rows_of(max_q, hq / hkv);
-  return (ctas * sizeof(int4) + 255) / 256 * 256 + ctas * 2 * rows * (d + 2) * sizeof(float);
+  return job_bytes(ctas) + ctas * 2 * rows * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, int* drv_err, cudaStream_t stream) {
