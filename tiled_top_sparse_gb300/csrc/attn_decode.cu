@@ -25,6 +25,7 @@
 // fp16 with its reference kept so that 2^-25 of the maximum still has all 11 bits. bf16
 // caches use bf16 products throughout. Sums and softmax statistics are fp32.
 #include <cstdint>
+#include <cstdlib>
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -269,7 +270,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     total += sum;
   }
   if (blockIdx.x == 0 && bad && p.dev_status != nullptr) atomicOr(p.dev_status, bad);
-  const int64_t runs = total < p.ctas ? total : p.ctas;  // runs with at least one tile each
+  // Runs of at least kNW tiles (the warps take one each, side by side): shorter ones would
+  // only leave more parts to join.
+  const int64_t most = (total + kNW - 1) / kNW;
+  const int64_t runs = most < p.ctas ? most : p.ctas;
   if (tid == 0) p.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if ((int64_t)blockIdx.x >= runs) return;
   const int64_t t0 = total * blockIdx.x / runs, t1 = total * (blockIdx.x + 1) / runs;
@@ -821,76 +825,93 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
-// Joins the parts of the units that CTA borders cut: block c for the unit that ended in CTA c,
-// eight warps over (row, piece of the parts): with R rows each warp takes one row of eight, all
-// parts in list order, four loads at a time.
+// Joins the parts of the units that CTA borders cut: block (c, j) for rows 8 j .. 8 j + 7 of the
+// unit that ended in CTA c. Eight warps take every eighth part each (all eight rows' loads in
+// flight together), then warp w joins the warps' results for row 8 j + w, in order.
 template <bool F8, int D, int NT>
 __global__ void __launch_bounds__(256) attn_decode_join_kernel(const Params p) {
   using C = Cfg<F8, D, NT>;
   constexpr int R = C::kR;
   constexpr float kBias = F8 ? 11.f : 0.f;
-  constexpr int kBatch = 4;  // parts whose loads are in flight together
-  const int c1 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float2 s_ml[8][8];
+  __shared__ float4 s_acc[8][8][D / 4];
+  const int c1 = blockIdx.x, row0 = blockIdx.y * 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the first launch is complete and its writes visible from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 job = p.jobs[c1];
   const int64_t q0 = p.job_q0[c1];
-  if (job.x < 0) return;
-  for (int row = warp; row < job.y; row += 8) {
-    float top = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = job.x; c <= c1; c += kBatch) {
-      float m[kBatch], l[kBatch];
-      float4 v[kBatch];
+  if (job.x < 0 || row0 >= job.y) return;
+  const bool mine = lane < D / 4;
+  float top[8], sum[8];
+  float4 acc[8];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int cc = c + i;
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (cc <= c1) {
-          const float* part = p.parts + (size_t)(2 * cc + (cc == job.x ? 1 : 0)) * (R * (D + 2));
-          const float2 ml = *reinterpret_cast<const float2*>(part + R * D + 2 * row);
-          m[i] = ml.x;
-          l[i] = ml.y;
-          if (lane < D / 4) v[i] = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
-        }
-      }
-      float n = top;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) n = fmaxf(n, m[i]);
-      const float f = top == -INFINITY ? 0.f : ex2_approx(top - n);
-      top = n;
-      sum *= f;
-      acc.x *= f;
-      acc.y *= f;
-      acc.z *= f;
-      acc.w *= f;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const float fi = m[i] == -INFINITY ? 0.f : ex2_approx(m[i] - n);
-        sum = fmaf(l[i], fi, sum);
-        acc.x = fmaf(v[i].x, fi, acc.x);
-        acc.y = fmaf(v[i].y, fi, acc.y);
-        acc.z = fmaf(v[i].z, fi, acc.z);
-        acc.w = fmaf(v[i].w, fi, acc.w);
-      }
-    }
-    const int rr = job.z + row, tok = rr / p.group;
-    const int64_t at = (q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    if (lane < D / 4) {
-      if (p.out_bf16) {
-        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane;
-        *o = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      } else {
-        reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[lane] =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-      }
-    }
-    if (p.lse != nullptr && lane == 0)
-      p.lse[at] = sum > 0.f ? (top - kBias + log2f(sum)) * kLn2 : -INFINITY;
+  for (int i = 0; i < 8; ++i) {
+    top[i] = -INFINITY;
+    sum[i] = 0.f;
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  for (int c = job.x + warp; c <= c1; c += 8) {
+    const float* part = p.parts + (size_t)(2 * c + (c == job.x ? 1 : 0)) * (R * (D + 2));
+    float2 ml[8];
+    float4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ml[i] = *reinterpret_cast<const float2*>(part + R * D + 2 * (row0 + i));
+      v[i] = mine ? *reinterpret_cast<const float4*>(part + (row0 + i) * D + lane * 4)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float n = fmaxf(top[i], ml[i].x);
+      const float fa = top[i] == -INFINITY ? 0.f : ex2_approx(top[i] - n);
+      const float fb = ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - n);
+      top[i] = n;
+      sum[i] = sum[i] * fa + ml[i].y * fb;
+      acc[i].x = acc[i].x * fa + v[i].x * fb;
+      acc[i].y = acc[i].y * fa + v[i].y * fb;
+      acc[i].z = acc[i].z * fa + v[i].z * fb;
+      acc[i].w = acc[i].w * fa + v[i].w * fb;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (lane == 0) s_ml[warp][i] = make_float2(top[i], sum[i]);
+    if (mine) s_acc[warp][i][lane] = acc[i];
+  }
+  __syncthreads();
+  const int row = row0 + warp;
+  if (row >= job.y) return;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, s_ml[w][warp].x);
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float2 ml = s_ml[w][warp];
+    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+    l = fmaf(ml.y, f, l);
+    if (mine) {
+      const float4 v = s_acc[w][warp][lane];
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+    }
+  }
+  const int rr = job.z + row, tok = rr / p.group;
+  const int64_t at = (q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (mine) {
+    if (p.out_bf16) {
+      uint2* to = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane;
+      *to = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    } else {
+      reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[lane] =
+          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    }
+  }
+  if (p.lse != nullptr && lane == 0)
+    p.lse[at] = l > 0.f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
 }
 
 int rows_of(int max_q, int group) { return max_q * group <= 8 ? 8 : 16; }
@@ -953,12 +974,12 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   if (e != cudaSuccess) return e;
   // The second launch may be set up while the first runs; it waits for its end itself.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas);
+  cfg.gridDim = dim3(p.ctas, NT);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
+  at.val.programmaticStreamSerializationAllowed = getenv("NOPDL") ? 0 : 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<F8, D, NT>, p);

@@ -117,6 +117,10 @@ struct AttnParams {
 struct WindowParams : AttnParams {
   int window, sinks;  // keys up to a row's own, first keys that stay visible
   int out_bf16;       // out is bf16
+  // The two query tiles of an item are two heads of a KV group on the same 128 rows (an even
+  // group): both see the same keys, where two tiles of consecutive rows stream one tile more
+  // than each needs. An odd group keeps the row pairs.
+  int pair_heads;
 };
 template <bool kWin>
 using ParamsFor = std::conditional_t<kWin, WindowParams, AttnParams>;
@@ -180,6 +184,7 @@ struct Item {
   int h, g, n_tiles;  // n_tiles: K/V tiles streamed = max(n0, n1)
   int n0, n1;         // tiles each warpgroup needs (0: no rows, or no visible key)
   int n_sink, win0;   // kWin: streamed tiles are [0, n_sink), then win0, win0 + 1, ...
+  int dh, dr;         // kWin: head and row of the second warpgroup's tile, from the first's
 };
 // Key tile that an item streams as its j-th.
 template <bool kWin>
@@ -189,8 +194,10 @@ __device__ __forceinline__ int key_tile(const Item& w, int j) {
 }
 template <bool kWin>
 __device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, Item& w, bool* bad) {
-  const int h = it % p.hq;
-  const int t = it / p.hq;
+  int heads = p.hq;
+  if constexpr (kWin) heads = p.pair_heads ? p.hq / 2 : p.hq;
+  int h = it % heads;
+  const int t = it / heads;
   const int b = t % p.batch;
   const int pr = p.pairs_max - 1 - t / p.batch;
   const int64_t q_start = p.cu_q[b], k_start = p.cu_k[b];
@@ -207,7 +214,19 @@ __device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, It
   // (the cheapest under a causal mask: one key tile) and the first warpgroup of pair 0
   // has no rows.
   const int64_t n_qt = (Lq + kBlockM - 1) / kBlockM;
-  const int64_t q_lo = (int64_t)pr * 2 * kBlockM - ((n_qt & 1) ? kBlockM : 0);
+  int64_t q_lo = (int64_t)pr * 2 * kBlockM - ((n_qt & 1) ? kBlockM : 0);
+  int64_t row1 = kBlockM;  // the second warpgroup's rows, from the first's
+  if constexpr (kWin) {
+    w.dh = 0;
+    w.dr = kBlockM;
+    if (p.pair_heads) {  // two heads of a KV group on the same rows
+      q_lo = (int64_t)pr * kBlockM;
+      h *= 2;
+      w.dh = 1;
+      w.dr = 0;
+      row1 = 0;
+    }
+  }
   if (q_lo >= Lq) return false;
   // Keys each warpgroup's rows can see: all of them, or (causal) up to its last row's
   // diagonal; none for a warpgroup without rows (the odd last tile of a sequence).
@@ -218,7 +237,7 @@ __device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, It
     return lim < 0 ? 0 : (lim < Lk ? lim : Lk);
   };
   const int64_t kv_end0 = keys_for(q_lo, q_lo + kBlockM);
-  const int64_t kv_end1 = keys_for(q_lo + kBlockM, q_lo + 2 * kBlockM);
+  const int64_t kv_end1 = keys_for(q_lo + row1, q_lo + row1 + kBlockM);
   const int64_t kv_end = kv_end0 > kv_end1 ? kv_end0 : kv_end1;
   w.q_start = q_start;
   w.k_start = k_start;
@@ -233,9 +252,10 @@ __device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, It
   if constexpr (kWin) {
     // First key inside the window of the first row that sees any (a later row's starts later).
     const int64_t off = Lk - Lq;
-    const int64_t row = kv_end0 > 0 ? (q_lo > 0 ? q_lo : 0) : q_lo + kBlockM;
+    const int64_t row = kv_end0 > 0 ? (q_lo > 0 ? q_lo : 0) : q_lo + row1;
     const int64_t lo = row + off + 1 - p.window;
-    const int64_t lo1 = q_lo + kBlockM + off + 1 - p.window;  // of the second warpgroup
+    // Last row's window: the first keys that no window of the item holds are kept apart.
+    const int64_t lo1 = q_lo + row1 + kBlockM - 1 + off + 1 - p.window;
     w.win0 = lo > 0 ? (int)(lo / kBlockN) : 0;
     const int64_t sinks = p.sinks < lo1 ? p.sinks : lo1;  // more are inside every window
     const int64_t ns = sinks > 0 ? (sinks + kBlockN - 1) / kBlockN : 0;
@@ -397,7 +417,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           const uint32_t bq = smem_u32(&bar_q[wq]);
           mbar_arrive_expect_tx(bq, C::kTileBytes);
-          load_tile<D, F8>(sQ[wq], &maps.q, &maps.q_t, bq, w.h,
+          if constexpr (kWin)
+            load_tile<D, F8>(sQ[wq], &maps.q, &maps.q_t, bq, w.h + wq * w.dh,
+                             (int)(w.q_start + w.q_lo + wq * w.dr));
+          else
+            load_tile<D, F8>(sQ[wq], &maps.q, &maps.q_t, bq, w.h,
                        (int)(w.q_start + w.q_lo + wq * kBlockM));
           q_armed[wq] = nq + 1;
         }
@@ -607,7 +631,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       decode_item<kWin>(p, it, w, &bad);
       const int n_tiles = wg == 0 ? w.n0 : w.n1;  // tiles this warpgroup's rows can see
       const int64_t Lq = w.Lq, Lk = w.Lk;
-      const int64_t i = w.q_lo + wg * kBlockM + row;  // query row within the sequence
+      int64_t first = w.q_lo + wg * kBlockM;  // this warpgroup's first row and its head
+      if constexpr (kWin) {
+        first = w.q_lo + wg * w.dr;
+        w.h += wg * w.dh;
+      }
+      const int64_t i = first + row;  // query row within the sequence
       int64_t limit = Lk;                            // keys [0, limit) visible to this row
       if (p.causal) {
         const int64_t lim = i + (Lk - Lq) + 1;
@@ -644,15 +673,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int64_t kv0 = (int64_t)key_tile<kWin>(w, j) * kBlockN;
         float tile_max = fmaxf(fmax3(part_max[0], part_max[1], part_max[2]), part_max[3]);
         if constexpr (kWin) {
-          if (kv0 + kBlockN > limit || (kv0 < win_lo && kv0 + kBlockN > p.sinks)) {
+          if (__any_sync(0xFFFFFFFFu, kv0 + kBlockN > limit ||
+                                          (kv0 < win_lo && kv0 + kBlockN > p.sinks))) {
             // visible columns of the tile: [0, sk) and [lo, lim)
-            const int64_t span = limit - kv0, first = win_lo - kv0, kept = p.sinks - kv0;
+            const int64_t span = limit - kv0, from = win_lo - kv0, kept = p.sinks - kv0;
             const int lim = span < 128 ? (int)(span < 0 ? 0 : span) : 128;
-            const int lo = first > 0 ? (int)(first < 128 ? first : 128) : 0;
+            const int lo = from > 0 ? (int)(from < 128 ? from : 128) : 0;
             const int sk = kept > 0 ? (int)(kept < 128 ? kept : 128) : 0;
+            // one bit per column: a test and a select each, where three comparisons took
+            // twice as long
+            auto below = [](int n, int c0) -> uint32_t {  // columns c0 .. c0 + 31 under n
+              const int b = n - c0;
+              return b <= 0 ? 0u : b >= 32 ? 0xFFFFFFFFu : (1u << b) - 1u;
+            };
   #pragma unroll
-            for (int cc = 0; cc < 128; ++cc)
-              if (cc >= lim || (cc < lo && cc >= sk)) s[cc] = -INFINITY;
+            for (int c0 = 0; c0 < 128; c0 += 32) {
+              const uint32_t see = below(lim, c0) & (~below(lo, c0) | below(sk, c0));
+              if (__all_sync(0xFFFFFFFFu, see == 0xFFFFFFFFu)) continue;
+  #pragma unroll
+              for (int cc = 0; cc < 32; ++cc)
+                if (!((see >> cc) & 1u)) s[c0 + cc] = -INFINITY;
+            }
             tile_max = row_max<128>(s);
           }
           if (kv0 + kBlockN > Lk) {  // rows behind the sequence: cleared once V has landed
@@ -731,7 +772,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
       // Rows leave TMEM one per thread; this warp's 4 KB staging slice turns them into
       // whole 128-byte row segments, so each store instruction writes full lines.
-      const int64_t row0 = w.q_lo + wg * kBlockM + (warp & 3) * 32;  // this warp's first row
+      const int64_t row0 = first + (warp & 3) * 32;  // this warp's first row
       bool rounded = false;
       if constexpr (kWin) rounded = p.out_bf16 != 0;
       if (rounded) {
@@ -899,8 +940,12 @@ cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
     p.window = a.window;
     p.sinks = a.sinks;
     p.out_bf16 = a.out_bf16 ? 1 : 0;
+    p.pair_heads = (a.hq / a.hkv) % 2 == 0 ? 1 : 0;
+    if (p.pair_heads) p.pairs_max = (a.max_seqlen_q + kBlockM - 1) / kBlockM;
   }
-  const int64_t items = (int64_t)a.batch * p.pairs_max * a.hq;
+  int heads = a.hq;  // items per (sequence, rows)
+  if constexpr (kWin) heads = p.pair_heads ? a.hq / 2 : a.hq;
+  const int64_t items = (int64_t)a.batch * p.pairs_max * heads;
   if (items == 0) return cudaSuccess;
   if (items > 0x7FFFFFFF || a.work_counter == nullptr) return cudaErrorInvalidConfiguration;
   p.work_counter = a.work_counter;
