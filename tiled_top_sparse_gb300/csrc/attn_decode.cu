@@ -25,7 +25,6 @@
 // fp16 with its reference kept so that 2^-25 of the maximum still has all 11 bits. bf16
 // caches use bf16 products throughout. Sums and softmax statistics are fp32.
 #include <cstdint>
-#include <cstdlib>
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -72,9 +71,9 @@ struct Params {
   // [CTAs], of the unit that was begun in an earlier CTA and ended in this one: {first CTA
   // (-1: no such unit), rows, first row within the request, g}
   int4* jobs;
-  int64_t* job_q0;  // and the request's first q row
+  int* job_q0;  // and the request's first q row
   uint32_t* dev_status;
-  int64_t total_q;
+  int total_q, max_keys;
   int batch, max_q, hq, hkv, group, num_pages, max_pages, page_size, page_shift, window, sinks;
   float scale_log2;
   int out_bf16, ctas;
@@ -85,44 +84,47 @@ struct Params {
 struct Req {
   int n, L, lo, sinks;  // new tokens, keys, first key of the window (0: none), kept first keys
   int st, lt, nt, rt;   // tiles of the first keys, first tile of the window, tiles, row tiles
-  int64_t q0;           // first q row
+  int q0;               // first q row
 };
-template <int TK, int R>
-__device__ __forceinline__ Req load_req(const Params& p, int b, uint32_t* bad) {
-  Req r;
-  int64_t q0 = b, q1 = b + 1;
+__device__ __forceinline__ void read_req(const Params& p, int b, int& n, int& L, int& q0,
+                                         uint32_t* bad) {
+  int q1 = b + 1;
+  q0 = b;
   if (p.cu_q != nullptr) {
     q0 = p.cu_q[b];
     q1 = p.cu_q[b + 1];
   }
-  int L = p.kv_lens[b];
-  r.n = 0;
-  r.q0 = q0;
+  L = p.kv_lens[b];
+  n = 0;
   if (q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.max_q)
     *bad |= kDevBadArg;
   else
-    r.n = (int)(q1 - q0);
-  if (L < 0 || (int64_t)L > (int64_t)p.max_pages * p.page_size) {
+    n = q1 - q0;
+  if (L < 0 || L > p.max_keys) {
     *bad |= kDevIndexRange;
     L = 0;  // its rows see no key
   }
+}
+template <int TK, int R>
+__device__ __forceinline__ Req make_req(const Params& p, int n, int L, int q0) {
+  Req r;
+  r.n = n;
   r.L = L;
-  r.lo = 0;
-  if (p.window > 0) {
-    const int64_t lo = (int64_t)L - r.n + 1 - p.window;
-    r.lo = lo > 0 ? (int)(lo < L ? lo : L) : 0;
-  }
-  r.sinks = p.sinks < r.lo ? p.sinks : r.lo;
-  r.lt = r.lo / TK;
-  r.st = (r.sinks + TK - 1) / TK;
-  if (r.st > r.lt) r.st = r.lt;
-  r.nt = r.st + (L + TK - 1) / TK - r.lt;
-  if (r.nt < 1) r.nt = 1;  // an empty tile: the unit writes zeros
-  r.rt = (r.n * p.group + R - 1) / R;
+  r.q0 = q0;
+  // keys and window are at most 2^30, so nothing here leaves 32 bits
+  r.lo = p.window > 0 ? max(L - n + 1 - p.window, 0) : 0;
+  r.sinks = min(p.sinks, r.lo);
+  r.lt = (int)((unsigned)r.lo / TK);
+  r.st = min((int)((unsigned)(r.sinks + TK - 1) / TK), r.lt);
+  r.nt = max(r.st + (int)((unsigned)(L + TK - 1) / TK) - r.lt, 1);  // 1: an empty tile, zeros
+  r.rt = (int)((unsigned)(n * p.group + R - 1) / R);
   return r;
 }
-__device__ __forceinline__ int64_t req_tiles(const Params& p, const Req& r) {
-  return (int64_t)p.hkv * r.rt * r.nt;
+template <int TK, int R>
+__device__ __forceinline__ Req load_req(const Params& p, int b, uint32_t* bad) {
+  int n, L, q0;
+  read_req(p, b, n, L, q0, bad);
+  return make_req<TK, R>(p, n, L, q0);
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -215,9 +217,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[S], bar_empty[S];
   __shared__ Meta s_meta[S];
-  __shared__ float2 s_ml[kNW][R];  // each warp's reference and sum of every row
-  __shared__ int64_t s_scan[kThreads / 32], s_off;
-  __shared__ int s_b, s_abort, s_issued;
+  __shared__ __align__(8) float s_m[kNW][R], s_l[kNW][R];  // references and sums of every row
+  __shared__ int s_scan[kThreads / 32], s_b, s_off, s_abort, s_issued;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -228,28 +229,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
   // ---- this CTA's run [t0, t1) of the list of tiles, and the request it begins in
   uint32_t bad = 0;
-  auto block_scan = [&](int64_t v, int64_t* total) -> int64_t {  // inclusive
-    int64_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    int64_t before = 0, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += s_scan[w];
-      sum += s_scan[w];
-    }
-    *total = sum;
-    return x + before;
-  };
-  auto tiles_of = [&](int b) -> int64_t {
-    return b < p.batch ? req_tiles(p, load_req<TK, R>(p, b, &bad)) : 0;
-  };
   if (tid == 0) {
     s_abort = s_issued = 0;
     for (int i = 0; i < S; ++i) {
@@ -257,60 +236,112 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       mbar_init(smem_u32(&bar_empty[i]), 1);
     }
     fence_mbar_init();
+    p.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
-  int64_t total = 0, v0 = 0, incl0 = 0;
-  for (int base = 0; base < p.batch; base += kThreads) {
-    const int64_t v = tiles_of(base + tid);
-    int64_t sum;
-    const int64_t incl = block_scan(v, &sum);
-    if (base == 0) {
-      v0 = v;
-      incl0 = incl;
+  auto scan32 = [&](int x) -> int {  // inclusive over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
     }
-    total += sum;
-  }
-  if (blockIdx.x == 0 && bad && p.dev_status != nullptr) atomicOr(p.dev_status, bad);
+    return x;
+  };
+  auto tiles_of = [&](const Req& r) -> int { return p.hkv * r.rt * r.nt; };
   // Runs of at least kNW tiles (the warps take one each, side by side): shorter ones would
-  // only leave more parts to join.
-  const int64_t most = (total + kNW - 1) / kNW;
-  const int64_t runs = most < p.ctas ? most : p.ctas;
-  if (tid == 0) p.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  if ((int64_t)blockIdx.x >= runs) return;
-  const int64_t t0 = total * blockIdx.x / runs, t1 = total * (blockIdx.x + 1) / runs;
-  {
-    int64_t carry = 0;
-    for (int base = 0; base < p.batch; base += kThreads) {
-      int64_t v = v0, incl = incl0, sum = 0;
-      if (p.batch > kThreads) {
-        v = tiles_of(base + tid);
-        incl = block_scan(v, &sum);
+  // only leave more parts to join. The first `more` runs have one tile more than the others.
+  int total = 0, runs = 0, len = 0, more = 0, t0 = 0, t1 = 0;
+  auto split = [&]() -> bool {
+    runs = min((int)((unsigned)(total + kNW - 1) / kNW), p.ctas);
+    if ((int)blockIdx.x >= runs) return false;
+    len = (int)((unsigned)total / (unsigned)runs);
+    more = total - len * runs;
+    t0 = blockIdx.x * len + min((int)blockIdx.x, more);
+    t1 = t0 + len + ((int)blockIdx.x < more ? 1 : 0);
+    return true;
+  };
+  int b = 0, off = 0;
+  Req r;
+  if (p.batch <= 32) {  // every warp for itself
+    int n = 0, L = 0, q0 = 0, v = 0;
+    if (lane < p.batch) {
+      read_req(p, lane, n, L, q0, &bad);
+      r = make_req<TK, R>(p, n, L, q0);
+      v = tiles_of(r);
+    }
+    if (blockIdx.x == 0 && warp == 0 && bad && p.dev_status != nullptr)
+      atomicOr(p.dev_status, bad);
+    const int incl = scan32(v);
+    total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    if (!split()) return;
+    b = __ffs(__ballot_sync(0xFFFFFFFFu, incl > t0)) - 1;
+    off = t0 - __shfl_sync(0xFFFFFFFFu, incl - v, b);
+    r = make_req<TK, R>(p, __shfl_sync(0xFFFFFFFFu, n, b), __shfl_sync(0xFFFFFFFFu, L, b),
+                        __shfl_sync(0xFFFFFFFFu, q0, b));
+  } else {
+    auto block_scan = [&](int v, int* sum) -> int {  // inclusive
+      const int x = scan32(v);
+      __syncthreads();
+      if (lane == 31) s_scan[warp] = x;
+      __syncthreads();
+      int before = 0;
+      *sum = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += s_scan[w];
+        *sum += s_scan[w];
       }
-      if (carry + incl > t0 && carry + incl - v <= t0) {
-        s_b = base + tid;
-        s_off = t0 - (carry + incl - v);
+      return x + before;
+    };
+    for (int base = 0; base < p.batch; base += kThreads) {
+      const int i = base + tid;
+      int sum;
+      block_scan(i < p.batch ? tiles_of(load_req<TK, R>(p, i, &bad)) : 0, &sum);
+      total += sum;
+    }
+    if (blockIdx.x == 0 && bad && p.dev_status != nullptr) atomicOr(p.dev_status, bad);
+    if (!split()) return;
+    for (int base = 0, carry = 0; base < p.batch && carry <= t0; base += kThreads) {
+      const int i = base + tid;
+      const int v = i < p.batch ? tiles_of(load_req<TK, R>(p, i, &bad)) : 0;
+      int sum;
+      const int incl = carry + block_scan(v, &sum);
+      if (incl > t0 && incl - v <= t0) {
+        s_b = i;
+        s_off = t0 - (incl - v);
       }
       carry += sum;
     }
+    __syncthreads();
+    b = s_b;
+    off = s_off;
+    r = load_req<TK, R>(p, b, &bad);
   }
   __syncthreads();
 
-  int b = s_b;
-  int64_t off = s_off, left = t1 - t0;
+  int left = t1 - t0;
   int it = 0;  // tiles of this run so far
-  Req r = load_req<TK, R>(p, b, &bad);
+  int seg_g = -1, seg_rt = 0;
   // The next unit's part in this run: head, row tile, tiles [x0, x1) of nt.
   auto next_seg = [&](int& g, int& rt, int& x0, int& x1) {
-    while (off >= req_tiles(p, r)) {  // requests without tiles are stepped over
-      ++b;
-      off = 0;
-      r = load_req<TK, R>(p, b, &bad);
+    if (seg_g < 0) {  // the run's first unit, perhaps from its middle
+      const int u = (int)((unsigned)off / (unsigned)r.nt);
+      x0 = off - u * r.nt;
+      seg_g = (int)((unsigned)u / (unsigned)r.rt);
+      seg_rt = u - seg_g * r.rt;
+    } else {
+      x0 = 0;
+      if (++seg_rt == r.rt) {
+        seg_rt = 0;
+        if (++seg_g == p.hkv) {
+          seg_g = 0;
+          do r = load_req<TK, R>(p, ++b, &bad);  // requests without new tokens have no units
+          while (r.rt == 0);
+        }
+      }
     }
-    const int u = (int)(off / r.nt);
-    x0 = (int)(off - (int64_t)u * r.nt);
-    g = u / r.rt;
-    rt = u - g * r.rt;
-    x1 = (int)(r.nt - x0 < left ? r.nt : x0 + left);
-    off += x1 - x0;
+    g = seg_g;
+    rt = seg_rt;
+    x1 = min(r.nt, x0 + left);
     left -= x1 - x0;
   };
   const int piece = p.page_size < TK ? p.page_size : TK;  // keys per TMA box
@@ -318,9 +349,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
   if (warp == kNW) {
     // ------------------------------------------------------------------ producer
+    // A tile must leave in well under the ~700 cycles that HBM takes for it, so lane i keeps
+    // page cache_at + i of the request (and what the consumers need of its scales for head
+    // cache_g) in registers, loaded 32 pages at a time.
     constexpr uint32_t kBox = C::kPanelBytes;
     int cache_b = -1, cache_at = 0, cache_g = -1, page = -1;
-    float ks = 1.f, vs = 1.f;
+    bool fine = true;                    // the page's scales are positive and finite
+    float ks = 1.f, vl = 0.f, vi = 1.f;  // key scale, log2 and inverse of the value scale
     bool ok = true;
     while (ok && left > 0) {
       int g, rt, x0, x1;
@@ -335,14 +370,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           cache_g = -1;
           const int lp = pg0 + lane;
           page = lp < p.max_pages ? p.page_tables[(int64_t)b * p.max_pages + lp] : -1;
+          if (page < 0 || page >= p.num_pages) page = -1;
         }
-        if (F8 && cache_g != g) {
-          cache_g = g;
-          ks = vs = 1.f;
-          if (page >= 0 && page < p.num_pages) {
-            ks = p.k_scale[(int64_t)page * p.hkv + g];
-            vs = p.v_scale[(int64_t)page * p.hkv + g];
-          }
+        float sk = 1.f, sv = 1.f;
+        const bool new_scales = F8 && cache_g != g;
+        if (new_scales && page >= 0) {  // asked for here, looked at behind the copies
+          sk = p.k_scale[(int64_t)page * p.hkv + g];
+          sv = p.v_scale[(int64_t)page * p.hkv + g];
         }
         if (it >= S)
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bar_empty[st]), ((it / S) - 1) & 1,
@@ -352,43 +386,46 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int pg = __shfl_sync(0xFFFFFFFFu, page, at);
         const int a = key0 + lane * piece;  // this lane's piece: keys [a, a + piece)
         const bool seen = lane < n_pieces && a < r.L && (a + piece > r.lo || a < r.sinks);
-        bool good = seen && pg >= 0 && pg < p.num_pages;
-        uint32_t flag = seen && !good ? kDevIndexRange : 0u;
-        if (good) {
+        const bool there = seen && pg >= 0;
+        const uint32_t bar = smem_u32(&bar_full[st]);
+        if (there) {
           const uint32_t dst = ring + st * C::kStageBytes + lane * piece * kBox;
           const int row = key0 & (p.page_size - 1);  // 0 unless the tile is inside a page
           const int slab = pg * p.hkv + g;
-          const uint32_t bar = smem_u32(&bar_full[st]);
 #pragma unroll
           for (int pn = 0; pn < C::kPanels; ++pn) {
             tma_load_3d(dst + pn * TK * kBox, &map_k, bar, pn * 64, row, slab);
             tma_load_3d(dst + C::kKBytes + pn * TK * kBox, &map_v, bar, pn * 64, row, slab);
           }
         }
-        const uint32_t sent = __ballot_sync(0xFFFFFFFFu, good);
+        const uint32_t sent = __ballot_sync(0xFFFFFFFFu, there);
+        uint32_t flag = seen && !there ? kDevIndexRange : 0u;
+        uint32_t use = sent;
         if constexpr (F8) {
-          const float pks = __shfl_sync(0xFFFFFFFFu, ks, at), pvs = __shfl_sync(0xFFFFFFFFu, vs, at);
-          if (good && !(pks > 0.f && pks < INFINITY && pvs > 0.f && pvs < INFINITY)) {
-            good = false;  // no scale a cache page can have: its keys are skipped
-            flag |= kDevBadArg;
+          if (new_scales) {
+            cache_g = g;
+            fine = sk > 0.f && sk < INFINITY && sv > 0.f && sv < INFINITY;
+            ks = sk;
+            vl = fine ? log2f(sv) : 0.f;
+            vi = fine ? 1.f / sv : 0.f;
           }
+          const uint32_t all = __ballot_sync(0xFFFFFFFFu, fine);
+          const bool good = there && ((all >> at) & 1u);
+          if (there && !good) flag |= kDevBadArg;  // no scale of a written page: keys skipped
+          use = __ballot_sync(0xFFFFFFFFu, good);
+          const float pk = __shfl_sync(0xFFFFFFFFu, ks, at), pl = __shfl_sync(0xFFFFFFFFu, vl, at),
+                      pi = __shfl_sync(0xFFFFFFFFu, vi, at);
           if (lane < n_pieces) {
-            s_meta[st].ks[lane] = pks;
-            s_meta[st].vl[lane] = good ? log2f(pvs) : 0.f;
-            s_meta[st].vi[lane] = good ? 1.f / pvs : 0.f;
+            s_meta[st].ks[lane] = pk;
+            s_meta[st].vl[lane] = pl;
+            s_meta[st].vi[lane] = pi;
           }
         }
         if (flag && p.dev_status != nullptr) atomicOr(p.dev_status, flag);
-        const uint32_t use = __ballot_sync(0xFFFFFFFFu, good);
-        if (lane == 0) {
-          s_meta[st].ok = use;
-        }
+        if (lane == 0) s_meta[st].ok = use;
         __syncwarp();
-        if (lane == 0)
-          mbar_arrive_expect_tx(smem_u32(&bar_full[st]),
-                                __popc(sent) * piece * C::kRowBytes * 2);
         if (lane == 0) {
-          __threadfence_block();
+          mbar_arrive_expect_tx(bar, __popc(sent) * piece * C::kRowBytes * 2);
           *issued_tiles = it + 1;
         }
       }
@@ -431,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       for (int j = 0; j < NT; ++j) {
         const int rr = rt * R + j * 8 + g8;
         const bool in = j * 8 + g8 < rows;
-        const int tok = in ? rr / p.group : 0;
+        const int tok = in && p.max_q > 1 ? rr / p.group : 0;
         const int h = in ? g * p.group + (rr - tok * p.group) : 0;
-        const uint16_t* src = p.q + ((r.q0 + tok) * p.hq + h) * (int64_t)D;
+        const uint16_t* src = p.q + ((int64_t)(r.q0 + tok) * p.hq + h) * D;
         uint32_t w[KS][2];
 #pragma unroll
         for (int i = 0; i < KS; i += 2) {
@@ -480,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
       // every row sees keys [max_lo, min_end) (and the first sinks)
       const int last_row = rt * R + (rows < R ? rows : R) - 1;
-      const int min_end = r.L - r.n + rt * R / p.group + 1;
-      const int max_pos = r.L - r.n + last_row / p.group;
+      const int min_end = r.L - r.n + (p.max_q > 1 ? rt * R / p.group : 0) + 1;
+      const int max_pos = r.L - r.n + (p.max_q > 1 ? last_row / p.group : 0);
       const int max_lo = p.window > 0 ? max_pos + 1 - p.window : 0;
 
       float o[NT][KS][4];
@@ -702,7 +739,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (lane == 0) mbar_arrive(smem_u32(&bar_empty[st]));
       }
 
-      // ---- join the four warps: warp w finishes m tiles [w kMQ, (w + 1) kMQ)
+      // ---- join the four warps: the largest reference first, then warp w sums m tiles
+      // [w kMQ, (w + 1) kMQ) of all four
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -710,15 +748,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           l0[j] += __shfl_xor_sync(0xFFFFFFFFu, l0[j], d);
           l1[j] += __shfl_xor_sync(0xFFFFFFFFu, l1[j], d);
         }
-        if (g8 == 0) {
-          s_ml[warp][j * 8 + 2 * t4] = make_float2(m0[j], l0[j]);
-          s_ml[warp][j * 8 + 2 * t4 + 1] = make_float2(m1[j], l1[j]);
+        if (g8 == 0)
+          *reinterpret_cast<float2*>(&s_m[warp][j * 8 + 2 * t4]) = make_float2(m0[j], m1[j]);
+      }
+      named_barrier_sync(1, kNW * 32);
+      float top0[NT], top1[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        top0[j] = top1[j] = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kNW; ++w) {
+          const float2 m = *reinterpret_cast<const float2*>(&s_m[w][j * 8 + 2 * t4]);
+          top0[j] = fmaxf(top0[j], m.x);
+          top1[j] = fmaxf(top1[j], m.y);
+        }
+        const float a0 = m0[j] == -INFINITY ? 0.f : ex2_approx(m0[j] - top0[j]);
+        const float a1 = m1[j] == -INFINITY ? 0.f : ex2_approx(m1[j] - top1[j]);
+        if (g8 == 0)
+          *reinterpret_cast<float2*>(&s_l[warp][j * 8 + 2 * t4]) = make_float2(l0[j] * a0, l1[j] * a1);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          o[j][i][0] *= a0;
+          o[j][i][1] *= a1;
+          o[j][i][2] *= a0;
+          o[j][i][3] *= a1;
         }
       }
-      // slot of (finishing warp, source warp): sources other than the finisher, in order
+      // slot of (summing warp, source warp): every source but itself
       auto join_at = [&](int dst, int src) -> float* {
         const int k = src < dst ? src : src - 1;
-        return join + (size_t)(dst * (kNW - 1) + k) * (NT * C::kMQ * 4 * 32) + lane;
+        return join + (dst * (kNW - 1) + k) * (NT * C::kMQ * 4 * 32) + lane;
       };
 #pragma unroll
       for (int dst = 0; dst < kNW; ++dst) {
@@ -737,87 +796,93 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       float* part = p.parts + (size_t)(2 * blockIdx.x + (whole_l ? 1 : 0)) * (R * (D + 2));
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, fw[kNW][2];
-#pragma unroll
-        for (int w = 0; w < kNW; ++w)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) top[k] = fmaxf(top[k], s_ml[w][j * 8 + 2 * t4 + k].x);
-#pragma unroll
-        for (int w = 0; w < kNW; ++w)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 ml = s_ml[w][j * 8 + 2 * t4 + k];
-            fw[w][k] = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top[k]);
-            sum[k] = fmaf(ml.y, fw[w][k], sum[k]);
-          }
         float acc[C::kMQ][4];
 #pragma unroll
-        for (int i = 0; i < C::kMQ; ++i)
+        for (int d = 0; d < kNW; ++d)
+          if (d == warp) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
+            for (int i = 0; i < C::kMQ; ++i)
 #pragma unroll
-        for (int w = 0; w < kNW; ++w) {
-          const float* from = join_at(warp, w == warp ? (warp == 0 ? 1 : 0) : w);
+              for (int k = 0; k < 4; ++k) acc[i][k] = o[j][d * C::kMQ + i][k];
+          }
+        // ((own + first) + second) + third other: the same order every time
+#pragma unroll
+        for (int w = 0; w < kNW - 1; ++w) {
+          const float* from = join + (warp * (kNW - 1) + w) * (NT * C::kMQ * 4 * 32) + lane;
 #pragma unroll
           for (int i = 0; i < C::kMQ; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float v = from[((j * C::kMQ + i) * 4 + k) * 32];
-              if (w == warp) {
+            for (int k = 0; k < 4; ++k) acc[i][k] += from[((j * C::kMQ + i) * 4 + k) * 32];
+        }
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int d = 0; d < kNW; ++d)
-                  if (d == warp) v = o[j][d * C::kMQ + i][k];
-              }
-              acc[i][k] = fmaf(v, fw[w][k & 1], acc[i][k]);
-            }
+        for (int w = 0; w < kNW; ++w) {
+          const float2 l = *reinterpret_cast<const float2*>(&s_l[w][j * 8 + 2 * t4]);
+          sum.x += l.x;
+          sum.y += l.y;
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // column 2 t4 + k: one q row
           const int row = j * 8 + 2 * t4 + k;
+          const float l = k ? sum.y : sum.x, top = k ? top1[j] : top0[j];
+          const float inv = !final ? 1.f : l > 0.f ? 1.f / l : 0.f;
           float v[2 * C::kMQ];
 #pragma unroll
           for (int i = 0; i < C::kMQ; ++i) {
-            v[2 * i] = acc[i][k];
-            v[2 * i + 1] = acc[i][k + 2];
+            v[2 * i] = acc[i][k] * inv;
+            v[2 * i + 1] = acc[i][k + 2] * inv;
           }
-          // v[2 i], v[2 i + 1] are elements d of m tile w kMQ + i: for e4m3 (D/8) g8 +
-          // 2 (w kMQ + i) + {0, 1}; for bf16 16 (w kMQ + i) + g8 + {0, 8}
+          int64_t at = 0;
           if (final) {
-            if (row < rows) {
-              const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;
-              const int rr = rt * R + row, tok = rr / p.group;
-              const int64_t at = (r.q0 + tok) * p.hq + g * p.group + (rr - tok * p.group);
-#pragma unroll
-              for (int i = 0; i < 2 * C::kMQ; ++i) {
-                const int m = warp * C::kMQ + i / 2;
-                const int d = F8 ? (D / 8) * g8 + 2 * m + (i & 1) : 16 * m + g8 + 8 * (i & 1);
-                if (p.out_bf16)
-                  static_cast<__nv_bfloat16*>(p.out)[at * D + d] = __float2bfloat16_rn(v[i] * inv);
-                else
-                  static_cast<float*>(p.out)[at * D + d] = v[i] * inv;
-              }
-              if (p.lse != nullptr && warp == 0 && g8 == 0)
-                p.lse[at] = sum[k] > 0.f ? (top[k] - kBias + log2f(sum[k])) * kLn2 : -INFINITY;
+            if (row >= rows) continue;
+            const int rr = rt * R + row, tok = p.max_q > 1 ? rr / p.group : 0;
+            at = (int64_t)(r.q0 + tok) * p.hq + g * p.group + (rr - tok * p.group);
+          }
+          float* to32 = final ? static_cast<float*>(p.out) + at * D : part + row * D;
+          uint16_t* to16 = static_cast<uint16_t*>(p.out) + at * D;
+          const bool half = final && p.out_bf16;
+          if constexpr (F8) {  // elements d0 .. d0 + 2 kMQ - 1 of the row
+            const int d0 = (D / 8) * g8 + 2 * C::kMQ * warp;
+            if constexpr (C::kMQ == 2) {
+              if (half)
+                *reinterpret_cast<uint2*>(to16 + d0) =
+                    make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+              else
+                *reinterpret_cast<float4*>(to32 + d0) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+              if (half)
+                *reinterpret_cast<uint32_t*>(to16 + d0) = pack_bf16x2(v[0], v[1]);
+              else
+                *reinterpret_cast<float2*>(to32 + d0) = make_float2(v[0], v[1]);
             }
-          } else {
+          } else {  // elements 16 m + g8 and 16 m + g8 + 8 of m tile m
 #pragma unroll
             for (int i = 0; i < 2 * C::kMQ; ++i) {
-              const int m = warp * C::kMQ + i / 2;
-              const int d = F8 ? (D / 8) * g8 + 2 * m + (i & 1) : 16 * m + g8 + 8 * (i & 1);
-              part[row * D + d] = v[i];
+              const int d = 16 * (warp * C::kMQ + i / 2) + g8 + 8 * (i & 1);
+              if (half)
+                to16[d] = (uint16_t)pack_bf16x2(v[i], 0.f);
+              else
+                to32[d] = v[i];
             }
-            if (warp == 0 && g8 == 0) {
-              part[R * D + 2 * row] = top[k];
-              part[R * D + 2 * row + 1] = sum[k];
+          }
+          if (warp == 0 && g8 == 0) {
+            if (final) {
+              if (p.lse != nullptr)
+                p.lse[at] = l > 0.f ? (top - kBias + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+              *reinterpret_cast<float2*>(part + R * D + 2 * row) = make_float2(top, l);
             }
           }
         }
       }
       if (!whole_l && whole_r && tid == 0) {
         // the unit ends here: tell the second launch where it began
-        const int64_t begin = t1 - left - x1;  // list index of the unit's first tile
-        p.jobs[blockIdx.x] =
-            make_int4((int)(((begin + 1) * runs - 1) / total), rows < R ? rows : R, rt * R, g);
+        const int begin = t1 - left - x1;  // list index of the unit's first tile
+        const int longer = more * (len + 1);  // tiles of the runs with one more
+        const int c0 = begin < longer
+                           ? (int)((unsigned)begin / (unsigned)(len + 1))
+                           : more + (int)((unsigned)(begin - longer) / (unsigned)len);
+        p.jobs[blockIdx.x] = make_int4(c0, rows < R ? rows : R, rt * R, g);
         p.job_q0[blockIdx.x] = r.q0;
       }
       named_barrier_sync(1, kNW * 32);
@@ -839,7 +904,7 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const Params p) {
   // the first launch is complete and its writes visible from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 job = p.jobs[c1];
-  const int64_t q0 = p.job_q0[c1];
+  const int q0 = p.job_q0[c1];
   if (job.x < 0 || row0 >= job.y) return;
   const bool mine = lane < D / 4;
   float top[8], sum[8];
@@ -899,7 +964,7 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const Params p) {
     }
   }
   const int rr = job.z + row, tok = rr / p.group;
-  const int64_t at = (q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
+  const int64_t at = (int64_t)(q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
   const float inv = l > 0.f ? 1.f / l : 0.f;
   if (mine) {
     if (p.out_bf16) {
@@ -916,7 +981,7 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const Params p) {
 
 int rows_of(int max_q, int group) { return max_q * group <= 8 ? 8 : 16; }
 size_t job_bytes(size_t ctas) {
-  return (ctas * (sizeof(int4) + sizeof(int64_t)) + 255) / 256 * 256;
+  return (ctas * (sizeof(int4) + sizeof(int)) + 255) / 256 * 256;
 }
 
 template <bool F8, int D, int NT>
@@ -932,7 +997,8 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   p.out = a.out;
   p.lse = a.lse;
   p.dev_status = a.dev_status;
-  p.total_q = a.total_q;
+  p.total_q = (int)a.total_q;
+  p.max_keys = a.max_pages * a.page_size;
   p.batch = a.batch;
   p.max_q = a.max_q;
   p.hq = a.hq;
@@ -949,7 +1015,7 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   p.out_bf16 = a.out_bf16 ? 1 : 0;
   p.ctas = kCtasPerSm * sms;
   p.jobs = static_cast<int4*>(a.workspace);
-  p.job_q0 = reinterpret_cast<int64_t*>(p.jobs + p.ctas);
+  p.job_q0 = reinterpret_cast<int*>(p.jobs + p.ctas);
   p.parts =
       reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + job_bytes((size_t)p.ctas));
   CUtensorMap mk, mv;
@@ -979,7 +1045,7 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   cfg.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = getenv("NOPDL") ? 0 : 1;
+  at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<F8, D, NT>, p);
