@@ -36,6 +36,10 @@ namespace {
 constexpr int kNW = 4;                        // consumer warps
 constexpr int kThreads = (kNW + 1) * 32;      // and one producer warp
 constexpr int kCtasPerSm = 2;
+// What the end of a unit costs (joining the warps, the next unit's q), in tiles: the list that
+// is cut into runs has this many empty places behind a unit's tiles, so that a run over many
+// short units is not the last to finish.
+constexpr int kEndTiles = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -220,7 +224,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   __shared__ __align__(8) float s_m[kNW][R], s_l[kNW][R];  // references and sums of every row
   __shared__ int s_scan[kThreads / 32], s_b, s_off, s_abort, s_issued;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   float* join = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S * C::kStageBytes);
@@ -246,8 +249,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     return x;
   };
-  auto tiles_of = [&](const Req& r) -> int { return p.hkv * r.rt * r.nt; };
-  // Runs of at least kNW tiles (the warps take one each, side by side): shorter ones would
+  auto tiles_of = [&](const Req& r) -> int { return p.hkv * r.rt * (r.nt + kEndTiles); };
+  // Runs of at least kNW places (the warps take one each, side by side): shorter ones would
   // only leave more parts to join. The first `more` runs have one tile more than the others.
   int total = 0, runs = 0, len = 0, more = 0, t0 = 0, t1 = 0;
   auto split = [&]() -> bool {
@@ -322,10 +325,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   int it = 0;  // tiles of this run so far
   int seg_g = -1, seg_rt = 0;
   // The next unit's part in this run: head, row tile, tiles [x0, x1) of nt.
-  auto next_seg = [&](int& g, int& rt, int& x0, int& x1) {
+  auto next_seg = [&](int& g, int& rt, int& x0, int& x1) -> bool {
     if (seg_g < 0) {  // the run's first unit, perhaps from its middle
-      const int u = (int)((unsigned)off / (unsigned)r.nt);
-      x0 = off - u * r.nt;
+      const int u = (int)((unsigned)off / (unsigned)(r.nt + kEndTiles));
+      x0 = off - u * (r.nt + kEndTiles);
       seg_g = (int)((unsigned)u / (unsigned)r.rt);
       seg_rt = u - seg_g * r.rt;
     } else {
@@ -342,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     g = seg_g;
     rt = seg_rt;
     x1 = min(r.nt, x0 + left);
-    left -= x1 - x0;
+    left -= min(r.nt + kEndTiles - x0, left);
+    return x0 < x1;  // else the run begins behind the unit's last tile
   };
   const int piece = p.page_size < TK ? p.page_size : TK;  // keys per TMA box
   const int n_pieces = TK / piece;
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     bool ok = true;
     while (ok && left > 0) {
       int g, rt, x0, x1;
-      next_seg(g, rt, x0, x1);
+      if (!next_seg(g, rt, x0, x1)) continue;
       for (int x = x0; ok && x < x1; ++x, ++it) {
         const int key0 = (x < r.st ? x : r.lt + x - r.st) * TK;
         const int st = it % S;
@@ -456,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     };
     while (left > 0) {
       int g, rt, x0, x1;
-      next_seg(g, rt, x0, x1);
+      const int before = t1 - left;
+      if (!next_seg(g, rt, x0, x1)) continue;
       const bool whole_l = x0 == 0, whole_r = x1 == r.nt;
       const int rows = r.n * p.group - rt * R;  // rows of this tile: min(rows, R)
 
@@ -877,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
       if (!whole_l && whole_r && tid == 0) {
         // the unit ends here: tell the second launch where it began
-        const int begin = t1 - left - x1;  // list index of the unit's first tile
+        const int begin = before - x0;  // list place of the unit's first tile
         const int longer = more * (len + 1);  // tiles of the runs with one more
         const int c0 = begin < longer
                            ? (int)((unsigned)begin / (unsigned)(len + 1))
@@ -901,8 +906,6 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const Params p) {
   __shared__ float2 s_ml[8][8];
   __shared__ float4 s_acc[8][8][D / 4];
   const int c1 = blockIdx.x, row0 = blockIdx.y * 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the first launch is complete and its writes visible from here on
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 job = p.jobs[c1];
   const int q0 = p.job_q0[c1];
   if (job.x < 0 || row0 >= job.y) return;
@@ -1038,17 +1041,8 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   attn_decode_kernel<F8, D, NT><<<p.ctas, kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // The second launch may be set up while the first runs; it waits for its end itself.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas, NT);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<F8, D, NT>, p);
+  attn_decode_join_kernel<F8, D, NT><<<dim3(p.ctas, NT), 256, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 template <bool F8, int D>
