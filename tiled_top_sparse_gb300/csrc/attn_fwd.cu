@@ -117,10 +117,13 @@ struct AttnParams {
 struct WindowParams : AttnParams {
   int window, sinks;  // keys up to a row's own, first keys that stay visible
   int out_bf16;       // out is bf16
-  // The two query tiles of an item are two heads of a KV group on the same 128 rows (an even
-  // group): both see the same keys, where two tiles of consecutive rows stream one tile more
-  // than each needs. An odd group keeps the row pairs.
-  int pair_heads;
+  // What the two query tiles of an item are. kHeads: two heads of a KV group on the same 128
+  // rows (an even group): both see the same keys, where two tiles of consecutive rows (kRows,
+  // an odd group) stream one tile more than each needs (ragged batch, window 1024: 213 -> 116
+  // us with the bit masks). kSolo: one tile alone, where all of them fit the GPU at once: a
+  // tile's chain is shorter without a second tile's between its steps.
+  enum Pairing : int { kRows, kHeads, kSolo };
+  int pairing;
 };
 template <bool kWin>
 using ParamsFor = std::conditional_t<kWin, WindowParams, AttnParams>;
@@ -195,7 +198,7 @@ __device__ __forceinline__ int key_tile(const Item& w, int j) {
 template <bool kWin>
 __device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, Item& w, bool* bad) {
   int heads = p.hq;
-  if constexpr (kWin) heads = p.pair_heads ? p.hq / 2 : p.hq;
+  if constexpr (kWin) heads = p.pairing == WindowParams::kHeads ? p.hq / 2 : p.hq;
   int h = it % heads;
   const int t = it / heads;
   const int b = t % p.batch;
@@ -219,8 +222,8 @@ __device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, It
   if constexpr (kWin) {
     w.dh = 0;
     w.dr = kBlockM;
-    if (p.pair_heads) {  // two heads of a KV group on the same rows
-      q_lo = (int64_t)pr * kBlockM;
+    if (p.pairing != WindowParams::kRows) q_lo = (int64_t)pr * kBlockM;
+    if (p.pairing == WindowParams::kHeads) {
       h *= 2;
       w.dh = 1;
       w.dr = 0;
@@ -237,7 +240,10 @@ __device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, It
     return lim < 0 ? 0 : (lim < Lk ? lim : Lk);
   };
   const int64_t kv_end0 = keys_for(q_lo, q_lo + kBlockM);
-  const int64_t kv_end1 = keys_for(q_lo + row1, q_lo + row1 + kBlockM);
+  int64_t kv_end1 = keys_for(q_lo + row1, q_lo + row1 + kBlockM);
+  if constexpr (kWin) {
+    if (p.pairing == WindowParams::kSolo) kv_end1 = row1 = 0;
+  }
   const int64_t kv_end = kv_end0 > kv_end1 ? kv_end0 : kv_end1;
   w.q_start = q_start;
   w.k_start = k_start;
@@ -342,6 +348,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       prefetch_tmap(&maps.k);
       prefetch_tmap(&maps.v);
       int ni = 0, nq = 0, gt = 0;
+      bool own = true;  // without a counter: this CTA's item is still to come
       int last_k[NS], last_v[NS];  // latest tile armed on each ring slot (-1: none)
       for (int i = 0; i < NS; ++i) last_k[i] = last_v[i] = -1;
       int q_armed[2] = {0, 0};  // per Q tile: items whose Q copy was started
@@ -384,7 +391,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         Item w;
         int it;
         for (;;) {  // next item with work (bad sequences are reported here, once)
-          it = (int)atomicAdd(p.work_counter, 1u);
+          if (kWin && p.work_counter == nullptr) {
+            it = own ? (int)blockIdx.x : p.n_items;
+            own = false;
+          } else {
+            it = (int)atomicAdd(p.work_counter, 1u);
+          }
           if (it >= p.n_items) {
             it = -1;
             break;
@@ -936,31 +948,38 @@ cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.q_scale = a.q_scale;
   p.k_scale = a.k_scale;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
   if constexpr (kWin) {
     p.window = a.window;
     p.sinks = a.sinks;
     p.out_bf16 = a.out_bf16 ? 1 : 0;
-    p.pair_heads = (a.hq / a.hkv) % 2 == 0 ? 1 : 0;
-    if (p.pair_heads) p.pairs_max = (a.max_seqlen_q + kBlockM - 1) / kBlockM;
+    const int tiles = (a.max_seqlen_q + kBlockM - 1) / kBlockM;
+    p.pairing = (int64_t)a.batch * tiles * a.hq <= sms ? WindowParams::kSolo
+                : (a.hq / a.hkv) % 2 == 0              ? WindowParams::kHeads
+                                                       : WindowParams::kRows;
+    if (p.pairing != WindowParams::kRows) p.pairs_max = tiles;
   }
   int heads = a.hq;  // items per (sequence, rows)
-  if constexpr (kWin) heads = p.pair_heads ? a.hq / 2 : a.hq;
+  if constexpr (kWin) heads = p.pairing == WindowParams::kHeads ? a.hq / 2 : a.hq;
   const int64_t items = (int64_t)a.batch * p.pairs_max * heads;
   if (items == 0) return cudaSuccess;
   if (items > 0x7FFFFFFF || a.work_counter == nullptr) return cudaErrorInvalidConfiguration;
   p.work_counter = a.work_counter;
   p.n_items = (int)items;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   // One persistent CTA per SM (the kernel's shared memory and TMEM allow one).
   const int grid = (int)(items < sms ? items : sms);
   e = cudaFuncSetAttribute(attn_fwd_kernel<D, F8, kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = cudaMemsetAsync(a.work_counter, 0, sizeof(uint32_t), stream);
-  if (e != cudaSuccess) return e;
+  if (kWin && items <= sms) {
+    p.work_counter = nullptr;  // one item per CTA: none to hand out, nothing to zero first
+  } else {
+    e = cudaMemsetAsync(a.work_counter, 0, sizeof(uint32_t), stream);
+    if (e != cudaSuccess) return e;
+  }
   attn_fwd_kernel<D, F8, kWin><<<grid, kAttnThreads, C::kSmemBytes, stream>>>(maps, p);
   return cudaGetLastError();
 }

@@ -45,6 +45,7 @@ struct KvAppendArgs {
   float* v_scale;
   bool f8;  // e4m3 cache with scales, else bf16
   int num_pages, page_size;
+  int page_shift = 0;  // log2 of page_size (set by the launch)
   void* q_out;
   void* k_out;  // may be null
   uint32_t* dev_status;
