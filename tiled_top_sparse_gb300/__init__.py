@@ -253,43 +253,18 @@ def attn_fwd_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, ma
 
     Arguments as attn_fwd_varlen; returns (out [total_q, Hq, d] in out_dtype, or in out's dtype:
     fp32 or bf16; lse fp32 [total_q, Hq])."""
-    dev = _device_of(q, "q")
-    dt, qshape, kshape = q.dtype, q.shape, k.shape
-    if dt != torch.bfloat16 and dt != torch.float32:
-        _refuse("q, k, v must share dtype bf16 or fp32")
-    if len(qshape) != 3 or len(kshape) != 3 or v.shape != kshape or qshape[2] != kshape[2]:
-        _refuse("q, k, v must be [tokens, heads, head_dim], k and v of the same shape")
-    total_q, hq, d = qshape
-    total_k, hkv = kshape[0], kshape[1]
-    batch = cu_seqlens_q.numel() - 1
-    if batch < 1 or cu_seqlens_k.numel() != batch + 1:
-        _refuse("cu_seqlens sizes must be batch+1")
-    if out is None:
-        out = torch.empty(qshape, dtype=out_dtype, device=q.device)
-    odt = out.dtype
-    if out.shape != qshape or (odt != torch.bfloat16 and odt != torch.float32):
-        _refuse("out must be fp32 or bf16 [total_q, Hq, head_dim]")
-    if lse is None and want_lse:
-        lse = torch.empty((total_q, hq), dtype=torch.float32, device=q.device)
-    lp = None
-    if lse is not None:
-        if lse.shape != qshape[:2]:
-            _refuse("lse must be [total_q, Hq]")
-        lp = _arg(lse, "lse", dev, torch.float32)
-    need = attn_workspace_bytes(total_q, total_k, hq, hkv, d, dt)
-    have = 0 if workspace is None else workspace.nbytes
-    if have < need:
+    out, lse = _attn_outputs(q, out, lse, want_lse, out_dtype)
+    call = (_nat or _binding()).attn_fwd_varlen_window
+    code = call(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, window, sinks,
+                scale, out, lse, workspace, status)
+    if code == TTS_ERR_WORKSPACE:  # missing or too small: nothing was enqueued
+        need = attn_workspace_bytes(q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2],
+                                    q.dtype)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        have = need
-    wp = _arg(workspace, "workspace", dev, workspace.dtype) if have else None
-    _call((_lib or lib()).tts_attn_fwd_varlen_window, "tts_attn_fwd_varlen_window", dev,
-          _arg(q, "q", dev, dt), _arg(k, "k", dev, dt), _arg(v, "v", dev, dt),
-          TTS_F32 if dt == torch.float32 else TTS_BF16, total_q, total_k,
-          _arg(cu_seqlens_q, "cu_seqlens_q", dev, torch.int32),
-          _arg(cu_seqlens_k, "cu_seqlens_k", dev, torch.int32), batch, int(max_seqlen_q),
-          int(max_seqlen_k), hq, hkv, d, int(window), int(sinks), float(scale),
-          _arg(out, "out", dev, odt), TTS_BF16 if odt == torch.bfloat16 else TTS_F32, lp, wp, have,
-          None if status is None else _arg(status, "status", dev, torch.int32))
+        code = call(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, window,
+                    sinks, scale, out, lse, workspace, status)
+    if code:
+        raise TTSError(code, "tts_attn_fwd_varlen_window")
     return out, lse
 
 
@@ -556,70 +531,37 @@ def attn_fwd_varlen_fp8(q8, q_scale, k8, k_scale, v, cu_seqlens_q, cu_seqlens_k,
     return out, lse
 
 
-# The calls of a decode step are short on the GPU, so their bindings look at each tensor once:
-# `_arg` checks one and returns its address.
-def _arg(t, name, dev, dtype):
-    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
-        _cuda_contig(t, name, dtype)
-        raise ValueError(f"{name} must be on cuda:{dev} like the call's other tensors")
-    return t.data_ptr()
+# The grouped-query calls are checked and made by a small native module (csrc/native.c): the
+# calls of a decode step are shorter on the GPU than the same checks written here.
+_nat = None
 
 
-def _refuse(msg):
-    raise ValueError(msg)
+def _binding():
+    """The native binding, given the library's entry points and torch's dtypes and streams."""
+    global _nat
+    if _nat is None:
+        L = lib()
+        try:
+            from . import _native as m
+        except ImportError as e:
+            raise ImportError("the native binding is not built; run "
+                              "tiled_top_sparse_gb300/_build.py") from e
+        m.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value
+                     for f in (L.tts_rope_kv_append, L.tts_attn_decode_paged,
+                               L.tts_attn_fwd_varlen_window)),
+               (torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn, torch.int32),
+               (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
+                torch._C._cuda_setDevice))
+        _nat = m
+    return _nat
 
 
-def _device_of(t, name):
-    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
-    if dev < 0:
-        _refuse(f"{name} must be a CUDA tensor")
-    return dev
-
-
-def _call(fn, what, dev, *args):
-    """Call fn on `dev`'s current stream, with that device current for the call."""
-    if dev == torch.cuda.current_device():
-        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with torch.cuda.device(dev):
-            code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if code != TTS_OK:
-        raise TTSError(code, what)
-
-
-def _token_rows(t, name, dev, heads, d):
-    """Address and token stride of [tokens, heads, d] bf16 whose heads are contiguous: views of
-    a packed projection pass without a copy."""
-    s0, s1, s2 = t.stride()
-    if t.dtype != torch.bfloat16 or t.get_device() != dev or s2 != 1 or (s1 != d and heads != 1):
-        _refuse(f"{name} must be bf16 [tokens, heads, head_dim] on cuda:{dev}, the heads of a token "
-                "contiguous")
-    return t.data_ptr(), (s0 if t.shape[0] > 1 else heads * d)
-
-
-_CODES = (torch.uint8, torch.float8_e4m3fn)
-
-
-def _cache(k_cache, v_cache, k_scale, v_scale, dev):
-    """Checks a grouped-query cache; returns its dtype code, shape and the four addresses."""
-    dt = k_cache.dtype
-    shape = k_cache.shape
-    f8 = dt in _CODES
-    if len(shape) != 4 or not (f8 or dt == torch.bfloat16):
-        _refuse("k_cache must be [pages, heads_kv, page_size, head_dim] in bf16, or uint8 / "
-                "float8_e4m3fn codes")
-    if v_cache.shape != shape:
-        _refuse("k_cache and v_cache must have the same shape")
-    if f8 != (k_scale is not None) or f8 != (v_scale is not None):
-        _refuse("k_scale and v_scale go with an e4m3 cache")
-    ks = vs = None
-    if f8:
-        if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
-            _refuse("k_scale and v_scale must be [pages, heads_kv]")
-        ks = _arg(k_scale, "k_scale", dev, torch.float32)
-        vs = _arg(v_scale, "v_scale", dev, torch.float32)
-    return (TTS_E4M3 if f8 else TTS_BF16, shape, _arg(k_cache, "k_cache", dev, dt),
-            _arg(v_cache, "v_cache", dev, dt), ks, vs)
+def _attn_outputs(q, out, lse, want_lse, out_dtype):
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    return out, lse
 
 
 def rope_kv_append(k, v, k_cache, v_cache, page_tables, past_lens, cu_new, max_new, k_scale=None,
@@ -633,59 +575,21 @@ def rope_kv_append(k, v, k_cache, v_cache, page_tables, past_lens, cu_new, max_n
     int32 [batch], cu_new int32 [batch + 1], cos_sin of rope_cache or None (no rotation). The
     caches and scales are written in place. Returns (q_out bf16 [tokens, Hq, d] or None, k_out
     bf16 [tokens, Hkv, d]; k_out is None unless given or asked for with want_k)."""
-    dev = _device_of(k, "k")
-    code, (pages, hkv, ps, d), kc, vc, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
-    kshape = k.shape
-    if len(kshape) != 3 or kshape[1] != hkv or kshape[2] != d or v.shape != kshape:
-        _refuse("k, v must be [tokens, Hkv, head_dim] with the cache's heads")
-    total = kshape[0]
-    kp, k_stride = _token_rows(k, "k", dev, hkv, d)
-    vp, v_stride = _token_rows(v, "v", dev, hkv, d)
-    batch = past_lens.numel()
-    tshape = page_tables.shape
-    if len(tshape) != 2 or tshape[0] != batch or cu_new.numel() != batch + 1:
-        _refuse("page_tables must be [batch, max_pages], past_lens [batch], cu_new [batch + 1]")
-    csp, max_pos = None, 0
-    if cos_sin is not None:
-        cshape = cos_sin.shape
-        if len(cshape) != 3 or cshape[1] != d // 2 or cshape[2] != 2:
-            _refuse("cos_sin must be [max_pos, head_dim/2, 2]")
-        csp, max_pos = _arg(cos_sin, "cos_sin", dev, torch.float32), cshape[0]
-    qp, q_stride, hq, qop, kop = None, 0, 0, None, None
-    if q is not None:
-        qshape = q.shape
-        if len(qshape) != 3 or qshape[0] != total or qshape[2] != d:
-            _refuse("q must be [tokens, Hq, head_dim]")
-        hq = qshape[1]
-        qp, q_stride = _token_rows(q, "q", dev, hq, d)
-        if q_out is None:
-            q_out = torch.empty(qshape, dtype=torch.bfloat16, device=k.device)
-        elif q_out.shape != qshape:
-            _refuse("q_out must have q's shape")
-        qop = _arg(q_out, "q_out", dev, torch.bfloat16)
-    elif q_out is not None:
-        _refuse("q_out goes with q")
-    if k_out is None and want_k:
-        k_out = torch.empty(kshape, dtype=torch.bfloat16, device=k.device)
-    if k_out is not None:
-        if k_out.shape != kshape:
-            _refuse("k_out must have k's shape")
-        kop = _arg(k_out, "k_out", dev, torch.bfloat16)
-    _call((_lib or lib()).tts_rope_kv_append, "tts_rope_kv_append", dev, qp, q_stride, hq, kp,
-          k_stride, vp, v_stride, total, _arg(cu_new, "cu_new", dev, torch.int32),
-          _arg(past_lens, "past_lens", dev, torch.int32), batch, int(max_new), hkv, d, csp, max_pos,
-          _arg(page_tables, "page_tables", dev, torch.int32), tshape[1], kc, vc, ks, vs, code,
-          pages, ps, qop, kop,
-          None if status is None else _arg(status, "status", dev, torch.int32))
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if want_k and k_out is None:
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+    code = (_nat or _binding()).rope_kv_append(k, v, k_cache, v_cache, page_tables, past_lens,
+                                              cu_new, max_new, k_scale, v_scale, cos_sin, q, q_out,
+                                              k_out, status)
+    if code:
+        raise TTSError(code, "tts_rope_kv_append")
     return q_out, k_out
 
 
 def attn_decode_workspace_bytes(max_seqlen_q, num_heads_q, num_heads_kv, head_dim) -> int:
     return int(lib().tts_attn_decode_workspace_bytes(int(max_seqlen_q), int(num_heads_q),
                                                      int(num_heads_kv), int(head_dim)))
-
-
-_decode_workspace = {}  # (device, max_seqlen_q, Hq, Hkv, d): bytes
 
 
 def attn_decode_paged(q, k_cache, v_cache, page_tables, kv_lens, scale, cu_seqlens_q=None,
@@ -697,52 +601,20 @@ def attn_decode_paged(q, k_cache, v_cache, page_tables, kv_lens, scale, cu_seqle
 
     q bf16 [tokens, Hq, d] (one token per request without cu_seqlens_q), the cache as in
     rope_kv_append, kv_lens int32 [batch] with the new tokens counted. window > 0: a token sees
-    the last `window` positions up to its own and the first `sinks`. Returns (out [tokens, Hq, d]
-    in out_dtype, or in out's dtype: fp32 or bf16; lse fp32 [tokens, Hq])."""
-    dev = _device_of(q, "q")
-    code, (pages, hkv, ps, d), kc, vc, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != d:
-        _refuse("q must be [tokens, Hq, head_dim]")
-    total, hq = shape[0], shape[1]
-    batch = kv_lens.numel()
-    tshape = page_tables.shape
-    if len(tshape) != 2 or tshape[0] != batch:
-        _refuse("page_tables must be [batch, max_pages], kv_lens [batch]")
-    cup = None
-    if cu_seqlens_q is not None:
-        if cu_seqlens_q.numel() != batch + 1:
-            _refuse("cu_seqlens_q must be [batch + 1]")
-        cup = _arg(cu_seqlens_q, "cu_seqlens_q", dev, torch.int32)
-    elif total != batch:
-        _refuse("q has one token per request without cu_seqlens_q")
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
-    odt = out.dtype
-    if out.shape != shape or (odt != torch.bfloat16 and odt != torch.float32):
-        _refuse("out must be fp32 or bf16 [tokens, Hq, head_dim]")
-    if lse is None and want_lse:
-        lse = torch.empty((total, hq), dtype=torch.float32, device=q.device)
-    lp = None
-    if lse is not None:
-        if lse.shape != shape[:2]:
-            _refuse("lse must be [tokens, Hq]")
-        lp = _arg(lse, "lse", dev, torch.float32)
-    key = (dev, max_seqlen_q, hq, hkv, d)
-    need = _decode_workspace.get(key)
-    if need is None:
-        with torch.cuda.device(dev):
-            need = _decode_workspace[key] = attn_decode_workspace_bytes(*key[1:])
-    have = 0 if workspace is None else workspace.nbytes
-    if have < need:
+    the last `window` positions up to its own and the first `sinks`. A workspace is allocated
+    here when it is missing or too small. Returns (out [tokens, Hq, d] in out_dtype, or in out's
+    dtype: fp32 or bf16; lse fp32 [tokens, Hq])."""
+    out, lse = _attn_outputs(q, out, lse, want_lse, out_dtype)
+    call = (_nat or _binding()).attn_decode_paged
+    code = call(q, k_cache, v_cache, k_scale, v_scale, page_tables, kv_lens, cu_seqlens_q,
+                max_seqlen_q, window, sinks, scale, out, lse, workspace, status)
+    if code == TTS_ERR_WORKSPACE:  # missing or too small: nothing was enqueued
+        with torch.cuda.device(q.device):
+            need = attn_decode_workspace_bytes(max_seqlen_q, q.shape[1], k_cache.shape[1],
+                                               q.shape[2])
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        have = need
-    wp = _arg(workspace, "workspace", dev, workspace.dtype) if have else None
-    _call((_lib or lib()).tts_attn_decode_paged, "tts_attn_decode_paged", dev,
-          _arg(q, "q", dev, torch.bfloat16), total, cup, batch, int(max_seqlen_q), hq, hkv, d, kc,
-          vc, ks, vs, code, pages, ps, _arg(page_tables, "page_tables", dev, torch.int32),
-          tshape[1], _arg(kv_lens, "kv_lens", dev, torch.int32), int(window), int(sinks),
-          float(scale), _arg(out, "out", dev, odt),
-          TTS_BF16 if odt == torch.bfloat16 else TTS_F32, lp, wp, have,
-          None if status is None else _arg(status, "status", dev, torch.int32))
+        code = call(q, k_cache, v_cache, k_scale, v_scale, page_tables, kv_lens, cu_seqlens_q,
+                    max_seqlen_q, window, sinks, scale, out, lse, workspace, status)
+    if code:
+        raise TTSError(code, "tts_attn_decode_paged")
     return out, lse

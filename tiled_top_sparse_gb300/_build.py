@@ -2,7 +2,8 @@
 
 Each .cu file compiles in its own nvcc process (in parallel), then nvcc links
 the shared library with the CUDA runtime linked statically, so the library
-loads on a machine without a GPU (the driver is looked up at run time).
+loads on a machine without a GPU (the driver is looked up at run time). The CPython
+module of the grouped-query calls (csrc/native.c) is built beside it with the C compiler.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtts.so")
+NATIVE_SRC = os.path.join(CSRC, "native.c")
+NATIVE = os.path.join(PKG, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]
@@ -43,7 +47,23 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_native(force: bool = False) -> str:
+    deps = (NATIVE_SRC, os.path.join(ROOT, "include", "tts.h"), __file__)
+    if not force and os.path.exists(NATIVE) and all(
+            os.path.getmtime(p) <= os.path.getmtime(NATIVE) for p in deps):
+        return NATIVE
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-shared", "-fPIC",
+           "-I" + sysconfig.get_paths()["include"], NATIVE_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {NATIVE_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+    return NATIVE
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    build_native(force)
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
