@@ -315,6 +315,9 @@ def run_decode(tts, seed, new, kv, hq, hkv, d, ps, f8, window=0, sinks=0, out_dt
     ([2, 1], [1500, 1300], 4, 2, 64, 128, 1, 1),                 # only itself and the first
     ([1, 1], [600, 200], 4, 2, 128, 64, 500, 300),               # sinks meet the window
     ([1], [300], 4, 2, 128, 64, 2 ** 31 - 1, 2 ** 31 - 1),
+    ([6, 1, 3], [700, 80, 2000], 16, 2, 128, 64, 0, 0),          # 48, 8 and 24 rows of a unit
+    ([6, 4, 0, 5], [1300, 40, 9, 500], 12, 2, 64, 32, 200, 4),   # 36 rows, a window per token
+    ([9, 2], [1000, 300], 20, 2, 128, 16, 0, 0),                 # 90 rows: two units
 ])
 def test_decode_parity(tts, f8, new, kv, hq, hkv, d, ps, window, sinks):
     run_decode(tts, sum(kv) + ps, new, kv, hq, hkv, d, ps, f8, window, sinks)
@@ -325,6 +328,13 @@ def test_decode_many_requests_bf16_out(tts, f8):
     r = np.random.default_rng(3)
     kv = [int(x) for x in r.integers(1, 900, 200)]
     run_decode(tts, 20, [1] * 200, kv, 4, 2, 128, 64, f8, out_dtype=torch.bfloat16, one=True)
+
+
+@pytest.mark.parametrize("f8", [True, False])
+def test_decode_one_long_request(tts, f8):
+    """One KV head of one request over the whole GPU: hundreds of parts joined."""
+    run_decode(tts, 25, [1], [40000], 2, 1, 128, 64, f8)
+    run_decode(tts, 26, [6], [20000], 8, 1, 64, 16, f8)
 
 
 def test_decode_queries_of_any_size(tts):

@@ -95,6 +95,8 @@ def test_many_items_per_cta(tts):
     """More items than CTAs: the ring, the Q tiles and the accumulators are reused."""
     check(tts, 7, [1500, 700, 1100], None, 16, 4, 128, 300, 4)
     check(tts, 8, [1200, 900], None, 32, 8, 64, 200, 130)
+    check(tts, 11, [1500, 700], None, 15, 5, 128, 260, 4)   # an odd group: pairs of row tiles
+    check(tts, 12, [1300, 500, 129], None, 12, 12, 80, 100, 1)
 
 
 @pytest.mark.parametrize("d", [64, 80, 128])
@@ -107,6 +109,11 @@ def test_wide_window_equals_causal(tts, d):
     a = tts.attn_fwd_varlen_window(q, k, v, cu, cu, 500, 500, 500, 3, d ** -0.5)
     b = tts.attn_fwd_varlen(q, k, v, cu, cu, 500, 500, True, d ** -0.5)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for hq, hkv in ((24, 6), (21, 7)):  # more tiles than SMs: pairs of heads, pairs of row tiles
+        q, k, v = inputs(13, lens, lens, hq, hkv, d, torch.bfloat16)
+        a = tts.attn_fwd_varlen_window(q, k, v, cu, cu, 500, 500, 500, 3, d ** -0.5)
+        b = tts.attn_fwd_varlen(q, k, v, cu, cu, 500, 500, True, d ** -0.5)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_bad_sequences_are_reported(tts):

@@ -3,13 +3,13 @@
 // tokens that stay visible.
 //
 // For KV head g the q rows of its group (token-major: row = token * G + head in the group)
-// are tiles of 8 NT rows; a unit is (request, g, row tile) and a tile is kTK consecutive keys.
+// are tiles of 8 to 64 rows; a unit is (request, g, row tile) and a tile is kTK consecutive keys.
 // With x_j = scale log2(e) sK[page(j)] q.k_j (q.k over codes), y_j = x_j + log2 sV[page(j)]:
 //   out = sum_j 2^(y_j - m) v_j / sum_j 2^(y_j - m) / sV[page(j)],  lse = ln 2 (m + log2 of the
 // denominator): the value scale rides in the exponent, so weights of pages with different
 // scales share one fp16 product with the codes, and the running maximum m is taken over y.
 //
-// Bound: HBM (each cached byte is used by 8 NT rows only). All tiles of all units form one
+// Bound: HBM (a cached byte is used by a unit's few rows only). All tiles of all units form one
 // list, cut into equal runs, one per CTA (two CTAs per SM), so ragged batches, one request and
 // many requests all fill the GPU; a unit cut by a run's border leaves unnormalised partial
 // sums, joined in a fixed order by a second launch. In a CTA one warp brings tiles by TMA
@@ -43,7 +43,9 @@ constexpr int kEndTiles = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-template <bool F8, int D, int NT>
+// NT: 8-row n tiles of a warp; RG: row groups. With RG > 1 every tile of keys is worked on by RG
+// warps, each for its own 8 NT rows, so that a unit of 8 NT RG rows reads its keys once.
+template <bool F8, int D, int NT, int RG>
 struct Cfg {
   static constexpr int kRowBytes = D * (F8 ? 1 : 2);
   static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;  // one swizzled TMA box row
@@ -52,10 +54,12 @@ struct Cfg {
   static constexpr int kMT = kTK / 16;
   static constexpr int kKBytes = kTK * kRowBytes;  // K (or V) of one tile
   static constexpr int kStageBytes = 2 * kKBytes;
-  static constexpr int kR = 8 * NT;        // q rows per unit
+  static constexpr int kGR = 8 * NT;       // q rows per row group
+  static constexpr int kR = kGR * RG;      // q rows per unit
+  static constexpr int kGW = kNW / RG;     // warps per row group: each takes every kGW-th tile
   static constexpr int kKS = D / 16;       // k steps of the first product, m tiles of the second
-  static constexpr int kMQ = kKS / kNW;    // m tiles each warp finishes when a unit ends
-  static constexpr int kJoinBytes = kNW * (kNW - 1) * NT * kMQ * 4 * 32 * 4;
+  static constexpr int kMQ = kKS / kGW;    // m tiles each warp finishes when a unit ends
+  static constexpr int kJoinBytes = kNW * (kGW - 1) * NT * kMQ * 4 * 32 * 4;
   // Two CTAs per SM: 113 KB each, less 1 KB to align the ring and 1 KB of barriers.
   static constexpr int kStagesFit = (113 * 1024 - 2048 - kJoinBytes) / kStageBytes;
   static constexpr int kStages = kStagesFit < 12 ? kStagesFit : 12;
@@ -212,16 +216,17 @@ struct Meta {  // of a ring slot, written by the producer
   float vi[4];   // 1 / that scale
 };
 
-template <bool F8, int D, int NT>
+template <bool F8, int D, int NT, int RG>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const Params p) {
-  using C = Cfg<F8, D, NT>;
-  constexpr int TK = C::kTK, MT = C::kMT, S = C::kStages, R = C::kR, KS = C::kKS;
+  using C = Cfg<F8, D, NT, RG>;
+  constexpr int TK = C::kTK, MT = C::kMT, S = C::kStages, R = C::kR, KS = C::kKS, GR = C::kGR,
+                GW = C::kGW;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[S], bar_empty[S];
   __shared__ Meta s_meta[S];
-  __shared__ __align__(8) float s_m[kNW][R], s_l[kNW][R];  // references and sums of every row
+  __shared__ __align__(8) float s_m[kNW][GR], s_l[kNW][GR];  // references and sums of every row
   __shared__ int s_scan[kThreads / 32], s_b, s_off, s_abort, s_issued;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     s_abort = s_issued = 0;
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_u32(&bar_full[i]), 1);
-      mbar_init(smem_u32(&bar_empty[i]), 1);
+      mbar_init(smem_u32(&bar_empty[i]), RG);
     }
     fence_mbar_init();
     p.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -250,11 +255,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     return x;
   };
   auto tiles_of = [&](const Req& r) -> int { return p.hkv * r.rt * (r.nt + kEndTiles); };
-  // Runs of at least kNW places (the warps take one each, side by side): shorter ones would
+  // Runs of at least GW places (the warps take one each, side by side): shorter ones would
   // only leave more parts to join. The first `more` runs have one tile more than the others.
   int total = 0, runs = 0, len = 0, more = 0, t0 = 0, t1 = 0;
   auto split = [&]() -> bool {
-    runs = min((int)((unsigned)(total + kNW - 1) / kNW), p.ctas);
+    runs = min((int)((unsigned)(total + GW - 1) / GW), p.ctas);
     if ((int)blockIdx.x >= runs) return false;
     len = (int)((unsigned)total / (unsigned)runs);
     more = total - len * runs;
@@ -443,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     constexpr float kThr = F8 ? 4.f : 8.f;    // the reference moves when exceeded by 2^kThr
     constexpr float kBias = F8 ? 11.f : 0.f;  // P is held times 2^kBias: at most 2^15 in fp16
     const int g8 = lane >> 2, t4 = lane & 3;
+    const int rg = warp / GW, wi = warp % GW;  // row group, place in it
     const int piece_shift = 31 - __clz(piece >> 4);  // 16-key m tile -> piece
     // Bounded wait until the producer has issued tile i (usually long ago).
     auto issued = [&](int i) -> bool {
@@ -463,7 +469,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const int before = t1 - left;
       if (!next_seg(g, rt, x0, x1)) continue;
       const bool whole_l = x0 == 0, whole_r = x1 == r.nt;
-      const int rows = r.n * p.group - rt * R;  // rows of this tile: min(rows, R)
+      const int row0 = rt * R + rg * GR;  // this row group's first row, and its rows: up to GR
+      const int rows = min(r.n * p.group - row0, GR);
 
       // q fragments of column g8 of every n tile: step i takes elements e0(i) .. e0(i) + 3
       uint32_t qf[NT][KS][2];
@@ -471,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       int pos0[NT], pos1[NT];    // positions of the two rows
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const int rr = rt * R + j * 8 + g8;
+        const int rr = row0 + j * 8 + g8;
         const bool in = j * 8 + g8 < rows;
         const int tok = in && p.max_q > 1 ? rr / p.group : 0;
         const int h = in ? g * p.group + (rr - tok * p.group) : 0;
@@ -521,9 +528,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         pos1[j] = __shfl_sync(0xFFFFFFFFu, pos, (2 * t4 + 1) * 4);
       }
       // every row sees keys [max_lo, min_end) (and the first sinks)
-      const int last_row = rt * R + (rows < R ? rows : R) - 1;
-      const int min_end = r.L - r.n + (p.max_q > 1 ? rt * R / p.group : 0) + 1;
-      const int max_pos = r.L - r.n + (p.max_q > 1 ? last_row / p.group : 0);
+      const int min_end = r.L - r.n + (p.max_q > 1 ? row0 / p.group : 0) + 1;
+      const int max_pos = r.L - r.n + (p.max_q > 1 ? (row0 + rows - 1) / p.group : 0);
       const int max_lo = p.window > 0 ? max_pos + 1 - p.window : 0;
 
       float o[NT][KS][4];
@@ -539,10 +545,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
 
       for (int x = x0; x < x1; ++x, ++it) {
-        if (it % kNW != warp) continue;
+        if (it % GW != wi) continue;
         const int st = it % S;
         // A parity wait is only unambiguous against the phase in progress. The slot's previous
-        // tile is another warp's (kNW need not divide kStages) and copies may land out of
+        // tile may be another warp's (GW need not divide S) and copies may land out of
         // order, so the tile must have been issued first: that tells that the slot's earlier
         // phases are complete.
         if (!issued(it) ||
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const uint32_t okp = s_meta[st].ok;
         const bool all_pieces = okp == (1u << n_pieces) - 1u;
         // rows of the tile that some new token sees all lie in pieces that are there
-        if (okp != 0) {
+        if (okp != 0 && rows > 0) {
           // ---- S^T = K Q^T
           float s[NT][MT][4];
 #pragma unroll
@@ -744,8 +750,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (lane == 0) mbar_arrive(smem_u32(&bar_empty[st]));
       }
 
-      // ---- join the four warps: the largest reference first, then warp w sums m tiles
-      // [w kMQ, (w + 1) kMQ) of all four
+      // ---- join the row group's warps: the largest reference first, then warp wi sums m tiles
+      // [wi kMQ, (wi + 1) kMQ) of all of them
+      auto group_sync = [&]() {
+        if constexpr (GW > 1)
+          named_barrier_sync(1 + rg, GW * 32);
+        else
+          __syncwarp();
+      };
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -756,14 +768,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (g8 == 0)
           *reinterpret_cast<float2*>(&s_m[warp][j * 8 + 2 * t4]) = make_float2(m0[j], m1[j]);
       }
-      named_barrier_sync(1, kNW * 32);
+      group_sync();
       float top0[NT], top1[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         top0[j] = top1[j] = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kNW; ++w) {
-          const float2 m = *reinterpret_cast<const float2*>(&s_m[w][j * 8 + 2 * t4]);
+        for (int w = 0; w < GW; ++w) {
+          const float2 m = *reinterpret_cast<const float2*>(&s_m[rg * GW + w][j * 8 + 2 * t4]);
           top0[j] = fmaxf(top0[j], m.x);
           top1[j] = fmaxf(top1[j], m.y);
         }
@@ -779,15 +791,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           o[j][i][3] *= a1;
         }
       }
-      // slot of (summing warp, source warp): every source but itself
-      auto join_at = [&](int dst, int src) -> float* {
-        const int k = src < dst ? src : src - 1;
-        return join + (dst * (kNW - 1) + k) * (NT * C::kMQ * 4 * 32) + lane;
-      };
+      // slot of (summing warp, source warp) of the group: every source but itself
+      constexpr int kSlot = NT * C::kMQ * 4 * 32;
+      float* const group_join = join + rg * (GW * (GW - 1) * kSlot) + lane;
 #pragma unroll
-      for (int dst = 0; dst < kNW; ++dst) {
-        if (dst == warp) continue;
-        float* to = join_at(dst, warp);
+      for (int dst = 0; dst < GW; ++dst) {
+        if (dst == wi) continue;
+        float* to = group_join + (dst * (GW - 1) + (wi < dst ? wi : wi - 1)) * kSlot;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -796,15 +806,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int k = 0; k < 4; ++k)
               to[((j * C::kMQ + i) * 4 + k) * 32] = o[j][dst * C::kMQ + i][k];
       }
-      named_barrier_sync(1, kNW * 32);
+      group_sync();
       const bool final = whole_l && whole_r;
       float* part = p.parts + (size_t)(2 * blockIdx.x + (whole_l ? 1 : 0)) * (R * (D + 2));
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float acc[C::kMQ][4];
 #pragma unroll
-        for (int d = 0; d < kNW; ++d)
-          if (d == warp) {
+        for (int d = 0; d < GW; ++d)
+          if (d == wi) {
 #pragma unroll
             for (int i = 0; i < C::kMQ; ++i)
 #pragma unroll
@@ -812,8 +822,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           }
         // ((own + first) + second) + third other: the same order every time
 #pragma unroll
-        for (int w = 0; w < kNW - 1; ++w) {
-          const float* from = join + (warp * (kNW - 1) + w) * (NT * C::kMQ * 4 * 32) + lane;
+        for (int w = 0; w < GW - 1; ++w) {
+          const float* from = group_join + (wi * (GW - 1) + w) * kSlot;
 #pragma unroll
           for (int i = 0; i < C::kMQ; ++i)
 #pragma unroll
@@ -821,8 +831,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kNW; ++w) {
-          const float2 l = *reinterpret_cast<const float2*>(&s_l[w][j * 8 + 2 * t4]);
+        for (int w = 0; w < GW; ++w) {
+          const float2 l = *reinterpret_cast<const float2*>(&s_l[rg * GW + w][j * 8 + 2 * t4]);
           sum.x += l.x;
           sum.y += l.y;
         }
@@ -838,22 +848,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             v[2 * i + 1] = acc[i][k + 2] * inv;
           }
           int64_t at = 0;
+          if (row >= rows) continue;
           if (final) {
-            if (row >= rows) continue;
-            const int rr = rt * R + row, tok = p.max_q > 1 ? rr / p.group : 0;
+            const int rr = row0 + row, tok = p.max_q > 1 ? rr / p.group : 0;
             at = (int64_t)(r.q0 + tok) * p.hq + g * p.group + (rr - tok * p.group);
           }
-          float* to32 = final ? static_cast<float*>(p.out) + at * D : part + row * D;
+          float* to32 = final ? static_cast<float*>(p.out) + at * D : part + (rg * GR + row) * D;
           uint16_t* to16 = static_cast<uint16_t*>(p.out) + at * D;
           const bool half = final && p.out_bf16;
           if constexpr (F8) {  // elements d0 .. d0 + 2 kMQ - 1 of the row
-            const int d0 = (D / 8) * g8 + 2 * C::kMQ * warp;
-            if constexpr (C::kMQ == 2) {
-              if (half)
-                *reinterpret_cast<uint2*>(to16 + d0) =
-                    make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-              else
-                *reinterpret_cast<float4*>(to32 + d0) = make_float4(v[0], v[1], v[2], v[3]);
+            const int d0 = (D / 8) * g8 + 2 * C::kMQ * wi;
+            if constexpr (C::kMQ >= 2) {
+#pragma unroll
+              for (int i = 0; i < 2 * C::kMQ; i += 4) {
+                if (half)
+                  *reinterpret_cast<uint2*>(to16 + d0 + i) =
+                      make_uint2(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]));
+                else
+                  *reinterpret_cast<float4*>(to32 + d0 + i) =
+                      make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              }
             } else {
               if (half)
                 *reinterpret_cast<uint32_t*>(to16 + d0) = pack_bf16x2(v[0], v[1]);
@@ -863,19 +877,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           } else {  // elements 16 m + g8 and 16 m + g8 + 8 of m tile m
 #pragma unroll
             for (int i = 0; i < 2 * C::kMQ; ++i) {
-              const int d = 16 * (warp * C::kMQ + i / 2) + g8 + 8 * (i & 1);
+              const int d = 16 * (wi * C::kMQ + i / 2) + g8 + 8 * (i & 1);
               if (half)
                 to16[d] = (uint16_t)pack_bf16x2(v[i], 0.f);
               else
                 to32[d] = v[i];
             }
           }
-          if (warp == 0 && g8 == 0) {
+          if (wi == 0 && g8 == 0) {
             if (final) {
               if (p.lse != nullptr)
                 p.lse[at] = l > 0.f ? (top - kBias + log2f(l)) * kLn2 : -INFINITY;
             } else {
-              *reinterpret_cast<float2*>(part + R * D + 2 * row) = make_float2(top, l);
+              *reinterpret_cast<float2*>(part + R * D + 2 * (rg * GR + row)) = make_float2(top, l);
             }
           }
         }
@@ -887,79 +901,76 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int c0 = begin < longer
                            ? (int)((unsigned)begin / (unsigned)(len + 1))
                            : more + (int)((unsigned)(begin - longer) / (unsigned)len);
-        p.jobs[blockIdx.x] = make_int4(c0, rows < R ? rows : R, rt * R, g);
+        p.jobs[blockIdx.x] = make_int4(c0, min(r.n * p.group - rt * R, R), rt * R, g);
         p.job_q0[blockIdx.x] = r.q0;
       }
-      named_barrier_sync(1, kNW * 32);
+      group_sync();  // before the next unit's references and sums
     }
   }
 }
 
-// Joins the parts of the units that CTA borders cut: block (c, j) for rows 8 j .. 8 j + 7 of the
-// unit that ended in CTA c. Eight warps take every eighth part each (all eight rows' loads in
-// flight together), then warp w joins the warps' results for row 8 j + w, in order.
-template <bool F8, int D, int NT>
-__global__ void __launch_bounds__(256) attn_decode_join_kernel(const Params p) {
-  using C = Cfg<F8, D, NT>;
-  constexpr int R = C::kR;
-  constexpr float kBias = F8 ? 11.f : 0.f;
-  __shared__ float2 s_ml[8][8];
-  __shared__ float4 s_acc[8][8][D / 4];
-  const int c1 = blockIdx.x, row0 = blockIdx.y * 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Joins the parts of the units that CTA borders cut: block (c, row) for one row of the unit that
+// ended in CTA c. Four warps take every fourth part each, kBatch parts' loads in flight (a unit
+// of one long request may have hundreds), then the warps' results are joined in order.
+template <int D>
+__global__ void __launch_bounds__(128) attn_decode_join_kernel(const Params p, int R, float bias) {
+  constexpr int kWarps = 4, kBatch = 4;
+  __shared__ float2 s_ml[kWarps];
+  __shared__ float4 s_acc[kWarps][D / 4];
+  const int c1 = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 job = p.jobs[c1];
   const int q0 = p.job_q0[c1];
-  if (job.x < 0 || row0 >= job.y) return;
+  if (job.x < 0 || row >= job.y) return;
   const bool mine = lane < D / 4;
-  float top[8], sum[8];
-  float4 acc[8];
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = zero;
+  for (int c = job.x + warp; c <= c1; c += kWarps * kBatch) {
+    float2 ml[kBatch];
+    float4 v[kBatch];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    top[i] = -INFINITY;
-    sum[i] = 0.f;
-    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  for (int c = job.x + warp; c <= c1; c += 8) {
-    const float* part = p.parts + (size_t)(2 * c + (c == job.x ? 1 : 0)) * (R * (D + 2));
-    float2 ml[8];
-    float4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ml[i] = *reinterpret_cast<const float2*>(part + R * D + 2 * (row0 + i));
-      v[i] = mine ? *reinterpret_cast<const float4*>(part + (row0 + i) * D + lane * 4)
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < kBatch; ++i) {
+      const int cc = c + i * kWarps;
+      ml[i] = make_float2(-INFINITY, 0.f);
+      v[i] = zero;
+      if (cc <= c1) {
+        const float* part = p.parts + (size_t)(2 * cc + (cc == job.x ? 1 : 0)) * (R * (D + 2));
+        ml[i] = *reinterpret_cast<const float2*>(part + R * D + 2 * row);
+        if (mine) v[i] = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
+      }
     }
+    float n = top;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float n = fmaxf(top[i], ml[i].x);
-      const float fa = top[i] == -INFINITY ? 0.f : ex2_approx(top[i] - n);
-      const float fb = ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - n);
-      top[i] = n;
-      sum[i] = sum[i] * fa + ml[i].y * fb;
-      acc[i].x = acc[i].x * fa + v[i].x * fb;
-      acc[i].y = acc[i].y * fa + v[i].y * fb;
-      acc[i].z = acc[i].z * fa + v[i].z * fb;
-      acc[i].w = acc[i].w * fa + v[i].w * fb;
+    for (int i = 0; i < kBatch; ++i) n = fmaxf(n, ml[i].x);
+    const float f = top == -INFINITY ? 0.f : ex2_approx(top - n);
+    top = n;
+    sum *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float fi = ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - n);
+      sum = fmaf(ml[i].y, fi, sum);
+      acc.x = fmaf(v[i].x, fi, acc.x);
+      acc.y = fmaf(v[i].y, fi, acc.y);
+      acc.z = fmaf(v[i].z, fi, acc.z);
+      acc.w = fmaf(v[i].w, fi, acc.w);
     }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (lane == 0) s_ml[warp][i] = make_float2(top[i], sum[i]);
-    if (mine) s_acc[warp][i][lane] = acc[i];
-  }
+  if (lane == 0) s_ml[warp] = make_float2(top, sum);
+  if (mine) s_acc[warp][lane] = acc;
   __syncthreads();
-  const int row = row0 + warp;
-  if (row >= job.y) return;
+  if (warp != 0) return;
   float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 o = zero;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) m = fmaxf(m, s_ml[w][warp].x);
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w].x);
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const float2 ml = s_ml[w][warp];
+  for (int w = 0; w < kWarps; ++w) {
+    const float2 ml = s_ml[w];
     const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
     l = fmaf(ml.y, f, l);
     if (mine) {
-      const float4 v = s_acc[w][warp][lane];
+      const float4 v = s_acc[w][lane];
       o.x = fmaf(v.x, f, o.x);
       o.y = fmaf(v.y, f, o.y);
       o.z = fmaf(v.z, f, o.z);
@@ -979,17 +990,22 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const Params p) {
     }
   }
   if (p.lse != nullptr && lane == 0)
-    p.lse[at] = l > 0.f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+    p.lse[at] = l > 0.f ? (m - bias + log2f(l)) * kLn2 : -INFINITY;
 }
 
-int rows_of(int max_q, int group) { return max_q * group <= 8 ? 8 : 16; }
+// Rows of a unit: the least of 8, 16, 32 and 64 that holds a request's rows of one KV head (64
+// for more, in several units).
+int rows_of(int max_q, int group) {
+  const int64_t rows = (int64_t)max_q * group;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
 size_t job_bytes(size_t ctas) {
   return (ctas * (sizeof(int4) + sizeof(int)) + 255) / 256 * 256;
 }
 
-template <bool F8, int D, int NT>
+template <bool F8, int D, int NT, int RG>
 cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t stream) {
-  using C = Cfg<F8, D, NT>;
+  using C = Cfg<F8, D, NT, RG>;
   Params p;
   p.q = static_cast<const uint16_t*>(a.q);
   p.cu_q = a.cu_q;
@@ -1035,20 +1051,24 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   };
   if (!make(&mk, const_cast<void*>(a.k_cache)) || !make(&mv, const_cast<void*>(a.v_cache)))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<F8, D, NT>,
+  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<F8, D, NT, RG>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  attn_decode_kernel<F8, D, NT><<<p.ctas, kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
+  attn_decode_kernel<F8, D, NT, RG><<<p.ctas, kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_decode_join_kernel<F8, D, NT><<<dim3(p.ctas, NT), 256, 0, stream>>>(p);
+  attn_decode_join_kernel<D><<<dim3(p.ctas, C::kR), 128, 0, stream>>>(p, C::kR, F8 ? 11.f : 0.f);
   return cudaGetLastError();
 }
 
 template <bool F8, int D>
 cudaError_t launch_nt(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t stream) {
-  return rows_of(a.max_q, a.hq / a.hkv) == 8 ? launch<F8, D, 1>(a, sms, drv_err, stream)
-                                             : launch<F8, D, 2>(a, sms, drv_err, stream);
+  switch (rows_of(a.max_q, a.hq / a.hkv)) {
+    case 8: return launch<F8, D, 1, 1>(a, sms, drv_err, stream);
+    case 16: return launch<F8, D, 2, 1>(a, sms, drv_err, stream);
+    case 32: return launch<F8, D, 2, 2>(a, sms, drv_err, stream);
+    default: return launch<F8, D, 2, 4>(a, sms, drv_err, stream);
+  }
 }
 
 }  // namespace
