@@ -25,6 +25,8 @@
 // fp16 with its reference kept so that 2^-25 of the maximum still has all 11 bits. bf16
 // caches use bf16 products throughout. Sums and softmax statistics are fp32.
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -43,23 +45,38 @@ constexpr int kEndTiles = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-// NT: 8-row n tiles of a warp; RG: row groups. With RG > 1 every tile of keys is worked on by RG
-// warps, each for its own 8 NT rows, so that a unit of 8 NT RG rows reads its keys once.
-template <bool F8, int D, int NT, int RG>
+// NT: 8-row n tiles of a warp. kGroups: a request with more than 8 NT rows per KV head has them
+// worked on by 2 or 4 row groups of warps on the same tiles of keys (which are then read once for
+// up to 32 NT rows), one with fewer by all warps on different tiles.
+template <bool F8, int D, int NT>
 struct Cfg {
   static constexpr int kRowBytes = D * (F8 ? 1 : 2);
   static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;  // one swizzled TMA box row
   static constexpr int kPanels = kRowBytes / kPanelBytes;
-  static constexpr int kTK = kRowBytes == 256 ? 32 : 64;  // keys per tile
+  // Keys per tile: 16 KB of K and V together, so that the producer's work per tile is a small
+  // part of the time its bytes take, but no more than 64 keys' scores in registers with two n
+  // tiles (64-wide e4m3 rows, 20,000 keys: 8 KB tiles 46.5 us, 16 KB tiles XX us).
+  static constexpr int kTK = kRowBytes == 256 ? 32 : kRowBytes == 64 && NT == 1 ? 128 : 64;
   static constexpr int kMT = kTK / 16;
   static constexpr int kKBytes = kTK * kRowBytes;  // K (or V) of one tile
   static constexpr int kStageBytes = 2 * kKBytes;
   static constexpr int kGR = 8 * NT;       // q rows per row group
-  static constexpr int kR = kGR * RG;      // q rows per unit
-  static constexpr int kGW = kNW / RG;     // warps per row group: each takes every kGW-th tile
   static constexpr int kKS = D / 16;       // k steps of the first product, m tiles of the second
-  static constexpr int kMQ = kKS / kGW;    // m tiles each warp finishes when a unit ends
-  static constexpr int kJoinBytes = kNW * (kGW - 1) * NT * kMQ * 4 * 32 * 4;
+  static constexpr int kPieces = kTK / 16;  // pages of a tile at most
+  static constexpr int kQStride = D * 2 + 16;  // bytes per q row in shared memory (two n tiles)
+  // Behind the ring: the warps' accumulators on their way to the one that sums them, and the q
+  // rows of RG row groups. They share the room: RG groups leave 1 / RG of the warps to join.
+  template <int RG>
+  static constexpr int join_bytes() {
+    return kNW * (kNW / RG - 1) * NT * (kKS * RG / kNW) * 4 * 32 * 4;
+  }
+  template <int RG>
+  static constexpr int room() {
+    return join_bytes<RG>() + (NT > 1 ? RG * kGR * kQStride : 0);
+  }
+  static constexpr int kJoinBytes =
+      room<1>() > room<2>() ? (room<1>() > room<4>() ? room<1>() : room<4>())
+                            : (room<2>() > room<4>() ? room<2>() : room<4>());
   // Two CTAs per SM: 113 KB each, less 1 KB to align the ring and 1 KB of barriers.
   static constexpr int kStagesFit = (113 * 1024 - 2048 - kJoinBytes) / kStageBytes;
   static constexpr int kStages = kStagesFit < 12 ? kStagesFit : 12;
@@ -75,7 +92,7 @@ struct Params {
   const float* v_scale;
   void* out;
   float* lse;
-  float* parts;  // [2 * CTAs][kR * (D + 2)]
+  float* parts;  // [2 * CTAs][unit_rows * (D + 2)]
   // [CTAs], of the unit that was begun in an earlier CTA and ended in this one: {first CTA
   // (-1: no such unit), rows, first row within the request, g}
   int4* jobs;
@@ -84,7 +101,7 @@ struct Params {
   int total_q, max_keys;
   int batch, max_q, hq, hkv, group, num_pages, max_pages, page_size, page_shift, window, sinks;
   float scale_log2;
-  int out_bf16, ctas;
+  int out_bf16, ctas, unit_rows, row_shift;  // a unit's q rows (a power of two)
 };
 
 // A request as the kernel sees it: its tokens, its visible keys as two runs of tiles (first
@@ -113,7 +130,7 @@ __device__ __forceinline__ void read_req(const Params& p, int b, int& n, int& L,
     L = 0;  // its rows see no key
   }
 }
-template <int TK, int R>
+template <int TK>
 __device__ __forceinline__ Req make_req(const Params& p, int n, int L, int q0) {
   Req r;
   r.n = n;
@@ -125,19 +142,19 @@ __device__ __forceinline__ Req make_req(const Params& p, int n, int L, int q0) {
   r.lt = (int)((unsigned)r.lo / TK);
   r.st = min((int)((unsigned)(r.sinks + TK - 1) / TK), r.lt);
   r.nt = max(r.st + (int)((unsigned)(L + TK - 1) / TK) - r.lt, 1);  // 1: an empty tile, zeros
-  r.rt = (int)((unsigned)(n * p.group + R - 1) / R);
+  r.rt = (n * p.group + p.unit_rows - 1) >> p.row_shift;
   return r;
 }
-template <int TK, int R>
+template <int TK>
 __device__ __forceinline__ Req load_req(const Params& p, int b, uint32_t* bad) {
   int n, L, q0;
   read_req(p, b, n, L, q0, bad);
-  return make_req<TK, R>(p, n, L, q0);
+  return make_req<TK>(p, n, L, q0);
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -145,7 +162,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -193,6 +210,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -209,23 +231,25 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row, int c) {
     return base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
+template <int kP>
 struct Meta {  // of a ring slot, written by the producer
   uint32_t ok;   // bit i: piece i of the tile (a page, or the tile if pages are larger) is there
-  float ks[4];   // scale of its keys
-  float vl[4];   // log2 of the scale of its values
-  float vi[4];   // 1 / that scale
+  float ks[kP];  // scale of its keys
+  float vl[kP];  // log2 of the scale of its values
+  float vi[kP];  // 1 / that scale
 };
 
-template <bool F8, int D, int NT, int RG>
+template <bool F8, int D, int NT, bool kGroups>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const Params p) {
-  using C = Cfg<F8, D, NT, RG>;
-  constexpr int TK = C::kTK, MT = C::kMT, S = C::kStages, R = C::kR, KS = C::kKS, GR = C::kGR,
-                GW = C::kGW;
+  using C = Cfg<F8, D, NT>;
+  constexpr int TK = C::kTK, MT = C::kMT, S = C::kStages, KS = C::kKS, GR = C::kGR;
+  // Releases of a ring slot: the one warp that worked on it, or with row groups every warp.
+  constexpr int kReleases = kGroups ? kNW : 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[S], bar_empty[S];
-  __shared__ Meta s_meta[S];
+  __shared__ Meta<F8 ? C::kPieces : 1> s_meta[S];
   __shared__ __align__(8) float s_m[kNW][GR], s_l[kNW][GR];  // references and sums of every row
   __shared__ int s_scan[kThreads / 32], s_b, s_off, s_abort, s_issued;
 
@@ -241,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     s_abort = s_issued = 0;
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_u32(&bar_full[i]), 1);
-      mbar_init(smem_u32(&bar_empty[i]), RG);
+      mbar_init(smem_u32(&bar_empty[i]), kReleases);
     }
     fence_mbar_init();
     p.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -255,11 +279,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     return x;
   };
   auto tiles_of = [&](const Req& r) -> int { return p.hkv * r.rt * (r.nt + kEndTiles); };
-  // Runs of at least GW places (the warps take one each, side by side): shorter ones would
+  // Runs of at least kNW places (the warps take one each, side by side): shorter ones would
   // only leave more parts to join. The first `more` runs have one tile more than the others.
   int total = 0, runs = 0, len = 0, more = 0, t0 = 0, t1 = 0;
   auto split = [&]() -> bool {
-    runs = min((int)((unsigned)(total + GW - 1) / GW), p.ctas);
+    runs = min((int)((unsigned)(total + kNW - 1) / kNW), p.ctas);
     if ((int)blockIdx.x >= runs) return false;
     len = (int)((unsigned)total / (unsigned)runs);
     more = total - len * runs;
@@ -273,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     int n = 0, L = 0, q0 = 0, v = 0;
     if (lane < p.batch) {
       read_req(p, lane, n, L, q0, &bad);
-      r = make_req<TK, R>(p, n, L, q0);
+      r = make_req<TK>(p, n, L, q0);
       v = tiles_of(r);
     }
     if (blockIdx.x == 0 && warp == 0 && bad && p.dev_status != nullptr)
@@ -283,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (!split()) return;
     b = __ffs(__ballot_sync(0xFFFFFFFFu, incl > t0)) - 1;
     off = t0 - __shfl_sync(0xFFFFFFFFu, incl - v, b);
-    r = make_req<TK, R>(p, __shfl_sync(0xFFFFFFFFu, n, b), __shfl_sync(0xFFFFFFFFu, L, b),
+    r = make_req<TK>(p, __shfl_sync(0xFFFFFFFFu, n, b), __shfl_sync(0xFFFFFFFFu, L, b),
                         __shfl_sync(0xFFFFFFFFu, q0, b));
   } else {
     auto block_scan = [&](int v, int* sum) -> int {  // inclusive
@@ -303,14 +327,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int base = 0; base < p.batch; base += kThreads) {
       const int i = base + tid;
       int sum;
-      block_scan(i < p.batch ? tiles_of(load_req<TK, R>(p, i, &bad)) : 0, &sum);
+      block_scan(i < p.batch ? tiles_of(load_req<TK>(p, i, &bad)) : 0, &sum);
       total += sum;
     }
     if (blockIdx.x == 0 && bad && p.dev_status != nullptr) atomicOr(p.dev_status, bad);
     if (!split()) return;
     for (int base = 0, carry = 0; base < p.batch && carry <= t0; base += kThreads) {
       const int i = base + tid;
-      const int v = i < p.batch ? tiles_of(load_req<TK, R>(p, i, &bad)) : 0;
+      const int v = i < p.batch ? tiles_of(load_req<TK>(p, i, &bad)) : 0;
       int sum;
       const int incl = carry + block_scan(v, &sum);
       if (incl > t0 && incl - v <= t0) {
@@ -322,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __syncthreads();
     b = s_b;
     off = s_off;
-    r = load_req<TK, R>(p, b, &bad);
+    r = load_req<TK>(p, b, &bad);
   }
   __syncthreads();
 
@@ -342,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         seg_rt = 0;
         if (++seg_g == p.hkv) {
           seg_g = 0;
-          do r = load_req<TK, R>(p, ++b, &bad);  // requests without new tokens have no units
+          do r = load_req<TK>(p, ++b, &bad);  // requests without new tokens have no units
           while (r.rt == 0);
         }
       }
@@ -387,15 +411,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           sk = p.k_scale[(int64_t)page * p.hkv + g];
           sv = p.v_scale[(int64_t)page * p.hkv + g];
         }
-        if (it >= S)
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bar_empty[st]), ((it / S) - 1) & 1,
-                                                 abort_flag, p.dev_status));
-        if (!ok) break;
         const int at = pg0 - cache_at + (lane < n_pieces ? lane : 0);
         const int pg = __shfl_sync(0xFFFFFFFFu, page, at);
         const int a = key0 + lane * piece;  // this lane's piece: keys [a, a + piece)
         const bool seen = lane < n_pieces && a < r.L && (a + piece > r.lo || a < r.sinks);
         const bool there = seen && pg >= 0;
+        const uint32_t sent = __ballot_sync(0xFFFFFFFFu, there);
+        uint32_t flag = seen && !there ? kDevIndexRange : 0u;
+        uint32_t use = sent;
+        float pk = 1.f, pl = 0.f, pi = 1.f;
+        auto scales = [&]() {
+          const uint32_t all = __ballot_sync(0xFFFFFFFFu, fine);
+          const bool good = there && ((all >> at) & 1u);
+          if (there && !good) flag |= kDevBadArg;  // no scale of a written page: keys skipped
+          use = __ballot_sync(0xFFFFFFFFu, good);
+          pk = __shfl_sync(0xFFFFFFFFu, ks, at);
+          pl = __shfl_sync(0xFFFFFFFFu, vl, at);
+          pi = __shfl_sync(0xFFFFFFFFu, vi, at);
+        };
+        if (F8 && !new_scales) scales();
+        // All of the above may be done before the slot is free; little is left behind the wait.
+        if (it >= S)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bar_empty[st]), ((it / S) - 1) & 1,
+                                                 abort_flag, p.dev_status));
+        if (!ok) break;
         const uint32_t bar = smem_u32(&bar_full[st]);
         if (there) {
           const uint32_t dst = ring + st * C::kStageBytes + lane * piece * kBox;
@@ -407,9 +446,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             tma_load_3d(dst + C::kKBytes + pn * TK * kBox, &map_v, bar, pn * 64, row, slab);
           }
         }
-        const uint32_t sent = __ballot_sync(0xFFFFFFFFu, there);
-        uint32_t flag = seen && !there ? kDevIndexRange : 0u;
-        uint32_t use = sent;
         if constexpr (F8) {
           if (new_scales) {
             cache_g = g;
@@ -417,13 +453,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             ks = sk;
             vl = fine ? log2f(sv) : 0.f;
             vi = fine ? 1.f / sv : 0.f;
+            scales();
           }
-          const uint32_t all = __ballot_sync(0xFFFFFFFFu, fine);
-          const bool good = there && ((all >> at) & 1u);
-          if (there && !good) flag |= kDevBadArg;  // no scale of a written page: keys skipped
-          use = __ballot_sync(0xFFFFFFFFu, good);
-          const float pk = __shfl_sync(0xFFFFFFFFu, ks, at), pl = __shfl_sync(0xFFFFFFFFu, vl, at),
-                      pi = __shfl_sync(0xFFFFFFFFu, vi, at);
           if (lane < n_pieces) {
             s_meta[st].ks[lane] = pk;
             s_meta[st].vl[lane] = pl;
@@ -448,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     constexpr float kThr = F8 ? 4.f : 8.f;    // the reference moves when exceeded by 2^kThr
     constexpr float kBias = F8 ? 11.f : 0.f;  // P is held times 2^kBias: at most 2^15 in fp16
     const int g8 = lane >> 2, t4 = lane & 3;
-    const int rg = warp / GW, wi = warp % GW;  // row group, place in it
     const int piece_shift = 31 - __clz(piece >> 4);  // 16-key m tile -> piece
     // Bounded wait until the producer has issued tile i (usually long ago).
     auto issued = [&](int i) -> bool {
@@ -464,16 +494,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
       return __all_sync(0xFFFFFFFFu, ok);
     };
-    while (left > 0) {
-      int g, rt, x0, x1;
-      const int before = t1 - left;
-      if (!next_seg(g, rt, x0, x1)) continue;
+    // One unit's part in this run, its rows in RG groups.
+    auto segment = [&](auto groups, int g, int rt, int x0, int x1, int before) {
+      constexpr int RG = decltype(groups)::value;
+      constexpr int GW = kNW / RG;  // warps per row group: each takes every GW-th tile
+      constexpr int MQ = KS / GW;   // m tiles each warp finishes when the unit ends
+      const int rg = warp / GW, wi = warp % GW;  // row group, place in it
       const bool whole_l = x0 == 0, whole_r = x1 == r.nt;
-      const int row0 = rt * R + rg * GR;  // this row group's first row, and its rows: up to GR
+      const int row0 = rt * p.unit_rows + rg * GR;  // this row group's first row, and its rows: up to GR
       const int rows = min(r.n * p.group - row0, GR);
 
-      // q fragments of column g8 of every n tile: step i takes elements e0(i) .. e0(i) + 3
-      uint32_t qf[NT][KS][2];
+      // q fragments of column g8 of every n tile: step i takes elements e0(i) .. e0(i) + 3. One n
+      // tile's stay in registers; two n tiles' go to shared memory, once per row group, each row
+      // as the products take it: step i's pairs of lanes 0 .. 3, then their second pairs.
+      uint32_t qf[NT == 1 ? KS : 1][2];
+      const uint32_t q_rows = smem_u32(join) + C::template join_bytes<RG>() + rg * (GR * C::kQStride);
       float f0[NT], f1[NT];      // factor of the scores of columns 2 t4 and 2 t4 + 1
       int pos0[NT], pos1[NT];    // positions of the two rows
 #pragma unroll
@@ -512,13 +547,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           for (int i = 0; i < KS; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              qf[j][i][k] = pack_f16x2(__uint_as_float(w[i][k] << 16) * up,
-                                       __uint_as_float(w[i][k] & 0xFFFF0000u) * up);
-        } else {
+              w[i][k] = pack_f16x2(__uint_as_float(w[i][k] << 16) * up,
+                                   __uint_as_float(w[i][k] & 0xFFFF0000u) * up);
+        }
+        if constexpr (NT == 1) {
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
-            qf[j][i][0] = w[i][0];
-            qf[j][i][1] = w[i][1];
+            qf[i][0] = w[i][0];
+            qf[i][1] = w[i][1];
+          }
+        } else if (wi == 0) {
+          const uint32_t to = q_rows + (j * 8 + g8) * C::kQStride + t4 * 4;
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + i * 32), "r"(w[i][0]) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + i * 32 + 16), "r"(w[i][1]) : "memory");
           }
         }
         const int pos = r.L - r.n + tok;
@@ -527,6 +570,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         pos0[j] = __shfl_sync(0xFFFFFFFFu, pos, (2 * t4) * 4);
         pos1[j] = __shfl_sync(0xFFFFFFFFu, pos, (2 * t4 + 1) * 4);
       }
+      auto group_sync = [&]() {
+        if constexpr (GW > 1)
+          named_barrier_sync(RG + rg, GW * 32);
+        else
+          __syncwarp();
+      };
+      if constexpr (NT > 1) group_sync();  // q rows written
+      // steps i and i + 1 of n tile j: b0, b1 of each
+      auto q_frag = [&](int j, int i, uint32_t (&b)[4]) {
+        if constexpr (NT == 1) {
+          b[0] = qf[i][0];
+          b[1] = qf[i][1];
+          b[2] = qf[i + 1][0];
+          b[3] = qf[i + 1][1];
+        } else {
+          ldsm_x4(b, q_rows + (j * 8 + (lane & 7)) * C::kQStride + i * 32 + (lane >> 3) * 16);
+        }
+      };
       // every row sees keys [max_lo, min_end) (and the first sinks)
       const int min_end = r.L - r.n + (p.max_q > 1 ? row0 / p.group : 0) + 1;
       const int max_pos = r.L - r.n + (p.max_q > 1 ? (row0 + rows - 1) / p.group : 0);
@@ -544,9 +605,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           for (int k = 0; k < 4; ++k) o[j][i][k] = 0.f;
       }
 
-      for (int x = x0; x < x1; ++x, ++it) {
-        if (it % GW != wi) continue;
+      const int it0 = it;  // of the part's first tile
+      for (int x = kGroups ? x0 : x0 + ((wi - it0) & (GW - 1)); x < x1; x += kGroups ? 1 : GW) {
+        it = it0 + (x - x0);
         const int st = it % S;
+        if constexpr (kGroups) {  // another warp's tile: its slot is released by all warps
+          if (it % GW != wi) {
+            if (issued(it) && lane == 0) mbar_arrive(smem_u32(&bar_empty[st]));
+            continue;
+          }
+        }
         // A parity wait is only unambiguous against the phase in progress. The slot's previous
         // tile may be another warp's (GW need not divide S) and copies may land out of
         // order, so the tile must have been issued first: that tells that the slot's earlier
@@ -563,48 +631,69 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           // ---- S^T = K Q^T
           float s[NT][MT][4];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s[j][mt][k] = 0.f;
+          // 16-byte chunks of the rows outside: a chunk's q fragments serve all m tiles
+          constexpr int kChunks = F8 ? D / 64 : D / 32;  // chunks per lane and row
+          constexpr int kSteps = F8 ? 4 : 2;             // k steps of a chunk
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            // e4m3: chunk c of this lane's D/64; bf16: panel c / 2, chunk 2 t4 + c % 2
+            const int ch = F8 ? (D / 64) * t4 + c : (c / 2) * 8 + 2 * t4 + (c & 1);
+            uint32_t bq[NT][kSteps / 2][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) s[j][mt][k] = 0.f;
-            const int ra = mt * 16 + g8, rb = ra + 8;
-            if constexpr (F8) {
+              for (int h = 0; h < kSteps / 2; ++h) q_frag(j, c * kSteps + 2 * h, bq[j][h]);
+            // two m tiles at a time, their products in turn: a product's accumulator is ready
+            // again 2 NT products later
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c) {
-                const uint4 va = lds128(chunk_at<TK, C::kPanelBytes>(sk, ra, (D / 64) * t4 + c));
-                const uint4 vb = lds128(chunk_at<TK, C::kPanelBytes>(sk, rb, (D / 64) * t4 + c));
-                const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+            for (int m0t = 0; m0t < MT; m0t += 2) {
+              uint32_t wa[2][4], wb[2][4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t a[4] = {e4m3_lo(wa[k]), e4m3_lo(wb[k]), e4m3_hi(wa[k]),
-                                         e4m3_hi(wb[k])};
+              for (int u = 0; u < 2; ++u) {
+                const int row = (m0t + u) * 16 + g8;
+                const uint4 va = lds128(chunk_at<TK, C::kPanelBytes>(sk, row, ch));
+                const uint4 vb = lds128(chunk_at<TK, C::kPanelBytes>(sk, row + 8, ch));
+                wa[u][0] = va.x;
+                wa[u][1] = va.y;
+                wa[u][2] = va.z;
+                wa[u][3] = va.w;
+                wb[u][0] = vb.x;
+                wb[u][1] = vb.y;
+                wb[u][2] = vb.z;
+                wb[u][3] = vb.w;
+              }
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  uint32_t af[4];
+                  if constexpr (F8) {
+                    af[0] = e4m3_lo(wa[u][k]);
+                    af[1] = e4m3_lo(wb[u][k]);
+                    af[2] = e4m3_hi(wa[u][k]);
+                    af[3] = e4m3_hi(wb[u][k]);
+                  } else {
+                    af[0] = wa[u][2 * k];
+                    af[1] = wb[u][2 * k];
+                    af[2] = wa[u][2 * k + 1];
+                    af[3] = wb[u][2 * k + 1];
+                  }
 #pragma unroll
                   for (int j = 0; j < NT; ++j)
-                    mma16<F8>(s[j][mt], a, qf[j][c * 4 + k][0], qf[j][c * 4 + k][1]);
+                    mma16<F8>(s[j][m0t + u], af, bq[j][k / 2][2 * (k & 1)],
+                              bq[j][k / 2][2 * (k & 1) + 1]);
                 }
-              }
-            } else {
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {  // panel c / 2, chunk 2 t4 + c % 2
-                const int ch = (c / 2) * 8 + 2 * t4 + (c & 1);
-                const uint4 va = lds128(chunk_at<TK, C::kPanelBytes>(sk, ra, ch));
-                const uint4 vb = lds128(chunk_at<TK, C::kPanelBytes>(sk, rb, ch));
-                const uint32_t a0[4] = {va.x, vb.x, va.y, vb.y}, a1[4] = {va.z, vb.z, va.w, vb.w};
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                  mma16<F8>(s[j][mt], a0, qf[j][2 * c][0], qf[j][2 * c][1]);
-                  mma16<F8>(s[j][mt], a1, qf[j][2 * c + 1][0], qf[j][2 * c + 1][1]);
-                }
-              }
             }
           }
           // ---- scores in the exp2 domain, masks, running reference
           const bool clear = all_pieces && key0 + TK <= min_end &&
                              (p.window == 0 || key0 >= max_lo || key0 + TK <= p.sinks);
           float t0m[NT], t1m[NT];
-#pragma unroll
-          for (int j = 0; j < NT; ++j) t0m[j] = t1m[j] = -INFINITY;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             float ks = 1.f, vl = 0.f;
@@ -620,20 +709,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               v[1] = fmaf(v[1], a1, vl);
               v[2] = fmaf(v[2], a0, vl);
               v[3] = fmaf(v[3], a1, vl);
-              if (!clear) {
-                const bool here = (okp >> (mt >> piece_shift)) & 1u;
-                const int ka = key0 + mt * 16 + g8, kb = ka + 8;
-                auto sees = [&](int key, int pos) {
-                  return here && key <= pos &&
-                         (p.window == 0 || key > pos - p.window || key < p.sinks);
-                };
+            }
+          }
+          if (!clear) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const bool here = (okp >> (mt >> piece_shift)) & 1u;
+              const int ka = key0 + mt * 16 + g8, kb = ka + 8;
+              auto sees = [&](int key, int pos) {
+                return here && key <= pos &&
+                       (p.window == 0 || key > pos - p.window || key < p.sinks);
+              };
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                float(&v)[4] = s[j][mt];
                 if (!sees(ka, pos0[j])) v[0] = -INFINITY;
                 if (!sees(ka, pos1[j])) v[1] = -INFINITY;
                 if (!sees(kb, pos0[j])) v[2] = -INFINITY;
                 if (!sees(kb, pos1[j])) v[3] = -INFINITY;
               }
-              t0m[j] = fmax3(t0m[j], v[0], v[2]);
-              t1m[j] = fmax3(t1m[j], v[1], v[3]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            t0m[j] = t1m[j] = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              t0m[j] = fmax3(t0m[j], s[j][mt][0], s[j][mt][2]);
+              t1m[j] = fmax3(t1m[j], s[j][mt][1], s[j][mt][3]);
             }
           }
           bool move = false;
@@ -681,6 +784,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             __syncwarp();
           }
           // ---- P and O^T += V^T P^T
+          float e0[NT], e1[NT];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            e0[j] = m0[j] == -INFINITY ? 0.f : m0[j] - kBias;
+            e1[j] = m1[j] == -INFINITY ? 0.f : m1[j] - kBias;
+          }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             float vi = 1.f;
@@ -688,13 +797,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             uint32_t b0[NT], b1[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              const float e0 = m0[j] == -INFINITY ? 0.f : m0[j] - kBias;
-              const float e1 = m1[j] == -INFINITY ? 0.f : m1[j] - kBias;
               float pr[4];
-              pr[0] = ex2_approx(s[j][mt][0] - e0);
-              pr[1] = ex2_approx(s[j][mt][1] - e1);
-              pr[2] = ex2_approx(s[j][mt][2] - e0);
-              pr[3] = ex2_approx(s[j][mt][3] - e1);
+              pr[0] = ex2_approx(s[j][mt][0] - e0[j]);
+              pr[1] = ex2_approx(s[j][mt][1] - e1[j]);
+              pr[2] = ex2_approx(s[j][mt][2] - e0[j]);
+              pr[3] = ex2_approx(s[j][mt][3] - e1[j]);
               l0[j] = fmaf(pr[0] + pr[2], vi, l0[j]);
               l1[j] = fmaf(pr[1] + pr[3], vi, l1[j]);
               b0[j] = movm(F8 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
@@ -750,14 +857,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (lane == 0) mbar_arrive(smem_u32(&bar_empty[st]));
       }
 
+      it = it0 + (x1 - x0);
       // ---- join the row group's warps: the largest reference first, then warp wi sums m tiles
-      // [wi kMQ, (wi + 1) kMQ) of all of them
-      auto group_sync = [&]() {
-        if constexpr (GW > 1)
-          named_barrier_sync(1 + rg, GW * 32);
-        else
-          __syncwarp();
-      };
+      // [wi MQ, (wi + 1) MQ) of all of them
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -792,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
       }
       // slot of (summing warp, source warp) of the group: every source but itself
-      constexpr int kSlot = NT * C::kMQ * 4 * 32;
+      constexpr int kSlot = NT * MQ * 4 * 32;
       float* const group_join = join + rg * (GW * (GW - 1) * kSlot) + lane;
 #pragma unroll
       for (int dst = 0; dst < GW; ++dst) {
@@ -801,33 +903,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int i = 0; i < C::kMQ; ++i)
+          for (int i = 0; i < MQ; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              to[((j * C::kMQ + i) * 4 + k) * 32] = o[j][dst * C::kMQ + i][k];
+              to[((j * MQ + i) * 4 + k) * 32] = o[j][dst * MQ + i][k];
       }
       group_sync();
       const bool final = whole_l && whole_r;
-      float* part = p.parts + (size_t)(2 * blockIdx.x + (whole_l ? 1 : 0)) * (R * (D + 2));
+      float* part = p.parts + (size_t)(2 * blockIdx.x + (whole_l ? 1 : 0)) * (p.unit_rows * (D + 2));
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        float acc[C::kMQ][4];
+        float acc[MQ][4];
 #pragma unroll
         for (int d = 0; d < GW; ++d)
           if (d == wi) {
 #pragma unroll
-            for (int i = 0; i < C::kMQ; ++i)
+            for (int i = 0; i < MQ; ++i)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) acc[i][k] = o[j][d * C::kMQ + i][k];
+              for (int k = 0; k < 4; ++k) acc[i][k] = o[j][d * MQ + i][k];
           }
         // ((own + first) + second) + third other: the same order every time
 #pragma unroll
         for (int w = 0; w < GW - 1; ++w) {
           const float* from = group_join + (wi * (GW - 1) + w) * kSlot;
 #pragma unroll
-          for (int i = 0; i < C::kMQ; ++i)
+          for (int i = 0; i < MQ; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[i][k] += from[((j * C::kMQ + i) * 4 + k) * 32];
+            for (int k = 0; k < 4; ++k) acc[i][k] += from[((j * MQ + i) * 4 + k) * 32];
         }
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -841,9 +943,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           const int row = j * 8 + 2 * t4 + k;
           const float l = k ? sum.y : sum.x, top = k ? top1[j] : top0[j];
           const float inv = !final ? 1.f : l > 0.f ? 1.f / l : 0.f;
-          float v[2 * C::kMQ];
+          float v[2 * MQ];
 #pragma unroll
-          for (int i = 0; i < C::kMQ; ++i) {
+          for (int i = 0; i < MQ; ++i) {
             v[2 * i] = acc[i][k] * inv;
             v[2 * i + 1] = acc[i][k + 2] * inv;
           }
@@ -856,11 +958,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           float* to32 = final ? static_cast<float*>(p.out) + at * D : part + (rg * GR + row) * D;
           uint16_t* to16 = static_cast<uint16_t*>(p.out) + at * D;
           const bool half = final && p.out_bf16;
-          if constexpr (F8) {  // elements d0 .. d0 + 2 kMQ - 1 of the row
-            const int d0 = (D / 8) * g8 + 2 * C::kMQ * wi;
-            if constexpr (C::kMQ >= 2) {
+          if constexpr (F8) {  // elements d0 .. d0 + 2 MQ - 1 of the row
+            const int d0 = (D / 8) * g8 + 2 * MQ * wi;
+            if constexpr (MQ >= 2) {
 #pragma unroll
-              for (int i = 0; i < 2 * C::kMQ; i += 4) {
+              for (int i = 0; i < 2 * MQ; i += 4) {
                 if (half)
                   *reinterpret_cast<uint2*>(to16 + d0 + i) =
                       make_uint2(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]));
@@ -876,8 +978,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
           } else {  // elements 16 m + g8 and 16 m + g8 + 8 of m tile m
 #pragma unroll
-            for (int i = 0; i < 2 * C::kMQ; ++i) {
-              const int d = 16 * (wi * C::kMQ + i / 2) + g8 + 8 * (i & 1);
+            for (int i = 0; i < 2 * MQ; ++i) {
+              const int d = 16 * (wi * MQ + i / 2) + g8 + 8 * (i & 1);
               if (half)
                 to16[d] = (uint16_t)pack_bf16x2(v[i], 0.f);
               else
@@ -889,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               if (p.lse != nullptr)
                 p.lse[at] = l > 0.f ? (top - kBias + log2f(l)) * kLn2 : -INFINITY;
             } else {
-              *reinterpret_cast<float2*>(part + R * D + 2 * (rg * GR + row)) = make_float2(top, l);
+              *reinterpret_cast<float2*>(part + p.unit_rows * D + 2 * (rg * GR + row)) = make_float2(top, l);
             }
           }
         }
@@ -901,10 +1003,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int c0 = begin < longer
                            ? (int)((unsigned)begin / (unsigned)(len + 1))
                            : more + (int)((unsigned)(begin - longer) / (unsigned)len);
-        p.jobs[blockIdx.x] = make_int4(c0, min(r.n * p.group - rt * R, R), rt * R, g);
+        p.jobs[blockIdx.x] = make_int4(c0, min(r.n * p.group - rt * p.unit_rows, p.unit_rows),
+                                        rt * p.unit_rows, g);
         p.job_q0[blockIdx.x] = r.q0;
       }
       group_sync();  // before the next unit's references and sums
+    };
+    while (left > 0) {
+      int g, rt, x0, x1;
+      const int before = t1 - left;
+      if (!next_seg(g, rt, x0, x1)) continue;
+      const int rows = kGroups ? min(r.n * p.group - rt * p.unit_rows, p.unit_rows) : 0;
+      if (rows > 2 * GR)
+        segment(std::integral_constant<int, kGroups ? 4 : 1>(), g, rt, x0, x1, before);
+      else if (rows > GR)
+        segment(std::integral_constant<int, kGroups ? 2 : 1>(), g, rt, x0, x1, before);
+      else
+        segment(std::integral_constant<int, 1>(), g, rt, x0, x1, before);
     }
   }
 }
@@ -913,8 +1028,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 // ended in CTA c. Four warps take every fourth part each, kBatch parts' loads in flight (a unit
 // of one long request may have hundreds), then the warps' results are joined in order.
 template <int D>
-__global__ void __launch_bounds__(128) attn_decode_join_kernel(const Params p, int R, float bias) {
+__global__ void __launch_bounds__(128) attn_decode_join_kernel(const Params p, float bias) {
   constexpr int kWarps = 4, kBatch = 4;
+  const int R = p.unit_rows;
   __shared__ float2 s_ml[kWarps];
   __shared__ float4 s_acc[kWarps][D / 4];
   const int c1 = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1003,9 +1119,9 @@ size_t job_bytes(size_t ctas) {
   return (ctas * (sizeof(int4) + sizeof(int)) + 255) / 256 * 256;
 }
 
-template <bool F8, int D, int NT, int RG>
+template <bool F8, int D, int NT, bool kGroups>
 cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t stream) {
-  using C = Cfg<F8, D, NT, RG>;
+  using C = Cfg<F8, D, NT>;
   Params p;
   p.q = static_cast<const uint16_t*>(a.q);
   p.cu_q = a.cu_q;
@@ -1033,6 +1149,9 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   p.scale_log2 = a.scale * kLog2e;
   p.out_bf16 = a.out_bf16 ? 1 : 0;
   p.ctas = kCtasPerSm * sms;
+  p.unit_rows = rows_of(a.max_q, p.group);
+  p.row_shift = 0;
+  while ((1 << p.row_shift) < p.unit_rows) ++p.row_shift;
   p.jobs = static_cast<int4*>(a.workspace);
   p.job_q0 = reinterpret_cast<int*>(p.jobs + p.ctas);
   p.parts =
@@ -1051,23 +1170,22 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   };
   if (!make(&mk, const_cast<void*>(a.k_cache)) || !make(&mv, const_cast<void*>(a.v_cache)))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<F8, D, NT, RG>,
+  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<F8, D, NT, kGroups>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  attn_decode_kernel<F8, D, NT, RG><<<p.ctas, kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
+  attn_decode_kernel<F8, D, NT, kGroups><<<p.ctas, kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_decode_join_kernel<D><<<dim3(p.ctas, C::kR), 128, 0, stream>>>(p, C::kR, F8 ? 11.f : 0.f);
+  attn_decode_join_kernel<D><<<dim3(p.ctas, p.unit_rows), 128, 0, stream>>>(p, F8 ? 11.f : 0.f);
   return cudaGetLastError();
 }
 
 template <bool F8, int D>
 cudaError_t launch_nt(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t stream) {
   switch (rows_of(a.max_q, a.hq / a.hkv)) {
-    case 8: return launch<F8, D, 1, 1>(a, sms, drv_err, stream);
-    case 16: return launch<F8, D, 2, 1>(a, sms, drv_err, stream);
-    case 32: return launch<F8, D, 2, 2>(a, sms, drv_err, stream);
-    default: return launch<F8, D, 2, 4>(a, sms, drv_err, stream);
+    case 8: return launch<F8, D, 1, false>(a, sms, drv_err, stream);
+    case 16: return launch<F8, D, 2, false>(a, sms, drv_err, stream);
+    default: return launch<F8, D, 2, true>(a, sms, drv_err, stream);
   }
 }
 
