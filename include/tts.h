@@ -428,6 +428,8 @@ tts_status tts_rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads
  * bf16), accumulated in fp32. Cached values that some new token of the request sees must be
  * finite; what the page holds behind the last token or outside the window is never used,
  * and pages without a visible key are not read (their table entries may be anything).
+ * The value scales of a request's visible pages lie within 2^100 of one another (a weight is
+ * held times its page's value scale in fp32).
  *
  * q           device bf16 [total_q, num_heads_q, head_dim]; rows outside every request are
  *             not read, and their out / lse rows are left as they were

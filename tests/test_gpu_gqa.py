@@ -470,3 +470,181 @@ def test_serving_loop(tts, f8):
             tables.numpy(), past, cu, d ** -0.5, window, sinks, F16_HALF if f8 else BF16_HALF)
         assert np.all(np.abs(out.cpu().numpy() - ro) <= tol), step
         assert np.all(np.abs(lse.cpu().numpy() - rl) <= tol_l), step
+
+
+# ------------------------------------------------------------------------------- as used
+def test_append_many_requests(tts):
+    """More requests than one round of bounds finds, prompts and steps, empty ones among them."""
+    r = np.random.default_rng(5)
+    for hi, ps, d in ((30, 16, 64), (2, 64, 128)):
+        new = [int(x) for x in r.integers(0, hi, 75)]
+        past = [int(x) for x in r.integers(0, 70, 75)]
+        new[-1] = hi - 1
+        c, q_out, k_out, (qr, kr, kc, vc, ks, vs), n = run_append(tts, 81, new, past, 4, 2, d, ps, True)
+        assert torch.equal(q_out.cpu(), torch.tensor(qr).to(torch.bfloat16))
+        assert torch.equal(k_out.cpu(), torch.tensor(kr).to(torch.bfloat16))
+        np.testing.assert_array_equal(c[1].cpu().numpy(), ks.astype(np.float32))
+        np.testing.assert_array_equal(ref.codes_of(c[0]), kc)
+        np.testing.assert_array_equal(ref.codes_of(c[2]), vc)
+
+
+@pytest.mark.parametrize("f8", [True, False])
+def test_cache_beyond_32_bits(tts, f8):
+    """The last pages of a cache whose offsets pass 2^31 values and 2^32 bytes."""
+    hkv, ps, d = 4, 128, 128
+    pages = (5 << 30 if f8 else 5 << 29) // (hkv * ps * d) + 1
+    kc, vc = (torch.empty(pages, hkv, ps, d, dtype=torch.uint8 if f8 else torch.bfloat16,
+                          device="cuda") for _ in range(2))
+    ks, vs = ((torch.ones(pages, hkv, device="cuda") for _ in range(2)) if f8 else (None, None))
+    assert kc.numel() > 2 ** 31 and kc.nbytes > 2 ** 32
+    n = 200
+    tables = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32)
+    x = torch.randn(n, 4 + 2 * hkv, d, generator=gen(90)).to(torch.bfloat16)
+    D = dev(x)
+    q, _ = tts.rope_kv_append(D[:, 4:4 + hkv], D[:, 4 + hkv:], kc, vc, dev(tables),
+                              torch.zeros(1, dtype=torch.int32, device="cuda"),
+                              torch.tensor([0, n], dtype=torch.int32, device="cuda"), n, k_scale=ks,
+                              v_scale=vs, q=D[:, :4].contiguous())
+    last = [t[-2:] if t is not None else None for t in (kc, vc, ks, vs)]
+    want = ref.append(None, x[:, 4:4 + hkv].float().numpy(), x[:, 4 + hkv:].float().numpy(),
+                      np.zeros((2, hkv, ps, d)), np.zeros((2, hkv, ps, d)),
+                      np.ones((2, hkv)) if f8 else None, np.ones((2, hkv)) if f8 else None,
+                      np.array([[1, 0]]), [0], cum([n]), None, ps)
+    got = ref.codes_of(last[0])
+    np.testing.assert_array_equal(got[1], want[2][1])
+    np.testing.assert_array_equal(got[0][:, :n - ps], want[2][0][:, :n - ps])
+    out, lse = tts.attn_decode_paged(q[-1:].contiguous(), kc, vc, dev(tables),
+                                     torch.tensor([n], dtype=torch.int32, device="cuda"), d ** -0.5,
+                                     k_scale=ks, v_scale=vs)
+    ro, rl, tol, tol_l = ref.attend(
+        q[-1:].float().cpu().numpy(), got, ref.codes_of(last[1]),
+        None if ks is None else last[2].cpu().numpy(), None if vs is None else last[3].cpu().numpy(),
+        np.array([[1, 0]]), [n], cum([1]), d ** -0.5, 0, 0, F16_HALF if f8 else BF16_HALF)
+    assert np.all(np.abs(out.cpu().numpy() - ro) <= tol)
+    assert np.all(np.abs(lse.cpu().numpy() - rl) <= tol_l)
+
+
+def test_step_in_a_graph(tts):
+    """Append and decode captured once, replayed as the lengths grow and on two graphs that share
+    the workspace: the same bits as the same calls made one by one."""
+    hq, hkv, d, ps, nreq = 8, 2, 128, 16, 3
+    tables, pages = make_tables(95, [100] * nreq, ps)
+    pool = make_pool(96, pages, hkv, ps, d, True)
+    cs = tts.rope_cache(100, d)
+    T = dev(tables)
+    cu = torch.arange(nreq + 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(tts.attn_decode_workspace_bytes(1, hq, hkv, d), dtype=torch.uint8, device="cuda")
+    steps = [dev(torch.randn(nreq, hq + 2 * hkv, d, generator=gen(97 + i)).to(torch.bfloat16))
+             for i in range(6)]
+
+    def state():
+        return dict(c=[dev(t).clone() for t in pool], qkv=steps[0].clone(),
+                    past=torch.tensor([5, 31, 60], dtype=torch.int32, device="cuda"),
+                    lens=torch.tensor([6, 32, 61], dtype=torch.int32, device="cuda"),
+                    q=torch.empty(nreq, hq, d, dtype=torch.bfloat16, device="cuda"),
+                    out=torch.empty(nreq, hq, d, device="cuda"),
+                    lse=torch.empty(nreq, hq, device="cuda"))
+
+    def step(s):
+        kc, ks, vc, vs = s["c"]
+        x = s["qkv"]
+        tts.rope_kv_append(x[:, hq:hq + hkv], x[:, hq + hkv:], kc, vc, T, s["past"], cu, 1, k_scale=ks,
+                           v_scale=vs, cos_sin=cs, q=x[:, :hq], q_out=s["q"])
+        tts.attn_decode_paged(s["q"], kc, vc, T, s["lens"], d ** -0.5, k_scale=ks, v_scale=vs,
+                              window=40, sinks=2, out=s["out"], lse=s["lse"], workspace=ws)
+        s["past"].add_(1)
+        s["lens"].add_(1)
+
+    plain, want = state(), []
+    for x in steps:
+        plain["qkv"].copy_(x)
+        step(plain)
+        want.append((plain["out"].clone(), plain["lse"].clone()))
+    step(state())  # what a first call sets up is not captured
+    torch.cuda.synchronize()
+    held = [state(), state()]
+    graphs = []
+    for s in held:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(s)
+        graphs.append(g)
+    for i, x in enumerate(steps):
+        for s, g in zip(held, graphs):
+            s["qkv"].copy_(x)
+            g.replay()
+        for s in held:
+            assert torch.equal(s["out"], want[i][0]) and torch.equal(s["lse"], want[i][1]), i
+    for s in held:
+        assert all(torch.equal(a, b) for a, b in zip(s["c"], plain["c"]))
+
+
+def test_calls_on_two_streams(tts):
+    """Two decode calls in flight at once, each with a workspace of its own."""
+    d, ps, hkv, kv = 128, 64, 2, [9000, 500]
+    tables, pages = make_tables(110, kv, ps)
+    kc, ks, vc, vs = [dev(t) for t in make_pool(111, pages, hkv, ps, d, True)]
+    T, L = dev(tables), dev(torch.tensor(kv, dtype=torch.int32))
+    qs = [dev(torch.randn(2, 8, d, generator=gen(112 + i)).to(torch.bfloat16)) for i in range(2)]
+    need = tts.attn_decode_workspace_bytes(1, 8, hkv, d)
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    call = lambda i: tts.attn_decode_paged(qs[i], kc, vc, T, L, d ** -0.5, k_scale=ks, v_scale=vs,  # noqa: E731
+                                           workspace=ws[i])
+    want = [tuple(t.clone() for t in call(i)) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(call(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, l in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+
+
+def test_workspace_is_found_or_made(tts):
+    """Without a workspace, and with one that is too small, the binding makes one."""
+    tables, pages = make_tables(120, [300], 64)
+    kc, ks, vc, vs = [dev(t) for t in make_pool(121, pages, 2, 64, 128, True)]
+    q = dev(torch.randn(1, 4, 128, generator=gen(122)).to(torch.bfloat16))
+    L = torch.tensor([300], dtype=torch.int32, device="cuda")
+    a = tts.attn_decode_paged(q, kc, vc, dev(tables), L, 0.1, k_scale=ks, v_scale=vs)
+    b = tts.attn_decode_paged(q, kc, vc, dev(tables), L, 0.1, k_scale=ks, v_scale=vs,
+                              workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_binding_refuses_tensors_that_do_not_fit(tts):
+    tables, pages = make_tables(130, [100], 64)
+    kc, ks, vc, vs = [dev(t) for t in make_pool(131, pages, 2, 64, 128, True)]
+    T, L = dev(tables), torch.tensor([100], dtype=torch.int32, device="cuda")
+    q = dev(torch.randn(1, 4, 128, generator=gen(132)).to(torch.bfloat16))
+    good = dict(q=q, k_cache=kc, v_cache=vc, page_tables=T, kv_lens=L, scale=0.1, k_scale=ks,
+                v_scale=vs)
+    tts.attn_decode_paged(**good)
+    for bad in (dict(q=q.float()), dict(q=q.cpu()), dict(q=q[:, :, :64]), dict(k_cache=kc[:-1]),
+                dict(k_cache=kc.view(torch.int8)), dict(k_scale=None), dict(v_scale=vs[:, :1]),
+                dict(page_tables=T.long()), dict(page_tables=T[0]), dict(kv_lens=L.cpu()),
+                dict(kv_lens=torch.cat([L, L])), dict(cu_seqlens_q=L), dict(out=q.half()),
+                dict(out=torch.empty(2, 4, 128, device="cuda")), dict(lse=torch.empty(4, device="cuda")),
+                dict(v_cache=vc.transpose(1, 2)), dict(status=torch.zeros(1, device="cuda"))):
+        with pytest.raises(ValueError):
+            tts.attn_decode_paged(**{**good, **bad})
+    for bad in (dict(scale=0.0), dict(window=-1), dict(max_seqlen_q=65)):
+        with pytest.raises(tts.TTSError):
+            tts.attn_decode_paged(**{**good, **bad})
+    k = dev(torch.randn(3, 2, 128, generator=gen(133)).to(torch.bfloat16))
+    cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    good = dict(k=k, v=k, k_cache=kc, v_cache=vc, page_tables=T, past_lens=L, cu_new=cu, max_new=3,
+                k_scale=ks, v_scale=vs)
+    tts.rope_kv_append(**good)
+    for bad in (dict(k=k.float()), dict(v=k[:2]), dict(k=k[:, :1]), dict(k=k.transpose(0, 1)),
+                dict(q=k[:2]), dict(q_out=k), dict(k_out=k[:2]), dict(cu_new=cu.long()),
+                dict(cu_new=cu[:1]), dict(cos_sin=torch.zeros(9, 32, 2, device="cuda")),
+                dict(past_lens=L.cpu()), dict(v_scale=None)):
+        with pytest.raises(ValueError):
+            tts.rope_kv_append(**{**good, **bad})
+    with pytest.raises(tts.TTSError):
+        tts.rope_kv_append(**{**good, "max_new": -1})

@@ -68,7 +68,8 @@ def test_decode_refusals(L):
                dict(scale=0.0), dict(scale=float("inf")), dict(dt=1), dict(odt=2),
                dict(cu=NUL, total=1)):
         assert decode(L, **kw) == tts.TTS_ERR_INVALID_ARG, kw
-    for kw in (dict(d=80), dict(ps=24), dict(max_q=65), dict(max_pages=1 << 25)):
+    for kw in (dict(d=80), dict(ps=24), dict(max_q=65), dict(max_pages=1 << 25),
+               dict(batch=1 << 12, max_pages=1 << 23)):  # more tiles than 32 bits count
         assert decode(L, **kw) == tts.TTS_ERR_UNSUPPORTED, kw
     assert decode(L, ws=NUL) == tts.TTS_ERR_WORKSPACE
     assert decode(L, ws=B) == tts.TTS_ERR_WORKSPACE
