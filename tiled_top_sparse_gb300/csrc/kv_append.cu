@@ -325,13 +325,15 @@ __device__ __forceinline__ void rotate_q_row(const KvAppendArgs& p, bool ok, int
 constexpr int kQHeads = 8;  // q heads that share one load of the table row
 
 // Prompts: a block per (page, head) of k and of v, then a block per (token tile, 8 q heads).
-// (Two passes: five blocks per SM instead of the four that 64 registers allow, 158 -> 155 us.)
-template <int D, bool kF8, int kPasses>
-__global__ void __launch_bounds__(256, kPasses == 2 ? 5 : 1) append_pages_kernel(const KvAppendArgs p,
+// Registers are held to 48 (64 for the pages of 2048 pieces), for five (two) blocks per SM: what
+// bounds the kernel is how many rows are on their way (28,000 tokens in pages of 128: 75 -> 55 us,
+// of 16 to 32: 58 -> 53 us; pages of 64 in blocks of 512 threads instead of 256: 50 -> 64 us).
+template <int D, bool kF8, int kPasses, int kMost>
+__global__ void __launch_bounds__(kMost, kMost == 256 ? 5 : 2) append_pages_kernel(const KvAppendArgs p,
                                                            int64_t kv_blocks, int q_shift,
                                                            int q_groups) {
   constexpr int kTpr = D / 16;
-  __shared__ float s_red[8];
+  __shared__ float s_red[16];
   if (blockIdx.x == 0) report(p);
   int64_t first;
   if ((int64_t)blockIdx.x < kv_blocks) {
@@ -414,7 +416,8 @@ cudaError_t launch_append(const KvAppendArgs& p, cudaStream_t stream) {
     return cudaGetLastError();
   }
   const int need = kTpr << p.page_shift;  // threads that hold a page in one pass
-  const int threads = need < 256 ? need : 256, passes = need / threads;
+  const int most = need <= 512 ? 256 : 512;
+  const int threads = need < most ? need : most, passes = need / threads;
   const int q_shift = log2_of(threads / kTpr);
   const int64_t kv_blocks = ((p.total_new >> p.page_shift) + 2 * (int64_t)p.batch) * 2 * p.hkv;
   const int q_groups = (p.hq + kQHeads - 1) / kQHeads;
@@ -423,13 +426,13 @@ cudaError_t launch_append(const KvAppendArgs& p, cudaStream_t stream) {
   if (kv_blocks + q_blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(kv_blocks + q_blocks);
   if (passes == 1)
-    append_pages_kernel<D, kF8, 1>
+    append_pages_kernel<D, kF8, 1, 256>
         <<<grid, threads, 0, stream>>>(p, kv_blocks, q_shift, q_groups);
-  else if (passes == 2)
-    append_pages_kernel<D, kF8, 2>
+  else if (most == 256)
+    append_pages_kernel<D, kF8, 2, 256>
         <<<grid, threads, 0, stream>>>(p, kv_blocks, q_shift, q_groups);
   else
-    append_pages_kernel<D, kF8, 4>
+    append_pages_kernel<D, kF8, 2, 512>
         <<<grid, threads, 0, stream>>>(p, kv_blocks, q_shift, q_groups);
   return cudaGetLastError();
 }
