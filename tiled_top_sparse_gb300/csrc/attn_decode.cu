@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   volatile int* abort_flag = &s_abort;
   volatile int* issued_tiles = &s_issued;
 
+  wait_for_prior_grids();
   // ---- this CTA's run [t0, t1) of the list of tiles, and the request it begins in
   uint32_t bad = 0;
   if (tid == 0) {
@@ -1034,6 +1035,7 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const Params p, f
   __shared__ float2 s_ml[kWarps];
   __shared__ float4 s_acc[kWarps][D / 4];
   const int c1 = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_prior_grids();  // the parts are written
   const int4 job = p.jobs[c1];
   const int q0 = p.job_q0[c1];
   if (job.x < 0 || row >= job.y) return;
@@ -1173,11 +1175,11 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<F8, D, NT, kGroups>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  attn_decode_kernel<F8, D, NT, kGroups><<<p.ctas, kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
-  e = cudaGetLastError();
+  e = launch_ahead(attn_decode_kernel<F8, D, NT, kGroups>, dim3(p.ctas), kThreads, C::kSmemBytes,
+                   stream, mk, mv, p);
   if (e != cudaSuccess) return e;
-  attn_decode_join_kernel<D><<<dim3(p.ctas, p.unit_rows), 128, 0, stream>>>(p, F8 ? 11.f : 0.f);
-  return cudaGetLastError();
+  return launch_ahead(attn_decode_join_kernel<D>, dim3(p.ctas, p.unit_rows), 128, 0, stream, p,
+                      F8 ? 11.f : 0.f);
 }
 
 template <bool F8, int D>

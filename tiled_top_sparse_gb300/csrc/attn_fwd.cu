@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
   volatile int* item_slot = s_item;
+  if constexpr (kWin) wait_for_prior_grids();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -979,6 +980,11 @@ cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
   } else {
     e = cudaMemsetAsync(a.work_counter, 0, sizeof(uint32_t), stream);
     if (e != cudaSuccess) return e;
+  }
+  if constexpr (kWin) {
+    if (p.work_counter == nullptr)  // else the kernel follows the counter's memset, not a kernel
+      return launch_ahead(attn_fwd_kernel<D, F8, kWin>, dim3(grid), kAttnThreads, C::kSmemBytes,
+                          stream, maps, p);
   }
   attn_fwd_kernel<D, F8, kWin><<<grid, kAttnThreads, C::kSmemBytes, stream>>>(maps, p);
   return cudaGetLastError();

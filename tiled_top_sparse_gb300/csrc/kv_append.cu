@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 5 : 2) append_pages_kern
                                                            int q_groups) {
   constexpr int kTpr = D / 16;
   __shared__ float s_red[16];
+  wait_for_prior_grids();
   if (blockIdx.x == 0) report(p);
   int64_t first;
   if ((int64_t)blockIdx.x < kv_blocks) {
@@ -367,6 +368,7 @@ template <int D, bool kF8>
 __global__ void __launch_bounds__(128) append_steps_kernel(const KvAppendArgs p, int pages_per,
                                                            int64_t kv_warps) {
   constexpr int kTpr = D / 16;
+  wait_for_prior_grids();
   if (blockIdx.x == 0) report(p);
   const int lane = threadIdx.x & 31;
   const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -412,8 +414,8 @@ cudaError_t launch_append(const KvAppendArgs& p, cudaStream_t stream) {
     const int64_t warps = kv_warps + (q_rows + kRowsPerWarp - 1) / kRowsPerWarp;
     const int64_t blocks = (warps + 3) / 4;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    append_steps_kernel<D, kF8><<<(unsigned)blocks, 128, 0, stream>>>(p, pages_per, kv_warps);
-    return cudaGetLastError();
+    return launch_ahead(append_steps_kernel<D, kF8>, dim3((unsigned)blocks), 128, 0, stream, p,
+                        pages_per, kv_warps);
   }
   const int need = kTpr << p.page_shift;  // threads that hold a page in one pass
   const int most = need <= 512 ? 256 : 512;
@@ -425,16 +427,10 @@ cudaError_t launch_append(const KvAppendArgs& p, cudaStream_t stream) {
       p.q != nullptr ? ((p.total_new >> q_shift) + 2 * (int64_t)p.batch) * q_groups : 0;
   if (kv_blocks + q_blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(kv_blocks + q_blocks);
-  if (passes == 1)
-    append_pages_kernel<D, kF8, 1, 256>
-        <<<grid, threads, 0, stream>>>(p, kv_blocks, q_shift, q_groups);
-  else if (most == 256)
-    append_pages_kernel<D, kF8, 2, 256>
-        <<<grid, threads, 0, stream>>>(p, kv_blocks, q_shift, q_groups);
-  else
-    append_pages_kernel<D, kF8, 2, 512>
-        <<<grid, threads, 0, stream>>>(p, kv_blocks, q_shift, q_groups);
-  return cudaGetLastError();
+  auto kernel = passes == 1   ? append_pages_kernel<D, kF8, 1, 256>
+                : most == 256 ? append_pages_kernel<D, kF8, 2, 256>
+                              : append_pages_kernel<D, kF8, 2, 512>;
+  return launch_ahead(kernel, dim3(grid), threads, 0, stream, p, kv_blocks, q_shift, q_groups);
 }
 
 }  // namespace
