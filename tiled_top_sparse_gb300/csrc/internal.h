@@ -7,29 +7,6 @@
 
 namespace tts {
 
-// Launches a kernel that begins with wait_for_prior_grids(): the launch may be set up while the
-// stream's previous kernel still runs, which takes about 2 us off a short kernel behind another.
-// Under stream capture the launch is a plain one (a graph's launches are set up already, and
-// its edges stay full dependencies).
-template <typename... P, typename... A>
-cudaError_t launch_ahead(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
-                         cudaStream_t stream, A... args) {
-  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  cudaError_t e = cudaStreamIsCapturing(stream, &capture);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &at;
-  cfg.numAttrs = capture == cudaStreamCaptureStatusNone ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-}
-
 // ---- top-k
 size_t topk_smem_bytes(int64_t row_stride, int k);
 cudaError_t launch_topk_select(const float* logits, int64_t row_stride, int32_t rows,

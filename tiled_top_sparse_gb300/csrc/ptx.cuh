@@ -117,13 +117,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// ---------------------------------------------------------------- dependent launch
-// Waits until the grids this one may have been launched ahead of are complete and their writes
-// visible (launch_ahead in internal.h); returns at once for a plain launch.
-__device__ __forceinline__ void wait_for_prior_grids() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // ---------------------------------------------------------------- fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
