@@ -21,19 +21,20 @@
 // the 16 rows and q rows as the 8 columns: a group of 4 to 8 heads fills the columns, where a
 // 128-row tcgen05 tile would be 3 to 6 % used and would need the codes widened in shared
 // memory; at HBM's rate an SM can issue about 2800 instructions per 16 KB tile, of which one n
-// tile takes a third (issue slots 29 % used, tensor pipe 18 %). e4m3 codes become fp16 (exactly) in registers; q is fp16
-// after a power-of-two scaling of its row (exact for every element within 2^-22 of the row's
-// largest), and P is fp16 with its reference kept so that 2^-25 of the maximum still has all
-// 11 bits. bf16 caches use bf16 products throughout. Sums and softmax statistics are fp32.
+// tile takes a third (issue slots 29 % used, tensor pipe 18 %). e4m3 codes become fp16
+// (exactly) in registers; q is fp16 after a power-of-two scaling of its row (exact for every
+// element within 2^-22 of the row's largest), and P is fp16 with its reference kept so that
+// 2^-25 of the maximum still has all 11 bits. bf16 caches use bf16 products throughout. Sums
+// and softmax statistics are fp32.
 //
 // Measured (32 / 8 heads of 128, CUDA graph): 64 requests x 32768 tokens in e4m3 616 to 632 us
 // from box to box (6.8 to 7.0 TB/s, 1.00 to 1.03 of the measured copy rate), one request of
 // 2590 tokens 8.9 us (the chain of launch, lengths, page table, tile, products and the parts'
 // launch; its bytes are 0.8 us), 33 ragged requests with a window of 4096 53.6 us (39.4 us of
 // bytes; about 2.5 us before the first tile, 3 for the parts, and the last CTAs), 1 to 4 tokens
-// of 16 requests over a bf16 cache 67 us (52.7). Many rows are bound by what each warp issues:
-// 16, 32 and 64 rows per KV head take 1.7, 2.5 and 4.0 times the bytes' time in e4m3 and 1.1,
-// 1.3 and 2.1 in bf16 (16 requests x 20000 tokens, 4 KV heads).
+// of 16 requests over a bf16 cache 65.5 us (52.7). Many rows are bound by what each warp issues:
+// 16, 32 and 64 rows per KV head take 1.6, 2.2 and 3.8 times the bytes' time in e4m3 and 1.1,
+// 1.3 and 2.0 in bf16 (16 requests x 20000 tokens, 4 KV heads).
 #include <cstdint>
 #include <type_traits>
 
@@ -69,6 +70,10 @@ struct Cfg {
   // tiles (64-wide e4m3 rows, 20,000 keys: 8 KB tiles 46.5 us, 16 KB tiles 36.7 us).
   static constexpr int kTK = kRowBytes == 256 ? 32 : kRowBytes == 64 && NT == 1 ? 128 : 64;
   static constexpr int kMT = kTK / 16;
+  // m tiles whose scores are in registers together: with two n tiles two, in passes over the
+  // tile. Shared memory leaves little of L1, so every register spilled is read from L2 (16 q
+  // rows, 16 x 20,000 keys of e4m3: 85 us with four m tiles, 77 with two and the room below).
+  static constexpr int kPass = NT == 2 ? 2 : kMT;
   static constexpr int kKBytes = kTK * kRowBytes;  // K (or V) of one tile
   static constexpr int kStageBytes = 2 * kKBytes;
   static constexpr int kGR = 8 * NT;       // q rows per row group
@@ -90,7 +95,9 @@ struct Cfg {
                             : (room<2>() > room<4>() ? room<2>() : room<4>());
   // Two CTAs per SM: 113 KB each, less 1 KB to align the ring and 1 KB of barriers.
   static constexpr int kStagesFit = (113 * 1024 - 2048 - kJoinBytes) / kStageBytes;
-  static constexpr int kStages = kStagesFit < 12 ? kStagesFit : 12;
+  // Two n tiles leave 16 KB to L1: their spilled registers are read from it.
+  static constexpr int kStages =
+      (kStagesFit < 12 ? kStagesFit : 12) - (NT == 2 ? 16384 / kStageBytes : 0);
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kJoinBytes;
 };
 
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const Params p) {
   using C = Cfg<F8, D, NT>;
-  constexpr int TK = C::kTK, MT = C::kMT, S = C::kStages, KS = C::kKS, GR = C::kGR;
+  constexpr int TK = C::kTK, MT = C::kPass, S = C::kStages, KS = C::kKS, GR = C::kGR;
   // Releases of a ring slot: the one warp that worked on it, or with row groups every warp.
   constexpr int kReleases = kGroups ? kNW : 1;
   extern __shared__ uint8_t smem_raw[];
@@ -513,14 +520,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       constexpr int MQ = KS / GW;   // m tiles each warp finishes when the unit ends
       const int rg = warp / GW, wi = warp % GW;  // row group, place in it
       const bool whole_l = x0 == 0, whole_r = x1 == r.nt;
-      const int row0 = rt * p.unit_rows + rg * GR;  // this row group's first row, and its rows: up to GR
+      // this row group's first row, and its rows: up to GR
+      const int row0 = rt * p.unit_rows + rg * GR;
       const int rows = min(r.n * p.group - row0, GR);
 
       // q fragments of column g8 of every n tile: step i takes elements e0(i) .. e0(i) + 3. One n
       // tile's stay in registers; two n tiles' go to shared memory, once per row group, each row
       // as the products take it: step i's pairs of lanes 0 .. 3, then their second pairs.
-      uint32_t qf[NT == 1 ? KS : 1][2];
-      const uint32_t q_rows = smem_u32(join) + C::template join_bytes<RG>() + rg * (GR * C::kQStride);
+      [[maybe_unused]] uint32_t qf[NT == 1 ? KS : 1][2];
+      const uint32_t q_rows =
+          smem_u32(join) + C::template join_bytes<RG>() + rg * (GR * C::kQStride);
       float f0[NT], f1[NT];      // factor of the scores of columns 2 t4 and 2 t4 + 1
       int pos0[NT], pos1[NT];    // positions of the two rows
 #pragma unroll
@@ -634,155 +643,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (!issued(it) ||
             !warp_wait(smem_u32(&bar_full[st]), (it / S) & 1, abort_flag, p.dev_status))
           continue;  // the run is lost; the barriers below still need every warp
-        const int key0 = (x < r.st ? x : r.lt + x - r.st) * TK;
+        const int tile0 = (x < r.st ? x : r.lt + x - r.st) * TK;
         const uint32_t sk = ring + st * C::kStageBytes, sv = sk + C::kKBytes;
         const uint32_t okp = s_meta[st].ok;
         const bool all_pieces = okp == (1u << n_pieces) - 1u;
         // rows of the tile that some new token sees all lie in pieces that are there
         if (okp != 0 && rows > 0) {
-          // ---- S^T = K Q^T
-          float s[NT][MT][4];
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) s[j][mt][k] = 0.f;
-          // 16-byte chunks of the rows outside: a chunk's q fragments serve all m tiles
-          constexpr int kChunks = F8 ? D / 64 : D / 32;  // chunks per lane and row
-          constexpr int kSteps = F8 ? 4 : 2;             // k steps of a chunk
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            // e4m3: chunk c of this lane's D/64; bf16: panel c / 2, chunk 2 t4 + c % 2
-            const int ch = F8 ? (D / 64) * t4 + c : (c / 2) * 8 + 2 * t4 + (c & 1);
-            uint32_t bq[NT][kSteps / 2][4];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int h = 0; h < kSteps / 2; ++h) q_frag(j, c * kSteps + 2 * h, bq[j][h]);
-            // two m tiles at a time, their products in turn: a product's accumulator is ready
-            // again 2 NT products later
-#pragma unroll
-            for (int m0t = 0; m0t < MT; m0t += 2) {
-              uint32_t wa[2][4], wb[2][4];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int row = (m0t + u) * 16 + g8;
-                const uint4 va = lds128(chunk_at<TK, C::kPanelBytes>(sk, row, ch));
-                const uint4 vb = lds128(chunk_at<TK, C::kPanelBytes>(sk, row + 8, ch));
-                wa[u][0] = va.x;
-                wa[u][1] = va.y;
-                wa[u][2] = va.z;
-                wa[u][3] = va.w;
-                wb[u][0] = vb.x;
-                wb[u][1] = vb.y;
-                wb[u][2] = vb.z;
-                wb[u][3] = vb.w;
-              }
-#pragma unroll
-              for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  uint32_t af[4];
-                  if constexpr (F8) {
-                    af[0] = e4m3_lo(wa[u][k]);
-                    af[1] = e4m3_lo(wb[u][k]);
-                    af[2] = e4m3_hi(wa[u][k]);
-                    af[3] = e4m3_hi(wb[u][k]);
-                  } else {
-                    af[0] = wa[u][2 * k];
-                    af[1] = wb[u][2 * k];
-                    af[2] = wa[u][2 * k + 1];
-                    af[3] = wb[u][2 * k + 1];
-                  }
-#pragma unroll
-                  for (int j = 0; j < NT; ++j)
-                    mma16<F8>(s[j][m0t + u], af, bq[j][k / 2][2 * (k & 1)],
-                              bq[j][k / 2][2 * (k & 1) + 1]);
-                }
-            }
-          }
-          // ---- scores in the exp2 domain, masks, running reference
-          const bool clear = all_pieces && key0 + TK <= min_end &&
-                             (p.window == 0 || key0 >= max_lo || key0 + TK <= p.sinks);
-          float t0m[NT], t1m[NT];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float ks = 1.f, vl = 0.f;
-            if constexpr (F8) {
-              ks = s_meta[st].ks[mt >> piece_shift];
-              vl = s_meta[st].vl[mt >> piece_shift];
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const float a0 = f0[j] * ks, a1 = f1[j] * ks;
-              float(&v)[4] = s[j][mt];
-              v[0] = fmaf(v[0], a0, vl);
-              v[1] = fmaf(v[1], a1, vl);
-              v[2] = fmaf(v[2], a0, vl);
-              v[3] = fmaf(v[3], a1, vl);
-            }
-          }
-          if (!clear) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const bool here = (okp >> (mt >> piece_shift)) & 1u;
-              const int ka = key0 + mt * 16 + g8, kb = ka + 8;
-              auto sees = [&](int key, int pos) {
-                return here && key <= pos &&
-                       (p.window == 0 || key > pos - p.window || key < p.sinks);
-              };
-#pragma unroll
-              for (int j = 0; j < NT; ++j) {
-                float(&v)[4] = s[j][mt];
-                if (!sees(ka, pos0[j])) v[0] = -INFINITY;
-                if (!sees(ka, pos1[j])) v[1] = -INFINITY;
-                if (!sees(kb, pos0[j])) v[2] = -INFINITY;
-                if (!sees(kb, pos1[j])) v[3] = -INFINITY;
-              }
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            t0m[j] = t1m[j] = -INFINITY;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              t0m[j] = fmax3(t0m[j], s[j][mt][0], s[j][mt][2]);
-              t1m[j] = fmax3(t1m[j], s[j][mt][1], s[j][mt][3]);
-            }
-          }
-          bool move = false;
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            move = move || t0m[j] > m0[j] + kThr || t1m[j] > m1[j] + kThr;
-          if (__any_sync(0xFFFFFFFFu, move)) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-#pragma unroll
-              for (int d = 4; d < 32; d <<= 1) {
-                t0m[j] = fmaxf(t0m[j], __shfl_xor_sync(0xFFFFFFFFu, t0m[j], d));
-                t1m[j] = fmaxf(t1m[j], __shfl_xor_sync(0xFFFFFFFFu, t1m[j], d));
-              }
-              const float n0 = fmaxf(m0[j], t0m[j]), n1 = fmaxf(m1[j], t1m[j]);
-              const float al0 = n0 == -INFINITY ? 1.f : ex2_approx(m0[j] - n0);
-              const float al1 = n1 == -INFINITY ? 1.f : ex2_approx(m1[j] - n1);
-              m0[j] = n0;
-              m1[j] = n1;
-              l0[j] *= al0;
-              l1[j] *= al1;
-#pragma unroll
-              for (int i = 0; i < KS; ++i) {
-                o[j][i][0] *= al0;
-                o[j][i][1] *= al1;
-                o[j][i][2] *= al0;
-                o[j][i][3] *= al1;
-              }
-            }
-          }
           // ---- values of keys nobody sees must not meet a weight of zero as NaN
-          if (!(all_pieces && key0 + TK <= r.L && (key0 >= r.lo || key0 + TK <= r.sinks))) {
+          if (!(all_pieces && tile0 + TK <= r.L && (tile0 >= r.lo || tile0 + TK <= r.sinks))) {
             for (int row = lane / 4; row < TK; row += 8) {
-              const int key = key0 + row;
+              const int key = tile0 + row;
               const bool seen = ((okp >> ((row >> 4) >> piece_shift)) & 1u) && key < r.L &&
                                 (key >= r.lo || key < r.sinks);
               if (!seen)
@@ -795,72 +665,215 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             fence_proxy_async_smem();  // before the slot is handed back to TMA
             __syncwarp();
           }
-          // ---- P and O^T += V^T P^T
-          float e0[NT], e1[NT];
+#pragma unroll 1
+          for (int pass = 0; pass < C::kMT / MT; ++pass) {
+            const int mt0 = pass * MT, key0 = tile0 + mt0 * 16;  // m tiles [mt0, mt0 + MT)
+            // ---- S^T = K Q^T
+            float s[NT][MT][4];
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            e0[j] = m0[j] == -INFINITY ? 0.f : m0[j] - kBias;
-            e1[j] = m1[j] == -INFINITY ? 0.f : m1[j] - kBias;
-          }
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float vi = 1.f;
-            if constexpr (F8) vi = s_meta[st].vi[mt >> piece_shift];
-            uint32_t b0[NT], b1[NT];
+              for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              float pr[4];
-              pr[0] = ex2_approx(s[j][mt][0] - e0[j]);
-              pr[1] = ex2_approx(s[j][mt][1] - e1[j]);
-              pr[2] = ex2_approx(s[j][mt][2] - e0[j]);
-              pr[3] = ex2_approx(s[j][mt][3] - e1[j]);
-              l0[j] = fmaf(pr[0] + pr[2], vi, l0[j]);
-              l1[j] = fmaf(pr[1] + pr[3], vi, l1[j]);
-              b0[j] = movm(F8 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
-              b1[j] = movm(F8 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
-            }
-            if constexpr (F8) {
-              // words of rows 2t, 2t + 1, 2t + 8, 2t + 9; d = (D/8) g8 + ...
-              constexpr int kWords = D / 32;  // 4-byte words per lane and row
-              uint32_t w[4][kWords];
+                for (int k = 0; k < 4; ++k) s[j][mt][k] = 0.f;
+            // 16-byte chunks of the rows outside: a chunk's q fragments serve all m tiles
+            constexpr int kChunks = F8 ? D / 64 : D / 32;  // chunks per lane and row
+            constexpr int kSteps = F8 ? 4 : 2;             // k steps of a chunk
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int row = mt * 16 + 2 * t4 + (k & 1) + (k >> 1) * 8;
-                if constexpr (kWords == 4) {
-                  const uint4 v = lds128(chunk_at<TK, C::kPanelBytes>(sv, row, g8));
-                  w[k][0] = v.x;
-                  w[k][1] = v.y;
-                  w[k][2] = v.z;
-                  w[k][3] = v.w;
-                } else {
-                  const uint2 v =
-                      lds64(chunk_at<TK, C::kPanelBytes>(sv, row, g8 >> 1) + (g8 & 1) * 8);
-                  w[k][0] = v.x;
-                  w[k][1] = v.y;
+            for (int c = 0; c < kChunks; ++c) {
+              // e4m3: chunk c of this lane's D/64; bf16: panel c / 2, chunk 2 t4 + c % 2
+              const int ch = F8 ? (D / 64) * t4 + c : (c / 2) * 8 + 2 * t4 + (c & 1);
+              uint32_t bq[NT][kSteps / 2][4];
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int h = 0; h < kSteps / 2; ++h) q_frag(j, c * kSteps + 2 * h, bq[j][h]);
+              // two m tiles at a time, their products in turn: a product's accumulator is ready
+              // again 2 NT products later
+#pragma unroll
+              for (int m0t = 0; m0t < MT; m0t += 2) {
+                uint32_t wa[2][4], wb[2][4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  const int row = (mt0 + m0t + u) * 16 + g8;
+                  const uint4 va = lds128(chunk_at<TK, C::kPanelBytes>(sk, row, ch));
+                  const uint4 vb = lds128(chunk_at<TK, C::kPanelBytes>(sk, row + 8, ch));
+                  wa[u][0] = va.x;
+                  wa[u][1] = va.y;
+                  wa[u][2] = va.z;
+                  wa[u][3] = va.w;
+                  wb[u][0] = vb.x;
+                  wb[u][1] = vb.y;
+                  wb[u][2] = vb.z;
+                  wb[u][3] = vb.w;
                 }
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                  for (int u = 0; u < 2; ++u) {
+                    uint32_t af[4];
+                    if constexpr (F8) {
+                      af[0] = e4m3_lo(wa[u][k]);
+                      af[1] = e4m3_lo(wb[u][k]);
+                      af[2] = e4m3_hi(wa[u][k]);
+                      af[3] = e4m3_hi(wb[u][k]);
+                    } else {
+                      af[0] = wa[u][2 * k];
+                      af[1] = wb[u][2 * k];
+                      af[2] = wa[u][2 * k + 1];
+                      af[3] = wb[u][2 * k + 1];
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                      mma16<F8>(s[j][m0t + u], af, bq[j][k / 2][2 * (k & 1)],
+                                bq[j][k / 2][2 * (k & 1) + 1]);
+                  }
+              }
+            }
+            // ---- scores in the exp2 domain, masks, running reference
+            const bool clear = all_pieces && key0 + MT * 16 <= min_end &&
+                               (p.window == 0 || key0 >= max_lo || key0 + MT * 16 <= p.sinks);
+            float t0m[NT], t1m[NT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              float ks = 1.f, vl = 0.f;
+              if constexpr (F8) {
+                ks = s_meta[st].ks[(mt0 + mt) >> piece_shift];
+                vl = s_meta[st].vl[(mt0 + mt) >> piece_shift];
               }
 #pragma unroll
-              for (int i = 0; i < kWords; ++i) {
-                const uint32_t xa = __byte_perm(w[0][i], w[1][i], 0x5140),
-                               xb = __byte_perm(w[0][i], w[1][i], 0x7362),
-                               ya = __byte_perm(w[2][i], w[3][i], 0x5140),
-                               yb = __byte_perm(w[2][i], w[3][i], 0x7362);
-                const uint32_t a0[4] = {e4m3_lo(xa), e4m3_hi(xa), e4m3_lo(ya), e4m3_hi(ya)};
-                const uint32_t a1[4] = {e4m3_lo(xb), e4m3_hi(xb), e4m3_lo(yb), e4m3_hi(yb)};
+              for (int j = 0; j < NT; ++j) {
+                const float a0 = f0[j] * ks, a1 = f1[j] * ks;
+                float(&v)[4] = s[j][mt];
+                v[0] = fmaf(v[0], a0, vl);
+                v[1] = fmaf(v[1], a1, vl);
+                v[2] = fmaf(v[2], a0, vl);
+                v[3] = fmaf(v[3], a1, vl);
+              }
+            }
+            if (!clear) {
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                const bool here = (okp >> ((mt0 + mt) >> piece_shift)) & 1u;
+                const int ka = key0 + mt * 16 + g8, kb = ka + 8;
+                auto sees = [&](int key, int pos) {
+                  return here && key <= pos &&
+                         (p.window == 0 || key > pos - p.window || key < p.sinks);
+                };
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                  mma16<F8>(o[j][2 * i], a0, b0[j], b1[j]);
-                  mma16<F8>(o[j][2 * i + 1], a1, b0[j], b1[j]);
+                  float(&v)[4] = s[j][mt];
+                  if (!sees(ka, pos0[j])) v[0] = -INFINITY;
+                  if (!sees(ka, pos1[j])) v[1] = -INFINITY;
+                  if (!sees(kb, pos0[j])) v[2] = -INFINITY;
+                  if (!sees(kb, pos1[j])) v[3] = -INFINITY;
                 }
               }
-            } else {
-              const int row = mt * 16 + (lane & 7) + ((lane >> 4) << 3);
+            }
 #pragma unroll
-              for (int i = 0; i < KS; ++i) {
-                uint32_t a[4];
-                ldsm_x4_trans(a, chunk_at<TK, C::kPanelBytes>(sv, row, 2 * i + ((lane >> 3) & 1)));
+            for (int j = 0; j < NT; ++j) {
+              t0m[j] = t1m[j] = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < NT; ++j) mma16<F8>(o[j][i], a, b0[j], b1[j]);
+              for (int mt = 0; mt < MT; ++mt) {
+                t0m[j] = fmax3(t0m[j], s[j][mt][0], s[j][mt][2]);
+                t1m[j] = fmax3(t1m[j], s[j][mt][1], s[j][mt][3]);
+              }
+            }
+            bool move = false;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              move = move || t0m[j] > m0[j] + kThr || t1m[j] > m1[j] + kThr;
+            if (__any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                  t0m[j] = fmaxf(t0m[j], __shfl_xor_sync(0xFFFFFFFFu, t0m[j], d));
+                  t1m[j] = fmaxf(t1m[j], __shfl_xor_sync(0xFFFFFFFFu, t1m[j], d));
+                }
+                const float n0 = fmaxf(m0[j], t0m[j]), n1 = fmaxf(m1[j], t1m[j]);
+                const float al0 = n0 == -INFINITY ? 1.f : ex2_approx(m0[j] - n0);
+                const float al1 = n1 == -INFINITY ? 1.f : ex2_approx(m1[j] - n1);
+                m0[j] = n0;
+                m1[j] = n1;
+                l0[j] *= al0;
+                l1[j] *= al1;
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                  o[j][i][0] *= al0;
+                  o[j][i][1] *= al1;
+                  o[j][i][2] *= al0;
+                  o[j][i][3] *= al1;
+                }
+              }
+            }
+            // ---- P and O^T += V^T P^T
+            float e0[NT], e1[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              e0[j] = m0[j] == -INFINITY ? 0.f : m0[j] - kBias;
+              e1[j] = m1[j] == -INFINITY ? 0.f : m1[j] - kBias;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              float vi = 1.f;
+              if constexpr (F8) vi = s_meta[st].vi[(mt0 + mt) >> piece_shift];
+              uint32_t b0[NT], b1[NT];
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                float pr[4];
+                pr[0] = ex2_approx(s[j][mt][0] - e0[j]);
+                pr[1] = ex2_approx(s[j][mt][1] - e1[j]);
+                pr[2] = ex2_approx(s[j][mt][2] - e0[j]);
+                pr[3] = ex2_approx(s[j][mt][3] - e1[j]);
+                l0[j] = fmaf(pr[0] + pr[2], vi, l0[j]);
+                l1[j] = fmaf(pr[1] + pr[3], vi, l1[j]);
+                b0[j] = movm(F8 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
+                b1[j] = movm(F8 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
+              }
+              if constexpr (F8) {
+                // words of rows 2t, 2t + 1, 2t + 8, 2t + 9; d = (D/8) g8 + ...
+                constexpr int kWords = D / 32;  // 4-byte words per lane and row
+                uint32_t w[4][kWords];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int row = (mt0 + mt) * 16 + 2 * t4 + (k & 1) + (k >> 1) * 8;
+                  if constexpr (kWords == 4) {
+                    const uint4 v = lds128(chunk_at<TK, C::kPanelBytes>(sv, row, g8));
+                    w[k][0] = v.x;
+                    w[k][1] = v.y;
+                    w[k][2] = v.z;
+                    w[k][3] = v.w;
+                  } else {
+                    const uint2 v =
+                        lds64(chunk_at<TK, C::kPanelBytes>(sv, row, g8 >> 1) + (g8 & 1) * 8);
+                    w[k][0] = v.x;
+                    w[k][1] = v.y;
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                  const uint32_t xa = __byte_perm(w[0][i], w[1][i], 0x5140),
+                                 xb = __byte_perm(w[0][i], w[1][i], 0x7362),
+                                 ya = __byte_perm(w[2][i], w[3][i], 0x5140),
+                                 yb = __byte_perm(w[2][i], w[3][i], 0x7362);
+                  const uint32_t a0[4] = {e4m3_lo(xa), e4m3_hi(xa), e4m3_lo(ya), e4m3_hi(ya)};
+                  const uint32_t a1[4] = {e4m3_lo(xb), e4m3_hi(xb), e4m3_lo(yb), e4m3_hi(yb)};
+#pragma unroll
+                  for (int j = 0; j < NT; ++j) {
+                    mma16<F8>(o[j][2 * i], a0, b0[j], b1[j]);
+                    mma16<F8>(o[j][2 * i + 1], a1, b0[j], b1[j]);
+                  }
+                }
+              } else {
+                const int row = (mt0 + mt) * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                  uint32_t a[4];
+                  ldsm_x4_trans(a, chunk_at<TK, C::kPanelBytes>(sv, row, 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+                  for (int j = 0; j < NT; ++j) mma16<F8>(o[j][i], a, b0[j], b1[j]);
+                }
               }
             }
           }
