@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the hot path runs in the library's
 CUDA kernels. PyTorch supplies device memory and the current stream. There is
-no fallback: if the library is missing or fails to load, calls raise.
+no fallback: if the library (or, for the grouped-query calls, the CPython module
+built beside it) is missing or fails to load, calls raise.
 
     attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                     causal, scale, out=None, lse=None, workspace=None, status=None)
