@@ -99,6 +99,32 @@ def test_many_items_per_cta(tts):
     check(tts, 12, [1300, 500, 129], None, 12, 12, 80, 100, 1)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_items_that_start_late(tts, out_dtype):
+    """Few items, most of which start after their neighbours have ended, because another stream
+    holds the SMs: every item writes its own rows and no other's."""
+    q, k, v = inputs(13, [1920], [1920], 8, 2, 64, torch.bfloat16)
+    cu = torch.tensor([0, 1920], dtype=torch.int32).cuda()
+    out = torch.empty(q.shape, dtype=out_dtype, device="cuda")
+    lse = torch.empty(q.shape[:2], device="cuda")
+
+    def call():
+        tts.attn_fwd_varlen_window(q, k, v, cu, cu, 1920, 1920, 500, 4, 0.125, out=out, lse=lse)
+
+    call()
+    want, want_l = out.clone(), lse.clone()
+    bq, bk, bv = inputs(14, [256], [40000], 120, 1, 128, torch.bfloat16)  # 120 long items
+    cq, ck = (torch.tensor([0, n], dtype=torch.int32).cuda() for n in (256, 40000))
+    busy = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(busy):
+            tts.attn_fwd_varlen(bq, bk, bv, cq, ck, 256, 40000, False, 0.1)
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_l)
+
+
 @pytest.mark.parametrize("d", [64, 80, 128])
 def test_wide_window_equals_causal(tts, d):
     """A window that holds every key takes the same tiles in the same order as the plain causal

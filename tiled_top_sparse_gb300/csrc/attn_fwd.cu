@@ -248,7 +248,11 @@ __device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, It
   const int64_t kv_end0 = keys_for(q_lo, q_lo + kBlockM);
   int64_t kv_end1 = keys_for(q_lo + row1, q_lo + row1 + kBlockM);
   if constexpr (kWin) {
-    if (p.pairing == WindowParams::kSolo) kv_end1 = row1 = 0;
+    if (p.pairing == WindowParams::kSolo) {
+      kv_end1 = row1 = 0;
+      // the second warpgroup's rows are all behind the sequence: the next ones are another item's
+      w.dr = (int)n_qt * kBlockM;
+    }
   }
   const int64_t kv_end = kv_end0 > kv_end1 ? kv_end0 : kv_end1;
   w.q_start = q_start;
