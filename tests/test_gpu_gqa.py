@@ -63,8 +63,8 @@ def cum(lens):
 
 # ------------------------------------------------------------------------------- append
 def run_append(tts, seed, new, past, hq, hkv, d, ps, f8, rope=True, with_q=True, packed=True,
-               gain=1.0, pool=None, pad_rows=0):
-    cu = cum(new)
+               gain=1.0, pool=None, pad_rows=0, max_new=None, front=0):
+    cu = cum(new) + np.int32(front)
     T = int(cu[-1]) + pad_rows
     ends = [a + b for a, b in zip(past, new)]
     tables, pages = make_tables(seed, ends, ps)
@@ -82,7 +82,7 @@ def run_append(tts, seed, new, past, hq, hkv, d, ps, f8, rope=True, with_q=True,
     q_out = torch.full((T, hq, d), 7.0, dtype=torch.bfloat16, device="cuda") if with_q else None
     k_out = torch.full((T, hkv, d), 7.0, dtype=torch.bfloat16, device="cuda")
     tts.rope_kv_append(dk, dv, c[0], c[2], dev(tables), dev(torch.tensor(past, dtype=torch.int32)),
-                       dev(torch.tensor(cu)), max(new), k_scale=c[1], v_scale=c[3],
+                       dev(torch.tensor(cu)), max_new or max(new), k_scale=c[1], v_scale=c[3],
                        cos_sin=None if cs is None else dev(torch.tensor(cs)),
                        q=dq if with_q else None, q_out=q_out, k_out=k_out, status=st)
     tts.check_status(st)
@@ -255,8 +255,8 @@ def poison(c, tables, kv_lens, new, ps, window, sinks, f8):
 
 
 def run_decode(tts, seed, new, kv, hq, hkv, d, ps, f8, window=0, sinks=0, out_dtype=torch.float32,
-               one=False, clean=False, q_gain=1.0):
-    cu = cum(new)
+               one=False, clean=False, q_gain=1.0, max_q=None, front=0):
+    cu = cum(new) + np.int32(front)
     T = int(cu[-1])
     tables, pages = make_tables(seed, kv, ps)
     pool = make_pool(seed + 1, pages, hkv, ps, d, f8)
@@ -275,8 +275,9 @@ def run_decode(tts, seed, new, kv, hq, hkv, d, ps, f8, window=0, sinks=0, out_dt
     def call():
         return tts.attn_decode_paged(
             dev(q), kc, vc, dev(tables), dev(torch.tensor(kv, dtype=torch.int32)), scale,
-            cu_seqlens_q=None if one else dev(torch.tensor(cu)), max_seqlen_q=max(new + [1]),
-            k_scale=ks, v_scale=vs, window=window, sinks=sinks, out=out, lse=lse, status=st)
+            cu_seqlens_q=None if one else dev(torch.tensor(cu)),
+            max_seqlen_q=max_q or max(new + [1]), k_scale=ks, v_scale=vs, window=window,
+            sinks=sinks, out=out, lse=lse, status=st)
 
     call()
     tts.check_status(st)
@@ -287,6 +288,8 @@ def run_decode(tts, seed, new, kv, hq, hkv, d, ps, f8, window=0, sinks=0, out_dt
     if out_dtype == torch.bfloat16:
         tol = tol + (np.abs(ro) + tol) * BF16_HALF
     o, l = out.float().cpu().numpy(), lse.cpu().numpy()
+    assert (o[:front] == 7).all() and (l[:front] == 7).all()  # rows in front of the first
+    o[:front], l[:front] = ro[:front], rl[:front]
     assert np.array_equal(np.isneginf(l[:T]), np.isneginf(rl))
     fin = np.isfinite(rl)
     assert np.all(np.abs(l[:T][fin] - rl[fin]) <= tol_l[fin]), np.abs(l[:T][fin] - rl[fin]).max()
@@ -577,6 +580,37 @@ def test_step_in_a_graph(tts):
             assert torch.equal(s["out"], want[i][0]) and torch.equal(s["lse"], want[i][1]), i
     for s in held:
         assert all(torch.equal(a, b) for a, b in zip(s["c"], plain["c"]))
+
+
+@pytest.mark.parametrize("f8", [True, False])
+def test_bounds_above_the_lengths(tts, f8):
+    """max_seqlen_q and max_new are bounds: single tokens through the kernels for many rows."""
+    for max_q in (3, 9, 64):
+        run_decode(tts, 140, [1, 2, 0, 1], [300, 65, 40, 1], 8, 2, 128, 64, f8, max_q=max_q)
+        run_decode(tts, 141, [1, 1], [700, 33], 8, 2, 64, 16, f8, window=50, sinks=3, max_q=max_q)
+    for max_new in (2, 5, 100):
+        c, q_out, k_out, (qr, kr, kc, vc, ks, vs), n = run_append(
+            tts, 142, [1, 0, 1, 1], [5, 9, 63, 64], 4, 2, 128, 64, f8, max_new=max_new)
+        assert torch.equal(q_out.cpu(), torch.tensor(qr).to(torch.bfloat16))
+        if f8:
+            np.testing.assert_array_equal(ref.codes_of(c[0]), kc)
+            np.testing.assert_array_equal(c[3].cpu().numpy(), vs.astype(np.float32))
+        else:
+            assert torch.equal(c[2].cpu(), torch.tensor(vc).float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("front", [1, 37, 300])
+def test_rows_in_front_of_the_first_request(tts, front):
+    """cu_new / cu_seqlens_q begin above 0: the rows in front belong to nobody."""
+    for new, past in (([1, 2, 1], [0, 63, 100]), ([70, 0, 130], [0, 5, 61])):
+        c, q_out, k_out, (qr, kr, kc, vc, ks, vs), n = run_append(
+            tts, 150, new, past, 4, 2, 128, 64, True, pad_rows=2, front=front)
+        for got, want in ((q_out, qr), (k_out, kr)):
+            assert bool((got[:front] == 7).all()) and bool((got[n:] == 7).all())
+            assert torch.equal(got[front:n].cpu(), torch.tensor(want[front:]).to(torch.bfloat16))
+        np.testing.assert_array_equal(ref.codes_of(c[0]), kc)
+        np.testing.assert_array_equal(ref.codes_of(c[2]), vc)
+    run_decode(tts, 151, [1, 2, 0, 3], [300, 65, 40, 3], 8, 2, 128, 64, True, front=front)
 
 
 def test_calls_on_two_streams(tts):

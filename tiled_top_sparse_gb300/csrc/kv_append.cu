@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 5 : 2) append_pages_kern
   const Req r = find_request(p, q_shift, u, &b, &first);
   const int c = threadIdx.x % kTpr;
   const int64_t i = ((u - first) << q_shift) + threadIdx.x / kTpr;
-  if (i >= r.n) return;
+  if (i < 0 || i >= r.n) return;  // i < 0: units in front of a first bound above 0
   Turn t;
   if (p.cos_sin != nullptr && r.ok) load_turn(p.cos_sin + ((r.past + i) * (D / 2) + c * 8) * 2, t);
   const int h1 = h0 + kQHeads < p.hq ? h0 + kQHeads : p.hq;
