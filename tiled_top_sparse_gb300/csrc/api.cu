@@ -542,10 +542,11 @@ tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* 
       max_seqlen_q > kDecodeMaxQ || total_q > 0x7FFFFF00LL ||
       (int64_t)max_seqlen_q * num_heads_q > 0x7FFFFFFFLL)
     return TTS_ERR_UNSUPPORTED;
-  // tiles of 32 keys, a unit per KV head and 8 q rows, counted in 32 bits
+  // tiles of 32 keys and a few places more per unit, a unit per KV head and 8 q rows, counted in
+  // 32 bits
   const double tiles = (double)batch * num_heads_kv *
                        ((double)max_seqlen_q * (num_heads_q / num_heads_kv) / 8 + 1) *
-                       ((double)max_pages * page_size / 32 + 2);
+                       ((double)max_pages * page_size / 32 + 6);
   if (tiles > 2e9) return TTS_ERR_UNSUPPORTED;
   if (total_q == 0) return TTS_OK;  // nothing to compute
   if (q == nullptr || k_cache == nullptr || v_cache == nullptr || page_tables == nullptr ||

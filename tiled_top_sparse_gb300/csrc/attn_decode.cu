@@ -489,10 +489,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
       }
     }
-    if (!ok) {  // copies in flight must land before the CTA can exit
-      for (int i = it > S ? it - S : 0; i < it; ++i)
-        mbar_wait(smem_u32(&bar_full[i % S]), (i / S) & 1, nullptr, nullptr);
-    }
+    // Copies in flight must land before the CTA can exit, also when a consumer's wait ran out.
+    for (int i = it > S ? it - S : 0; i < it; ++i)
+      mbar_wait(smem_u32(&bar_full[i % S]), (i / S) & 1, nullptr, nullptr);
   } else {
     // ------------------------------------------------------------------ consumers
     constexpr float kThr = F8 ? 4.f : 8.f;    // the reference moves when exceeded by 2^kThr
@@ -647,7 +646,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const uint32_t sk = ring + st * C::kStageBytes, sv = sk + C::kKBytes;
         const uint32_t okp = s_meta[st].ok;
         const bool all_pieces = okp == (1u << n_pieces) - 1u;
-        // rows of the tile that some new token sees all lie in pieces that are there
         if (okp != 0 && rows > 0) {
           // ---- values of keys nobody sees must not meet a weight of zero as NaN
           if (!(all_pieces && tile0 + TK <= r.L && (tile0 >= r.lo || tile0 + TK <= r.sinks))) {

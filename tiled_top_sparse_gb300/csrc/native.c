@@ -71,7 +71,10 @@ static int look(PyObject* t, const char* name, long dev, Tensor* o) {
   }
   Py_DECREF(o->dtype);
   const int64_t at = call_int(t, s_get_device);
-  if (at < 0) return refuse(name, "must be a CUDA tensor");
+  if (at < 0) {
+    PyErr_Clear();
+    return refuse(name, "must be a CUDA tensor");
+  }
   if (at != dev) return refuse(name, "must be on the device of the call's other tensors");
   PyObject* shape = PyObject_GetAttr(t, s_shape);
   o->nd = sizes(shape, o->shape, 4);
@@ -207,6 +210,10 @@ static long device_of(PyObject* t, const char* name) {
 }
 
 static int nargs_are(Py_ssize_t n, Py_ssize_t want) {
+  if (f_append == NULL) {
+    PyErr_SetString(PyExc_RuntimeError, "bind() has not been called");
+    return -1;
+  }
   if (n == want) return 0;
   PyErr_Format(PyExc_TypeError, "%zd arguments wanted, got %zd", want, n);
   return -1;
