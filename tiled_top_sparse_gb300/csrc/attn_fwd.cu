@@ -105,6 +105,11 @@ struct AttnMaps {
   CUtensorMap q_t, k_t;          // SW32 boxes {16, 1, 128} for the d=64..79 tail
   CUtensorMap v_t;               // d=80: SW64 boxes {32, 1, 128} for all of V
 };
+struct WindowMaps : AttnMaps {
+  CUtensorMap o;  // out, 128-byte boxes of 32 rows: {64 bf16 or 32 fp32, 1, 32}
+};
+template <bool kWin>
+using MapsFor = std::conditional_t<kWin, WindowMaps, AttnMaps>;
 
 struct AttnParams {
   const int32_t* cu_q;
@@ -133,6 +138,22 @@ struct WindowParams : AttnParams {
 };
 template <bool kWin>
 using ParamsFor = std::conditional_t<kWin, WindowParams, AttnParams>;
+
+// kWin: registers move from the warpgroup of the issuing warps to the two softmax warpgroups,
+// which hold 128 scores and the masks. 128 x 80 + 256 x 208 = 63488 of the
+// 384 x 168 = 64512 that the block is launched with.
+constexpr int kIssueRegs = 80, kSoftmaxRegs = 208;
+// The sum must not pass what the block was launched with, or the taking warps would wait for ever;
+// the launch looks at the compiled kernel's registers before its first call.
+constexpr int kLaunchRegs = (128 * kIssueRegs + 256 * kSoftmaxRegs + kAttnThreads - 1) / kAttnThreads;
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // Load one 128-row tile (all boxes) of a [tokens, heads, D] tensor (F8: of e4m3 q / k).
 template <int D, bool F8 = false>
@@ -290,7 +311,7 @@ __device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, It
 // (ring slots, S / P phases), nq = items with at least one tile (Q, O phases).
 template <int D, bool F8 = false, bool kWin = false>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    attn_fwd_kernel(const __grid_constant__ AttnMaps maps, const ParamsFor<kWin> p) {
+    attn_fwd_kernel(const __grid_constant__ MapsFor<kWin> maps, const ParamsFor<kWin> p) {
   using C = AttnCfg<D, F8>;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -305,6 +326,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       bar_k[NS], bar_v[NS], bar_k_empty[NS], bar_kv_empty[NS], bar_s[2], bar_p[2], bar_o[2],
       bar_drain;
   __shared__ int s_item[2];
+  __shared__ Item s_work[2];  // kWin: the decoded items
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
 
@@ -352,6 +374,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   volatile int* item_slot = s_item;
   if constexpr (kWin) wait_for_prior_grids();
 
+  if (warp < 4) {
+  if constexpr (kWin) give_registers<kIssueRegs>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -422,6 +446,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                        p.dev_status))
           break;
         item_slot[slot] = it;
+        if constexpr (kWin) s_work[slot] = w;
         mbar_arrive(smem_u32(&bar_item_full[slot]));  // release: the slot write is visible
         ++ni;
         if (it < 0) break;
@@ -430,7 +455,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // The first ring tiles go first (their slots free up while the previous item
         // finishes); Q waits for the previous item's last S MMAs; the remaining tiles
         // need slots that this item's own MMAs free, so they come after Q.
-        const int pre = n < NS ? n : NS;
+        int pre = n < NS ? n : NS;
+        // kWin, items of few tiles: the slot of the previous item's last tile is free only when
+        // that item is done, its last S MMAs a tile earlier, so Q comes before the tile that
+        // needs it (and first of all in a CTA's first item).
+        if constexpr (kWin) pre = nq == 0 ? 0 : n < NS - 1 ? n : NS - 1;
         for (int j = 0; ok && j < pre; ++j) ok = load_k(gt + j, w, j) && load_v(gt + j, w, j);
         for (int wq = 0; ok && wq < 2; ++wq) {
           if (nq >= 1 && !mbar_wait(smem_u32(&bar_q_empty[wq]), (nq - 1) & 1, abort_flag,
@@ -492,13 +521,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!warp_wait(smem_u32(&bar_item_full[slot]), (ni >> 1) & 1, abort_flag, p.dev_status))
         break;
       const int it = item_slot[slot];
+      Item w;
+      if constexpr (kWin) w = s_work[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bar_item_empty[slot]));
       ++ni;
       if (it < 0) break;
-      Item w;
-      bool bad;
-      decode_item<kWin>(p, it, w, &bad);
+      if constexpr (!kWin) {
+        bool bad;
+        decode_item<kWin>(p, it, w, &bad);
+      }
       const int n = w.n_tiles, n0 = w.n0, n1 = w.n1;
       if (n == 0) continue;
       const int st0 = gt % NS;
@@ -628,8 +660,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // Drain: every MMA issued by this warp is complete before TMEM is freed.
     mma_commit_elect(smem_u32(&bar_drain), e);
     mbar_wait(smem_u32(&bar_drain), 0, nullptr, p.dev_status);
-  } else if (warp >= 4) {
+  }
+  } else {
     // ------------------------------------------------------------ softmax / epilogue
+    if constexpr (kWin) take_registers<kSoftmaxRegs>();
     const int wg = (warp - 4) >> 2;            // 0 or 1
     const int row = ((warp & 3) << 5) + lane;  // TMEM lane == row within the tile
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -645,13 +679,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                               abort_flag, p.dev_status));
       if (!ok) break;
       const int it = item_slot[slot];
+      Item w;
+      if constexpr (kWin) w = s_work[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bar_item_empty[slot]));
       ++ni;
       if (it < 0) break;
-      Item w;
-      bool bad;
-      decode_item<kWin>(p, it, w, &bad);
+      if constexpr (!kWin) {
+        bool bad;
+        decode_item<kWin>(p, it, w, &bad);
+      }
       const int n_tiles = wg == 0 ? w.n0 : w.n1;  // tiles this warpgroup's rows can see
       const int64_t Lq = w.Lq, Lk = w.Lk;
       int64_t first = w.q_lo + wg * kBlockM;  // this warpgroup's first row and its head
@@ -695,6 +732,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float* s = reinterpret_cast<float*>(sr);
         const int64_t kv0 = (int64_t)key_tile<kWin>(w, j) * kBlockN;
         float tile_max = fmaxf(fmax3(part_max[0], part_max[1], part_max[2]), part_max[3]);
+        bool dead[2] = {false, false};  // kWin: no row of the warp sees these 64 columns
         if constexpr (kWin) {
           if (__any_sync(0xFFFFFFFFu, kv0 + kBlockN > limit ||
                                           (kv0 < win_lo && kv0 + kBlockN > p.sinks))) {
@@ -709,15 +747,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const int b = n - c0;
               return b <= 0 ? 0u : b >= 32 ? 0xFFFFFFFFu : (1u << b) - 1u;
             };
+            // A warp's 32 rows end in one or two words: those are masked and their maximum taken
+            // again; words all rows see keep TMEM's; and 64 columns that no row sees get no
+            // exponentials (d = 128: their weights are written as zeros).
+            uint32_t see[4];
   #pragma unroll
-            for (int c0 = 0; c0 < 128; c0 += 32) {
-              const uint32_t see = below(lim, c0) & (~below(lo, c0) | below(sk, c0));
-              if (__all_sync(0xFFFFFFFFu, see == 0xFFFFFFFFu)) continue;
+            for (int q = 0; q < 4; ++q)
+              see[q] = below(lim, 32 * q) & (~below(lo, 32 * q) | below(sk, 32 * q));
   #pragma unroll
-              for (int cc = 0; cc < 32; ++cc)
-                if (!((see >> cc) & 1u)) s[c0 + cc] = -INFINITY;
+            for (int h = 0; h < 2; ++h)
+              if constexpr (D >= 128)
+                dead[h] = !__any_sync(0xFFFFFFFFu, (see[2 * h] | see[2 * h + 1]) != 0);
+  #pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (dead[q / 2]) {
+                part_max[q] = -INFINITY;
+              } else if (!__all_sync(0xFFFFFFFFu, see[q] == 0xFFFFFFFFu)) {
+  #pragma unroll
+                for (int cc = 0; cc < 32; ++cc)
+                  if (!((see[q] >> cc) & 1u)) s[32 * q + cc] = -INFINITY;
+                part_max[q] = row_max<32>(s + 32 * q);
+              }
             }
-            tile_max = row_max<128>(s);
+            tile_max = fmaxf(fmax3(part_max[0], part_max[1], part_max[2]), part_max[3]);
           }
           if (kv0 + kBlockN > Lk) {  // rows behind the sequence: cleared once V has landed
             const int gr = ring + j, st = gr % NS;
@@ -758,9 +810,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if constexpr (D >= 128) {
           // Two halves: the first half of P goes to TMEM while the second is computed
           // (and fewer values stay live, which at d = 128 removes most spills).
-          const float l_a = exp2_pack_sum<64>(sr, c, neg_mc);
+          auto half = [&](uint32_t* x, bool none) -> float {
+            if (kWin && none) {
+  #pragma unroll
+              for (int q = 0; q < 32; ++q) x[q] = 0u;
+              return 0.f;
+            }
+            return exp2_pack_sum<64>(x, c, neg_mc);
+          };
+          const float l_a = half(sr, dead[0]);
           tmem_st32(S_row, *reinterpret_cast<const uint32_t(*)[32]>(&sr[0]));
-          const float l_b = exp2_pack_sum<64>(sr + 64, c, neg_mc);
+          const float l_b = half(sr + 64, dead[1]);
           tmem_st32(S_row + 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[64]));
           l += l_a + l_b;
         } else {
@@ -793,57 +853,88 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+      if constexpr (kWin) {
+        // 128 bytes of each of the warp's 32 rows at a time (64 bf16 or 32 fp32 columns; less in
+        // d = 80's tail): one row per thread out of TMEM, through the warp's staging slice,
+        // and from there by one TMA store, so that the warp goes on with the next item while the
+        // rows are still on their way. Rows that end inside the 32 (a sequence's last) and the tail
+        // leave by plain stores. bf16: each value rounded to nearest even, the only rounding.
+        const int64_t row0 = first + (warp & 3) * 32;  // this warp's first row
+        if (row0 + 32 > 0 && row0 < Lq) {              // uniform: row0 is a multiple of 32
+          const bool whole = row0 + 32 <= Lq;
+          const uint32_t slice = smem_u32(stage);
+          auto columns = [&](auto out_bf16) {
+            constexpr bool kHalf = decltype(out_bf16)::value;
+            constexpr int kCols = kHalf ? 64 : 32, kSize = kHalf ? 2 : 4;
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += kCols) {
+              const int cw = D - c0 < kCols ? D - c0 : kCols;  // kCols, or 16 for the tail
+              uint32_t o[kCols];
+#pragma unroll
+              for (int h = 0; h < kCols; h += 32) {
+                if (h >= cw) continue;
+                if (n_tiles > 0) {
+                  if (cw - h >= 32)
+                    tmem_ld32(O_row + c0 + h, *reinterpret_cast<uint32_t(*)[32]>(&o[h]));
+                  else
+                    tmem_ld16(O_row + c0 + h, *reinterpret_cast<uint32_t(*)[16]>(&o[h]));
+                } else {
+#pragma unroll
+                  for (int q = 0; q < 32; ++q) o[h + q] = 0u;
+                }
+              }
+              tmem_ld_wait();
+              if (lane == 0) bulk_wait_read_all();  // the slice's last store has read it
+              __syncwarp();
+#pragma unroll
+              for (int q = 0; q < 8; ++q)  // 16 bytes; the order is TMA's 128-byte swizzle
+                if (q * 16 < cw * kSize) {
+                  uint32_t v[4];
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) {
+                    if constexpr (kHalf)
+                      v[z] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * z]) * inv_l,
+                                         __uint_as_float(o[8 * q + 2 * z + 1]) * inv_l);
+                    else
+                      v[z] = __float_as_uint(__uint_as_float(o[4 * q + z]) * inv_l);
+                  }
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                   slice + lane * 128 + ((q ^ (lane & 7)) << 4)),
+                               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                               : "memory");
+                }
+              if (whole && cw == kCols) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  tma_store_3d(&maps.o, slice, c0, w.h, (int)(w.q_start + row0));
+                  bulk_commit();
+                }
+              } else {
+                __syncwarp();
+                const int lpr = cw * kSize / 16;  // lanes per row segment
+                for (int rr = 0; rr < 32; rr += 32 / lpr) {
+                  const int r = rr + lane / lpr, q = lane % lpr;
+                  const uint4 v = reinterpret_cast<const uint4*>(stage)[r * 8 + (q ^ (r & 7))];
+                  const int64_t ii = row0 + r;
+                  if (ii < Lq)
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.out) +
+                                              (((w.q_start + ii) * p.hq + w.h) * (int64_t)D + c0) *
+                                                  kSize + 16 * q) = v;
+                }
+                __syncwarp();
+              }
+            }
+          };
+          if (p.out_bf16)
+            columns(std::true_type());
+          else
+            columns(std::false_type());
+        }
+      } else {
       // Rows leave TMEM one per thread; this warp's 4 KB staging slice turns them into
       // whole 128-byte row segments, so each store instruction writes full lines.
       const int64_t row0 = first + (warp & 3) * 32;  // this warp's first row
-      bool rounded = false;
-      if constexpr (kWin) rounded = p.out_bf16 != 0;
-      if (rounded) {
-        // 64 columns at a time, rounded to bf16 (nearest even): 128-byte row segments again
-        // (32 for the d = 80 tail)
-        uint4* stage16 = reinterpret_cast<uint4*>(stage);
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 64) {
-          const int cw = (D - c0 < 64) ? D - c0 : 64;  // 64, or 16 for the d = 80 tail
-#pragma unroll
-          for (int h = 0; h < 64; h += 32) {
-            if (h >= cw) continue;
-            uint32_t o[32];
-            if (n_tiles > 0) {
-              if (cw - h >= 32)
-                tmem_ld32(O_row + c0 + h, o);
-              else
-                tmem_ld16(O_row + c0 + h, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-              tmem_ld_wait();
-            } else {
-#pragma unroll
-              for (int q = 0; q < 32; ++q) o[q] = 0u;
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (h + 8 * q < cw) {
-                uint32_t v[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                  v[z] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * z]) * inv_l,
-                                     __uint_as_float(o[8 * q + 2 * z + 1]) * inv_l);
-                stage16[lane * 8 + ((h / 8 + q) ^ (lane & 7))] = make_uint4(v[0], v[1], v[2], v[3]);
-              }
-          }
-          __syncwarp();
-          const int lpr = cw / 8;  // lanes per row segment
-          for (int rr = 0; rr < 32; rr += 32 / lpr) {
-            const int r = rr + lane / lpr, q = lane % lpr;
-            const uint4 v = stage16[r * 8 + (q ^ (r & 7))];
-            const int64_t ii = row0 + r;
-            if (ii >= 0 && ii < Lq)
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) +
-                                        ((w.q_start + ii) * p.hq + w.h) * (int64_t)D + c0 + 8 * q) =
-                  v;
-          }
-          __syncwarp();
-        }
-      } else {
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
         constexpr int kW = 32;
@@ -886,6 +977,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if constexpr (kWin) ring += w.n_tiles;
       if (n_tiles > 0) ++nq;
     }
+    if constexpr (kWin) {
+      if (lane == 0) bulk_wait_read_all();  // shared memory stays until then
+    }
   }
 
   tc_fence_before();
@@ -908,16 +1002,18 @@ __global__ void f32_to_bf16_kernel(const float4* __restrict__ in, uint2* __restr
 template <int D, bool F8 = false, bool kWin = false>
 cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
   using C = AttnCfg<D, F8>;
-  AttnMaps maps;
-  // es: bytes per value (2: bf16, 1: e4m3 q / k)
+  MapsFor<kWin> maps;
+  // es: bytes per value (2: bf16, 1: e4m3 q / k, 4: fp32 out)
   auto make = [&](CUtensorMap* m, const void* base, int64_t tokens, int heads, uint32_t box0,
-                  CUtensorMapSwizzle sw, int es = 2) -> bool {
+                  CUtensorMapSwizzle sw, int es = 2, int box_rows = kBlockN) -> bool {
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)heads, (uint64_t)tokens};
     const uint64_t strides[2] = {(uint64_t)D * es, (uint64_t)heads * D * es};
-    const uint32_t box[3] = {box0, 1, (uint32_t)kBlockN};
-    CUresult r = encode_tensor_map(
-        m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-        const_cast<void*>(base), dims, strides, box, sw);
+    const uint32_t box[3] = {box0, 1, (uint32_t)box_rows};
+    CUresult r = encode_tensor_map(m,
+                                   es == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                                   3, const_cast<void*>(base), dims, strides, box, sw);
     if (r != CUDA_SUCCESS) {
       *drv_err = (int)r;
       return false;
@@ -939,6 +1035,11 @@ cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
     maps.q_t = maps.q;
     maps.k_t = maps.k;
     maps.v_t = maps.v;
+  }
+  if constexpr (kWin) {
+    if (!make(&maps.o, a.out, tq, a.hq, a.out_bf16 ? 64 : 32, CU_TENSOR_MAP_SWIZZLE_128B,
+              a.out_bf16 ? 2 : 4, 32))
+      return cudaErrorInvalidValue;
   }
   ParamsFor<kWin> p;
   p.cu_q = a.cu_q;
@@ -985,6 +1086,13 @@ cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
   e = cudaFuncSetAttribute(attn_fwd_kernel<D, F8, kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmemBytes);
   if (e != cudaSuccess) return e;
+  if constexpr (kWin) {
+    static const int regs = [] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, attn_fwd_kernel<D, F8, kWin>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
   if (kWin && items <= sms) {
     p.work_counter = nullptr;  // one item per CTA: none to hand out, nothing to zero first
   } else {
