@@ -192,18 +192,45 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t q_d, uint64_t
 
 // O[tmem] (+)= P[tmem] V[smem]; V is MN-major (d contiguous). v_d describes the
 // first V box (SW128 boxes for d=64/128, SW64 boxes for d=80).
-template <int D>
+// Keys [16 kFrom, 16 kTo) of the tile.
+template <int D, int kFrom = 0, int kTo = kBlockN / 16>
 __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint64_t v_d,
                                          uint32_t accumulate, uint32_t e) {
   using C = AttnCfg<D>;
   constexpr uint32_t idesc = idesc_bf16_f32(128, C::kPvN, 0, 1);
   constexpr uint32_t kStep = C::kTail ? 16 * 64 : 16 * 128;  // 16 key rows of one box
 #pragma unroll
-  for (int ks = 0; ks < kBlockN / 16; ++ks)
+  for (int ks = kFrom; ks < kTo; ++ks)
     mma_ts_elect(o_tmem, p_tmem + ks * 8, v_d + ((ks * kStep) >> 4), idesc,
                  (ks > 0) ? 1u : accumulate, e);
 }
 
+
+// exp2_pack_sum with the four partial sums carried from part to part, and their total.
+template <int N>
+__device__ __forceinline__ void exp2_pack_acc(uint32_t* sr, float c, float nmc, float2 (&acc)[4]) {
+  const float* s = reinterpret_cast<const float*>(sr);
+  const float2 c2 = make_float2(c, c), nm2 = make_float2(nmc, nmc);
+#pragma unroll
+  for (int k0 = 0; k0 < N / 2; k0 += 8) {
+    float2 x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      x[u] = ffma2(make_float2(s[2 * (k0 + u)], s[2 * (k0 + u) + 1]), c2, nm2);
+      x[u].x = ex2_approx(x[u].x);
+      x[u].y = ex2_approx(x[u].y);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      acc[u & 3] = fadd2(acc[u & 3], x[u]);
+      sr[k0 + u] = pack_bf16x2(x[u].x, x[u].y);
+    }
+  }
+}
+__device__ __forceinline__ float sum_of(const float2 (&acc)[4]) {
+  const float2 a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+  return a.x + a.y;
+}
 
 // One work item = (256-row query pair, sequence, head); `it` enumerates them with
 // the heaviest (latest, causal) pairs of every sequence first. Every role decodes
@@ -327,6 +354,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       bar_drain;
   __shared__ int s_item[2];
   __shared__ Item s_work[2];  // kWin: the decoded items
+  __shared__ __align__(8) uint64_t bar_half[2];  // kWin: the weights of a tile's first 64 keys
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
 
@@ -352,6 +380,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(smem_u32(&bar_s[i]), 1);
       mbar_init(smem_u32(&bar_p[i]), kBlockM);
       mbar_init(smem_u32(&bar_o[i]), 1);
+      if constexpr (kWin) mbar_init(smem_u32(&bar_half[i]), kBlockM);
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(smem_u32(&bar_k[i]), 1);
@@ -516,6 +545,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // phases); nq: items with tiles (Q phases).
     int ni = 0, nq = 0, gt = 0, g0 = 0, g1 = 0;
     bool ok = true;
+    // PV of tile j (ring stage st) of warpgroup w once its weights are there; kWin: the first 64
+    // keys' products start while the weights of the others are still computed.
+    auto pv = [&](int w, int st, int j, int tiles) -> bool {
+      const uint32_t ph = (tiles + j) & 1;
+      if constexpr (kWin) {
+        if (!warp_wait(smem_u32(&bar_half[w]), ph, abort_flag, p.dev_status)) return false;
+        tc_fence_after();
+        issue_pv<D, 0, 4>(O_t[w], S_t[w], vd[st], j > 0, e);
+      }
+      if (!warp_wait(smem_u32(&bar_p[w]), ph, abort_flag, p.dev_status)) return false;
+      tc_fence_after();
+      issue_pv<D, kWin ? 4 : 0>(O_t[w], S_t[w], vd[st], j > 0, e);
+      return true;
+    };
     while (ok) {
       const int slot = ni & 1;
       if (!warp_wait(smem_u32(&bar_item_full[slot]), (ni >> 1) & 1, abort_flag, p.dev_status))
@@ -533,6 +576,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       const int n = w.n_tiles, n0 = w.n0, n1 = w.n1;
       if (n == 0) continue;
+      int tail_row = kBlockN;  // kWin: first row of the last tile that is behind the sequence
+      if constexpr (kWin) tail_row = (int)(w.Lk - (int64_t)key_tile<true>(w, n - 1) * kBlockN);
       const int st0 = gt % NS;
       ok = warp_wait(smem_u32(&bar_q[0]), nq & 1, abort_flag, p.dev_status) &&
            warp_wait(smem_u32(&bar_k[st0]), (gt / NS) & 1, abort_flag, p.dev_status);
@@ -558,7 +603,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // the last one or two, where a warpgroup may stop or sit out.
       const int nb = n0 < n1 ? n0 : n1;
       int j = 0;
-      for (; j + 1 < nb; ++j) {
+      // kWin, d = 64: all by the second loop. What the instruction cache does not hold costs more
+      // there than the branches (88 -> 84 us; d = 128: 105 -> 108).
+      constexpr bool kStraight = !(kWin && D == 64);
+      for (; kStraight && j + 1 < nb; ++j) {
         const int gj = gt + j;
         const int st = gj % NS;
         const int st1 = (gj + 1) % NS;
@@ -566,12 +614,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           ok = false;
           break;
         }
-        if (!warp_wait(smem_u32(&bar_p[0]), (g0 + j) & 1, abort_flag, p.dev_status)) {
+        if (!pv(0, st, j, g0)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        issue_pv<D>(O_t[0], S_t[0], vd[st], j > 0, e);
         if (!warp_wait(smem_u32(&bar_k[st1]), ((gj + 1) / NS) & 1, abort_flag, p.dev_status)) {
           ok = false;
           break;
@@ -580,12 +626,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         issue_qk<D, F8>(S_t[0], qd[0], kd[st1], qtd[0], ktd[st1], e);
         mma_commit_elect(smem_u32(&bar_s[0]), e);
         if (j + 2 == n0) mma_commit_elect(smem_u32(&bar_q_empty[0]), e);
-        if (!warp_wait(smem_u32(&bar_p[1]), (g1 + j) & 1, abort_flag, p.dev_status)) {
+        if (!pv(1, st, j, g1)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        issue_pv<D>(O_t[1], S_t[1], vd[st], j > 0, e);
         mma_commit_elect(smem_u32(&bar_kv_empty[st]), e);
         issue_qk<D, F8>(S_t[1], qd[1], kd[st1], qtd[1], ktd[st1], e);
         mma_commit_elect(smem_u32(&bar_s[1]), e);
@@ -602,14 +646,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           ok = false;
           break;
         }
+        if constexpr (kWin) {
+          // Rows of V behind the sequence's last key: what they hold must not meet a weight of zero
+          // as NaN (V has landed: waited for above, or with K).
+          if (j == n - 1 && tail_row < kBlockN) {
+            constexpr int kRow = C::kVBoxBytes / kBlockN;  // bytes of a row in one box
+            for (int b = 0; b < C::kVBoxes; ++b)
+              for (int o = tail_row * kRow + lane * 16; o < kBlockN * kRow; o += 32 * 16)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 sV(st) + b * C::kVBoxBytes + o),
+                             "r"(0)
+                             : "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
         // warpgroup 0
         if (act0) {
-          if (!warp_wait(smem_u32(&bar_p[0]), (g0 + j) & 1, abort_flag, p.dev_status)) {
+          if (!pv(0, st, j, g0)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          issue_pv<D>(O_t[0], S_t[0], vd[st], j > 0, e);
           if (more0) {
             if (!warp_wait(smem_u32(&bar_k[st1]), ((gj + 1) / NS) & 1, abort_flag,
                            p.dev_status)) {
@@ -627,12 +684,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         // warpgroup 1
         if (act1) {
-          if (!warp_wait(smem_u32(&bar_p[1]), (g1 + j) & 1, abort_flag, p.dev_status)) {
+          if (!pv(1, st, j, g1)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          issue_pv<D>(O_t[1], S_t[1], vd[st], j > 0, e);
         }
         mma_commit_elect(smem_u32(&bar_kv_empty[st]), e);  // every PV of this tile issued
         if (act1) {
@@ -671,7 +726,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t O_row = tmem + 256 + wg * 128 + lane_off;
     float4* stage = reinterpret_cast<float4*>(stage_base + (warp - 4) * 4096);
     int ni = 0, nq = 0, gt = 0;
-    int ring = 0;  // kWin: K/V tiles streamed before this item
     bool ok = true;
     while (ok) {
       const int slot = ni & 1;
@@ -732,7 +786,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float* s = reinterpret_cast<float*>(sr);
         const int64_t kv0 = (int64_t)key_tile<kWin>(w, j) * kBlockN;
         float tile_max = fmaxf(fmax3(part_max[0], part_max[1], part_max[2]), part_max[3]);
-        bool dead[2] = {false, false};  // kWin: no row of the warp sees these 64 columns
         if constexpr (kWin) {
           if (__any_sync(0xFFFFFFFFu, kv0 + kBlockN > limit ||
                                           (kv0 < win_lo && kv0 + kBlockN > p.sinks))) {
@@ -747,48 +800,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const int b = n - c0;
               return b <= 0 ? 0u : b >= 32 ? 0xFFFFFFFFu : (1u << b) - 1u;
             };
-            // A warp's 32 rows end in one or two words: those are masked and their maximum taken
-            // again; words all rows see keep TMEM's; and 64 columns that no row sees get no
-            // exponentials (d = 128: their weights are written as zeros).
-            uint32_t see[4];
-  #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              see[q] = below(lim, 32 * q) & (~below(lo, 32 * q) | below(sk, 32 * q));
-  #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if constexpr (D >= 128)
-                dead[h] = !__any_sync(0xFFFFFFFFu, (see[2 * h] | see[2 * h + 1]) != 0);
+            // words that all rows see keep the maximum that came with them
   #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              if (dead[q / 2]) {
-                part_max[q] = -INFINITY;
-              } else if (!__all_sync(0xFFFFFFFFu, see[q] == 0xFFFFFFFFu)) {
+              const uint32_t see = below(lim, 32 * q) & (~below(lo, 32 * q) | below(sk, 32 * q));
+              if (__all_sync(0xFFFFFFFFu, see == 0xFFFFFFFFu)) continue;
   #pragma unroll
-                for (int cc = 0; cc < 32; ++cc)
-                  if (!((see[q] >> cc) & 1u)) s[32 * q + cc] = -INFINITY;
-                part_max[q] = row_max<32>(s + 32 * q);
-              }
+              for (int cc = 0; cc < 32; ++cc)
+                if (!((see >> cc) & 1u)) s[32 * q + cc] = -INFINITY;
+              part_max[q] = row_max<32>(s + 32 * q);
             }
             tile_max = fmaxf(fmax3(part_max[0], part_max[1], part_max[2]), part_max[3]);
-          }
-          if (kv0 + kBlockN > Lk) {  // rows behind the sequence: cleared once V has landed
-            const int gr = ring + j, st = gr % NS;
-            const bool landed = mbar_wait(smem_u32(kOneKV ? &bar_k[st] : &bar_v[st]),
-                                          (gr / NS) & 1, abort_flag, p.dev_status);
-            ok = __all_sync(0xFFFFFFFFu, landed);
-            if (!ok) break;
-            if (row >= Lk - kv0) {
-              constexpr int kRow = C::kVBoxBytes / kBlockN;  // bytes of a row in one box
-  #pragma unroll 1
-              for (int b = 0; b < C::kVBoxes; ++b)
-  #pragma unroll 1
-                for (int o = 0; o < kRow; o += 16)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                   sV(st) + b * C::kVBoxBytes + row * kRow + o),
-                               "r"(0)
-                               : "memory");
-            }
-            fence_proxy_async_smem();
           }
         } else if (kv0 + kBlockN > limit) {  // masked columns must not count in the max
           const int64_t lim = limit - kv0;
@@ -806,21 +828,48 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           m_ref = m_new;
         }
         const float neg_mc = (m_ref == -INFINITY) ? 0.f : -m_ref * c;
+        auto rescale = [&]() {
+          // Rescale O (its previous PV finished: it was issued before this tile's S MMA,
+          // whose completion this thread observed).
+          if (j > 0 && __any_sync(0xFFFFFFFFu, resc)) {
+  #pragma unroll (kWin ? 1 : D / 16)
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t o[16];
+              tmem_ld16(O_row + c0, o);
+              tmem_ld_wait();
+  #pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(O_row + c0, o);
+            }
+          }
+        };
+        if constexpr (kWin) {
+          // The weights of 64 keys go to TMEM and are announced while the others are computed.
+          // Sums in the order of the kernel without a window.
+          float2 acc[4] = {};
+          float l_a = 0.f;
+          exp2_pack_acc<64>(sr, c, neg_mc, acc);
+          if constexpr (D >= 128) {
+            l_a = sum_of(acc);
+  #pragma unroll
+            for (int q = 0; q < 4; ++q) acc[q] = make_float2(0.f, 0.f);
+          }
+          tmem_st32(S_row, *reinterpret_cast<const uint32_t(*)[32]>(&sr[0]));
+          rescale();
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(smem_u32(&bar_half[wg]));
+          exp2_pack_acc<64>(sr + 64, c, neg_mc, acc);
+          tmem_st32(S_row + 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[64]));
+          l += D >= 128 ? l_a + sum_of(acc) : sum_of(acc);
+        } else {
         // P packed as bf16 pairs in place (over sr[0..63], or sr[0..31] and sr[64..95]).
         if constexpr (D >= 128) {
           // Two halves: the first half of P goes to TMEM while the second is computed
           // (and fewer values stay live, which at d = 128 removes most spills).
-          auto half = [&](uint32_t* x, bool none) -> float {
-            if (kWin && none) {
-  #pragma unroll
-              for (int q = 0; q < 32; ++q) x[q] = 0u;
-              return 0.f;
-            }
-            return exp2_pack_sum<64>(x, c, neg_mc);
-          };
-          const float l_a = half(sr, dead[0]);
+          const float l_a = exp2_pack_sum<64>(sr, c, neg_mc);
           tmem_st32(S_row, *reinterpret_cast<const uint32_t(*)[32]>(&sr[0]));
-          const float l_b = half(sr + 64, dead[1]);
+          const float l_b = exp2_pack_sum<64>(sr + 64, c, neg_mc);
           tmem_st32(S_row + 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[64]));
           l += l_a + l_b;
         } else {
@@ -829,18 +878,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int q4 = 0; q4 < 2; ++q4)
             tmem_st32(S_row + q4 * 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[q4 * 32]));
         }
-        // Rescale O (its previous PV finished: it was issued before this tile's S MMA,
-        // whose completion this thread observed).
-        if (j > 0 && __any_sync(0xFFFFFFFFu, resc)) {
-  #pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t o[16];
-            tmem_ld16(O_row + c0, o);
-            tmem_ld_wait();
-  #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st16(O_row + c0, o);
-          }
+        rescale();
         }
         tmem_st_wait();
         tc_fence_before();
@@ -866,7 +904,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           auto columns = [&](auto out_bf16) {
             constexpr bool kHalf = decltype(out_bf16)::value;
             constexpr int kCols = kHalf ? 64 : 32, kSize = kHalf ? 2 : 4;
-#pragma unroll
+#pragma unroll (D % 64 == 0 ? 1 : D / kCols + 1)
             for (int c0 = 0; c0 < D; c0 += kCols) {
               const int cw = D - c0 < kCols ? D - c0 : kCols;  // kCols, or 16 for the tail
               uint32_t o[kCols];
@@ -974,7 +1012,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         p.lse[(w.q_start + i) * p.hq + w.h] =
             (l > 0.f) ? m_ref * sc + log2f(l) * 0.69314718055994531f : -INFINITY;
       gt += n_tiles;
-      if constexpr (kWin) ring += w.n_tiles;
       if (n_tiles > 0) ++nq;
     }
     if constexpr (kWin) {
