@@ -14,7 +14,7 @@
 // Bound: HBM. A prompt token moves (4 Hq + (6 + 2 c) Hkv) d bytes (c = 2 or 1 bytes per cached
 // value; k_out included), read and written once: a page of one head stays in registers between
 // the maximum and the rounding, and the rotation's table row is read once per eight q heads.
-// 36,411 tokens of 32 / 8 heads of 128 into e4m3: 154 us, 5.8 TB/s, 0.86 of the measured copy
+// 36,411 tokens of 32 / 8 heads of 128 into e4m3: 147 us, 6.1 TB/s, 0.90 of the measured copy
 // rate (what is left: the blocks' chain of lengths, rows, reduction and stores, 50 % of the warps
 // resident). A step is one launch's latency: 3.0 us for 8 requests, 3.3 for 64.
 #include <cstdint>
@@ -328,32 +328,35 @@ __device__ __forceinline__ void rotate_q_row(const KvAppendArgs& p, bool ok, int
 
 constexpr int kQHeads = 8;  // q heads that share one load of the table row
 
-// Prompts: a block per (page, head) of k and of v, then a block per (token tile, 8 q heads).
+// Prompts: a block per (page, head) of k and of v, and a block per (token tile, 8 q heads).
 // Registers are held to 48 (64 for the pages of 2048 pieces), for five (two) blocks per SM: what
 // bounds the kernel is how many rows are on their way (28,000 tokens in pages of 128: 75 -> 55 us,
 // of 16 to 32: 58 -> 53 us; pages of 64 in blocks of 512 threads instead of 256: 50 -> 64 us).
 template <int D, bool kF8, int kPasses, int kMost>
 __global__ void __launch_bounds__(kMost, kMost == 256 ? 5 : 2) append_pages_kernel(const KvAppendArgs p,
-                                                           int64_t kv_blocks, int q_shift,
+                                                           uint64_t q_share, int q_shift,
                                                            int q_groups) {
   constexpr int kTpr = D / 16;
   __shared__ float s_red[16];
   wait_for_prior_grids();
   if (blockIdx.x == 0) report(p);
   int64_t first;
-  if ((int64_t)blockIdx.x < kv_blocks) {
-    const int heads = 2 * p.hkv;
-    const int64_t u = blockIdx.x / heads;
-    const int hh = blockIdx.x % heads;
+  // q_share: the part of the blocks that rotates q, as a fraction of 2^32. The two kinds alternate at
+  // that rate: what a page's block waits for (its reduction) is filled by a q block's plain
+  // streaming (36,000 tokens: 154 us one kind after the other, 147 so).
+  const unsigned qb = (unsigned)((blockIdx.x * q_share) >> 32);  // q blocks before this one
+  if (qb == (unsigned)(((blockIdx.x + 1ull) * q_share) >> 32)) {
+    const unsigned kb = blockIdx.x - qb, heads = 2 * p.hkv;
+    const int64_t u = kb / heads;
+    const int hh = (int)(kb % heads);
     int b;
     const Req r = find_request(p, p.page_shift, u, &b, &first);
     append_page<D, kF8, kPasses, false>(p, b, r, (int)(u - first), hh >= p.hkv ? hh - p.hkv : hh,
                                         hh >= p.hkv, threadIdx.x, blockDim.x, s_red);
     return;
   }
-  const int64_t v = (int64_t)blockIdx.x - kv_blocks;
-  const int64_t u = v / q_groups;
-  const int h0 = (int)(v % q_groups) * kQHeads;
+  const int64_t u = qb / (unsigned)q_groups;
+  const int h0 = (int)(qb % (unsigned)q_groups) * kQHeads;
   int b;
   const Req r = find_request(p, q_shift, u, &b, &first);
   const int c = threadIdx.x % kTpr;
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 5 : 2) append_pages_kern
   Turn t;
   if (p.cos_sin != nullptr && r.ok) load_turn(p.cos_sin + ((r.past + i) * (D / 2) + c * 8) * 2, t);
   const int h1 = h0 + kQHeads < p.hq ? h0 + kQHeads : p.hq;
-#pragma unroll 4
+#pragma unroll 8
   for (int h = h0; h < h1; ++h) rotate_q_row<D>(p, r.ok, r.t0 + i, h, c, t);
 }
 
@@ -431,10 +434,12 @@ cudaError_t launch_append(const KvAppendArgs& p, cudaStream_t stream) {
       p.q != nullptr ? ((p.total_new >> q_shift) + 2 * (int64_t)p.batch) * q_groups : 0;
   if (kv_blocks + q_blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(kv_blocks + q_blocks);
+  // rounded up: grid * q_share / 2^32 is then q_blocks exactly, for grid < 2^32
+  const uint64_t q_share = (((uint64_t)q_blocks << 32) + grid - 1) / grid;
   auto kernel = passes == 1   ? append_pages_kernel<D, kF8, 1, 256>
                 : most == 256 ? append_pages_kernel<D, kF8, 2, 256>
                               : append_pages_kernel<D, kF8, 2, 512>;
-  return launch_ahead(kernel, dim3(grid), threads, 0, stream, p, kv_blocks, q_shift, q_groups);
+  return launch_ahead(kernel, dim3(grid), threads, 0, stream, p, q_share, q_shift, q_groups);
 }
 
 }  // namespace
