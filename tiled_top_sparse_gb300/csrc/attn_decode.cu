@@ -1047,90 +1047,98 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
-// Joins the parts of the units that CTA borders cut: block (c, row) for one row of the unit that
-// ended in CTA c. Four warps take every fourth part each, kBatch parts' loads in flight (a unit
-// of one long request may have hundreds), then the warps' results are joined in order.
-template <int D>
+// Joins the parts of the units that CTA borders cut: block (c, y) for rows y, y + kJoinRows, ..
+// of the unit that ended in CTA c (with a block for each of 64 rows most blocks are empty: 4
+// requests x 3000 keys, 40 rows 25 -> 20 us). Four warps take every fourth part each, kBatch
+// parts' loads in flight (a unit of one long request may have hundreds), then the warps'
+// results are joined in order.
+constexpr int kJoinRows = 16;
+template <int D, bool kMany>  // kMany: more rows than that
 __global__ void __launch_bounds__(128) attn_decode_join_kernel(const Params p, float bias) {
   constexpr int kWarps = 4, kBatch = 4;
   const int R = p.unit_rows;
   __shared__ float2 s_ml[kWarps];
   __shared__ float4 s_acc[kWarps][D / 4];
-  const int c1 = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c1 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_prior_grids();  // the parts are written
   const int4 job = p.jobs[c1];
   const int q0 = p.job_q0[c1];
-  if (job.x < 0 || row >= job.y) return;
+  if (job.x < 0 || (int)blockIdx.y >= job.y) return;
   const bool mine = lane < D / 4;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  float top = -INFINITY, sum = 0.f;
-  float4 acc = zero;
-  for (int c = job.x + warp; c <= c1; c += kWarps * kBatch) {
-    float2 ml[kBatch];
-    float4 v[kBatch];
+  for (int row = blockIdx.y; row < job.y; row += kJoinRows) {
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = zero;
+    for (int c = job.x + warp; c <= c1; c += kWarps * kBatch) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int cc = c + i * kWarps;
-      ml[i] = make_float2(-INFINITY, 0.f);
-      v[i] = zero;
-      if (cc <= c1) {
-        const float* part = p.parts + (size_t)(2 * cc + (cc == job.x ? 1 : 0)) * (R * (D + 2));
-        ml[i] = *reinterpret_cast<const float2*>(part + R * D + 2 * row);
-        if (mine) v[i] = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
+      for (int i = 0; i < kBatch; ++i) {
+        const int cc = c + i * kWarps;
+        ml[i] = make_float2(-INFINITY, 0.f);
+        v[i] = zero;
+        if (cc <= c1) {
+          const float* part = p.parts + (size_t)(2 * cc + (cc == job.x ? 1 : 0)) * (R * (D + 2));
+          ml[i] = *reinterpret_cast<const float2*>(part + R * D + 2 * row);
+          if (mine) v[i] = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
+        }
+      }
+      float n = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) n = fmaxf(n, ml[i].x);
+      const float f = top == -INFINITY ? 0.f : ex2_approx(top - n);
+      top = n;
+      sum *= f;
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float fi = ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - n);
+        sum = fmaf(ml[i].y, fi, sum);
+        acc.x = fmaf(v[i].x, fi, acc.x);
+        acc.y = fmaf(v[i].y, fi, acc.y);
+        acc.z = fmaf(v[i].z, fi, acc.z);
+        acc.w = fmaf(v[i].w, fi, acc.w);
       }
     }
-    float n = top;
+    if (lane == 0) s_ml[warp] = make_float2(top, sum);
+    if (mine) s_acc[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0) {
+      float m = -INFINITY, l = 0.f;
+      float4 o = zero;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) n = fmaxf(n, ml[i].x);
-    const float f = top == -INFINITY ? 0.f : ex2_approx(top - n);
-    top = n;
-    sum *= f;
-    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w].x);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const float fi = ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - n);
-      sum = fmaf(ml[i].y, fi, sum);
-      acc.x = fmaf(v[i].x, fi, acc.x);
-      acc.y = fmaf(v[i].y, fi, acc.y);
-      acc.z = fmaf(v[i].z, fi, acc.z);
-      acc.w = fmaf(v[i].w, fi, acc.w);
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = s_ml[w];
+        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+        l = fmaf(ml.y, f, l);
+        if (mine) {
+          const float4 v = s_acc[w][lane];
+          o.x = fmaf(v.x, f, o.x);
+          o.y = fmaf(v.y, f, o.y);
+          o.z = fmaf(v.z, f, o.z);
+          o.w = fmaf(v.w, f, o.w);
+        }
+      }
+      const int rr = job.z + row, tok = rr / p.group;
+      const int64_t at = (int64_t)(q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      if (mine) {
+        if (p.out_bf16) {
+          uint2* to = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane;
+          *to = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        } else {
+          reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[lane] =
+              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        }
+      }
+      if (p.lse != nullptr && lane == 0)
+        p.lse[at] = l > 0.f ? (m - bias + log2f(l)) * kLn2 : -INFINITY;
     }
+    if (!kMany) return;
+    if (row + kJoinRows < job.y) __syncthreads();  // before the next row's results
   }
-  if (lane == 0) s_ml[warp] = make_float2(top, sum);
-  if (mine) s_acc[warp][lane] = acc;
-  __syncthreads();
-  if (warp != 0) return;
-  float m = -INFINITY, l = 0.f;
-  float4 o = zero;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w].x);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const float2 ml = s_ml[w];
-    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-    l = fmaf(ml.y, f, l);
-    if (mine) {
-      const float4 v = s_acc[w][lane];
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
-    }
-  }
-  const int rr = job.z + row, tok = rr / p.group;
-  const int64_t at = (int64_t)(q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  if (mine) {
-    if (p.out_bf16) {
-      uint2* to = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane;
-      *to = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    } else {
-      reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[lane] =
-          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    }
-  }
-  if (p.lse != nullptr && lane == 0)
-    p.lse[at] = l > 0.f ? (m - bias + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Rows of a unit: the least of 8, 16, 32 and 64 that holds a request's rows of one KV head (64
@@ -1200,7 +1208,9 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   e = launch_ahead(attn_decode_kernel<F8, D, NT, kGroups>, dim3(p.ctas), kThreads, C::kSmemBytes,
                    stream, mk, mv, p);
   if (e != cudaSuccess) return e;
-  return launch_ahead(attn_decode_join_kernel<D>, dim3(p.ctas, p.unit_rows), 128, 0, stream, p,
+  const bool many = p.unit_rows > kJoinRows;
+  return launch_ahead(many ? attn_decode_join_kernel<D, true> : attn_decode_join_kernel<D, false>,
+                      dim3(p.ctas, many ? kJoinRows : p.unit_rows), 128, 0, stream, p,
                       F8 ? 11.f : 0.f);
 }
 
