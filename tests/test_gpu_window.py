@@ -36,13 +36,14 @@ def inputs(seed, lq, lk, hq, hkv, d, dtype, tail=0):
 
 
 def check(tts, seed, lq, lk, hq, hkv, d, window, sinks, dtype=torch.bfloat16,
-          out_dtype=torch.float32, tail=5):
+          out_dtype=torch.float32, tail=5, out_at=0):
     lk = lq if lk is None else lk
     q, k, v = inputs(seed, lq, lk, hq, hkv, d, dtype, tail)
     cq, ck = cum(lq), cum(lk)
     T = int(cq[-1])
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out = torch.full(q.shape, 7.0, dtype=out_dtype, device="cuda")
+    flat = torch.full((out_at + q.numel() + 64,), 7.0, dtype=out_dtype, device="cuda")
+    out = flat[out_at:out_at + q.numel()].view(q.shape)
     lse = torch.full(q.shape[:2], 7.0, device="cuda")
 
     def call():
@@ -64,6 +65,7 @@ def check(tts, seed, lq, lk, hq, hkv, d, window, sinks, dtype=torch.bfloat16,
     err = np.abs(o[:T] - ro)
     assert np.all(err <= tol), (err - tol).max()
     assert (o[T:] == 7).all() and (l[T:] == 7).all()
+    assert bool((flat[:out_at] == 7).all()) and bool((flat[out_at + q.numel():] == 7).all())
     a, b = out.clone(), lse.clone()
     call()
     assert torch.equal(a, out) and torch.equal(b, lse)
@@ -89,6 +91,48 @@ def test_window_parity(tts, d, lq, lk, hq, hkv, window, sinks):
 def test_bf16_out_and_fp32_in(tts, d):
     check(tts, 5, [333, 70], None, 4, 2, d, 96, 4, out_dtype=torch.bfloat16)
     check(tts, 6, [333, 70], None, 4, 2, d, 96, 4, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_rows_that_end_inside_a_store(tts, d, out_dtype):
+    """Rows leave 32 at a time: lengths around multiples of 32 and 128, an output that begins at 16
+    bytes of a line, with few and with many items per CTA."""
+    at = 4 if out_dtype == torch.float32 else 8
+    check(tts, 20, [1, 31, 32, 33, 127, 128, 129, 159, 160], None, 4, 2, d, 70, 2,
+          out_dtype=out_dtype, out_at=at)
+    check(tts, 21, [481, 672, 95, 800, 1], None, 24, 6, d, 150, 9, out_dtype=out_dtype, out_at=at)
+    check(tts, 22, [481, 95, 64], [490, 30, 700], 15, 5, d, 150, 9, out_dtype=out_dtype, tail=0)
+
+
+def test_captured(tts):
+    """Two graphs of windowed calls with workspaces of their own, replayed in turn and over new
+    inputs, give what the calls give."""
+    cases = []
+    for lens, hq, d in (([700], 4, 64), ([900, 300, 411], 32, 128)):
+        q, k, v = inputs(23, lens, lens, hq, 2, d, torch.bfloat16)
+        cu = torch.tensor(cum(lens)).cuda()
+        out, lse = torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+        ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+
+        def call(q=q, k=k, v=v, cu=cu, lens=lens, d=d, out=out, lse=lse, ws=ws):
+            tts.attn_fwd_varlen_window(q, k, v, cu, cu, max(lens), max(lens), 200, 4, d ** -0.5,
+                                       out=out, lse=lse, workspace=ws)
+
+        call()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        cases.append((g, call, q, out, lse))
+    for turn in range(3):
+        for g, call, q, out, lse in cases:
+            q.copy_(torch.roll(q, turn + 1, 0))
+            out.fill_(7)
+            g.replay()
+        for g, call, q, out, lse in cases:
+            a, b = out.clone(), lse.clone()
+            call()
+            assert torch.equal(a, out) and torch.equal(b, lse)
 
 
 def test_many_items_per_cta(tts):
