@@ -36,11 +36,17 @@
 // window + sinks) whatever the prompt's length. Rows of a last tile behind the sequence's
 // end (another sequence's, or padding) are cleared in V before the product, so that what
 // they hold cannot reach a row through a weight of zero.
-// Measured: 16,000 tokens, window 4096, 16 / 4 heads of 128: 325 us, 1.48 PFLOP/s over visible
-// pairs (0.77 of the measured bf16 rate); four prompts of 827 to 3212 tokens, window 1024, 32 / 8
-// heads: 116 us, 0.82 PFLOP/s (ten tiles for the keys of eight: the sinks' tile and two at the
-// window's ends, whose masks cost half a tile more; 6.4 items per CTA, each with an epilogue);
-// 700 tokens, window 256, 8 / 2 heads of 64: 12 us, five tiles' chain of 1.8 us each.
+// What differs from the kernel without a window, because its items are short: the producer hands the
+// decoded item on; registers move to the softmax warps; the products with a tile's first 64
+// weights start while the others are computed; rows leave by TMA stores; and the code is kept
+// small, since an item runs once through all of it and what the instruction cache misses is a
+// fifth of the softmax warps' time.
+// Measured: 16,000 tokens, window 4096, 128 sinks, 16 / 4 heads of 128: 302 to 314 us, 1.53 to 1.59
+// PFLOP/s over visible pairs (0.80 to 0.83 of the measured bf16 rate; 1.27 us per pair of tiles, the
+// tensor core's rate, and 3 us per item); four prompts of 827 to 3212 tokens, window 1024, 32 / 8
+// heads: 101 us, 0.94 PFLOP/s (ten tiles for the keys of eight: the sinks' tile and two at the
+// window's ends, whose masks add to each; 6.4 items per CTA at 3 us each); 700 tokens, window 256,
+// 8 / 2 heads of 64: 10.4 us, launch, five tiles' chain of 1.3 us each, and the rows' store.
 #include <cstdint>
 #include <type_traits>
 
@@ -131,7 +137,7 @@ struct WindowParams : AttnParams {
   // What the two query tiles of an item are. kHeads: two heads of a KV group on the same 128
   // rows (an even group): both see the same keys, where two tiles of consecutive rows (kRows,
   // an odd group) stream one tile more than each needs (ragged batch, window 1024: 213 -> 116
-  // us with the bit masks). kSolo: one tile alone, where all of them fit the GPU at once: a
+  // us, with the masks as words). kSolo: one tile alone, where all of them fit the GPU at once: a
   // tile's chain is shorter without a second tile's between its steps.
   enum Pairing : int { kRows, kHeads, kSolo };
   int pairing;
