@@ -186,6 +186,17 @@ def test_wide_window_equals_causal(tts, d):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_bounds_far_above_the_lengths(tts):
+    """max_seqlen_q and max_seqlen_k are bounds: the largest int gives what the lengths give."""
+    top = 2 ** 31 - 1
+    for lens, hq, hkv, d in (([300, 129], 4, 2, 64), ([900, 411], 32, 8, 128), ([700, 500], 15, 5, 80)):
+        q, k, v = inputs(24, lens, lens, hq, hkv, d, torch.bfloat16)
+        cu = torch.tensor(cum(lens)).cuda()
+        a = tts.attn_fwd_varlen_window(q, k, v, cu, cu, max(lens), max(lens), 200, 3, d ** -0.5)
+        b = tts.attn_fwd_varlen_window(q, k, v, cu, cu, top, top, 200, 3, d ** -0.5)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_bad_sequences_are_reported(tts):
     q, k, v = inputs(10, [100, 100], [100, 100], 2, 1, 64, torch.bfloat16)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")

@@ -1143,7 +1143,10 @@ cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
     p.window = a.window;
     p.sinks = a.sinks;
     p.out_bf16 = a.out_bf16 ? 1 : 0;
-    const int tiles = (a.max_seqlen_q + kBlockM - 1) / kBlockM;
+    // the bound may be any int; no sequence is longer than all rows
+    const int64_t longest = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
+    const int tiles = (int)((longest + kBlockM - 1) / kBlockM);
+    p.pairs_max = (tiles + 1) / 2;
     p.pairing = (int64_t)a.batch * tiles * a.hq <= sms ? WindowParams::kSolo
                 : (a.hq / a.hkv) % 2 == 0              ? WindowParams::kHeads
                                                        : WindowParams::kRows;
