@@ -35,6 +35,7 @@
 // of 16 requests over a bf16 cache 65.5 us (52.7). Many rows are bound by what each warp issues:
 // 16, 32 and 64 rows per KV head take 1.6, 2.2 and 3.8 times the bytes' time in e4m3 and 1.1,
 // 1.3 and 2.0 in bf16 (16 requests x 20000 tokens, 4 KV heads).
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -1152,7 +1153,7 @@ size_t job_bytes(size_t ctas) {
 }
 
 template <bool F8, int D, int NT, bool kGroups>
-cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t stream) {
+cudaError_t launch(const AttnDecodeArgs& a, int dev, int sms, int* drv_err, cudaStream_t stream) {
   using C = Cfg<F8, D, NT>;
   Params p;
   p.q = static_cast<const uint16_t*>(a.q);
@@ -1202,12 +1203,23 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
   };
   if (!make(&mk, const_cast<void*>(a.k_cache)) || !make(&mv, const_cast<void*>(a.v_cache)))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<F8, D, NT, kGroups>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  if (e != cudaSuccess) return e;
+  // The kernel's shared-memory limit is set once per device (bit i: device i), not per call: 0.8 of
+  // the 9 us that a small call takes the host. A launch that fails has it set again.
+  static std::atomic<uint64_t> set{0};
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  cudaError_t e = cudaSuccess;
+  if (!(set.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(attn_decode_kernel<F8, D, NT, kGroups>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   e = launch_ahead(attn_decode_kernel<F8, D, NT, kGroups>, dim3(p.ctas), kThreads, C::kSmemBytes,
                    stream, mk, mv, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess) {
+    set.fetch_and(~bit, std::memory_order_relaxed);
+    return e;
+  }
   const bool many = p.unit_rows > kJoinRows;
   return launch_ahead(many ? attn_decode_join_kernel<D, true> : attn_decode_join_kernel<D, false>,
                       dim3(p.ctas, many ? kJoinRows : p.unit_rows), 128, 0, stream, p,
@@ -1215,11 +1227,12 @@ cudaError_t launch(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t 
 }
 
 template <bool F8, int D>
-cudaError_t launch_nt(const AttnDecodeArgs& a, int sms, int* drv_err, cudaStream_t stream) {
+cudaError_t launch_nt(const AttnDecodeArgs& a, int dev, int sms, int* drv_err,
+                      cudaStream_t stream) {
   switch (rows_of(a.max_q, a.hq / a.hkv)) {
-    case 8: return launch<F8, D, 1, false>(a, sms, drv_err, stream);
-    case 16: return launch<F8, D, 2, false>(a, sms, drv_err, stream);
-    default: return launch<F8, D, 2, true>(a, sms, drv_err, stream);
+    case 8: return launch<F8, D, 1, false>(a, dev, sms, drv_err, stream);
+    case 16: return launch<F8, D, 2, false>(a, dev, sms, drv_err, stream);
+    default: return launch<F8, D, 2, true>(a, dev, sms, drv_err, stream);
   }
 }
 
@@ -1236,11 +1249,11 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs& a, int* drv_err, cudaStream
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   if (a.d == 64)
-    return a.f8 ? launch_nt<true, 64>(a, sms, drv_err, stream)
-                : launch_nt<false, 64>(a, sms, drv_err, stream);
+    return a.f8 ? launch_nt<true, 64>(a, dev, sms, drv_err, stream)
+                : launch_nt<false, 64>(a, dev, sms, drv_err, stream);
   if (a.d == 128)
-    return a.f8 ? launch_nt<true, 128>(a, sms, drv_err, stream)
-                : launch_nt<false, 128>(a, sms, drv_err, stream);
+    return a.f8 ? launch_nt<true, 128>(a, dev, sms, drv_err, stream)
+                : launch_nt<false, 128>(a, dev, sms, drv_err, stream);
   return cudaErrorInvalidValue;
 }
 
