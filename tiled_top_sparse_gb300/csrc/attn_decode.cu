@@ -278,6 +278,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   volatile int* abort_flag = &s_abort;
   volatile int* issued_tiles = &s_issued;
 
+  if (tid == kNW * 32) {  // on their way while the lengths are read
+    prefetch_tmap(&map_k);
+    prefetch_tmap(&map_v);
+  }
   wait_for_prior_grids();
   // ---- this CTA's run [t0, t1) of the list of tiles, and the request it begins in
   uint32_t bad = 0;

@@ -437,16 +437,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
   volatile int* item_slot = s_item;
-  if constexpr (kWin) wait_for_prior_grids();
+  if constexpr (kWin) {
+    if (tid == 64) {  // on their way while the first item is found
+      prefetch_tmap(&maps.q);
+      prefetch_tmap(&maps.k);
+      prefetch_tmap(&maps.v);
+      prefetch_tmap(&maps.o);
+    }
+    wait_for_prior_grids();
+  }
 
   if (warp < 4) {
   if constexpr (kWin) give_registers<kIssueRegs>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      prefetch_tmap(&maps.q);
-      prefetch_tmap(&maps.k);
-      prefetch_tmap(&maps.v);
+      if constexpr (!kWin) {
+        prefetch_tmap(&maps.q);
+        prefetch_tmap(&maps.k);
+        prefetch_tmap(&maps.v);
+      }
       int ni = 0, nq = 0, gt = 0;
       bool own = true;  // without a counter: this CTA's item is still to come
       int last_k[NS], last_v[NS];  // latest tile armed on each ring slot (-1: none)
