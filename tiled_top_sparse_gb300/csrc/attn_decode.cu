@@ -30,9 +30,9 @@
 // Measured (32 / 8 heads of 128, CUDA graph): 64 requests x 32768 tokens in e4m3 616 to 632 us
 // from box to box (6.8 to 7.0 TB/s, 1.00 to 1.03 of the measured copy rate), one request of
 // 2590 tokens 8.9 us (the chain of launch, lengths, page table, tile, products and the parts'
-// launch; its bytes are 0.8 us), 33 ragged requests with a window of 4096 53.6 us (39.4 us of
+// launch; its bytes are 0.8 us), 33 ragged requests with a window of 4096 53.4 us (39.4 us of
 // bytes; about 2.5 us before the first tile, 3 for the parts, and the last CTAs), 1 to 4 tokens
-// of 16 requests over a bf16 cache 65.5 us (52.7). Many rows are bound by what each warp issues:
+// of 16 requests over a bf16 cache 64.2 us (52.7). Many rows are bound by what each warp issues:
 // 16, 32 and 64 rows per KV head take 1.6, 2.2 and 3.8 times the bytes' time in e4m3 and 1.1,
 // 1.3 and 2.0 in bf16 (16 requests x 20000 tokens, 4 KV heads).
 #include <atomic>
@@ -53,7 +53,8 @@ constexpr int kThreads = (kNW + 1) * 32;      // and one producer warp
 constexpr int kCtasPerSm = 2;
 // What the end of a unit costs (joining the warps, the next unit's q), in tiles: the list that
 // is cut into runs has this many empty places behind a unit's tiles, so that a run over many
-// short units is not the last to finish.
+// short units is not the last to finish (33 ragged requests, window 4096, pages of 64: 57.9 us
+// without, 51.8 with).
 constexpr int kEndTiles = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
