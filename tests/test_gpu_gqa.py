@@ -613,6 +613,30 @@ def test_rows_in_front_of_the_first_request(tts, front):
     run_decode(tts, 151, [1, 2, 0, 3], [300, 65, 40, 3], 8, 2, 128, 64, True, front=front)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("f8", [True, False])
+def test_units_of_mixed_rows(tts, d, f8):
+    """Requests of 1 to 64 new tokens side by side: a CTA goes from units of one number of row
+    groups to another's, over and over; every call gives the same bits."""
+    g = gen(160)
+    new = torch.randint(0, 65, (60,), generator=g).tolist()
+    new[::3] = [min(n, 5) for n in new[::3]]
+    kv = [max(n, int(x)) for n, x in zip(new, torch.randint(1, 200, (60,), generator=g))]
+    run_decode(tts, 161, new, kv, 10, 2, d, 64, f8, max_q=64)
+    tables, pages = make_tables(162, kv, 64)
+    kc, ks, vc, vs = [None if t is None else dev(t) for t in make_pool(163, pages, 2, 64, d, f8)]
+    q = dev(torch.randn(sum(new), 10, d, generator=g).to(torch.bfloat16))
+    cu, lens = dev(torch.tensor(cum(new))), dev(torch.tensor(kv, dtype=torch.int32))
+    tables = dev(tables)
+    first = None
+    for _ in range(300):
+        got = tts.attn_decode_paged(q, kc, vc, tables, lens, 0.1, cu_seqlens_q=cu,
+                                    max_seqlen_q=64, k_scale=ks, v_scale=vs)
+        if first is None:
+            first = got
+        assert torch.equal(first[0], got[0]) and torch.equal(first[1], got[1])
+
+
 def test_calls_on_two_streams(tts):
     """Two decode calls in flight at once, each with a workspace of its own."""
     d, ps, hkv, kv = 128, 64, 2, [9000, 500]

@@ -1038,11 +1038,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
       group_sync();  // before the next unit's references and sums
     };
+    [[maybe_unused]] int last = 0;  // row groups of the part before
     while (left > 0) {
       int g, rt, x0, x1;
       const int before = t1 - left;
       if (!next_seg(g, rt, x0, x1)) continue;
       const int rows = kGroups ? min(r.n * p.group - rt * p.unit_rows, p.unit_rows) : 0;
+      if constexpr (kGroups) {
+        // Groups of another size lay their q rows and accumulators over one another's: all warps
+        // must be done with the part before (each group waits only for its own warps there).
+        const int groups = rows > 2 * GR ? 4 : rows > GR ? 2 : 1;
+        if (last != 0 && groups != last) named_barrier_sync(1, kNW * 32);
+        last = groups;
+      }
       if (rows > 2 * GR)
         segment(std::integral_constant<int, kGroups ? 4 : 1>(), g, rt, x0, x1, before);
       else if (rows > GR)
