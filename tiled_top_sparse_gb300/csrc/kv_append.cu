@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(128) append_steps_kernel(const KvAppendArgs p,
                                  hh >= p.hkv, lane, 32, nullptr);
     return;
   }
+  if (p.q == nullptr) return;  // the last block's spare warps: there are no q heads to divide by
   const int64_t row = (w - kv_warps) * (32 / kTpr) + lane / kTpr;
   const int h = (int)(row % p.hq);
   const int64_t bi = row / p.hq;
