@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import gqa_ref as ref
-from test_gpu_gqa import cum, dev, gen, make_pool, make_tables, run_append
+from test_gpu_gqa import F16_HALF, cum, dev, gen, make_pool, make_tables, run_append
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,42 @@ def test_append_step_without_q_reads_no_bounds_in_front(tts):
     np.testing.assert_array_equal(ref.codes_of(c[0]), want[2])
     np.testing.assert_array_equal(ref.codes_of(c[2]), want[3])
     np.testing.assert_array_equal(c[1].cpu().numpy(), want[4].astype(np.float32))
+
+
+# ------------------------------------------------------------------------------- decode
+@pytest.mark.parametrize("tiny", [1e-40, 2.0 ** -149, 2.0 ** -128])
+@pytest.mark.parametrize("new,kv,hq,hkv,d,ps,window,sinks", [
+    ([1, 1], [20, 70], 8, 2, 128, 16, 0, 0),            # pages behind the end, inside its tile
+    ([1, 1], [1, 33], 4, 2, 128, 32, 0, 0),
+    ([1], [60], 4, 1, 64, 64, 0, 0),                    # two pages of 64 to a tile
+    ([1, 1], [500, 300], 8, 2, 128, 16, 30, 4),         # between the first tokens and the window
+    ([3, 2], [90, 700], 8, 2, 64, 16, 70, 1),
+    ([6, 1], [300, 40], 16, 2, 128, 16, 50, 0),         # row groups
+])
+def test_decode_scales_of_unseen_pages(tts, tiny, new, kv, hq, hkv, d, ps, window, sinks):
+    """Table entries without a visible key name a page of the pool that was never written: its
+    scales are subnormal (small integers read as fp32), its codes NaN."""
+    tables, pages = make_tables(sum(kv), kv, ps)
+    kc, ks, vc, vs = make_pool(220, pages + 1, hkv, ps, d, True)
+    ks[pages], vs[pages] = tiny, tiny
+    kc[pages], vc[pages] = 0x7F, 0x7F
+    tables = torch.cat([tables, torch.full((len(kv), 8), -1, dtype=torch.int32)], 1)
+    for r, L in enumerate(kv):
+        lo = max(0, L - new[r] + 1 - window) if window > 0 else 0
+        for a in range(tables.shape[1]):
+            j = np.arange(a * ps, (a + 1) * ps)
+            if not ((j < L) & ((j >= lo) | (j < sinks))).any():
+                tables[r, a] = pages
+    cu = cum(new)
+    q = torch.randn(int(cu[-1]), hq, d, generator=gen(221)).to(torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = tts.attn_decode_paged(
+        dev(q), dev(kc), dev(vc), dev(tables), dev(torch.tensor(kv, dtype=torch.int32)), d ** -0.5,
+        cu_seqlens_q=dev(torch.tensor(cu)), max_seqlen_q=max(new), k_scale=dev(ks), v_scale=dev(vs),
+        window=window, sinks=sinks, status=st)
+    assert int(st.item()) == 0
+    ro, rl, tol, tol_l = ref.attend(q.float().numpy(), ref.codes_of(kc), ref.codes_of(vc),
+                                    ks.numpy(), vs.numpy(), tables.numpy(), kv, cu, d ** -0.5,
+                                    window, sinks, F16_HALF)
+    assert np.all(np.abs(out.cpu().numpy() - ro) <= tol)
+    assert np.all(np.abs(lse.cpu().numpy() - rl) <= tol_l)

@@ -450,9 +450,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           const bool good = there && ((all >> at) & 1u);
           if (there && !good) flag |= kDevBadArg;  // no scale of a written page: keys skipped
           use = __ballot_sync(0xFFFFFFFFu, good);
-          pk = __shfl_sync(0xFFFFFFFFu, ks, at);
-          pl = __shfl_sync(0xFFFFFFFFu, vl, at);
-          pi = __shfl_sync(0xFFFFFFFFu, vi, at);
+          // Pieces that are not used stay neutral: their page's scales may be anything (an inverse
+          // of infinity times a weight of zero is NaN).
+          const float k_of = __shfl_sync(0xFFFFFFFFu, ks, at), l_of = __shfl_sync(0xFFFFFFFFu, vl, at),
+                      i_of = __shfl_sync(0xFFFFFFFFu, vi, at);
+          pk = good ? k_of : 1.f;
+          pl = good ? l_of : 0.f;
+          pi = good ? i_of : 0.f;
         };
         if (F8 && !new_scales) scales();
         // All of the above may be done before the slot is free; little is left behind the wait.
