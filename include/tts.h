@@ -435,9 +435,9 @@ tts_status tts_rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads
  *             not read, and their out / lse rows are left as they were
  * max_seqlen_q  host upper bound of n_r, 1 .. 64 (longer: TTS_ERR_UNSUPPORTED; prompts go
  *             through tts_attn_fwd_varlen_window); a longer request is flagged and skipped
- * k_cache .. page_size, page_tables, max_pages: as tts_rope_kv_append. k_scale / v_scale may
- *             hold any positive finite values (others: TTS_DEV_BAD_ARG, the page's keys are
- *             skipped); NULL for a bf16 cache.
+ * k_cache .. page_size, page_tables, max_pages: as tts_rope_kv_append. k_scale may hold any
+ *             positive finite values, v_scale finite ones of at least 2^-80, the denominator's
+ *             range (others: TTS_DEV_BAD_ARG, the page's keys are skipped); NULL for a bf16 cache.
  * kv_lens     device int32 [batch], the new tokens included; an entry outside
  *             [0, max_pages * page_size] reads as 0 and sets TTS_DEV_INDEX_RANGE, and so
  *             does a page outside [0, num_pages) with visible keys, which are skipped

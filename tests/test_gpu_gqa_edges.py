@@ -1,4 +1,6 @@
 """GPU tests of the grouped-query calls at the edges of what their documentation allows."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -94,3 +96,59 @@ def test_decode_scales_of_unseen_pages(tts, tiny, new, kv, hq, hkv, d, ps, windo
                                     window, sinks, F16_HALF)
     assert np.all(np.abs(out.cpu().numpy() - ro) <= tol)
     assert np.all(np.abs(lse.cpu().numpy() - rl) <= tol_l)
+
+
+@pytest.mark.parametrize("low,high,L", [(-80, -80, 40000), (-80, -60, 500), (-80, 20, 500),
+                                        (0, 100, 500), (100, 100, 3000)])
+def test_decode_value_scales_at_the_bounds(tts, low, high, L):
+    """Value scales down to 2^-80 and pages 2^100 apart. The scale's log2 rides in the score, up to
+    2^7 in size, so what is rounded there is rounded to half a step of 2^-17: the score with it, and
+    log2 itself to one step. Both move a weight by a factor of 2^(3 x 2^-18) at most, once in the
+    result's numerator and once in its denominator. lse adds the reference less its bias (half a
+    step) and log2 of the sum (one step)."""
+    d, ps, hkv = 64, 16, 1
+    tables, pages = make_tables(230, [L], ps)
+    kc, ks, vc, vs = make_pool(231, pages, hkv, ps, d, True)
+    e = torch.randint(low, high + 1, vs.shape, generator=gen(232))
+    e[0], e[1] = low, high
+    # 1.5 times a power of two, the smallest exactly at the bound
+    vs = torch.exp2(e.double()).float() * torch.where(e == low, 1.0, 1.5)
+    q = torch.randn(1, 4, d, generator=gen(233)).to(torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = tts.attn_decode_paged(dev(q), dev(kc), dev(vc), dev(tables),
+                                     torch.tensor([L], dtype=torch.int32, device="cuda"),
+                                     d ** -0.5, k_scale=dev(ks), v_scale=dev(vs), status=st)
+    assert int(st.item()) == 0
+    ro, rl, tol, tol_l = ref.attend(q.float().numpy(), ref.codes_of(kc), ref.codes_of(vc),
+                                    ks.numpy(), vs.numpy(), tables.numpy(), [L], cum([1]),
+                                    d ** -0.5, 0, 0, F16_HALF)
+    move = math.log(2) * 3 * 2.0 ** -18
+    # tol's first part is at least F16_HALF of sum p|v| / l: its size, to add the factor to
+    tol = tol * (1 + 2 * move / F16_HALF)
+    assert np.all(np.abs(out.cpu().numpy() - ro) <= tol)
+    assert np.all(np.abs(lse.cpu().numpy() - rl) <= tol_l + 2 * move)
+
+
+@pytest.mark.parametrize("bad", [2.0 ** -81, 2.0 ** -118, 2.0 ** -130, 2.0 ** -149])
+def test_decode_value_scale_below_the_bound(tts, bad):
+    """A value scale too small for the denominator's range is reported and its page's keys are
+    skipped, like a scale that is not positive; a request of such pages alone sees no key."""
+    d, ps, hkv, kv = 128, 32, 2, [300, 200, 1]
+    tables, pages = make_tables(240, kv, ps)
+    kc, ks, vc, vs = make_pool(241, pages, hkv, ps, d, True)
+    gone = [int(tables[0, 3]), int(tables[2, 0])]
+    for pg in gone:
+        vs[pg] = bad
+    q = torch.randn(3, 4, d, generator=gen(242)).to(torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = tts.attn_decode_paged(dev(q), dev(kc), dev(vc), dev(tables),
+                                     dev(torch.tensor(kv, dtype=torch.int32)), d ** -0.5,
+                                     k_scale=dev(ks), v_scale=dev(vs), status=st)
+    assert int(st.item()) == tts.TTS_DEV_BAD_ARG
+    ro, rl, tol, tol_l = ref.attend(q.float().numpy(), ref.codes_of(kc), ref.codes_of(vc),
+                                    ks.numpy(), vs.numpy(), tables.numpy(), kv, cum([1, 1, 1]),
+                                    d ** -0.5, 0, 0, F16_HALF, lambda pg: pg in gone)
+    assert np.all(np.abs(out.cpu().numpy() - ro) <= tol)
+    l = lse.cpu().numpy()
+    assert np.array_equal(np.isneginf(l), np.isneginf(rl)) and np.isneginf(l[2]).all()
+    assert np.all(np.abs(l[:2] - rl[:2]) <= tol_l[:2])

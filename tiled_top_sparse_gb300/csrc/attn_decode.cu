@@ -56,6 +56,9 @@ constexpr int kCtasPerSm = 2;
 // short units is not the last to finish (33 ragged requests, window 4096, pages of 64: 57.9 us
 // without, 51.8 with).
 constexpr int kEndTiles = 3;
+// Smallest value scale: a key adds a weight of at most 2^15 over its scale to the denominator, which
+// for 2^30 keys then stays under 2^125. The append writes none below 2^-60.
+constexpr float kMinValueScale = 0x1p-80f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // cache_g) in registers, loaded 32 pages at a time.
     constexpr uint32_t kBox = C::kPanelBytes;
     int cache_b = -1, cache_at = 0, cache_g = -1, page = -1;
-    bool fine = true;                    // the page's scales are positive and finite
+    bool fine = true;                    // the page's scales are in range
     float ks = 1.f, vl = 0.f, vi = 1.f;  // key scale, log2 and inverse of the value scale
     bool ok = true;
     while (ok && left > 0) {
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if constexpr (F8) {
           if (new_scales) {
             cache_g = g;
-            fine = sk > 0.f && sk < INFINITY && sv > 0.f && sv < INFINITY;
+            fine = sk > 0.f && sk < INFINITY && sv >= kMinValueScale && sv < INFINITY;
             ks = sk;
             vl = fine ? log2f(sv) : 0.f;
             vi = fine ? 1.f / sv : 0.f;
