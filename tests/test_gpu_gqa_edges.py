@@ -59,6 +59,17 @@ def test_append_step_without_q_reads_no_bounds_in_front(tts):
     np.testing.assert_array_equal(c[1].cpu().numpy(), want[4].astype(np.float32))
 
 
+def test_append_refuses_an_empty_rotation_table(tts):
+    """A table without positions is not `no rotation`."""
+    tables, pages = make_tables(250, [10], 16)
+    kc, ks, vc, vs = [dev(t) for t in make_pool(251, pages, 1, 16, 64, True)]
+    x = dev(torch.randn(1, 1, 64, generator=gen(252)).to(torch.bfloat16))
+    with pytest.raises(ValueError):
+        tts.rope_kv_append(x, x, kc, vc, dev(tables), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                           torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 1, k_scale=ks,
+                           v_scale=vs, cos_sin=torch.empty(0, 32, 2, device="cuda"))
+
+
 # ------------------------------------------------------------------------------- decode
 @pytest.mark.parametrize("tiny", [1e-40, 2.0 ** -149, 2.0 ** -128])
 @pytest.mark.parametrize("new,kv,hq,hkv,d,ps,window,sinks", [

@@ -249,9 +249,9 @@ static PyObject* rope_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n
   int32_t max_new;
   if (int32_arg(a[7], "max_new", &max_new) < 0) return NULL;
   if (optional(a[10], "cos_sin", dev, d_f32, 3, &cs) < 0) return NULL;
-  if (cs.ptr != NULL || a[10] != Py_None) {
-    if (cs.shape[1] != d / 2 || cs.shape[2] != 2) {
-      refuse("cos_sin", "must be [max_pos, head_dim/2, 2]");
+  if (a[10] != Py_None) {  /* a table of no positions has a null address: not `no rotation` */
+    if (cs.shape[0] < 1 || cs.shape[1] != d / 2 || cs.shape[2] != 2) {
+      refuse("cos_sin", "must be [max_pos, head_dim/2, 2] with a position at least");
       return NULL;
     }
     max_pos = cs.shape[0];
