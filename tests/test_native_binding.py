@@ -82,3 +82,42 @@ def test_empty_rotation_table_is_refused(load):
     with pytest.raises(ValueError, match="cos_sin"):
         m.rope_kv_append(*append_args(cos_sin=Fake((0, 32, 2), F32, 0)))
     assert len(calls) == 2
+
+
+def decode_args(device=0, ptr=0x10000):
+    t = lambda shape, dtype: Fake(shape, dtype, ptr, device)  # noqa: E731
+    return [t((1, 4, 64), BF16), t((4, 2, 16, 64), BF16), t((4, 2, 16, 64), BF16), None, None,
+            t((1, 2), I32), t((1,), I32), None, 1, 0, 0, 0.1, t((1, 4, 64), F32), None,
+            t((1,), U8), None]
+
+
+def window_args(device=0, ptr=0x10000):
+    t = lambda shape, dtype: Fake(shape, dtype, ptr, device)  # noqa: E731
+    return [t((5, 4, 64), BF16), t((5, 2, 64), BF16), t((5, 2, 64), BF16), t((2,), I32),
+            t((2,), I32), 5, 5, 3, 1, 0.1, t((5, 4, 64), F32), None, t((1,), U8), None]
+
+
+CALLS = [("rope_kv_append", append_args), ("attn_decode_paged", decode_args),
+         ("attn_fwd_varlen_window", window_args)]
+
+
+@pytest.mark.parametrize("name,args", CALLS)
+def test_device_is_restored(load, name, args):
+    """The caller's device is current again after a call, also where the stream of the tensors'
+    device cannot be had; that error is the one that is raised."""
+    now = [0]
+    calls, keep, addr = counting()
+
+    def put(dev):
+        now[0] = dev
+
+    def no_stream(dev):
+        assert now[0] == 1
+        raise RuntimeError("no stream")
+
+    m = load((addr, addr, addr), get=lambda: now[0], put=put)
+    assert getattr(m, name)(*args(device=1)) == 0 and now[0] == 0 and len(calls) == 1
+    m = load((addr, addr, addr), stream=no_stream, get=lambda: now[0], put=put)
+    with pytest.raises(RuntimeError, match="no stream"):
+        getattr(m, name)(*args(device=1))
+    assert now[0] == 0 and len(calls) == 1

@@ -168,37 +168,44 @@ static int int32_arg(PyObject* o, const char* name, int32_t* out) {
   return fits32(v, name);
 }
 
-/* The current stream of `dev`, that device made current (*back: the one to restore, or -1). */
+static int make_current(long dev) {
+  PyObject* d = PyLong_FromLong(dev);
+  PyObject* r = d == NULL ? NULL : PyObject_CallOneArg(set_device, d);
+  Py_XDECREF(d);
+  Py_XDECREF(r);
+  return r == NULL ? -1 : 0;
+}
+/* The current stream of `dev`, that device made current (*back: the one to restore, or -1). Where
+ * that fails, the device that was current is so again. */
 static int enter(long dev, void** stream, long* back) {
   *back = -1;
   PyObject* now = PyObject_CallNoArgs(get_device);
   if (now == NULL) return -1;
   const long cur = PyLong_AsLong(now);
   Py_DECREF(now);
-  PyObject* d = PyLong_FromLong(dev);
-  if (d == NULL) return -1;
-  int ok = 0;
+  if (cur == -1 && PyErr_Occurred()) return -1;
   if (cur != dev) {
-    PyObject* r = PyObject_CallOneArg(set_device, d);
-    if (r == NULL) ok = -1;
-    Py_XDECREF(r);
+    if (make_current(dev) < 0) return -1;
     *back = cur;
   }
-  PyObject* s = ok == 0 ? PyObject_CallOneArg(raw_stream, d) : NULL;
-  Py_DECREF(d);
-  if (s == NULL) return -1;
+  PyObject* d = PyLong_FromLong(dev);
+  PyObject* s = d == NULL ? NULL : PyObject_CallOneArg(raw_stream, d);
+  Py_XDECREF(d);
+  if (s == NULL) {
+    if (*back >= 0) {
+      PyObject *type, *value, *trace;
+      PyErr_Fetch(&type, &value, &trace);
+      if (make_current(*back) < 0) PyErr_Clear();
+      PyErr_Restore(type, value, trace);
+    }
+    return -1;
+  }
   *stream = (void*)(uintptr_t)PyLong_AsUnsignedLongLongMask(s);
   Py_DECREF(s);
   return 0;
 }
 static PyObject* leave(long back, int status) {
-  if (back >= 0) {
-    PyObject* d = PyLong_FromLong(back);
-    PyObject* r = d == NULL ? NULL : PyObject_CallOneArg(set_device, d);
-    Py_XDECREF(d);
-    if (r == NULL) return NULL;
-    Py_DECREF(r);
-  }
+  if (back >= 0 && make_current(back) < 0) return NULL;
   return PyLong_FromLong(status);
 }
 
