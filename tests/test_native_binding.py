@@ -4,6 +4,8 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import shutil
+import threading
+import time
 
 import pytest
 
@@ -121,3 +123,34 @@ def test_device_is_restored(load, name, args):
     with pytest.raises(RuntimeError, match="no stream"):
         getattr(m, name)(*args(device=1))
     assert now[0] == 0 and len(calls) == 1
+
+
+@pytest.mark.parametrize("name,args", CALLS)
+def test_other_threads_run_during_a_call(load, name, args):
+    """A call that blocks (a full queue, a kernel's first load) leaves the interpreter to the other
+    threads. The stand-in is the C library's usleep, whose microseconds are the first tensor's
+    address (the append's is its q)."""
+    pause = 400000
+    addr = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+    m = load((addr, addr, addr))
+    a = args(ptr=pause)
+    if name == "rope_kv_append":
+        a[11] = a[12] = Fake((3, 4, 64), BF16, pause)
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.is_set():
+            ticks.append(time.monotonic())
+            time.sleep(0.001)
+
+    other = threading.Thread(target=tick)
+    other.start()
+    try:
+        begin = time.monotonic()
+        assert getattr(m, name)(*a) == 0
+        end = time.monotonic()
+    finally:
+        stop.set()
+        other.join()
+    assert end - begin >= 0.9e-6 * pause
+    assert any(begin + 0.1 < t < end - 0.1 for t in ticks)

@@ -292,11 +292,15 @@ static PyObject* rope_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n
   void* stream;
   long back;
   if (enter(dev, &stream, &back) < 0) return NULL;
-  return leave(back, f_append(tq.ptr, q_stride, (int32_t)hq, tk.ptr, k_stride, tv.ptr, v_stride,
-                              total, cu.ptr, past.ptr, (int32_t)batch, max_new, (int32_t)hkv,
-                              (int32_t)d, cs.ptr, (int32_t)max_pos, pt.ptr, (int32_t)pt.shape[1],
-                              c.k.ptr, c.v.ptr, c.ks.ptr, c.vs.ptr, c.code, (int32_t)c.k.shape[0],
-                              (int32_t)c.k.shape[2], qo.ptr, ko.ptr, st.ptr, stream));
+  tts_status status;
+  Py_BEGIN_ALLOW_THREADS  /* a launch may block */
+  status = f_append(tq.ptr, q_stride, (int32_t)hq, tk.ptr, k_stride, tv.ptr, v_stride, total,
+                    cu.ptr, past.ptr, (int32_t)batch, max_new, (int32_t)hkv, (int32_t)d, cs.ptr,
+                    (int32_t)max_pos, pt.ptr, (int32_t)pt.shape[1], c.k.ptr, c.v.ptr, c.ks.ptr,
+                    c.vs.ptr, c.code, (int32_t)c.k.shape[0], (int32_t)c.k.shape[2], qo.ptr, ko.ptr,
+                    st.ptr, stream);
+  Py_END_ALLOW_THREADS
+  return leave(back, status);
 }
 
 /* out and lse of an attention call on q [tokens, heads, d]. */
@@ -363,12 +367,16 @@ static PyObject* attn_decode_paged(PyObject* self, PyObject* const* a, Py_ssize_
   void* stream;
   long back;
   if (enter(dev, &stream, &back) < 0) return NULL;
-  return leave(back, f_decode(q.ptr, q.shape[0], cu.ptr, (int32_t)batch, max_q, (int32_t)q.shape[1],
-                              (int32_t)c.k.shape[1], (int32_t)d, c.k.ptr, c.v.ptr, c.ks.ptr,
-                              c.vs.ptr, c.code, (int32_t)c.k.shape[0], (int32_t)c.k.shape[2],
-                              pt.ptr, (int32_t)pt.shape[1], lens.ptr, window, sinks, (float)scale,
-                              out.ptr, out.dtype == d_bf16 ? TTS_BF16 : TTS_F32, lse.ptr, ws.ptr,
-                              bytes, st.ptr, stream));
+  tts_status status;
+  Py_BEGIN_ALLOW_THREADS  /* a launch may block */
+  status = f_decode(q.ptr, q.shape[0], cu.ptr, (int32_t)batch, max_q, (int32_t)q.shape[1],
+                    (int32_t)c.k.shape[1], (int32_t)d, c.k.ptr, c.v.ptr, c.ks.ptr, c.vs.ptr, c.code,
+                    (int32_t)c.k.shape[0], (int32_t)c.k.shape[2], pt.ptr, (int32_t)pt.shape[1],
+                    lens.ptr, window, sinks, (float)scale, out.ptr,
+                    out.dtype == d_bf16 ? TTS_BF16 : TTS_F32, lse.ptr, ws.ptr, bytes, st.ptr,
+                    stream);
+  Py_END_ALLOW_THREADS
+  return leave(back, status);
 }
 
 static PyObject* attn_fwd_varlen_window(PyObject* self, PyObject* const* a, Py_ssize_t n) {
@@ -411,12 +419,15 @@ static PyObject* attn_fwd_varlen_window(PyObject* self, PyObject* const* a, Py_s
   void* stream;
   long back;
   if (enter(dev, &stream, &back) < 0) return NULL;
-  return leave(back,
-               f_window(q.ptr, k.ptr, v.ptr, q.dtype == d_f32 ? TTS_F32 : TTS_BF16, q.shape[0],
-                        k.shape[0], cq.ptr, ck.ptr, (int32_t)batch, max_q, max_k,
-                        (int32_t)q.shape[1], (int32_t)k.shape[1], (int32_t)q.shape[2], window, sinks,
-                        (float)scale, out.ptr, out.dtype == d_bf16 ? TTS_BF16 : TTS_F32, lse.ptr,
-                        ws.ptr, bytes, st.ptr, stream));
+  tts_status status;
+  Py_BEGIN_ALLOW_THREADS  /* a launch may block */
+  status = f_window(q.ptr, k.ptr, v.ptr, q.dtype == d_f32 ? TTS_F32 : TTS_BF16, q.shape[0],
+                    k.shape[0], cq.ptr, ck.ptr, (int32_t)batch, max_q, max_k, (int32_t)q.shape[1],
+                    (int32_t)k.shape[1], (int32_t)q.shape[2], window, sinks, (float)scale, out.ptr,
+                    out.dtype == d_bf16 ? TTS_BF16 : TTS_F32, lse.ptr, ws.ptr, bytes, st.ptr,
+                    stream);
+  Py_END_ALLOW_THREADS
+  return leave(back, status);
 }
 
 /* bind((append, decode, window addresses), (bf16, fp32, uint8, e4m3, int32),
