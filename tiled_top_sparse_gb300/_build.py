@@ -47,14 +47,22 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def build_native(force: bool = False) -> str:
+def build_native(force: bool = False) -> str | None:
+    """The binding's path; None on a machine without Python's C headers, which goes without it."""
     deps = (NATIVE_SRC, os.path.join(ROOT, "include", "tts.h"), __file__)
     if not force and os.path.exists(NATIVE) and all(
             os.path.getmtime(p) <= os.path.getmtime(NATIVE) for p in deps):
         return NATIVE
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        sys.stderr.write(f"no Python.h in {include}: the binding of the grouped-query calls is left "
+                         "out, and they raise\n")
+        if os.path.exists(NATIVE):  # of other sources
+            os.remove(NATIVE)
+        return None
     tmp = NATIVE + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-shared", "-fPIC",
-           "-I" + sysconfig.get_paths()["include"], NATIVE_SRC, "-o", tmp]
+           "-I" + include, NATIVE_SRC, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for {NATIVE_SRC}:\n{r.stdout}\n{r.stderr}")
@@ -63,7 +71,12 @@ def build_native(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    lib = build_lib(force, verbose, extra)
     build_native(force)
+    return lib
+
+
+def build_lib(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
