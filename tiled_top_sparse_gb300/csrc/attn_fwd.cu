@@ -47,6 +47,7 @@
 // heads: 101 us, 0.94 PFLOP/s (ten tiles for the keys of eight: the sinks' tile and two at the
 // window's ends, whose masks add to each; 6.4 items per CTA at 3 us each); 700 tokens, window 256,
 // 8 / 2 heads of 64: 10.4 us, launch, five tiles' chain of 1.3 us each, and the rows' store.
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -1175,10 +1176,15 @@ cudaError_t launch_d(const AttnArgs& a, int* drv_err, cudaStream_t stream) {
                            C::kSmemBytes);
   if (e != cudaSuccess) return e;
   if constexpr (kWin) {
-    static const int regs = [] {
+    static std::atomic<int> known{0};
+    int regs = 0;
+    e = ask_once(known, &regs, [](int* n) {
       cudaFuncAttributes f;
-      return cudaFuncGetAttributes(&f, attn_fwd_kernel<D, F8, kWin>) == cudaSuccess ? f.numRegs : 0;
-    }();
+      const cudaError_t err = cudaFuncGetAttributes(&f, attn_fwd_kernel<D, F8, kWin>);
+      if (err == cudaSuccess) *n = f.numRegs;
+      return err;
+    });
+    if (e != cudaSuccess) return e;
     if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   }
   if (kWin && items <= sms) {

@@ -1,5 +1,8 @@
-// Dependent launches: a kernel set up while the stream's previous kernel still runs.
+// Host side of launches: kernels set up while the stream's previous kernel still runs, and what is
+// asked about a kernel once.
 #pragma once
+#include <atomic>
+
 #include <cuda_runtime.h>
 
 namespace tts {
@@ -31,6 +34,17 @@ cudaError_t launch_ahead(void (*kernel)(P...), dim3 grid, unsigned threads, size
   cfg.attrs = &at;
   cfg.numAttrs = capture == cudaStreamCaptureStatusNone ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// A property of a compiled kernel, asked for once and kept in `known` (0: not known yet). A query
+// that fails is not kept: its error is returned, and the next call asks again.
+template <typename Query>
+cudaError_t ask_once(std::atomic<int>& known, int* value, Query query) {
+  *value = known.load(std::memory_order_relaxed);
+  if (*value != 0) return cudaSuccess;
+  const cudaError_t e = query(value);
+  if (e == cudaSuccess) known.store(*value, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace tts
