@@ -123,8 +123,8 @@ tts_status tts_attn_fwd_varlen(const void* q, const void* k, const void* v, tts_
  * decode steps call tts_attn_decode_paged with the same window and sinks.
  *
  * window >= 1 (larger than the sequence: plain causal attention), sinks >= 0. k and v must be
- * finite for every key a row's 128-key tile shares with it; rows behind a sequence's last key
- * (another sequence's, or padding) may hold anything.
+ * finite for every key that some row of the sequence sees; the others (sinks <= j <= Lk - Lq -
+ * window) and rows behind a sequence's last key (another sequence's, or padding) may hold anything.
  */
 tts_status tts_attn_fwd_varlen_window(const void* q, const void* k, const void* v,
                                       tts_dtype in_dtype, int64_t total_q, int64_t total_k,

@@ -34,7 +34,8 @@
 // (P - window, P] and the first `sinks`, so an item streams only the tiles that one of its
 // rows sees: the sinks' tiles, then the window's. The work per row is then 4 d min(P + 1,
 // window + sinks) whatever the prompt's length. Rows of a last tile behind the sequence's
-// end (another sequence's, or padding) are cleared in V before the product, so that what
+// end (another sequence's, or padding), and keys that no row of the sequence sees (between the
+// first tokens and the first row's window), are cleared in V before the product, so that what
 // they hold cannot reach a row through a weight of zero.
 // What differs from the kernel without a window, because its items are short: the producer hands the
 // decoded item on; registers move to the softmax warps; the products with a tile's first 64
@@ -624,7 +625,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int n = w.n_tiles, n0 = w.n0, n1 = w.n1;
       if (n == 0) continue;
       int tail_row = kBlockN;  // kWin: first row of the last tile that is behind the sequence
-      if constexpr (kWin) tail_row = (int)(w.Lk - (int64_t)key_tile<true>(w, n - 1) * kBlockN);
+      // kWin: keys [sinks, hid_end) are hidden from every row of the sequence. Tiles up to last_hid
+      // may hold some: the sinks' last one and the window's first.
+      int64_t hid_end = 0;
+      int last_hid = -1;
+      if constexpr (kWin) {
+        tail_row = (int)(w.Lk - (int64_t)key_tile<true>(w, n - 1) * kBlockN);
+        hid_end = w.Lk - w.Lq + 1 - p.window;
+        if (hid_end > p.sinks)
+          last_hid = (int64_t)w.win0 * kBlockN < hid_end ? w.n_sink : w.n_sink - 1;
+      }
       const int st0 = gt % NS;
       ok = all_wait<kWin>(smem_u32(&bar_q[0]), nq & 1, abort_flag, p.dev_status) &&
            all_wait<kWin>(smem_u32(&bar_k[st0]), (gt / NS) & 1, abort_flag, p.dev_status);
@@ -653,107 +663,124 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // kWin, d = 64: all by the second loop. What the instruction cache does not hold costs more
       // there than the branches (88 -> 84 us; d = 128: 105 -> 108).
       constexpr bool kStraight = !(kWin && D == 64);
-      for (; kStraight && j + 1 < nb; ++j) {
-        const int gj = gt + j;
-        const int st = gj % NS;
-        const int st1 = (gj + 1) % NS;
-        if (!kOneKV && !all_wait<kWin>(smem_u32(&bar_v[st]), (gj / NS) & 1, abort_flag, p.dev_status)) {
-          ok = false;
-          break;
-        }
-        if (!pv(0, st, j, g0)) {
-          ok = false;
-          break;
-        }
-        if (!all_wait<kWin>(smem_u32(&bar_k[st1]), ((gj + 1) / NS) & 1, abort_flag, p.dev_status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        issue_qk<D, F8>(S_t[0], qd[0], kd[st1], qtd[0], ktd[st1], e);
-        mma_commit_elect(smem_u32(&bar_s[0]), e);
-        if (j + 2 == n0) mma_commit_elect(smem_u32(&bar_q_empty[0]), e);
-        if (!pv(1, st, j, g1)) {
-          ok = false;
-          break;
-        }
-        mma_commit_elect(smem_u32(&bar_kv_empty[st]), e);
-        issue_qk<D, F8>(S_t[1], qd[1], kd[st1], qtd[1], ktd[st1], e);
-        mma_commit_elect(smem_u32(&bar_s[1]), e);
-        if (!kOneKV) mma_commit_elect(smem_u32(&bar_k_empty[st1]), e);
-        if (j + 2 == n1) mma_commit_elect(smem_u32(&bar_q_empty[1]), e);
-      }
-      for (; ok && j < n; ++j) {
-        const int gj = gt + j;
-        const int st = gj % NS;
-        const int st1 = (gj + 1) % NS;
-        const bool act0 = j < n0, act1 = j < n1;
-        const bool more0 = j + 1 < n0, more1 = j + 1 < n1;
-        if (!kOneKV && !all_wait<kWin>(smem_u32(&bar_v[st]), (gj / NS) & 1, abort_flag, p.dev_status)) {
-          ok = false;
-          break;
-        }
-        if constexpr (kWin) {
-          // Rows of V behind the sequence's last key: what they hold must not meet a weight of zero
-          // as NaN (V has landed: waited for above, or with K).
-          if (j == n - 1 && tail_row < kBlockN) {
-            constexpr int kRow = C::kVBoxBytes / kBlockN;  // bytes of a row in one box
-            for (int b = 0; b < C::kVBoxes; ++b)
-              for (int o = tail_row * kRow + lane * 16; o < kBlockN * kRow; o += 32 * 16)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 sV(st) + b * C::kVBoxBytes + o),
-                             "r"(0)
-                             : "memory");
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        // warpgroup 0
-        if (act0) {
-          if (!pv(0, st, j, g0)) {
-            ok = false;
-            break;
-          }
-          if (more0) {
-            if (!all_wait<kWin>(smem_u32(&bar_k[st1]), ((gj + 1) / NS) & 1, abort_flag,
-                           p.dev_status)) {
+      // kWin: first the second loop for the tiles with hidden keys, then both in turn.
+      int until = kWin ? last_hid + 1 : n;
+      do {
+        if (!kWin || j >= until) {
+          for (; kStraight && j + 1 < nb; ++j) {
+            const int gj = gt + j;
+            const int st = gj % NS;
+            const int st1 = (gj + 1) % NS;
+            if (!kOneKV && !all_wait<kWin>(smem_u32(&bar_v[st]), (gj / NS) & 1, abort_flag, p.dev_status)) {
+              ok = false;
+              break;
+            }
+            if (!pv(0, st, j, g0)) {
+              ok = false;
+              break;
+            }
+            if (!all_wait<kWin>(smem_u32(&bar_k[st1]), ((gj + 1) / NS) & 1, abort_flag, p.dev_status)) {
               ok = false;
               break;
             }
             tc_fence_after();
             issue_qk<D, F8>(S_t[0], qd[0], kd[st1], qtd[0], ktd[st1], e);
             mma_commit_elect(smem_u32(&bar_s[0]), e);
-            if (!kOneKV && !more1) mma_commit_elect(smem_u32(&bar_k_empty[st1]), e);
             if (j + 2 == n0) mma_commit_elect(smem_u32(&bar_q_empty[0]), e);
-          } else {
-            mma_commit_elect(smem_u32(&bar_o[0]), e);
-          }
-        }
-        // warpgroup 1
-        if (act1) {
-          if (!pv(1, st, j, g1)) {
-            ok = false;
-            break;
-          }
-        }
-        mma_commit_elect(smem_u32(&bar_kv_empty[st]), e);  // every PV of this tile issued
-        if (act1) {
-          if (more1) {
-            if (!more0 && !all_wait<kWin>(smem_u32(&bar_k[st1]), ((gj + 1) / NS) & 1, abort_flag,
-                                     p.dev_status)) {
+            if (!pv(1, st, j, g1)) {
               ok = false;
               break;
             }
-            tc_fence_after();
+            mma_commit_elect(smem_u32(&bar_kv_empty[st]), e);
             issue_qk<D, F8>(S_t[1], qd[1], kd[st1], qtd[1], ktd[st1], e);
             mma_commit_elect(smem_u32(&bar_s[1]), e);
             if (!kOneKV) mma_commit_elect(smem_u32(&bar_k_empty[st1]), e);
             if (j + 2 == n1) mma_commit_elect(smem_u32(&bar_q_empty[1]), e);
-          } else {
-            mma_commit_elect(smem_u32(&bar_o[1]), e);
+          }
+          until = n;
+        }
+        for (; ok && j < until; ++j) {
+          const int gj = gt + j;
+          const int st = gj % NS;
+          const int st1 = (gj + 1) % NS;
+          const bool act0 = j < n0, act1 = j < n1;
+          const bool more0 = j + 1 < n0, more1 = j + 1 < n1;
+          if (!kOneKV && !all_wait<kWin>(smem_u32(&bar_v[st]), (gj / NS) & 1, abort_flag, p.dev_status)) {
+            ok = false;
+            break;
+          }
+          if constexpr (kWin) {
+            // Rows of V that no row of the sequence sees, and those behind its last key: what they
+            // hold must not meet a weight of zero as NaN (V has landed: waited for above, or with K).
+            const bool end = j == n - 1 && tail_row < kBlockN;
+            if (end || j <= last_hid) {
+              const int64_t kv0 = (int64_t)key_tile<true>(w, j) * kBlockN;
+              auto row_of = [&](int64_t key) -> int {
+                return key <= kv0 ? 0 : key - kv0 < kBlockN ? (int)(key - kv0) : kBlockN;
+              };
+              const int from = row_of(p.sinks), to = j <= last_hid ? row_of(hid_end) : 0;
+              const int behind = end ? tail_row : kBlockN;
+              constexpr int kRow = C::kVBoxBytes / kBlockN;  // bytes of a row in one box
+              for (int b = 0; b < C::kVBoxes; ++b)
+                for (int o = lane * 16; o < kBlockN * kRow; o += 32 * 16) {
+                  const int r = o / kRow;
+                  if ((r >= from && r < to) || r >= behind)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                     sV(st) + b * C::kVBoxBytes + o),
+                                 "r"(0)
+                                 : "memory");
+                }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          // warpgroup 0
+          if (act0) {
+            if (!pv(0, st, j, g0)) {
+              ok = false;
+              break;
+            }
+            if (more0) {
+              if (!all_wait<kWin>(smem_u32(&bar_k[st1]), ((gj + 1) / NS) & 1, abort_flag,
+                             p.dev_status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              issue_qk<D, F8>(S_t[0], qd[0], kd[st1], qtd[0], ktd[st1], e);
+              mma_commit_elect(smem_u32(&bar_s[0]), e);
+              if (!kOneKV && !more1) mma_commit_elect(smem_u32(&bar_k_empty[st1]), e);
+              if (j + 2 == n0) mma_commit_elect(smem_u32(&bar_q_empty[0]), e);
+            } else {
+              mma_commit_elect(smem_u32(&bar_o[0]), e);
+            }
+          }
+          // warpgroup 1
+          if (act1) {
+            if (!pv(1, st, j, g1)) {
+              ok = false;
+              break;
+            }
+          }
+          mma_commit_elect(smem_u32(&bar_kv_empty[st]), e);  // every PV of this tile issued
+          if (act1) {
+            if (more1) {
+              if (!more0 && !all_wait<kWin>(smem_u32(&bar_k[st1]), ((gj + 1) / NS) & 1, abort_flag,
+                                       p.dev_status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              issue_qk<D, F8>(S_t[1], qd[1], kd[st1], qtd[1], ktd[st1], e);
+              mma_commit_elect(smem_u32(&bar_s[1]), e);
+              if (!kOneKV) mma_commit_elect(smem_u32(&bar_k_empty[st1]), e);
+              if (j + 2 == n1) mma_commit_elect(smem_u32(&bar_q_empty[1]), e);
+            } else {
+              mma_commit_elect(smem_u32(&bar_o[1]), e);
+            }
           }
         }
-      }
+      } while (kWin && ok && j < n);
       gt += n;
       g0 += n0;
       g1 += n1;
