@@ -54,6 +54,7 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 inline tts_status from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return TTS_OK;
+  cudaGetLastError();  // or the next call's launch would be taken to have failed with it
   if (e == cudaErrorInvalidValue) return TTS_ERR_INVALID_ARG;
   return TTS_ERR_CUDA;
 }
