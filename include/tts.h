@@ -370,10 +370,10 @@ tts_status tts_attn_fwd_varlen_fp8(const void* q8, const float* q_scale, const v
  * cos_sin[pos]; in fp32, each product and sum rounded; cos_sin NULL: no rotation).
  *   q_out[t] = bf16(R q[t])    k_out[t] = bf16(R k[t])    k row = R k[t]    v row = v[t]
  * A bf16 cache takes the rows rounded to nearest even. An e4m3 cache takes e4m3(x / s)
- * (nearest even, saturating; s ignores non-finite x). A page whose first slot is written by
- * this call takes s from the new rows alone (what it held before is forgotten); a page that
- * already holds rows of the request keeps its s if the new rows fit and else grows it, and the
- * codes of its earlier rows become e4m3(code * s_old / s_new). Slots behind the last appended
+ * (nearest even, saturating; s ignores non-finite x). A page whose first slot is written by this
+ * call takes s from the new rows alone (what it held before is forgotten); a page that already
+ * holds rows of the request takes the larger of its s and the new rows', and where that grows it
+ * the codes of its earlier rows become e4m3(code * s_old / s_new). Slots behind the last appended
  * token keep their bytes; they are past the end.
  *
  * q, k, v     device bf16, token t's heads at q + t * q_stride (in values; head h at + h *
@@ -381,7 +381,8 @@ tts_status tts_attn_fwd_varlen_fp8(const void* q8, const float* q_scale, const v
  *             q_out, num_heads_q and q_stride are not looked at).
  * total_new   rows of q / k / v; max_new: host upper bound of n_r (it chooses the kernel; a
  *             longer request is flagged TTS_DEV_BAD_ARG and skipped, like entries of cu_new
- *             that decrease or leave [0, total_new])
+ *             that decrease or leave [0, total_new]; where entries decrease, rows of the call's
+ *             other requests may be left out too)
  * cu_new      device int32 [batch + 1];  past_lens device int32 [batch]
  * cos_sin     device fp32 [max_pos, head_dim / 2, 2] of tts_rope_cache, or NULL
  * page_tables device int32 [batch, max_pages]
@@ -391,13 +392,15 @@ tts_status tts_attn_fwd_varlen_fp8(const void* q8, const float* q_scale, const v
  * A request whose positions do not fit [0, max_pages * page_size) (or max_pos with a table)
  * is not cached, its q_out / k_out rows are zeros, and TTS_DEV_INDEX_RANGE is set; a page
  * outside [0, num_pages) takes no rows and sets the same bit. A partly filled page whose scale
- * is not a positive finite number is treated as new and sets TTS_DEV_BAD_ARG. Two requests
- * of one call must not append to the same page (what it then holds is unspecified). Rows
- * of q_out / k_out outside every request are left as they were.
+ * is not a positive finite number is treated as new and sets TTS_DEV_BAD_ARG. Two requests of one
+ * call must not append to the same page, nor one request to it through two entries of its table
+ * (what it then holds is unspecified). Rows of q_out / k_out outside every request are left as
+ * they were.
  *
- * cache_dtype TTS_BF16 or TTS_E4M3; head_dim 64 or 128, other page sizes or head_dims:
- * TTS_ERR_UNSUPPORTED. Strides are multiples of 8 and at least heads * head_dim; q, k, v,
- * the caches, q_out, k_out and cos_sin are 16-byte aligned. One launch, nothing allocated.
+ * cache_dtype TTS_BF16 or TTS_E4M3; head_dim 64 or 128, max_pages * page_size at most 2^30,
+ * num_pages * num_heads_kv under 2^31; other sizes: TTS_ERR_UNSUPPORTED. Strides are multiples of
+ * 8 and at least heads * head_dim; q, k, v, the caches, q_out, k_out and cos_sin are 16-byte
+ * aligned. One launch, nothing allocated.
  */
 tts_status tts_rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads_q, const void* k,
                               int64_t k_stride, const void* v, int64_t v_stride,
@@ -447,9 +450,11 @@ tts_status tts_rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads
  * workspace   device scratch of at least tts_attn_decode_workspace_bytes(...) bytes, 16-byte
  *             aligned, owned by the caller, not shared by calls that may overlap; nothing in
  *             it needs to be initialised. Missing or smaller: TTS_ERR_WORKSPACE.
- * head_dim 64 or 128, page_size 16, 32, 64 or 128 (else TTS_ERR_UNSUPPORTED); q, caches and out
- * 16-byte aligned. Results are bitwise reproducible, but the split of the keys over CTAs, and
- * so the rounding of a request's result, depends on the whole batch's lengths.
+ * head_dim, page_size, max_pages and num_pages as tts_rope_kv_append, and the key tiles that batch
+ * requests of max_pages pages could have, counted for all KV heads and row tiles, within 2e9 (else
+ * TTS_ERR_UNSUPPORTED); q, caches and out 16-byte aligned. Results are bitwise reproducible, but
+ * the split of the keys over CTAs, and so the rounding of a request's result, depends on the whole
+ * batch's lengths.
  */
 size_t tts_attn_decode_workspace_bytes(int32_t max_seqlen_q, int32_t num_heads_q,
                                        int32_t num_heads_kv, int32_t head_dim);

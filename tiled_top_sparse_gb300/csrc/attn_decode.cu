@@ -17,24 +17,26 @@
 // warps takes every fourth tile for itself, with its own running maximum, sum and
 // accumulators, joined through shared memory at the end of the unit: no barrier inside a unit.
 //
-// S^T = K Q^T and O^T = V^T P^T run on m16n8k16 tensor-core products with keys (then d) as
-// the 16 rows and q rows as the 8 columns: a group of 4 to 8 heads fills the columns, where a
-// 128-row tcgen05 tile would be 3 to 6 % used and would need the codes widened in shared
-// memory; at HBM's rate an SM can issue about 2800 instructions per 16 KB tile, of which one n
-// tile takes a third (issue slots 29 % used, tensor pipe 18 %). e4m3 codes become fp16
-// (exactly) in registers; q is fp16 after a power-of-two scaling of its row (exact for every
-// element within 2^-22 of the row's largest), and P is fp16 with its reference kept so that
-// 2^-25 of the maximum still has all 11 bits. bf16 caches use bf16 products throughout. Sums
-// and softmax statistics are fp32.
+// S^T = K Q^T and O^T = V^T P^T run on m16n8k16 tensor-core products with keys (then d) as the 16
+// rows and q rows as the 8 columns: a group of 4 to 8 heads fills the columns, and a warp takes
+// its operands from shared memory into registers, where e4m3 is widened; at HBM's rate an SM can
+// issue about 2800 instructions per 16 KB tile, of which one n tile takes a third (issue slots 29
+// % used, tensor pipe 18 %), so that up to 8 rows the bytes are the bound. More rows repeat the
+// loads and the widening of a tile in each row group: there tcgen05 products with 128 keys (then
+// d) as rows and the q rows as columns would take a tile once. They are not built. e4m3 codes
+// become fp16 (exactly) in registers; q is fp16 after a power-of-two scaling of its row (exact for
+// every element within 2^-22 of the row's largest), and P is fp16 with its reference kept so that
+// 2^-25 of the maximum still has all 11 bits. bf16 caches use bf16 products throughout. Sums and
+// softmax statistics are fp32.
 //
-// Measured (32 / 8 heads of 128, CUDA graph): 64 requests x 32768 tokens in e4m3 616 to 632 us
-// from box to box (6.8 to 7.0 TB/s, 1.00 to 1.03 of the measured copy rate), one request of
-// 2590 tokens 8.9 us (the chain of launch, lengths, page table, tile, products and the parts'
-// launch; its bytes are 0.8 us), 33 ragged requests with a window of 4096 53.4 us (39.4 us of
-// bytes; about 2.5 us before the first tile, 3 for the parts, and the last CTAs), 1 to 4 tokens
-// of 16 requests over a bf16 cache 64.2 us (52.7). Many rows are bound by what each warp issues:
-// 16, 32 and 64 rows per KV head take 1.6, 2.2 and 3.8 times the bytes' time in e4m3 and 1.1,
-// 1.3 and 2.0 in bf16 (16 requests x 20000 tokens, 4 KV heads).
+// Measured (32 / 8 heads of 128; from one GPU to another): 64 requests x 32768 tokens in e4m3 616
+// to 636 us (6.8 to 7.0 TB/s, 1.00 to 1.03 of the measured copy rate), one request of 2590 tokens
+// 8.5 to 9.7 us (the chain of launch, lengths, page table, tile, products and the parts' launch;
+// its bytes are 0.8 us), 33 ragged requests with a window of 4096 53 us (39.4 us of bytes; about
+// 2.5 us before the first tile, 3 for the parts, and the last CTAs), 1 to 4 tokens of 16 requests
+// over a bf16 cache 64 to 66 us (52.7). Many rows are bound by what each warp issues: 8, 16, 32
+// and 64 rows per KV head take 1.2, 1.6, 2.2 and 3.7 times the bytes' time in e4m3 and 1.1, 1.1,
+// 1.3 and 2.0 in bf16 (16 requests x 20000 tokens, 4 KV heads; CUDA graph).
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -307,8 +309,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     return x;
   };
   auto tiles_of = [&](const Req& r) -> int { return p.hkv * r.rt * (r.nt + kEndTiles); };
-  // Runs of at least kNW places (the warps take one each, side by side): shorter ones would
-  // only leave more parts to join. The first `more` runs have one tile more than the others.
+  // One run per kNW places of the list, rounded up (the warps take one each, side by side): shorter
+  // runs would only leave more parts to join. The first `more` runs have one place more than the
+  // others; rounding may leave a run of a short list a place or two under kNW.
   int total = 0, runs = 0, len = 0, more = 0, t0 = 0, t1 = 0;
   auto split = [&]() -> bool {
     runs = min((int)((unsigned)(total + kNW - 1) / kNW), p.ctas);

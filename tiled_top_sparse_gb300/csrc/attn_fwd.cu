@@ -42,12 +42,15 @@
 // weights start while the others are computed; rows leave by TMA stores; and the code is kept
 // small, since an item runs once through all of it and what the instruction cache misses is a
 // fifth of the softmax warps' time.
-// Measured: 16,000 tokens, window 4096, 128 sinks, 16 / 4 heads of 128: 302 to 314 us, 1.53 to 1.59
-// PFLOP/s over visible pairs (0.80 to 0.83 of the measured bf16 rate; 1.27 us per pair of tiles, the
-// tensor core's rate, and 3 us per item); four prompts of 827 to 3212 tokens, window 1024, 32 / 8
-// heads: 101 us, 0.94 PFLOP/s (ten tiles for the keys of eight: the sinks' tile and two at the
-// window's ends, whose masks add to each; 6.4 items per CTA at 3 us each); 700 tokens, window 256,
-// 8 / 2 heads of 64: 10.4 us, launch, five tiles' chain of 1.3 us each, and the rows' store.
+// Measured: 16,000 tokens, window 4096, 128 sinks, 16 / 4 heads of 128: 302 to 316 us, 1.53 to
+// 1.59 PFLOP/s over visible pairs (0.80 to 0.83 of the measured bf16 rate; 1.27 us per pair of
+// tiles, the tensor core's rate, and 3 us per item; 286 in a graph that repeats it on the same
+// data); four prompts of 827 to 3212 tokens, window 1024, 32 / 8 heads: 100 to 103 us, 0.94
+// PFLOP/s (ten tiles for the keys of eight: the sinks' tile and two at the window's ends, whose
+// masks add to each; 6.4 items per CTA at 3 us each); 700 tokens, window 256, 8 / 2 heads of 64:
+// 9.7 to 10.7 us, launch, five tiles' chain of 1.3 us each, and the rows' store. Smaller heads
+// keep the softmax work per score and have fewer products beside it: three prompts of 3000 to 8000
+// tokens, window 1024, 32 / 8 heads of 64, 80 and 128: 186, 205 and 221 us.
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -340,7 +343,6 @@ __device__ __forceinline__ bool decode_item(const ParamsFor<kWin>& p, int it, It
   return true;
 }
 
-// Persistent: one CTA per SM takes items from a global counter until none are left.
 // Waits of the kernel. kWin: the same bounded wait in half the instructions (32-bit nanoseconds,
 // the status set once at the end): its code competes with the tiles' for the instruction cache
 // (ragged prompts, window 1024: 104 -> 101 us; window 128: 67 -> 63). The issuing warp looks
@@ -371,6 +373,8 @@ __device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, volatile
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
+// Persistent: one CTA per SM takes items from a global counter until none are left (kWin: its one
+// item where there are no more items than CTAs).
 // Per CTA, items flow through a two-slot ring (producer -> MMA warp + softmax warps);
 // barrier phases run on counters that continue across items: gt = K/V tiles so far
 // (ring slots, S / P phases), nq = items with at least one tile (Q, O phases).

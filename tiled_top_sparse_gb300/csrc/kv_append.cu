@@ -16,7 +16,9 @@
 // the maximum and the rounding, and the rotation's table row is read once per eight q heads.
 // 36,411 tokens of 32 / 8 heads of 128 into e4m3: 147 us, 6.1 TB/s, 0.90 of the measured copy
 // rate (what is left: the blocks' chain of lengths, rows, reduction and stores, 50 % of the warps
-// resident). A step is one launch's latency: 3.0 us for 8 requests, 3.3 for 64.
+// resident). A step is one launch's latency: 3.0 us for 8 requests, 3.3 for 64. Where a page grows
+// its scale one warp reads and rewrites the page's earlier rows: 64 requests whose k and v pages
+// all grow take 6.1 us at slot 60 of pages of 64, 8.1 at slot 120 of 128.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -331,7 +333,9 @@ constexpr int kQHeads = 8;  // q heads that share one load of the table row
 // Prompts: a block per (page, head) of k and of v, and a block per (token tile, 8 q heads).
 // Registers are held to 48 (64 for the pages of 2048 pieces), for five (two) blocks per SM: what
 // bounds the kernel is how many rows are on their way (28,000 tokens in pages of 128: 75 -> 55 us,
-// of 16 to 32: 58 -> 53 us; pages of 64 in blocks of 512 threads instead of 256: 50 -> 64 us).
+// of 16 to 32: 58 -> 53 us; pages of 64 in blocks of 512 threads instead of 256: 50 -> 64 us), and
+// that outweighs what it spills: 20 bytes a thread where a page takes one pass, 44 to 52 where it
+// takes two, none at 64 registers.
 template <int D, bool kF8, int kPasses, int kMost>
 __global__ void __launch_bounds__(kMost, kMost == 256 ? 5 : 2) append_pages_kernel(const KvAppendArgs p,
                                                            uint64_t q_share, int q_shift,
