@@ -42,8 +42,8 @@
 // weights start while the others are computed; rows leave by TMA stores; and the code is kept
 // small, since an item runs once through all of it and what the instruction cache misses is a
 // fifth of the softmax warps' time.
-// Measured: 16,000 tokens, window 4096, 128 sinks, 16 / 4 heads of 128: 302 to 316 us, 1.53 to
-// 1.59 PFLOP/s over visible pairs (0.80 to 0.83 of the measured bf16 rate; 1.27 us per pair of
+// Measured: 16,000 tokens, window 4096, 128 sinks, 16 / 4 heads of 128: 302 to 324 us, 1.48 to
+// 1.59 PFLOP/s over visible pairs (0.78 to 0.83 of the measured bf16 rate; 1.27 us per pair of
 // tiles, the tensor core's rate, and 3 us per item; 286 in a graph that repeats it on the same
 // data); four prompts of 827 to 3212 tokens, window 1024, 32 / 8 heads: 100 to 103 us, 0.94
 // PFLOP/s (ten tiles for the keys of eight: the sinks' tile and two at the window's ends, whose
