@@ -413,6 +413,103 @@ tts_status tts_rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads
                               void* q_out, void* k_out, uint32_t* dev_status, void* stream);
 
 /*
+ * The same append with explicit positions on one or several axes: images and video in a prompt
+ * (time, height and width of a patch; text has the same position on all of them), and drafted
+ * trees, whose tokens take the position of their depth while their rows lie in order.
+ *
+ * As tts_rope_kv_append (same cache, slots past_lens[r] + i, scales, layouts, device checks and
+ * errors), except that pair (j, j + head_dim / 2) of token t turns by
+ *   cos_sin[positions[pair_axis[j], t], j].
+ * One axis with all pair_axis 0 and positions past_lens[r] + i gives the same bits as
+ * tts_rope_kv_append.
+ *
+ * positions   device int32 [num_axes, total_new], num_axes 1 .. 4. A token with a position outside
+ *             [0, max_pos) on any axis gets zeros for its q_out, k_out and cached key, and sets
+ *             TTS_DEV_INDEX_RANGE; its value is cached as it is. Requests' own positions
+ *             past_lens[r] + i may lie beyond max_pos.
+ * pair_axis   host bytes [head_dim / 2], read during the call: the axis of every pair, below
+ *             num_axes (sections of consecutive pairs, axes in turn, or any other assignment)
+ * cos_sin     required: device fp32 [max_pos, head_dim / 2, 2]; column j holds the frequency of
+ *             pair j (tts_rope_cache's table has the one-dimensional head's)
+ */
+tts_status tts_rope_kv_append_axes(
+    const void* q, int64_t q_stride, int32_t num_heads_q, const void* k, int64_t k_stride,
+    const void* v, int64_t v_stride, int64_t total_new, const int32_t* cu_new,
+    const int32_t* past_lens, int32_t batch, int32_t max_new, int32_t num_heads_kv,
+    int32_t head_dim, const float* cos_sin, int32_t max_pos, const int32_t* positions,
+    int32_t num_axes, const uint8_t* pair_axis, const int32_t* page_tables, int32_t max_pages,
+    void* k_cache, void* v_cache, float* k_scale, float* v_scale, tts_dtype cache_dtype,
+    int32_t num_pages, int32_t page_size, void* q_out, void* k_out, uint32_t* dev_status,
+    void* stream);
+
+/*
+ * The accepted path of a drafted tree, brought together in the cache: of the new tokens that
+ * request r has behind its past_lens[r] cached ones, the tokens path[r, 0] < path[r, 1] < ..
+ * (m = path_lens[r] of them, counted from 0 behind the cached ones) are kept, and row
+ * past + path[r, i] is moved to past + i, keys and values of every head:
+ *   kv_lens[r] = past_lens[r] + m
+ * Rows with path[r, i] = i stay where they are. The rows behind the last kept one are past the
+ * end, and hold anything.
+ *
+ * A bf16 cache's rows keep their bits. In an e4m3 cache a row moved to a page with the same scale
+ * keeps its codes; else the codes become e4m3(code * s_from / s_to) (nearest even, saturating; fp32,
+ * exact for powers of two), and where the page's scale is too small for a moved row's
+ * largest finite value, it becomes the smallest power of two s >= 2^-60 that holds the rows moved
+ * into the page, and all of the page's codes move to it. A page's scale never shrinks here.
+ *
+ * k_cache .. page_tables, max_pages: as tts_rope_kv_append (both caches are written in place)
+ * past_lens  device int32 [batch], without the new tokens
+ * path       device int32 [batch, max_path], max_path 0 .. 64 (else TTS_ERR_UNSUPPORTED); entries
+ *            behind a request's m may be anything
+ * path_lens  device int32 [batch]
+ * kv_lens    device int32 [batch], written; must not overlap past_lens
+ * A request whose m is outside [0, max_path] or whose path does not increase from 0 on sets
+ * TTS_DEV_BAD_ARG; one with rows outside [0, max_pages * page_size) sets TTS_DEV_INDEX_RANGE.
+ * Nothing of either is moved, and its kv_lens is its past_lens (0 where that is negative). A row
+ * from or to a page outside [0, num_pages) is not moved (TTS_DEV_INDEX_RANGE), nor is one from a
+ * page whose scale is not a positive finite number (TTS_DEV_BAD_ARG); a page with such a scale
+ * that rows are moved to is treated as new (TTS_DEV_BAD_ARG). A page that rows are moved to, or
+ * from, must not be another request's as well, if a request of the call moves rows to it. One
+ * launch, nothing allocated.
+ */
+tts_status tts_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                          tts_dtype cache_dtype, int32_t num_pages, int32_t num_heads_kv,
+                          int32_t page_size, int32_t head_dim, const int32_t* page_tables,
+                          int32_t max_pages, const int32_t* past_lens, int32_t batch,
+                          const int32_t* path, int32_t max_path, const int32_t* path_lens,
+                          int32_t* kv_lens, uint32_t* dev_status, void* stream);
+
+/*
+ * Requests forked: several samples or beams that continue cached tokens. New request i becomes a
+ * continuation of request p = parents[i] with L = kv_lens[p] tokens; full pages are shared, the
+ * page that its next token goes to is its own:
+ *   lens_out[i] = L
+ *   tables_out[i, a] = page_tables[p, a]   for a < L / page_size
+ *                      new_pages[i]        for a = L / page_size < max_pages
+ *                      -1                  behind
+ * and where L is not a multiple of page_size, the first L % page_size rows of page
+ * page_tables[p, L / page_size] (keys and values of every head, and e4m3 scales) are copied to
+ * new_pages[i]. new_pages[i] < 0: row i of tables_out is the parent's whole row and nothing is
+ * copied (a child that takes its parent's place).
+ *
+ * k_cache .. page_tables, max_pages: as tts_rope_kv_append; page_tables [batch, max_pages] and
+ * kv_lens [batch] are read, tables_out int32 [children, max_pages] and lens_out int32 [children]
+ * written (neither may overlap its input); parents, new_pages device int32 [children].
+ * new_pages must be different pages that no request uses (what they hold is unspecified
+ * otherwise). A parent outside [0, batch) or a length outside [0, max_pages * page_size] sets
+ * TTS_DEV_INDEX_RANGE: length 0, a row of -1. A new page >= num_pages sets it too (entries from
+ * L / page_size on become -1), and so does a parent's partly filled page outside [0, num_pages)
+ * (nothing is copied). One launch, nothing allocated.
+ */
+tts_status tts_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                       tts_dtype cache_dtype, int32_t num_pages, int32_t num_heads_kv,
+                       int32_t page_size, int32_t head_dim, const int32_t* page_tables,
+                       int32_t max_pages, const int32_t* kv_lens, int32_t batch,
+                       const int32_t* parents, const int32_t* new_pages, int32_t children,
+                       int32_t* tables_out, int32_t* lens_out, uint32_t* dev_status,
+                       void* stream);
+
+/*
  * Attention of each request's newest tokens over the cache of tts_rope_kv_append: the decode
  * step (one token per request) and steps of a few tokens (drafts to verify), with an optional
  * sliding window and first tokens that stay visible.
@@ -471,6 +568,40 @@ tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* 
                                  void* stream);
 
 /*
+ * Attention of a drafted tree over the cache: as tts_attn_decode_paged (same requests, cache,
+ * layouts, types, scales, device checks and errors), except for which keys a token sees. With
+ * L = kv_lens[r], n new tokens (keys L - n .. L - 1) and the bits m < n of tree_mask[t] (bit m:
+ * the token sees its request's new token m; a tree's token has its ancestors' bits and its own),
+ * token t, at position P = L - n + max(c - 1, 0) with c = the number of those bits, sees
+ *   new token m (key L - n + m)  iff  bit m is set
+ *   key j < L - n                iff  window = 0  or  j > P - window  or  j < sinks
+ * A token without a visible key gets out = 0, lse = -inf (padding: an empty mask, in a request
+ * that has new tokens only).
+ *
+ * tree_mask   device uint64 [total_q]; bits from n on are not looked at
+ * Cached values that some new token sees must be finite; of the keys that none sees, any may hold
+ * anything (a drafted token that no mask has, keys hidden by the window, rows behind the
+ * last token). With a window, pages of keys from L - n + 1 - window on and of the first `sinks` are
+ * read. Products: e4m3 keys by q as the sum of two e4m3 values after a power-of-two row scaling (exact
+ * within 2^-9 of the row's largest value, to 2^-17 of it below), e4m3 values as fp16 by weights
+ * rounded to fp16; bf16 x bf16 for a bf16 cache (weights rounded to bf16); accumulated in fp32.
+ * workspace of at least tts_attn_decode_tree_workspace_bytes(...) bytes, as there.
+ */
+size_t tts_attn_decode_tree_workspace_bytes(int32_t max_seqlen_q, int32_t num_heads_q,
+                                            int32_t num_heads_kv, int32_t head_dim);
+
+tts_status tts_attn_decode_tree(const void* q, int64_t total_q, const int32_t* cu_seqlens_q,
+                                const uint64_t* tree_mask, int32_t batch, int32_t max_seqlen_q,
+                                int32_t num_heads_q, int32_t num_heads_kv, int32_t head_dim,
+                                const void* k_cache, const void* v_cache, const float* k_scale,
+                                const float* v_scale, tts_dtype cache_dtype, int32_t num_pages,
+                                int32_t page_size, const int32_t* page_tables, int32_t max_pages,
+                                const int32_t* kv_lens, int32_t window, int32_t sinks,
+                                float scale, void* out, tts_dtype out_dtype, float* lse,
+                                void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                void* stream);
+
+/*
  * cos/sin table of rotary position embedding, built once and read by tts_qkv_rope.
  *
  * The position-indexed table of "从 SGLang Kernel源码到 GPU Trace" (section 3.3: cos
@@ -524,6 +655,26 @@ tts_status tts_qkv_rope(const void* x, int64_t n, int32_t hidden, const void* w,
                         const float* bias, const int32_t* positions, const float* cos_sin,
                         int32_t max_pos, int32_t num_heads, int32_t head_dim, void* q, void* k,
                         void* v, uint32_t* dev_status, void* stream);
+
+/*
+ * The same projection with positions on several axes: row and column of an image's patch, and the
+ * time of a video's.
+ *
+ * As tts_qkv_rope (same layouts, products, device checks and errors), except that pair
+ * (j, j + head_dim / 2) of token t turns by cos_sin[positions[pair_axis[j], t], j].
+ *
+ * positions  device int32 [num_axes, n], num_axes 1 .. 4; a token with a position outside
+ *            [0, max_pos) on any axis gets zeros for its q and k, and sets TTS_DEV_INDEX_RANGE
+ * pair_axis  host bytes [head_dim / 2], read during the call: the axis of every pair, below num_axes
+ * cos_sin    device fp32 [max_pos, head_dim / 2, 2]; column j holds the frequency of pair j. Where
+ *            every axis has its own run of frequencies over its part of the head, that is the
+ *            tables of tts_rope_cache for the parts' sizes side by side.
+ */
+tts_status tts_qkv_rope_axes(const void* x, int64_t n, int32_t hidden, const void* w,
+                             const float* bias, const int32_t* positions, int32_t num_axes,
+                             const uint8_t* pair_axis, const float* cos_sin, int32_t max_pos,
+                             int32_t num_heads, int32_t head_dim, void* q, void* k, void* v,
+                             uint32_t* dev_status, void* stream);
 
 /*
  * Diagnostics (no counterpart in the pages): launches one thread that waits on a

@@ -22,9 +22,22 @@ built beside it) is missing or fails to load, calls raise.
     attn_decode_paged(q, k_cache, v_cache, page_tables, kv_lens, scale, cu_seqlens_q=None,
                       max_seqlen_q=1, k_scale=None, v_scale=None, window=0, sinks=0, out=None,
                       lse=None, workspace=None, status=None)
+    rope_kv_append_axes(k, v, k_cache, v_cache, page_tables, past_lens, cu_new, max_new,
+                        positions, pair_axis, cos_sin, k_scale=None, v_scale=None, q=None,
+                        q_out=None, k_out=None, status=None)
+    attn_decode_tree(q, k_cache, v_cache, page_tables, kv_lens, tree_mask, scale, cu_seqlens_q,
+                     max_seqlen_q, k_scale=None, v_scale=None, window=0, sinks=0, out=None,
+                     lse=None, workspace=None, status=None)
+    kv_compact(k_cache, v_cache, page_tables, past_lens, path, path_lens, k_scale=None,
+               v_scale=None, kv_lens=None, status=None)
+    kv_fork(k_cache, v_cache, page_tables, kv_lens, parents, new_pages, k_scale=None,
+            v_scale=None, tables_out=None, lens_out=None, status=None)
+    rope_axes(sections, interleaved=False)
     rope_cache(max_pos, rot_dim, base=10000.0, out=None, device=None)
     qkv_rope(x, w, bias, positions, cos_sin, num_heads, q=None, k=None, v=None,
              status=None)
+    qkv_rope_axes(x, w, bias, positions, pair_axis, cos_sin, num_heads, q=None, k=None, v=None,
+                  status=None)
 
 `status`, when given, is a 1-element int32 CUDA tensor the kernels OR their
 device-side flags into (see TTS_DEV_* in the header); `check_status(status)`
@@ -71,10 +84,16 @@ EXPORTED = (
     "tts_quantize_fp8_prefill",
     "tts_attn_fwd_varlen_fp8",
     "tts_rope_kv_append",
+    "tts_rope_kv_append_axes",
+    "tts_kv_compact",
+    "tts_kv_fork",
     "tts_attn_decode_workspace_bytes",
     "tts_attn_decode_paged",
+    "tts_attn_decode_tree_workspace_bytes",
+    "tts_attn_decode_tree",
     "tts_rope_cache",
     "tts_qkv_rope",
+    "tts_qkv_rope_axes",
     "tts_attn_fwd_varlen_f32_noalloc",
     "tts_debug_wait_timeout",
 )
@@ -143,6 +162,25 @@ def lib() -> ctypes.CDLL:
                                         ctypes.c_int, i32, i32, P, i32, P, i32, i32, f32, P,
                                         ctypes.c_int, P, P, ctypes.c_size_t, P, P]
     L.tts_attn_decode_paged.restype = ctypes.c_int
+    L.tts_rope_kv_append_axes.argtypes = [
+        P, i64, i32, P, i64, P, i64, i64, P, P, i32, i32, i32, i32, P, i32, P, i32, ctypes.c_char_p,
+        P, i32, P, P, P, P, ctypes.c_int, i32, i32, P, P, P, P]
+    L.tts_rope_kv_append_axes.restype = ctypes.c_int
+    L.tts_kv_compact.argtypes = [P, P, P, P, ctypes.c_int, i32, i32, i32, i32, P, i32, P, i32, P,
+                                 i32, P, P, P, P]
+    L.tts_kv_compact.restype = ctypes.c_int
+    L.tts_kv_fork.argtypes = [P, P, P, P, ctypes.c_int, i32, i32, i32, i32, P, i32, P, i32, P, P,
+                              i32, P, P, P, P]
+    L.tts_kv_fork.restype = ctypes.c_int
+    L.tts_attn_decode_tree_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.tts_attn_decode_tree_workspace_bytes.restype = ctypes.c_size_t
+    L.tts_attn_decode_tree.argtypes = [P, i64, P, P, i32, i32, i32, i32, i32, P, P, P, P,
+                                       ctypes.c_int, i32, i32, P, i32, P, i32, i32, f32, P,
+                                       ctypes.c_int, P, P, ctypes.c_size_t, P, P]
+    L.tts_attn_decode_tree.restype = ctypes.c_int
+    L.tts_qkv_rope_axes.argtypes = [P, i64, i32, P, P, P, i32, ctypes.c_char_p, P, i32, i32, i32,
+                                    P, P, P, P, P]
+    L.tts_qkv_rope_axes.restype = ctypes.c_int
     L.tts_rope_cache.argtypes = [i32, i32, f32, P, P]
     L.tts_rope_cache.restype = ctypes.c_int
     L.tts_qkv_rope.argtypes = [P, i64, i32, P, P, P, P, i32, i32, i32, P, P, P, P, P]
@@ -553,6 +591,10 @@ def _binding():
                (torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn, torch.int32),
                (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
                 torch._C._cuda_setDevice))
+        m.bind_more(tuple(ctypes.cast(f, ctypes.c_void_p).value
+                          for f in (L.tts_rope_kv_append_axes, L.tts_attn_decode_tree,
+                                    L.tts_kv_compact, L.tts_kv_fork, L.tts_qkv_rope_axes)),
+                    torch.int64)
         _nat = m
     return _nat
 
@@ -619,3 +661,118 @@ def attn_decode_paged(q, k_cache, v_cache, page_tables, kv_lens, scale, cu_seqle
     if code:
         raise TTSError(code, "tts_attn_decode_paged")
     return out, lse
+
+
+def rope_axes(sections, interleaved=False) -> bytes:
+    """The axis of every rotation pair (pair_axis of rope_kv_append_axes and qkv_rope_axes):
+    sections[a] pairs turn by axis a. Consecutive runs, or, interleaved, pair j on axis j modulo
+    their number as long as that one has pairs left, else on the first one that has."""
+    sections = [int(n) for n in sections]
+    _need(1 <= len(sections) <= 4 and min(sections) >= 0, "1 to 4 sections of 0 or more pairs")
+    if not interleaved:
+        return b"".join(bytes([a]) * n for a, n in enumerate(sections))
+    axes, left, out = len(sections), list(sections), []
+    for j in range(sum(sections)):
+        a = j % axes if left[j % axes] > 0 else next(x for x in range(axes) if left[x] > 0)
+        left[a] -= 1
+        out.append(a)
+    return bytes(out)
+
+
+def rope_kv_append_axes(k, v, k_cache, v_cache, page_tables, past_lens, cu_new, max_new, positions,
+                        pair_axis, cos_sin, k_scale=None, v_scale=None, q=None, q_out=None,
+                        k_out=None, status=None, want_k=False):
+    """rope_kv_append with explicit positions on one or several axes (tts_rope_kv_append_axes):
+    positions int32 [axes, tokens], pair_axis bytes of head_dim/2 axes (rope_axes), cos_sin fp32
+    [max_pos, head_dim/2, 2]. Images and video in a prompt, and drafted trees (one axis: the
+    depth behind the cached tokens). Everything else, and what is returned, as there."""
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if want_k and k_out is None:
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+    code = (_nat or _binding()).rope_kv_append_axes(
+        k, v, k_cache, v_cache, page_tables, past_lens, cu_new, max_new, k_scale, v_scale, cos_sin,
+        q, q_out, k_out, status, positions, pair_axis)
+    if code:
+        raise TTSError(code, "tts_rope_kv_append_axes")
+    return q_out, k_out
+
+
+def attn_decode_tree_workspace_bytes(max_seqlen_q, num_heads_q, num_heads_kv, head_dim) -> int:
+    return int(lib().tts_attn_decode_tree_workspace_bytes(int(max_seqlen_q), int(num_heads_q),
+                                                          int(num_heads_kv), int(head_dim)))
+
+
+def attn_decode_tree(q, k_cache, v_cache, page_tables, kv_lens, tree_mask, scale, cu_seqlens_q=None,
+                     max_seqlen_q=1, k_scale=None, v_scale=None, window=0, sinks=0, out=None,
+                     lse=None, workspace=None, status=None, want_lse=True,
+                     out_dtype=torch.float32):
+    """Attention of a drafted tree's tokens over a paged grouped-query cache
+    (tts_attn_decode_tree): as attn_decode_paged, but of its request's new tokens a token sees those
+    of its mask. tree_mask int64 [tokens]: bit m, the request's new token m is seen (a tree's
+    token has its ancestors' bits and its own)."""
+    out, lse = _attn_outputs(q, out, lse, want_lse, out_dtype)
+    call = (_nat or _binding()).attn_decode_tree
+    code = call(q, k_cache, v_cache, k_scale, v_scale, page_tables, kv_lens, cu_seqlens_q,
+                max_seqlen_q, window, sinks, scale, out, lse, workspace, status, tree_mask)
+    if code == TTS_ERR_WORKSPACE:  # missing or too small: nothing was enqueued
+        with torch.cuda.device(q.device):
+            need = attn_decode_tree_workspace_bytes(max_seqlen_q, q.shape[1], k_cache.shape[1],
+                                                    q.shape[2])
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        code = call(q, k_cache, v_cache, k_scale, v_scale, page_tables, kv_lens, cu_seqlens_q,
+                    max_seqlen_q, window, sinks, scale, out, lse, workspace, status, tree_mask)
+    if code:
+        raise TTSError(code, "tts_attn_decode_tree")
+    return out, lse
+
+
+def kv_compact(k_cache, v_cache, page_tables, past_lens, path, path_lens, k_scale=None,
+               v_scale=None, kv_lens=None, status=None):
+    """Brings the accepted path of each request's drafted tree together in the cache
+    (tts_kv_compact): of the new tokens behind past_lens[r] cached ones, path[r, :path_lens[r]]
+    (int32 [batch, max_path], increasing, counted from 0) are kept, moved to the slots from
+    past_lens[r] on. In place; returns kv_lens int32 [batch] = past_lens + path_lens."""
+    if kv_lens is None:
+        kv_lens = torch.empty_like(past_lens)
+    code = (_nat or _binding()).kv_compact(k_cache, v_cache, page_tables, past_lens, path, path_lens,
+                                          k_scale, v_scale, kv_lens, status)
+    if code:
+        raise TTSError(code, "tts_kv_compact")
+    return kv_lens
+
+
+def kv_fork(k_cache, v_cache, page_tables, kv_lens, parents, new_pages, k_scale=None, v_scale=None,
+            tables_out=None, lens_out=None, status=None):
+    """Requests that continue others' cached tokens (tts_kv_fork): new request i shares the full
+    pages of request parents[i] (row of page_tables) and gets a copy of its last, partly filled
+    page in new_pages[i] (int32, free pages; -1: the parent's row is taken as it is). Returns
+    (tables int32 [children, max_pages], lengths int32 [children])."""
+    if tables_out is None:
+        tables_out = torch.empty((parents.numel(), page_tables.shape[1]), dtype=torch.int32,
+                                 device=parents.device)
+    if lens_out is None:
+        lens_out = torch.empty(parents.numel(), dtype=torch.int32, device=parents.device)
+    code = (_nat or _binding()).kv_fork(k_cache, v_cache, page_tables, kv_lens, parents, new_pages,
+                                        k_scale, v_scale, tables_out, lens_out, status)
+    if code:
+        raise TTSError(code, "tts_kv_fork")
+    return tables_out, lens_out
+
+
+def qkv_rope_axes(x, w, bias, positions, pair_axis, cos_sin, num_heads, q=None, k=None, v=None,
+                  status=None):
+    """qkv_rope with positions on several axes (tts_qkv_rope_axes): positions int32 [axes, n] (row
+    and column of a patch, time in front of them for video), pair_axis bytes of head_dim/2 axes
+    (rope_axes), cos_sin fp32 [max_pos, d/2, 2] with each pair's own frequencies. Returns
+    (q, k, v) bf16 [n, H, d]."""
+    _need(isinstance(x, torch.Tensor) and x.dim() == 2 and w.dim() == 2 and int(num_heads) > 0,
+          "x [n, hidden], w [3*H*d, hidden]")
+    shape = (x.shape[0], int(num_heads), w.shape[0] // (3 * int(num_heads)))
+    q, k, v = (torch.empty(shape, dtype=torch.bfloat16, device=x.device) if t is None else t
+               for t in (q, k, v))
+    code = (_nat or _binding()).qkv_rope_axes(x, w, bias, positions, pair_axis, cos_sin,
+                                              int(num_heads), q, k, v, status)
+    if code:
+        raise TTSError(code, "tts_qkv_rope_axes")
+    return q, k, v

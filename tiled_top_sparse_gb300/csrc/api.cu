@@ -62,6 +62,19 @@ inline tts_status from_cuda(cudaError_t e) {
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 constexpr size_t kCounterBytes = 256;  // attention workspace: work-item counter
 constexpr int kDecodeMaxQ = 64;        // new tokens per request of tts_attn_decode_paged
+constexpr int kMaxAxes = 4;            // position axes, two bits a rotation pair
+
+// The axis of every rotation pair: a host array of `pairs` entries below num_axes.
+inline bool axes_fit(int32_t num_axes, const uint8_t* pair_axis, int pairs) {
+  if (num_axes < 1 || num_axes > kMaxAxes || pair_axis == nullptr) return false;
+  for (int j = 0; j < pairs; ++j)
+    if (pair_axis[j] >= num_axes) return false;
+  return true;
+}
+inline void pack_axes(const uint8_t* pair_axis, int pairs, uint64_t (&to)[2]) {
+  to[0] = to[1] = 0;
+  for (int j = 0; j < pairs; ++j) to[j / 32] |= (uint64_t)pair_axis[j] << (2 * (j % 32));
+}
 
 // Shapes of the grouped-query cache that the append and decode kernels are built for; a
 // request's positions and the cache's rows stay below 2^30, so that sums of a position, a
@@ -441,15 +454,18 @@ tts_status tts_attn_fwd_varlen_fp8(const void* q8, const float* q_scale, const v
   return from_cuda(e);
 }
 
-tts_status tts_rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads_q, const void* k,
-                              int64_t k_stride, const void* v, int64_t v_stride,
-                              int64_t total_new, const int32_t* cu_new, const int32_t* past_lens,
-                              int32_t batch, int32_t max_new, int32_t num_heads_kv,
-                              int32_t head_dim, const float* cos_sin, int32_t max_pos,
-                              const int32_t* page_tables, int32_t max_pages, void* k_cache,
-                              void* v_cache, float* k_scale, float* v_scale,
-                              tts_dtype cache_dtype, int32_t num_pages, int32_t page_size,
-                              void* q_out, void* k_out, uint32_t* dev_status, void* stream) {
+// Both appends; num_axes 0: positions past + i.
+static tts_status rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads_q,
+                                 const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                 int64_t total_new, const int32_t* cu_new,
+                                 const int32_t* past_lens, int32_t batch, int32_t max_new,
+                                 int32_t num_heads_kv, int32_t head_dim, const float* cos_sin,
+                                 int32_t max_pos, const int32_t* positions, int32_t num_axes,
+                                 const uint8_t* pair_axis, const int32_t* page_tables,
+                                 int32_t max_pages, void* k_cache, void* v_cache, float* k_scale,
+                                 float* v_scale, tts_dtype cache_dtype, int32_t num_pages,
+                                 int32_t page_size, void* q_out, void* k_out,
+                                 uint32_t* dev_status, void* stream) {
   if (total_new < 0 || batch < 1 || max_new < 0 || num_heads_kv < 1 || head_dim < 1 ||
       max_pages < 1 || num_pages < 1 || page_size < 1)
     return TTS_ERR_INVALID_ARG;
@@ -505,11 +521,130 @@ tts_status tts_rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads
   a.q_out = q_out;
   a.k_out = k_out;
   a.dev_status = dev_status;
+  if (num_axes > 0) {
+    a.positions = positions;
+    a.axes = num_axes;
+    pack_axes(pair_axis, head_dim / 2, a.pair_axis);
+  }
   return from_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
 }
 
-size_t tts_attn_decode_workspace_bytes(int32_t max_seqlen_q, int32_t num_heads_q,
-                                       int32_t num_heads_kv, int32_t head_dim) {
+tts_status tts_rope_kv_append(const void* q, int64_t q_stride, int32_t num_heads_q, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride,
+                              int64_t total_new, const int32_t* cu_new, const int32_t* past_lens,
+                              int32_t batch, int32_t max_new, int32_t num_heads_kv,
+                              int32_t head_dim, const float* cos_sin, int32_t max_pos,
+                              const int32_t* page_tables, int32_t max_pages, void* k_cache,
+                              void* v_cache, float* k_scale, float* v_scale,
+                              tts_dtype cache_dtype, int32_t num_pages, int32_t page_size,
+                              void* q_out, void* k_out, uint32_t* dev_status, void* stream) {
+  return rope_kv_append(q, q_stride, num_heads_q, k, k_stride, v, v_stride, total_new, cu_new,
+                        past_lens, batch, max_new, num_heads_kv, head_dim, cos_sin, max_pos,
+                        nullptr, 0, nullptr, page_tables, max_pages, k_cache, v_cache, k_scale,
+                        v_scale, cache_dtype, num_pages, page_size, q_out, k_out, dev_status,
+                        stream);
+}
+
+tts_status tts_rope_kv_append_axes(
+    const void* q, int64_t q_stride, int32_t num_heads_q, const void* k, int64_t k_stride,
+    const void* v, int64_t v_stride, int64_t total_new, const int32_t* cu_new,
+    const int32_t* past_lens, int32_t batch, int32_t max_new, int32_t num_heads_kv,
+    int32_t head_dim, const float* cos_sin, int32_t max_pos, const int32_t* positions,
+    int32_t num_axes, const uint8_t* pair_axis, const int32_t* page_tables, int32_t max_pages,
+    void* k_cache, void* v_cache, float* k_scale, float* v_scale, tts_dtype cache_dtype,
+    int32_t num_pages, int32_t page_size, void* q_out, void* k_out, uint32_t* dev_status,
+    void* stream) {
+  if (head_dim != 64 && head_dim != 128)
+    return head_dim < 1 ? TTS_ERR_INVALID_ARG : TTS_ERR_UNSUPPORTED;
+  if (!axes_fit(num_axes, pair_axis, head_dim / 2)) return TTS_ERR_INVALID_ARG;
+  if (total_new > 0 && max_new > 0 && (positions == nullptr || cos_sin == nullptr))
+    return TTS_ERR_INVALID_ARG;
+  return rope_kv_append(q, q_stride, num_heads_q, k, k_stride, v, v_stride, total_new, cu_new,
+                        past_lens, batch, max_new, num_heads_kv, head_dim, cos_sin, max_pos,
+                        positions, num_axes, pair_axis, page_tables, max_pages, k_cache, v_cache,
+                        k_scale, v_scale, cache_dtype, num_pages, page_size, q_out, k_out,
+                        dev_status, stream);
+}
+
+// A cache that rows are moved in, and the calls' other sizes.
+static tts_status moved_cache(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                              tts_dtype cache_dtype, int32_t num_pages, int32_t num_heads_kv,
+                              int32_t page_size, int32_t head_dim, int32_t max_pages,
+                              KvCache* c) {
+  if (num_pages < 1 || num_heads_kv < 1 || page_size < 1 || head_dim < 1 || max_pages < 1)
+    return TTS_ERR_INVALID_ARG;
+  if (cache_dtype != TTS_BF16 && cache_dtype != TTS_E4M3) return TTS_ERR_INVALID_ARG;
+  if (!cache_shape_built(head_dim, page_size, num_pages, max_pages, num_heads_kv))
+    return TTS_ERR_UNSUPPORTED;
+  if (k_cache == nullptr || v_cache == nullptr || !aligned16(k_cache) || !aligned16(v_cache))
+    return TTS_ERR_INVALID_ARG;
+  if (cache_dtype == TTS_E4M3 && (k_scale == nullptr || v_scale == nullptr))
+    return TTS_ERR_INVALID_ARG;
+  *c = {k_cache, v_cache, k_scale, v_scale, cache_dtype == TTS_E4M3, num_pages, num_heads_kv,
+        page_size, head_dim};
+  return TTS_OK;
+}
+
+tts_status tts_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                          tts_dtype cache_dtype, int32_t num_pages, int32_t num_heads_kv,
+                          int32_t page_size, int32_t head_dim, const int32_t* page_tables,
+                          int32_t max_pages, const int32_t* past_lens, int32_t batch,
+                          const int32_t* path, int32_t max_path, const int32_t* path_lens,
+                          int32_t* kv_lens, uint32_t* dev_status, void* stream) {
+  if (batch < 1 || max_path < 0) return TTS_ERR_INVALID_ARG;
+  KvCompactArgs a;
+  const tts_status st = moved_cache(k_cache, v_cache, k_scale, v_scale, cache_dtype, num_pages,
+                                    num_heads_kv, page_size, head_dim, max_pages, &a.cache);
+  if (st != TTS_OK) return st;
+  if (max_path > kDecodeMaxQ) return TTS_ERR_UNSUPPORTED;
+  if (page_tables == nullptr || past_lens == nullptr || path_lens == nullptr ||
+      kv_lens == nullptr || (path == nullptr && max_path > 0) || kv_lens == past_lens)
+    return TTS_ERR_INVALID_ARG;
+  a.page_tables = page_tables;
+  a.max_pages = max_pages;
+  a.batch = batch;
+  a.max_path = max_path;
+  a.past_lens = past_lens;
+  a.path = path;
+  a.path_lens = path_lens;
+  a.kv_lens = kv_lens;
+  a.dev_status = dev_status;
+  return from_cuda(launch_kv_compact(a, static_cast<cudaStream_t>(stream)));
+}
+
+tts_status tts_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                       tts_dtype cache_dtype, int32_t num_pages, int32_t num_heads_kv,
+                       int32_t page_size, int32_t head_dim, const int32_t* page_tables,
+                       int32_t max_pages, const int32_t* kv_lens, int32_t batch,
+                       const int32_t* parents, const int32_t* new_pages, int32_t children,
+                       int32_t* tables_out, int32_t* lens_out, uint32_t* dev_status,
+                       void* stream) {
+  if (batch < 1 || children < 0) return TTS_ERR_INVALID_ARG;
+  KvForkArgs a;
+  const tts_status st = moved_cache(k_cache, v_cache, k_scale, v_scale, cache_dtype, num_pages,
+                                    num_heads_kv, page_size, head_dim, max_pages, &a.cache);
+  if (st != TTS_OK) return st;
+  if (children == 0) return TTS_OK;  // nothing to write
+  if (page_tables == nullptr || kv_lens == nullptr || parents == nullptr || new_pages == nullptr ||
+      tables_out == nullptr || lens_out == nullptr || tables_out == page_tables ||
+      lens_out == kv_lens)
+    return TTS_ERR_INVALID_ARG;
+  a.page_tables = page_tables;
+  a.max_pages = max_pages;
+  a.batch = batch;
+  a.children = children;
+  a.kv_lens = kv_lens;
+  a.parents = parents;
+  a.new_pages = new_pages;
+  a.tables_out = tables_out;
+  a.lens_out = lens_out;
+  a.dev_status = dev_status;
+  return from_cuda(launch_kv_fork(a, static_cast<cudaStream_t>(stream)));
+}
+
+// Workspace of either attention over the cache on the current device.
+static size_t decode_workspace(bool tree, int32_t max_seqlen_q, int32_t num_heads_q,
+                               int32_t num_heads_kv, int32_t head_dim) {
   if (max_seqlen_q < 1 || max_seqlen_q > kDecodeMaxQ || num_heads_q < 1 || num_heads_kv < 1 ||
       num_heads_q % num_heads_kv != 0 || (head_dim != 64 && head_dim != 128))
     return 0;
@@ -519,19 +654,31 @@ size_t tts_attn_decode_workspace_bytes(int32_t max_seqlen_q, int32_t num_heads_q
     cudaGetLastError();  // no device
     return 0;
   }
-  return attn_decode_workspace_bytes(max_seqlen_q, num_heads_q, num_heads_kv, head_dim, sms);
+  return (tree ? attn_tree_workspace_bytes : attn_decode_workspace_bytes)(
+      max_seqlen_q, num_heads_q, num_heads_kv, head_dim, sms);
 }
 
-tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* cu_seqlens_q,
-                                 int32_t batch, int32_t max_seqlen_q, int32_t num_heads_q,
-                                 int32_t num_heads_kv, int32_t head_dim, const void* k_cache,
-                                 const void* v_cache, const float* k_scale, const float* v_scale,
-                                 tts_dtype cache_dtype, int32_t num_pages, int32_t page_size,
-                                 const int32_t* page_tables, int32_t max_pages,
-                                 const int32_t* kv_lens, int32_t window, int32_t sinks,
-                                 float scale, void* out, tts_dtype out_dtype, float* lse,
-                                 void* workspace, size_t workspace_bytes, uint32_t* dev_status,
-                                 void* stream) {
+size_t tts_attn_decode_workspace_bytes(int32_t max_seqlen_q, int32_t num_heads_q,
+                                       int32_t num_heads_kv, int32_t head_dim) {
+  return decode_workspace(false, max_seqlen_q, num_heads_q, num_heads_kv, head_dim);
+}
+
+size_t tts_attn_decode_tree_workspace_bytes(int32_t max_seqlen_q, int32_t num_heads_q,
+                                            int32_t num_heads_kv, int32_t head_dim) {
+  return decode_workspace(true, max_seqlen_q, num_heads_q, num_heads_kv, head_dim);
+}
+
+// Attention over the cache; tree: with a mask of the new tokens for each of them.
+static tts_status attn_decode(bool tree, const void* q, int64_t total_q,
+                              const int32_t* cu_seqlens_q, const uint64_t* tree_mask,
+                              int32_t batch, int32_t max_seqlen_q, int32_t num_heads_q,
+                              int32_t num_heads_kv, int32_t head_dim, const void* k_cache,
+                              const void* v_cache, const float* k_scale, const float* v_scale,
+                              tts_dtype cache_dtype, int32_t num_pages, int32_t page_size,
+                              const int32_t* page_tables, int32_t max_pages,
+                              const int32_t* kv_lens, int32_t window, int32_t sinks, float scale,
+                              void* out, tts_dtype out_dtype, float* lse, void* workspace,
+                              size_t workspace_bytes, uint32_t* dev_status, void* stream) {
   if (total_q < 0 || batch < 1 || max_seqlen_q < 1 || num_heads_q < 1 || num_heads_kv < 1 ||
       head_dim < 1 || num_pages < 1 || page_size < 1 || max_pages < 1 || window < 0 || sinks < 0)
     return TTS_ERR_INVALID_ARG;
@@ -551,7 +698,7 @@ tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* 
   if (tiles > 2e9) return TTS_ERR_UNSUPPORTED;
   if (total_q == 0) return TTS_OK;  // nothing to compute
   if (q == nullptr || k_cache == nullptr || v_cache == nullptr || page_tables == nullptr ||
-      kv_lens == nullptr || out == nullptr)
+      kv_lens == nullptr || out == nullptr || (tree && tree_mask == nullptr))
     return TTS_ERR_INVALID_ARG;
   if (cache_dtype == TTS_E4M3 && (k_scale == nullptr || v_scale == nullptr))
     return TTS_ERR_INVALID_ARG;
@@ -559,8 +706,7 @@ tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* 
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
     return TTS_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned16(workspace) ||
-      workspace_bytes < tts_attn_decode_workspace_bytes(max_seqlen_q, num_heads_q, num_heads_kv,
-                                                        head_dim))
+      workspace_bytes < decode_workspace(tree, max_seqlen_q, num_heads_q, num_heads_kv, head_dim))
     return TTS_ERR_WORKSPACE;
   AttnDecodeArgs a;
   a.q = q;
@@ -590,10 +736,44 @@ tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* 
   a.lse = lse;
   a.workspace = workspace;
   a.dev_status = dev_status;
+  a.tree_mask = tree_mask;
   int drv = 0;
-  const cudaError_t e = launch_attn_decode(a, &drv, static_cast<cudaStream_t>(stream));
+  const cudaError_t e =
+      (tree ? launch_attn_tree : launch_attn_decode)(a, &drv, static_cast<cudaStream_t>(stream));
   if (drv != 0) return TTS_ERR_CUDA;
   return from_cuda(e);
+}
+
+tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* cu_seqlens_q,
+                                 int32_t batch, int32_t max_seqlen_q, int32_t num_heads_q,
+                                 int32_t num_heads_kv, int32_t head_dim, const void* k_cache,
+                                 const void* v_cache, const float* k_scale, const float* v_scale,
+                                 tts_dtype cache_dtype, int32_t num_pages, int32_t page_size,
+                                 const int32_t* page_tables, int32_t max_pages,
+                                 const int32_t* kv_lens, int32_t window, int32_t sinks,
+                                 float scale, void* out, tts_dtype out_dtype, float* lse,
+                                 void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                 void* stream) {
+  return attn_decode(false, q, total_q, cu_seqlens_q, nullptr, batch, max_seqlen_q, num_heads_q,
+                     num_heads_kv, head_dim, k_cache, v_cache, k_scale, v_scale, cache_dtype,
+                     num_pages, page_size, page_tables, max_pages, kv_lens, window, sinks, scale,
+                     out, out_dtype, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
+tts_status tts_attn_decode_tree(const void* q, int64_t total_q, const int32_t* cu_seqlens_q,
+                                const uint64_t* tree_mask, int32_t batch, int32_t max_seqlen_q,
+                                int32_t num_heads_q, int32_t num_heads_kv, int32_t head_dim,
+                                const void* k_cache, const void* v_cache, const float* k_scale,
+                                const float* v_scale, tts_dtype cache_dtype, int32_t num_pages,
+                                int32_t page_size, const int32_t* page_tables, int32_t max_pages,
+                                const int32_t* kv_lens, int32_t window, int32_t sinks,
+                                float scale, void* out, tts_dtype out_dtype, float* lse,
+                                void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                void* stream) {
+  return attn_decode(true, q, total_q, cu_seqlens_q, tree_mask, batch, max_seqlen_q, num_heads_q,
+                     num_heads_kv, head_dim, k_cache, v_cache, k_scale, v_scale, cache_dtype,
+                     num_pages, page_size, page_tables, max_pages, kv_lens, window, sinks, scale,
+                     out, out_dtype, lse, workspace, workspace_bytes, dev_status, stream);
 }
 
 tts_status tts_rope_cache(int32_t max_pos, int32_t rot_dim, float base, float* cos_sin,
@@ -605,10 +785,12 @@ tts_status tts_rope_cache(int32_t max_pos, int32_t rot_dim, float base, float* c
                                      static_cast<cudaStream_t>(stream)));
 }
 
-tts_status tts_qkv_rope(const void* x, int64_t n, int32_t hidden, const void* w,
-                        const float* bias, const int32_t* positions, const float* cos_sin,
-                        int32_t max_pos, int32_t num_heads, int32_t head_dim, void* q, void* k,
-                        void* v, uint32_t* dev_status, void* stream) {
+// Both projections; num_axes 0: positions [n], one axis.
+static tts_status qkv_rope(const void* x, int64_t n, int32_t hidden, const void* w,
+                           const float* bias, const int32_t* positions, int32_t num_axes,
+                           const uint8_t* pair_axis, const float* cos_sin, int32_t max_pos,
+                           int32_t num_heads, int32_t head_dim, void* q, void* k, void* v,
+                           uint32_t* dev_status, void* stream) {
   if (n < 0 || n > 0x7FFFFFFFLL || hidden < 8 || hidden % 8 != 0 || max_pos < 1 ||
       num_heads < 1 || head_dim < 2)
     return TTS_ERR_INVALID_ARG;
@@ -637,10 +819,34 @@ tts_status tts_qkv_rope(const void* x, int64_t n, int32_t hidden, const void* w,
   a.k = k;
   a.v = v;
   a.dev_status = dev_status;
+  if (num_axes > 0) {
+    a.axes = num_axes;
+    pack_axes(pair_axis, head_dim / 2, a.pair_axis);
+  }
   int drv = 0;
   cudaError_t e = launch_qkv_rope(a, &drv, static_cast<cudaStream_t>(stream));
   if (drv != 0) return TTS_ERR_CUDA;
   return from_cuda(e);
+}
+
+tts_status tts_qkv_rope(const void* x, int64_t n, int32_t hidden, const void* w,
+                        const float* bias, const int32_t* positions, const float* cos_sin,
+                        int32_t max_pos, int32_t num_heads, int32_t head_dim, void* q, void* k,
+                        void* v, uint32_t* dev_status, void* stream) {
+  return qkv_rope(x, n, hidden, w, bias, positions, 0, nullptr, cos_sin, max_pos, num_heads,
+                  head_dim, q, k, v, dev_status, stream);
+}
+
+tts_status tts_qkv_rope_axes(const void* x, int64_t n, int32_t hidden, const void* w,
+                             const float* bias, const int32_t* positions, int32_t num_axes,
+                             const uint8_t* pair_axis, const float* cos_sin, int32_t max_pos,
+                             int32_t num_heads, int32_t head_dim, void* q, void* k, void* v,
+                             uint32_t* dev_status, void* stream) {
+  if (head_dim < 2) return TTS_ERR_INVALID_ARG;
+  if (qkv_heads_per_tile(head_dim) == 0) return TTS_ERR_UNSUPPORTED;
+  if (!axes_fit(num_axes, pair_axis, head_dim / 2)) return TTS_ERR_INVALID_ARG;
+  return qkv_rope(x, n, hidden, w, bias, positions, num_axes, pair_axis, cos_sin, max_pos,
+                  num_heads, head_dim, q, k, v, dev_status, stream);
 }
 
 }  // extern "C"

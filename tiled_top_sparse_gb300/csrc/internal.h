@@ -49,8 +49,46 @@ struct KvAppendArgs {
   void* q_out;
   void* k_out;  // may be null
   uint32_t* dev_status;
+  // Explicit positions [axes, total_new] (null: past + i); pair j takes the one on axis
+  // (pair_axis[j / 32] >> 2 (j % 32)) & 3.
+  const int32_t* positions = nullptr;
+  int axes = 0;
+  uint64_t pair_axis[2] = {0, 0};
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
+
+// ---- rows moved inside that cache
+struct KvCache {
+  void* k;  // [num_pages, hkv, page_size, d] bf16 or e4m3
+  void* v;
+  float* k_scale;  // [num_pages, hkv] (e4m3)
+  float* v_scale;
+  bool f8;
+  int num_pages, hkv, page_size, d;
+};
+struct KvCompactArgs {
+  KvCache cache;
+  const int32_t* page_tables;
+  int max_pages, batch, max_path;
+  const int32_t* past_lens;
+  const int32_t* path;  // [batch, max_path]
+  const int32_t* path_lens;
+  int32_t* kv_lens;
+  uint32_t* dev_status;
+};
+cudaError_t launch_kv_compact(const KvCompactArgs& a, cudaStream_t stream);
+struct KvForkArgs {
+  KvCache cache;
+  const int32_t* page_tables;
+  int max_pages, batch, children;
+  const int32_t* kv_lens;
+  const int32_t* parents;
+  const int32_t* new_pages;
+  int32_t* tables_out;  // [children, max_pages]
+  int32_t* lens_out;
+  uint32_t* dev_status;
+};
+cudaError_t launch_kv_fork(const KvForkArgs& a, cudaStream_t stream);
 
 // ---- attention of a few new tokens over that cache
 struct AttnDecodeArgs {
@@ -74,9 +112,13 @@ struct AttnDecodeArgs {
   float* lse;
   void* workspace;
   uint32_t* dev_status;
+  // Drafted trees: bit m of a token's mask says that it sees its request's new token m.
+  const uint64_t* tree_mask = nullptr;  // [total_q]
 };
 size_t attn_decode_workspace_bytes(int max_q, int hq, int hkv, int d, int sms);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, int* drv_err, cudaStream_t stream);
+size_t attn_tree_workspace_bytes(int max_q, int hq, int hkv, int d, int sms);
+cudaError_t launch_attn_tree(const AttnDecodeArgs& a, int* drv_err, cudaStream_t stream);
 
 // ---- dense attention
 struct AttnArgs {
@@ -140,6 +182,8 @@ struct QkvArgs {
   void* k;
   void* v;
   uint32_t* dev_status;
+  int axes = 0;  // positions [axes, n], pair_axis as in KvAppendArgs (0: one axis, all pairs)
+  uint64_t pair_axis[2] = {0, 0};
 };
 // Heads per output tile for head_dim (0: head_dim not built).
 int qkv_heads_per_tile(int head_dim);

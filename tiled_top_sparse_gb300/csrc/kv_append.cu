@@ -22,43 +22,13 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "e4m3.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "ptx.cuh"
 
 namespace tts {
 namespace {
-
-constexpr uint32_t kMinScaleExp = 127 - 60;
-
-// Smallest power of two s >= 2^-60 with amax <= 448 s (448 = 1.75 * 2^8); amax finite, >= 0.
-__device__ __forceinline__ float block_scale(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return __uint_as_float((uint32_t)(e > (int)kMinScaleExp ? e : (int)kMinScaleExp) << 23);
-}
-
-__device__ __forceinline__ float finite_abs(float x) {  // 0 for inf and NaN: they set no scale
-  const float a = fabsf(x);
-  return a < INFINITY ? a : 0.f;
-}
-
-// Two values to e4m3 (nearest even, saturating), lo in the low byte.
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Two e4m3 codes (low byte first) to floats, exactly.
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-  float2 f;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-      : "=f"(f.x), "=f"(f.y)
-      : "r"(h));
-  return f;
-}
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -92,6 +62,35 @@ __device__ __forceinline__ void load_turn(const float* __restrict__ cs, Turn& t)
     t.s[2 * i + 1] = v.w;
   }
 }
+// The same with explicit positions: pair j turns by the table's row at the token's position on axis
+// pair_axis[j] (two bits a pair). False, and no turn, where a position lies outside the table.
+template <int D>
+__device__ __forceinline__ bool load_turn_axes(const KvAppendArgs& p, int64_t tok, int c, Turn& t) {
+  int pos[4];
+  bool ok = true;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    pos[a] = 0;
+    if (a < p.axes) pos[a] = __ldg(p.positions + a * p.total_new + tok);
+    ok = ok && pos[a] >= 0 && pos[a] < p.max_pos;
+  }
+  const uint32_t axis = (uint32_t)(p.pair_axis[c >> 2] >> ((c & 3) * 16)) & 0xFFFFu;
+  auto row = [&](uint32_t a) -> const float* {  // pairs [8c, 8c + 8) at the position on axis a
+    const int at = !ok ? 0 : a & 2 ? (a & 1 ? pos[3] : pos[2]) : (a & 1 ? pos[1] : pos[0]);
+    return p.cos_sin + ((int64_t)at * (D / 2) + c * 8) * 2;
+  };
+  if (axis == (axis & 3) * 0x5555u) {
+    load_turn(row(axis & 3), t);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = __ldg(reinterpret_cast<const float2*>(row((axis >> (2 * i)) & 3)) + i);
+      t.c[i] = v.x;
+      t.s[i] = v.y;
+    }
+  }
+  return ok;
+}
 // The rotation, every product and sum rounded on its own (no contraction: the result does
 // not depend on which of two products an FMA would keep exact).
 __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Turn& t) {
@@ -109,6 +108,7 @@ struct Req {
   int past;    // tokens already in the cache
   bool ok;     // positions fit the page table and the cos/sin table
 };
+template <bool kAxes>
 __device__ __forceinline__ Req make_req(const KvAppendArgs& p, int a, int e, int past,
                                         uint32_t* bad) {
   Req r;
@@ -123,18 +123,20 @@ __device__ __forceinline__ Req make_req(const KvAppendArgs& p, int a, int e, int
   r.n = e - a;
   const int64_t end = (int64_t)past + r.n;
   r.ok = past >= 0 && end <= ((int64_t)p.max_pages << p.page_shift) &&
-         (p.cos_sin == nullptr || end <= p.max_pos);
+         (kAxes || p.cos_sin == nullptr || end <= p.max_pos);
   if (!r.ok && r.n > 0) *bad |= kDevIndexRange;
   return r;
 }
+template <bool kAxes>
 __device__ __forceinline__ Req load_req(const KvAppendArgs& p, int b, uint32_t* bad) {
-  return make_req(p, p.cu_new[b], p.cu_new[b + 1], p.past_lens[b], bad);
+  return make_req<kAxes>(p, p.cu_new[b], p.cu_new[b + 1], p.past_lens[b], bad);
 }
 
 // The request that owns unit u, where request b owns units [cu[b] / size + 2b, cu[b+1] / size +
 // 2(b+1)): at least as many as it has pieces of `size` = 2^shift tokens, whatever their offset.
 // Warp-collective: the last b whose first unit is <= u, found 32 bounds at a time; with up to 32
 // requests the one round of loads brings the request itself too.
+template <bool kAxes>
 __device__ __forceinline__ Req find_request(const KvAppendArgs& p, int shift, int64_t u, int* b,
                                             int64_t* first) {
   const int lane = threadIdx.x & 31;
@@ -150,7 +152,7 @@ __device__ __forceinline__ Req find_request(const KvAppendArgs& p, int shift, in
     const uint32_t m = __ballot_sync(0xFFFFFFFFu, lane < p.batch && begin <= u);
     *b = m ? 31 - __clz(m) : 0;
     *first = __shfl_sync(0xFFFFFFFFu, begin, *b);
-    return make_req(p, __shfl_sync(0xFFFFFFFFu, a, *b), __shfl_sync(0xFFFFFFFFu, e, *b),
+    return make_req<kAxes>(p, __shfl_sync(0xFFFFFFFFu, a, *b), __shfl_sync(0xFFFFFFFFu, e, *b),
                     __shfl_sync(0xFFFFFFFFu, past, *b), &bad);
   }
   int lo = 0, span = p.batch;
@@ -167,14 +169,15 @@ __device__ __forceinline__ Req find_request(const KvAppendArgs& p, int shift, in
   }
   *b = lo;
   *first = (int64_t)(p.cu_new[lo] >> shift) + 2 * lo;
-  return load_req(p, lo, &bad);
+  return load_req<kAxes>(p, lo, &bad);
 }
 
 // Report bad requests once (block 0 of either kernel).
+template <bool kAxes>
 __device__ __forceinline__ void report(const KvAppendArgs& p) {
   if (p.dev_status == nullptr) return;
   uint32_t bad = 0;
-  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) load_req(p, b, &bad);
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) load_req<kAxes>(p, b, &bad);
   if (bad) atomicOr(p.dev_status, bad);
 }
 
@@ -183,7 +186,7 @@ __device__ __forceinline__ void report(const KvAppendArgs& p) {
 // `id` holds, per pass, 16 values of row id / (D/16): [8c, 8c + 8) and the same of the row's
 // second half, c = id % (D/16), i.e. both members of eight rotation pairs. kWarp: the threads
 // are one warp; else they are the block, and all of it comes here together.
-template <int D, bool kF8, int kPasses, bool kWarp>
+template <int D, bool kF8, int kPasses, bool kWarp, bool kAxes>
 __device__ __forceinline__ void append_page(const KvAppendArgs& p, int b, const Req& r, int pi,
                                             int g, bool is_v, int id, int lanes, float* s_red) {
   constexpr int kTpr = D / 16;  // threads per row
@@ -238,7 +241,18 @@ __device__ __forceinline__ void append_page(const KvAppendArgs& p, int b, const 
     float(&bb)[8] = *reinterpret_cast<float(*)[8]>(&x[s][8]);
     unpack8(raw[s][0], a);
     unpack8(raw[s][1], bb);
-    if (!is_v && p.cos_sin != nullptr && row < nr && r.ok) {
+    if constexpr (kAxes) {
+      if (!is_v && row < nr && r.ok) {
+        Turn t;
+        if (load_turn_axes<D>(p, tok0 + row, c, t)) {
+          rotate(a, bb, t);
+        } else {  // a position outside the table: reported, and the key is zeros
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[s][i] = 0.f;
+          if (c == 0 && g == 0 && p.dev_status != nullptr) atomicOr(p.dev_status, kDevIndexRange);
+        }
+      }
+    } else if (!is_v && p.cos_sin != nullptr && row < nr && r.ok) {
       Turn t;
       load_turn(p.cos_sin + ((int64_t)(lo + row) * (D / 2) + c * 8) * 2, t);
       rotate(a, bb, t);
@@ -336,14 +350,14 @@ constexpr int kQHeads = 8;  // q heads that share one load of the table row
 // of 16 to 32: 58 -> 53 us; pages of 64 in blocks of 512 threads instead of 256: 50 -> 64 us), and
 // that outweighs what it spills: 20 bytes a thread where a page takes one pass, 44 to 52 where it
 // takes two, none at 64 registers.
-template <int D, bool kF8, int kPasses, int kMost>
+template <int D, bool kF8, int kPasses, int kMost, bool kAxes>
 __global__ void __launch_bounds__(kMost, kMost == 256 ? 5 : 2) append_pages_kernel(const KvAppendArgs p,
                                                            uint64_t q_share, int q_shift,
                                                            int q_groups) {
   constexpr int kTpr = D / 16;
   __shared__ float s_red[16];
   wait_for_prior_grids();
-  if (blockIdx.x == 0) report(p);
+  if (blockIdx.x == 0) report<kAxes>(p);
   int64_t first;
   // q_share: the part of the blocks that rotates q, as a fraction of 2^32. The two kinds alternate at
   // that rate: what a page's block waits for (its reduction) is filled by a q block's plain
@@ -354,33 +368,37 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 5 : 2) append_pages_kern
     const int64_t u = kb / heads;
     const int hh = (int)(kb % heads);
     int b;
-    const Req r = find_request(p, p.page_shift, u, &b, &first);
-    append_page<D, kF8, kPasses, false>(p, b, r, (int)(u - first), hh >= p.hkv ? hh - p.hkv : hh,
+    const Req r = find_request<kAxes>(p, p.page_shift, u, &b, &first);
+    append_page<D, kF8, kPasses, false, kAxes>(p, b, r, (int)(u - first), hh >= p.hkv ? hh - p.hkv : hh,
                                         hh >= p.hkv, threadIdx.x, blockDim.x, s_red);
     return;
   }
   const int64_t u = qb / (unsigned)q_groups;
   const int h0 = (int)(qb % (unsigned)q_groups) * kQHeads;
   int b;
-  const Req r = find_request(p, q_shift, u, &b, &first);
+  const Req r = find_request<kAxes>(p, q_shift, u, &b, &first);
   const int c = threadIdx.x % kTpr;
   const int64_t i = ((u - first) << q_shift) + threadIdx.x / kTpr;
   if (i < 0 || i >= r.n) return;  // i < 0: units in front of a first bound above 0
   Turn t;
-  if (p.cos_sin != nullptr && r.ok) load_turn(p.cos_sin + ((r.past + i) * (D / 2) + c * 8) * 2, t);
+  bool ok = r.ok;
+  if constexpr (kAxes)
+    ok = ok && load_turn_axes<D>(p, r.t0 + i, c, t);
+  else if (p.cos_sin != nullptr && r.ok)
+    load_turn(p.cos_sin + ((r.past + i) * (D / 2) + c * 8) * 2, t);
   const int h1 = h0 + kQHeads < p.hq ? h0 + kQHeads : p.hq;
 #pragma unroll 8
-  for (int h = h0; h < h1; ++h) rotate_q_row<D>(p, r.ok, r.t0 + i, h, c, t);
+  for (int h = h0; h < h1; ++h) rotate_q_row<D>(p, ok, r.t0 + i, h, c, t);
 }
 
 // Steps (a few new tokens per request: all of a page's new rows fit one warp): a warp per
 // (request, touched page, head) of k and of v, then D/16 lanes per q row.
-template <int D, bool kF8>
+template <int D, bool kF8, bool kAxes>
 __global__ void __launch_bounds__(128) append_steps_kernel(const KvAppendArgs p, int pages_per,
                                                            int64_t kv_warps) {
   constexpr int kTpr = D / 16;
   wait_for_prior_grids();
-  if (blockIdx.x == 0) report(p);
+  if (blockIdx.x == 0) report<kAxes>(p);
   const int lane = threadIdx.x & 31;
   const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   uint32_t bad = 0;
@@ -389,8 +407,8 @@ __global__ void __launch_bounds__(128) append_steps_kernel(const KvAppendArgs p,
     const int hh = (int)(w % heads);
     const int64_t u = w / heads;
     const int b = (int)(u / pages_per);
-    const Req r = load_req(p, b, &bad);
-    append_page<D, kF8, 1, true>(p, b, r, (int)(u % pages_per), hh >= p.hkv ? hh - p.hkv : hh,
+    const Req r = load_req<kAxes>(p, b, &bad);
+    append_page<D, kF8, 1, true, kAxes>(p, b, r, (int)(u % pages_per), hh >= p.hkv ? hh - p.hkv : hh,
                                  hh >= p.hkv, lane, 32, nullptr);
     return;
   }
@@ -401,13 +419,16 @@ __global__ void __launch_bounds__(128) append_steps_kernel(const KvAppendArgs p,
   const int64_t b = bi / p.max_new;
   const int i = (int)(bi % p.max_new);
   if (b >= p.batch) return;
-  const Req r = load_req(p, (int)b, &bad);
+  const Req r = load_req<kAxes>(p, (int)b, &bad);
   if (i >= r.n) return;
   const int c = lane % kTpr;
   Turn t;
-  if (p.cos_sin != nullptr && r.ok)
+  bool ok = r.ok;
+  if constexpr (kAxes)
+    ok = ok && load_turn_axes<D>(p, r.t0 + i, c, t);
+  else if (p.cos_sin != nullptr && r.ok)
     load_turn(p.cos_sin + (((int64_t)r.past + i) * (D / 2) + c * 8) * 2, t);
-  rotate_q_row<D>(p, r.ok, r.t0 + i, h, c, t);
+  rotate_q_row<D>(p, ok, r.t0 + i, h, c, t);
 }
 
 int log2_of(int x) {
@@ -416,7 +437,7 @@ int log2_of(int x) {
   return s;
 }
 
-template <int D, bool kF8>
+template <int D, bool kF8, bool kAxes>
 cudaError_t launch_append(const KvAppendArgs& p, cudaStream_t stream) {
   constexpr int kTpr = D / 16, kRowsPerWarp = 32 / kTpr;
   if (p.max_new <= kRowsPerWarp) {
@@ -426,7 +447,7 @@ cudaError_t launch_append(const KvAppendArgs& p, cudaStream_t stream) {
     const int64_t warps = kv_warps + (q_rows + kRowsPerWarp - 1) / kRowsPerWarp;
     const int64_t blocks = (warps + 3) / 4;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch_ahead(append_steps_kernel<D, kF8>, dim3((unsigned)blocks), 128, 0, stream, p,
+    return launch_ahead(append_steps_kernel<D, kF8, kAxes>, dim3((unsigned)blocks), 128, 0, stream, p,
                         pages_per, kv_warps);
   }
   const int need = kTpr << p.page_shift;  // threads that hold a page in one pass
@@ -441,10 +462,16 @@ cudaError_t launch_append(const KvAppendArgs& p, cudaStream_t stream) {
   const unsigned grid = (unsigned)(kv_blocks + q_blocks);
   // rounded up: grid * q_share / 2^32 is then q_blocks exactly, for grid < 2^32
   const uint64_t q_share = (((uint64_t)q_blocks << 32) + grid - 1) / grid;
-  auto kernel = passes == 1   ? append_pages_kernel<D, kF8, 1, 256>
-                : most == 256 ? append_pages_kernel<D, kF8, 2, 256>
-                              : append_pages_kernel<D, kF8, 2, 512>;
+  auto kernel = passes == 1   ? append_pages_kernel<D, kF8, 1, 256, kAxes>
+                : most == 256 ? append_pages_kernel<D, kF8, 2, 256, kAxes>
+                              : append_pages_kernel<D, kF8, 2, 512, kAxes>;
   return launch_ahead(kernel, dim3(grid), threads, 0, stream, p, q_share, q_shift, q_groups);
+}
+
+template <int D, bool kF8>
+cudaError_t launch_positions(const KvAppendArgs& p, cudaStream_t stream) {
+  return p.positions != nullptr ? launch_append<D, kF8, true>(p, stream)
+                                : launch_append<D, kF8, false>(p, stream);
 }
 
 }  // namespace
@@ -452,9 +479,10 @@ cudaError_t launch_append(const KvAppendArgs& p, cudaStream_t stream) {
 cudaError_t launch_kv_append(const KvAppendArgs& args, cudaStream_t stream) {
   KvAppendArgs a = args;
   a.page_shift = log2_of(a.page_size);
-  if (a.d == 64) return a.f8 ? launch_append<64, true>(a, stream) : launch_append<64, false>(a, stream);
+  if (a.d == 64)
+    return a.f8 ? launch_positions<64, true>(a, stream) : launch_positions<64, false>(a, stream);
   if (a.d == 128)
-    return a.f8 ? launch_append<128, true>(a, stream) : launch_append<128, false>(a, stream);
+    return a.f8 ? launch_positions<128, true>(a, stream) : launch_positions<128, false>(a, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -28,11 +28,39 @@ typedef tts_status (*window_fn)(const void*, const void*, const void*, tts_dtype
                                 int32_t, int32_t, int32_t, int32_t, float, void*, tts_dtype, float*,
                                 void*, size_t, uint32_t*, void*);
 
+typedef tts_status (*append_axes_fn)(const void*, int64_t, int32_t, const void*, int64_t,
+                                     const void*, int64_t, int64_t, const int32_t*, const int32_t*,
+                                     int32_t, int32_t, int32_t, int32_t, const float*, int32_t,
+                                     const int32_t*, int32_t, const uint8_t*, const int32_t*,
+                                     int32_t, void*, void*, float*, float*, tts_dtype, int32_t,
+                                     int32_t, void*, void*, uint32_t*, void*);
+typedef tts_status (*tree_fn)(const void*, int64_t, const int32_t*, const uint64_t*, int32_t,
+                              int32_t, int32_t, int32_t, int32_t, const void*, const void*,
+                              const float*, const float*, tts_dtype, int32_t, int32_t,
+                              const int32_t*, int32_t, const int32_t*, int32_t, int32_t, float,
+                              void*, tts_dtype, float*, void*, size_t, uint32_t*, void*);
+typedef tts_status (*compact_fn)(void*, void*, float*, float*, tts_dtype, int32_t, int32_t, int32_t,
+                                 int32_t, const int32_t*, int32_t, const int32_t*, int32_t,
+                                 const int32_t*, int32_t, const int32_t*, int32_t*, uint32_t*,
+                                 void*);
+typedef tts_status (*fork_fn)(void*, void*, float*, float*, tts_dtype, int32_t, int32_t, int32_t,
+                              int32_t, const int32_t*, int32_t, const int32_t*, int32_t,
+                              const int32_t*, const int32_t*, int32_t, int32_t*, int32_t*,
+                              uint32_t*, void*);
+typedef tts_status (*qkv_axes_fn)(const void*, int64_t, int32_t, const void*, const float*,
+                                  const int32_t*, int32_t, const uint8_t*, const float*, int32_t,
+                                  int32_t, int32_t, void*, void*, void*, uint32_t*, void*);
+
 static append_fn f_append;
 static decode_fn f_decode;
 static window_fn f_window;
+static append_axes_fn f_append_axes;
+static tree_fn f_tree;
+static compact_fn f_compact;
+static fork_fn f_fork;
+static qkv_axes_fn f_qkv_axes;
 static PyObject *s_dtype, *s_shape, *s_get_device, *s_is_contiguous, *s_data_ptr, *s_stride, *s_nbytes;
-static PyObject *d_bf16, *d_f32, *d_u8, *d_e4m3, *d_i32;
+static PyObject *d_bf16, *d_f32, *d_u8, *d_e4m3, *d_i32, *d_i64;
 static PyObject *raw_stream, *get_device, *set_device;
 
 typedef struct {
@@ -226,9 +254,20 @@ static int nargs_are(Py_ssize_t n, Py_ssize_t want) {
   return -1;
 }
 
-static PyObject* rope_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  (void)self;
-  if (nargs_are(n, 15) < 0) return NULL;
+/* Explicit positions int32 [axes, tokens] and the axis of every rotation pair, as bytes. */
+static int axes(PyObject* positions, PyObject* pair_axis, long dev, int64_t tokens, int64_t pairs,
+                Tensor* pos, const uint8_t** axis) {
+  if (plain(positions, "positions", dev, d_i32, 2, pos) < 0) return -1;
+  if (pos->shape[1] != tokens || pos->shape[0] < 1)
+    return refuse("positions", "must be [axes, tokens]");
+  if (!PyBytes_Check(pair_axis) || PyBytes_GET_SIZE(pair_axis) != pairs)
+    return refuse("pair_axis", "must be bytes, one for each of the head_dim/2 pairs");
+  *axis = (const uint8_t*)PyBytes_AS_STRING(pair_axis);
+  return fits32(pos->shape[0], "axes");
+}
+
+/* Both appends; with_axes: the arguments go on with positions and pair_axis. */
+static PyObject* append(PyObject* const* a, int with_axes) {
   PyObject *k = a[0], *v = a[1], *q = a[11];
   const long dev = device_of(k, "k");
   if (dev < 0) return NULL;
@@ -289,10 +328,30 @@ static PyObject* rope_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n
   if (fits32(batch, "batch") < 0 || fits32(c.k.shape[0], "pages") < 0 ||
       fits32(pt.shape[1], "max_pages") < 0 || fits32(max_pos, "max_pos") < 0)
     return NULL;
+  Tensor pos;
+  const uint8_t* axis = NULL;
+  if (with_axes) {
+    if (axes(a[15], a[16], dev, total, d / 2, &pos, &axis) < 0) return NULL;
+    if (cs.ptr == NULL) {
+      refuse("cos_sin", "goes with positions");
+      return NULL;
+    }
+  }
   void* stream;
   long back;
   if (enter(dev, &stream, &back) < 0) return NULL;
   tts_status status;
+  if (with_axes) {
+    Py_BEGIN_ALLOW_THREADS
+    status = f_append_axes(tq.ptr, q_stride, (int32_t)hq, tk.ptr, k_stride, tv.ptr, v_stride, total,
+                           cu.ptr, past.ptr, (int32_t)batch, max_new, (int32_t)hkv, (int32_t)d,
+                           cs.ptr, (int32_t)max_pos, pos.ptr, (int32_t)pos.shape[0], axis, pt.ptr,
+                           (int32_t)pt.shape[1], c.k.ptr, c.v.ptr, c.ks.ptr, c.vs.ptr, c.code,
+                           (int32_t)c.k.shape[0], (int32_t)c.k.shape[2], qo.ptr, ko.ptr, st.ptr,
+                           stream);
+    Py_END_ALLOW_THREADS
+    return leave(back, status);
+  }
   Py_BEGIN_ALLOW_THREADS  /* a launch may block */
   status = f_append(tq.ptr, q_stride, (int32_t)hq, tk.ptr, k_stride, tv.ptr, v_stride, total,
                     cu.ptr, past.ptr, (int32_t)batch, max_new, (int32_t)hkv, (int32_t)d, cs.ptr,
@@ -301,6 +360,22 @@ static PyObject* rope_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n
                     st.ptr, stream);
   Py_END_ALLOW_THREADS
   return leave(back, status);
+}
+
+static int more_are(Py_ssize_t n, Py_ssize_t want) {
+  if (f_append_axes == NULL) {
+    PyErr_SetString(PyExc_RuntimeError, "bind_more() has not been called");
+    return -1;
+  }
+  return nargs_are(n, want);
+}
+static PyObject* rope_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  return nargs_are(n, 15) < 0 ? NULL : append(a, 0);
+}
+static PyObject* rope_kv_append_axes(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  return more_are(n, 17) < 0 ? NULL : append(a, 1);
 }
 
 /* out and lse of an attention call on q [tokens, heads, d]. */
@@ -325,9 +400,8 @@ static int scratch(PyObject* ws, long dev, Tensor* t, size_t* bytes) {
   return 0;
 }
 
-static PyObject* attn_decode_paged(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  (void)self;
-  if (nargs_are(n, 16) < 0) return NULL;
+/* Attention over the cache; tree: the arguments go on with the tokens' masks. */
+static PyObject* decode(PyObject* const* a, int tree) {
   const long dev = device_of(a[0], "q");
   if (dev < 0) return NULL;
   Cache c;
@@ -364,10 +438,29 @@ static PyObject* attn_decode_paged(PyObject* self, PyObject* const* a, Py_ssize_
   if (fits32(batch, "batch") < 0 || fits32(c.k.shape[0], "pages") < 0 ||
       fits32(pt.shape[1], "max_pages") < 0)
     return NULL;
+  Tensor mask;
+  if (tree) {
+    if (plain(a[16], "tree_mask", dev, d_i64, 1, &mask) < 0) return NULL;
+    if (mask.shape[0] != q.shape[0]) {
+      refuse("tree_mask", "must be [tokens]");
+      return NULL;
+    }
+  }
   void* stream;
   long back;
   if (enter(dev, &stream, &back) < 0) return NULL;
   tts_status status;
+  if (tree) {
+    Py_BEGIN_ALLOW_THREADS
+    status = f_tree(q.ptr, q.shape[0], cu.ptr, mask.ptr, (int32_t)batch, max_q,
+                    (int32_t)q.shape[1], (int32_t)c.k.shape[1], (int32_t)d, c.k.ptr, c.v.ptr,
+                    c.ks.ptr, c.vs.ptr, c.code, (int32_t)c.k.shape[0], (int32_t)c.k.shape[2],
+                    pt.ptr, (int32_t)pt.shape[1], lens.ptr, window, sinks, (float)scale, out.ptr,
+                    out.dtype == d_bf16 ? TTS_BF16 : TTS_F32, lse.ptr, ws.ptr, bytes, st.ptr,
+                    stream);
+    Py_END_ALLOW_THREADS
+    return leave(back, status);
+  }
   Py_BEGIN_ALLOW_THREADS  /* a launch may block */
   status = f_decode(q.ptr, q.shape[0], cu.ptr, (int32_t)batch, max_q, (int32_t)q.shape[1],
                     (int32_t)c.k.shape[1], (int32_t)d, c.k.ptr, c.v.ptr, c.ks.ptr, c.vs.ptr, c.code,
@@ -375,6 +468,151 @@ static PyObject* attn_decode_paged(PyObject* self, PyObject* const* a, Py_ssize_
                     lens.ptr, window, sinks, (float)scale, out.ptr,
                     out.dtype == d_bf16 ? TTS_BF16 : TTS_F32, lse.ptr, ws.ptr, bytes, st.ptr,
                     stream);
+  Py_END_ALLOW_THREADS
+  return leave(back, status);
+}
+
+static PyObject* attn_decode_paged(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  return nargs_are(n, 16) < 0 ? NULL : decode(a, 0);
+}
+static PyObject* attn_decode_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  return more_are(n, 17) < 0 ? NULL : decode(a, 1);
+}
+
+/* kv_compact(k_cache, v_cache, page_tables, past_lens, path, path_lens, k_scale, v_scale, kv_lens,
+ *            status) */
+static PyObject* kv_compact(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (more_are(n, 10) < 0) return NULL;
+  const long dev = device_of(a[0], "k_cache");
+  if (dev < 0) return NULL;
+  Cache c;
+  Tensor pt, past, path, count_of, lens, st;
+  if (cache(a[0], a[1], a[6], a[7], dev, &c) < 0 ||
+      plain(a[2], "page_tables", dev, d_i32, 2, &pt) < 0 ||
+      plain(a[3], "past_lens", dev, d_i32, -1, &past) < 0 ||
+      plain(a[4], "path", dev, d_i32, 2, &path) < 0 ||
+      plain(a[5], "path_lens", dev, d_i32, -1, &count_of) < 0 ||
+      plain(a[8], "kv_lens", dev, d_i32, -1, &lens) < 0 ||
+      optional(a[9], "status", dev, d_i32, -1, &st) < 0)
+    return NULL;
+  const int64_t batch = count(&past);
+  if (pt.shape[0] != batch || path.shape[0] != batch || count(&count_of) != batch ||
+      count(&lens) != batch) {
+    refuse("page_tables, past_lens, path, path_lens, kv_lens",
+           "must be [batch, max_pages], [batch], [batch, max_path], [batch], [batch]");
+    return NULL;
+  }
+  if (fits32(batch, "batch") < 0 || fits32(c.k.shape[0], "pages") < 0 ||
+      fits32(pt.shape[1], "max_pages") < 0 || fits32(path.shape[1], "max_path") < 0)
+    return NULL;
+  void* stream;
+  long back;
+  if (enter(dev, &stream, &back) < 0) return NULL;
+  tts_status status;
+  Py_BEGIN_ALLOW_THREADS
+  status = f_compact(c.k.ptr, c.v.ptr, c.ks.ptr, c.vs.ptr, c.code, (int32_t)c.k.shape[0],
+                     (int32_t)c.k.shape[1], (int32_t)c.k.shape[2], (int32_t)c.k.shape[3], pt.ptr,
+                     (int32_t)pt.shape[1], past.ptr, (int32_t)batch, path.ptr,
+                     (int32_t)path.shape[1], count_of.ptr, lens.ptr, st.ptr, stream);
+  Py_END_ALLOW_THREADS
+  return leave(back, status);
+}
+
+/* kv_fork(k_cache, v_cache, page_tables, kv_lens, parents, new_pages, k_scale, v_scale, tables_out,
+ *         lens_out, status) */
+static PyObject* kv_fork(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (more_are(n, 11) < 0) return NULL;
+  const long dev = device_of(a[0], "k_cache");
+  if (dev < 0) return NULL;
+  Cache c;
+  Tensor pt, lens, parents, pages, to, tl, st;
+  if (cache(a[0], a[1], a[6], a[7], dev, &c) < 0 ||
+      plain(a[2], "page_tables", dev, d_i32, 2, &pt) < 0 ||
+      plain(a[3], "kv_lens", dev, d_i32, -1, &lens) < 0 ||
+      plain(a[4], "parents", dev, d_i32, -1, &parents) < 0 ||
+      plain(a[5], "new_pages", dev, d_i32, -1, &pages) < 0 ||
+      plain(a[8], "tables_out", dev, d_i32, 2, &to) < 0 ||
+      plain(a[9], "lens_out", dev, d_i32, -1, &tl) < 0 ||
+      optional(a[10], "status", dev, d_i32, -1, &st) < 0)
+    return NULL;
+  const int64_t batch = count(&lens), children = count(&parents);
+  if (pt.shape[0] != batch) {
+    refuse("page_tables, kv_lens", "must be [batch, max_pages], [batch]");
+    return NULL;
+  }
+  if (count(&pages) != children || to.shape[0] != children || to.shape[1] != pt.shape[1] ||
+      count(&tl) != children) {
+    refuse("new_pages, tables_out, lens_out", "must be [children], [children, max_pages], [children]");
+    return NULL;
+  }
+  if (fits32(batch, "batch") < 0 || fits32(children, "children") < 0 ||
+      fits32(c.k.shape[0], "pages") < 0 || fits32(pt.shape[1], "max_pages") < 0)
+    return NULL;
+  void* stream;
+  long back;
+  if (enter(dev, &stream, &back) < 0) return NULL;
+  tts_status status;
+  Py_BEGIN_ALLOW_THREADS
+  status = f_fork(c.k.ptr, c.v.ptr, c.ks.ptr, c.vs.ptr, c.code, (int32_t)c.k.shape[0],
+                  (int32_t)c.k.shape[1], (int32_t)c.k.shape[2], (int32_t)c.k.shape[3], pt.ptr,
+                  (int32_t)pt.shape[1], lens.ptr, (int32_t)batch, parents.ptr, pages.ptr,
+                  (int32_t)children, to.ptr, tl.ptr, st.ptr, stream);
+  Py_END_ALLOW_THREADS
+  return leave(back, status);
+}
+
+/* qkv_rope_axes(x, w, bias, positions, pair_axis, cos_sin, num_heads, q, k, v, status) */
+static PyObject* qkv_rope_axes(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (more_are(n, 11) < 0) return NULL;
+  const long dev = device_of(a[0], "x");
+  if (dev < 0) return NULL;
+  Tensor x, w, bias, pos, cs, out[3], st;
+  const uint8_t* axis;
+  int32_t heads;
+  if (int32_arg(a[6], "num_heads", &heads) < 0 || plain(a[0], "x", dev, d_bf16, 2, &x) < 0 ||
+      plain(a[1], "w", dev, d_bf16, 2, &w) < 0 ||
+      optional(a[2], "bias", dev, d_f32, -1, &bias) < 0 ||
+      plain(a[5], "cos_sin", dev, d_f32, 3, &cs) < 0)
+    return NULL;
+  if (heads < 1 || w.shape[1] != x.shape[1] || w.shape[0] % (3 * (int64_t)heads) != 0 ||
+      w.shape[0] == 0) {
+    refuse("x and w", "must be [n, hidden] and [3 * num_heads * head_dim, hidden]");
+    return NULL;
+  }
+  const int64_t d = w.shape[0] / (3 * (int64_t)heads);
+  if (a[2] != Py_None && count(&bias) != w.shape[0]) {
+    refuse("bias", "must be [3 * num_heads * head_dim]");
+    return NULL;
+  }
+  if (cs.shape[0] < 1 || cs.shape[1] != d / 2 || cs.shape[2] != 2) {
+    refuse("cos_sin", "must be [max_pos, head_dim/2, 2] with a position at least");
+    return NULL;
+  }
+  if (axes(a[3], a[4], dev, x.shape[0], d / 2, &pos, &axis) < 0) return NULL;
+  static const char* const names[3] = {"q", "k", "v"};
+  for (int i = 0; i < 3; ++i) {
+    if (plain(a[7 + i], names[i], dev, d_bf16, 3, &out[i]) < 0) return NULL;
+    if (out[i].shape[0] != x.shape[0] || out[i].shape[1] != heads || out[i].shape[2] != d) {
+      refuse(names[i], "must be [n, num_heads, head_dim]");
+      return NULL;
+    }
+  }
+  if (optional(a[10], "status", dev, d_i32, -1, &st) < 0 || fits32(x.shape[1], "hidden") < 0 ||
+      fits32(cs.shape[0], "max_pos") < 0 || fits32(d, "head_dim") < 0)
+    return NULL;
+  void* stream;
+  long back;
+  if (enter(dev, &stream, &back) < 0) return NULL;
+  tts_status status;
+  Py_BEGIN_ALLOW_THREADS
+  status = f_qkv_axes(x.ptr, x.shape[0], (int32_t)x.shape[1], w.ptr, bias.ptr, pos.ptr,
+                      (int32_t)pos.shape[0], axis, cs.ptr, (int32_t)cs.shape[0], heads, (int32_t)d,
+                      out[0].ptr, out[1].ptr, out[2].ptr, st.ptr, stream);
   Py_END_ALLOW_THREADS
   return leave(back, status);
 }
@@ -452,12 +690,34 @@ static PyObject* bind(PyObject* self, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+/* bind_more((append_axes, tree, compact, fork, qkv_axes addresses), int64): after bind() */
+static PyObject* bind_more(PyObject* self, PyObject* args) {
+  (void)self;
+  unsigned long long f[5];
+  PyObject* i64;
+  if (!PyArg_ParseTuple(args, "(KKKKK)O", &f[0], &f[1], &f[2], &f[3], &f[4], &i64)) return NULL;
+  f_append_axes = (append_axes_fn)(uintptr_t)f[0];
+  f_tree = (tree_fn)(uintptr_t)f[1];
+  f_compact = (compact_fn)(uintptr_t)f[2];
+  f_fork = (fork_fn)(uintptr_t)f[3];
+  f_qkv_axes = (qkv_axes_fn)(uintptr_t)f[4];
+  Py_INCREF(i64);
+  Py_XSETREF(d_i64, i64);
+  Py_RETURN_NONE;
+}
+
 static PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, "bind(addresses, dtypes, torch functions)"},
     {"rope_kv_append", (PyCFunction)(void (*)(void))rope_kv_append, METH_FASTCALL, NULL},
     {"attn_decode_paged", (PyCFunction)(void (*)(void))attn_decode_paged, METH_FASTCALL, NULL},
     {"attn_fwd_varlen_window", (PyCFunction)(void (*)(void))attn_fwd_varlen_window, METH_FASTCALL,
      NULL},
+    {"bind_more", bind_more, METH_VARARGS, "bind_more(addresses, dtype)"},
+    {"rope_kv_append_axes", (PyCFunction)(void (*)(void))rope_kv_append_axes, METH_FASTCALL, NULL},
+    {"attn_decode_tree", (PyCFunction)(void (*)(void))attn_decode_tree, METH_FASTCALL, NULL},
+    {"kv_compact", (PyCFunction)(void (*)(void))kv_compact, METH_FASTCALL, NULL},
+    {"kv_fork", (PyCFunction)(void (*)(void))kv_fork, METH_FASTCALL, NULL},
+    {"qkv_rope_axes", (PyCFunction)(void (*)(void))qkv_rope_axes, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", NULL, -1, methods, NULL, NULL,
                                     NULL, NULL};

@@ -34,8 +34,14 @@
 //               the accumulator is handed back to the leader's MMA warp by local /
 //               remote arrives.
 // Pair tiles go to pairs round-robin; every wait is bounded.
+//
+// kAxes: a token has positions on up to four axes (row, column; time in front of them for video), and
+// every pair's axis chooses the one that it turns by. Only the fetch of a tile's cos/sin rows
+// differs, which runs while the tile's products do.
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -77,6 +83,12 @@ struct QkvParams {
   uint32_t* dev_status;
   int n, heads, max_pos, tiles_n, n_tiles, k_steps;  // n_tiles: 256-token pair tiles
 };
+struct QkvAxesParams : QkvParams {
+  int axes;               // pos is [axes, n]
+  uint64_t pair_axis[2];  // two bits a pair
+};
+template <bool kAxes>
+using QkvParamsFor = std::conditional_t<kAxes, QkvAxesParams, QkvParams>;
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int c0, int c1) {
   asm volatile(
@@ -186,9 +198,9 @@ __device__ __forceinline__ bool warp_spin_cl(uint32_t bar, uint32_t parity, vola
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-template <int D>
+template <int D, bool kAxes>
 __global__ void __launch_bounds__(kQkvThreads, 1)
-    qkv_rope_kernel(const __grid_constant__ QkvMaps maps, const QkvParams p) {
+    qkv_rope_kernel(const __grid_constant__ QkvMaps maps, const QkvParamsFor<kAxes> p) {
   using C = QkvCfg<D>;
   constexpr int NS = C::kStages;
   constexpr int H2 = D / 2;
@@ -339,7 +351,7 @@ __global__ void __launch_bounds__(kQkvThreads, 1)
       // and that token's q and k are written as zeros.
       int pos = 0;
       bool pos_ok = true;
-      if (ok && live && row < p.n && any_rot) {
+      if (!kAxes && ok && live && row < p.n && any_rot) {
         pos = p.pos[row];
         pos_ok = pos >= 0 && pos < p.max_pos;
         if (!pos_ok) {
@@ -349,13 +361,44 @@ __global__ void __launch_bounds__(kQkvThreads, 1)
       }
       const float4* cs4 =
           reinterpret_cast<const float4*>(p.cos_sin + static_cast<int64_t>(pos) * H2);
+      [[maybe_unused]] int at[4] = {0, 0, 0, 0};  // the token's positions on the axes
+      if constexpr (kAxes) {
+        if (ok && live && row < p.n && any_rot) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (x < p.axes) at[x] = p.pos[static_cast<int64_t>(x) * p.n + row];
+            pos_ok = pos_ok && at[x] >= 0 && at[x] < p.max_pos;
+          }
+          if (!pos_ok) {
+            if (p.dev_status) atomicOr(p.dev_status, kDevIndexRange);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) at[x] = 0;
+          }
+        }
+      }
+      // cos / sin of pairs 2u and 2u + 1
+      auto turn_of = [&](int u) -> float4 {
+        if constexpr (kAxes) {
+          const uint32_t w = static_cast<uint32_t>(p.pair_axis[u >> 4] >> (4 * (u & 15)));
+          auto row_at = [&](uint32_t x) -> const float2* {
+            const int q = x & 2 ? (x & 1 ? at[3] : at[2]) : (x & 1 ? at[1] : at[0]);
+            return p.cos_sin + static_cast<int64_t>(q) * H2 + 2 * u;
+          };
+          const uint32_t x0 = w & 3, x1 = (w >> 2) & 3;
+          if (x0 == x1) return __ldg(reinterpret_cast<const float4*>(row_at(x0)));
+          const float2 a = __ldg(row_at(x0)), b = __ldg(row_at(x1) + 1);
+          return make_float4(a.x, a.y, b.x, b.y);
+        } else {
+          return __ldg(cs4 + u);
+        }
+      };
       // d <= 80: the token's cos/sin row (d/2 pairs) is kept in registers for the tile.
       constexpr bool kCsRegs = D <= 80;
       float4 csr[kCsRegs ? H2 / 2 : 1];
       if constexpr (kCsRegs) {
         if (ok && live && any_rot) {
 #pragma unroll
-          for (int u = 0; u < H2 / 2; ++u) csr[u] = __ldg(cs4 + u);
+          for (int u = 0; u < H2 / 2; ++u) csr[u] = turn_of(u);
         }
       }
       named_barrier_sync(1, 128);  // the bias is in shared memory
@@ -395,7 +438,7 @@ __global__ void __launch_bounds__(kQkvThreads, 1)
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
                 const float4 v = kCsRegs ? csr[(j0 / 2 + u) % (kCsRegs ? H2 / 2 : 1)]
-                                         : __ldg(cs4 + j0 / 2 + u);
+                                         : turn_of(j0 / 2 + u);
                 cs[4 * u] = v.x;
                 cs[4 * u + 1] = v.y;
                 cs[4 * u + 2] = v.z;
@@ -463,8 +506,8 @@ __global__ void __launch_bounds__(kQkvThreads, 1)
   }
 }
 
-// Co-resident CTA pairs of qkv_rope_kernel<D> on the current device (cached per device).
-template <int D>
+// Co-resident CTA pairs of qkv_rope_kernel<D, kAxes> on the current device (cached per device).
+template <int D, bool kAxes>
 int max_pairs(int dev, const cudaLaunchConfig_t& cfg) {
   // Host threads may make their first calls at the same time: every thread that finds
   // the slot empty computes the same value, and the slot is read and written atomically.
@@ -474,7 +517,7 @@ int max_pairs(int dev, const cudaLaunchConfig_t& cfg) {
     if (c > 0) return c;
   }
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, qkv_rope_kernel<D>, &cfg) != cudaSuccess || n < 1) {
+  if (cudaOccupancyMaxActiveClusters(&n, qkv_rope_kernel<D, kAxes>, &cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();
     int sms = 0;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -484,7 +527,7 @@ int max_pairs(int dev, const cudaLaunchConfig_t& cfg) {
   return n;
 }
 
-template <int D>
+template <int D, bool kAxes>
 cudaError_t launch_qkv_d(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
   using C = QkvCfg<D>;
   QkvMaps maps;
@@ -510,7 +553,12 @@ cudaError_t launch_qkv_d(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
       !make(&maps.out[1], a.k, (uint64_t)a.heads * D, n, D, 32, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !make(&maps.out[2], a.v, (uint64_t)a.heads * D, n, D, 32, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  QkvParams p;
+  QkvParamsFor<kAxes> p;
+  if constexpr (kAxes) {
+    p.axes = a.axes;
+    p.pair_axis[0] = a.pair_axis[0];
+    p.pair_axis[1] = a.pair_axis[1];
+  }
   p.bias = a.bias;
   p.pos = a.positions;
   p.cos_sin = reinterpret_cast<const float2*>(a.cos_sin);
@@ -527,7 +575,7 @@ cudaError_t launch_qkv_d(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(qkv_rope_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(qkv_rope_kernel<D, kAxes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -542,10 +590,10 @@ cudaError_t launch_qkv_d(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(2, 1, 1);
-  const int pairs_max = max_pairs<D>(dev, cfg);
+  const int pairs_max = max_pairs<D, kAxes>(dev, cfg);
   const int pairs = static_cast<int>(n_tiles < pairs_max ? n_tiles : pairs_max);
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  e = cudaLaunchKernelEx(&cfg, qkv_rope_kernel<D>, maps, p);
+  e = cudaLaunchKernelEx(&cfg, qkv_rope_kernel<D, kAxes>, maps, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -566,6 +614,16 @@ __global__ void rope_cache_kernel(float2* __restrict__ out, int max_pos, int rot
   }
 }
 
+template <bool kAxes>
+cudaError_t launch_qkv(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
+  switch (a.head_dim) {
+    case 64: return launch_qkv_d<64, kAxes>(a, drv_err, stream);
+    case 80: return launch_qkv_d<80, kAxes>(a, drv_err, stream);
+    case 128: return launch_qkv_d<128, kAxes>(a, drv_err, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 }  // namespace
 
 int qkv_heads_per_tile(int head_dim) {
@@ -578,12 +636,7 @@ int qkv_heads_per_tile(int head_dim) {
 }
 
 cudaError_t launch_qkv_rope(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
-  switch (a.head_dim) {
-    case 64: return launch_qkv_d<64>(a, drv_err, stream);
-    case 80: return launch_qkv_d<80>(a, drv_err, stream);
-    case 128: return launch_qkv_d<128>(a, drv_err, stream);
-    default: return cudaErrorInvalidValue;
-  }
+  return a.axes > 0 ? launch_qkv<true>(a, drv_err, stream) : launch_qkv<false>(a, drv_err, stream);
 }
 
 cudaError_t launch_rope_cache(int max_pos, int rot_dim, double base, float* cos_sin,
