@@ -5,13 +5,37 @@
 // first ones); its position is past the cached tokens by the number of new tokens that it
 // sees besides one (itself).
 //
-// A block per (token, q head): 128 keys at a time, a key per thread for the scores, a value column
-// per thread for the sums.
+// A tree has more q rows per KV head than a decode step (16 to 64 tokens by the group's heads), so the
+// products run on the tensor cores with the q rows as M = 128: S = Q K^T, O += P V, accumulators in
+// TMEM, a softmax thread per q row. For KV head g the rows of its group (token-major) are blocks of
+// 128, or 256 where requests have more; a unit is (request, g, row block), a tile kTK keys. All
+// tiles of all units form one list, cut into equal runs, one per CTA (one CTA per SM); a
+// unit cut by a run's border leaves unnormalised sums that a second launch joins in order. Roles:
+//   warp 0       TMA producer: pages through the table into a ring of K tiles and one of V tiles
+//   warp 1       tcgen05 issuer (TMEM: S0, S1 at columns 0 and 128, O0, O1 at 256 and 384)
+//   warps 2, 3   V for the second product: e4m3 codes to fp16; rows that no token sees to zeros
+//   warps 4..11  two softmax warpgroups. Up to 128 rows: both hold the same rows and take the tiles in
+//                turn, each with its own running maximum, sum and accumulator, joined at the unit's
+//                end. More rows: each holds 128 and takes every tile.
+// Either way the products of one warpgroup run while the other's softmax does.
+//
+// e4m3 caches: K codes are multiplied as they are (kind::f8f6f4), with q as the sum of two e4m3
+// values: a row is scaled by a power of two so that its largest value lies in [2^7, 2^8); hi has
+// the leading 4 bits and lo the next 4, all of a bf16 value, down to 2^-9 of the row's largest; below
+// that lo ends at 2^-10, 2^-17 of the largest. Widening K instead would read and write
+// three times the tile's bytes in shared memory, whose rate is what the tensor core's operands
+// leave least of. Weights are fp16 against V widened to fp16 (exactly): e4m3 weights, in two
+// terms as well, would end at 2^-18 of the largest, and a flat tail of keys under a dominant one loses
+// digits there. The value scale of a page rides in the exponent as in attn_decode.cu:
+//   x_j = scale log2(e) sK q.k_j + log2 sV,   weights 2^(x_j - m), summed with 1 / sV.
+// bf16 caches use bf16 products throughout. Sums and statistics are fp32.
+#include <atomic>
 #include <cstdint>
+#include <type_traits>
 
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "e4m3.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -19,124 +43,1116 @@
 namespace tts {
 namespace {
 
-template <bool F8, int D>
-__global__ void __launch_bounds__(128) attn_tree_simple_kernel(const AttnDecodeArgs a) {
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kThreads = 384;
+constexpr int kRows = 128;  // q rows of a tile (TMEM lanes)
+// What the end of a unit costs (joining, the next unit's q), in tiles of the list.
+constexpr int kEndTiles = 3;
+constexpr int kMinRun = 2;  // tiles of a run at least: one for each warpgroup
+constexpr float kMinValueScale = 0x1p-80f;  // as in attn_decode.cu
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// kTwo: units of up to 256 rows, two q tiles.
+template <bool F8, int D, bool kTwo>
+struct Cfg {
+  static constexpr int kRowBytes = D * (F8 ? 1 : 2);
+  static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;  // one swizzled row
+  static constexpr int kPanels = kRowBytes / kPanelBytes;
+  static constexpr int kTK = kRowBytes == 256 ? 64 : 128;  // keys per tile
+  static constexpr int kTileBytes = kTK * kRowBytes;       // K (or V) of one tile
+  static constexpr int kQTiles = kTwo ? 2 : 1;
+  // e4m3: the hi and the lo half one after the other, each kRows rows of one panel
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kWideBytes = F8 ? kTK * D * 2 : 0;  // V as fp16
+  static constexpr int kWides = F8 ? 2 : 0;
+  static constexpr int kLimit = 224 * 1024;  // of 227 KB: 1 KB to align, 2 of barriers and the rest
+  static constexpr int kRing = (kLimit - kQTiles * kQBytes - kWides * kWideBytes) / (2 * kTileBytes);
+  static constexpr int kStages = kRing < 8 ? kRing : 8;
+  // A tile's scales are read until its weights are computed, two jobs behind its K's last reader.
+  static constexpr int kMeta = kStages + 2;
+  static constexpr int kSmemBytes =
+      1024 + kQTiles * kQBytes + kWides * kWideBytes + kStages * 2 * kTileBytes;
+  static constexpr int kPieces = F8 ? kTK / 16 : 1;
+  static constexpr int kUnitRows = kQTiles * kRows;
+  static_assert(kStages >= 3, "ring");
+};
+
+// Registers move from the warps that issue to the softmax warps, which hold a tile's scores: 128 x
+// 80 + 256 x 208 = 63488 of the 384 x 168 = 64512 that the block is launched with.
+constexpr int kIssueRegs = 80, kSoftmaxRegs = 208;
+constexpr int kLaunchRegs = (128 * kIssueRegs + 256 * kSoftmaxRegs + kThreads - 1) / kThreads;
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// kind::f16 with fp16 A and B, fp32 D; b_mn: B is N-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t b_mn) {
+  return (1u << 4) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+// kind::f8f6f4 with e4m3 A and B, both K-major, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss_f8_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate,
+                                                uint32_t pred) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(pred)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The two e4m3 codes in the low / high half of w as two fp16 values (exact).
+__device__ __forceinline__ uint32_t e4m3_half(uint32_t w, int high) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)(high ? w >> 16 : w)));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+// Shared-memory address of 16-byte chunk c of row `row`, as TMA's swizzle and the matrix descriptors
+// place it, in panels of `rows` rows (128-byte rows: chunk ^ row mod 8; 64-byte rows: chunk ^
+// row / 2 mod 4).
+template <int PB>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t base, int rows, int row, int c) {
+  if constexpr (PB == 128)
+    return base + (c >> 3) * (rows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+  else
+    return base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ uint32_t below(int n, int c0) {  // bits of columns c0 .. c0 + 31 under n
+  const int b = n - c0;
+  return b <= 0 ? 0u : b >= 32 ? kAll : (1u << b) - 1u;
+}
+
+template <int kP>
+struct Meta {  // of a tile, written by the producer
+  uint32_t ok;   // bit i: piece i (a page, or the tile if pages are larger) is there
+  float ks[kP];  // scale of its keys
+  float vl[kP];  // log2 of the scale of its values
+  float vi[kP];  // 1 / that scale
+};
+
+struct Params {
+  const uint16_t* q;
+  const int32_t* cu_q;  // null: one token per request
+  const uint64_t* mask;
+  const int32_t* page_tables;
+  const int32_t* kv_lens;
+  const float* k_scale;
+  const float* v_scale;
+  void* out;
+  float* lse;
+  float* parts;  // [2 * CTAs][unit_rows * (D + 2)]
+  // [CTAs], of the unit that was begun in an earlier CTA and ended in this one: {first CTA
+  // (-1: no such unit), rows, first row within the request, g}
+  int4* jobs;
+  int* job_q0;  // and the request's first q row
+  uint32_t* dev_status;
+  int total_q, max_keys;
+  int batch, max_q, hq, hkv, group, num_pages, max_pages, page_size, page_shift, window, sinks;
+  float scale_log2;
+  int out_bf16, ctas, unit_rows;
+};
+
+// A request as the kernel sees it: its tokens, its visible keys as two runs of tiles (first
+// tokens, window) and the number of units per head.
+struct Req {
+  int n, L, lo, sinks;  // new tokens, keys, first key of the widest window (0: none), first keys kept
+  int st, lt, nt, rt;   // tiles of the first keys, first tile of the window, tiles, row blocks
+  int q0;               // first q row
+};
+template <int TK>
+__device__ __forceinline__ Req load_req(const Params& p, int b, uint32_t* bad) {
+  Req r;
+  int q1 = b + 1;
+  r.q0 = b;
+  if (p.cu_q != nullptr) {
+    r.q0 = p.cu_q[b];
+    q1 = p.cu_q[b + 1];
+  }
+  r.L = p.kv_lens[b];
+  r.n = 0;
+  if (r.q0 < 0 || q1 < r.q0 || q1 > p.total_q || q1 - r.q0 > p.max_q)
+    *bad |= kDevBadArg;
+  else
+    r.n = q1 - r.q0;
+  if (r.L < 0 || r.L > p.max_keys) {
+    *bad |= kDevIndexRange;
+    r.L = 0;  // its rows see no key
+  }
+  // keys and window are at most 2^30, so nothing here leaves 32 bits
+  r.lo = p.window > 0 ? max(r.L - r.n + 1 - p.window, 0) : 0;
+  r.sinks = min(p.sinks, r.lo);
+  r.lt = (int)((unsigned)r.lo / TK);
+  r.st = min((int)((unsigned)(r.sinks + TK - 1) / TK), r.lt);
+  r.nt = max(r.st + (int)((unsigned)(r.L + TK - 1) / TK) - r.lt, 1);  // 1: an empty tile, zeros
+  r.rt = (r.n * p.group + p.unit_rows - 1) / p.unit_rows;
+  return r;
+}
+// Bits of new tokens that are there: m < n and a key of its own (a length under n has none for some).
+__device__ __forceinline__ uint64_t present(int n, int base) {
+  uint64_t m = n >= 64 ? ~0ull : (1ull << n) - 1;
+  if (base < 0) m = -base >= 64 ? 0 : m >> -base << -base;
+  return m;
+}
+
+template <bool F8, int D, bool kTwo>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tree_kernel(const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const Params p) {
+  using C = Cfg<F8, D, kTwo>;
+  constexpr int TK = C::kTK, S = C::kStages, PB = C::kPanelBytes;
+  extern __shared__ uint8_t smem_raw[];
+  // K and V landed; K's last product done; V ready for its product (widened, or cleared); V's slot
+  // (e4m3: the codes') free; the tile's scales written; e4m3: a widened V's last product done; a
+  // warpgroup's scores, weights and sums; its q tile written; its sums read; the second
+  // warpgroup's statistics
+  __shared__ __align__(8) uint64_t bar_k[S], bar_v[S], bar_k_empty[S], bar_v_empty[S],
+      bar_ready[S], bar_meta[C::kMeta], bar_wide_empty[2], bar_s[2], bar_p[2], bar_o[2], bar_q[2], bar_o_free[2],
+      bar_ml, bar_drain;
+  __shared__ Meta<C::kPieces> s_meta[C::kMeta];
+  __shared__ float2 s_ml[kRows];  // references and sums of the second warpgroup's rows
+  __shared__ int s_scan[kThreads / 32], s_b, s_off, s_abort;
+  __shared__ uint32_t s_tmem;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sq = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t wide = sq + C::kQTiles * C::kQBytes;
+  const uint32_t ring = wide + C::kWides * C::kWideBytes;
+  auto sK = [&](int st) -> uint32_t { return ring + st * 2 * C::kTileBytes; };
+  auto sV = [&](int st) -> uint32_t { return ring + st * 2 * C::kTileBytes + C::kTileBytes; };
+  volatile int* abort_flag = &s_abort;
+
+  if (tid == 0) {
+    prefetch_tmap(&map_k);  // on their way while the lengths are read
+    prefetch_tmap(&map_v);
+    s_abort = 0;
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&bar_k[i]), 1);
+      mbar_init(smem_u32(&bar_v[i]), 1);
+      mbar_init(smem_u32(&bar_k_empty[i]), 1);
+      mbar_init(smem_u32(&bar_v_empty[i]), F8 ? 2 : 1);
+      mbar_init(smem_u32(&bar_ready[i]), 2);
+    }
+    for (int i = 0; i < C::kMeta; ++i) mbar_init(smem_u32(&bar_meta[i]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bar_wide_empty[i]), 1);
+      mbar_init(smem_u32(&bar_s[i]), 1);
+      mbar_init(smem_u32(&bar_p[i]), kRows);
+      mbar_init(smem_u32(&bar_o[i]), 1);
+      mbar_init(smem_u32(&bar_q[i]), kRows);
+      mbar_init(smem_u32(&bar_o_free[i]), kRows);
+    }
+    mbar_init(smem_u32(&bar_ml), kRows);
+    mbar_init(smem_u32(&bar_drain), 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s_tmem), 512);
+    tmem_relinquish();
+  }
   wait_for_prior_grids();
-  __shared__ float s_q[D], s_p[128], s_red[4];
-  __shared__ int s_row[128], s_b, s_n, s_q0;
-  const int tid = threadIdx.x, t = blockIdx.x, h = blockIdx.y, g = h / (a.hq / a.hkv);
-  if (tid == 0) s_b = -1;
+  if (tid == 0) p.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
+
+  // ---- this CTA's run [t0, t1) of the list of tiles, and the request it begins in
+  uint32_t bad = 0;
+  auto scan32 = [&](int x) -> int {  // inclusive over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  auto tiles_of = [&](const Req& r) -> int { return p.hkv * r.rt * (r.nt + kEndTiles); };
+  int total = 0, runs = 0, len = 0, more = 0, t0 = 0, t1 = 0;
+  auto split = [&]() -> bool {
+    runs = min((int)((unsigned)(total + kMinRun - 1) / kMinRun), p.ctas);
+    if ((int)blockIdx.x >= runs) return false;
+    len = (int)((unsigned)total / (unsigned)runs);
+    more = total - len * runs;
+    t0 = blockIdx.x * len + min((int)blockIdx.x, more);
+    t1 = t0 + len + ((int)blockIdx.x < more ? 1 : 0);
+    return true;
+  };
+  auto block_scan = [&](int v, int* sum) -> int {  // inclusive
+    const int x = scan32(v);
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int before = 0;
+    *sum = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += s_scan[w];
+      *sum += s_scan[w];
+    }
+    return x + before;
+  };
+  int b = 0, off = 0;
+  bool work;
+  if (p.batch <= 32) {  // every warp for itself
+    const int v = lane < p.batch ? tiles_of(load_req<TK>(p, lane, &bad)) : 0;
+    const int incl = scan32(v);
+    total = __shfl_sync(kAll, incl, 31);
+    work = split();
+    if (work) {
+      b = __ffs(__ballot_sync(kAll, incl > t0)) - 1;
+      off = t0 - __shfl_sync(kAll, incl - v, b);
+    }
+    if (warp != 0) bad = 0;
+  } else {
+    for (int base = 0; base < p.batch; base += kThreads) {
+      const int i = base + tid;
+      int sum;
+      block_scan(i < p.batch ? tiles_of(load_req<TK>(p, i, &bad)) : 0, &sum);
+      total += sum;
+    }
+    work = split();
+    uint32_t again = 0;
+    for (int base = 0, carry = 0; work && base < p.batch && carry <= t0; base += kThreads) {
+      const int i = base + tid;
+      const int v = i < p.batch ? tiles_of(load_req<TK>(p, i, &again)) : 0;
+      int sum;
+      const int incl = carry + block_scan(v, &sum);
+      if (incl > t0 && incl - v <= t0) {
+        s_b = i;
+        s_off = t0 - (incl - v);
+      }
+      carry += sum;
+    }
+    __syncthreads();
+    b = s_b;
+    off = s_off;
+  }
+  if (blockIdx.x == 0 && bad && p.dev_status != nullptr) atomicOr(p.dev_status, bad);
+  tc_fence_before();
   __syncthreads();
-  for (int b = tid; b < a.batch; b += 128) {
-    const int q0 = a.cu_q ? a.cu_q[b] : b, q1 = a.cu_q ? a.cu_q[b + 1] : b + 1;
-    if (q0 < 0 || q1 < q0 || q1 > a.total_q || q1 - q0 > a.max_q) {
-      if (t == 0 && h == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadArg);
-    } else if (t >= q0 && t < q1) {
-      s_b = b;
-      s_n = q1 - q0;
-      s_q0 = q0;
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  if (!work) {  // the same for the block
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
+  Req r = load_req<TK>(p, b, &bad);
+
+  int left = t1 - t0;
+  int seg_g = -1, seg_rt = 0;
+  // The next unit's part in this run: head, row block, tiles [x0, x1) of nt. Every role walks the
+  // run for itself.
+  auto next_seg = [&](int& g, int& rt, int& x0, int& x1) -> bool {
+    if (seg_g < 0) {  // the run's first unit, perhaps from its middle
+      const int u = (int)((unsigned)off / (unsigned)(r.nt + kEndTiles));
+      x0 = off - u * (r.nt + kEndTiles);
+      seg_g = (int)((unsigned)u / (unsigned)r.rt);
+      seg_rt = u - seg_g * r.rt;
+    } else {
+      x0 = 0;
+      if (++seg_rt == r.rt) {
+        seg_rt = 0;
+        if (++seg_g == p.hkv) {
+          seg_g = 0;
+          do r = load_req<TK>(p, ++b, &bad);  // requests without new tokens have no units
+          while (r.rt == 0);
+        }
+      }
+    }
+    g = seg_g;
+    rt = seg_rt;
+    x1 = min(r.nt, x0 + left);
+    left -= min(r.nt + kEndTiles - x0, left);
+    return x0 < x1;  // else the run begins behind the unit's last tile
+  };
+  auto rows_of_unit = [&](int rt) -> int { return min(r.n * p.group - rt * C::kUnitRows, C::kUnitRows); };
+  auto first_key = [&](int x) -> int { return (x < r.st ? x : r.lt + x - r.st) * TK; };
+  const int piece = p.page_size < TK ? p.page_size : TK;  // keys per TMA box
+  const int n_pieces = TK / piece;
+  const int piece_shift = 31 - __clz(piece >> 4);  // 16 keys -> piece
+
+  if (warp < 4) {
+    give_registers<kIssueRegs>();
+    if (warp == 0) {
+      // ------------------------------------------------------------------ producer
+      // Lane i keeps page cache_at + i of the request (and what the others need of its scales for
+      // head cache_g) in registers, loaded 32 pages at a time.
+      int it = 0;
+      int cache_b = -1, cache_at = 0, cache_g = -1, page = -1;
+      bool fine = true;                    // the page's scales are in range
+      float ks = 1.f, vl = 0.f, vi = 1.f;  // key scale, log2 and inverse of the value scale
+      bool ok = true;
+      while (ok && left > 0) {
+        int g, rt, x0, x1;
+        if (!next_seg(g, rt, x0, x1)) continue;
+        for (int x = x0; x < x1; ++x, ++it) {
+          const int key0 = first_key(x), st = it % S;
+          const int pg0 = key0 >> p.page_shift;
+          if (cache_b != b || pg0 < cache_at || pg0 + n_pieces > cache_at + 32) {
+            cache_b = b;
+            cache_at = pg0;
+            cache_g = -1;
+            const int lp = pg0 + lane;
+            page = lp < p.max_pages ? p.page_tables[(int64_t)b * p.max_pages + lp] : -1;
+            if (page < 0 || page >= p.num_pages) page = -1;
+          }
+          float sk = 1.f, sv = 1.f;
+          const bool new_scales = F8 && cache_g != g;
+          if (new_scales && page >= 0) {  // asked for here, looked at behind the copies
+            sk = p.k_scale[(int64_t)page * p.hkv + g];
+            sv = p.v_scale[(int64_t)page * p.hkv + g];
+          }
+          const int at = pg0 - cache_at + (lane < n_pieces ? lane : 0);
+          const int pg = __shfl_sync(kAll, page, at);
+          const int a = key0 + lane * piece;  // this lane's piece: keys [a, a + piece)
+          const bool seen = lane < n_pieces && a < r.L && (a + piece > r.lo || a < r.sinks);
+          const bool there = seen && pg >= 0;
+          const uint32_t sent = __ballot_sync(kAll, there);
+          if (it >= S) {
+            ok = warp_wait(smem_u32(&bar_k_empty[st]), ((it / S) - 1) & 1, abort_flag, p.dev_status);
+            if (!ok) break;
+          }
+          const uint32_t bytes = __popc(sent) * piece * C::kRowBytes;
+          const int row = key0 & (p.page_size - 1);  // 0 unless the tile is inside a page
+          const int slab = pg * p.hkv + g;
+          if (there) {
+#pragma unroll
+            for (int pn = 0; pn < C::kPanels; ++pn)
+              tma_load_3d(sK(st) + pn * TK * PB + lane * piece * PB, &map_k, smem_u32(&bar_k[st]),
+                          pn * 64, row, slab);
+          }
+          uint32_t flag = seen && !there ? kDevIndexRange : 0u;
+          uint32_t use = sent;
+          Meta<C::kPieces>& meta = s_meta[it % C::kMeta];
+          if constexpr (F8) {
+            if (new_scales) {
+              cache_g = g;
+              fine = sk > 0.f && sk < INFINITY && sv >= kMinValueScale && sv < INFINITY;
+              ks = sk;
+              vl = fine ? log2f(sv) : 0.f;
+              vi = fine ? 1.f / sv : 0.f;
+            }
+            const uint32_t all = __ballot_sync(kAll, fine);
+            const bool good = there && ((all >> at) & 1u);
+            if (there && !good) flag |= kDevBadArg;  // no scale of a written page: keys skipped
+            use = __ballot_sync(kAll, good);
+            const float k_of = __shfl_sync(kAll, ks, at), l_of = __shfl_sync(kAll, vl, at),
+                        i_of = __shfl_sync(kAll, vi, at);
+            if (lane < n_pieces) {  // pieces that are not used stay neutral
+              meta.ks[lane] = good ? k_of : 1.f;
+              meta.vl[lane] = good ? l_of : 0.f;
+              meta.vi[lane] = good ? i_of : 0.f;
+            }
+          }
+          if (flag && p.dev_status != nullptr) atomicOr(p.dev_status, flag);
+          if (lane == 0) meta.ok = use;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&bar_meta[it % C::kMeta]));
+            mbar_arrive_expect_tx(smem_u32(&bar_k[st]), bytes);
+          }
+          bool v_ok = true;
+          if (it >= S)
+            v_ok = warp_wait(smem_u32(&bar_v_empty[st]), ((it / S) - 1) & 1, abort_flag, p.dev_status);
+          if (v_ok && there) {
+#pragma unroll
+            for (int pn = 0; pn < C::kPanels; ++pn)
+              tma_load_3d(sV(st) + pn * TK * PB + lane * piece * PB, &map_v, smem_u32(&bar_v[st]),
+                          pn * 64, row, slab);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bar_v[st]), v_ok ? bytes : 0);
+          if (!v_ok) {
+            ok = false;
+            ++it;
+            break;
+          }
+        }
+      }
+      // Copies in flight must land before the CTA can exit, also when a wait ran out.
+      for (int i = it > S ? it - S : 0; i < it; ++i) {
+        mbar_wait(smem_u32(&bar_k[i % S]), (i / S) & 1, nullptr, nullptr);
+        mbar_wait(smem_u32(&bar_v[i % S]), (i / S) & 1, nullptr, nullptr);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ tcgen05 issuer
+      const uint32_t e = elect_one();
+      auto s_t = [&](int w) -> uint32_t { return tmem + w * 128; };
+      auto o_t = [&](int w) -> uint32_t { return tmem + 256 + w * 128; };
+      constexpr uint32_t kKSbo = PB * 8;  // eight rows
+      constexpr SmemLayout kLay = PB == 128 ? kSw128 : kSw64;
+      auto issue_s = [&](int w, int tile, int st) {
+        const uint64_t qd = smem_desc(sq + tile * C::kQBytes, 16, kKSbo, kLay);
+        const uint64_t kd = smem_desc(sK(st), 16, kKSbo, kLay);
+        if constexpr (F8) {
+          constexpr uint32_t idesc = idesc_e4m3_f32(kRows, TK);
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              mma_ss_f8_elect(s_t(w), qd + ((half * kRows * PB + k * 32) >> 4), kd + ((k * 32) >> 4),
+                              idesc, half + k > 0, e);
+        } else {
+          constexpr uint32_t idesc = idesc_bf16_f32(kRows, TK, 0, 0);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss_elect(s_t(w), qd + (((k / 4) * kRows * 128 + (k % 4) * 32) >> 4),
+                         kd + (((k / 4) * TK * 128 + (k % 4) * 32) >> 4), idesc, k > 0, e);
+        }
+      };
+      auto issue_o = [&](int w, uint32_t v, bool acc) {
+        const uint64_t vd = smem_desc(v, TK * 128, 1024, kSw128);
+        constexpr uint32_t idesc = F8 ? idesc_f16_f32(kRows, D, 1) : idesc_bf16_f32(kRows, D, 0, 1);
+#pragma unroll
+        for (int k = 0; k < TK / 16; ++k)
+          mma_ts_elect(o_t(w), s_t(w) + k * 8, vd + ((k * 16 * 128) >> 4), idesc, acc || k > 0, e);
+      };
+      int gt = 0, seg = 0;        // tiles and parts so far
+      int jobs[2] = {0, 0}, nq[2] = {0, 0};  // of each warpgroup: jobs, q tiles
+      bool ok = true;
+      while (ok && left > 0) {
+        int g, rt, x0, x1;
+        if (!next_seg(g, rt, x0, x1)) continue;
+        const bool alt = !kTwo || rows_of_unit(rt) <= kRows;
+        const int T = x1 - x0, J = alt ? T : 2 * T;
+        // job i: warpgroup i % 2, and tile i, or i / 2 where each warpgroup takes every tile
+        for (int i = 0; ok && i < J + 2; ++i) {
+          const int w = i & 1;
+          if (i >= 2) {
+            const int j = i - 2, t = gt + (alt ? j : j >> 1), st = t % S;
+            ok = warp_wait(smem_u32(&bar_ready[st]), (t / S) & 1, abort_flag, p.dev_status) &&
+                 warp_wait(smem_u32(&bar_p[w]), (jobs[w] + (j >> 1)) & 1, abort_flag, p.dev_status);
+            if (ok && j < 2 && seg > 0)  // the sums of the part before have been read
+              ok = warp_wait(smem_u32(&bar_o_free[w]), (seg - 1) & 1, abort_flag, p.dev_status);
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(w, F8 ? wide + (t & 1) * C::kWideBytes : sV(st), j >= 2);
+            if (alt || w == 1)
+              mma_commit_elect(smem_u32(F8 ? &bar_wide_empty[t & 1] : &bar_v_empty[st]), e);
+            if (j + 2 >= J) mma_commit_elect(smem_u32(&bar_o[w]), e);
+          }
+          if (i < J) {
+            const int t = gt + (alt ? i : i >> 1), st = t % S, tile = alt ? 0 : w;
+            if (i < 2 && (!alt || i == 0)) {
+              ok = warp_wait(smem_u32(&bar_q[tile]), nq[tile] & 1, abort_flag, p.dev_status);
+              nq[tile]++;
+            }
+            ok = ok && warp_wait(smem_u32(&bar_k[st]), (t / S) & 1, abort_flag, p.dev_status);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(w, tile, st);
+            mma_commit_elect(smem_u32(&bar_s[w]), e);
+            if (alt || w == 1) mma_commit_elect(smem_u32(&bar_k_empty[st]), e);
+          }
+        }
+        gt += T;
+        jobs[0] += (J + 1) >> 1;
+        jobs[1] += J >> 1;
+        ++seg;
+      }
+      // Every product is complete before TMEM is freed.
+      mma_commit_elect(smem_u32(&bar_drain), e);
+      mbar_wait(smem_u32(&bar_drain), 0, nullptr, p.dev_status);
+    } else {
+      // ------------------------------------------------------------------ V for the second product
+      int it = 0;
+      bool ok = true;
+      while (ok && left > 0) {
+        int g, rt, x0, x1;
+        if (!next_seg(g, rt, x0, x1)) continue;
+        // new tokens that some token sees, and the first key of the windows
+        const int base = r.L - r.n;
+        const uint64_t here = present(r.n, base);
+        uint64_t any = 0;
+        int least = 64;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (lane + 32 * k < r.n) {
+            const uint64_t m = p.mask[r.q0 + lane + 32 * k];
+            any |= m;
+            least = min(least, max(__popcll(m & (r.n >= 64 ? ~0ull : (1ull << r.n) - 1)) - 1, 0));
+          }
+        any = here & ((uint64_t)__reduce_or_sync(kAll, (uint32_t)any) |
+                      (uint64_t)__reduce_or_sync(kAll, (uint32_t)(any >> 32)) << 32);
+        least = __reduce_min_sync(kAll, least);
+        const int lo = p.window > 0 ? max(base + least + 1 - p.window, 0) : 0;
+        const int kept = min(p.sinks, lo);
+        for (int x = x0; x < x1; ++x, ++it) {
+          const int st = it % S, key0 = first_key(x);
+          // (K's barrier may be a tile's phase further; V's slot waits for this warp)
+          ok = warp_wait(smem_u32(&bar_v[st]), (it / S) & 1, abort_flag, p.dev_status);
+          if (F8 && ok && it >= 2)
+            ok = warp_wait(smem_u32(&bar_wide_empty[it & 1]), ((it >> 1) - 1) & 1, abort_flag,
+                           p.dev_status);
+          if (!ok) break;
+          const uint32_t okp = s_meta[it % C::kMeta].ok;
+          // all of the tile's keys are seen by some token
+          const bool all = okp == (1u << n_pieces) - 1u && key0 + TK <= base &&
+                           (key0 >= lo || key0 + TK <= kept);
+          auto row_seen = [&](int row) -> bool {
+            const int key = key0 + row;
+            if (!((okp >> ((row >> 4) >> piece_shift)) & 1u)) return false;
+            if (key < base) return key >= lo || key < kept;
+            return key - base < 64 && ((any >> (key - base)) & 1u);
+          };
+          if constexpr (F8) {
+            const uint32_t from = sV(st), to = wide + (it & 1) * C::kWideBytes;
+            constexpr int kCpr = D / 16;  // chunks of 16 codes per row
+#pragma unroll 4
+            for (int i = (warp - 2) * 32 + lane; i < TK * kCpr; i += 64) {
+              const int row = i / kCpr, c = i % kCpr;
+              uint4 v = lds128(chunk_at<PB>(from, TK, row, c));
+              if (!all && !row_seen(row)) v = make_uint4(0, 0, 0, 0);
+              sts128(chunk_at<128>(to, TK, row, 2 * c),
+                     make_uint4(e4m3_half(v.x, 0), e4m3_half(v.x, 1), e4m3_half(v.y, 0),
+                                e4m3_half(v.y, 1)));
+              sts128(chunk_at<128>(to, TK, row, 2 * c + 1),
+                     make_uint4(e4m3_half(v.z, 0), e4m3_half(v.z, 1), e4m3_half(v.w, 0),
+                                e4m3_half(v.w, 1)));
+            }
+            fence_proxy_async_smem();
+          } else if (!all) {
+            for (int i = (warp - 2) * 32 + lane; i < TK * (D / 8); i += 64) {
+              const int row = i / (D / 8), c = i % (D / 8);
+              if (!row_seen(row)) sts128(chunk_at<PB>(sV(st), TK, row, c), make_uint4(0, 0, 0, 0));
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&bar_ready[st]));
+            if (F8) mbar_arrive(smem_u32(&bar_v_empty[st]));
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    take_registers<kSoftmaxRegs>();
+    constexpr float kThr = F8 ? 4.f : 8.f;    // the reference moves when exceeded by 2^kThr
+    constexpr float kBias = F8 ? 11.f : 0.f;  // weights are held times 2^kBias: at most 2^15 in fp16
+    const int w = (warp - 4) >> 2;
+    const int lane_row = ((warp & 3) << 5) + lane;  // TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t S_row = tmem + w * 128 + lane_off;
+    int gt = 0, jobs = 0, no[2] = {0, 0}, nml = 0;
+    bool ok = true;
+    while (ok && left > 0) {
+      int g, rt, x0, x1;
+      const int before = t1 - left;
+      if (!next_seg(g, rt, x0, x1)) continue;
+      const int rows = rows_of_unit(rt);
+      const bool alt = !kTwo || rows <= kRows;
+      const int T = x1 - x0;
+      const int n_jobs = alt ? (T + 1 - w) >> 1 : T;  // this warpgroup's
+      const bool whole_l = x0 == 0, whole_r = x1 == r.nt;
+      // this thread's q row: token, head, position, mask
+      const int row = lane_row + (alt ? 0 : w * kRows);
+      const bool in = row < rows;
+      const int rr = rt * C::kUnitRows + row;
+      const int tok = in ? rr / p.group : 0;
+      const int head = in ? g * p.group + (rr - tok * p.group) : 0;
+      const int base = r.L - r.n;
+      uint64_t mask = 0;
+      if (in) mask = p.mask[r.q0 + tok] & (r.n >= 64 ? ~0ull : (1ull << r.n) - 1);
+      const int pos = base + max(__popcll(mask) - 1, 0);
+      mask &= present(r.n, base);
+      float fac = p.scale_log2;
+      // ---- q
+      {
+        const uint16_t* src = p.q + ((int64_t)(r.q0 + tok) * p.hq + head) * D;
+        const bool mine = w == 0 || !alt;  // this warpgroup writes the tile
+        const uint32_t to = sq + (alt ? 0 : w) * C::kQBytes;
+        uint4 v[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          v[i] = in ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+        if constexpr (F8) {
+          uint32_t top = 0;  // largest |q| of the row, as bf16 bits
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t m[4] = {v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu, v[i].z & 0x7FFF7FFFu,
+                                   v[i].w & 0x7FFF7FFFu};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max(top, max(m[k] & 0xFFFFu, m[k] >> 16));
+          }
+          const int ex = max((int)(top >> 7), 27);  // biased exponent; q' = q 2^(7 - e) < 2^8
+          const float up = __uint_as_float((uint32_t)(261 - ex < 1 ? 1 : 261 - ex) << 23);
+          fac *= __uint_as_float((uint32_t)(ex < 8 ? 1 : ex - 7) << 23);
+          if (mine) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {  // 16 values: a chunk of each half
+              uint32_t hi[4], lo[4];
+              const uint32_t u[8] = {v[2 * c].x,     v[2 * c].y,     v[2 * c].z,     v[2 * c].w,
+                                     v[2 * c + 1].x, v[2 * c + 1].y, v[2 * c + 1].z, v[2 * c + 1].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                hi[k] = lo[k] = 0;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const float a = __uint_as_float(u[2 * k + z] << 16) * up,
+                              c2 = __uint_as_float(u[2 * k + z] & 0xFFFF0000u) * up;
+                  const uint32_t h2 = cvt_e4m3x2(a, c2);
+                  const float2 back = e4m3x2_to_float2((uint16_t)h2);
+                  hi[k] |= h2 << (16 * z);
+                  lo[k] |= cvt_e4m3x2(a - back.x, c2 - back.y) << (16 * z);
+                }
+              }
+              const uint32_t dst = chunk_at<PB>(to, kRows, lane_row, c);
+              sts128(dst, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+              sts128(dst + kRows * PB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+            }
+          }
+        } else if (mine) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) sts128(chunk_at<PB>(to, kRows, lane_row, c), v[c]);
+        }
+        if (mine) {
+          fence_proxy_async_smem();
+          mbar_arrive(smem_u32(&bar_q[alt ? 0 : w]));
+        }
+      }
+      // every row sees the keys of a tile in front of `base` and, with a window, from clear_lo on (or
+      // among the first ones)
+      const int clear_lo = p.window > 0 ? base + r.n - p.window : 0;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int jj = 0; jj < n_jobs; ++jj) {
+        const int j = alt ? 2 * jj + w : jj;  // tile of the part
+        const int t = gt + j;
+        ok = warp_wait(smem_u32(&bar_meta[t % C::kMeta]), (t / C::kMeta) & 1, abort_flag,
+                       p.dev_status) &&
+             warp_wait(smem_u32(&bar_s[w]), (jobs + jj) & 1, abort_flag, p.dev_status);
+        if (!ok) break;
+        tc_fence_after();
+        const int kv0 = first_key(x0 + j);
+        const Meta<C::kPieces>& meta = s_meta[t % C::kMeta];
+        uint32_t sr[TK];
+        float part_max[TK / 32];
+#pragma unroll
+        for (int c = 0; c < TK / 32; ++c)
+          part_max[c] =
+              tmem_ld32_max(S_row + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+        tmem_ld_wait();
+        float* s = reinterpret_cast<float*>(sr);
+        const uint32_t okp = meta.ok;
+        const bool clear = okp == (1u << n_pieces) - 1u && kv0 + TK <= base &&
+                           (p.window == 0 || kv0 >= clear_lo || kv0 + TK <= p.sinks);
+        if (!clear) {
+#pragma unroll
+          for (int c = 0; c < TK / 32; ++c) {
+            const int k0 = kv0 + 32 * c;
+            uint32_t see = below(base, k0);
+            if (p.window > 0) see &= ~below(pos + 1 - p.window, k0) | below(p.sinks, k0);
+            const int sh = k0 - base;  // the word's first column among the new tokens
+            if (sh > -32 && sh < 64) see |= (uint32_t)(sh >= 0 ? mask >> sh : mask << -sh);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (!((okp >> ((2 * c + h) >> piece_shift)) & 1u)) see &= ~(0xFFFFu << (16 * h));
+            if (__all_sync(kAll, see == kAll)) continue;
+#pragma unroll
+            for (int cc = 0; cc < 32; ++cc)
+              if (!((see >> cc) & 1u)) s[32 * c + cc] = -INFINITY;
+            part_max[c] = row_max<32>(s + 32 * c);
+          }
+        }
+        // ---- scores in the exp2 domain are s a + vl, with a and vl of the key's page; a > 0, so a
+        // page's largest score has its largest s
+        float tile_max = -INFINITY;
+        if constexpr (F8) {
+          if (piece_shift == 0) {
+#pragma unroll
+            for (int c = 0; c < TK / 16; ++c)
+              tile_max = fmaxf(tile_max, fmaf(row_max<16>(s + 16 * c), fac * meta.ks[c], meta.vl[c]));
+          } else {
+#pragma unroll
+            for (int c = 0; c < TK / 32; ++c) {
+              const int pc = (2 * c) >> piece_shift;
+              tile_max = fmaxf(tile_max, fmaf(part_max[c], fac * meta.ks[pc], meta.vl[pc]));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < TK / 32; ++c) tile_max = fmaxf(tile_max, part_max[c]);
+          tile_max *= fac;
+        }
+        const bool resc = tile_max > m_ref + kThr;  // false for -inf
+        float alpha = 1.f;
+        if (resc) {
+          alpha = ex2_approx(m_ref - tile_max);  // 0 from -inf
+          l *= alpha;
+          m_ref = tile_max;
+        }
+        const float shift = m_ref == -INFINITY ? 0.f : kBias - m_ref;
+        // ---- weights, packed in place
+#pragma unroll
+        for (int c = 0; c < TK / 16; ++c) {
+          float a = fac, add = shift, inv = 1.f;
+          if constexpr (F8) {
+            const int pc = c >> piece_shift;
+            a = fac * meta.ks[pc];
+            add = shift + meta.vl[pc];
+            inv = meta.vi[pc];
+          }
+          const float2 a2 = make_float2(a, a), b2 = make_float2(add, add);
+          float2 acc = make_float2(0.f, 0.f);
+          float2 y[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            y[u] = ffma2(make_float2(s[16 * c + 2 * u], s[16 * c + 2 * u + 1]), a2, b2);
+            y[u].x = ex2_approx(y[u].x);
+            y[u].y = ex2_approx(y[u].y);
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            acc = fadd2(acc, y[u]);
+            sr[8 * c + u] = F8 ? pack_f16x2(y[u].x, y[u].y) : pack_bf16x2(y[u].x, y[u].y);
+          }
+          l = fmaf(acc.x + acc.y, inv, l);
+          if (c % 4 == 3)
+            tmem_st32(S_row + (c / 4) * 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[(c / 4) * 32]));
+        }
+        // The accumulator: its last product was issued before this tile's S, which is complete.
+        if (jj > 0 && __any_sync(kAll, resc)) {
+          const uint32_t O_row = tmem + 256 + w * 128 + lane_off;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(O_row + c0, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+            tmem_st16(O_row + c0, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&bar_p[w]));
+      }
+      if (!ok) break;
+      jobs += n_jobs;
+      gt += T;
+      // ---- the unit's part ends
+      // No second warpgroup's statistics without a tile of its own: only a tile's scores tell it that
+      // the first one has read those of the part before.
+      const bool other = alt && T > 1;
+      if (alt && w == 1) {
+        if (other) {
+          s_ml[lane_row] = make_float2(m_ref, l);
+          mbar_arrive(smem_u32(&bar_ml));
+        }
+        no[1] += other;
+      } else {
+        float m1 = -INFINITY, l1 = 0.f;
+        if (other) {
+          ok = warp_wait(smem_u32(&bar_ml), nml & 1, abort_flag, p.dev_status);
+          if (!ok) break;
+          ++nml;
+          const float2 ml = s_ml[lane_row];
+          m1 = ml.x;
+          l1 = ml.y;
+        }
+        ok = warp_wait(smem_u32(&bar_o[w]), no[w] & 1, abort_flag, p.dev_status);
+        ++no[w];
+        if (ok && other) ok = warp_wait(smem_u32(&bar_o[1]), no[1] & 1, abort_flag, p.dev_status);
+        if (w == 0 && (other || !alt)) ++no[1];
+        if (!ok) break;
+        tc_fence_after();
+        const bool final = whole_l && whole_r;
+        const float top = fmaxf(m_ref, m1);
+        float f0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - top);
+        float f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - top);
+        const float sum = l * f0 + l1 * f1;
+        if (final) {
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          f0 *= inv;
+          f1 *= inv;
+        }
+        const int64_t at = (int64_t)(r.q0 + tok) * p.hq + head;
+        float* part = p.parts + (size_t)(2 * blockIdx.x + (whole_l ? 1 : 0)) * (C::kUnitRows * (D + 2));
+        float* to32 = final ? static_cast<float*>(p.out) + at * D : part + row * D;
+        uint16_t* to16 = static_cast<uint16_t*>(p.out) + at * D;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(tmem + 256 + w * 128 + lane_off + c0, o);
+          tmem_ld_wait();
+          float v[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(o[q]) * f0;
+          if (other) {
+            tmem_ld32(tmem + 384 + lane_off + c0, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = fmaf(__uint_as_float(o[q]), f1, v[q]);
+          }
+          if (!in) continue;
+          if (final && p.out_bf16) {
+#pragma unroll
+            for (int q = 0; q < 32; q += 8)
+              *reinterpret_cast<uint4*>(to16 + c0 + q) =
+                  make_uint4(pack_bf16x2(v[q], v[q + 1]), pack_bf16x2(v[q + 2], v[q + 3]),
+                             pack_bf16x2(v[q + 4], v[q + 5]), pack_bf16x2(v[q + 6], v[q + 7]));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 32; q += 4)
+              *reinterpret_cast<float4*>(to32 + c0 + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+          }
+        }
+        if (in) {
+          if (!final)
+            *reinterpret_cast<float2*>(part + C::kUnitRows * D + 2 * row) = make_float2(top, sum);
+          else if (p.lse != nullptr)
+            p.lse[at] = sum > 0.f ? (top - kBias + log2f(sum)) * kLn2 : -INFINITY;
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&bar_o_free[w]));
+        if (alt) mbar_arrive(smem_u32(&bar_o_free[1]));
+        if (!whole_l && whole_r && tid == 128) {
+          // the unit ends here: tell the second launch where it began
+          const int begin = before - x0;  // list place of the unit's first tile
+          const int longer = more * (len + 1);  // tiles of the runs with one more
+          const int c0 = begin < longer
+                             ? (int)((unsigned)begin / (unsigned)(len + 1))
+                             : more + (int)((unsigned)(begin - longer) / (unsigned)len);
+          p.jobs[blockIdx.x] = make_int4(c0, rows, rt * C::kUnitRows, g);
+          p.job_q0[blockIdx.x] = r.q0;
+        }
+      }
     }
   }
+  tc_fence_before();
   __syncthreads();
-  if (s_b < 0) return;
-  const int b = s_b, n = s_n;
-  int L = a.kv_lens[b];
-  if (L < 0 || L > a.max_pages * a.page_size) {
-    if (tid == 0 && a.dev_status) atomicOr(a.dev_status, kDevIndexRange);
-    L = 0;
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
-  const int base = L - n;
-  uint64_t mask = a.tree_mask[t];
-  if (n < 64) mask &= (1ull << n) - 1;
-  const int pos = base + max(__popcll(mask) - 1, 0);
-  for (int i = tid; i < D; i += 128)
-    s_q[i] = __uint_as_float((uint32_t) static_cast<const uint16_t*>(
-                                 a.q)[((int64_t)t * a.hq + h) * D + i]
-                             << 16);
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int k0 = 0; k0 < L; k0 += 128) {
+}
+
+// Joins the parts of the units that CTA borders cut: block (c, y) for rows y, y + kJoinRows, .. of
+// the unit that ended in CTA c. Four warps take every fourth part each, kBatch parts' loads in
+// flight, then the warps' results are joined in order.
+constexpr int kJoinRows = 16;
+template <int D>
+__global__ void __launch_bounds__(128) attn_tree_join_kernel(const Params p, float bias) {
+  constexpr int kWarps = 4, kBatch = 4;
+  const int R = p.unit_rows;
+  __shared__ float2 s_ml[kWarps];
+  __shared__ float4 s_acc[kWarps][D / 4];
+  const int c1 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_prior_grids();  // the parts are written
+  const int4 job = p.jobs[c1];
+  const int q0 = p.job_q0[c1];
+  if (job.x < 0) return;
+  const bool mine = lane < D / 4;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int row = blockIdx.y; row < job.y; row += kJoinRows) {
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = zero;
+    for (int c = job.x + warp; c <= c1; c += kWarps * kBatch) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int cc = c + i * kWarps;
+        ml[i] = make_float2(-INFINITY, 0.f);
+        v[i] = zero;
+        if (cc <= c1) {
+          const float* part = p.parts + (size_t)(2 * cc + (cc == job.x ? 1 : 0)) * (R * (D + 2));
+          ml[i] = *reinterpret_cast<const float2*>(part + R * D + 2 * row);
+          if (mine) v[i] = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
+        }
+      }
+      float n = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) n = fmaxf(n, ml[i].x);
+      const float f = top == -INFINITY ? 0.f : ex2_approx(top - n);
+      top = n;
+      sum *= f;
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float fi = ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - n);
+        sum = fmaf(ml[i].y, fi, sum);
+        acc.x = fmaf(v[i].x, fi, acc.x);
+        acc.y = fmaf(v[i].y, fi, acc.y);
+        acc.z = fmaf(v[i].z, fi, acc.z);
+        acc.w = fmaf(v[i].w, fi, acc.w);
+      }
+    }
+    if (lane == 0) s_ml[warp] = make_float2(top, sum);
+    if (mine) s_acc[warp][lane] = acc;
     __syncthreads();
-    const int key = k0 + tid;
-    const bool see =
-        key < L && (key < base ? a.window == 0 || key > pos - a.window || key < a.sinks
-                               : ((mask >> (key - base)) & 1) != 0);
-    float x = -INFINITY;
-    int page = -1;
-    if (see) {
-      page = a.page_tables[(int64_t)b * a.max_pages + key / a.page_size];
-      if (page < 0 || page >= a.num_pages) {
-        page = -1;
-        if (a.dev_status) atomicOr(a.dev_status, kDevIndexRange);
+    if (warp == 0) {
+      float m = -INFINITY, l = 0.f;
+      float4 o = zero;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = s_ml[w];
+        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+        l = fmaf(ml.y, f, l);
+        if (mine) {
+          const float4 v = s_acc[w][lane];
+          o.x = fmaf(v.x, f, o.x);
+          o.y = fmaf(v.y, f, o.y);
+          o.z = fmaf(v.z, f, o.z);
+          o.w = fmaf(v.w, f, o.w);
+        }
       }
-    }
-    if (F8 && page >= 0) {
-      const float ks = a.k_scale[(int64_t)page * a.hkv + g], vs = a.v_scale[(int64_t)page * a.hkv + g];
-      if (!(ks > 0.f && ks < INFINITY && vs >= 0x1p-80f && vs < INFINITY)) {
-        page = -1;
-        if (a.dev_status) atomicOr(a.dev_status, kDevBadArg);
+      const int rr = job.z + row, tok = rr / p.group;
+      const int64_t at = (int64_t)(q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      if (mine) {
+        if (p.out_bf16) {
+          uint2* to = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane;
+          *to = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        } else {
+          reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[lane] =
+              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        }
       }
+      if (p.lse != nullptr && lane == 0)
+        p.lse[at] = l > 0.f ? (m - bias + log2f(l)) * kLn2 : -INFINITY;
     }
-    if (page >= 0) {
-      const int64_t row = ((int64_t)page * a.hkv + g) * a.page_size + key % a.page_size;
-      x = 0.f;
-      for (int i = 0; i < D; ++i) {
-        float k;
-        if constexpr (F8)
-          k = float(reinterpret_cast<const __nv_fp8_e4m3*>(a.k_cache)[row * D + i]);
-        else
-          k = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.k_cache)[row * D + i] << 16);
-        x = fmaf(s_q[i], k, x);
-      }
-      if constexpr (F8) x *= a.k_scale[(int64_t)page * a.hkv + g];
-      x *= a.scale;
-    }
-    s_row[tid] = page;
-    float top = x;
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    if ((tid & 31) == 0) s_red[tid >> 5] = top;
-    __syncthreads();
-    const float nm = fmaxf(fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3])), m);
-    const float al = m == -INFINITY ? 0.f : expf(m - nm);
-    m = nm;
-    s_p[tid] = x == -INFINITY ? 0.f : expf(x - m);
-    __syncthreads();
-    l *= al;
-    o *= al;
-    for (int j = 0; j < 128; ++j) {
-      const float p = s_p[j];
-      l += p;
-      if (tid < D && s_row[j] >= 0) {
-        const int64_t head = (int64_t)s_row[j] * a.hkv + g;
-        const int64_t at = (head * a.page_size + (k0 + j) % a.page_size) * D + tid;
-        if constexpr (F8)
-          o = fmaf(p * a.v_scale[head], float(reinterpret_cast<const __nv_fp8_e4m3*>(a.v_cache)[at]), o);
-        else
-          o = fmaf(p, __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.v_cache)[at] << 16), o);
-      }
-    }
+    __syncthreads();  // before the next row's results
   }
-  const int64_t at = (int64_t)t * a.hq + h;
-  if (tid < D) {
-    const float v = l > 0.f ? o / l : 0.f;
-    if (a.out_bf16)
-      static_cast<uint16_t*>(a.out)[at * D + tid] = (uint16_t)pack_bf16x2(v, 0.f);
-    else
-      static_cast<float*>(a.out)[at * D + tid] = v;
+}
+
+// Rows of a unit: one q tile of 128, or two where a request may have more rows of one KV head.
+int rows_of(int max_q, int group) { return (int64_t)max_q * group <= kRows ? kRows : 2 * kRows; }
+size_t job_bytes(size_t ctas) {
+  return (ctas * (sizeof(int4) + sizeof(int)) + 255) / 256 * 256;
+}
+
+template <bool F8, int D, bool kTwo>
+cudaError_t launch(const AttnDecodeArgs& a, int dev, int sms, int* drv_err, cudaStream_t stream) {
+  using C = Cfg<F8, D, kTwo>;
+  Params p;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.cu_q = a.cu_q;
+  p.mask = a.tree_mask;
+  p.page_tables = a.page_tables;
+  p.kv_lens = a.kv_lens;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.dev_status = a.dev_status;
+  p.total_q = (int)a.total_q;
+  p.max_keys = a.max_pages * a.page_size;
+  p.batch = a.batch;
+  p.max_q = a.max_q;
+  p.hq = a.hq;
+  p.hkv = a.hkv;
+  p.group = a.hq / a.hkv;
+  p.num_pages = a.num_pages;
+  p.max_pages = a.max_pages;
+  p.page_size = a.page_size;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.scale_log2 = a.scale * kLog2e;
+  p.out_bf16 = a.out_bf16 ? 1 : 0;
+  p.ctas = sms;
+  p.unit_rows = C::kUnitRows;
+  p.jobs = static_cast<int4*>(a.workspace);
+  p.job_q0 = reinterpret_cast<int*>(p.jobs + p.ctas);
+  p.parts =
+      reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + job_bytes((size_t)p.ctas));
+  CUtensorMap mk, mv;
+  auto make = [&](CUtensorMap* m, void* base) -> bool {
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.page_size, (uint64_t)a.num_pages * a.hkv};
+    const uint64_t strides[2] = {(uint64_t)C::kRowBytes, (uint64_t)C::kRowBytes * a.page_size};
+    const uint32_t box[3] = {(uint32_t)(F8 ? D : 64),
+                             (uint32_t)(a.page_size < C::kTK ? a.page_size : C::kTK), 1};
+    const CUresult e = encode_tensor_map(
+        m, F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims,
+        strides, box, C::kPanelBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+    if (e != CUDA_SUCCESS) *drv_err = (int)e;
+    return e == CUDA_SUCCESS;
+  };
+  if (!make(&mk, const_cast<void*>(a.k_cache)) || !make(&mv, const_cast<void*>(a.v_cache)))
+    return cudaErrorInvalidValue;
+  auto kernel = attn_tree_kernel<F8, D, kTwo>;
+  // The registers that move between the warps must be those that the block is launched with.
+  static std::atomic<int> known{0};
+  int regs = 0;
+  cudaError_t e = ask_once(known, &regs, [&](int* n) {
+    cudaFuncAttributes f;
+    const cudaError_t err = cudaFuncGetAttributes(&f, kernel);
+    if (err == cudaSuccess) *n = f.numRegs;
+    return err;
+  });
+  if (e != cudaSuccess) return e;
+  if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+  // The kernel's shared-memory limit is set once per device (bit i: device i), not per call. A
+  // launch that fails has it set again.
+  static std::atomic<uint64_t> set{0};
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(set.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
   }
-  if (tid == 0 && a.lse != nullptr) a.lse[at] = l > 0.f ? m + logf(l) : -INFINITY;
+  e = launch_ahead(kernel, dim3(p.ctas), kThreads, C::kSmemBytes, stream, mk, mv, p);
+  if (e != cudaSuccess) {
+    set.fetch_and(~bit, std::memory_order_relaxed);
+    return e;
+  }
+  return launch_ahead(attn_tree_join_kernel<D>, dim3(p.ctas, kJoinRows), 128, 0, stream, p,
+                      F8 ? 11.f : 0.f);
+}
+
+template <bool F8, int D>
+cudaError_t launch_rows(const AttnDecodeArgs& a, int dev, int sms, int* drv_err,
+                        cudaStream_t stream) {
+  return rows_of(a.max_q, a.hq / a.hkv) == kRows ? launch<F8, D, false>(a, dev, sms, drv_err, stream)
+                                                 : launch<F8, D, true>(a, dev, sms, drv_err, stream);
 }
 
 }  // namespace
 
-size_t attn_tree_workspace_bytes(int, int, int, int, int) { return 16; }
+size_t attn_tree_workspace_bytes(int max_q, int hq, int hkv, int d, int sms) {
+  const size_t ctas = (size_t)sms, rows = rows_of(max_q, hq / hkv);
+  return job_bytes(ctas) + ctas * 2 * rows * (d + 2) * sizeof(float);
+}
 
-cudaError_t launch_attn_tree(const AttnDecodeArgs& a, int*, cudaStream_t stream) {
-  const dim3 grid((unsigned)a.total_q, (unsigned)a.hq);
+cudaError_t launch_attn_tree(const AttnDecodeArgs& a, int* drv_err, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
   if (a.d == 64)
-    return launch_ahead(a.f8 ? attn_tree_simple_kernel<true, 64> : attn_tree_simple_kernel<false, 64>,
-                        grid, 128, 0, stream, a);
-  return launch_ahead(a.f8 ? attn_tree_simple_kernel<true, 128> : attn_tree_simple_kernel<false, 128>,
-                      grid, 128, 0, stream, a);
+    return a.f8 ? launch_rows<true, 64>(a, dev, sms, drv_err, stream)
+                : launch_rows<false, 64>(a, dev, sms, drv_err, stream);
+  if (a.d == 128)
+    return a.f8 ? launch_rows<true, 128>(a, dev, sms, drv_err, stream)
+                : launch_rows<false, 128>(a, dev, sms, drv_err, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace tts
