@@ -79,8 +79,8 @@ struct Cfg {
 };
 
 // Registers move from the warps that issue to the softmax warps, which hold a tile's scores: 128 x
-// 80 + 256 x 208 = 63488 of the 384 x 168 = 64512 that the block is launched with.
-constexpr int kIssueRegs = 80, kSoftmaxRegs = 208;
+// 104 + 256 x 200 = 64512 = 384 x 168, all that the block is launched with.
+constexpr int kIssueRegs = 104, kSoftmaxRegs = 200;
 constexpr int kLaunchRegs = (128 * kIssueRegs + 256 * kSoftmaxRegs + kThreads - 1) / kThreads;
 template <int N>
 __device__ __forceinline__ void give_registers() {
@@ -166,7 +166,9 @@ struct Params {
   const float* v_scale;
   void* out;
   float* lse;
-  float* parts;  // [2 * CTAs][unit_rows * (D + 2)]
+  // [2 * CTAs] parts: sums [D / 4][unit_rows] of four columns each (a row's thread writes beside its
+  // neighbours'), then [unit_rows] {reference, denominator}
+  float* parts;
   // [CTAs], of the unit that was begun in an earlier CTA and ended in this one: {first CTA
   // (-1: no such unit), rows, first row within the request, g}
   int4* jobs;
@@ -213,6 +215,18 @@ __device__ __forceinline__ Req load_req(const Params& p, int b, uint32_t* bad) {
   r.rt = (r.n * p.group + p.unit_rows - 1) / p.unit_rows;
   return r;
 }
+// A place in a ring of N slots and the parity of its current round.
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t odd = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      odd ^= 1;
+    }
+  }
+};
 // Bits of new tokens that are there: m < n and a key of its own (a length under n has none for some).
 __device__ __forceinline__ uint64_t present(int n, int base) {
   uint64_t m = n >= 64 ? ~0ull : (1ull << n) - 1;
@@ -400,6 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Lane i keeps page cache_at + i of the request (and what the others need of its scales for
       // head cache_g) in registers, loaded 32 pages at a time.
       int it = 0;
+      Ring<S> slot;
+      Ring<C::kMeta> mslot;
       int cache_b = -1, cache_at = 0, cache_g = -1, page = -1;
       bool fine = true;                    // the page's scales are in range
       float ks = 1.f, vl = 0.f, vi = 1.f;  // key scale, log2 and inverse of the value scale
@@ -407,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && left > 0) {
         int g, rt, x0, x1;
         if (!next_seg(g, rt, x0, x1)) continue;
-        for (int x = x0; x < x1; ++x, ++it) {
-          const int key0 = first_key(x), st = it % S;
+        for (int x = x0; x < x1; ++x, ++it, slot.next(), mslot.next()) {
+          const int key0 = first_key(x), st = slot.at;
           const int pg0 = key0 >> p.page_shift;
           if (cache_b != b || pg0 < cache_at || pg0 + n_pieces > cache_at + 32) {
             cache_b = b;
@@ -431,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool there = seen && pg >= 0;
           const uint32_t sent = __ballot_sync(kAll, there);
           if (it >= S) {
-            ok = warp_wait(smem_u32(&bar_k_empty[st]), ((it / S) - 1) & 1, abort_flag, p.dev_status);
+            ok = warp_wait(smem_u32(&bar_k_empty[st]), slot.odd ^ 1, abort_flag, p.dev_status);
             if (!ok) break;
           }
           const uint32_t bytes = __popc(sent) * piece * C::kRowBytes;
@@ -445,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint32_t flag = seen && !there ? kDevIndexRange : 0u;
           uint32_t use = sent;
-          Meta<C::kPieces>& meta = s_meta[it % C::kMeta];
+          Meta<C::kPieces>& meta = s_meta[mslot.at];
           if constexpr (F8) {
             if (new_scales) {
               cache_g = g;
@@ -470,12 +486,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) meta.ok = use;
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(smem_u32(&bar_meta[it % C::kMeta]));
+            mbar_arrive(smem_u32(&bar_meta[mslot.at]));
             mbar_arrive_expect_tx(smem_u32(&bar_k[st]), bytes);
           }
           bool v_ok = true;
           if (it >= S)
-            v_ok = warp_wait(smem_u32(&bar_v_empty[st]), ((it / S) - 1) & 1, abort_flag, p.dev_status);
+            v_ok = warp_wait(smem_u32(&bar_v_empty[st]), slot.odd ^ 1, abort_flag, p.dev_status);
           if (v_ok && there) {
 #pragma unroll
             for (int pn = 0; pn < C::kPanels; ++pn)
@@ -529,48 +545,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < TK / 16; ++k)
           mma_ts_elect(o_t(w), s_t(w) + k * 8, vd + ((k * 16 * 128) >> 4), idesc, acc || k > 0, e);
       };
-      int gt = 0, seg = 0;        // tiles and parts so far
-      int jobs[2] = {0, 0}, nq[2] = {0, 0};  // of each warpgroup: jobs, q tiles
+      Ring<S> kslot, vslot;   // of the next tile whose S, whose P V is issued
+      uint32_t wide_at = 0;   // e4m3: its widened V
+      uint32_t odd_p[2] = {0, 0}, odd_q[2] = {0, 0}, odd_o = 0;  // parities of the phases waited for next
+      bool first = true;      // part
       bool ok = true;
       while (ok && left > 0) {
         int g, rt, x0, x1;
         if (!next_seg(g, rt, x0, x1)) continue;
         const bool alt = !kTwo || rows_of_unit(rt) <= kRows;
-        const int T = x1 - x0, J = alt ? T : 2 * T;
-        // job i: warpgroup i % 2, and tile i, or i / 2 where each warpgroup takes every tile
-        for (int i = 0; ok && i < J + 2; ++i) {
-          const int w = i & 1;
-          if (i >= 2) {
-            const int j = i - 2, t = gt + (alt ? j : j >> 1), st = t % S;
-            ok = warp_wait(smem_u32(&bar_ready[st]), (t / S) & 1, abort_flag, p.dev_status) &&
-                 warp_wait(smem_u32(&bar_p[w]), (jobs[w] + (j >> 1)) & 1, abort_flag, p.dev_status);
-            if (ok && j < 2 && seg > 0)  // the sums of the part before have been read
-              ok = warp_wait(smem_u32(&bar_o_free[w]), (seg - 1) & 1, abort_flag, p.dev_status);
-            if (!ok) break;
+        const int J = alt ? x1 - x0 : 2 * (x1 - x0);
+        // Job i: warpgroup i % 2, and tile i, or i / 2 where each warpgroup takes every tile. The product
+        // of job i - 2's weights comes in front of job i's scores, which overwrite them.
+        auto step = [&](auto which, int i) -> bool {
+          constexpr int w = decltype(which)::value;
+          if (i >= 2 && i < J + 2) {
+            if (!warp_wait(smem_u32(&bar_ready[vslot.at]), vslot.odd, abort_flag, p.dev_status) ||
+                !warp_wait(smem_u32(&bar_p[w]), odd_p[w], abort_flag, p.dev_status))
+              return false;
+            odd_p[w] ^= 1;
+            // the sums of the part before have been read
+            if (i < 4 && !first &&
+                !warp_wait(smem_u32(&bar_o_free[w]), odd_o, abort_flag, p.dev_status))
+              return false;
             tc_fence_after();
-            issue_o(w, F8 ? wide + (t & 1) * C::kWideBytes : sV(st), j >= 2);
-            if (alt || w == 1)
-              mma_commit_elect(smem_u32(F8 ? &bar_wide_empty[t & 1] : &bar_v_empty[st]), e);
-            if (j + 2 >= J) mma_commit_elect(smem_u32(&bar_o[w]), e);
+            issue_o(w, F8 ? wide + wide_at * C::kWideBytes : sV(vslot.at), i >= 4);
+            if (alt || w == 1) {
+              mma_commit_elect(smem_u32(F8 ? &bar_wide_empty[wide_at] : &bar_v_empty[vslot.at]), e);
+              vslot.next();
+              wide_at ^= 1;
+            }
+            if (i >= J) mma_commit_elect(smem_u32(&bar_o[w]), e);
           }
           if (i < J) {
-            const int t = gt + (alt ? i : i >> 1), st = t % S, tile = alt ? 0 : w;
-            if (i < 2 && (!alt || i == 0)) {
-              ok = warp_wait(smem_u32(&bar_q[tile]), nq[tile] & 1, abort_flag, p.dev_status);
-              nq[tile]++;
+            const int tile = alt ? 0 : w;
+            if (i < 2 && (!alt || w == 0)) {
+              if (!warp_wait(smem_u32(&bar_q[w]), odd_q[w], abort_flag, p.dev_status)) return false;
+              odd_q[w] ^= 1;
             }
-            ok = ok && warp_wait(smem_u32(&bar_k[st]), (t / S) & 1, abort_flag, p.dev_status);
-            if (!ok) break;
+            if (!warp_wait(smem_u32(&bar_k[kslot.at]), kslot.odd, abort_flag, p.dev_status))
+              return false;
             tc_fence_after();
-            issue_s(w, tile, st);
+            issue_s(w, tile, kslot.at);
             mma_commit_elect(smem_u32(&bar_s[w]), e);
-            if (alt || w == 1) mma_commit_elect(smem_u32(&bar_k_empty[st]), e);
+            if (alt || w == 1) {
+              mma_commit_elect(smem_u32(&bar_k_empty[kslot.at]), e);
+              kslot.next();
+            }
           }
-        }
-        gt += T;
-        jobs[0] += (J + 1) >> 1;
-        jobs[1] += J >> 1;
-        ++seg;
+          return true;
+        };
+        for (int i = 0; ok && i < J + 2; i += 2)
+          ok = step(std::integral_constant<int, 0>(), i) && step(std::integral_constant<int, 1>(), i + 1);
+        if (!first) odd_o ^= 1;
+        first = false;
       }
       // Every product is complete before TMEM is freed.
       mma_commit_elect(smem_u32(&bar_drain), e);
@@ -578,6 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ------------------------------------------------------------------ V for the second product
       int it = 0;
+      Ring<S> slot;
+      Ring<C::kMeta> mslot;
       bool ok = true;
       while (ok && left > 0) {
         int g, rt, x0, x1;
@@ -599,15 +629,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         least = __reduce_min_sync(kAll, least);
         const int lo = p.window > 0 ? max(base + least + 1 - p.window, 0) : 0;
         const int kept = min(p.sinks, lo);
-        for (int x = x0; x < x1; ++x, ++it) {
-          const int st = it % S, key0 = first_key(x);
+        for (int x = x0; x < x1; ++x, ++it, slot.next(), mslot.next()) {
+          const int st = slot.at, key0 = first_key(x);
           // (K's barrier may be a tile's phase further; V's slot waits for this warp)
-          ok = warp_wait(smem_u32(&bar_v[st]), (it / S) & 1, abort_flag, p.dev_status);
+          ok = warp_wait(smem_u32(&bar_v[st]), slot.odd, abort_flag, p.dev_status);
           if (F8 && ok && it >= 2)
             ok = warp_wait(smem_u32(&bar_wide_empty[it & 1]), ((it >> 1) - 1) & 1, abort_flag,
                            p.dev_status);
           if (!ok) break;
-          const uint32_t okp = s_meta[it % C::kMeta].ok;
+          const uint32_t okp = s_meta[mslot.at].ok;
           // all of the tile's keys are seen by some token
           const bool all = okp == (1u << n_pieces) - 1u && key0 + TK <= base &&
                            (key0 >= lo || key0 + TK <= kept);
@@ -619,18 +649,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           if constexpr (F8) {
             const uint32_t from = sV(st), to = wide + (it & 1) * C::kWideBytes;
-            constexpr int kCpr = D / 16;  // chunks of 16 codes per row
-#pragma unroll 4
-            for (int i = (warp - 2) * 32 + lane; i < TK * kCpr; i += 64) {
-              const int row = i / kCpr, c = i % kCpr;
-              uint4 v = lds128(chunk_at<PB>(from, TK, row, c));
-              if (!all && !row_seen(row)) v = make_uint4(0, 0, 0, 0);
-              sts128(chunk_at<128>(to, TK, row, 2 * c),
-                     make_uint4(e4m3_half(v.x, 0), e4m3_half(v.x, 1), e4m3_half(v.y, 0),
-                                e4m3_half(v.y, 1)));
-              sts128(chunk_at<128>(to, TK, row, 2 * c + 1),
-                     make_uint4(e4m3_half(v.z, 0), e4m3_half(v.z, 1), e4m3_half(v.w, 0),
-                                e4m3_half(v.w, 1)));
+            // A thread's chunks of 16 codes lie kStep rows apart in one column: the swizzle is the
+            // same for all of them. kDeep are on their way at a time.
+            constexpr int kCpr = D / 16, kStep = 64 / kCpr, kDeep = 8;
+            static_assert(TK % (kStep * kDeep) == 0 && kStep % 8 == 0, "chunks");
+            const int i0 = (warp - 2) * 32 + lane, row0 = i0 / kCpr, c = i0 % kCpr;
+            // the second panel's lanes store the other chunk first: eight lanes, all banks
+            const int odd = c >> 2 & 1;
+            const uint32_t src = chunk_at<PB>(from, TK, row0, c);
+            const uint32_t dst0 = chunk_at<128>(to, TK, row0, 2 * c + odd),
+                           dst1 = chunk_at<128>(to, TK, row0, 2 * c + 1 - odd);
+#pragma unroll 1
+            for (int k0 = 0; k0 < TK / kStep; k0 += kDeep) {
+              uint4 v[kDeep];
+#pragma unroll
+              for (int k = 0; k < kDeep; ++k) v[k] = lds128(src + (k0 + k) * kStep * PB);
+              if (!all) {
+#pragma unroll
+                for (int k = 0; k < kDeep; ++k)
+                  if (!row_seen(row0 + (k0 + k) * kStep)) v[k] = make_uint4(0, 0, 0, 0);
+              }
+#pragma unroll
+              for (int k = 0; k < kDeep; ++k) {
+                const uint32_t x[4] = {odd ? v[k].z : v[k].x, odd ? v[k].w : v[k].y,
+                                       odd ? v[k].x : v[k].z, odd ? v[k].y : v[k].w};
+                sts128(dst0 + (k0 + k) * kStep * 128,
+                       make_uint4(e4m3_half(x[0], 0), e4m3_half(x[0], 1), e4m3_half(x[1], 0),
+                                  e4m3_half(x[1], 1)));
+                sts128(dst1 + (k0 + k) * kStep * 128,
+                       make_uint4(e4m3_half(x[2], 0), e4m3_half(x[2], 1), e4m3_half(x[3], 0),
+                                  e4m3_half(x[3], 1)));
+              }
             }
             fence_proxy_async_smem();
           } else if (!all) {
@@ -657,7 +706,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane_row = ((warp & 3) << 5) + lane;  // TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t S_row = tmem + w * 128 + lane_off;
-    int gt = 0, jobs = 0, no[2] = {0, 0}, nml = 0;
+    Ring<C::kMeta> mslot;  // of the part's next tile
+    // parities of the phases waited for next: own scores, own sums, the other's sums, its statistics
+    uint32_t odd_s = 0, odd_o = 0, odd_other = 0, odd_ml = 0;
     bool ok = true;
     while (ok && left > 0) {
       int g, rt, x0, x1;
@@ -666,7 +717,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = rows_of_unit(rt);
       const bool alt = !kTwo || rows <= kRows;
       const int T = x1 - x0;
-      const int n_jobs = alt ? (T + 1 - w) >> 1 : T;  // this warpgroup's
       const bool whole_l = x0 == 0, whole_r = x1 == r.nt;
       // this thread's q row: token, head, position, mask
       const int row = lane_row + (alt ? 0 : w * kRows);
@@ -738,103 +788,111 @@ __global__ void __launch_bounds__(kThreads, 1)
       // among the first ones)
       const int clear_lo = p.window > 0 ? base + r.n - p.window : 0;
       float m_ref = -INFINITY, l = 0.f;
-      for (int jj = 0; jj < n_jobs; ++jj) {
-        const int j = alt ? 2 * jj + w : jj;  // tile of the part
-        const int t = gt + j;
-        ok = warp_wait(smem_u32(&bar_meta[t % C::kMeta]), (t / C::kMeta) & 1, abort_flag,
-                       p.dev_status) &&
-             warp_wait(smem_u32(&bar_s[w]), (jobs + jj) & 1, abort_flag, p.dev_status);
+      for (int j = 0; j < T; ++j, mslot.next()) {  // tile of the part
+        if (alt && (j & 1) != w) continue;
+        ok = warp_wait(smem_u32(&bar_meta[mslot.at]), mslot.odd, abort_flag, p.dev_status) &&
+             warp_wait(smem_u32(&bar_s[w]), odd_s, abort_flag, p.dev_status);
         if (!ok) break;
+        odd_s ^= 1;
         tc_fence_after();
         const int kv0 = first_key(x0 + j);
-        const Meta<C::kPieces>& meta = s_meta[t % C::kMeta];
-        uint32_t sr[TK];
-        float part_max[TK / 32];
-#pragma unroll
-        for (int c = 0; c < TK / 32; ++c)
-          part_max[c] =
-              tmem_ld32_max(S_row + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-        tmem_ld_wait();
-        float* s = reinterpret_cast<float*>(sr);
+        const Meta<C::kPieces>& meta = s_meta[mslot.at];
         const uint32_t okp = meta.ok;
         const bool clear = okp == (1u << n_pieces) - 1u && kv0 + TK <= base &&
                            (p.window == 0 || kv0 >= clear_lo || kv0 + TK <= p.sinks);
-        if (!clear) {
+        // 64 columns at a time: 128 scores in registers spill. A tile of 128 has its second half
+        // looked at for the maximum first and loaded again for its weights.
+        float tile_max = -INFINITY, alpha = 1.f, shift = 0.f;
+        bool resc = false;
+#pragma unroll 1
+        for (int turn = TK == 128 ? 0 : 1; turn < (TK == 128 ? 3 : 2); ++turn) {
+          const int half = turn == 1 ? 0 : 1;
+          uint32_t sr[64];
+          float part_max[2];
 #pragma unroll
-          for (int c = 0; c < TK / 32; ++c) {
-            const int k0 = kv0 + 32 * c;
-            uint32_t see = below(base, k0);
-            if (p.window > 0) see &= ~below(pos + 1 - p.window, k0) | below(p.sinks, k0);
-            const int sh = k0 - base;  // the word's first column among the new tokens
-            if (sh > -32 && sh < 64) see |= (uint32_t)(sh >= 0 ? mask >> sh : mask << -sh);
+          for (int c = 0; c < 2; ++c)
+            part_max[c] = tmem_ld32_max(S_row + half * 64 + c * 32,
+                                        *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          tmem_ld_wait();
+          float* s = reinterpret_cast<float*>(sr);
+          if (!clear) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (!((okp >> ((2 * c + h) >> piece_shift)) & 1u)) see &= ~(0xFFFFu << (16 * h));
-            if (__all_sync(kAll, see == kAll)) continue;
+            for (int c = 0; c < 2; ++c) {
+              const int k0 = kv0 + half * 64 + 32 * c;
+              uint32_t see = below(base, k0);
+              if (p.window > 0) see &= ~below(pos + 1 - p.window, k0) | below(p.sinks, k0);
+              const int sh = k0 - base;  // the word's first column among the new tokens
+              if (sh > -32 && sh < 64) see |= (uint32_t)(sh >= 0 ? mask >> sh : mask << -sh);
 #pragma unroll
-            for (int cc = 0; cc < 32; ++cc)
-              if (!((see >> cc) & 1u)) s[32 * c + cc] = -INFINITY;
-            part_max[c] = row_max<32>(s + 32 * c);
-          }
-        }
-        // ---- scores in the exp2 domain are s a + vl, with a and vl of the key's page; a > 0, so a
-        // page's largest score has its largest s
-        float tile_max = -INFINITY;
-        if constexpr (F8) {
-          if (piece_shift == 0) {
+              for (int u = 0; u < 2; ++u)
+                if (!((okp >> ((4 * half + 2 * c + u) >> piece_shift)) & 1u)) see &= ~(0xFFFFu << (16 * u));
+              if (__all_sync(kAll, see == kAll)) continue;
 #pragma unroll
-            for (int c = 0; c < TK / 16; ++c)
-              tile_max = fmaxf(tile_max, fmaf(row_max<16>(s + 16 * c), fac * meta.ks[c], meta.vl[c]));
-          } else {
-#pragma unroll
-            for (int c = 0; c < TK / 32; ++c) {
-              const int pc = (2 * c) >> piece_shift;
-              tile_max = fmaxf(tile_max, fmaf(part_max[c], fac * meta.ks[pc], meta.vl[pc]));
+              for (int cc = 0; cc < 32; ++cc)
+                if (!((see >> cc) & 1u)) s[32 * c + cc] = -INFINITY;
+              part_max[c] = row_max<32>(s + 32 * c);
             }
           }
-        } else {
+          // Scores in the exp2 domain are s a + vl, with a and vl of the key's page; a > 0, so a
+          // page's largest score has its largest s.
+          if (turn < 2) {
+            if constexpr (F8) {
+              if (piece_shift == 0) {
 #pragma unroll
-          for (int c = 0; c < TK / 32; ++c) tile_max = fmaxf(tile_max, part_max[c]);
-          tile_max *= fac;
-        }
-        const bool resc = tile_max > m_ref + kThr;  // false for -inf
-        float alpha = 1.f;
-        if (resc) {
-          alpha = ex2_approx(m_ref - tile_max);  // 0 from -inf
-          l *= alpha;
-          m_ref = tile_max;
-        }
-        const float shift = m_ref == -INFINITY ? 0.f : kBias - m_ref;
-        // ---- weights, packed in place
+                for (int c = 0; c < 4; ++c)
+                  tile_max = fmaxf(tile_max, fmaf(row_max<16>(s + 16 * c), fac * meta.ks[4 * half + c],
+                                                  meta.vl[4 * half + c]));
+              } else {
 #pragma unroll
-        for (int c = 0; c < TK / 16; ++c) {
-          float a = fac, add = shift, inv = 1.f;
-          if constexpr (F8) {
-            const int pc = c >> piece_shift;
-            a = fac * meta.ks[pc];
-            add = shift + meta.vl[pc];
-            inv = meta.vi[pc];
+                for (int c = 0; c < 2; ++c) {
+                  const int pc = (4 * half + 2 * c) >> piece_shift;
+                  tile_max = fmaxf(tile_max, fmaf(part_max[c], fac * meta.ks[pc], meta.vl[pc]));
+                }
+              }
+            } else {
+              tile_max = fmaxf(tile_max, fmaxf(part_max[0], part_max[1]) * fac);
+            }
           }
-          const float2 a2 = make_float2(a, a), b2 = make_float2(add, add);
-          float2 acc = make_float2(0.f, 0.f);
-          float2 y[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            y[u] = ffma2(make_float2(s[16 * c + 2 * u], s[16 * c + 2 * u + 1]), a2, b2);
-            y[u].x = ex2_approx(y[u].x);
-            y[u].y = ex2_approx(y[u].y);
+          if (turn == 0) continue;
+          if (turn == 1) {
+            resc = tile_max > m_ref + kThr;  // false for -inf
+            if (resc) {
+              alpha = ex2_approx(m_ref - tile_max);  // 0 from -inf
+              l *= alpha;
+              m_ref = tile_max;
+            }
+            shift = m_ref == -INFINITY ? 0.f : kBias - m_ref;
           }
+          // ---- weights, packed in place
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            acc = fadd2(acc, y[u]);
-            sr[8 * c + u] = F8 ? pack_f16x2(y[u].x, y[u].y) : pack_bf16x2(y[u].x, y[u].y);
+          for (int c = 0; c < 4; ++c) {
+            float a = fac, add = shift, inv = 1.f;
+            if constexpr (F8) {
+              const int pc = (4 * half + c) >> piece_shift;
+              a = fac * meta.ks[pc];
+              add = shift + meta.vl[pc];
+              inv = meta.vi[pc];
+            }
+            const float2 a2 = make_float2(a, a), b2 = make_float2(add, add);
+            float2 acc = make_float2(0.f, 0.f);
+            float2 y[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              y[u] = ffma2(make_float2(s[16 * c + 2 * u], s[16 * c + 2 * u + 1]), a2, b2);
+              y[u].x = ex2_approx(y[u].x);
+              y[u].y = ex2_approx(y[u].y);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              acc = fadd2(acc, y[u]);
+              sr[8 * c + u] = F8 ? pack_f16x2(y[u].x, y[u].y) : pack_bf16x2(y[u].x, y[u].y);
+            }
+            l = fmaf(acc.x + acc.y, inv, l);
           }
-          l = fmaf(acc.x + acc.y, inv, l);
-          if (c % 4 == 3)
-            tmem_st32(S_row + (c / 4) * 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[(c / 4) * 32]));
+          tmem_st32(S_row + half * 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[0]));
         }
         // The accumulator: its last product was issued before this tile's S, which is complete.
-        if (jj > 0 && __any_sync(kAll, resc)) {
+        if (j > (alt ? w : 0) && __any_sync(kAll, resc)) {
           const uint32_t O_row = tmem + 256 + w * 128 + lane_off;
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 16) {
@@ -851,8 +909,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(smem_u32(&bar_p[w]));
       }
       if (!ok) break;
-      jobs += n_jobs;
-      gt += T;
       // ---- the unit's part ends
       // No second warpgroup's statistics without a tile of its own: only a tile's scores tell it that
       // the first one has read those of the part before.
@@ -861,22 +917,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (other) {
           s_ml[lane_row] = make_float2(m_ref, l);
           mbar_arrive(smem_u32(&bar_ml));
+          odd_o ^= 1;  // the first warpgroup waits for the sums
         }
-        no[1] += other;
       } else {
         float m1 = -INFINITY, l1 = 0.f;
         if (other) {
-          ok = warp_wait(smem_u32(&bar_ml), nml & 1, abort_flag, p.dev_status);
+          ok = warp_wait(smem_u32(&bar_ml), odd_ml, abort_flag, p.dev_status);
           if (!ok) break;
-          ++nml;
+          odd_ml ^= 1;
           const float2 ml = s_ml[lane_row];
           m1 = ml.x;
           l1 = ml.y;
         }
-        ok = warp_wait(smem_u32(&bar_o[w]), no[w] & 1, abort_flag, p.dev_status);
-        ++no[w];
-        if (ok && other) ok = warp_wait(smem_u32(&bar_o[1]), no[1] & 1, abort_flag, p.dev_status);
-        if (w == 0 && (other || !alt)) ++no[1];
+        ok = warp_wait(smem_u32(&bar_o[w]), odd_o, abort_flag, p.dev_status);
+        odd_o ^= 1;
+        if (ok && other) ok = warp_wait(smem_u32(&bar_o[1]), odd_other, abort_flag, p.dev_status);
+        if (other || !alt) odd_other ^= 1;  // the second warpgroup had sums
         if (!ok) break;
         tc_fence_after();
         const bool final = whole_l && whole_r;
@@ -891,7 +947,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int64_t at = (int64_t)(r.q0 + tok) * p.hq + head;
         float* part = p.parts + (size_t)(2 * blockIdx.x + (whole_l ? 1 : 0)) * (C::kUnitRows * (D + 2));
-        float* to32 = final ? static_cast<float*>(p.out) + at * D : part + row * D;
+        float* to32 = final ? static_cast<float*>(p.out) + at * D : part + row * 4;
+        const int quad = final ? 4 : 4 * C::kUnitRows;  // from four columns to the next
         uint16_t* to16 = static_cast<uint16_t*>(p.out) + at * D;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -917,7 +974,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
 #pragma unroll
             for (int q = 0; q < 32; q += 4)
-              *reinterpret_cast<float4*>(to32 + c0 + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+              *reinterpret_cast<float4*>(to32 + (c0 + q) / 4 * quad) =
+                  make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
           }
         }
         if (in) {
@@ -950,95 +1008,103 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the units that CTA borders cut: block (c, y) for rows y, y + kJoinRows, .. of
-// the unit that ended in CTA c. Four warps take every fourth part each, kBatch parts' loads in
-// flight, then the warps' results are joined in order.
-constexpr int kJoinRows = 16;
+// Joins the parts of the units that CTA borders cut: block (c, y, z) for rows 32 y .. of the unit that
+// ended in CTA c, columns 32 z .. . A lane is a row; warps are four groups of parts by two groups of 16
+// columns, a group takes every fourth part, two at a time, and the groups' sums are joined in
+// order through shared memory, from where rows leave.
 template <int D>
-__global__ void __launch_bounds__(128) attn_tree_join_kernel(const Params p, float bias) {
-  constexpr int kWarps = 4, kBatch = 4;
+__global__ void __launch_bounds__(256) attn_tree_join_kernel(const Params p, float bias) {
+  constexpr int kGroups = 4, kBatch = 2;
+  __shared__ float2 s_ml[kGroups][32];
+  __shared__ float s_acc[kGroups][32][33];
   const int R = p.unit_rows;
-  __shared__ float2 s_ml[kWarps];
-  __shared__ float4 s_acc[kWarps][D / 4];
   const int c1 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = warp >> 1, half = warp & 1;
   wait_for_prior_grids();  // the parts are written
   const int4 job = p.jobs[c1];
+  const int row0 = blockIdx.y * 32, row = row0 + lane;
+  if (job.x < 0 || row0 >= job.y) return;
   const int q0 = p.job_q0[c1];
-  if (job.x < 0) return;
-  const bool mine = lane < D / 4;
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int row = blockIdx.y; row < job.y; row += kJoinRows) {
-    float top = -INFINITY, sum = 0.f;
-    float4 acc = zero;
-    for (int c = job.x + warp; c <= c1; c += kWarps * kBatch) {
-      float2 ml[kBatch];
-      float4 v[kBatch];
+  float top = -INFINITY, sum = 0.f;
+  float4 acc[4];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int cc = c + i * kWarps;
-        ml[i] = make_float2(-INFINITY, 0.f);
-        v[i] = zero;
-        if (cc <= c1) {
-          const float* part = p.parts + (size_t)(2 * cc + (cc == job.x ? 1 : 0)) * (R * (D + 2));
-          ml[i] = *reinterpret_cast<const float2*>(part + R * D + 2 * row);
-          if (mine) v[i] = *reinterpret_cast<const float4*>(part + row * D + lane * 4);
-        }
-      }
-      float n = top;
+  for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = job.x + grp; c <= c1; c += kGroups * kBatch) {
+    float2 ml[kBatch];
+    float4 v[kBatch][4];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) n = fmaxf(n, ml[i].x);
-      const float f = top == -INFINITY ? 0.f : ex2_approx(top - n);
-      top = n;
-      sum *= f;
-      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    for (int i = 0; i < kBatch; ++i) {
+      const int cc = c + i * kGroups;
+      ml[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const float fi = ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - n);
-        sum = fmaf(ml[i].y, fi, sum);
-        acc.x = fmaf(v[i].x, fi, acc.x);
-        acc.y = fmaf(v[i].y, fi, acc.y);
-        acc.z = fmaf(v[i].z, fi, acc.z);
-        acc.w = fmaf(v[i].w, fi, acc.w);
+      for (int q = 0; q < 4; ++q) v[i][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (cc <= c1 && row < job.y) {
+        const float* part = p.parts + (size_t)(2 * cc + (cc == job.x ? 1 : 0)) * (R * (D + 2));
+        ml[i] = *reinterpret_cast<const float2*>(part + R * D + 2 * row);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          v[i][q] = *reinterpret_cast<const float4*>(
+              part + ((blockIdx.z * 8 + half * 4 + q) * (size_t)R + row) * 4);
       }
     }
-    if (lane == 0) s_ml[warp] = make_float2(top, sum);
-    if (mine) s_acc[warp][lane] = acc;
-    __syncthreads();
-    if (warp == 0) {
-      float m = -INFINITY, l = 0.f;
-      float4 o = zero;
+    float n = top;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w].x);
+    for (int i = 0; i < kBatch; ++i) n = fmaxf(n, ml[i].x);
+    const float f = top == -INFINITY ? 0.f : ex2_approx(top - n);
+    top = n;
+    sum *= f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = s_ml[w];
-        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-        l = fmaf(ml.y, f, l);
-        if (mine) {
-          const float4 v = s_acc[w][lane];
-          o.x = fmaf(v.x, f, o.x);
-          o.y = fmaf(v.y, f, o.y);
-          o.z = fmaf(v.z, f, o.z);
-          o.w = fmaf(v.w, f, o.w);
-        }
+    for (int q = 0; q < 4; ++q)
+      acc[q] = make_float4(acc[q].x * f, acc[q].y * f, acc[q].z * f, acc[q].w * f);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float fi = ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - n);
+      sum = fmaf(ml[i].y, fi, sum);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        acc[q].x = fmaf(v[i][q].x, fi, acc[q].x);
+        acc[q].y = fmaf(v[i][q].y, fi, acc[q].y);
+        acc[q].z = fmaf(v[i][q].z, fi, acc[q].z);
+        acc[q].w = fmaf(v[i][q].w, fi, acc[q].w);
       }
-      const int rr = job.z + row, tok = rr / p.group;
-      const int64_t at = (int64_t)(q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      if (mine) {
-        if (p.out_bf16) {
-          uint2* to = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane;
-          *to = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        } else {
-          reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D)[lane] =
-              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        }
-      }
-      if (p.lse != nullptr && lane == 0)
-        p.lse[at] = l > 0.f ? (m - bias + log2f(l)) * kLn2 : -INFINITY;
     }
-    __syncthreads();  // before the next row's results
   }
+  if (half == 0) s_ml[grp][lane] = make_float2(top, sum);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float* to = &s_acc[grp][lane][half * 16 + 4 * q];
+    to[0] = acc[q].x;
+    to[1] = acc[q].y;
+    to[2] = acc[q].z;
+    to[3] = acc[q].w;
+  }
+  __syncthreads();
+  // eight lanes write a row's 32 columns, a warp four rows
+  const int rr0 = warp * 4 + (lane >> 3), c0 = (lane & 7) * 4;
+  if (row0 + rr0 >= job.y) return;
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < kGroups; ++w) m = fmaxf(m, s_ml[w][rr0].x);
+#pragma unroll
+  for (int w = 0; w < kGroups; ++w) {
+    const float2 ml = s_ml[w][rr0];
+    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = fmaf(s_acc[w][rr0][c0 + k], f, o[k]);
+  }
+  const int rr = job.z + row0 + rr0, tok = rr / p.group;
+  const int64_t at = (int64_t)(q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int64_t to = at * D + blockIdx.z * 32 + c0;
+  if (p.out_bf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) =
+        make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  if (p.lse != nullptr && blockIdx.z == 0 && (lane & 7) == 0)
+    p.lse[at] = l > 0.f ? (m - bias + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Rows of a unit: one q tile of 128, or two where a request may have more rows of one KV head.
@@ -1123,8 +1189,8 @@ cudaError_t launch(const AttnDecodeArgs& a, int dev, int sms, int* drv_err, cuda
     set.fetch_and(~bit, std::memory_order_relaxed);
     return e;
   }
-  return launch_ahead(attn_tree_join_kernel<D>, dim3(p.ctas, kJoinRows), 128, 0, stream, p,
-                      F8 ? 11.f : 0.f);
+  return launch_ahead(attn_tree_join_kernel<D>, dim3(p.ctas, C::kUnitRows / 32, D / 32), 256, 0,
+                      stream, p, F8 ? 11.f : 0.f);
 }
 
 template <bool F8, int D>
