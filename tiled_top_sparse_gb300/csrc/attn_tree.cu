@@ -148,6 +148,34 @@ __device__ __forceinline__ uint32_t below(int n, int c0) {  // bits of columns c
   return b <= 0 ? 0u : b >= 32 ? kAll : (1u << b) - 1u;
 }
 
+// Bounded wait of a converged warp in few instructions: every role has its own, and what the
+// instruction cache does not hold is waited for as well. Sets *abort where it runs out.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+  uint32_t since = 0;
+  bool ok = true;
+  if (!mbar_peek(bar, parity)) {
+    while (!mbar_test(bar, parity)) {
+      if (*abort) {
+        ok = false;
+        break;
+      }
+      uint32_t now;
+      asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));
+      if (since == 0) since = now | 1u;
+      if ((int)(now - since) > (int)kWaitLimitNs) *abort = 1;
+    }
+  }
+  return __all_sync(kAll, ok);
+}
+// Two columns of a warp's TMEM lanes.
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t a, uint32_t b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(a), "r"(b)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t& a, uint32_t& b) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(taddr));
+}
+
 template <int kP>
 struct Meta {  // of a tile, written by the producer
   uint32_t ok;   // bit i: piece i (a page, or the tile if pages are larger) is there
@@ -243,13 +271,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   // K and V landed; K's last product done; V ready for its product (widened, or cleared); V's slot
   // (e4m3: the codes') free; the tile's scales written; e4m3: a widened V's last product done; a
-  // warpgroup's scores, weights and sums; its q tile written; its sums read; the second
-  // warpgroup's statistics
+  // warpgroup's scores, weights and sums; the q tiles written; the warpgroups done with a part (its
+  // sums read, its products complete); the second warpgroup's statistics
   __shared__ __align__(8) uint64_t bar_k[S], bar_v[S], bar_k_empty[S], bar_v_empty[S],
-      bar_ready[S], bar_meta[C::kMeta], bar_wide_empty[2], bar_s[2], bar_p[2], bar_o[2], bar_q[2], bar_o_free[2],
+      bar_ready[S], bar_meta[C::kMeta], bar_wide_empty[2], bar_s[2], bar_p[2], bar_o[2], bar_q, bar_done,
       bar_ml, bar_drain;
   __shared__ Meta<C::kPieces> s_meta[C::kMeta];
-  __shared__ float2 s_ml[kRows];  // references and sums of the second warpgroup's rows
+  __shared__ uint8_t s_ex[C::kUnitRows];  // e4m3: the exponent that a q row was scaled by
   __shared__ int s_scan[kThreads / 32], s_b, s_off, s_abort;
   __shared__ uint32_t s_tmem;
 
@@ -278,9 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bar_s[i]), 1);
       mbar_init(smem_u32(&bar_p[i]), kRows);
       mbar_init(smem_u32(&bar_o[i]), 1);
-      mbar_init(smem_u32(&bar_q[i]), kRows);
-      mbar_init(smem_u32(&bar_o_free[i]), kRows);
     }
+    mbar_init(smem_u32(&bar_q), 2 * kRows);
+    mbar_init(smem_u32(&bar_done), 2 * kRows);
     mbar_init(smem_u32(&bar_ml), kRows);
     mbar_init(smem_u32(&bar_drain), 1);
     fence_mbar_init();
@@ -447,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool there = seen && pg >= 0;
           const uint32_t sent = __ballot_sync(kAll, there);
           if (it >= S) {
-            ok = warp_wait(smem_u32(&bar_k_empty[st]), slot.odd ^ 1, abort_flag, p.dev_status);
+            ok = wait_for(smem_u32(&bar_k_empty[st]), slot.odd ^ 1, abort_flag);
             if (!ok) break;
           }
           const uint32_t bytes = __popc(sent) * piece * C::kRowBytes;
@@ -491,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           bool v_ok = true;
           if (it >= S)
-            v_ok = warp_wait(smem_u32(&bar_v_empty[st]), slot.odd ^ 1, abort_flag, p.dev_status);
+            v_ok = wait_for(smem_u32(&bar_v_empty[st]), slot.odd ^ 1, abort_flag);
           if (v_ok && there) {
 #pragma unroll
             for (int pn = 0; pn < C::kPanels; ++pn)
@@ -547,8 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Ring<S> kslot, vslot;   // of the next tile whose S, whose P V is issued
       uint32_t wide_at = 0;   // e4m3: its widened V
-      uint32_t odd_p[2] = {0, 0}, odd_q[2] = {0, 0}, odd_o = 0;  // parities of the phases waited for next
-      bool first = true;      // part
+      uint32_t odd_p[2] = {0, 0}, odd_q = 0;  // parities of the phases waited for next
       bool ok = true;
       while (ok && left > 0) {
         int g, rt, x0, x1;
@@ -560,14 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto step = [&](auto which, int i) -> bool {
           constexpr int w = decltype(which)::value;
           if (i >= 2 && i < J + 2) {
-            if (!warp_wait(smem_u32(&bar_ready[vslot.at]), vslot.odd, abort_flag, p.dev_status) ||
-                !warp_wait(smem_u32(&bar_p[w]), odd_p[w], abort_flag, p.dev_status))
+            if (!wait_for(smem_u32(&bar_ready[vslot.at]), vslot.odd, abort_flag) ||
+                !wait_for(smem_u32(&bar_p[w]), odd_p[w], abort_flag))
               return false;
             odd_p[w] ^= 1;
-            // the sums of the part before have been read
-            if (i < 4 && !first &&
-                !warp_wait(smem_u32(&bar_o_free[w]), odd_o, abort_flag, p.dev_status))
-              return false;
             tc_fence_after();
             issue_o(w, F8 ? wide + wide_at * C::kWideBytes : sV(vslot.at), i >= 4);
             if (alt || w == 1) {
@@ -579,11 +602,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (i < J) {
             const int tile = alt ? 0 : w;
-            if (i < 2 && (!alt || w == 0)) {
-              if (!warp_wait(smem_u32(&bar_q[w]), odd_q[w], abort_flag, p.dev_status)) return false;
-              odd_q[w] ^= 1;
+            if (w == 0 && i == 0) {  // the sums of the part before have been read, too
+              if (!wait_for(smem_u32(&bar_q), odd_q, abort_flag)) return false;
+              odd_q ^= 1;
             }
-            if (!warp_wait(smem_u32(&bar_k[kslot.at]), kslot.odd, abort_flag, p.dev_status))
+            if (!wait_for(smem_u32(&bar_k[kslot.at]), kslot.odd, abort_flag))
               return false;
             tc_fence_after();
             issue_s(w, tile, kslot.at);
@@ -597,8 +620,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (int i = 0; ok && i < J + 2; i += 2)
           ok = step(std::integral_constant<int, 0>(), i) && step(std::integral_constant<int, 1>(), i + 1);
-        if (!first) odd_o ^= 1;
-        first = false;
       }
       // Every product is complete before TMEM is freed.
       mma_commit_elect(smem_u32(&bar_drain), e);
@@ -632,10 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = x0; x < x1; ++x, ++it, slot.next(), mslot.next()) {
           const int st = slot.at, key0 = first_key(x);
           // (K's barrier may be a tile's phase further; V's slot waits for this warp)
-          ok = warp_wait(smem_u32(&bar_v[st]), slot.odd, abort_flag, p.dev_status);
+          ok = wait_for(smem_u32(&bar_v[st]), slot.odd, abort_flag);
           if (F8 && ok && it >= 2)
-            ok = warp_wait(smem_u32(&bar_wide_empty[it & 1]), ((it >> 1) - 1) & 1, abort_flag,
-                           p.dev_status);
+            ok = wait_for(smem_u32(&bar_wide_empty[it & 1]), ((it >> 1) - 1) & 1, abort_flag);
           if (!ok) break;
           const uint32_t okp = s_meta[mslot.at].ok;
           // all of the tile's keys are seen by some token
@@ -707,8 +727,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t S_row = tmem + w * 128 + lane_off;
     Ring<C::kMeta> mslot;  // of the part's next tile
-    // parities of the phases waited for next: own scores, own sums, the other's sums, its statistics
-    uint32_t odd_s = 0, odd_o = 0, odd_other = 0, odd_ml = 0;
+    // parities of the phases waited for next: own scores, own sums, the other's sums, its statistics,
+    // q tiles, the part before
+    uint32_t odd_s = 0, odd_o = 0, odd_other = 0, odd_ml = 0, odd_q = 0, odd_done = 0;
+    bool first = true;  // part
     bool ok = true;
     while (ok && left > 0) {
       int g, rt, x0, x1;
@@ -729,60 +751,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (in) mask = p.mask[r.q0 + tok] & (r.n >= 64 ? ~0ull : (1ull << r.n) - 1);
       const int pos = base + max(__popcll(mask) - 1, 0);
       mask &= present(r.n, base);
-      float fac = p.scale_log2;
-      // ---- q
+      // ---- q tiles, by both warpgroups: D / 16 lanes to a row, 16 values each
       {
-        const uint16_t* src = p.q + ((int64_t)(r.q0 + tok) * p.hq + head) * D;
-        const bool mine = w == 0 || !alt;  // this warpgroup writes the tile
-        const uint32_t to = sq + (alt ? 0 : w) * C::kQBytes;
-        uint4 v[D / 8];
+        constexpr int kLanes = D / 16, kPass = 8 * 32 / kLanes, kPasses = kRows / kPass;
+        const int c = lane % kLanes;
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += kRows) {
+          const uint32_t to = sq + (r0 ? C::kQBytes : 0);
+          uint4 v[kPasses][2];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          v[i] = in ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
-        if constexpr (F8) {
-          uint32_t top = 0;  // largest |q| of the row, as bf16 bits
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint32_t m[4] = {v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu, v[i].z & 0x7FFF7FFFu,
-                                   v[i].w & 0x7FFF7FFFu};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) top = max(top, max(m[k] & 0xFFFFu, m[k] >> 16));
-          }
-          const int ex = max((int)(top >> 7), 27);  // biased exponent; q' = q 2^(7 - e) < 2^8
-          const float up = __uint_as_float((uint32_t)(261 - ex < 1 ? 1 : 261 - ex) << 23);
-          fac *= __uint_as_float((uint32_t)(ex < 8 ? 1 : ex - 7) << 23);
-          if (mine) {
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {  // 16 values: a chunk of each half
-              uint32_t hi[4], lo[4];
-              const uint32_t u[8] = {v[2 * c].x,     v[2 * c].y,     v[2 * c].z,     v[2 * c].w,
-                                     v[2 * c + 1].x, v[2 * c + 1].y, v[2 * c + 1].z, v[2 * c + 1].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                hi[k] = lo[k] = 0;
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const float a = __uint_as_float(u[2 * k + z] << 16) * up,
-                              c2 = __uint_as_float(u[2 * k + z] & 0xFFFF0000u) * up;
-                  const uint32_t h2 = cvt_e4m3x2(a, c2);
-                  const float2 back = e4m3x2_to_float2((uint16_t)h2);
-                  hi[k] |= h2 << (16 * z);
-                  lo[k] |= cvt_e4m3x2(a - back.x, c2 - back.y) << (16 * z);
-                }
-              }
-              const uint32_t dst = chunk_at<PB>(to, kRows, lane_row, c);
-              sts128(dst, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-              sts128(dst + kRows * PB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          for (int k = 0; k < kPasses; ++k) {
+            const int row_k = r0 + k * kPass + (warp - 4) * (32 / kLanes) + lane / kLanes;
+            v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+            if (row_k < rows) {
+              const int rr_k = rt * C::kUnitRows + row_k, tok_k = rr_k / p.group;
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  p.q + ((int64_t)(r.q0 + tok_k) * p.hq + g * p.group + (rr_k - tok_k * p.group)) * D + c * 16);
+              v[k][0] = src[0];
+              v[k][1] = src[1];
             }
           }
-        } else if (mine) {
+          // both warpgroups are done with the part before: its products have read the q tiles
+          if (r0 == 0 && !first) {
+            ok = wait_for(smem_u32(&bar_done), odd_done, abort_flag);
+            odd_done ^= 1;
+          }
+          if (!ok) break;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) sts128(chunk_at<PB>(to, kRows, lane_row, c), v[c]);
+          for (int k = 0; k < kPasses; ++k) {
+            const int base_k = r0 + k * kPass + (warp - 4) * (32 / kLanes);
+            if (base_k >= rows) continue;  // the same for the warp; such rows are not looked at
+            const int row_k = base_k + lane / kLanes - r0;
+            if constexpr (F8) {
+              const uint32_t u[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                                     v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+              uint32_t top = 0;  // largest |q| of the row, as bf16 bits
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t m = u[i] & 0x7FFF7FFFu;
+                top = max(top, max(m & 0xFFFFu, m >> 16));
+              }
+#pragma unroll
+              for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
+              const int ex = max((int)(top >> 7), 27);  // biased exponent; q' = q 2^(7 - e) < 2^8
+              const float up = __uint_as_float((uint32_t)(261 - ex < 1 ? 1 : 261 - ex) << 23);
+              if (c == 0) s_ex[r0 + row_k] = (uint8_t)ex;
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float a = __uint_as_float(u[i] << 16) * up,
+                            b2 = __uint_as_float(u[i] & 0xFFFF0000u) * up;
+                const uint32_t h = cvt_e4m3x2(a, b2);
+                const float2 back = e4m3x2_to_float2((uint16_t)h);
+                const uint32_t low = cvt_e4m3x2(a - back.x, b2 - back.y);
+                hi[i / 2] = i & 1 ? hi[i / 2] | h << 16 : h;
+                lo[i / 2] = i & 1 ? lo[i / 2] | low << 16 : low;
+              }
+              const uint32_t dst = chunk_at<PB>(to, kRows, row_k, c);
+              sts128(dst, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+              sts128(dst + kRows * PB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+            } else {
+              sts128(chunk_at<PB>(to, kRows, row_k, 2 * c), v[k][0]);
+              sts128(chunk_at<PB>(to, kRows, row_k, 2 * c + 1), v[k][1]);
+            }
+          }
         }
-        if (mine) {
-          fence_proxy_async_smem();
-          mbar_arrive(smem_u32(&bar_q[alt ? 0 : w]));
-        }
+        first = false;
+        if (!ok) break;
+        fence_proxy_async_smem();
+        mbar_arrive(smem_u32(&bar_q));
+        if constexpr (F8) ok = wait_for(smem_u32(&bar_q), odd_q, abort_flag);  // the rows' exponents
+        odd_q ^= 1;
+        if (!ok) break;
+      }
+      float fac = p.scale_log2;
+      if constexpr (F8) {
+        const int ex = in ? s_ex[row] : 127;
+        fac *= __uint_as_float((uint32_t)(ex < 8 ? 1 : ex - 7) << 23);
       }
       // every row sees the keys of a tile in front of `base` and, with a window, from clear_lo on (or
       // among the first ones)
@@ -790,8 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < T; ++j, mslot.next()) {  // tile of the part
         if (alt && (j & 1) != w) continue;
-        ok = warp_wait(smem_u32(&bar_meta[mslot.at]), mslot.odd, abort_flag, p.dev_status) &&
-             warp_wait(smem_u32(&bar_s[w]), odd_s, abort_flag, p.dev_status);
+        ok = wait_for(smem_u32(&bar_meta[mslot.at]), mslot.odd, abort_flag) &&
+             wait_for(smem_u32(&bar_s[w]), odd_s, abort_flag);
         if (!ok) break;
         odd_s ^= 1;
         tc_fence_after();
@@ -910,28 +955,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the unit's part ends
-      // No second warpgroup's statistics without a tile of its own: only a tile's scores tell it that
-      // the first one has read those of the part before.
+      // The second warpgroup's statistics go through two columns behind its last weights, on the same
+      // lanes.
       const bool other = alt && T > 1;
       if (alt && w == 1) {
         if (other) {
-          s_ml[lane_row] = make_float2(m_ref, l);
+          tmem_st2(S_row + 126, __float_as_uint(m_ref), __float_as_uint(l));
+          tmem_st_wait();
+          tc_fence_before();
           mbar_arrive(smem_u32(&bar_ml));
           odd_o ^= 1;  // the first warpgroup waits for the sums
         }
       } else {
         float m1 = -INFINITY, l1 = 0.f;
         if (other) {
-          ok = warp_wait(smem_u32(&bar_ml), odd_ml, abort_flag, p.dev_status);
+          ok = wait_for(smem_u32(&bar_ml), odd_ml, abort_flag);
           if (!ok) break;
           odd_ml ^= 1;
-          const float2 ml = s_ml[lane_row];
-          m1 = ml.x;
-          l1 = ml.y;
+          tc_fence_after();
+          uint32_t a, b2;
+          tmem_ld2(tmem + 128 + lane_off + 126, a, b2);
+          tmem_ld_wait();
+          m1 = __uint_as_float(a);
+          l1 = __uint_as_float(b2);
         }
-        ok = warp_wait(smem_u32(&bar_o[w]), odd_o, abort_flag, p.dev_status);
+        ok = wait_for(smem_u32(&bar_o[w]), odd_o, abort_flag);
         odd_o ^= 1;
-        if (ok && other) ok = warp_wait(smem_u32(&bar_o[1]), odd_other, abort_flag, p.dev_status);
+        if (ok && other) ok = wait_for(smem_u32(&bar_o[1]), odd_other, abort_flag);
         if (other || !alt) odd_other ^= 1;  // the second warpgroup had sums
         if (!ok) break;
         tc_fence_after();
@@ -985,8 +1035,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.lse[at] = sum > 0.f ? (top - kBias + log2f(sum)) * kLn2 : -INFINITY;
         }
         tc_fence_before();
-        mbar_arrive(smem_u32(&bar_o_free[w]));
-        if (alt) mbar_arrive(smem_u32(&bar_o_free[1]));
         if (!whole_l && whole_r && tid == 128) {
           // the unit ends here: tell the second launch where it began
           const int begin = before - x0;  // list place of the unit's first tile
@@ -998,10 +1046,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.job_q0[blockIdx.x] = r.q0;
         }
       }
+      mbar_arrive(smem_u32(&bar_done));
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort_flag && p.dev_status != nullptr) atomicOr(p.dev_status, kDevTimeout);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
