@@ -59,7 +59,7 @@ struct Cfg {
   static constexpr int kRowBytes = D * (F8 ? 1 : 2);
   static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;  // one swizzled row
   static constexpr int kPanels = kRowBytes / kPanelBytes;
-  static constexpr int kTK = kRowBytes == 256 ? 64 : 128;  // keys per tile
+  static constexpr int kTK = 128;                    // keys per tile
   static constexpr int kTileBytes = kTK * kRowBytes;       // K (or V) of one tile
   static constexpr int kQTiles = kTwo ? 2 : 1;
   // e4m3: the hi and the lo half one after the other, each kRows rows of one panel
@@ -75,7 +75,7 @@ struct Cfg {
       1024 + kQTiles * kQBytes + kWides * kWideBytes + kStages * 2 * kTileBytes;
   static constexpr int kPieces = F8 ? kTK / 16 : 1;
   static constexpr int kUnitRows = kQTiles * kRows;
-  static_assert(kStages >= 3, "ring");
+  static_assert(kStages >= 2, "ring");
 };
 
 // Registers move from the warps that issue to the softmax warps, which hold a tile's scores: 128 x
@@ -178,10 +178,18 @@ __device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t& a, uint32_t& 
 
 template <int kP>
 struct Meta {  // of a tile, written by the producer
-  uint32_t ok;   // bit i: piece i (a page, or the tile if pages are larger) is there
-  float ks[kP];  // scale of its keys
-  float vl[kP];  // log2 of the scale of its values
-  float vi[kP];  // 1 / that scale
+  float4 scale[kP];  // of a piece (a page, or the tile if pages are larger): its keys', log2 of its
+                     // values', 1 / its values'
+  int key0;          // first key
+  uint32_t ok;       // bit i: piece i is there
+  int clear;         // every row sees all of its keys
+};
+struct Part {  // tiles of one unit in a CTA's run, as the producer describes them
+  int T;                 // tiles (0: the run is over)
+  int q0, n, base;       // the request's first q row, its new tokens, its other keys
+  int g, row0, rows;     // KV head, first row within the request, rows
+  int whole_l, whole_r;  // the unit's first, its last tile are among them
+  int c0;                // CTA that the unit began in, where it ends here
 };
 
 struct Params {
@@ -269,14 +277,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<F8, D, kTwo>;
   constexpr int TK = C::kTK, S = C::kStages, PB = C::kPanelBytes;
   extern __shared__ uint8_t smem_raw[];
-  // K and V landed; K's last product done; V ready for its product (widened, or cleared); V's slot
-  // (e4m3: the codes') free; the tile's scales written; e4m3: a widened V's last product done; a
-  // warpgroup's scores, weights and sums; the q tiles written; the warpgroups done with a part (its
-  // sums read, its products complete); the second warpgroup's statistics
-  __shared__ __align__(8) uint64_t bar_k[S], bar_v[S], bar_k_empty[S], bar_v_empty[S],
-      bar_ready[S], bar_meta[C::kMeta], bar_wide_empty[2], bar_s[2], bar_p[2], bar_o[2], bar_q, bar_done,
-      bar_ml, bar_drain;
-  __shared__ Meta<C::kPieces> s_meta[C::kMeta];
+  // Of a part: described, its description read. Of a tile: K and V landed; its K's products done; V
+  // ready for its product (widened, or cleared); V's slot (e4m3: the codes') free; its scales
+  // written; e4m3: a widened V's last product done. Of a warpgroup: scores, weights, sums. Of a part:
+  // q tiles written; both warpgroups done with it (its sums read, its products complete); the second
+  // warpgroup's statistics.
+  __shared__ __align__(8) uint64_t bar_part[2], bar_part_empty[2], bar_k[S], bar_v[S],
+      bar_k_empty[S], bar_v_empty[S], bar_ready[S], bar_meta[C::kMeta], bar_wide_empty[2], bar_s[2],
+      bar_p[2], bar_o[2], bar_q, bar_done, bar_ml, bar_drain;
+  __shared__ __align__(16) Meta<C::kPieces> s_meta[C::kMeta];
+  __shared__ Part s_part[2];
   __shared__ uint8_t s_ex[C::kUnitRows];  // e4m3: the exponent that a q row was scaled by
   __shared__ int s_scan[kThreads / 32], s_b, s_off, s_abort;
   __shared__ uint32_t s_tmem;
@@ -302,6 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < C::kMeta; ++i) mbar_init(smem_u32(&bar_meta[i]), 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bar_part[i]), 1);
+      mbar_init(smem_u32(&bar_part_empty[i]), kThreads / 32 - 1);  // every warp but the producer
       mbar_init(smem_u32(&bar_wide_empty[i]), 1);
       mbar_init(smem_u32(&bar_s[i]), 1);
       mbar_init(smem_u32(&bar_p[i]), kRows);
@@ -400,47 +412,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
     return;
   }
-  Req r = load_req<TK>(p, b, &bad);
-
-  int left = t1 - t0;
-  int seg_g = -1, seg_rt = 0;
-  // The next unit's part in this run: head, row block, tiles [x0, x1) of nt. Every role walks the
-  // run for itself.
-  auto next_seg = [&](int& g, int& rt, int& x0, int& x1) -> bool {
-    if (seg_g < 0) {  // the run's first unit, perhaps from its middle
-      const int u = (int)((unsigned)off / (unsigned)(r.nt + kEndTiles));
-      x0 = off - u * (r.nt + kEndTiles);
-      seg_g = (int)((unsigned)u / (unsigned)r.rt);
-      seg_rt = u - seg_g * r.rt;
-    } else {
-      x0 = 0;
-      if (++seg_rt == r.rt) {
-        seg_rt = 0;
-        if (++seg_g == p.hkv) {
-          seg_g = 0;
-          do r = load_req<TK>(p, ++b, &bad);  // requests without new tokens have no units
-          while (r.rt == 0);
-        }
-      }
-    }
-    g = seg_g;
-    rt = seg_rt;
-    x1 = min(r.nt, x0 + left);
-    left -= min(r.nt + kEndTiles - x0, left);
-    return x0 < x1;  // else the run begins behind the unit's last tile
-  };
-  auto rows_of_unit = [&](int rt) -> int { return min(r.n * p.group - rt * C::kUnitRows, C::kUnitRows); };
-  auto first_key = [&](int x) -> int { return (x < r.st ? x : r.lt + x - r.st) * TK; };
   const int piece = p.page_size < TK ? p.page_size : TK;  // keys per TMA box
   const int n_pieces = TK / piece;
   const int piece_shift = 31 - __clz(piece >> 4);  // 16 keys -> piece
+  // The next part of the run, as the producer describes it to the other warps; false: there is none.
+  Ring<2> pslot;
+  auto next_part = [&](Part& q) -> bool {
+    if (!wait_for(smem_u32(&bar_part[pslot.at]), pslot.odd, abort_flag)) return false;
+    q = s_part[pslot.at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar_part_empty[pslot.at]));
+    pslot.next();
+    return q.T > 0;
+  };
 
   if (warp < 4) {
     give_registers<kIssueRegs>();
     if (warp == 0) {
       // ------------------------------------------------------------------ producer
-      // Lane i keeps page cache_at + i of the request (and what the others need of its scales for
-      // head cache_g) in registers, loaded 32 pages at a time.
+      // Walks the run. Lane i keeps page cache_at + i of the request (and what the others need of its
+      // scales for head cache_g) in registers, loaded 32 pages at a time.
+      Req r = load_req<TK>(p, b, &bad);
+      int left = t1 - t0, parts = 0;
+      int g, rt, x0;
+      {  // the run's first unit, perhaps from its middle
+        const int u = (int)((unsigned)off / (unsigned)(r.nt + kEndTiles));
+        x0 = off - u * (r.nt + kEndTiles);
+        g = (int)((unsigned)u / (unsigned)r.rt);
+        rt = u - g * r.rt;
+      }
       int it = 0;
       Ring<S> slot;
       Ring<C::kMeta> mslot;
@@ -448,11 +448,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool fine = true;                    // the page's scales are in range
       float ks = 1.f, vl = 0.f, vi = 1.f;  // key scale, log2 and inverse of the value scale
       bool ok = true;
+      auto describe = [&](const Part& q) -> bool {
+        if (parts >= 2 && !wait_for(smem_u32(&bar_part_empty[pslot.at]), pslot.odd ^ 1, abort_flag))
+          return false;
+        if (lane == 0) {
+          s_part[pslot.at] = q;
+          mbar_arrive(smem_u32(&bar_part[pslot.at]));
+        }
+        __syncwarp();
+        pslot.next();
+        ++parts;
+        return true;
+      };
       while (ok && left > 0) {
-        int g, rt, x0, x1;
-        if (!next_seg(g, rt, x0, x1)) continue;
-        for (int x = x0; x < x1; ++x, ++it, slot.next(), mslot.next()) {
-          const int key0 = first_key(x), st = slot.at;
+        const int before = t1 - left, x1 = min(r.nt, x0 + left);
+        left -= min(r.nt + kEndTiles - x0, left);
+        const int base = r.L - r.n;
+        if (x0 < x1) {  // else the run begins behind the unit's last tile
+          Part q;
+          q.T = x1 - x0;
+          q.q0 = r.q0;
+          q.n = r.n;
+          q.base = base;
+          q.g = g;
+          q.row0 = rt * C::kUnitRows;
+          q.rows = min(r.n * p.group - q.row0, C::kUnitRows);
+          q.whole_l = x0 == 0;
+          q.whole_r = x1 == r.nt;
+          q.c0 = 0;
+          if (!q.whole_l && q.whole_r) {  // the unit ends here: where it began
+            const int begin = before - x0;        // list place of the unit's first tile
+            const int longer = more * (len + 1);  // tiles of the runs with one more
+            q.c0 = begin < longer ? (int)((unsigned)begin / (unsigned)(len + 1))
+                                  : more + (int)((unsigned)(begin - longer) / (unsigned)len);
+          }
+          ok = describe(q);
+        }
+        // every row sees the keys of a tile in front of `base` and, with a window, from clear_lo on (or
+        // among the first ones)
+        const int clear_lo = p.window > 0 ? base + r.n - p.window : 0;
+        for (int x = x0; ok && x < x1; ++x, ++it, slot.next(), mslot.next()) {
+          const int key0 = (x < r.st ? x : r.lt + x - r.st) * TK, st = slot.at;
           const int pg0 = key0 >> p.page_shift;
           if (cache_b != b || pg0 < cache_at || pg0 + n_pieces > cache_at + 32) {
             cache_b = b;
@@ -504,22 +540,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             use = __ballot_sync(kAll, good);
             const float k_of = __shfl_sync(kAll, ks, at), l_of = __shfl_sync(kAll, vl, at),
                         i_of = __shfl_sync(kAll, vi, at);
-            if (lane < n_pieces) {  // pieces that are not used stay neutral
-              meta.ks[lane] = good ? k_of : 1.f;
-              meta.vl[lane] = good ? l_of : 0.f;
-              meta.vi[lane] = good ? i_of : 0.f;
-            }
+            if (lane < n_pieces)  // pieces that are not used stay neutral
+              meta.scale[lane] = good ? make_float4(k_of, l_of, i_of, 0.f) : make_float4(1.f, 0.f, 0.f, 0.f);
           }
           if (flag && p.dev_status != nullptr) atomicOr(p.dev_status, flag);
-          if (lane == 0) meta.ok = use;
+          if (lane == 0) {
+            meta.key0 = key0;
+            meta.ok = use;
+            meta.clear = use == (1u << n_pieces) - 1u && key0 + TK <= base &&
+                         (p.window == 0 || key0 >= clear_lo || key0 + TK <= p.sinks);
+          }
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(smem_u32(&bar_meta[mslot.at]));
             mbar_arrive_expect_tx(smem_u32(&bar_k[st]), bytes);
           }
           bool v_ok = true;
-          if (it >= S)
-            v_ok = wait_for(smem_u32(&bar_v_empty[st]), slot.odd ^ 1, abort_flag);
+          if (it >= S) v_ok = wait_for(smem_u32(&bar_v_empty[st]), slot.odd ^ 1, abort_flag);
           if (v_ok && there) {
 #pragma unroll
             for (int pn = 0; pn < C::kPanels; ++pn)
@@ -534,7 +571,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
         }
+        x0 = 0;
+        if (left > 0 && ++rt == r.rt) {
+          rt = 0;
+          if (++g == p.hkv) {
+            g = 0;
+            do r = load_req<TK>(p, ++b, &bad);  // requests without new tokens have no units
+            while (r.rt == 0);
+          }
+        }
       }
+      Part none;
+      none.T = 0;
+      if (ok) describe(none);
       // Copies in flight must land before the CTA can exit, also when a wait ran out.
       for (int i = it > S ? it - S : 0; i < it; ++i) {
         mbar_wait(smem_u32(&bar_k[i % S]), (i / S) & 1, nullptr, nullptr);
@@ -576,45 +625,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<S> kslot, vslot;   // of the next tile whose S, whose P V is issued
       uint32_t wide_at = 0;   // e4m3: its widened V
       uint32_t odd_p[2] = {0, 0}, odd_q = 0;  // parities of the phases waited for next
+      Part q;
       bool ok = true;
-      while (ok && left > 0) {
-        int g, rt, x0, x1;
-        if (!next_seg(g, rt, x0, x1)) continue;
-        const bool alt = !kTwo || rows_of_unit(rt) <= kRows;
-        const int J = alt ? x1 - x0 : 2 * (x1 - x0);
+      while (ok && next_part(q)) {
+        const bool alt = !kTwo || q.rows <= kRows;
+        const int J = alt ? q.T : 2 * q.T;
+        // the q tiles are written, and the sums of the part before have been read
+        ok = wait_for(smem_u32(&bar_q), odd_q, abort_flag);
+        odd_q ^= 1;
         // Job i: warpgroup i % 2, and tile i, or i / 2 where each warpgroup takes every tile. The product
         // of job i - 2's weights comes in front of job i's scores, which overwrite them.
         auto step = [&](auto which, int i) -> bool {
           constexpr int w = decltype(which)::value;
-          if (i >= 2 && i < J + 2) {
-            if (!wait_for(smem_u32(&bar_ready[vslot.at]), vslot.odd, abort_flag) ||
-                !wait_for(smem_u32(&bar_p[w]), odd_p[w], abort_flag))
+          const bool pv = i >= 2 && i < J + 2, qk = i < J;
+          // everything the step needs is looked at together: a look takes as long as an issue
+          bool there = true;
+          if (pv)
+            there = mbar_peek(smem_u32(&bar_ready[vslot.at]), vslot.odd) &
+                    mbar_peek(smem_u32(&bar_p[w]), odd_p[w]);
+          if (qk) there &= mbar_peek(smem_u32(&bar_k[kslot.at]), kslot.odd);
+          if (!__all_sync(kAll, there)) {
+            if (pv && (!wait_for(smem_u32(&bar_ready[vslot.at]), vslot.odd, abort_flag) ||
+                       !wait_for(smem_u32(&bar_p[w]), odd_p[w], abort_flag)))
               return false;
+            if (qk && !wait_for(smem_u32(&bar_k[kslot.at]), kslot.odd, abort_flag)) return false;
+          }
+          tc_fence_after();
+          if (pv) {
             odd_p[w] ^= 1;
-            tc_fence_after();
             issue_o(w, F8 ? wide + wide_at * C::kWideBytes : sV(vslot.at), i >= 4);
+            if (F8 && (alt || w == 1)) mma_commit_elect(smem_u32(&bar_wide_empty[wide_at]), e);
+          }
+          if (qk) {
+            issue_s(w, alt ? 0 : w, kslot.at);
+            mma_commit_elect(smem_u32(&bar_s[w]), e);  // its reader hands K's slot back
+            if (alt || w == 1) kslot.next();
+          }
+          if (pv) {
             if (alt || w == 1) {
-              mma_commit_elect(smem_u32(F8 ? &bar_wide_empty[wide_at] : &bar_v_empty[vslot.at]), e);
+              if (!F8) mma_commit_elect(smem_u32(&bar_v_empty[vslot.at]), e);
               vslot.next();
               wide_at ^= 1;
             }
             if (i >= J) mma_commit_elect(smem_u32(&bar_o[w]), e);
-          }
-          if (i < J) {
-            const int tile = alt ? 0 : w;
-            if (w == 0 && i == 0) {  // the sums of the part before have been read, too
-              if (!wait_for(smem_u32(&bar_q), odd_q, abort_flag)) return false;
-              odd_q ^= 1;
-            }
-            if (!wait_for(smem_u32(&bar_k[kslot.at]), kslot.odd, abort_flag))
-              return false;
-            tc_fence_after();
-            issue_s(w, tile, kslot.at);
-            mma_commit_elect(smem_u32(&bar_s[w]), e);
-            if (alt || w == 1) {
-              mma_commit_elect(smem_u32(&bar_k_empty[kslot.at]), e);
-              kslot.next();
-            }
           }
           return true;
         };
@@ -629,43 +682,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = 0;
       Ring<S> slot;
       Ring<C::kMeta> mslot;
+      Part q;
       bool ok = true;
-      while (ok && left > 0) {
-        int g, rt, x0, x1;
-        if (!next_seg(g, rt, x0, x1)) continue;
+      while (ok && next_part(q)) {
         // new tokens that some token sees, and the first key of the windows
-        const int base = r.L - r.n;
-        const uint64_t here = present(r.n, base);
+        const uint64_t here = present(q.n, q.base);
         uint64_t any = 0;
         int least = 64;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          if (lane + 32 * k < r.n) {
-            const uint64_t m = p.mask[r.q0 + lane + 32 * k];
+          if (lane + 32 * k < q.n) {
+            const uint64_t m = p.mask[q.q0 + lane + 32 * k];
             any |= m;
-            least = min(least, max(__popcll(m & (r.n >= 64 ? ~0ull : (1ull << r.n) - 1)) - 1, 0));
+            least = min(least, max(__popcll(m & (q.n >= 64 ? ~0ull : (1ull << q.n) - 1)) - 1, 0));
           }
         any = here & ((uint64_t)__reduce_or_sync(kAll, (uint32_t)any) |
                       (uint64_t)__reduce_or_sync(kAll, (uint32_t)(any >> 32)) << 32);
         least = __reduce_min_sync(kAll, least);
-        const int lo = p.window > 0 ? max(base + least + 1 - p.window, 0) : 0;
+        const int lo = p.window > 0 ? max(q.base + least + 1 - p.window, 0) : 0;
         const int kept = min(p.sinks, lo);
-        for (int x = x0; x < x1; ++x, ++it, slot.next(), mslot.next()) {
-          const int st = slot.at, key0 = first_key(x);
+        for (int x = 0; x < q.T; ++x, ++it, slot.next(), mslot.next()) {
+          const int st = slot.at;
           // (K's barrier may be a tile's phase further; V's slot waits for this warp)
           ok = wait_for(smem_u32(&bar_v[st]), slot.odd, abort_flag);
           if (F8 && ok && it >= 2)
             ok = wait_for(smem_u32(&bar_wide_empty[it & 1]), ((it >> 1) - 1) & 1, abort_flag);
           if (!ok) break;
           const uint32_t okp = s_meta[mslot.at].ok;
-          // all of the tile's keys are seen by some token
-          const bool all = okp == (1u << n_pieces) - 1u && key0 + TK <= base &&
-                           (key0 >= lo || key0 + TK <= kept);
-          auto row_seen = [&](int row) -> bool {
+          const int key0 = s_meta[mslot.at].key0;
+          const bool all = s_meta[mslot.at].clear;
+          auto row_seen = [&](int row) -> bool {  // by some token
             const int key = key0 + row;
             if (!((okp >> ((row >> 4) >> piece_shift)) & 1u)) return false;
-            if (key < base) return key >= lo || key < kept;
-            return key - base < 64 && ((any >> (key - base)) & 1u);
+            if (key < q.base) return key >= lo || key < kept;
+            return key - q.base < 64 && ((any >> (key - q.base)) & 1u);
           };
           if constexpr (F8) {
             const uint32_t from = sV(st), to = wide + (it & 1) * C::kWideBytes;
@@ -691,14 +741,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
 #pragma unroll
               for (int k = 0; k < kDeep; ++k) {
-                const uint32_t x[4] = {odd ? v[k].z : v[k].x, odd ? v[k].w : v[k].y,
-                                       odd ? v[k].x : v[k].z, odd ? v[k].y : v[k].w};
+                const uint32_t x4[4] = {odd ? v[k].z : v[k].x, odd ? v[k].w : v[k].y,
+                                        odd ? v[k].x : v[k].z, odd ? v[k].y : v[k].w};
                 sts128(dst0 + (k0 + k) * kStep * 128,
-                       make_uint4(e4m3_half(x[0], 0), e4m3_half(x[0], 1), e4m3_half(x[1], 0),
-                                  e4m3_half(x[1], 1)));
+                       make_uint4(e4m3_half(x4[0], 0), e4m3_half(x4[0], 1), e4m3_half(x4[1], 0),
+                                  e4m3_half(x4[1], 1)));
                 sts128(dst1 + (k0 + k) * kStep * 128,
-                       make_uint4(e4m3_half(x[2], 0), e4m3_half(x[2], 1), e4m3_half(x[3], 0),
-                                  e4m3_half(x[3], 1)));
+                       make_uint4(e4m3_half(x4[2], 0), e4m3_half(x4[2], 1), e4m3_half(x4[3], 0),
+                                  e4m3_half(x4[3], 1)));
               }
             }
             fence_proxy_async_smem();
@@ -726,47 +776,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane_row = ((warp & 3) << 5) + lane;  // TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t S_row = tmem + w * 128 + lane_off;
-    Ring<C::kMeta> mslot;  // of the part's next tile
+    Ring<S> kslot;         // of the part's next tile
+    Ring<C::kMeta> mslot;
     // parities of the phases waited for next: own scores, own sums, the other's sums, its statistics,
     // q tiles, the part before
     uint32_t odd_s = 0, odd_o = 0, odd_other = 0, odd_ml = 0, odd_q = 0, odd_done = 0;
     bool first = true;  // part
+    Part q;
     bool ok = true;
-    while (ok && left > 0) {
-      int g, rt, x0, x1;
-      const int before = t1 - left;
-      if (!next_seg(g, rt, x0, x1)) continue;
-      const int rows = rows_of_unit(rt);
-      const bool alt = !kTwo || rows <= kRows;
-      const int T = x1 - x0;
-      const bool whole_l = x0 == 0, whole_r = x1 == r.nt;
-      // this thread's q row: token, head, position, mask
-      const int row = lane_row + (alt ? 0 : w * kRows);
-      const bool in = row < rows;
-      const int rr = rt * C::kUnitRows + row;
-      const int tok = in ? rr / p.group : 0;
-      const int head = in ? g * p.group + (rr - tok * p.group) : 0;
-      const int base = r.L - r.n;
-      uint64_t mask = 0;
-      if (in) mask = p.mask[r.q0 + tok] & (r.n >= 64 ? ~0ull : (1ull << r.n) - 1);
-      const int pos = base + max(__popcll(mask) - 1, 0);
-      mask &= present(r.n, base);
+    while (ok && next_part(q)) {
+      const bool alt = !kTwo || q.rows <= kRows;
       // ---- q tiles, by both warpgroups: D / 16 lanes to a row, 16 values each
       {
         constexpr int kLanes = D / 16, kPass = 8 * 32 / kLanes, kPasses = kRows / kPass;
         const int c = lane % kLanes;
 #pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += kRows) {
+        for (int r0 = 0; r0 < q.rows; r0 += kRows) {
           const uint32_t to = sq + (r0 ? C::kQBytes : 0);
           uint4 v[kPasses][2];
 #pragma unroll
           for (int k = 0; k < kPasses; ++k) {
             const int row_k = r0 + k * kPass + (warp - 4) * (32 / kLanes) + lane / kLanes;
             v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
-            if (row_k < rows) {
-              const int rr_k = rt * C::kUnitRows + row_k, tok_k = rr_k / p.group;
+            if (row_k < q.rows) {
+              const int rr_k = q.row0 + row_k, tok_k = rr_k / p.group;
               const uint4* src = reinterpret_cast<const uint4*>(
-                  p.q + ((int64_t)(r.q0 + tok_k) * p.hq + g * p.group + (rr_k - tok_k * p.group)) * D + c * 16);
+                  p.q + ((int64_t)(q.q0 + tok_k) * p.hq + q.g * p.group + (rr_k - tok_k * p.group)) * D +
+                  c * 16);
               v[k][0] = src[0];
               v[k][1] = src[1];
             }
@@ -780,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kPasses; ++k) {
             const int base_k = r0 + k * kPass + (warp - 4) * (32 / kLanes);
-            if (base_k >= rows) continue;  // the same for the warp; such rows are not looked at
+            if (base_k >= q.rows) continue;  // the same for the warp; such rows are not looked at
             const int row_k = base_k + lane / kLanes - r0;
             if constexpr (F8) {
               const uint32_t u[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
@@ -820,121 +856,117 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_proxy_async_smem();
         mbar_arrive(smem_u32(&bar_q));
-        if constexpr (F8) ok = wait_for(smem_u32(&bar_q), odd_q, abort_flag);  // the rows' exponents
-        odd_q ^= 1;
-        if (!ok) break;
       }
+      // ---- this thread's q row: position, mask, factor of its scores
+      const int row = lane_row + (alt ? 0 : w * kRows);
+      const bool in = row < q.rows;
+      uint64_t mask = 0;
+      if (in)
+        mask = p.mask[q.q0 + (q.row0 + row) / p.group] & (q.n >= 64 ? ~0ull : (1ull << q.n) - 1);
+      const int pos = q.base + max(__popcll(mask) - 1, 0);
+      mask &= present(q.n, q.base);
       float fac = p.scale_log2;
       if constexpr (F8) {
+        ok = wait_for(smem_u32(&bar_q), odd_q, abort_flag);  // the rows' exponents
+        if (!ok) break;
         const int ex = in ? s_ex[row] : 127;
         fac *= __uint_as_float((uint32_t)(ex < 8 ? 1 : ex - 7) << 23);
       }
-      // every row sees the keys of a tile in front of `base` and, with a window, from clear_lo on (or
-      // among the first ones)
-      const int clear_lo = p.window > 0 ? base + r.n - p.window : 0;
+      odd_q ^= 1;
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = 0; j < T; ++j, mslot.next()) {  // tile of the part
+      for (int j = 0; j < q.T; ++j, mslot.next(), kslot.next()) {  // tile of the part
         if (alt && (j & 1) != w) continue;
         ok = wait_for(smem_u32(&bar_meta[mslot.at]), mslot.odd, abort_flag) &&
              wait_for(smem_u32(&bar_s[w]), odd_s, abort_flag);
         if (!ok) break;
         odd_s ^= 1;
+        if (lane_row == 0 && (alt || w == 1)) mbar_arrive(smem_u32(&bar_k_empty[kslot.at]));
         tc_fence_after();
-        const int kv0 = first_key(x0 + j);
         const Meta<C::kPieces>& meta = s_meta[mslot.at];
-        const uint32_t okp = meta.ok;
-        const bool clear = okp == (1u << n_pieces) - 1u && kv0 + TK <= base &&
-                           (p.window == 0 || kv0 >= clear_lo || kv0 + TK <= p.sinks);
-        // 64 columns at a time: 128 scores in registers spill. A tile of 128 has its second half
-        // looked at for the maximum first and loaded again for its weights.
-        float tile_max = -INFINITY, alpha = 1.f, shift = 0.f;
-        bool resc = false;
-#pragma unroll 1
-        for (int turn = TK == 128 ? 0 : 1; turn < (TK == 128 ? 3 : 2); ++turn) {
-          const int half = turn == 1 ? 0 : 1;
-          uint32_t sr[64];
-          float part_max[2];
+        uint32_t sr[TK];
+        float part_max[TK / 32];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            part_max[c] = tmem_ld32_max(S_row + half * 64 + c * 32,
-                                        *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-          tmem_ld_wait();
-          float* s = reinterpret_cast<float*>(sr);
-          if (!clear) {
+        for (int c = 0; c < TK / 32; ++c)
+          part_max[c] =
+              tmem_ld32_max(S_row + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+        tmem_ld_wait();
+        float* s = reinterpret_cast<float*>(sr);
+        if (!meta.clear) {
+          const uint32_t okp = meta.ok;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int k0 = kv0 + half * 64 + 32 * c;
-              uint32_t see = below(base, k0);
-              if (p.window > 0) see &= ~below(pos + 1 - p.window, k0) | below(p.sinks, k0);
-              const int sh = k0 - base;  // the word's first column among the new tokens
-              if (sh > -32 && sh < 64) see |= (uint32_t)(sh >= 0 ? mask >> sh : mask << -sh);
+          for (int c = 0; c < TK / 32; ++c) {
+            const int k0 = meta.key0 + 32 * c;
+            uint32_t see = below(q.base, k0);
+            if (p.window > 0) see &= ~below(pos + 1 - p.window, k0) | below(p.sinks, k0);
+            const int sh = k0 - q.base;  // the word's first column among the new tokens
+            if (sh > -32 && sh < 64) see |= (uint32_t)(sh >= 0 ? mask >> sh : mask << -sh);
 #pragma unroll
-              for (int u = 0; u < 2; ++u)
-                if (!((okp >> ((4 * half + 2 * c + u) >> piece_shift)) & 1u)) see &= ~(0xFFFFu << (16 * u));
-              if (__all_sync(kAll, see == kAll)) continue;
+            for (int u = 0; u < 2; ++u)
+              if (!((okp >> ((2 * c + u) >> piece_shift)) & 1u)) see &= ~(0xFFFFu << (16 * u));
+            if (__all_sync(kAll, see == kAll)) continue;
 #pragma unroll
-              for (int cc = 0; cc < 32; ++cc)
-                if (!((see >> cc) & 1u)) s[32 * c + cc] = -INFINITY;
-              part_max[c] = row_max<32>(s + 32 * c);
+            for (int cc = 0; cc < 32; ++cc)
+              if (!((see >> cc) & 1u)) s[32 * c + cc] = -INFINITY;
+            part_max[c] = row_max<32>(s + 32 * c);
+          }
+        }
+        // Scores in the exp2 domain are s a + vl, with a and vl of the key's page; a > 0, so a page's
+        // largest score has its largest s.
+        float tile_max = -INFINITY;
+        if constexpr (F8) {
+          if (piece_shift == 0) {
+#pragma unroll
+            for (int c = 0; c < TK / 16; ++c) {
+              const float4 sc = meta.scale[c];
+              tile_max = fmaxf(tile_max, fmaf(row_max<16>(s + 16 * c), fac * sc.x, sc.y));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < TK / 32; ++c) {
+              const float4 sc = meta.scale[(2 * c) >> piece_shift];
+              tile_max = fmaxf(tile_max, fmaf(part_max[c], fac * sc.x, sc.y));
             }
           }
-          // Scores in the exp2 domain are s a + vl, with a and vl of the key's page; a > 0, so a
-          // page's largest score has its largest s.
-          if (turn < 2) {
-            if constexpr (F8) {
-              if (piece_shift == 0) {
+        } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  tile_max = fmaxf(tile_max, fmaf(row_max<16>(s + 16 * c), fac * meta.ks[4 * half + c],
-                                                  meta.vl[4 * half + c]));
-              } else {
+          for (int c = 0; c < TK / 32; ++c) tile_max = fmaxf(tile_max, part_max[c]);
+          tile_max *= fac;
+        }
+        const bool resc = tile_max > m_ref + kThr;  // false for -inf
+        float alpha = 1.f;
+        if (resc) {
+          alpha = ex2_approx(m_ref - tile_max);  // 0 from -inf
+          l *= alpha;
+          m_ref = tile_max;
+        }
+        const float shift = m_ref == -INFINITY ? 0.f : kBias - m_ref;
+        // ---- weights, packed in place
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  const int pc = (4 * half + 2 * c) >> piece_shift;
-                  tile_max = fmaxf(tile_max, fmaf(part_max[c], fac * meta.ks[pc], meta.vl[pc]));
-                }
-              }
-            } else {
-              tile_max = fmaxf(tile_max, fmaxf(part_max[0], part_max[1]) * fac);
-            }
+        for (int c = 0; c < TK / 16; ++c) {
+          float a = fac, add = shift, inv = 1.f;
+          if constexpr (F8) {
+            const float4 sc = meta.scale[c >> piece_shift];
+            a = fac * sc.x;
+            add = shift + sc.y;
+            inv = sc.z;
           }
-          if (turn == 0) continue;
-          if (turn == 1) {
-            resc = tile_max > m_ref + kThr;  // false for -inf
-            if (resc) {
-              alpha = ex2_approx(m_ref - tile_max);  // 0 from -inf
-              l *= alpha;
-              m_ref = tile_max;
-            }
-            shift = m_ref == -INFINITY ? 0.f : kBias - m_ref;
+          const float2 a2 = make_float2(a, a), b2 = make_float2(add, add);
+          float2 acc = make_float2(0.f, 0.f);
+          float2 y[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            y[u] = ffma2(make_float2(s[16 * c + 2 * u], s[16 * c + 2 * u + 1]), a2, b2);
+            y[u].x = ex2_approx(y[u].x);
+            y[u].y = ex2_approx(y[u].y);
           }
-          // ---- weights, packed in place
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float a = fac, add = shift, inv = 1.f;
-            if constexpr (F8) {
-              const int pc = (4 * half + c) >> piece_shift;
-              a = fac * meta.ks[pc];
-              add = shift + meta.vl[pc];
-              inv = meta.vi[pc];
-            }
-            const float2 a2 = make_float2(a, a), b2 = make_float2(add, add);
-            float2 acc = make_float2(0.f, 0.f);
-            float2 y[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              y[u] = ffma2(make_float2(s[16 * c + 2 * u], s[16 * c + 2 * u + 1]), a2, b2);
-              y[u].x = ex2_approx(y[u].x);
-              y[u].y = ex2_approx(y[u].y);
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              acc = fadd2(acc, y[u]);
-              sr[8 * c + u] = F8 ? pack_f16x2(y[u].x, y[u].y) : pack_bf16x2(y[u].x, y[u].y);
-            }
-            l = fmaf(acc.x + acc.y, inv, l);
+          for (int u = 0; u < 8; ++u) {
+            acc = fadd2(acc, y[u]);
+            sr[8 * c + u] = F8 ? pack_f16x2(y[u].x, y[u].y) : pack_bf16x2(y[u].x, y[u].y);
           }
-          tmem_st32(S_row + half * 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[0]));
+          l = fmaf(acc.x + acc.y, inv, l);
+          if (c % 4 == 3)
+            tmem_st32(S_row + (c / 4) * 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[(c / 4) * 32]));
         }
         // The accumulator: its last product was issued before this tile's S, which is complete.
         if (j > (alt ? w : 0) && __any_sync(kAll, resc)) {
@@ -945,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld16(O_row + c0, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
             tmem_st16(O_row + c0, o);
           }
         }
@@ -957,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the unit's part ends
       // The second warpgroup's statistics go through two columns behind its last weights, on the same
       // lanes.
-      const bool other = alt && T > 1;
+      const bool other = alt && q.T > 1;
       if (alt && w == 1) {
         if (other) {
           tmem_st2(S_row + 126, __float_as_uint(m_ref), __float_as_uint(l));
@@ -985,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (other || !alt) odd_other ^= 1;  // the second warpgroup had sums
         if (!ok) break;
         tc_fence_after();
-        const bool final = whole_l && whole_r;
+        const bool final = q.whole_l && q.whole_r;
         const float top = fmaxf(m_ref, m1);
         float f0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - top);
         float f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - top);
@@ -995,8 +1027,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           f0 *= inv;
           f1 *= inv;
         }
-        const int64_t at = (int64_t)(r.q0 + tok) * p.hq + head;
-        float* part = p.parts + (size_t)(2 * blockIdx.x + (whole_l ? 1 : 0)) * (C::kUnitRows * (D + 2));
+        const int rr = q.row0 + row, tok = in ? rr / p.group : 0;
+        const int64_t at = (int64_t)(q.q0 + tok) * p.hq + q.g * p.group + (rr - tok * p.group);
+        float* part = p.parts + (size_t)(2 * blockIdx.x + (q.whole_l ? 1 : 0)) * (C::kUnitRows * (D + 2));
         float* to32 = final ? static_cast<float*>(p.out) + at * D : part + row * 4;
         const int quad = final ? 4 : 4 * C::kUnitRows;  // from four columns to the next
         uint16_t* to16 = static_cast<uint16_t*>(p.out) + at * D;
@@ -1007,25 +1040,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           float v[32];
 #pragma unroll
-          for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(o[q]) * f0;
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f0;
           if (other) {
             tmem_ld32(tmem + 384 + lane_off + c0, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] = fmaf(__uint_as_float(o[q]), f1, v[q]);
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), f1, v[i]);
           }
           if (!in) continue;
           if (final && p.out_bf16) {
 #pragma unroll
-            for (int q = 0; q < 32; q += 8)
-              *reinterpret_cast<uint4*>(to16 + c0 + q) =
-                  make_uint4(pack_bf16x2(v[q], v[q + 1]), pack_bf16x2(v[q + 2], v[q + 3]),
-                             pack_bf16x2(v[q + 4], v[q + 5]), pack_bf16x2(v[q + 6], v[q + 7]));
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4*>(to16 + c0 + i) =
+                  make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
+                             pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
           } else {
 #pragma unroll
-            for (int q = 0; q < 32; q += 4)
-              *reinterpret_cast<float4*>(to32 + (c0 + q) / 4 * quad) =
-                  make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(to32 + (c0 + i) / 4 * quad) =
+                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
         }
         if (in) {
@@ -1035,15 +1068,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.lse[at] = sum > 0.f ? (top - kBias + log2f(sum)) * kLn2 : -INFINITY;
         }
         tc_fence_before();
-        if (!whole_l && whole_r && tid == 128) {
-          // the unit ends here: tell the second launch where it began
-          const int begin = before - x0;  // list place of the unit's first tile
-          const int longer = more * (len + 1);  // tiles of the runs with one more
-          const int c0 = begin < longer
-                             ? (int)((unsigned)begin / (unsigned)(len + 1))
-                             : more + (int)((unsigned)(begin - longer) / (unsigned)len);
-          p.jobs[blockIdx.x] = make_int4(c0, rows, rt * C::kUnitRows, g);
-          p.job_q0[blockIdx.x] = r.q0;
+        if (!q.whole_l && q.whole_r && tid == 128) {  // tell the second launch where the unit began
+          p.jobs[blockIdx.x] = make_int4(q.c0, q.rows, q.row0, q.g);
+          p.job_q0[blockIdx.x] = q.q0;
         }
       }
       mbar_arrive(smem_u32(&bar_done));
