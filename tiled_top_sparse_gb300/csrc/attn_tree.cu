@@ -167,6 +167,22 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   }
   return __all_sync(kAll, ok);
 }
+// Looks at three barriers at once.
+__device__ __forceinline__ bool peek3(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, uint32_t c,
+                                      uint32_t pc) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+      "and.pred p, p, q;\n\tand.pred p, p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(a), "r"(pa), "r"(b), "r"(pb), "r"(c), "r"(pc)
+      : "memory");
+  return ok != 0;
+}
 // Two columns of a warp's TMEM lanes.
 __device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t a, uint32_t b) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(a), "r"(b)
@@ -279,12 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   // Of a part: described, its description read. Of a tile: K and V landed; its K's products done; V
   // ready for its product (widened, or cleared); V's slot (e4m3: the codes') free; its scales
-  // written; e4m3: a widened V's last product done. Of a warpgroup: scores, weights, sums. Of a part:
-  // q tiles written; both warpgroups done with it (its sums read, its products complete); the second
-  // warpgroup's statistics.
+  // written. Of a warpgroup: scores, weights, sums. Of a part: q tiles written; both warpgroups done
+  // with it (its sums read, its products complete); the second warpgroup's statistics.
   __shared__ __align__(8) uint64_t bar_part[2], bar_part_empty[2], bar_k[S], bar_v[S],
-      bar_k_empty[S], bar_v_empty[S], bar_ready[S], bar_meta[C::kMeta], bar_wide_empty[2], bar_s[2],
-      bar_p[2], bar_o[2], bar_q, bar_done, bar_ml, bar_drain;
+      bar_k_empty[S], bar_v_empty[S], bar_ready[S], bar_meta[C::kMeta], bar_s[2], bar_p[2], bar_o[2],
+      bar_q, bar_done, bar_ml, bar_drain;
   __shared__ __align__(16) Meta<C::kPieces> s_meta[C::kMeta];
   __shared__ Part s_part[2];
   __shared__ uint8_t s_ex[C::kUnitRows];  // e4m3: the exponent that a q row was scaled by
@@ -314,7 +329,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bar_part[i]), 1);
       mbar_init(smem_u32(&bar_part_empty[i]), kThreads / 32 - 1);  // every warp but the producer
-      mbar_init(smem_u32(&bar_wide_empty[i]), 1);
       mbar_init(smem_u32(&bar_s[i]), 1);
       mbar_init(smem_u32(&bar_p[i]), kRows);
       mbar_init(smem_u32(&bar_o[i]), 1);
@@ -638,32 +652,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto step = [&](auto which, int i) -> bool {
           constexpr int w = decltype(which)::value;
           const bool pv = i >= 2 && i < J + 2, qk = i < J;
-          // everything the step needs is looked at together: a look takes as long as an issue
-          bool there = true;
-          if (pv)
-            there = mbar_peek(smem_u32(&bar_ready[vslot.at]), vslot.odd) &
-                    mbar_peek(smem_u32(&bar_p[w]), odd_p[w]);
-          if (qk) there &= mbar_peek(smem_u32(&bar_k[kslot.at]), kslot.odd);
-          if (!__all_sync(kAll, there)) {
-            if (pv && (!wait_for(smem_u32(&bar_ready[vslot.at]), vslot.odd, abort_flag) ||
-                       !wait_for(smem_u32(&bar_p[w]), odd_p[w], abort_flag)))
-              return false;
-            if (qk && !wait_for(smem_u32(&bar_k[kslot.at]), kslot.odd, abort_flag)) return false;
+          // Everything the step needs is looked at together: a look takes as long as an issue. A barrier
+          // that is not needed stands in for none (its phase is known to be complete).
+          const uint32_t any = smem_u32(&bar_q);
+          const uint32_t bar_a = pv ? smem_u32(&bar_ready[vslot.at]) : any, odd_a = pv ? vslot.odd : odd_q ^ 1;
+          const uint32_t bar_b = pv ? smem_u32(&bar_p[w]) : any, odd_b = pv ? odd_p[w] : odd_q ^ 1;
+          const uint32_t bar_c = qk ? smem_u32(&bar_k[kslot.at]) : any, odd_c = qk ? kslot.odd : odd_q ^ 1;
+          uint32_t since = 0;
+          while (!__all_sync(kAll, peek3(bar_a, odd_a, bar_b, odd_b, bar_c, odd_c))) {
+            if (__any_sync(kAll, *abort_flag)) return false;
+            uint32_t now;
+            asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));
+            if (since == 0) since = now | 1u;
+            if ((int)(now - since) > (int)kWaitLimitNs) *abort_flag = 1;
           }
           tc_fence_after();
           if (pv) {
             odd_p[w] ^= 1;
             issue_o(w, F8 ? wide + wide_at * C::kWideBytes : sV(vslot.at), i >= 4);
-            if (F8 && (alt || w == 1)) mma_commit_elect(smem_u32(&bar_wide_empty[wide_at]), e);
           }
           if (qk) {
             issue_s(w, alt ? 0 : w, kslot.at);
-            mma_commit_elect(smem_u32(&bar_s[w]), e);  // its reader hands K's slot back
+            // One commit a step (each takes the issuer 200 cycles): who sees it hands back K's slot and that
+            // of the V two jobs before.
+            mma_commit_elect(smem_u32(&bar_s[w]), e);
             if (alt || w == 1) kslot.next();
           }
           if (pv) {
             if (alt || w == 1) {
-              if (!F8) mma_commit_elect(smem_u32(&bar_v_empty[vslot.at]), e);
               vslot.next();
               wide_at ^= 1;
             }
@@ -679,12 +695,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(smem_u32(&bar_drain), 0, nullptr, p.dev_status);
     } else {
       // ------------------------------------------------------------------ V for the second product
-      int it = 0;
       Ring<S> slot;
       Ring<C::kMeta> mslot;
+      uint32_t wide_at = 0, odd_s[2] = {0, 0};  // e4m3: the widened V, parities of the next scores
       Part q;
       bool ok = true;
       while (ok && next_part(q)) {
+        const bool alt = !kTwo || q.rows <= kRows;
         // new tokens that some token sees, and the first key of the windows
         const uint64_t here = present(q.n, q.base);
         uint64_t any = 0;
@@ -701,12 +718,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         least = __reduce_min_sync(kAll, least);
         const int lo = p.window > 0 ? max(q.base + least + 1 - p.window, 0) : 0;
         const int kept = min(p.sinks, lo);
-        for (int x = 0; x < q.T; ++x, ++it, slot.next(), mslot.next()) {
+        for (int x = 0; x < q.T; ++x, slot.next(), mslot.next(), wide_at ^= 1) {
           const int st = slot.at;
           // (K's barrier may be a tile's phase further; V's slot waits for this warp)
           ok = wait_for(smem_u32(&bar_v[st]), slot.odd, abort_flag);
-          if (F8 && ok && it >= 2)
-            ok = wait_for(smem_u32(&bar_wide_empty[it & 1]), ((it >> 1) - 1) & 1, abort_flag);
+          // e4m3: with the tile's own scores (the first of them) the products with the V two tiles before
+          // are complete, whose place this one takes; the next scores of that warpgroup wait for it.
+          if constexpr (F8) {
+            const bool second = alt && (x & 1);
+            ok = ok && wait_for(smem_u32(&bar_s[second]), second ? odd_s[1] : odd_s[0], abort_flag);
+            if (second || !alt) odd_s[1] ^= 1;
+            if (!second) odd_s[0] ^= 1;
+          }
           if (!ok) break;
           const uint32_t okp = s_meta[mslot.at].ok;
           const int key0 = s_meta[mslot.at].key0;
@@ -718,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return key - q.base < 64 && ((any >> (key - q.base)) & 1u);
           };
           if constexpr (F8) {
-            const uint32_t from = sV(st), to = wide + (it & 1) * C::kWideBytes;
+            const uint32_t from = sV(st), to = wide + wide_at * C::kWideBytes;
             // A thread's chunks of 16 codes lie kStep rows apart in one column: the swizzle is the
             // same for all of them. kDeep are on their way at a time.
             constexpr int kCpr = D / 16, kStep = 64 / kCpr, kDeep = 8;
@@ -874,13 +897,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       odd_q ^= 1;
       float m_ref = -INFINITY, l = 0.f;
+      int v_before = 0;  // slot of the job before
       for (int j = 0; j < q.T; ++j, mslot.next(), kslot.next()) {  // tile of the part
         if (alt && (j & 1) != w) continue;
         ok = wait_for(smem_u32(&bar_meta[mslot.at]), mslot.odd, abort_flag) &&
              wait_for(smem_u32(&bar_s[w]), odd_s, abort_flag);
         if (!ok) break;
         odd_s ^= 1;
-        if (lane_row == 0 && (alt || w == 1)) mbar_arrive(smem_u32(&bar_k_empty[kslot.at]));
+        if (lane_row == 0 && (alt || w == 1)) {
+          mbar_arrive(smem_u32(&bar_k_empty[kslot.at]));
+          // the product of this warpgroup's job before is complete, too
+          if (!F8 && j > (alt ? w : 0)) mbar_arrive(smem_u32(&bar_v_empty[v_before]));
+          v_before = kslot.at;
+        }
         tc_fence_after();
         const Meta<C::kPieces>& meta = s_meta[mslot.at];
         uint32_t sr[TK];
@@ -996,7 +1025,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(smem_u32(&bar_ml));
-          odd_o ^= 1;  // the first warpgroup waits for the sums
+          ok = wait_for(smem_u32(&bar_o[1]), odd_o, abort_flag);
+          if (!ok) break;
+          odd_o ^= 1;
         }
       } else {
         float m1 = -INFINITY, l1 = 0.f;
@@ -1073,6 +1104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.job_q0[blockIdx.x] = q.q0;
         }
       }
+      if (!F8 && lane_row == 0 && (alt ? q.T > w : w == 1)) mbar_arrive(smem_u32(&bar_v_empty[v_before]));
       mbar_arrive(smem_u32(&bar_done));
     }
   }
