@@ -48,7 +48,7 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;  // q rows of a tile (TMEM lanes)
 // What the end of a unit costs (joining, the next unit's q), in tiles of the list.
 constexpr int kEndTiles = 3;
-constexpr int kMinRun = 2;  // tiles of a run at least: one for each warpgroup
+constexpr int kMinRun = 2;  // places of a run at least: a tile for each warpgroup
 constexpr float kMinValueScale = 0x1p-80f;  // as in attn_decode.cu
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -267,6 +267,13 @@ __device__ __forceinline__ Req load_req(const Params& p, int b, uint32_t* bad) {
   r.rt = (r.n * p.group + p.unit_rows - 1) / p.unit_rows;
   return r;
 }
+// Places of the list that a tile of a request's last row block takes: two where it has more than 128
+// rows, which both warpgroups then go through (ragged trees of up to 155 rows, window 4096: 67 us
+// with one place each, XX with two).
+__device__ __forceinline__ int last_weight(const Params& p, int n, int unit_rows) {
+  const int rows = n * p.group;
+  return (rows - 1) % unit_rows >= kRows ? 2 : 1;
+}
 // A place in a ring of N slots and the parity of its current round.
 template <int N>
 struct Ring {
@@ -295,10 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   // Of a part: described, its description read. Of a tile: K and V landed; its K's products done; V
   // ready for its product (widened, or cleared); V's slot (e4m3: the codes') free; its scales
-  // written. Of a warpgroup: scores, weights, sums. Of a part: q tiles written; both warpgroups done
+  // written. Of a warpgroup: scores, weights of a tile's first 64 keys, all weights, sums. Of a part: q tiles written; both warpgroups done
   // with it (its sums read, its products complete); the second warpgroup's statistics.
   __shared__ __align__(8) uint64_t bar_part[2], bar_part_empty[2], bar_k[S], bar_v[S],
-      bar_k_empty[S], bar_v_empty[S], bar_ready[S], bar_meta[C::kMeta], bar_s[2], bar_p[2], bar_o[2],
+      bar_k_empty[S], bar_v_empty[S], bar_ready[S], bar_meta[C::kMeta], bar_s[2], bar_half[2], bar_p[2], bar_o[2],
       bar_q, bar_done, bar_ml, bar_drain;
   __shared__ __align__(16) Meta<C::kPieces> s_meta[C::kMeta];
   __shared__ Part s_part[2];
@@ -330,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bar_part[i]), 1);
       mbar_init(smem_u32(&bar_part_empty[i]), kThreads / 32 - 1);  // every warp but the producer
       mbar_init(smem_u32(&bar_s[i]), 1);
+      mbar_init(smem_u32(&bar_half[i]), kRows);
       mbar_init(smem_u32(&bar_p[i]), kRows);
       mbar_init(smem_u32(&bar_o[i]), 1);
     }
@@ -356,10 +364,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return x;
   };
-  auto tiles_of = [&](const Req& r) -> int { return p.hkv * r.rt * (r.nt + kEndTiles); };
+  auto places_of = [&](const Req& r) -> int {  // the last row block may have up to 128 rows
+    if (r.rt == 0) return 0;
+    return p.hkv * ((r.rt - 1) * r.nt * C::kQTiles + r.nt * last_weight(p, r.n, C::kUnitRows) + r.rt * kEndTiles);
+  };
   int total = 0, runs = 0, len = 0, more = 0, t0 = 0, t1 = 0;
   auto split = [&]() -> bool {
-    runs = min((int)((unsigned)(total + kMinRun - 1) / kMinRun), p.ctas);
+    if (total == 0) return false;
+    runs = min(max((int)((unsigned)total / kMinRun), 1), p.ctas);
     if ((int)blockIdx.x >= runs) return false;
     len = (int)((unsigned)total / (unsigned)runs);
     more = total - len * runs;
@@ -384,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int b = 0, off = 0;
   bool work;
   if (p.batch <= 32) {  // every warp for itself
-    const int v = lane < p.batch ? tiles_of(load_req<TK>(p, lane, &bad)) : 0;
+    const int v = lane < p.batch ? places_of(load_req<TK>(p, lane, &bad)) : 0;
     const int incl = scan32(v);
     total = __shfl_sync(kAll, incl, 31);
     work = split();
@@ -397,14 +409,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int base = 0; base < p.batch; base += kThreads) {
       const int i = base + tid;
       int sum;
-      block_scan(i < p.batch ? tiles_of(load_req<TK>(p, i, &bad)) : 0, &sum);
+      block_scan(i < p.batch ? places_of(load_req<TK>(p, i, &bad)) : 0, &sum);
       total += sum;
     }
     work = split();
     uint32_t again = 0;
     for (int base = 0, carry = 0; work && base < p.batch && carry <= t0; base += kThreads) {
       const int i = base + tid;
-      const int v = i < p.batch ? tiles_of(load_req<TK>(p, i, &again)) : 0;
+      const int v = i < p.batch ? places_of(load_req<TK>(p, i, &again)) : 0;
       int sum;
       const int incl = carry + block_scan(v, &sum);
       if (incl > t0 && incl - v <= t0) {
@@ -448,12 +460,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // scales for head cache_g) in registers, loaded 32 pages at a time.
       Req r = load_req<TK>(p, b, &bad);
       int left = t1 - t0, parts = 0;
-      int g, rt, x0;
+      int g, rt, at0;  // place within the unit
       {  // the run's first unit, perhaps from its middle
-        const int u = (int)((unsigned)off / (unsigned)(r.nt + kEndTiles));
-        x0 = off - u * (r.nt + kEndTiles);
-        g = (int)((unsigned)u / (unsigned)r.rt);
-        rt = u - g * r.rt;
+        const int full = r.nt * C::kQTiles + kEndTiles;  // places of a full row block
+        const int head = (int)((unsigned)places_of(r) / (unsigned)p.hkv);
+        g = (int)((unsigned)off / (unsigned)head);
+        at0 = off - g * head;
+        rt = min((int)((unsigned)at0 / (unsigned)full), r.rt - 1);
+        at0 -= rt * full;
       }
       int it = 0;
       Ring<S> slot;
@@ -475,8 +489,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       while (ok && left > 0) {
-        const int before = t1 - left, x1 = min(r.nt, x0 + left);
-        left -= min(r.nt + kEndTiles - x0, left);
+        // A unit whose warpgroups each take every tile counts a tile as two places: tile x begins at
+        // place x weight. Runs have two places at least, so that none lies between two tiles.
+        const int weight = rt == r.rt - 1 ? last_weight(p, r.n, C::kUnitRows) : C::kQTiles;
+        const int begin = t1 - left - at0;  // list place of the unit's first tile
+        const int x0 = (at0 + weight - 1) >> (weight - 1);
+        const int x1 = min(r.nt, (at0 + left + weight - 1) >> (weight - 1));
+        left -= min(r.nt * weight + kEndTiles - at0, left);
+        at0 = 0;
         const int base = r.L - r.n;
         if (x0 < x1) {  // else the run begins behind the unit's last tile
           Part q;
@@ -491,7 +511,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           q.whole_r = x1 == r.nt;
           q.c0 = 0;
           if (!q.whole_l && q.whole_r) {  // the unit ends here: where it began
-            const int begin = before - x0;        // list place of the unit's first tile
             const int longer = more * (len + 1);  // tiles of the runs with one more
             q.c0 = begin < longer ? (int)((unsigned)begin / (unsigned)(len + 1))
                                   : more + (int)((unsigned)(begin - longer) / (unsigned)len);
@@ -585,7 +604,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
         }
-        x0 = 0;
         if (left > 0 && ++rt == r.rt) {
           rt = 0;
           if (++g == p.hkv) {
@@ -629,11 +647,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                          kd + (((k / 4) * TK * 128 + (k % 4) * 32) >> 4), idesc, k > 0, e);
         }
       };
-      auto issue_o = [&](int w, uint32_t v, bool acc) {
+      auto issue_o = [&](int w, uint32_t v, bool acc, auto half) {
+        constexpr int k0 = decltype(half)::value * (TK / 32);
         const uint64_t vd = smem_desc(v, TK * 128, 1024, kSw128);
         constexpr uint32_t idesc = F8 ? idesc_f16_f32(kRows, D, 1) : idesc_bf16_f32(kRows, D, 0, 1);
 #pragma unroll
-        for (int k = 0; k < TK / 16; ++k)
+        for (int k = k0; k < k0 + TK / 32; ++k)
           mma_ts_elect(o_t(w), s_t(w) + k * 8, vd + ((k * 16 * 128) >> 4), idesc, acc || k > 0, e);
       };
       Ring<S> kslot, vslot;   // of the next tile whose S, whose P V is issued
@@ -656,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // that is not needed stands in for none (its phase is known to be complete).
           const uint32_t any = smem_u32(&bar_q);
           const uint32_t bar_a = pv ? smem_u32(&bar_ready[vslot.at]) : any, odd_a = pv ? vslot.odd : odd_q ^ 1;
-          const uint32_t bar_b = pv ? smem_u32(&bar_p[w]) : any, odd_b = pv ? odd_p[w] : odd_q ^ 1;
+          const uint32_t bar_b = pv ? smem_u32(&bar_half[w]) : any, odd_b = pv ? odd_p[w] : odd_q ^ 1;
           const uint32_t bar_c = qk ? smem_u32(&bar_k[kslot.at]) : any, odd_c = qk ? kslot.odd : odd_q ^ 1;
           uint32_t since = 0;
           while (!__all_sync(kAll, peek3(bar_a, odd_a, bar_b, odd_b, bar_c, odd_c))) {
@@ -668,8 +687,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           if (pv) {
+            // the products with the first 64 weights run while the others are computed
+            const uint32_t v = F8 ? wide + wide_at * C::kWideBytes : sV(vslot.at);
+            issue_o(w, v, i >= 4, std::integral_constant<int, 0>());
+            if (!wait_for(smem_u32(&bar_p[w]), odd_p[w], abort_flag)) return false;
+            tc_fence_after();
+            issue_o(w, v, true, std::integral_constant<int, 1>());
             odd_p[w] ^= 1;
-            issue_o(w, F8 ? wide + wide_at * C::kWideBytes : sV(vslot.at), i >= 4);
           }
           if (qk) {
             issue_s(w, alt ? 0 : w, kslot.at);
@@ -996,18 +1020,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = fmaf(acc.x + acc.y, inv, l);
           if (c % 4 == 3)
             tmem_st32(S_row + (c / 4) * 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[(c / 4) * 32]));
-        }
-        // The accumulator: its last product was issued before this tile's S, which is complete.
-        if (j > (alt ? w : 0) && __any_sync(kAll, resc)) {
-          const uint32_t O_row = tmem + 256 + w * 128 + lane_off;
+          if (c == 3) {
+            // The accumulator: its last product was issued before this tile's S, which is complete.
+            if (j > (alt ? w : 0) && __any_sync(kAll, resc)) {
+              const uint32_t O_row = tmem + 256 + w * 128 + lane_off;
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t o[16];
-            tmem_ld16(O_row + c0, o);
-            tmem_ld_wait();
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld16(O_row + c0, o);
+                tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st16(O_row + c0, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st16(O_row + c0, o);
+              }
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&bar_half[w]));
           }
         }
         tmem_st_wait();
