@@ -48,6 +48,7 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;  // q rows of a tile (TMEM lanes)
 // What the end of a unit costs (joining, the next unit's q), in tiles of the list.
 constexpr int kEndTiles = 3;
+constexpr int kParts = 4;   // parts of a run that are described ahead
 constexpr int kMinRun = 2;  // places of a run at least: a tile for each warpgroup
 constexpr float kMinValueScale = 0x1p-80f;  // as in attn_decode.cu
 constexpr float kLog2e = 1.4426950408889634f;
@@ -59,7 +60,7 @@ struct Cfg {
   static constexpr int kRowBytes = D * (F8 ? 1 : 2);
   static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;  // one swizzled row
   static constexpr int kPanels = kRowBytes / kPanelBytes;
-  static constexpr int kTK = 128;                    // keys per tile
+  static constexpr int kTK = 128;                    // keys per tile: whole pages
   static constexpr int kTileBytes = kTK * kRowBytes;       // K (or V) of one tile
   static constexpr int kQTiles = kTwo ? 2 : 1;
   // e4m3: the hi and the lo half one after the other, each kRows rows of one panel
@@ -300,15 +301,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<F8, D, kTwo>;
   constexpr int TK = C::kTK, S = C::kStages, PB = C::kPanelBytes;
   extern __shared__ uint8_t smem_raw[];
-  // Of a part: described, its description read. Of a tile: K and V landed; its K's products done; V
-  // ready for its product (widened, or cleared); V's slot (e4m3: the codes') free; its scales
-  // written. Of a warpgroup: scores, weights of a tile's first 64 keys, all weights, sums. Of a part: q tiles written; both warpgroups done
+  // Of a part: described, its description read. Of a tile: K and V landed; their slots free (K's
+  // products done; V's products done, or its codes widened: K's place is filled again a product earlier);
+  // V ready for its product (widened, or cleared); its scales written. Of a warpgroup: scores, weights of a tile's first 64 keys, all weights, sums. Of a part: q tiles written; both warpgroups done
   // with it (its sums read, its products complete); the second warpgroup's statistics.
-  __shared__ __align__(8) uint64_t bar_part[2], bar_part_empty[2], bar_k[S], bar_v[S],
+  __shared__ __align__(8) uint64_t bar_part[kParts], bar_part_empty[kParts], bar_k[S], bar_v[S],
       bar_k_empty[S], bar_v_empty[S], bar_ready[S], bar_meta[C::kMeta], bar_s[2], bar_half[2], bar_p[2], bar_o[2],
       bar_q, bar_done, bar_ml, bar_drain;
   __shared__ __align__(16) Meta<C::kPieces> s_meta[C::kMeta];
-  __shared__ Part s_part[2];
+  __shared__ Part s_part[kParts];
   __shared__ uint8_t s_ex[C::kUnitRows];  // e4m3: the exponent that a q row was scaled by
   __shared__ int s_scan[kThreads / 32], s_b, s_off, s_abort;
   __shared__ uint32_t s_tmem;
@@ -329,13 +330,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bar_k[i]), 1);
       mbar_init(smem_u32(&bar_v[i]), 1);
       mbar_init(smem_u32(&bar_k_empty[i]), 1);
-      mbar_init(smem_u32(&bar_v_empty[i]), F8 ? 2 : 1);
+      mbar_init(smem_u32(&bar_v_empty[i]), F8 ? 2 : 1);  // both warps that widen it
       mbar_init(smem_u32(&bar_ready[i]), 2);
     }
     for (int i = 0; i < C::kMeta; ++i) mbar_init(smem_u32(&bar_meta[i]), 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kParts; ++i) {
       mbar_init(smem_u32(&bar_part[i]), 1);
       mbar_init(smem_u32(&bar_part_empty[i]), kThreads / 32 - 1);  // every warp but the producer
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bar_s[i]), 1);
       mbar_init(smem_u32(&bar_half[i]), kRows);
       mbar_init(smem_u32(&bar_p[i]), kRows);
@@ -438,26 +441,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
     return;
   }
-  const int piece = p.page_size < TK ? p.page_size : TK;  // keys per TMA box
-  const int n_pieces = TK / piece;
+  const int piece = p.page_size, n_pieces = TK / piece;  // keys per TMA box, a page; pages of a tile
   const int piece_shift = 31 - __clz(piece >> 4);  // 16 keys -> piece
-  // The next part of the run, as the producer describes it to the other warps; false: there is none.
-  Ring<2> pslot;
-  auto next_part = [&](Part& q) -> bool {
-    if (!wait_for(smem_u32(&bar_part[pslot.at]), pslot.odd, abort_flag)) return false;
-    q = s_part[pslot.at];
+  // The next part of the run, as the producer describes it to the other warps (false: there is none),
+  // where it stays until the warp is done with it: registers are scarce.
+  Ring<kParts> pslot;
+  auto next_part = [&]() -> bool {
+    return wait_for(smem_u32(&bar_part[pslot.at]), pslot.odd, abort_flag) && s_part[pslot.at].T > 0;
+  };
+  auto part_done = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bar_part_empty[pslot.at]));
     pslot.next();
-    return q.T > 0;
   };
 
   if (warp < 4) {
     give_registers<kIssueRegs>();
     if (warp == 0) {
       // ------------------------------------------------------------------ producer
-      // Walks the run. Lane i keeps page cache_at + i of the request (and what the others need of its
-      // scales for head cache_g) in registers, loaded 32 pages at a time.
+      // Walks the run. What it does for a tile must take well under the 1400 (heads of 64: 700) cycles
+      // that HBM takes for an SM's share of it.
       Req r = load_req<TK>(p, b, &bad);
       int left = t1 - t0, parts = 0;
       int g, rt, at0;  // place within the unit
@@ -472,12 +475,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = 0;
       Ring<S> slot;
       Ring<C::kMeta> mslot;
-      int cache_b = -1, cache_at = 0, cache_g = -1, page = -1;
-      bool fine = true;                    // the page's scales are in range
-      float ks = 1.f, vl = 0.f, vi = 1.f;  // key scale, log2 and inverse of the value scale
+      // Of page cache_at + lane of request cache_b: the page, for head cache_g its key scale, log2 and
+      // inverse of its value scale, and whether they are in range. The next 32 pages' are on their way.
+      int cache_b = -1, cache_at = 0, cache_g = -1, page = -1, page_next = -1;
+      bool fine = true;
+      float ks = 1.f, vl = 0.f, vi = 1.f, sk_next = 1.f, sv_next = 1.f;
+      bool asked = false;  // for the next pages' scales
+      auto page_of = [&](int first) -> int {
+        const int lp = first + lane;
+        const int pg = lp < p.max_pages ? p.page_tables[(int64_t)b * p.max_pages + lp] : -1;
+        return pg < p.num_pages ? pg : -1;  // < 0: none
+      };
+      auto scales_of = [&](int pg, float& sk, float& sv) {
+        sk = sv = 1.f;
+        if (pg >= 0) {
+          sk = p.k_scale[(int64_t)pg * p.hkv + g];
+          sv = p.v_scale[(int64_t)pg * p.hkv + g];
+        }
+      };
       bool ok = true;
       auto describe = [&](const Part& q) -> bool {
-        if (parts >= 2 && !wait_for(smem_u32(&bar_part_empty[pslot.at]), pslot.odd ^ 1, abort_flag))
+        if (parts >= kParts && !wait_for(smem_u32(&bar_part_empty[pslot.at]), pslot.odd ^ 1, abort_flag))
           return false;
         if (lane == 0) {
           s_part[pslot.at] = q;
@@ -523,60 +541,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = x0; ok && x < x1; ++x, ++it, slot.next(), mslot.next()) {
           const int key0 = (x < r.st ? x : r.lt + x - r.st) * TK, st = slot.at;
           const int pg0 = key0 >> p.page_shift;
-          if (cache_b != b || pg0 < cache_at || pg0 + n_pieces > cache_at + 32) {
+          if (cache_b != b || cache_g != g || pg0 < cache_at || pg0 + n_pieces > cache_at + 32) {
+            float sk = 1.f, sv = 1.f;
+            if (cache_b == b && cache_g == g && pg0 == cache_at + 32) {
+              page = page_next;
+              if (F8 && !asked) scales_of(page, sk_next, sv_next);
+              sk = sk_next;
+              sv = sv_next;
+            } else {
+              page = page_of(pg0);
+              if (F8) scales_of(page, sk, sv);
+            }
             cache_b = b;
             cache_at = pg0;
-            cache_g = -1;
-            const int lp = pg0 + lane;
-            page = lp < p.max_pages ? p.page_tables[(int64_t)b * p.max_pages + lp] : -1;
-            if (page < 0 || page >= p.num_pages) page = -1;
-          }
-          float sk = 1.f, sv = 1.f;
-          const bool new_scales = F8 && cache_g != g;
-          if (new_scales && page >= 0) {  // asked for here, looked at behind the copies
-            sk = p.k_scale[(int64_t)page * p.hkv + g];
-            sv = p.v_scale[(int64_t)page * p.hkv + g];
-          }
-          const int at = pg0 - cache_at + (lane < n_pieces ? lane : 0);
-          const int pg = __shfl_sync(kAll, page, at);
-          const int a = key0 + lane * piece;  // this lane's piece: keys [a, a + piece)
-          const bool seen = lane < n_pieces && a < r.L && (a + piece > r.lo || a < r.sinks);
-          const bool there = seen && pg >= 0;
-          const uint32_t sent = __ballot_sync(kAll, there);
-          if (it >= S) {
-            ok = wait_for(smem_u32(&bar_k_empty[st]), slot.odd ^ 1, abort_flag);
-            if (!ok) break;
-          }
-          const uint32_t bytes = __popc(sent) * piece * C::kRowBytes;
-          const int row = key0 & (p.page_size - 1);  // 0 unless the tile is inside a page
-          const int slab = pg * p.hkv + g;
-          if (there) {
-#pragma unroll
-            for (int pn = 0; pn < C::kPanels; ++pn)
-              tma_load_3d(sK(st) + pn * TK * PB + lane * piece * PB, &map_k, smem_u32(&bar_k[st]),
-                          pn * 64, row, slab);
-          }
-          uint32_t flag = seen && !there ? kDevIndexRange : 0u;
-          uint32_t use = sent;
-          Meta<C::kPieces>& meta = s_meta[mslot.at];
-          if constexpr (F8) {
-            if (new_scales) {
-              cache_g = g;
+            cache_g = g;
+            page_next = page_of(pg0 + 32);
+            asked = false;
+            if constexpr (F8) {
               fine = sk > 0.f && sk < INFINITY && sv >= kMinValueScale && sv < INFINITY;
               ks = sk;
               vl = fine ? log2f(sv) : 0.f;
               vi = fine ? 1.f / sv : 0.f;
             }
-            const uint32_t all = __ballot_sync(kAll, fine);
-            const bool good = there && ((all >> at) & 1u);
-            if (there && !good) flag |= kDevBadArg;  // no scale of a written page: keys skipped
-            use = __ballot_sync(kAll, good);
-            const float k_of = __shfl_sync(kAll, ks, at), l_of = __shfl_sync(kAll, vl, at),
-                        i_of = __shfl_sync(kAll, vi, at);
-            if (lane < n_pieces)  // pieces that are not used stay neutral
-              meta.scale[lane] = good ? make_float4(k_of, l_of, i_of, 0.f) : make_float4(1.f, 0.f, 0.f, 0.f);
+          } else if (F8 && !asked) {
+            scales_of(page_next, sk_next, sv_next);
+            asked = true;
           }
-          if (flag && p.dev_status != nullptr) atomicOr(p.dev_status, flag);
+          // Lane cache's page that is piece k of the tile: keys [a, a + piece)
+          const int k = lane - (pg0 - cache_at), a = key0 + k * piece;
+          const bool seen = k >= 0 && k < n_pieces && a < r.L && (a + piece > r.lo || a < r.sinks);
+          const bool there = seen && page >= 0;
+          const uint32_t sent = __ballot_sync(kAll, there);
+          const uint32_t use = (F8 ? __ballot_sync(kAll, there && fine) : sent) >> (pg0 - cache_at);
+          const uint32_t full_k = smem_u32(&bar_k[st]), full_v = smem_u32(&bar_v[st]);
+          const uint32_t bytes = __popc(sent) * piece * C::kRowBytes;
+          const int slab = page * p.hkv + g;
+          auto load = [&](uint32_t to, const CUtensorMap* map, uint32_t bar) {
+            if (there) {
+#pragma unroll
+              for (int pn = 0; pn < C::kPanels; ++pn)
+                tma_load_3d(to + pn * TK * PB + k * piece * PB, map, bar, pn * 64, 0, slab);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          };
+          if (it >= S) {
+            ok = wait_for(smem_u32(&bar_k_empty[st]), slot.odd ^ 1, abort_flag);
+            if (!ok) break;
+          }
+          load(sK(st), &map_k, full_k);
+          Meta<C::kPieces>& meta = s_meta[mslot.at];
+          if constexpr (F8) {
+            if (k >= 0 && k < n_pieces)  // pieces that are not used stay neutral
+              meta.scale[k] = there && fine ? make_float4(ks, vl, vi, 0.f) : make_float4(1.f, 0.f, 0.f, 0.f);
+          }
+          if (seen && !(there && fine) && p.dev_status != nullptr)  // or no scale of a written page
+            atomicOr(p.dev_status, there ? kDevBadArg : kDevIndexRange);
           if (lane == 0) {
             meta.key0 = key0;
             meta.ok = use;
@@ -584,25 +604,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                          (p.window == 0 || key0 >= clear_lo || key0 + TK <= p.sinks);
           }
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_u32(&bar_meta[mslot.at]));
-            mbar_arrive_expect_tx(smem_u32(&bar_k[st]), bytes);
+          if (lane == 0) mbar_arrive(smem_u32(&bar_meta[mslot.at]));
+          if (it >= S) {
+            ok = wait_for(smem_u32(&bar_v_empty[st]), slot.odd ^ 1, abort_flag);
+            if (!ok) {
+              if (lane == 0) mbar_arrive(full_v);  // nothing is on its way
+              ++it;
+              break;
+            }
           }
-          bool v_ok = true;
-          if (it >= S) v_ok = wait_for(smem_u32(&bar_v_empty[st]), slot.odd ^ 1, abort_flag);
-          if (v_ok && there) {
-#pragma unroll
-            for (int pn = 0; pn < C::kPanels; ++pn)
-              tma_load_3d(sV(st) + pn * TK * PB + lane * piece * PB, &map_v, smem_u32(&bar_v[st]),
-                          pn * 64, row, slab);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bar_v[st]), v_ok ? bytes : 0);
-          if (!v_ok) {
-            ok = false;
-            ++it;
-            break;
-          }
+          load(sV(st), &map_v, full_v);
         }
         if (left > 0 && ++rt == r.rt) {
           rt = 0;
@@ -658,11 +669,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<S> kslot, vslot;   // of the next tile whose S, whose P V is issued
       uint32_t wide_at = 0;   // e4m3: its widened V
       uint32_t odd_p[2] = {0, 0}, odd_q = 0;  // parities of the phases waited for next
-      Part q;
       bool ok = true;
-      while (ok && next_part(q)) {
-        const bool alt = !kTwo || q.rows <= kRows;
-        const int J = alt ? q.T : 2 * q.T;
+      while (ok && next_part()) {
+        const bool alt = !kTwo || s_part[pslot.at].rows <= kRows;
+        const int J = alt ? s_part[pslot.at].T : 2 * s_part[pslot.at].T;
+        part_done();
         // the q tiles are written, and the sums of the part before have been read
         ok = wait_for(smem_u32(&bar_q), odd_q, abort_flag);
         odd_q ^= 1;
@@ -694,21 +705,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             issue_o(w, v, true, std::integral_constant<int, 1>());
             odd_p[w] ^= 1;
-          }
-          if (qk) {
-            issue_s(w, alt ? 0 : w, kslot.at);
-            // One commit a step (each takes the issuer 200 cycles): who sees it hands back K's slot and that
-            // of the V two jobs before.
-            mma_commit_elect(smem_u32(&bar_s[w]), e);
-            if (alt || w == 1) kslot.next();
-          }
-          if (pv) {
             if (alt || w == 1) {
+              if (!F8) mma_commit_elect(smem_u32(&bar_v_empty[vslot.at]), e);
               vslot.next();
               wide_at ^= 1;
             }
-            if (i >= J) mma_commit_elect(smem_u32(&bar_o[w]), e);
           }
+          if (qk) {
+            issue_s(w, alt ? 0 : w, kslot.at);
+            // who sees it hands K back, and widens the next V
+            mma_commit_elect(smem_u32(&bar_s[w]), e);
+            if (alt || w == 1) kslot.next();
+          }
+          if (pv && i >= J) mma_commit_elect(smem_u32(&bar_o[w]), e);
           return true;
         };
         for (int i = 0; ok && i < J + 2; i += 2)
@@ -722,9 +731,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<S> slot;
       Ring<C::kMeta> mslot;
       uint32_t wide_at = 0, odd_s[2] = {0, 0};  // e4m3: the widened V, parities of the next scores
-      Part q;
       bool ok = true;
-      while (ok && next_part(q)) {
+      while (ok && next_part()) {
+        const Part q = s_part[pslot.at];
+        part_done();
         const bool alt = !kTwo || q.rows <= kRows;
         // new tokens that some token sees, and the first key of the windows
         const uint64_t here = present(q.n, q.base);
@@ -744,8 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kept = min(p.sinks, lo);
         for (int x = 0; x < q.T; ++x, slot.next(), mslot.next(), wide_at ^= 1) {
           const int st = slot.at;
-          // (K's barrier may be a tile's phase further; V's slot waits for this warp)
-          ok = wait_for(smem_u32(&bar_v[st]), slot.odd, abort_flag);
+          ok = wait_for(smem_u32(&bar_v[st]), slot.odd, abort_flag);  // and the tile's description written
           // e4m3: with the tile's own scores (the first of them) the products with the V two tiles before
           // are complete, whose place this one takes; the next scores of that warpgroup wait for it.
           if constexpr (F8) {
@@ -829,9 +838,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // q tiles, the part before
     uint32_t odd_s = 0, odd_o = 0, odd_other = 0, odd_ml = 0, odd_q = 0, odd_done = 0;
     bool first = true;  // part
-    Part q;
     bool ok = true;
-    while (ok && next_part(q)) {
+    while (ok && next_part()) {
+      const Part& q = s_part[pslot.at];
       const bool alt = !kTwo || q.rows <= kRows;
       // ---- q tiles, by both warpgroups: D / 16 lanes to a row, 16 values each
       {
@@ -906,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- this thread's q row: position, mask, factor of its scores
       const int row = lane_row + (alt ? 0 : w * kRows);
-      const bool in = row < q.rows;
+      const bool in = row < q.rows, live = row - lane < q.rows;
       uint64_t mask = 0;
       if (in)
         mask = p.mask[q.q0 + (q.row0 + row) / p.group] & (q.n >= 64 ? ~0ull : (1ull << q.n) - 1);
@@ -921,18 +930,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       odd_q ^= 1;
       float m_ref = -INFINITY, l = 0.f;
-      int v_before = 0;  // slot of the job before
       for (int j = 0; j < q.T; ++j, mslot.next(), kslot.next()) {  // tile of the part
         if (alt && (j & 1) != w) continue;
         ok = wait_for(smem_u32(&bar_meta[mslot.at]), mslot.odd, abort_flag) &&
              wait_for(smem_u32(&bar_s[w]), odd_s, abort_flag);
         if (!ok) break;
         odd_s ^= 1;
-        if (lane_row == 0 && (alt || w == 1)) {
-          mbar_arrive(smem_u32(&bar_k_empty[kslot.at]));
-          // the product of this warpgroup's job before is complete, too
-          if (!F8 && j > (alt ? w : 0)) mbar_arrive(smem_u32(&bar_v_empty[v_before]));
-          v_before = kslot.at;
+        if (lane_row == 0 && (alt || w == 1)) mbar_arrive(smem_u32(&bar_k_empty[kslot.at]));
+        if (!live) {  // no row of this warp is one of the unit's: what its lanes hold is never read
+          mbar_arrive(smem_u32(&bar_half[w]));
+          mbar_arrive(smem_u32(&bar_p[w]));
+          continue;
         }
         tc_fence_after();
         const Meta<C::kPieces>& meta = s_meta[mslot.at];
@@ -1094,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quad = final ? 4 : 4 * C::kUnitRows;  // from four columns to the next
         uint16_t* to16 = static_cast<uint16_t*>(p.out) + at * D;
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        for (int c0 = 0; live && c0 < D; c0 += 32) {
           uint32_t o[32];
           tmem_ld32(tmem + 256 + w * 128 + lane_off + c0, o);
           tmem_ld_wait();
@@ -1133,8 +1141,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.job_q0[blockIdx.x] = q.q0;
         }
       }
-      if (!F8 && lane_row == 0 && (alt ? q.T > w : w == 1)) mbar_arrive(smem_u32(&bar_v_empty[v_before]));
       mbar_arrive(smem_u32(&bar_done));
+      part_done();
     }
   }
   tc_fence_before();
@@ -1292,7 +1300,7 @@ cudaError_t launch(const AttnDecodeArgs& a, int dev, int sms, int* drv_err, cuda
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.page_size, (uint64_t)a.num_pages * a.hkv};
     const uint64_t strides[2] = {(uint64_t)C::kRowBytes, (uint64_t)C::kRowBytes * a.page_size};
     const uint32_t box[3] = {(uint32_t)(F8 ? D : 64),
-                             (uint32_t)(a.page_size < C::kTK ? a.page_size : C::kTK), 1};
+                             (uint32_t)a.page_size, 1};  // pages have 128 tokens at most
     const CUresult e = encode_tensor_map(
         m, F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims,
         strides, box, C::kPanelBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
