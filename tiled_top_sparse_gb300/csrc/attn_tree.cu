@@ -47,7 +47,7 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kThreads = 384;
 constexpr int kRows = 128;  // q rows of a tile (TMEM lanes)
 // What the end of a unit costs (joining, the next unit's q), in tiles of the list.
-constexpr int kEndTiles = 3;
+constexpr int kEndTiles = 8;
 constexpr int kParts = 4;   // parts of a run that are described ahead
 constexpr int kMinRun = 2;  // places of a run at least: a tile for each warpgroup
 constexpr float kMinValueScale = 0x1p-80f;  // as in attn_decode.cu
