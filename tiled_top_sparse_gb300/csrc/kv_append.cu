@@ -64,16 +64,23 @@ __device__ __forceinline__ void load_turn(const float* __restrict__ cs, Turn& t)
 }
 // The same with explicit positions: pair j turns by the table's row at the token's position on axis
 // pair_axis[j] (two bits a pair). False, and no turn, where a position lies outside the table.
-template <int D>
-__device__ __forceinline__ bool load_turn_axes(const KvAppendArgs& p, int64_t tok, int c, Turn& t) {
-  int pos[4];
-  bool ok = true;
+struct Positions {
+  int at[4];
+};
+__device__ __forceinline__ void load_positions(const KvAppendArgs& p, int64_t tok, Positions& pos) {
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
-    pos[a] = 0;
-    if (a < p.axes) pos[a] = __ldg(p.positions + a * p.total_new + tok);
-    ok = ok && pos[a] >= 0 && pos[a] < p.max_pos;
+    pos.at[a] = 0;
+    if (a < p.axes) pos.at[a] = __ldg(p.positions + a * p.total_new + tok);
   }
+}
+template <int D>
+__device__ __forceinline__ bool load_turn_axes(const KvAppendArgs& p, const Positions& from, int c,
+                                               Turn& t) {
+  const int(&pos)[4] = from.at;
+  bool ok = true;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) ok = ok && pos[a] >= 0 && pos[a] < p.max_pos;
   const uint32_t axis = (uint32_t)(p.pair_axis[c >> 2] >> ((c & 3) * 16)) & 0xFFFFu;
   auto row = [&](uint32_t a) -> const float* {  // pairs [8c, 8c + 8) at the position on axis a
     const int at = !ok ? 0 : a & 2 ? (a & 1 ? pos[3] : pos[2]) : (a & 1 ? pos[1] : pos[0]);
@@ -206,9 +213,13 @@ __device__ __forceinline__ void append_page(const KvAppendArgs& p, int b, const 
   const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v : p.k) + (int64_t)g * D + c * 8;
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
   uint4 raw[kPasses][2];
+  [[maybe_unused]] Positions pos[kAxes ? kPasses : 1];
 #pragma unroll
   for (int s = 0; s < kPasses; ++s) {
     const int row = s * rows_per + row_in;
+    if constexpr (kAxes) {
+      if (!is_v && row < nr) load_positions(p, tok0 + row, pos[s]);
+    }
     raw[s][0] = raw[s][1] = make_uint4(0, 0, 0, 0);
     if (row < nr) {
       const uint16_t* at = src + (tok0 + row) * stride;
@@ -244,7 +255,7 @@ __device__ __forceinline__ void append_page(const KvAppendArgs& p, int b, const 
     if constexpr (kAxes) {
       if (!is_v && row < nr && r.ok) {
         Turn t;
-        if (load_turn_axes<D>(p, tok0 + row, c, t)) {
+        if (load_turn_axes<D>(p, pos[s], c, t)) {
           rotate(a, bb, t);
         } else {  // a position outside the table: reported, and the key is zeros
 #pragma unroll
@@ -349,9 +360,11 @@ constexpr int kQHeads = 8;  // q heads that share one load of the table row
 // bounds the kernel is how many rows are on their way (28,000 tokens in pages of 128: 75 -> 55 us,
 // of 16 to 32: 58 -> 53 us; pages of 64 in blocks of 512 threads instead of 256: 50 -> 64 us), and
 // that outweighs what it spills: 20 bytes a thread where a page takes one pass, 44 to 52 where it
-// takes two, none at 64 registers.
+// takes two, none at 64 registers. With explicit positions a page of two passes holds two rows' more of
+// them: 220 to 250 bytes of spills at 48 registers, none at 64 and four blocks per SM (26,800 prompt tokens
+// into e4m3 pages of 64 123 -> 119 us, trees of 25 to 64 tokens 7.9 -> 7.2; pages of one pass 107 -> 112).
 template <int D, bool kF8, int kPasses, int kMost, bool kAxes>
-__global__ void __launch_bounds__(kMost, kMost == 256 ? 5 : 2) append_pages_kernel(const KvAppendArgs p,
+__global__ void __launch_bounds__(kMost, kMost == 256 ? (kAxes && kPasses == 2 ? 4 : 5) : 2) append_pages_kernel(const KvAppendArgs p,
                                                            uint64_t q_share, int q_shift,
                                                            int q_groups) {
   constexpr int kTpr = D / 16;
@@ -382,10 +395,13 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 5 : 2) append_pages_kern
   if (i < 0 || i >= r.n) return;  // i < 0: units in front of a first bound above 0
   Turn t;
   bool ok = r.ok;
-  if constexpr (kAxes)
-    ok = ok && load_turn_axes<D>(p, r.t0 + i, c, t);
-  else if (p.cos_sin != nullptr && r.ok)
+  if constexpr (kAxes) {
+    Positions pos;
+    load_positions(p, r.t0 + i, pos);
+    ok = ok && load_turn_axes<D>(p, pos, c, t);
+  } else if (p.cos_sin != nullptr && r.ok) {
     load_turn(p.cos_sin + ((r.past + i) * (D / 2) + c * 8) * 2, t);
+  }
   const int h1 = h0 + kQHeads < p.hq ? h0 + kQHeads : p.hq;
 #pragma unroll 8
   for (int h = h0; h < h1; ++h) rotate_q_row<D>(p, ok, r.t0 + i, h, c, t);
@@ -424,10 +440,13 @@ __global__ void __launch_bounds__(128) append_steps_kernel(const KvAppendArgs p,
   const int c = lane % kTpr;
   Turn t;
   bool ok = r.ok;
-  if constexpr (kAxes)
-    ok = ok && load_turn_axes<D>(p, r.t0 + i, c, t);
-  else if (p.cos_sin != nullptr && r.ok)
+  if constexpr (kAxes) {
+    Positions pos;
+    load_positions(p, r.t0 + i, pos);
+    ok = ok && load_turn_axes<D>(p, pos, c, t);
+  } else if (p.cos_sin != nullptr && r.ok) {
     load_turn(p.cos_sin + (((int64_t)r.past + i) * (D / 2) + c * 8) * 2, t);
+  }
   rotate_q_row<D>(p, ok, r.t0 + i, h, c, t);
 }
 

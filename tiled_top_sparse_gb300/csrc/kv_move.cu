@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
   const bool is_v = hh >= p.hkv;
   const int h = is_v ? hh - p.hkv : hh;
   const bool first = hh == 0;  // reports, and writes the length
+  float* const scales = is_v ? p.scale[1] : p.scale[0];
   const int past = p.past[r];
   int m = p.path_lens[r];
   int at[2];  // path of rows lane and lane + 32
@@ -106,7 +107,6 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
   const int f = __popc(same0) + __popc(same1);  // strictly increasing: they come first
   if (f == m) return;
   const int slots = 1 << p.page_shift;
-  const int page0 = (past + f) >> p.page_shift;  // first page that rows are moved into
   int64_t from[2], to[2];                        // cache rows, -1: this row is not moved
   [[maybe_unused]] float s_from[2] = {1.f, 1.f}, s_to[2] = {1.f, 1.f};
 #pragma unroll
@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
     }
     const int64_t ss = (int64_t)ps * p.hkv + h, sd = (int64_t)pd * p.hkv + h;
     if constexpr (kF8) {
-      s_from[k] = p.scale[is_v][ss];
-      s_to[k] = p.scale[is_v][sd];
+      s_from[k] = scales[ss];
+      s_to[k] = scales[sd];
       if (!(s_from[k] > 0.f && s_from[k] < INFINITY)) {  // no scale a cached row can have
         bad |= kDevBadArg;
         continue;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
     to[k] = (sd << p.page_shift) + (dst & (slots - 1));
   }
   if (bad && p.dev_status != nullptr) atomicOr(p.dev_status, bad);
-  uint4* const rows = reinterpret_cast<uint4*>(p.cache[is_v]);
+  uint4* const rows = reinterpret_cast<uint4*>(is_v ? p.cache[1] : p.cache[0]);
   auto row64 = [&](const int64_t (&x)[2], int i) -> int64_t {  // x of row i (lane-varying)
     const int64_t a = __shfl_sync(kAll, x[0], i & 31), b = __shfl_sync(kAll, x[1], i & 31);
     return i < 32 ? a : b;
@@ -147,9 +147,13 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
     const float a = __shfl_sync(kAll, x[0], i & 31), b = __shfl_sync(kAll, x[1], i & 31);
     return i < 32 ? a : b;
   };
-  for (int b0 = f; b0 < m; b0 += kBatchRows) {
-    const int pieces = min(m - b0, kBatchRows) * kCpr;
+  // e4m3: page by page. A later page's sources lie behind this page, so that its codes may move to a new
+  // scale once the rows that come into it are read.
+  for (int b0 = f, b1; b0 < m; b0 = b1) {
+    b1 = min(m, kF8 ? (((past + b0) >> p.page_shift) + 1 << p.page_shift) - past : b0 + kBatchRows);
+    const int pieces = (b1 - b0) * kCpr;
     uint4 held[kHold];
+    float top = 0.f;  // largest value that comes into the page
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
       held[k] = make_uint4(0, 0, 0, 0);
@@ -159,54 +163,30 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
       if (x < pieces && src >= 0) held[k] = rows[src * kCpr + x % kCpr];
     }
     __syncwarp();  // all rows are read before any is written
+    [[maybe_unused]] float scale = 1.f;
     if constexpr (kF8) {
-      // pages of this head that rows are moved into: 64 rows touch five pages of 16 at most
-      float page_scale[5];
-      const int pages = ((past + m - 1) >> p.page_shift) - page0 + 1;
 #pragma unroll
-      for (int g = 0; g < 5; ++g) {
-        page_scale[g] = 1.f;
-        if (g >= pages) continue;
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < kHold; ++k) {
-          if (k * 32 >= pieces) continue;
-          const int i = b0 + (k * 32 + lane) / kCpr;
-          const float s = rowf(s_from, i);
-          if (k * 32 + lane < pieces && ((past + i) >> p.page_shift) - page0 == g)
-            top = fmaxf(top, amax16(held[k]) * s);
+      for (int k = 0; k < kHold; ++k)
+        if (k * 32 < pieces) {
+          const float s = rowf(s_from, b0 + (k * 32 + lane) / kCpr);
+          top = fmaxf(top, amax16(held[k]) * s);  // rows that are not moved are held as zeros
         }
-        top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(top)));
-        // the page's first moved row that is there tells the page
-        const int lo = max(f, ((page0 + g) << p.page_shift) - past);
-        const int hi = min(m, ((page0 + g + 1) << p.page_shift) - past);
-        const uint32_t in0 = __ballot_sync(kAll, lane >= lo && lane < hi && to[0] >= 0);
-        const uint32_t in1 = __ballot_sync(kAll, lane + 32 >= lo && lane + 32 < hi && to[1] >= 0);
-        if ((in0 | in1) == 0) continue;
-        const int i = in0 ? __ffs(in0) - 1 : 31 + __ffs(in1);
-        const int64_t dst = row64(to, i);
-        const float old = rowf(s_to, i);
-        if (top <= 448.f * old && old > 0.f) {
-          page_scale[g] = old;
-          continue;
-        }
-        page_scale[g] = block_scale(top);
-        uint4* slab = rows + (dst >> p.page_shift << p.page_shift) * kCpr;
+      top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(top)));
+      // a row that is moved tells the page
+      const uint32_t in0 = __ballot_sync(kAll, lane >= b0 && lane < b1 && to[0] >= 0);
+      const uint32_t in1 = __ballot_sync(kAll, lane + 32 >= b0 && lane + 32 < b1 && to[1] >= 0);
+      if ((in0 | in1) == 0) continue;
+      const int i = in0 ? __ffs(in0) - 1 : 31 + __ffs(in1);
+      const int64_t slab = row64(to, i) >> p.page_shift;
+      const float old = rowf(s_to, i);
+      scale = old;
+      if (!(old > 0.f && top <= 448.f * old)) {
+        scale = block_scale(top);
+        uint4* at = rows + (slab << p.page_shift) * kCpr;
         if (old > 0.f)
-          for (int x = lane; x < slots * kCpr; x += 32)
-            slab[x] = rescale16(slab[x], old / page_scale[g]);
-        if (lane == 0) p.scale[is_v][dst >> p.page_shift] = page_scale[g];
-      }
-      __syncwarp();  // rows are written over a page that has its new codes
-#pragma unroll
-      for (int k = 0; k < kHold; ++k) {
-        if (k * 32 >= pieces) continue;
-        const int i = b0 + (k * 32 + lane) / kCpr, g = ((past + i) >> p.page_shift) - page0;
-        const float s = rowf(s_from, i);
-        float t = page_scale[0];
-#pragma unroll
-        for (int u = 1; u < 5; ++u) t = g == u ? page_scale[u] : t;
-        if (s != t) held[k] = rescale16(held[k], s / t);
+          for (int x = lane; x < slots * kCpr; x += 32) at[x] = rescale16(at[x], old / scale);
+        if (lane == 0) scales[slab] = scale;
+        __syncwarp();  // rows are written over a page that has its new codes
       }
     }
 #pragma unroll
@@ -214,6 +194,10 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
       if (k * 32 >= pieces) continue;
       const int x = k * 32 + lane;
       const int64_t dst = row64(to, b0 + x / kCpr);
+      if constexpr (kF8) {
+        const float s = rowf(s_from, b0 + x / kCpr);
+        if (s != scale) held[k] = rescale16(held[k], s / scale);
+      }
       if (x < pieces && dst >= 0) rows[dst * kCpr + x % kCpr] = held[k];
     }
     __syncwarp();
@@ -224,7 +208,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
 // New request i continues request parents[i]: its table row is the parent's up to the last full
 // page, its last, partly filled page is new_pages[i] with the parent's rows (and scales) in it.
 //
-// A block per (new request, K or V of a head) copies the used rows of one page, one more per request
+// A block per (new request, head) copies the used rows of a page's K and V, one more per request
 // writes the table row and the length.
 struct ForkParams {
   uint4* cache[2];
@@ -243,7 +227,7 @@ constexpr int kForkThreads = 128;
 __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) {
   wait_for_prior_grids();
   const int tid = threadIdx.x;
-  const int i = (int)(blockIdx.x / (2 * p.hkv + 1)), part = (int)(blockIdx.x % (2 * p.hkv + 1));
+  const int i = (int)(blockIdx.x / (p.hkv + 1)), part = (int)(blockIdx.x % (p.hkv + 1));
   const int parent = p.parents[i];
   const int fresh = p.new_pages[i];
   uint32_t bad = 0;
@@ -261,7 +245,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
   const int32_t* old = p.page_tables + (int64_t)(bad ? 0 : parent) * p.max_pages;
   if (fresh >= p.num_pages) bad |= kDevIndexRange;
   const bool own = fresh >= 0 && fresh < p.num_pages;  // else the parent's row is shared whole
-  if (part == 2 * p.hkv) {
+  if (part == p.hkv) {
     int32_t* t = p.tables_out + (int64_t)i * p.max_pages;
     const bool none = parent < 0 || parent >= p.batch || (bad && len == 0);
     for (int x = tid; x < p.max_pages; x += kForkThreads) {
@@ -285,27 +269,33 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
   if (bad || !own || used == 0) return;
   const int src = old[full];
   if (src < 0 || src >= p.num_pages || src == fresh) return;
-  const bool is_v = part >= p.hkv;
-  const int h = is_v ? part - p.hkv : part;
-  const int64_t from = (int64_t)src * p.hkv + h, to = (int64_t)fresh * p.hkv + h;
-  const uint4* a = p.cache[is_v] + (from << p.page_shift) * p.cpr;
-  uint4* b = p.cache[is_v] + (to << p.page_shift) * p.cpr;
+  const int64_t from = (int64_t)src * p.hkv + part, to = (int64_t)fresh * p.hkv + part;
+  const int64_t at_from = (from << p.page_shift) * p.cpr, at_to = (to << p.page_shift) * p.cpr;
+  if (tid == 0 && p.scale[0] != nullptr) {
+    p.scale[0][to] = p.scale[0][from];
+    p.scale[1][to] = p.scale[1][from];
+  }
   const int n = used * p.cpr;
-  constexpr int kDeep = 8;
+  constexpr int kDeep = 4;
   for (int x0 = 0; x0 < n; x0 += kForkThreads * kDeep) {
-    uint4 v[kDeep];
+    uint4 v[2][kDeep];
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
       const int x = x0 + k * kForkThreads + tid;
-      if (x < n) v[k] = a[x];
+      if (x < n) {
+        v[0][k] = p.cache[0][at_from + x];
+        v[1][k] = p.cache[1][at_from + x];
+      }
     }
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
       const int x = x0 + k * kForkThreads + tid;
-      if (x < n) b[x] = v[k];
+      if (x < n) {
+        p.cache[0][at_to + x] = v[0][k];
+        p.cache[1][at_to + x] = v[1][k];
+      }
     }
   }
-  if (tid == 0 && p.scale[is_v] != nullptr) p.scale[is_v][to] = p.scale[is_v][from];
 }
 
 int log2_of(int x) {
@@ -365,7 +355,7 @@ cudaError_t launch_kv_fork(const KvForkArgs& a, cudaStream_t stream) {
   p.max_pages = a.max_pages;
   p.batch = a.batch;
   p.cpr = a.cache.d * (a.cache.f8 ? 1 : 2) / 16;
-  const int64_t blocks = (int64_t)a.children * (2 * a.cache.hkv + 1);
+  const int64_t blocks = (int64_t)a.children * (a.cache.hkv + 1);
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   return launch_ahead(fork_kernel, dim3((unsigned)blocks), kForkThreads, 0, stream, p);
 }
