@@ -270,7 +270,7 @@ __device__ __forceinline__ Req load_req(const Params& p, int b, uint32_t* bad) {
 }
 // Places of the list that a tile of a request's last row block takes: two where it has more than 128
 // rows, which both warpgroups then go through (ragged trees of up to 155 rows, window 4096: 67 us
-// with one place each, XX with two).
+// with one place each, 53 with two).
 __device__ __forceinline__ int last_weight(const Params& p, int n, int unit_rows) {
   const int rows = n * p.group;
   return (rows - 1) % unit_rows >= kRows ? 2 : 1;
@@ -937,6 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         odd_s ^= 1;
         if (lane_row == 0 && (alt || w == 1)) mbar_arrive(smem_u32(&bar_k_empty[kslot.at]));
+        __syncwarp();  // TMEM is read by converged warps
         if (!live) {  // no row of this warp is one of the unit's: what its lanes hold is never read
           mbar_arrive(smem_u32(&bar_half[w]));
           mbar_arrive(smem_u32(&bar_p[w]));
@@ -1000,6 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= alpha;
           m_ref = tile_max;
         }
+        __syncwarp();
         const float shift = m_ref == -INFINITY ? 0.f : kBias - m_ref;
         // ---- weights, packed in place
 #pragma unroll
@@ -1115,19 +1117,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), f1, v[i]);
           }
-          if (!in) continue;
-          if (final && p.out_bf16) {
+          if (in) {
+            if (final && p.out_bf16) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(to16 + c0 + i) =
-                  make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
-                             pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
-          } else {
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(to16 + c0 + i) =
+                    make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
+                               pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(to32 + (c0 + i) / 4 * quad) =
-                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(to32 + (c0 + i) / 4 * quad) =
+                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
           }
+          __syncwarp();
         }
         if (in) {
           if (!final)
