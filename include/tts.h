@@ -462,7 +462,7 @@ tts_status tts_rope_kv_append_axes(
  * path       device int32 [batch, max_path], max_path 0 .. 64 (else TTS_ERR_UNSUPPORTED); entries
  *            behind a request's m may be anything
  * path_lens  device int32 [batch]
- * kv_lens    device int32 [batch], written; must not overlap past_lens
+ * kv_lens    device int32 [batch], written; must not overlap the other arguments
  * A request whose m is outside [0, max_path] or whose path does not increase from 0 on sets
  * TTS_DEV_BAD_ARG; one with rows outside [0, max_pages * page_size) sets TTS_DEV_INDEX_RANGE.
  * Nothing of either is moved, and its kv_lens is its past_lens (0 where that is negative). A row
@@ -494,7 +494,7 @@ tts_status tts_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v
  *
  * k_cache .. page_tables, max_pages: as tts_rope_kv_append; page_tables [batch, max_pages] and
  * kv_lens [batch] are read, tables_out int32 [children, max_pages] and lens_out int32 [children]
- * written (neither may overlap its input); parents, new_pages device int32 [children].
+ * written (neither may overlap another argument); parents, new_pages device int32 [children].
  * new_pages must be different pages that no request uses (what they hold is unspecified
  * otherwise). A parent outside [0, batch) or a length outside [0, max_pages * page_size] sets
  * TTS_DEV_INDEX_RANGE: length 0, a row of -1. A new page >= num_pages sets it too (entries from
@@ -578,8 +578,8 @@ tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* 
  * A token without a visible key gets out = 0, lse = -inf (padding: an empty mask, in a request
  * that has new tokens only).
  *
- * tree_mask   device uint64 [total_q]; bits from n on are not looked at
- * Cached values that some new token sees must be finite; of the keys that none sees, any may hold
+ * tree_mask   device uint64 [total_q], 8-byte aligned; bits from n on are not looked at
+ * q must be finite. Cached values that some new token sees must be finite; of the keys that none sees, any may hold
  * anything (a drafted token that no mask has, keys hidden by the window, rows behind the
  * last token). With a window, pages of keys from L - n + 1 - window on and of the first `sinks` are
  * read. Products: e4m3 keys by q as the sum of two e4m3 values after a power-of-two row scaling (exact

@@ -295,6 +295,29 @@ def test_many_requests(tts):
     Case(42, new, kv, 4, 1, 128, 16, False, 60, 2).check(tts)
 
 
+@pytest.mark.parametrize("f8", [True, False])
+def test_more_requests_than_threads(tts, f8):
+    """The list of tiles is added up in rounds of the block's threads."""
+    rng = np.random.default_rng(47)
+    new = [int(x) for x in rng.integers(0, 4, 900)]
+    kv = [int(x) + n for x, n in zip(rng.integers(0, 150, 900), new)]
+    new[-1], kv[-1], new[400], kv[400] = 3, 900, 40, 300
+    Case(47, new, kv, 2, 1, 64, 16, f8).check(tts)
+
+
+def test_scales_that_are_no_powers_of_two(tts):
+    c = Case(53, [20, 3], [700, 90], 8, 2, 128, 16, True)
+    rng = np.random.default_rng(1)
+    c.s = [torch.tensor(np.exp(rng.uniform(-9, 1, t.shape)), dtype=torch.float32) for t in c.s]
+    c.check(tts)
+
+
+def test_a_large_group(tts):
+    """16 q heads per KV head and 64 tokens: four row blocks of each KV head."""
+    Case(59, [64, 1, 33], [500, 200, 33], 16, 1, 64, 32, True).check(tts)
+    Case(61, [64], [900], 32, 1, 128, 64, False, 300, 5).check(tts)
+
+
 def test_random_calls(tts):
     rng = np.random.default_rng(43)
     for i in range(40):

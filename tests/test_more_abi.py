@@ -67,6 +67,7 @@ def test_tree_refusals(L):
         assert tree(L, **{n: NUL}) == tts.TTS_ERR_INVALID_ARG, n
     for n in ("q", "kc", "vc", "out"):
         assert tree(L, **{n: B}) == tts.TTS_ERR_INVALID_ARG, n
+    assert tree(L, mask=ctypes.c_void_p(0x10004)) == tts.TTS_ERR_INVALID_ARG
     for kw in (dict(total=-1), dict(batch=0), dict(max_q=0), dict(hkv=3), dict(window=-1),
                dict(sinks=-1), dict(scale=0.0), dict(scale=float("nan")), dict(dt=1), dict(odt=2),
                dict(cu=NUL, total=1)):
@@ -116,6 +117,7 @@ def test_move_sizes(L):
     assert compact(L, max_path=65) == tts.TTS_ERR_UNSUPPORTED
     assert compact(L, lens=A) == tts.TTS_ERR_INVALID_ARG  # in place of past_lens
     assert fork(L, children=-1) == tts.TTS_ERR_INVALID_ARG
+    assert compact(L, lens=A, past=ctypes.c_void_p(0x30000)) == tts.TTS_ERR_INVALID_ARG  # of path_lens
     assert fork(L, to=A) == tts.TTS_ERR_INVALID_ARG and fork(L, tl=A) == tts.TTS_ERR_INVALID_ARG
     assert fork(L, children=0, parents=NUL, new=NUL) == tts.TTS_OK
 

@@ -598,7 +598,8 @@ tts_status tts_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v
   if (st != TTS_OK) return st;
   if (max_path > kDecodeMaxQ) return TTS_ERR_UNSUPPORTED;
   if (page_tables == nullptr || past_lens == nullptr || path_lens == nullptr ||
-      kv_lens == nullptr || (path == nullptr && max_path > 0) || kv_lens == past_lens)
+      kv_lens == nullptr || (path == nullptr && max_path > 0) || kv_lens == past_lens ||
+      kv_lens == path_lens || kv_lens == path)
     return TTS_ERR_INVALID_ARG;
   a.page_tables = page_tables;
   a.max_pages = max_pages;
@@ -627,7 +628,7 @@ tts_status tts_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_sc
   if (children == 0) return TTS_OK;  // nothing to write
   if (page_tables == nullptr || kv_lens == nullptr || parents == nullptr || new_pages == nullptr ||
       tables_out == nullptr || lens_out == nullptr || tables_out == page_tables ||
-      lens_out == kv_lens)
+      lens_out == kv_lens || lens_out == parents || lens_out == new_pages)
     return TTS_ERR_INVALID_ARG;
   a.page_tables = page_tables;
   a.max_pages = max_pages;
@@ -691,14 +692,14 @@ static tts_status attn_decode(bool tree, const void* q, int64_t total_q,
       (int64_t)max_seqlen_q * num_heads_q > 0x7FFFFFFFLL)
     return TTS_ERR_UNSUPPORTED;
   // tiles of 32 keys and a few places more per unit, a unit per KV head and 8 q rows, counted in
-  // 32 bits
+  // 32 bits (trees have fewer units and tiles, and more places behind each)
   const double tiles = (double)batch * num_heads_kv *
                        ((double)max_seqlen_q * (num_heads_q / num_heads_kv) / 8 + 1) *
-                       ((double)max_pages * page_size / 32 + 6);
+                       ((double)max_pages * page_size / 32 + (tree ? 12 : 6));
   if (tiles > 2e9) return TTS_ERR_UNSUPPORTED;
   if (total_q == 0) return TTS_OK;  // nothing to compute
   if (q == nullptr || k_cache == nullptr || v_cache == nullptr || page_tables == nullptr ||
-      kv_lens == nullptr || out == nullptr || (tree && tree_mask == nullptr))
+      kv_lens == nullptr || out == nullptr || (tree && (tree_mask == nullptr || (reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0)))
     return TTS_ERR_INVALID_ARG;
   if (cache_dtype == TTS_E4M3 && (k_scale == nullptr || v_scale == nullptr))
     return TTS_ERR_INVALID_ARG;
