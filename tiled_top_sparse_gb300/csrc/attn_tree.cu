@@ -1158,43 +1158,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the units that CTA borders cut: block (c, y, z) for rows 32 y .. of the unit that
-// ended in CTA c, columns 32 z .. . A lane is a row; warps are four groups of parts by two groups of 16
-// columns, a group takes every fourth part, two at a time, and the groups' sums are joined in
-// order through shared memory, from where rows leave.
+// Joins the parts of the units that CTA borders cut: block (c, y) for rows 32 y .. of the unit that
+// ended in CTA c. A lane is a row, a warp 16 columns (the parts lie so that a warp reads whole lines), kBatch
+// parts' loads are in flight, and each lane writes whole sectors. The parts are joined in the
+// list's order.
 template <int D>
-__global__ void __launch_bounds__(256) attn_tree_join_kernel(const Params p, float bias) {
-  constexpr int kGroups = 4, kBatch = 2;
-  __shared__ float2 s_ml[kGroups][32];
-  __shared__ float s_acc[kGroups][32][33];
+__global__ void __launch_bounds__(2 * D) attn_tree_join_kernel(const Params p, float bias) {
+  constexpr int kBatch = 4;
   const int R = p.unit_rows;
-  const int c1 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int grp = warp >> 1, half = warp & 1;
+  const int c1 = blockIdx.x, warp = threadIdx.x >> 5, row = blockIdx.y * 32 + (threadIdx.x & 31);
   wait_for_prior_grids();  // the parts are written
   const int4 job = p.jobs[c1];
-  const int row0 = blockIdx.y * 32, row = row0 + lane;
-  if (job.x < 0 || row0 >= job.y) return;
   const int q0 = p.job_q0[c1];
+  if (job.x < 0 || row >= job.y) return;
   float top = -INFINITY, sum = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = job.x + grp; c <= c1; c += kGroups * kBatch) {
+  for (int c = job.x; c <= c1; c += kBatch) {
     float2 ml[kBatch];
     float4 v[kBatch][4];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int cc = c + i * kGroups;
       ml[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[i][q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (cc <= c1 && row < job.y) {
-        const float* part = p.parts + (size_t)(2 * cc + (cc == job.x ? 1 : 0)) * (R * (D + 2));
+      if (c + i <= c1) {
+        const float* part =
+            p.parts + (size_t)(2 * (c + i) + (c + i == job.x ? 1 : 0)) * (R * (D + 2));
         ml[i] = *reinterpret_cast<const float2*>(part + R * D + 2 * row);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          v[i][q] = *reinterpret_cast<const float4*>(
-              part + ((blockIdx.z * 8 + half * 4 + q) * (size_t)R + row) * 4);
+          v[i][q] = *reinterpret_cast<const float4*>(part + ((warp * 4 + q) * (size_t)R + row) * 4);
       }
     }
     float n = top;
@@ -1219,42 +1214,26 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const Params p, flo
       }
     }
   }
-  if (half == 0) s_ml[grp][lane] = make_float2(top, sum);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float* to = &s_acc[grp][lane][half * 16 + 4 * q];
-    to[0] = acc[q].x;
-    to[1] = acc[q].y;
-    to[2] = acc[q].z;
-    to[3] = acc[q].w;
-  }
-  __syncthreads();
-  // eight lanes write a row's 32 columns, a warp four rows
-  const int rr0 = warp * 4 + (lane >> 3), c0 = (lane & 7) * 4;
-  if (row0 + rr0 >= job.y) return;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int w = 0; w < kGroups; ++w) m = fmaxf(m, s_ml[w][rr0].x);
-#pragma unroll
-  for (int w = 0; w < kGroups; ++w) {
-    const float2 ml = s_ml[w][rr0];
-    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-    l = fmaf(ml.y, f, l);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = fmaf(s_acc[w][rr0][c0 + k], f, o[k]);
-  }
-  const int rr = job.z + row0 + rr0, tok = rr / p.group;
+  const int rr = job.z + row, tok = rr / p.group;
   const int64_t at = (int64_t)(q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int64_t to = at * D + blockIdx.z * 32 + c0;
-  if (p.out_bf16)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to) =
-        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-  else
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) =
-        make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-  if (p.lse != nullptr && blockIdx.z == 0 && (lane & 7) == 0)
-    p.lse[at] = l > 0.f ? (m - bias + log2f(l)) * kLn2 : -INFINITY;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int64_t to = at * D + warp * 16;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    acc[q] = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
+  if (p.out_bf16) {
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      o[q] = make_uint4(pack_bf16x2(acc[2 * q].x, acc[2 * q].y), pack_bf16x2(acc[2 * q].z, acc[2 * q].w),
+                        pack_bf16x2(acc[2 * q + 1].x, acc[2 * q + 1].y),
+                        pack_bf16x2(acc[2 * q + 1].z, acc[2 * q + 1].w));
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      reinterpret_cast<float4*>(static_cast<float*>(p.out) + to)[q] = acc[q];
+  }
+  if (p.lse != nullptr && warp == 0) p.lse[at] = sum > 0.f ? (top - bias + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Rows of a unit: one q tile of 128, or two where a request may have more rows of one KV head.
@@ -1339,8 +1318,8 @@ cudaError_t launch(const AttnDecodeArgs& a, int dev, int sms, int* drv_err, cuda
     set.fetch_and(~bit, std::memory_order_relaxed);
     return e;
   }
-  return launch_ahead(attn_tree_join_kernel<D>, dim3(p.ctas, C::kUnitRows / 32, D / 32), 256, 0,
-                      stream, p, F8 ? 11.f : 0.f);
+  return launch_ahead(attn_tree_join_kernel<D>, dim3(p.ctas, C::kUnitRows / 32), 2 * D, 0, stream,
+                      p, F8 ? 11.f : 0.f);
 }
 
 template <bool F8, int D>
