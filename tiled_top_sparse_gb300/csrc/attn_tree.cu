@@ -29,6 +29,18 @@
 // digits there. The value scale of a page rides in the exponent as in attn_decode.cu:
 //   x_j = scale log2(e) sK q.k_j + log2 sV,   weights 2^(x_j - m), summed with 1 / sV.
 // bf16 caches use bf16 products throughout. Sums and statistics are fp32.
+//
+// Measured (one GPU, CUDA graph; 16 requests x 20000 tokens, 4 KV heads of 128; reading the cache
+// once at the rate of a copy takes 48 us in e4m3, 97 in bf16; products at the rate of a large bf16
+// matrix product 0.34 us per row):
+//   rows per KV head     8      32     128     256     512
+//   e4m3, us          78.0    79.1    88.9     140     260
+//   bf16, us           106     108     112     132     249
+// Up to 128 rows over bf16 HBM bounds it (0.91 of the copy rate at 32 rows, 1.03 over 32 requests
+// x 32768); over e4m3 a tile of 128 keys takes 0.87 us per CTA for 0.73 us of HBM: its chain of S,
+// weights, P V, whose two halves the two warpgroups overlap. From 256 rows on the tensor core
+// does: 1.58 us a tile of 256 rows against 1.33 at the rate above. The decode kernel's 16-row products are faster over e4m3 at 8 rows (58 us) and slower from
+// 32 on (107; 177 at 64).
 #include <atomic>
 #include <cstdint>
 #include <type_traits>

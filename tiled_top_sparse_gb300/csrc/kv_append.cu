@@ -19,6 +19,11 @@
 // resident). A step is one launch's latency: 3.0 us for 8 requests, 3.3 for 64. Where a page grows
 // its scale one warp reads and rewrites the page's earlier rows: 64 requests whose k and v pages
 // all grow take 6.1 us at slot 60 of pages of 64, 8.1 at slot 120 of 128.
+//
+// kAxes: positions are the caller's, on up to four axes, and two bits per rotation pair choose the
+// one whose table row it takes; eight pairs of one axis are loaded as without axes. The price is a
+// load in front of the table's: 26,800 prompt tokens with three axes into e4m3 118 us, 0.82 of the copy
+// rate; 16 trees of 25 to 64 tokens into bf16 7.2 us, one wave of blocks.
 #include <cstdint>
 #include <cuda_runtime.h>
 

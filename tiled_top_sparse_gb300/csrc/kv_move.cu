@@ -26,6 +26,10 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 //
 // e4m3: a page's scale holds for all of its slots. Where the rows moved into a page need a larger
 // one, it becomes the smallest power of two that holds them and every code of the page moves with it.
+//
+// Measured (CUDA graph): 8 requests of e4m3 4.7 us, 256 of bf16 (15 MB read and written) 6.3 us for 2.2 us of
+// bytes at the rate of a copy; the chain of dependent loads (lengths, path, table, rows) is what is
+// left.
 struct CompactParams {
   uint8_t* cache[2];  // K, V
   float* scale[2];
@@ -210,6 +214,9 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
 //
 // A block per (new request, head) copies the used rows of a page's K and V, one more per request
 // writes the table row and the length.
+//
+// Bound: HBM for many beams (CUDA graph, 512 of them in bf16, 33 MB read and 33 written: 11.8 us for 9.8 at the rate of a copy),
+// a launch and one chain of loads for few (4 samples in e4m3: 2.3 us).
 struct ForkParams {
   uint4* cache[2];
   float* scale[2];  // null: bf16
