@@ -41,6 +41,7 @@
 // weights, P V, whose two halves the two warpgroups overlap. From 256 rows on the tensor core
 // does: 1.58 us a tile of 256 rows against 1.33 at the rate above. The decode kernel's 16-row products are faster over e4m3 at 8 rows (58 us) and slower from
 // 32 on (107; 177 at 64).
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -287,6 +288,35 @@ __device__ __forceinline__ int last_weight(const Params& p, int n, int unit_rows
   const int rows = n * p.group;
   return (rows - 1) % unit_rows >= kRows ? 2 : 1;
 }
+// Places of the list that a request takes: its last row block may have up to 128 rows.
+template <int kQTiles>
+__device__ __forceinline__ int places_of(const Params& p, const Req& r) {
+  if (r.rt == 0) return 0;
+  return p.hkv * ((r.rt - 1) * r.nt * kQTiles + r.nt * last_weight(p, r.n, kQTiles * kRows) +
+                  r.rt * kEndTiles);
+}
+// The list cut into runs of `len` or, the first `more` of them, one more place.
+struct Runs {
+  int runs, len, more;
+  __device__ __forceinline__ Runs(int total, int ctas) {
+    runs = min(max((int)((unsigned)total / kMinRun), 1), ctas);
+    len = (int)((unsigned)total / (unsigned)runs);
+    more = total - len * runs;
+  }
+  __device__ __forceinline__ int cta_of(int place) const {
+    const int longer = more * (len + 1);  // places of the runs with one more
+    return place < longer ? (int)((unsigned)place / (unsigned)(len + 1))
+                          : more + (int)((unsigned)(place - longer) / (unsigned)len);
+  }
+};
+__device__ __forceinline__ int warp_scan(int x, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
 // A place in a ring of N slots and the parity of its current round.
 template <int N>
 struct Ring {
@@ -371,31 +401,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this CTA's run [t0, t1) of the list of tiles, and the request it begins in
   uint32_t bad = 0;
-  auto scan32 = [&](int x) -> int {  // inclusive over the warp
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kAll, x, o);
-      if (lane >= o) x += y;
-    }
-    return x;
-  };
-  auto places_of = [&](const Req& r) -> int {  // the last row block may have up to 128 rows
-    if (r.rt == 0) return 0;
-    return p.hkv * ((r.rt - 1) * r.nt * C::kQTiles + r.nt * last_weight(p, r.n, C::kUnitRows) + r.rt * kEndTiles);
-  };
-  int total = 0, runs = 0, len = 0, more = 0, t0 = 0, t1 = 0;
+  int total = 0, t0 = 0, t1 = 0;
   auto split = [&]() -> bool {
     if (total == 0) return false;
-    runs = min(max((int)((unsigned)total / kMinRun), 1), p.ctas);
-    if ((int)blockIdx.x >= runs) return false;
-    len = (int)((unsigned)total / (unsigned)runs);
-    more = total - len * runs;
-    t0 = blockIdx.x * len + min((int)blockIdx.x, more);
-    t1 = t0 + len + ((int)blockIdx.x < more ? 1 : 0);
+    const Runs cut(total, p.ctas);
+    if ((int)blockIdx.x >= cut.runs) return false;
+    t0 = blockIdx.x * cut.len + min((int)blockIdx.x, cut.more);
+    t1 = t0 + cut.len + ((int)blockIdx.x < cut.more ? 1 : 0);
     return true;
   };
   auto block_scan = [&](int v, int* sum) -> int {  // inclusive
-    const int x = scan32(v);
+    const int x = warp_scan(v, lane);
     __syncthreads();
     if (lane == 31) s_scan[warp] = x;
     __syncthreads();
@@ -411,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int b = 0, off = 0;
   bool work;
   if (p.batch <= 32) {  // every warp for itself
-    const int v = lane < p.batch ? places_of(load_req<TK>(p, lane, &bad)) : 0;
-    const int incl = scan32(v);
+    const int v = lane < p.batch ? places_of<C::kQTiles>(p, load_req<TK>(p, lane, &bad)) : 0;
+    const int incl = warp_scan(v, lane);
     total = __shfl_sync(kAll, incl, 31);
     work = split();
     if (work) {
@@ -424,14 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int base = 0; base < p.batch; base += kThreads) {
       const int i = base + tid;
       int sum;
-      block_scan(i < p.batch ? places_of(load_req<TK>(p, i, &bad)) : 0, &sum);
+      block_scan(i < p.batch ? places_of<C::kQTiles>(p, load_req<TK>(p, i, &bad)) : 0, &sum);
       total += sum;
     }
     work = split();
     uint32_t again = 0;
     for (int base = 0, carry = 0; work && base < p.batch && carry <= t0; base += kThreads) {
       const int i = base + tid;
-      const int v = i < p.batch ? places_of(load_req<TK>(p, i, &again)) : 0;
+      const int v = i < p.batch ? places_of<C::kQTiles>(p, load_req<TK>(p, i, &again)) : 0;
       int sum;
       const int incl = carry + block_scan(v, &sum);
       if (incl > t0 && incl - v <= t0) {
@@ -478,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int g, rt, at0;  // place within the unit
       {  // the run's first unit, perhaps from its middle
         const int full = r.nt * C::kQTiles + kEndTiles;  // places of a full row block
-        const int head = (int)((unsigned)places_of(r) / (unsigned)p.hkv);
+        const int head = (int)((unsigned)places_of<C::kQTiles>(p, r) / (unsigned)p.hkv);
         g = (int)((unsigned)off / (unsigned)head);
         at0 = off - g * head;
         rt = min((int)((unsigned)at0 / (unsigned)full), r.rt - 1);
@@ -540,11 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           q.whole_l = x0 == 0;
           q.whole_r = x1 == r.nt;
           q.c0 = 0;
-          if (!q.whole_l && q.whole_r) {  // the unit ends here: where it began
-            const int longer = more * (len + 1);  // tiles of the runs with one more
-            q.c0 = begin < longer ? (int)((unsigned)begin / (unsigned)(len + 1))
-                                  : more + (int)((unsigned)(begin - longer) / (unsigned)len);
-          }
+          if (!q.whole_l && q.whole_r) q.c0 = Runs(total, p.ctas).cta_of(begin);  // the unit ends here
           ok = describe(q);
         }
         // every row sees the keys of a tile in front of `base` and, with a window, from clear_lo on (or
@@ -1170,38 +1182,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the units that CTA borders cut: block (c, y) for rows 32 y .. of the unit that
-// ended in CTA c. A lane is a row, a warp 16 columns (the parts lie so that a warp reads whole lines), kBatch
-// parts' loads are in flight, and each lane writes whole sectors. The parts are joined in the
-// list's order.
-template <int D>
-__global__ void __launch_bounds__(2 * D) attn_tree_join_kernel(const Params p, float bias) {
-  constexpr int kBatch = 4;
+// Parts c, c + step, .. c1 of a unit begun in CTA c0, of one row the columns [16 x, 16 x + 16): kBatch
+// parts' loads are in flight.
+template <int D, int kBatch>
+__device__ __forceinline__ void join_parts(const Params& p, int c, int c0, int c1, int step, int row,
+                                           bool in, int x, float& top, float& sum, float4 (&acc)[4]) {
   const int R = p.unit_rows;
-  const int c1 = blockIdx.x, warp = threadIdx.x >> 5, row = blockIdx.y * 32 + (threadIdx.x & 31);
-  wait_for_prior_grids();  // the parts are written
-  const int4 job = p.jobs[c1];
-  const int q0 = p.job_q0[c1];
-  if (job.x < 0 || row >= job.y) return;
-  float top = -INFINITY, sum = 0.f;
-  float4 acc[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = job.x; c <= c1; c += kBatch) {
+  for (; c <= c1; c += kBatch * step) {
     float2 ml[kBatch];
     float4 v[kBatch][4];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
+      const int at = c + i * step;
       ml[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[i][q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c + i <= c1) {
-        const float* part =
-            p.parts + (size_t)(2 * (c + i) + (c + i == job.x ? 1 : 0)) * (R * (D + 2));
+      if (at <= c1 && in) {
+        const float* part = p.parts + (size_t)(2 * at + (at == c0 ? 1 : 0)) * (R * (D + 2));
         ml[i] = *reinterpret_cast<const float2*>(part + R * D + 2 * row);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          v[i][q] = *reinterpret_cast<const float4*>(part + ((warp * 4 + q) * (size_t)R + row) * 4);
+          v[i][q] = *reinterpret_cast<const float4*>(part + ((x * 4 + q) * (size_t)R + row) * 4);
       }
     }
     float n = top;
@@ -1226,6 +1227,25 @@ __global__ void __launch_bounds__(2 * D) attn_tree_join_kernel(const Params p, f
       }
     }
   }
+}
+
+// Joins the parts of the units that CTA borders cut: block (c, y) for rows 32 y .. of the unit that
+// ended in CTA c. A lane is a row, a warp 16 columns (the parts lie so that a warp reads whole lines), kBatch
+// parts' loads are in flight, and each lane writes whole sectors. The parts are joined in the
+// list's order.
+template <int D>
+__global__ void __launch_bounds__(2 * D) attn_tree_join_kernel(const Params p, float bias) {
+  constexpr int kBatch = 4;
+  const int c1 = blockIdx.x, warp = threadIdx.x >> 5, row = blockIdx.y * 32 + (threadIdx.x & 31);
+  wait_for_prior_grids();  // the parts are written
+  const int4 job = p.jobs[c1];
+  const int q0 = p.job_q0[c1];
+  if (job.x < 0 || row >= job.y) return;
+  float top = -INFINITY, sum = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  join_parts<D, kBatch>(p, job.x, job.x, c1, 1, row, true, warp, top, sum, acc);
   const int rr = job.z + row, tok = rr / p.group;
   const int64_t at = (int64_t)(q0 + tok) * p.hq + job.w * p.group + (rr - tok * p.group);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -1246,6 +1266,80 @@ __global__ void __launch_bounds__(2 * D) attn_tree_join_kernel(const Params p, f
       reinterpret_cast<float4*>(static_cast<float*>(p.out) + to)[q] = acc[q];
   }
   if (p.lse != nullptr && warp == 0) p.lse[at] = sum > 0.f ? (top - bias + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// The same where units are few and have many parts each (kDeep at least on average, over the longest
+// lists): block (u, y, z) for rows 32 y .., columns 16 z .. of unit u, whose parts follow from the
+// lengths. A warp takes every kDeep-th part, kBatch at a time, and the warps' sums are joined in order
+// through shared memory. One request of 2590 tokens and eight KV heads, eleven parts to a unit: 15.3 us
+// with the kernel above (three rounds of loads, and blocks for every CTA), 13.4 with this one; 8192
+// tokens and two KV heads, 76 parts to a unit: 29 and 15 us.
+constexpr int kDeep = 8;
+template <int D, bool kTwo>
+__global__ void __launch_bounds__(kDeep * 32) attn_tree_join_deep_kernel(const Params p, float bias) {
+  using C = Cfg<true, D, kTwo>;  // tiles and units are the same for either cache
+  constexpr int kBatch = 4;
+  __shared__ float2 s_ml[kDeep][32];
+  __shared__ float s_acc[kDeep][32][17];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int blocks = (p.max_q * p.group + C::kUnitRows - 1) / C::kUnitRows;  // of rows, a unit each
+  const int rt = blockIdx.x % blocks, g = blockIdx.x / blocks % p.hkv, b = blockIdx.x / blocks / p.hkv;
+  wait_for_prior_grids();  // the parts are written
+  uint32_t bad = 0;
+  Req r;
+  r.n = r.nt = r.rt = r.q0 = 0;
+  if (lane < p.batch) r = load_req<C::kTK>(p, lane, &bad);
+  const int v = places_of<C::kQTiles>(p, r), incl = warp_scan(v, lane);
+  const int n = __shfl_sync(kAll, r.n, b), nt = __shfl_sync(kAll, r.nt, b),
+            rts = __shfl_sync(kAll, r.rt, b), q0 = __shfl_sync(kAll, r.q0, b),
+            places = __shfl_sync(kAll, v, b), before = __shfl_sync(kAll, incl, b) - places;
+  if (rt >= rts) return;
+  const int weight = rt == rts - 1 ? last_weight(p, n, C::kUnitRows) : C::kQTiles;
+  const int begin = before + places / p.hkv * g + rt * (nt * C::kQTiles + kEndTiles);
+  const Runs cut(__shfl_sync(kAll, incl, 31), p.ctas);
+  const int c0 = cut.cta_of(begin), c1 = cut.cta_of(begin + weight * (nt - 1));
+  const int row0 = blockIdx.y * 32, rows = min(n * p.group - rt * C::kUnitRows, C::kUnitRows);
+  if (c0 == c1 || row0 >= rows) return;  // the same for the block
+  const int row = row0 + lane;
+  float top = -INFINITY, sum = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  join_parts<D, kBatch>(p, c0 + warp, c0, c1, kDeep, row, row < rows, blockIdx.z, top, sum, acc);
+  s_ml[warp][lane] = make_float2(top, sum);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float* to = &s_acc[warp][lane][4 * q];
+    to[0] = acc[q].x;
+    to[1] = acc[q].y;
+    to[2] = acc[q].z;
+    to[3] = acc[q].w;
+  }
+  __syncthreads();
+  // eight lanes write a row's 16 columns
+  const int at_row = threadIdx.x >> 3, col = (threadIdx.x & 7) * 2;
+  if (row0 + at_row >= rows) return;
+  float m = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+  for (int w = 0; w < kDeep; ++w) m = fmaxf(m, s_ml[w][at_row].x);
+#pragma unroll
+  for (int w = 0; w < kDeep; ++w) {
+    const float2 ml = s_ml[w][at_row];
+    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+    l = fmaf(ml.y, f, l);
+    x = fmaf(s_acc[w][at_row][col], f, x);
+    y = fmaf(s_acc[w][at_row][col + 1], f, y);
+  }
+  const int rr = rt * C::kUnitRows + row0 + at_row, tok = rr / p.group;
+  const int64_t at = (int64_t)(q0 + tok) * p.hq + g * p.group + (rr - tok * p.group);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int64_t to = at * D + blockIdx.z * 16 + col;
+  if (p.out_bf16)
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + to) = pack_bf16x2(x * inv, y * inv);
+  else
+    *reinterpret_cast<float2*>(static_cast<float*>(p.out) + to) = make_float2(x * inv, y * inv);
+  if (p.lse != nullptr && blockIdx.z == 0 && col == 0)
+    p.lse[at] = l > 0.f ? (m - bias + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Rows of a unit: one q tile of 128, or two where a request may have more rows of one KV head.
@@ -1330,8 +1424,14 @@ cudaError_t launch(const AttnDecodeArgs& a, int dev, int sms, int* drv_err, cuda
     set.fetch_and(~bit, std::memory_order_relaxed);
     return e;
   }
-  return launch_ahead(attn_tree_join_kernel<D>, dim3(p.ctas, C::kUnitRows / 32), 2 * D, 0, stream,
-                      p, F8 ? 11.f : 0.f);
+  const float bias = F8 ? 11.f : 0.f;
+  const int64_t rows = (int64_t)p.max_q * p.group;
+  const int64_t units = (rows + C::kUnitRows - 1) / C::kUnitRows * p.hkv * p.batch;
+  const unsigned blocks = (unsigned)((std::min<int64_t>(rows, C::kUnitRows) + 31) / 32);
+  if (units * kDeep <= p.ctas && p.batch <= 32)
+    return launch_ahead(attn_tree_join_deep_kernel<D, kTwo>, dim3((unsigned)units, blocks, D / 16),
+                        kDeep * 32, 0, stream, p, bias);
+  return launch_ahead(attn_tree_join_kernel<D>, dim3(p.ctas, blocks), 2 * D, 0, stream, p, bias);
 }
 
 template <bool F8, int D>
