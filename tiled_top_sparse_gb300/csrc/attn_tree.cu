@@ -30,17 +30,19 @@
 //   x_j = scale log2(e) sK q.k_j + log2 sV,   weights 2^(x_j - m), summed with 1 / sV.
 // bf16 caches use bf16 products throughout. Sums and statistics are fp32.
 //
+// Code that a part runs once, or few tiles do, is kept short (loops that are not unrolled): three warps
+// of different roles share an SM quarter's instruction cache, and what it does not hold is waited for.
+// The q rows' conversion unrolled over four rows instead of one cost 16 large trees 10 us of 104.
+//
 // Measured (one GPU, CUDA graph; 16 requests x 20000 tokens, 4 KV heads of 128; reading the cache
 // once at the rate of a copy takes 48 us in e4m3, 97 in bf16; products at the rate of a large bf16
 // matrix product 0.34 us per row):
-//   rows per KV head     8      32     128     256     512
-//   e4m3, us          78.0    79.1    88.9     140     260
-//   bf16, us           106     108     112     132     249
+//   rows per KV head      32     128     256     512
+//   e4m3, us            69.7    78.4     135     249
+//   bf16, us             107     112     129     245
 // Up to 128 rows over bf16 HBM bounds it (0.91 of the copy rate at 32 rows, 1.03 over 32 requests
-// x 32768); over e4m3 a tile of 128 keys takes 0.87 us per CTA for 0.73 us of HBM: its chain of S,
-// weights, P V, whose two halves the two warpgroups overlap. From 256 rows on the tensor core
-// does: 1.58 us a tile of 256 rows against 1.33 at the rate above. The decode kernel's 16-row products are faster over e4m3 at 8 rows (58 us) and slower from
-// 32 on (107; 177 at 64).
+// x 32768); over e4m3 the chain of a tile's S, weights, P V, of which each warpgroup has one under way.
+// From 256 rows on that chain and the tensor core (0.65 of the rate above).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -59,8 +61,9 @@ namespace {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kThreads = 384;
 constexpr int kRows = 128;  // q rows of a tile (TMEM lanes)
-// What the end of a unit costs (joining, the next unit's q), in tiles of the list.
-constexpr int kEndTiles = 8;
+// What the end of a unit costs (its sums, the next unit's first tile), in tiles of the list: 4 to 8 are
+// within 5 % of one another on batches of 1 to 100 requests.
+constexpr int kEndTiles = 7;
 constexpr int kParts = 4;   // parts of a run that are described ahead
 constexpr int kMinRun = 2;  // places of a run at least: a tile for each warpgroup
 constexpr float kMinValueScale = 0x1p-80f;  // as in attn_decode.cu
@@ -162,6 +165,20 @@ __device__ __forceinline__ uint32_t below(int n, int c0) {  // bits of columns c
   return b <= 0 ? 0u : b >= 32 ? kAll : (1u << b) - 1u;
 }
 
+// Which of the keys k0 .. k0 + 31 (word c of a tile) are seen: those before `base` from lo on (with a
+// window) or among the first `sinks`, the new tokens in `mask`, on pages that are there.
+__device__ __forceinline__ uint32_t seen_word(int k0, int c, int base, int window, int lo, int sinks,
+                                              uint64_t mask, uint32_t pieces, int piece_shift) {
+  uint32_t see = below(base, k0);
+  if (window > 0) see &= ~below(lo, k0) | below(sinks, k0);
+  const int sh = k0 - base;  // the word's first key among the new tokens
+  if (sh > -32 && sh < 64) see |= (uint32_t)(sh >= 0 ? mask >> sh : mask << -sh);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (!((pieces >> ((2 * c + u) >> piece_shift)) & 1u)) see &= ~(0xFFFFu << (16 * u));
+  return see;
+}
+
 // Bounded wait of a converged warp in few instructions: every role has its own, and what the
 // instruction cache does not hold is waited for as well. Sets *abort where it runs out.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
@@ -180,6 +197,9 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
     }
   }
   return __all_sync(kAll, ok);
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 // Looks at three barriers at once.
 __device__ __forceinline__ bool peek3(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, uint32_t c,
@@ -345,11 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   // Of a part: described, its description read. Of a tile: K and V landed; their slots free (K's
   // products done; V's products done, or its codes widened: K's place is filled again a product earlier);
-  // V ready for its product (widened, or cleared); its scales written. Of a warpgroup: scores, weights of a tile's first 64 keys, all weights, sums. Of a part: q tiles written; both warpgroups done
-  // with it (its sums read, its products complete); the second warpgroup's statistics.
+  // V ready for its product (widened, or cleared); its scales written. Of a warpgroup: scores, weights
+  // of a tile's first 64 keys, all weights, sums. Of a part: the q tile written that a warpgroup's
+  // scores read; every score read (the q tiles may be overwritten, and the columns that statistics
+  // go through); the second warpgroup's statistics.
   __shared__ __align__(8) uint64_t bar_part[kParts], bar_part_empty[kParts], bar_k[S], bar_v[S],
-      bar_k_empty[S], bar_v_empty[S], bar_ready[S], bar_meta[C::kMeta], bar_s[2], bar_half[2], bar_p[2], bar_o[2],
-      bar_q, bar_done, bar_ml, bar_drain;
+      bar_k_empty[S], bar_v_empty[S], bar_ready[S], bar_meta[C::kMeta], bar_s[2], bar_half[2],
+      bar_p[2], bar_o[2], bar_q[2], bar_q_empty, bar_ml, bar_drain;
   __shared__ __align__(16) Meta<C::kPieces> s_meta[C::kMeta];
   __shared__ Part s_part[kParts];
   __shared__ uint8_t s_ex[C::kUnitRows];  // e4m3: the exponent that a q row was scaled by
@@ -385,9 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bar_half[i]), kRows);
       mbar_init(smem_u32(&bar_p[i]), kRows);
       mbar_init(smem_u32(&bar_o[i]), 1);
+      mbar_init(smem_u32(&bar_q[i]), 2 * kRows);
     }
-    mbar_init(smem_u32(&bar_q), 2 * kRows);
-    mbar_init(smem_u32(&bar_done), 2 * kRows);
+    mbar_init(smem_u32(&bar_q_empty), 8);
     mbar_init(smem_u32(&bar_ml), kRows);
     mbar_init(smem_u32(&bar_drain), 1);
     fence_mbar_init();
@@ -698,20 +720,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool alt = !kTwo || s_part[pslot.at].rows <= kRows;
         const int J = alt ? s_part[pslot.at].T : 2 * s_part[pslot.at].T;
         part_done();
-        // the q tiles are written, and the sums of the part before have been read
-        ok = wait_for(smem_u32(&bar_q), odd_q, abort_flag);
-        odd_q ^= 1;
         // Job i: warpgroup i % 2, and tile i, or i / 2 where each warpgroup takes every tile. The product
-        // of job i - 2's weights comes in front of job i's scores, which overwrite them.
+        // of job i - 2's weights comes in front of job i's scores, which overwrite them. A part's first
+        // scores run while the sums of the part before are read: its first product, which overwrites
+        // them, waits for weights that the warpgroup computes after it read them (the second warpgroup's
+        // sums, read by the first where they take turns, as well: its job comes after job 0).
         auto step = [&](auto which, int i) -> bool {
           constexpr int w = decltype(which)::value;
           const bool pv = i >= 2 && i < J + 2, qk = i < J;
-          // Everything the step needs is looked at together: a look takes as long as an issue. A barrier
-          // that is not needed stands in for none (its phase is known to be complete).
-          const uint32_t any = smem_u32(&bar_q);
-          const uint32_t bar_a = pv ? smem_u32(&bar_ready[vslot.at]) : any, odd_a = pv ? vslot.odd : odd_q ^ 1;
-          const uint32_t bar_b = pv ? smem_u32(&bar_half[w]) : any, odd_b = pv ? odd_p[w] : odd_q ^ 1;
-          const uint32_t bar_c = qk ? smem_u32(&bar_k[kslot.at]) : any, odd_c = qk ? kslot.odd : odd_q ^ 1;
+          if (!pv && !qk) return true;
+          // Everything the step needs is looked at together: a look takes as long as an issue.
+          const uint32_t bar_a = pv ? smem_u32(&bar_half[w]) : smem_u32(&bar_q[w]);
+          const uint32_t bar_b = pv ? smem_u32(&bar_ready[vslot.at]) : bar_a;
+          const uint32_t bar_c = qk ? smem_u32(&bar_k[kslot.at]) : bar_a;
+          const uint32_t odd_a = pv ? odd_p[w] : odd_q, odd_b = pv ? vslot.odd : odd_a,
+                         odd_c = qk ? kslot.odd : odd_a;
           uint32_t since = 0;
           while (!__all_sync(kAll, peek3(bar_a, odd_a, bar_b, odd_b, bar_c, odd_c))) {
             if (__any_sync(kAll, *abort_flag)) return false;
@@ -746,6 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (int i = 0; ok && i < J + 2; i += 2)
           ok = step(std::integral_constant<int, 0>(), i) && step(std::integral_constant<int, 1>(), i + 1);
+        odd_q ^= 1;
       }
       // Every product is complete before TMEM is freed.
       mma_commit_elect(smem_u32(&bar_drain), e);
@@ -791,17 +815,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t okp = s_meta[mslot.at].ok;
           const int key0 = s_meta[mslot.at].key0;
           const bool all = s_meta[mslot.at].clear;
-          auto row_seen = [&](int row) -> bool {  // by some token
-            const int key = key0 + row;
-            if (!((okp >> ((row >> 4) >> piece_shift)) & 1u)) return false;
-            if (key < q.base) return key >= lo || key < kept;
-            return key - q.base < 64 && ((any >> (key - q.base)) & 1u);
+          // words of the rows that some token sees, one a lane: the others' V is cleared
+          const int word = lane & 3;
+          const uint32_t mine = all ? kAll
+                                    : seen_word(key0 + 32 * word, word, q.base, p.window, lo, kept, any,
+                                                okp, piece_shift);
+          auto clear_unseen = [&](auto clear, int row0, int step) {
+            if (all) return;
+#pragma unroll 1
+            for (int c = 0; c < TK / 32; ++c) {
+              const uint32_t see = __shfl_sync(kAll, mine, c);
+              if (see == kAll) continue;
+#pragma unroll 1
+              for (int row = row0; row < 32; row += step)
+                if (!((see >> row) & 1u)) clear(32 * c + row);
+            }
           };
           if constexpr (F8) {
             const uint32_t from = sV(st), to = wide + wide_at * C::kWideBytes;
             // A thread's chunks of 16 codes lie kStep rows apart in one column: the swizzle is the
             // same for all of them. kDeep are on their way at a time.
-            constexpr int kCpr = D / 16, kStep = 64 / kCpr, kDeep = 8;
+            constexpr int kCpr = D / 16, kStep = 64 / kCpr, kDeep = 4;
             static_assert(TK % (kStep * kDeep) == 0 && kStep % 8 == 0, "chunks");
             const int i0 = (warp - 2) * 32 + lane, row0 = i0 / kCpr, c = i0 % kCpr;
             // the second panel's lanes store the other chunk first: eight lanes, all banks
@@ -814,11 +848,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint4 v[kDeep];
 #pragma unroll
               for (int k = 0; k < kDeep; ++k) v[k] = lds128(src + (k0 + k) * kStep * PB);
-              if (!all) {
-#pragma unroll
-                for (int k = 0; k < kDeep; ++k)
-                  if (!row_seen(row0 + (k0 + k) * kStep)) v[k] = make_uint4(0, 0, 0, 0);
-              }
 #pragma unroll
               for (int k = 0; k < kDeep; ++k) {
                 const uint32_t x4[4] = {odd ? v[k].z : v[k].x, odd ? v[k].w : v[k].y,
@@ -831,12 +860,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   e4m3_half(x4[3], 1)));
               }
             }
+            clear_unseen(
+                [&](int row) {  // whole steps from row0
+                  sts128(dst0 + (row - row0) * 128, make_uint4(0, 0, 0, 0));
+                  sts128(dst1 + (row - row0) * 128, make_uint4(0, 0, 0, 0));
+                },
+                row0, kStep);
             fence_proxy_async_smem();
           } else if (!all) {
-            for (int i = (warp - 2) * 32 + lane; i < TK * (D / 8); i += 64) {
-              const int row = i / (D / 8), c = i % (D / 8);
-              if (!row_seen(row)) sts128(chunk_at<PB>(sV(st), TK, row, c), make_uint4(0, 0, 0, 0));
-            }
+            const int i0 = (warp - 2) * 32 + lane, c = i0 % (D / 8);
+            clear_unseen([&](int row) { sts128(chunk_at<PB>(sV(st), TK, row, c), make_uint4(0, 0, 0, 0)); },
+                         i0 / (D / 8), 64 / (D / 8));
             fence_proxy_async_smem();
           }
           __syncwarp();
@@ -859,95 +893,103 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<S> kslot;         // of the part's next tile
     Ring<C::kMeta> mslot;
     // parities of the phases waited for next: own scores, own sums, the other's sums, its statistics,
-    // q tiles, the part before
-    uint32_t odd_s = 0, odd_o = 0, odd_other = 0, odd_ml = 0, odd_q = 0, odd_done = 0;
+    // q tiles, the scores of the part before
+    uint32_t odd_s = 0, odd_o = 0, odd_other = 0, odd_ml = 0, odd_q = 0, odd_empty = 1;
+    // A q tile is written by one warpgroup: its own, or, where they take turns, by the second while the
+    // first writes the sums of the part before (a run's first q tile by both). D / 16 lanes to a row, 16
+    // values each, which lie in shared memory as copied (e4m3: in the place of the row's two halves) until
+    // the lane turns them into its 16 codes of either half.
+    constexpr int kLanes = D / 16, kPass = 4 * 32 / kLanes;
     bool first = true;  // part
-    bool ok = true;
-    while (ok && next_part()) {
-      const Part& q = s_part[pslot.at];
-      const bool alt = !kTwo || q.rows <= kRows;
-      // ---- q tiles, by both warpgroups: D / 16 lanes to a row, 16 values each
-      {
-        constexpr int kLanes = D / 16, kPass = 8 * 32 / kLanes, kPasses = kRows / kPass;
-        const int c = lane % kLanes;
+    uint64_t seen = 0;  // this thread's row's mask
+    auto takes_turns = [&](const Part& q) -> bool { return !kTwo || q.rows <= kRows; };
+    const int q_lane = lane % kLanes, q_row = (warp & 3) * (32 / kLanes) + lane / kLanes;
+    auto raw_at = [&](uint32_t to, int row, int i) -> uint32_t {  // i-th of the lane's two pieces
+      if constexpr (F8)
+        return chunk_at<PB>(to + (2 * q_lane >= kLanes ? kRows * PB : 0), kRows, row,
+                            (2 * q_lane + i) % kLanes);
+      else
+        return chunk_at<PB>(to, kRows, row, 2 * q_lane + i);
+    };
+    auto ask = [&](const Part& q) -> bool {  // of the next part
+      const bool alt = takes_turns(q);
+      const int r0 = alt ? 0 : w * kRows;
+      if (r0 + lane_row < q.rows) seen = p.mask[q.q0 + (q.row0 + r0 + lane_row) / p.group];
+      if (alt && w == 0 && !first) return true;
+      if (!first && !wait_for(smem_u32(&bar_q_empty), odd_empty, abort_flag)) return false;
+      const uint32_t to = sq + (r0 ? C::kQBytes : 0);
+      const int share = alt && first;
 #pragma unroll 1
-        for (int r0 = 0; r0 < q.rows; r0 += kRows) {
+      for (int row = q_row + share * w * kPass; row - lane / kLanes < q.rows - r0 && row < kRows;
+           row += kPass << share) {
+        const bool in = r0 + row < q.rows;
+        const int rr = q.row0 + r0 + row, tok = in ? rr / p.group : 0;
+        const int64_t at = (int64_t)(q.q0 + tok) * p.hq + q.g * p.group + (rr - tok * p.group);
+        const uint16_t* src = in ? p.q + at * D + q_lane * 16 : p.q;
+        cp_async_16(raw_at(to, row, 0), src, in ? 16 : 0);
+        cp_async_16(raw_at(to, row, 1), src + 8, in ? 16 : 0);
+      }
+      return true;
+    };
+    bool ok = next_part() && ask(s_part[pslot.at]);
+    while (ok) {
+      const Part& q = s_part[pslot.at];
+      const bool alt = takes_turns(q);
+      const int share = alt && first;
+      if (!alt || w == 1 || share) {
+        cp_async_wait_all();
+        if constexpr (F8) {
+          const int r0 = alt ? 0 : w * kRows;
           const uint32_t to = sq + (r0 ? C::kQBytes : 0);
-          uint4 v[kPasses][2];
+#pragma unroll 1
+          for (int row = q_row + share * w * kPass; row - lane / kLanes < q.rows - r0 && row < kRows;
+               row += kPass << share) {
+            const uint4 v0 = lds128(raw_at(to, row, 0)), v1 = lds128(raw_at(to, row, 1));
+            const uint32_t u[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            uint32_t top = 0;  // largest |q| of the row, as bf16 bits
 #pragma unroll
-          for (int k = 0; k < kPasses; ++k) {
-            const int row_k = r0 + k * kPass + (warp - 4) * (32 / kLanes) + lane / kLanes;
-            v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
-            if (row_k < q.rows) {
-              const int rr_k = q.row0 + row_k, tok_k = rr_k / p.group;
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  p.q + ((int64_t)(q.q0 + tok_k) * p.hq + q.g * p.group + (rr_k - tok_k * p.group)) * D +
-                  c * 16);
-              v[k][0] = src[0];
-              v[k][1] = src[1];
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t m = u[i] & 0x7FFF7FFFu;
+              top = max(top, max(m & 0xFFFFu, m >> 16));
             }
-          }
-          // both warpgroups are done with the part before: its products have read the q tiles
-          if (r0 == 0 && !first) {
-            ok = wait_for(smem_u32(&bar_done), odd_done, abort_flag);
-            odd_done ^= 1;
-          }
-          if (!ok) break;
 #pragma unroll
-          for (int k = 0; k < kPasses; ++k) {
-            const int base_k = r0 + k * kPass + (warp - 4) * (32 / kLanes);
-            if (base_k >= q.rows) continue;  // the same for the warp; such rows are not looked at
-            const int row_k = base_k + lane / kLanes - r0;
-            if constexpr (F8) {
-              const uint32_t u[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
-                                     v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
-              uint32_t top = 0;  // largest |q| of the row, as bf16 bits
+            for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
+            const int ex = max((int)(top >> 7), 27);  // biased exponent; q' = q 2^(7 - e) < 2^8
+            const float up = __uint_as_float((uint32_t)(261 - ex < 1 ? 1 : 261 - ex) << 23);
+            if (q_lane == 0) s_ex[r0 + row] = (uint8_t)ex;
+            uint32_t hi[4], lo[4];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t m = u[i] & 0x7FFF7FFFu;
-                top = max(top, max(m & 0xFFFFu, m >> 16));
-              }
-#pragma unroll
-              for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
-              const int ex = max((int)(top >> 7), 27);  // biased exponent; q' = q 2^(7 - e) < 2^8
-              const float up = __uint_as_float((uint32_t)(261 - ex < 1 ? 1 : 261 - ex) << 23);
-              if (c == 0) s_ex[r0 + row_k] = (uint8_t)ex;
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float a = __uint_as_float(u[i] << 16) * up,
-                            b2 = __uint_as_float(u[i] & 0xFFFF0000u) * up;
-                const uint32_t h = cvt_e4m3x2(a, b2);
-                const float2 back = e4m3x2_to_float2((uint16_t)h);
-                const uint32_t low = cvt_e4m3x2(a - back.x, b2 - back.y);
-                hi[i / 2] = i & 1 ? hi[i / 2] | h << 16 : h;
-                lo[i / 2] = i & 1 ? lo[i / 2] | low << 16 : low;
-              }
-              const uint32_t dst = chunk_at<PB>(to, kRows, row_k, c);
-              sts128(dst, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-              sts128(dst + kRows * PB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-            } else {
-              sts128(chunk_at<PB>(to, kRows, row_k, 2 * c), v[k][0]);
-              sts128(chunk_at<PB>(to, kRows, row_k, 2 * c + 1), v[k][1]);
+            for (int i = 0; i < 8; ++i) {
+              const float a = __uint_as_float(u[i] << 16) * up,
+                          b2 = __uint_as_float(u[i] & 0xFFFF0000u) * up;
+              const uint32_t h = cvt_e4m3x2(a, b2);
+              const float2 back = e4m3x2_to_float2((uint16_t)h);
+              const uint32_t low = cvt_e4m3x2(a - back.x, b2 - back.y);
+              hi[i / 2] = i & 1 ? hi[i / 2] | h << 16 : h;
+              lo[i / 2] = i & 1 ? lo[i / 2] | low << 16 : low;
             }
+            __syncwarp();  // the row is read
+            const uint32_t dst = chunk_at<PB>(to, kRows, row, q_lane);
+            sts128(dst, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            sts128(dst + kRows * PB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
         }
-        first = false;
-        if (!ok) break;
         fence_proxy_async_smem();
-        mbar_arrive(smem_u32(&bar_q));
+        const uint32_t n = 2 - share;
+        mbar_arrive_n(smem_u32(&bar_q[w]), n);
+        if (alt) mbar_arrive_n(smem_u32(&bar_q[w ^ 1]), n);
       }
+      first = false;
+      odd_empty ^= 1;
       // ---- this thread's q row: position, mask, factor of its scores
       const int row = lane_row + (alt ? 0 : w * kRows);
       const bool in = row < q.rows, live = row - lane < q.rows;
-      uint64_t mask = 0;
-      if (in)
-        mask = p.mask[q.q0 + (q.row0 + row) / p.group] & (q.n >= 64 ? ~0ull : (1ull << q.n) - 1);
+      uint64_t mask = in ? seen & (q.n >= 64 ? ~0ull : (1ull << q.n) - 1) : 0;
       const int pos = q.base + max(__popcll(mask) - 1, 0);
       mask &= present(q.n, q.base);
       float fac = p.scale_log2;
       if constexpr (F8) {
-        ok = wait_for(smem_u32(&bar_q), odd_q, abort_flag);  // the rows' exponents
+        ok = wait_for(smem_u32(&bar_q[w]), odd_q, abort_flag);  // the rows' exponents
         if (!ok) break;
         const int ex = in ? s_ex[row] : 127;
         fac *= __uint_as_float((uint32_t)(ex < 8 ? 1 : ex - 7) << 23);
@@ -969,55 +1011,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const Meta<C::kPieces>& meta = s_meta[mslot.at];
-        uint32_t sr[TK];
-        float part_max[TK / 32];
+        // Scores in the exp2 domain are s a + vl, with a and vl of the key's page; a > 0, so a page's
+        // largest score has its largest s. They are read twice, for their maximum and for their weights.
+        float tile_max = -INFINITY;
+        if (meta.clear && (!F8 || piece_shift > 0)) {
+          uint32_t x[32];
+          float most[TK / 32];
 #pragma unroll
-        for (int c = 0; c < TK / 32; ++c)
-          part_max[c] =
-              tmem_ld32_max(S_row + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-        tmem_ld_wait();
-        float* s = reinterpret_cast<float*>(sr);
-        if (!meta.clear) {
-          const uint32_t okp = meta.ok;
+          for (int c = 0; c < TK / 32; ++c) most[c] = tmem_ld32_max(S_row + c * 32, x);
+          tmem_ld_wait();
 #pragma unroll
           for (int c = 0; c < TK / 32; ++c) {
-            const int k0 = meta.key0 + 32 * c;
-            uint32_t see = below(q.base, k0);
-            if (p.window > 0) see &= ~below(pos + 1 - p.window, k0) | below(p.sinks, k0);
-            const int sh = k0 - q.base;  // the word's first column among the new tokens
-            if (sh > -32 && sh < 64) see |= (uint32_t)(sh >= 0 ? mask >> sh : mask << -sh);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              if (!((okp >> ((2 * c + u) >> piece_shift)) & 1u)) see &= ~(0xFFFFu << (16 * u));
-            if (__all_sync(kAll, see == kAll)) continue;
-#pragma unroll
-            for (int cc = 0; cc < 32; ++cc)
-              if (!((see >> cc) & 1u)) s[32 * c + cc] = -INFINITY;
-            part_max[c] = row_max<32>(s + 32 * c);
-          }
-        }
-        // Scores in the exp2 domain are s a + vl, with a and vl of the key's page; a > 0, so a page's
-        // largest score has its largest s.
-        float tile_max = -INFINITY;
-        if constexpr (F8) {
-          if (piece_shift == 0) {
-#pragma unroll
-            for (int c = 0; c < TK / 16; ++c) {
-              const float4 sc = meta.scale[c];
-              tile_max = fmaxf(tile_max, fmaf(row_max<16>(s + 16 * c), fac * sc.x, sc.y));
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < TK / 32; ++c) {
+            if constexpr (F8) {
               const float4 sc = meta.scale[(2 * c) >> piece_shift];
-              tile_max = fmaxf(tile_max, fmaf(part_max[c], fac * sc.x, sc.y));
+              most[c] = fmaf(most[c], fac * sc.x, sc.y);
             }
+            tile_max = fmaxf(tile_max, most[c]);
           }
         } else {
+          // What a row does not see becomes -inf, in TMEM: a short loop, since such tiles are few and
+          // code that is seldom run is waited for.
+          const uint32_t okp = meta.ok;
+#pragma unroll 1
+          for (int c = 0; c < TK / 32; ++c) {
+            const uint32_t see = seen_word(meta.key0 + 32 * c, c, q.base, p.window, pos + 1 - p.window,
+                                           p.sinks, mask, okp, piece_shift);
+            uint32_t x[32];
+            tmem_ld32(S_row + c * 32, x);
+            tmem_ld_wait();
+            if (!__all_sync(kAll, see == kAll)) {
 #pragma unroll
-          for (int c = 0; c < TK / 32; ++c) tile_max = fmaxf(tile_max, part_max[c]);
-          tile_max *= fac;
+              for (int i = 0; i < 32; ++i)
+                if (!((see >> i) & 1u)) x[i] = 0xFF800000u;
+              tmem_st32(S_row + c * 32, x);
+            }
+            const float* s = reinterpret_cast<const float*>(x);
+            if constexpr (F8) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float4 sc = meta.scale[(2 * c + u) >> piece_shift];
+                tile_max = fmaxf(tile_max, fmaf(row_max<16>(s + 16 * u), fac * sc.x, sc.y));
+              }
+            } else {
+              tile_max = fmaxf(tile_max, row_max<32>(s));
+            }
+          }
+          tmem_st_wait();
         }
+        if (!F8) tile_max *= fac;
         const bool resc = tile_max > m_ref + kThr;  // false for -inf
         float alpha = 1.f;
         if (resc) {
@@ -1027,34 +1068,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         const float shift = m_ref == -INFINITY ? 0.f : kBias - m_ref;
-        // ---- weights, packed in place
+        // ---- weights, packed in front of the scores that are still to be read
+#pragma unroll 4
+        for (int c = 0; c < TK / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld32(S_row + c * 32, x);
+          tmem_ld_wait();
+          const float* s = reinterpret_cast<const float*>(x);
+          uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < TK / 16; ++c) {
-          float a = fac, add = shift, inv = 1.f;
-          if constexpr (F8) {
-            const float4 sc = meta.scale[c >> piece_shift];
-            a = fac * sc.x;
-            add = shift + sc.y;
-            inv = sc.z;
-          }
-          const float2 a2 = make_float2(a, a), b2 = make_float2(add, add);
-          float2 acc = make_float2(0.f, 0.f);
-          float2 y[8];
+          for (int h = 0; h < 2; ++h) {
+            float a = fac, add = shift, inv = 1.f;
+            if constexpr (F8) {
+              const float4 sc = meta.scale[(2 * c + h) >> piece_shift];
+              a = fac * sc.x;
+              add = shift + sc.y;
+              inv = sc.z;
+            }
+            const float2 a2 = make_float2(a, a), b2 = make_float2(add, add);
+            float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            y[u] = ffma2(make_float2(s[16 * c + 2 * u], s[16 * c + 2 * u + 1]), a2, b2);
-            y[u].x = ex2_approx(y[u].x);
-            y[u].y = ex2_approx(y[u].y);
+            for (int u = 0; u < 8; ++u) {
+              float2 y = ffma2(make_float2(s[16 * h + 2 * u], s[16 * h + 2 * u + 1]), a2, b2);
+              y.x = ex2_approx(y.x);
+              y.y = ex2_approx(y.y);
+              acc = fadd2(acc, y);
+              pk[8 * h + u] = F8 ? pack_f16x2(y.x, y.y) : pack_bf16x2(y.x, y.y);
+            }
+            l = fmaf(acc.x + acc.y, inv, l);
           }
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            acc = fadd2(acc, y[u]);
-            sr[8 * c + u] = F8 ? pack_f16x2(y[u].x, y[u].y) : pack_bf16x2(y[u].x, y[u].y);
-          }
-          l = fmaf(acc.x + acc.y, inv, l);
-          if (c % 4 == 3)
-            tmem_st32(S_row + (c / 4) * 32, *reinterpret_cast<const uint32_t(*)[32]>(&sr[(c / 4) * 32]));
-          if (c == 3) {
+          tmem_st16(S_row + c * 16, pk);
+          if (c == 1) {
             // The accumulator: its last product was issued before this tile's S, which is complete.
             if (j > (alt ? w : 0) && __any_sync(kAll, resc)) {
               const uint32_t O_row = tmem + 256 + w * 128 + lane_off;
@@ -1082,29 +1126,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The second warpgroup's statistics go through two columns behind its last weights, on the same
       // lanes.
       const bool other = alt && q.T > 1;
+      float m1 = -INFINITY, l1 = 0.f;
+      if (other && w == 1) {
+        tmem_st2(S_row + 126, __float_as_uint(m_ref), __float_as_uint(l));
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&bar_ml));
+      } else if (other) {
+        ok = wait_for(smem_u32(&bar_ml), odd_ml, abort_flag);
+        if (!ok) break;
+        odd_ml ^= 1;
+        tc_fence_after();
+        uint32_t a, b2;
+        tmem_ld2(tmem + 128 + lane_off + 126, a, b2);
+        tmem_ld_wait();
+        tc_fence_before();
+        m1 = __uint_as_float(a);
+        l1 = __uint_as_float(b2);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bar_q_empty));
+      // the next part
+      Ring<kParts> here = pslot;
+      pslot.next();
+      const bool again = next_part() && ask(s_part[pslot.at]);
       if (alt && w == 1) {
         if (other) {
-          tmem_st2(S_row + 126, __float_as_uint(m_ref), __float_as_uint(l));
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&bar_ml));
           ok = wait_for(smem_u32(&bar_o[1]), odd_o, abort_flag);
           if (!ok) break;
           odd_o ^= 1;
         }
       } else {
-        float m1 = -INFINITY, l1 = 0.f;
-        if (other) {
-          ok = wait_for(smem_u32(&bar_ml), odd_ml, abort_flag);
-          if (!ok) break;
-          odd_ml ^= 1;
-          tc_fence_after();
-          uint32_t a, b2;
-          tmem_ld2(tmem + 128 + lane_off + 126, a, b2);
-          tmem_ld_wait();
-          m1 = __uint_as_float(a);
-          l1 = __uint_as_float(b2);
-        }
         ok = wait_for(smem_u32(&bar_o[w]), odd_o, abort_flag);
         odd_o ^= 1;
         if (ok && other) ok = wait_for(smem_u32(&bar_o[1]), odd_other, abort_flag);
@@ -1169,9 +1221,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.job_q0[blockIdx.x] = q.q0;
         }
       }
-      mbar_arrive(smem_u32(&bar_done));
-      part_done();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bar_part_empty[here.at]));
+      ok = again;
     }
+    cp_async_wait_all();  // also where a wait ran out
   }
   tc_fence_before();
   __syncthreads();
