@@ -203,3 +203,59 @@ def test_vision_positions_outside_the_table(tts):
     assert int(st.item()) == tts.TTS_DEV_INDEX_RANGE
     assert bool((q[[7, 11]] == 0).all()) and bool((k[[7, 11]] == 0).all())
     assert bool((v[[7, 11]] != 0).any()) and bool((q[8] != 0).any())
+
+
+@pytest.mark.parametrize("d,heads", [(64, 8), (128, 4), (80, 6)])
+def test_vision_rows_do_not_depend_on_the_others(tts, d, heads):
+    """A token's row is the same to the bit in a call of few tokens, whose tiles are one head's, and in
+    one of many: every element is the same products in the same order."""
+    g = torch.Generator("cpu").manual_seed(d)
+    n, hidden = 2400, 192
+    x = torch.randn(n, hidden, generator=g).to(torch.bfloat16).cuda()
+    w = (torch.randn(3 * heads * d, hidden, generator=g) * 0.1).to(torch.bfloat16).cuda()
+    bias = torch.randn(3 * heads * d, generator=g).cuda()
+    pos = torch.randint(0, 64, (2, n), generator=g, dtype=torch.int32).cuda()
+    cs, axis = tts.rope_cache(64, d, device="cuda"), tts.rope_axes([d // 8, d // 2 - d // 8])
+    full = tts.qkv_rope_axes(x, w, bias, pos, axis, cs, heads)
+    plain = tts.qkv_rope(x, w, bias, pos[1].contiguous(), cs, heads)
+    for m in (1, 130, 256, 500):
+        few = tts.qkv_rope_axes(x[:m], w, bias, pos[:, :m].contiguous(), axis, cs, heads)
+        assert all(torch.equal(a, b[:m]) for a, b in zip(few, full)), m
+        few = tts.qkv_rope(x[:m], w, bias, pos[1, :m].contiguous(), cs, heads)
+        assert all(torch.equal(a, b[:m]) for a, b in zip(few, plain)), m
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_vision_behind_what_writes_its_inputs(tts, captured):
+    """The projection may be set up while the launch before it runs: it reads what that one wrote."""
+    g = torch.Generator("cpu").manual_seed(5)
+    n, hidden, heads, d = 700, 256, 4, 64
+    w = (torch.randn(3 * heads * d, hidden, generator=g) * 0.1).to(torch.bfloat16).cuda()
+    pos = torch.randint(0, 64, (2, n), generator=g, dtype=torch.int32).cuda()
+    cs, axis = tts.rope_cache(64, d, device="cuda"), tts.rope_axes([d // 4, d // 4])
+    xs = [torch.randn(n, hidden, generator=g).to(torch.bfloat16).cuda() for _ in range(8)]
+    want = [[t.clone() for t in tts.qkv_rope_axes(x, w, None, pos, axis, cs, heads)] for x in xs]
+    x = torch.empty_like(xs[0])
+    out = [torch.empty(n, heads, d, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    got = [[torch.empty_like(t) for t in out] for _ in xs]
+
+    def steps():
+        for src, dst in zip(xs, got):
+            x.copy_(src)
+            tts.qkv_rope_axes(x, w, None, pos, axis, cs, heads, *out)
+            for a, b in zip(dst, out):
+                a.copy_(b)
+
+    steps()
+    if captured:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            steps()
+        for dst in got:
+            for t in dst:
+                t.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))

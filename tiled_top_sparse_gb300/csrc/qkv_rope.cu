@@ -38,7 +38,8 @@
 // kAxes: a token has positions on up to four axes (row, column; time in front of them for video), and
 // every pair's axis chooses the one that it turns by. Only the fetch of a tile's cos/sin rows
 // differs, which runs while the tile's products do: 8547 patches of 1280 into 16 heads of 80 take
-// 57.5 us in a CUDA graph (1.46 PFLOP/s, 0.76 of a large bf16 product's rate), as without axes.
+// 57.1 us in a CUDA graph (1.47 PFLOP/s, 0.77 of a large bf16 product's rate), as without axes; 8500 of
+// 512 into 16 heads of 128 106 us (97 without axes; 160 with each pair's turn chosen by itself).
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -46,6 +47,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace tts {
@@ -55,12 +57,18 @@ constexpr int kQkvThreads = 192;
 constexpr int kBM = 128;  // tokens per CTA (256 per CTA pair)
 constexpr int kBK = 64;   // hidden columns per stage (one 128-byte swizzle row)
 
-template <int D>
+// Heads of a tile: as many as fill the MMA's N. Where tiles of one head each all run at the same time,
+// one tile's products and its epilogue are what the call takes, and one head it is (512 hidden columns,
+// 8 heads of 64, axes: 768 tokens 10.4 -> 6.9 us, CUDA graph; 8 of 128 21.5 -> 10.1. In two rounds, 1000
+// tokens, 10.5 with full tiles and 11.0 with one head). Not heads of 80, whose N is no multiple of 32.
+constexpr int full_tile(int d) { return d == 80 ? 3 : 256 / d; }
+constexpr int least_tile(int d) { return d == 80 ? 3 : 1; }
+template <int D, int kHeads>
 struct QkvCfg {
-  static constexpr int kHpt = (D == 80) ? 3 : 256 / D;  // heads per tile
-  static constexpr int kBN = kHpt * D;                  // MMA N: 240 / 256 / 256
+  static constexpr int kHpt = kHeads;
+  static constexpr int kBN = kHpt * D;                  // MMA N: 240 / 256 / 256 (or D)
   static constexpr int kBNh = kBN / 2;                  // W rows staged by each CTA
-  static constexpr int kStages = 6;
+  static constexpr int kStages = kBN >= 240 ? 6 : 8;
   static constexpr int kABytes = kBM * 128;
   static constexpr int kBBytes = kBNh * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
@@ -69,6 +77,7 @@ struct QkvCfg {
   static_assert(kBN % 16 == 0 && kBN <= 256 && kBNh % 8 == 0, "MMA N");
   static_assert(kStageBytes % 1024 == 0 && kABytes % 1024 == 0, "swizzle atoms");
   static_assert(kSmemBytes + 256 + kBN * 4 <= 232448, "shared memory");
+  static_assert(kSmemBytes > 232448 / 2, "one CTA per SM: each takes all of TMEM");
 };
 
 struct QkvMaps {
@@ -199,10 +208,10 @@ __device__ __forceinline__ bool warp_spin_cl(uint32_t bar, uint32_t parity, vola
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-template <int D, bool kAxes>
+template <int D, int kHeads, bool kAxes>
 __global__ void __launch_bounds__(kQkvThreads, 1)
     qkv_rope_kernel(const __grid_constant__ QkvMaps maps, const QkvParamsFor<kAxes> p) {
-  using C = QkvCfg<D>;
+  using C = QkvCfg<D, kHeads>;
   constexpr int NS = C::kStages;
   constexpr int H2 = D / 2;
   extern __shared__ uint8_t smem_raw[];
@@ -239,6 +248,7 @@ __global__ void __launch_bounds__(kQkvThreads, 1)
     tmem_alloc_pair(smem_u32(&s_tmem), 512);
     tmem_relinquish_pair();
   }
+  wait_for_prior_grids();
   tc_fence_before();
   pair_sync();  // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after();
@@ -377,17 +387,17 @@ __global__ void __launch_bounds__(kQkvThreads, 1)
           }
         }
       }
+      auto row_at = [&](uint32_t x) -> const float2* {  // axes: the table's row of one of them
+        const int q = x & 2 ? (x & 1 ? at[3] : at[2]) : (x & 1 ? at[1] : at[0]);
+        return p.cos_sin + static_cast<int64_t>(q) * H2;
+      };
       // cos / sin of pairs 2u and 2u + 1
       auto turn_of = [&](int u) -> float4 {
         if constexpr (kAxes) {
           const uint32_t w = static_cast<uint32_t>(p.pair_axis[u >> 4] >> (4 * (u & 15)));
-          auto row_at = [&](uint32_t x) -> const float2* {
-            const int q = x & 2 ? (x & 1 ? at[3] : at[2]) : (x & 1 ? at[1] : at[0]);
-            return p.cos_sin + static_cast<int64_t>(q) * H2 + 2 * u;
-          };
           const uint32_t x0 = w & 3, x1 = (w >> 2) & 3;
-          if (x0 == x1) return __ldg(reinterpret_cast<const float4*>(row_at(x0)));
-          const float2 a = __ldg(row_at(x0)), b = __ldg(row_at(x1) + 1);
+          if (D <= 80 && x0 == x1) return __ldg(reinterpret_cast<const float4*>(row_at(x0) + 2 * u));
+          const float2 a = __ldg(row_at(x0) + 2 * u), b = __ldg(row_at(x1) + 2 * u + 1);
           return make_float4(a.x, a.y, b.x, b.y);
         } else {
           return __ldg(cs4 + u);
@@ -417,53 +427,74 @@ __global__ void __launch_bounds__(kQkvThreads, 1)
         uint8_t* myrow = obuf + lane * (D * 2);
         if (live) {
           uint4 packed[D / 8];  // the head's D bf16 results, written after the wait below
-          uint32_t r[D];  // the head's D accumulator columns of this row, one round trip
+          // The head's accumulator columns of this row, one round trip; heads of 128 with axes in four
+          // parts, each with its turns asked for together.
+          constexpr int kParts = kAxes && !kCsRegs ? 4 : 1, HP = H2 / kParts;
 #pragma unroll
-          for (int c = 0; c < D; c += 8)
-            tmem_ld8(tcol + c, *reinterpret_cast<uint32_t(*)[8]>(&r[c]));
-          tmem_ld_wait();
+          for (int p0 = 0; p0 < H2; p0 += HP) {
+            uint32_t r[2 * HP];
+            [[maybe_unused]] float4 turns[kParts > 1 ? HP / 2 : 1];
+            if constexpr (kParts > 1) {
+              // 16 pairs, two bits each: mostly of one axis
+              const uint32_t axes = static_cast<uint32_t>(p.pair_axis[p0 / 32] >> (2 * (p0 % 32)));
+              if (rot && axes == (axes & 3) * 0x55555555u) {
+                const float4* from = reinterpret_cast<const float4*>(row_at(axes & 3)) + p0 / 2;
 #pragma unroll
-          for (int j0 = 0; j0 < H2; j0 += 8) {
-            float ylo[8], yhi[8];
-            const float4 b0 = b4[j0 / 4], b1 = b4[j0 / 4 + 1];
-            const float4 c0 = b4[(H2 + j0) / 4], c1 = b4[(H2 + j0) / 4 + 1];
-            const float bl[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-            const float bh[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                for (int u = 0; u < HP / 2; ++u) turns[u] = __ldg(from + u);
+              } else if (rot) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              ylo[u] = __uint_as_float(r[j0 + u]) + bl[u];
-              yhi[u] = __uint_as_float(r[H2 + j0 + u]) + bh[u];
-            }
-            if (rot) {
-              float cs[16];  // (cos, sin) of pairs j0 .. j0+7
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const float4 v = kCsRegs ? csr[(j0 / 2 + u) % (kCsRegs ? H2 / 2 : 1)]
-                                         : turn_of(j0 / 2 + u);
-                cs[4 * u] = v.x;
-                cs[4 * u + 1] = v.y;
-                cs[4 * u + 2] = v.z;
-                cs[4 * u + 3] = v.w;
+                for (int u = 0; u < HP / 2; ++u) turns[u] = turn_of(p0 / 2 + u);
               }
+            }
+#pragma unroll
+            for (int c = 0; c < 2 * HP; c += 8)
+              tmem_ld8(tcol + p0 + c + (c < HP ? 0 : H2 - HP), *reinterpret_cast<uint32_t(*)[8]>(&r[c]));
+            tmem_ld_wait();
+#pragma unroll
+            for (int j1 = 0; j1 < HP; j1 += 8) {
+              const int j0 = p0 + j1;
+              float ylo[8], yhi[8];
+              const float4 b0 = b4[j0 / 4], b1 = b4[j0 / 4 + 1];
+              const float4 c0 = b4[(H2 + j0) / 4], c1 = b4[(H2 + j0) / 4 + 1];
+              const float bl[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+              const float bh[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
               for (int u = 0; u < 8; ++u) {
-                const float c = pos_ok ? cs[2 * u] : 0.f, s = pos_ok ? cs[2 * u + 1] : 0.f;
-                const float a0 = ylo[u], b0 = yhi[u];
-                ylo[u] = fmaf(a0, c, -b0 * s);
-                yhi[u] = fmaf(a0, s, b0 * c);
+                ylo[u] = __uint_as_float(r[j1 + u]) + bl[u];
+                yhi[u] = __uint_as_float(r[HP + j1 + u]) + bh[u];
               }
+              if (rot) {
+                float cs[16];  // (cos, sin) of pairs j0 .. j0+7
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const float4 v = kCsRegs      ? csr[(j0 / 2 + u) % (kCsRegs ? H2 / 2 : 1)]
+                                   : kParts > 1 ? turns[(j1 / 2 + u) % (kParts > 1 ? HP / 2 : 1)]
+                                                : turn_of(j0 / 2 + u);
+                  cs[4 * u] = v.x;
+                  cs[4 * u + 1] = v.y;
+                  cs[4 * u + 2] = v.z;
+                  cs[4 * u + 3] = v.w;
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                  const float c = pos_ok ? cs[2 * u] : 0.f, s = pos_ok ? cs[2 * u + 1] : 0.f;
+                  const float a0 = ylo[u], b0 = yhi[u];
+                  ylo[u] = fmaf(a0, c, -b0 * s);
+                  yhi[u] = fmaf(a0, s, b0 * c);
+                }
+              }
+              uint4 plo, phi;
+              plo.x = pack_bf16x2(ylo[0], ylo[1]);
+              plo.y = pack_bf16x2(ylo[2], ylo[3]);
+              plo.z = pack_bf16x2(ylo[4], ylo[5]);
+              plo.w = pack_bf16x2(ylo[6], ylo[7]);
+              phi.x = pack_bf16x2(yhi[0], yhi[1]);
+              phi.y = pack_bf16x2(yhi[2], yhi[3]);
+              phi.z = pack_bf16x2(yhi[4], yhi[5]);
+              phi.w = pack_bf16x2(yhi[6], yhi[7]);
+              packed[j0 / 8] = plo;
+              packed[(H2 + j0) / 8] = phi;
             }
-            uint4 plo, phi;
-            plo.x = pack_bf16x2(ylo[0], ylo[1]);
-            plo.y = pack_bf16x2(ylo[2], ylo[3]);
-            plo.z = pack_bf16x2(ylo[4], ylo[5]);
-            plo.w = pack_bf16x2(ylo[6], ylo[7]);
-            phi.x = pack_bf16x2(yhi[0], yhi[1]);
-            phi.y = pack_bf16x2(yhi[2], yhi[3]);
-            phi.z = pack_bf16x2(yhi[4], yhi[5]);
-            phi.w = pack_bf16x2(yhi[6], yhi[7]);
-            packed[j0 / 8] = plo;
-            packed[(H2 + j0) / 8] = phi;
           }
           // The previous head's store must be done reading the staging buffer; it was
           // issued before this head's TMEM loads and arithmetic, which hide most of it.
@@ -507,8 +538,8 @@ __global__ void __launch_bounds__(kQkvThreads, 1)
   }
 }
 
-// Co-resident CTA pairs of qkv_rope_kernel<D, kAxes> on the current device (cached per device).
-template <int D, bool kAxes>
+// Co-resident CTA pairs of qkv_rope_kernel<D, kHeads, kAxes> on the current device (cached per device).
+template <int D, int kHeads, bool kAxes>
 int max_pairs(int dev, const cudaLaunchConfig_t& cfg) {
   // Host threads may make their first calls at the same time: every thread that finds
   // the slot empty computes the same value, and the slot is read and written atomically.
@@ -518,7 +549,7 @@ int max_pairs(int dev, const cudaLaunchConfig_t& cfg) {
     if (c > 0) return c;
   }
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, qkv_rope_kernel<D, kAxes>, &cfg) != cudaSuccess || n < 1) {
+  if (cudaOccupancyMaxActiveClusters(&n, qkv_rope_kernel<D, kHeads, kAxes>, &cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();
     int sms = 0;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -528,9 +559,9 @@ int max_pairs(int dev, const cudaLaunchConfig_t& cfg) {
   return n;
 }
 
-template <int D, bool kAxes>
-cudaError_t launch_qkv_d(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
-  using C = QkvCfg<D>;
+template <int D, int kHeads, bool kAxes>
+cudaError_t launch_qkv_tiles(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
+  using C = QkvCfg<D, kHeads>;
   QkvMaps maps;
   const uint64_t n = static_cast<uint64_t>(a.n);
   const uint64_t hidden = static_cast<uint64_t>(a.hidden);
@@ -576,14 +607,19 @@ cudaError_t launch_qkv_d(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(qkv_rope_kernel<D, kAxes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(qkv_rope_kernel<D, kHeads, kAxes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  e = cudaStreamIsCapturing(stream, &capture);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];  // the second as in launch_ahead
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kQkvThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmemBytes;
@@ -591,12 +627,26 @@ cudaError_t launch_qkv_d(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(2, 1, 1);
-  const int pairs_max = max_pairs<D, kAxes>(dev, cfg);
+  const int pairs_max = max_pairs<D, kHeads, kAxes>(dev, cfg);
   const int pairs = static_cast<int>(n_tiles < pairs_max ? n_tiles : pairs_max);
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  e = cudaLaunchKernelEx(&cfg, qkv_rope_kernel<D, kAxes>, maps, p);
+  cfg.numAttrs = capture == cudaStreamCaptureStatusNone ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, qkv_rope_kernel<D, kHeads, kAxes>, maps, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+template <int D, bool kAxes>
+cudaError_t launch_qkv_d(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
+  if constexpr (least_tile(D) < full_tile(D)) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (a.n + 2 * kBM - 1) / (2 * kBM) * 3 * a.heads;
+    if (tiles <= sms / 2) return launch_qkv_tiles<D, least_tile(D), kAxes>(a, drv_err, stream);
+  }
+  return launch_qkv_tiles<D, full_tile(D), kAxes>(a, drv_err, stream);
 }
 
 // The cos/sin table: pair j of position p turns by p * base^(-2j/rot_dim). The angle
@@ -628,12 +678,7 @@ cudaError_t launch_qkv(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
 }  // namespace
 
 int qkv_heads_per_tile(int head_dim) {
-  switch (head_dim) {
-    case 64: return QkvCfg<64>::kHpt;
-    case 80: return QkvCfg<80>::kHpt;
-    case 128: return QkvCfg<128>::kHpt;
-    default: return 0;
-  }
+  return head_dim == 64 || head_dim == 80 || head_dim == 128 ? full_tile(head_dim) : 0;
 }
 
 cudaError_t launch_qkv_rope(const QkvArgs& a, int* drv_err, cudaStream_t stream) {
