@@ -331,3 +331,32 @@ def test_random_calls(tts):
         Case(100 + i, new if max(new) else [1] * b, kv, hq, hkv, int(rng.choice([64, 128])),
              int(rng.choice([16, 32, 64, 128])), bool(rng.integers(2)), w, s).check(
                  tts, [torch.float32, torch.bfloat16][rng.integers(2)])
+
+
+@pytest.mark.parametrize("f8", [True, False])
+@pytest.mark.parametrize("new,kv,hq,hkv,d,window", [
+    ([3], [9000], 4, 1, 128, 0),             # one unit in as many parts as it has tiles
+    ([64], [5000], 8, 1, 64, 0),             # two blocks of 256 rows, a tile counting twice
+    ([40], [3003], 8, 1, 128, 700),          # one of 256 and one of 64 rows
+    ([5, 0, 16], [7000, 300, 2100], 16, 2, 128, 0),  # a request without tokens between two
+    ([4, 9], [0, 6001], 4, 2, 64, 0),        # nothing cached
+    ([64, 1], [65, 8191], 20, 2, 128, 0),    # whole units beside cut ones, odd groups
+])
+def test_few_units_in_many_parts(tts, f8, new, kv, hq, hkv, d, window):
+    """The workspace holds NaN before the call: what is read from it was written by the call."""
+    c = Case(7, new, kv, hq, hkv, d, 64, f8, window=window, sinks=3 if window else 0)
+    need = tts.attn_decode_tree_workspace_bytes(max(new), hq, hkv, d)
+    for out_dtype in (torch.float32, torch.bfloat16):
+        c.check(tts, out_dtype, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+
+
+def test_parts_of_rows_that_follow_in_one_run(tts):
+    """Runs of many short units of 1 to 256 rows, e4m3 and bf16: the q rows of the next are written, and
+    its first scores computed, while the sums of one leave."""
+    rng = np.random.default_rng(11)
+    for f8, d in ((True, 128), (True, 64), (False, 128), (False, 64)):
+        new = [int(x) for x in rng.choice([1, 2, 15, 16, 17, 33, 64], 90)]
+        kv = [n + int(x) for n, x in zip(new, rng.choice([0, 1, 63, 128, 300], 90))]
+        c = Case(12, new, kv, 16, 4, d, 32, f8)
+        need = tts.attn_decode_tree_workspace_bytes(64, 16, 4, d)
+        c.check(tts, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
