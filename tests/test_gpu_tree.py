@@ -360,3 +360,59 @@ def test_parts_of_rows_that_follow_in_one_run(tts):
         c = Case(12, new, kv, 16, 4, d, 32, f8)
         need = tts.attn_decode_tree_workspace_bytes(64, 16, 4, d)
         c.check(tts, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+
+
+def zero_keys(c, pages=None):
+    """The keys that some token sees become zeros on these pages (None: on all), with the scale that a
+    page of zeros is given; the others keep what they hold."""
+    at = range(c.c[0].shape[0]) if pages is None else pages
+    for p in at:
+        if c.f8:
+            c.c[0][p] = torch.where(c.c[0][p] == 0x7F, c.c[0][p], torch.zeros_like(c.c[0][p]))
+            c.s[0][p] = 2.0 ** -60
+        else:
+            c.c[0][p] = torch.where(c.c[0][p].isnan(), c.c[0][p], torch.zeros_like(c.c[0][p]))
+
+
+@pytest.mark.parametrize("f8", [True, False])
+@pytest.mark.parametrize("new,kv,hq,hkv,d,ps,window,sinks", [
+    ([1], [1], 1, 1, 128, 64, 0, 0),                  # one visible key
+    ([9, 3], [90, 20], 4, 2, 128, 16, 0, 0),          # one tile
+    ([9, 3], [90, 20], 4, 2, 64, 64, 0, 0),
+    ([5], [2590], 8, 2, 64, 64, 0, 0),                # one request in many parts
+    ([16, 1, 7], [900, 130, 7], 8, 2, 128, 32, 0, 0),
+    ([64, 40], [700, 64], 8, 2, 128, 64, 0, 0),       # up to 256 rows: both warpgroups a q tile each
+    ([12, 20] * 20, [300, 77] * 20, 4, 2, 128, 64, 100, 3),  # a window, more units than parts
+    ([30, 64], [500, 300], 8, 2, 64, 16, 70, 2),
+])
+def test_rows_of_zeros_over_keys_of_zeros(tts, f8, new, kv, hq, hkv, d, ps, window, sinks):
+    """Rows of zero q over pages of zero keys, as padding leaves them: the mean of the visible values, and
+    whatever hidden keys and values hold. Zeros on one side alone, too."""
+    for all_q, pages in ((True, None), (False, None), (True, "last"), (False, "last")):
+        c = Case(sum(kv) + ps, new, kv, hq, hkv, d, ps, f8, window, sinks)
+        zero_keys(c, None if pages is None else
+                  [int(c.tables[r, (L - 1) // ps]) for r, L in enumerate(kv)])
+        c.q[slice(None) if all_q else slice(0, None, 2)] = 0
+        c.check(tts)
+
+
+def test_zero_values_beside_others(tts):
+    """Pages whose values are zeros, with the scale that they are given, among pages with others."""
+    c = Case(67, [9, 20], [300, 90], 4, 2, 128, 32, True)
+    for p in (int(c.tables[0, 1]), int(c.tables[1, 2])):
+        c.c[1][p] = torch.where(c.c[1][p] == 0x7F, c.c[1][p], torch.zeros_like(c.c[1][p]))
+        c.s[1][p] = 2.0 ** -60
+    c.q[3] = 0
+    zero_keys(c, [int(c.tables[0, 1])])
+    c.check(tts)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-45])
+def test_the_smallest_scales(tts, scale):
+    """A scale whose product with a page's underflows: every visible key has the same weight."""
+    for f8 in (True, False):
+        c = Case(71, [9, 3], [400, 20], 4, 2, 128, 64, f8)
+        c.scale = scale
+        if f8:
+            c.s[0][:] = 2.0 ** -40
+        c.check(tts)

@@ -404,3 +404,37 @@ def test_another_stream(tts):
         got = attend(tts, z, q)
     st.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("f8", [True, False])
+@pytest.mark.parametrize("d,ps", [(128, 64), (64, 16)])
+def test_a_step_at_positions_outside_the_table(tts, f8, d, ps):
+    """Tokens outside the rotation table are cached with zero keys and get zero queries: on fresh pages their
+    attention is the mean of the values that they see. A padded batch of zeros is the same."""
+    new, hq, hkv = [12, 1, 30], 8, 2
+    rng = np.random.default_rng(d)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    masks = [m for n in new for m in tree_ref.masks_of(tree_ref.random_tree(rng, n))]
+    tables = np.arange(9).reshape(3, 3).astype(np.int32)
+    for max_pos, gain in ((4, 1.0), (400, 0.0)):
+        c = cache(10, hkv, ps, d, f8)
+        x = torch.tensor(rng.standard_normal((43, hq + 2 * hkv, d)))
+        x[:, :hq + hkv] *= gain
+        x = x.to(torch.bfloat16).cuda()
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q, _ = tts.rope_kv_append_axes(
+            x[:, hq:hq + hkv], x[:, hq + hkv:], *c[:2], cuda(tables), cuda([0, 0, 0]), cuda(cu), 30,
+            cuda(np.arange(100, 143)[None]), tts.rope_axes([d // 2]), tts.rope_cache(max_pos, d),
+            k_scale=c[2], v_scale=c[3], q=x[:, :hq], status=st)
+        assert int(st.item()) == (tts.TTS_DEV_INDEX_RANGE if gain else 0)
+        assert bool((q == 0).all())
+        st.zero_()
+        out, lse = tts.attn_decode_tree(q, *c[:2], cuda(tables), cuda(new), masks_tensor(masks), d ** -0.5,
+                                        cuda(cu), 30, k_scale=c[2], v_scale=c[3], status=st)
+        tts.check_status(st)
+        s = [None if t is None else t.cpu().numpy() for t in c[2:]]
+        o, l, tol, tol_l = tree_ref.attend_tree(
+            q.float().cpu().numpy(), ref.codes_of(c[0]), ref.codes_of(c[1]), *s, tables, new, cu, masks,
+            d ** -0.5, 0, 0)
+        assert bool((np.abs(out.cpu().double().numpy() - o) <= tol).all())
+        assert bool((np.abs(lse.cpu().double().numpy() - l) <= tol_l).all())

@@ -995,6 +995,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         fac *= __uint_as_float((uint32_t)(ex < 8 ? 1 : ex - 7) << 23);
       }
       odd_q ^= 1;
+      // A tile's scores by a page's key scale. Kept above 0 where the product underflows (a row of zeros,
+      // whose factor is 2^-107 of the scale, over a page of zeros, whose scale is 2^-60): hidden keys hold
+      // -inf in front of it, and -inf times 0 is NaN. Scores are below 2^25, so that a visible one stays
+      // under 2^-101, which moves no weight.
+      auto factor = [&](float key_scale) -> float { return fmaxf(fac * key_scale, 0x1p-126f); };
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < q.T; ++j, mslot.next(), kslot.next()) {  // tile of the part
         if (alt && (j & 1) != w) continue;
@@ -1024,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < TK / 32; ++c) {
             if constexpr (F8) {
               const float4 sc = meta.scale[(2 * c) >> piece_shift];
-              most[c] = fmaf(most[c], fac * sc.x, sc.y);
+              most[c] = fmaf(most[c], factor(sc.x), sc.y);
             }
             tile_max = fmaxf(tile_max, most[c]);
           }
@@ -1050,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
                 const float4 sc = meta.scale[(2 * c + u) >> piece_shift];
-                tile_max = fmaxf(tile_max, fmaf(row_max<16>(s + 16 * u), fac * sc.x, sc.y));
+                tile_max = fmaxf(tile_max, fmaf(row_max<16>(s + 16 * u), factor(sc.x), sc.y));
               }
             } else {
               tile_max = fmaxf(tile_max, row_max<32>(s));
@@ -1081,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float a = fac, add = shift, inv = 1.f;
             if constexpr (F8) {
               const float4 sc = meta.scale[(2 * c + h) >> piece_shift];
-              a = fac * sc.x;
+              a = factor(sc.x);
               add = shift + sc.y;
               inv = sc.z;
             }
