@@ -219,6 +219,25 @@ def test_compact_after_an_append_of_a_tree(tts):
             assert torch.equal(a[tables[0, i // ps], :, i % ps], b[tables[0, i // ps], :, i % ps])
 
 
+def test_compact_entries_at_the_end_of_32_bits(tts):
+    """A last entry up to the largest int lies behind the table, whatever the sum would be in 32 bits:
+    said, and nothing of that request is moved."""
+    rng = np.random.default_rng(11)
+    top = 2 ** 31 - 1
+    past = [5, 0, 40, 10, 1]
+    path = [[0, top], [top], list(range(39)) + [top], [2, top - 9], [0, 3]]
+    tables, pages, _ = tables_for(rng, [60] * 5, 16)
+    for f8 in (True, False):
+        c, s = pool(rng, pages, 2, 16, 64, f8, -3, -3)
+        got, out, st = compact(tts, c, s, tables, past, path)
+        assert st == tts.TTS_DEV_INDEX_RANGE
+        np.testing.assert_array_equal(out.cpu().numpy(), [5, 0, 40, 10, 3])
+        want = [t.clone() for t in c]
+        for t, o in zip(want, c):
+            t[tables[4, 0], :, 2] = o[tables[4, 0], :, 4]
+        assert all(torch.equal(a.cpu(), b) for a, b in zip(got[:2], want))
+
+
 # --------------------------------------------------------------------------------- fork
 def run_fork(tts, c, s, tables, kv, parents, new_pages, **kw):
     d = [cuda(t) for t in (*c, *s)]

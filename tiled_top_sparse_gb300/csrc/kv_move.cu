@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
     if (__any_sync(kAll, wrong)) bad |= kDevBadArg;
   }
   const int last0 = __shfl_sync(kAll, at[0], (m - 1) & 31), last1 = __shfl_sync(kAll, at[1], (m - 1) & 31);
-  const int64_t end = (int64_t)past + (m == 0 ? 0 : (m > 32 ? last1 : last0) + 1);
+  // in 64 bits: a path's entries may be any int
+  const int64_t last = m == 0 ? -1 : m > 32 ? last1 : last0, end = past + last + 1;
   if (past < 0 || end > ((int64_t)p.max_pages << p.page_shift)) bad |= kDevIndexRange;
   if (first && lane == 0) {
     p.kv_lens[r] = bad ? (past > 0 ? past : 0) : past + m;
