@@ -238,6 +238,31 @@ def test_compact_entries_at_the_end_of_32_bits(tts):
         assert all(torch.equal(a.cpu(), b) for a, b in zip(got[:2], want))
 
 
+def test_compact_rows_of_zeros_between_far_scales(tts):
+    """Zero rows of a page with a huge scale stay zeros in a page whose scale is 2^160 times smaller; NaN
+    codes beside them stay NaN, and rows with values make the page's scale grow."""
+    rng = np.random.default_rng(12)
+    tables, pages, _ = tables_for(rng, [70, 70], 16)
+    c, s = pool(rng, pages, 2, 16, 128, True, -3, -3)
+    for x, sc in zip(c, s):
+        for r in range(2):
+            sc[int(tables[r, 0])] = 2.0 ** -60  # a page that was begun with zeros
+            x[int(tables[r, 0])] = 0
+            sc[int(tables[r, 2])] = 2.0 ** 100  # beside a huge row
+            x[int(tables[r, 2]), :, :6] = 0
+            x[int(tables[r, 2]), :, 3, 5] = 0x7F
+            x[int(tables[r, 2]), :, 4, 9] = 0xFF
+    past, path = [8, 8], [[0, 24, 25, 26, 27, 28, 29], [0, 24, 27, 31]]  # the last: row 39, with values
+    want = tree_ref.compact(values(c[0]), values(c[1]), s[0].numpy(), s[1].numpy(), tables, past, path,
+                            [7, 4])
+    got, out, st = compact(tts, c, s, tables, past, path)
+    assert st == 0
+    np.testing.assert_array_equal(out.cpu().numpy(), want[4])
+    same(got, want[:4])
+    assert float(got[2][int(tables[0, 0]), 0]) == 2.0 ** -60
+    assert float(got[2][int(tables[1, 0]), 0]) > 2.0 ** 90
+
+
 # --------------------------------------------------------------------------------- fork
 def run_fork(tts, c, s, tables, kv, parents, new_pages, **kw):
     d = [cuda(t) for t in (*c, *s)]

@@ -1,7 +1,9 @@
 // Rows moved inside the paged grouped-query cache: the accepted path of a drafted tree brought
 // together behind the cached tokens (compact), and requests that continue another one's tokens in
 // pages of their own (fork). The cache is laid out as in kv_append.cu: [page, KV head, slot, d].
+#include <cfloat>
 #include <cstdint>
+
 #include <cuda_runtime.h>
 
 #include "e4m3.cuh"
@@ -201,7 +203,8 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
       const int64_t dst = row64(to, b0 + x / kCpr);
       if constexpr (kF8) {
         const float s = rowf(s_from, b0 + x / kCpr);
-        if (s != scale) held[k] = rescale16(held[k], s / scale);
+        // finite also where scales lie further apart than fp32 reaches: such a row is zeros
+        if (s != scale) held[k] = rescale16(held[k], fminf(s / scale, FLT_MAX));
       }
       if (x < pieces && dst >= 0) rows[dst * kCpr + x % kCpr] = held[k];
     }
