@@ -530,6 +530,8 @@ tts_status tts_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_sc
  * and pages without a visible key are not read (their table entries may be anything).
  * The value scales of a request's visible pages lie within 2^100 of one another (a weight is
  * held times its page's value scale in fp32).
+ * Scores s_j lie below 2^22 in size: from there on their fp32 differences, which the weights are
+ * powers of, are off by steps that no longer fit the weights' types (out may be NaN).
  *
  * q           device bf16 [total_q, num_heads_q, head_dim]; rows outside every request are
  *             not read, and their out / lse rows are left as they were

@@ -416,3 +416,59 @@ def test_the_smallest_scales(tts, scale):
         if f8:
             c.s[0][:] = 2.0 ** -40
         c.check(tts)
+
+
+@pytest.mark.parametrize("f8", [True, False])
+@pytest.mark.parametrize("new,kv,hq,hkv,d,ps", [
+    ([9, 3], [300, 20], 4, 2, 128, 64),
+    ([5], [2590], 8, 2, 64, 16),
+    ([64], [700], 8, 2, 128, 32),
+])
+@pytest.mark.parametrize("exp", [10, 20, 22])
+def test_scores_up_to_their_limit(tts, f8, new, kv, hq, hkv, d, ps, exp):
+    """Scores up to 2^exp in units of log2: finite, and the value of the key with the largest score where that
+    one leads by more than scores are off. Masks of a chain, so that plain decoding is the same."""
+    masks = [(1 << (i + 1)) - 1 for n in new for i in range(n)]
+    c = Case(73 + exp, new, kv, hq, hkv, d, ps, f8, masks=masks, gain=16.0)
+    if f8:
+        c.s[0][:] = 2.0 ** -3
+    k, v = (np.nan_to_num(ref.codes_of(t)) for t in c.c)
+    s = [1.0 if t is None else t.numpy()[:, :, None, None] for t in c.s]
+    k, v = k * s[0], v * s[1]
+    rows, most = [], 0
+    for r, (n, L) in enumerate(zip(new, kv)):
+        j = np.arange(L)
+        at = (c.tables[r, j // ps], slice(None), j % ps)
+        for i in range(n):
+            q = c.q[c.cu[r] + i].double().numpy().reshape(hkv, hq // hkv, d)
+            see = tree_ref.sees(masks[c.cu[r] + i], n, L, 0, 0)
+            K, V = k[at][see].transpose(1, 0, 2), v[at][see].transpose(1, 0, 2)
+            x = q @ K.transpose(0, 2, 1) * np.log2(np.e)
+            most = max(most, np.abs(x).max())
+            # products summed in fp32, q over e4m3 keys to 2^-17 of its row's largest value
+            off = 3 * d * 2.0 ** -24 * (np.abs(q) @ np.abs(K).transpose(0, 2, 1)).max(-1) + \
+                2.0 ** -16 * np.abs(q).max(-1) * np.abs(K).sum(-1).max()
+            rows.append((x, off * np.log2(np.e), V))
+    c.scale = float(np.float32(2.0 ** exp / most))
+    dev = [None if t is None else t.cuda() for t in (*c.c, *c.s)]
+    plain = tts.attn_decode_paged(
+        c.q.cuda(), dev[0], dev[1], torch.tensor(c.tables).cuda(),
+        torch.tensor(c.kv, dtype=torch.int32).cuda(), c.scale, torch.tensor(c.cu).cuda(), max(new),
+        k_scale=dev[2], v_scale=dev[3])
+    for out, lse in (c.run(tts), plain):
+        got = out.cpu().double().numpy().reshape(len(rows), hkv, hq // hkv, d)
+        l = lse.cpu().double().numpy().reshape(len(rows), hkv, hq // hkv)
+        assert np.isfinite(got).all() and np.isfinite(l).all()
+        led = 0
+        for (x, off, V), o, lo in zip(rows, got, l):
+            x, off = x * c.scale, off * c.scale + 8
+            top = np.sort(x, -1)
+            lead = top[..., -1] - top[..., -2] if x.shape[-1] > 1 else np.full(x.shape[:2], np.inf)
+            for g, h in zip(*np.nonzero(lead > 2 * off + 40)):
+                led += 1
+                want = V[g, x[g, h].argmax()]
+                # the weight is rounded to fp16 or bf16; the others are under 2^-25 of it
+                assert (np.abs(o[g, h] - want) <= 2.0 ** (-9 if f8 else -7) * np.abs(want)
+                        + 2.0 ** -25 * np.abs(V[g]).sum(0)).all()
+                assert abs(lo[g, h] * np.log2(np.e) - top[g, h, -1]) <= off[g, h] + 20
+        assert led > 0 or exp < 20

@@ -885,7 +885,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ softmax
     take_registers<kSoftmaxRegs>();
     constexpr float kThr = F8 ? 4.f : 8.f;    // the reference moves when exceeded by 2^kThr
-    constexpr float kBias = F8 ? 11.f : 0.f;  // weights are held times 2^kBias: at most 2^15 in fp16
+    // Weights are held times 2^kBias: at most 2^15 in fp16, where three roundings of scores below 2^23 (in
+    // units of log2; steps of 1/2) add up to 3/4.
+    constexpr float kBias = F8 ? 11.f : 0.f;
     const int w = (warp - 4) >> 2;
     const int lane_row = ((warp & 3) << 5) + lane;  // TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
