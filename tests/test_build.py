@@ -50,3 +50,19 @@ def test_a_missing_binding_is_an_error(monkeypatch):
     x = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
     with pytest.raises(ImportError, match="not built"):
         tts.rope_kv_append(x, x, x, x, x, x, x, 1)
+
+
+def test_the_projection_with_axes_needs_no_binding(monkeypatch):
+    """As the one without axes: what it refuses without the binding is the tensors, not the call."""
+    import sys
+
+    import torch
+
+    import tiled_top_sparse_gb300 as tts
+    monkeypatch.setattr(tts, "_nat", None)
+    monkeypatch.setitem(sys.modules, "tiled_top_sparse_gb300._native", None)
+    monkeypatch.delattr(tts, "_native", raising=False)
+    x = torch.zeros(3, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="x must be a CUDA tensor"):
+        tts.qkv_rope_axes(x, torch.zeros(3 * 64, 64, dtype=torch.bfloat16), None,
+                          torch.zeros(2, 3, dtype=torch.int32), bytes(32), torch.zeros(9, 32, 2), 1)

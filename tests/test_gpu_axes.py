@@ -259,3 +259,41 @@ def test_vision_behind_what_writes_its_inputs(tts, captured):
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_vision_without_the_binding(tts, monkeypatch):
+    """A machine without Python's C headers has no binding: the projection with axes is made all the same,
+    with its checks, as the one without axes is."""
+    g = torch.Generator("cpu").manual_seed(6)
+    n, hidden, heads, d = 130, 128, 4, 64
+    a = dict(x=torch.randn(n, hidden, generator=g).to(torch.bfloat16).cuda(),
+             w=(torch.randn(3 * heads * d, hidden, generator=g) * 0.1).to(torch.bfloat16).cuda(),
+             bias=torch.randn(3 * heads * d, generator=g).cuda(),
+             positions=torch.randint(0, 64, (2, n), generator=g, dtype=torch.int32).cuda(),
+             pair_axis=tts.rope_axes([8, 24]), cos_sin=tts.rope_cache(64, d), num_heads=heads)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = tts.qkv_rope_axes(**a, status=st)
+
+    def missing():
+        raise ImportError("the native binding is not built")
+
+    monkeypatch.setattr(tts, "_nat", None)
+    monkeypatch.setattr(tts, "_binding", missing)
+    got = tts.qkv_rope_axes(**a, status=st)
+    tts.check_status(st)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    assert all(torch.equal(p, q) for p, q in zip(tts.qkv_rope_axes(**{**a, "bias": None}),
+                                                 tts.qkv_rope_axes(**{**a, "bias": a["bias"] * 0})))
+    z = torch.empty(n, heads, d, device="cuda")
+    for bad in (dict(w=a["w"][:100]), dict(bias=a["bias"][:5]), dict(positions=a["positions"][:, 1:]),
+                dict(positions=a["positions"].long()), dict(positions=a["positions"].cpu()),
+                dict(positions=a["positions"].t()), dict(pair_axis=bytes(33)), dict(pair_axis=[0] * 32),
+                dict(cos_sin=a["cos_sin"][:0]), dict(cos_sin=a["cos_sin"][:, 1:].contiguous()),
+                dict(num_heads=5), dict(num_heads=0), dict(q=z), dict(k=z[1:].bfloat16()),
+                dict(status=st.cpu())):
+        with pytest.raises(ValueError):
+            tts.qkv_rope_axes(**{**a, **bad})
+    with pytest.raises(tts.TTSError):
+        tts.qkv_rope_axes(**{**a, "pair_axis": bytes([2] * 32)})
+    a.update(x=a["x"][:0], positions=a["positions"][:, :0].contiguous())
+    assert tts.qkv_rope_axes(**a)[0].shape == (0, heads, d)

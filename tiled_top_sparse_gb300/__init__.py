@@ -771,8 +771,41 @@ def qkv_rope_axes(x, w, bias, positions, pair_axis, cos_sin, num_heads, q=None, 
     shape = (x.shape[0], int(num_heads), w.shape[0] // (3 * int(num_heads)))
     q, k, v = (torch.empty(shape, dtype=torch.bfloat16, device=x.device) if t is None else t
                for t in (q, k, v))
-    code = (_nat or _binding()).qkv_rope_axes(x, w, bias, positions, pair_axis, cos_sin,
-                                              int(num_heads), q, k, v, status)
+    try:
+        call = (_nat or _binding()).qkv_rope_axes
+    except ImportError:  # no binding: made from here, as qkv_rope is
+        call = _qkv_rope_axes
+    code = call(x, w, bias, positions, pair_axis, cos_sin, int(num_heads), q, k, v, status)
     if code:
         raise TTSError(code, "tts_qkv_rope_axes")
     return q, k, v
+
+
+def _qkv_rope_axes(x, w, bias, positions, pair_axis, cos_sin, heads, q, k, v, status):
+    """The binding's checks and call, on a machine that has none."""
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    for t, name, dtype in ((x, "x", bf16), (w, "w", bf16), (bias, "bias", f32),
+                           (positions, "positions", i32), (cos_sin, "cos_sin", f32), (q, "q", bf16),
+                           (k, "k", bf16), (v, "v", bf16), (status, "status", i32)):
+        if t is None and name in ("bias", "status"):
+            continue
+        _cuda_contig(t, name, dtype)
+        _need(t.device == x.device, f"{name} must be on x's device")
+    n, hidden = x.shape
+    _need(w.shape[0] > 0 and w.shape[0] % (3 * heads) == 0 and w.shape[1] == hidden,
+          "x and w must be [n, hidden] and [3 * num_heads * head_dim, hidden]")
+    d = w.shape[0] // (3 * heads)
+    _need(bias is None or bias.numel() == w.shape[0], "bias must be [3 * num_heads * head_dim]")
+    _need(cos_sin.dim() == 3 and cos_sin.shape[0] > 0 and tuple(cos_sin.shape[1:]) == (d // 2, 2),
+          "cos_sin must be [max_pos, head_dim/2, 2] with a position at least")
+    _need(positions.dim() == 2 and positions.shape[0] > 0 and positions.shape[1] == n,
+          "positions must be [axes, tokens]")
+    _need(isinstance(pair_axis, bytes) and len(pair_axis) == d // 2,
+          "pair_axis must be bytes, one for each of the head_dim/2 pairs")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _need(tuple(t.shape) == (n, heads, d), f"{name} must be [n, num_heads, head_dim]")
+    with torch.cuda.device(x.device):
+        return lib().tts_qkv_rope_axes(
+            _ptr(x), n, hidden, _ptr(w), _ptr(bias), _ptr(positions), positions.shape[0], pair_axis,
+            _ptr(cos_sin), cos_sin.shape[0], heads, d, _ptr(q), _ptr(k), _ptr(v), _ptr(status),
+            _stream(x.device))
