@@ -578,15 +578,17 @@ tts_status tts_attn_decode_paged(const void* q, int64_t total_q, const int32_t* 
  *   new token m (key L - n + m)  iff  bit m is set
  *   key j < L - n                iff  window = 0  or  j > P - window  or  j < sinks
  * A token without a visible key gets out = 0, lse = -inf (padding: an empty mask, in a request
- * that has new tokens only).
+ * that has new tokens only). The window hides no new token, whatever the mask's: a chain's masks are
+ * tts_attn_decode_paged's steps where the window is at least as long as the chain.
  *
  * tree_mask   device uint64 [total_q], 8-byte aligned; bits from n on are not looked at
- * q must be finite. Cached values that some new token sees must be finite; of the keys that none sees, any may hold
- * anything (a drafted token that no mask has, keys hidden by the window, rows behind the
- * last token). With a window, pages of keys from L - n + 1 - window on and of the first `sinks` are
+ * q must be finite. Cached values that some new token sees must be finite; of the keys that none
+ * sees, any may hold anything (a drafted token that no mask has, keys hidden by the window, rows
+ * behind the last token). With a window, pages of keys from L - n + 1 - window on and of the first `sinks` are
  * read. Products: e4m3 keys by q as the sum of two e4m3 values after a power-of-two row scaling (exact
  * within 2^-9 of the row's largest value, to 2^-17 of it below), e4m3 values as fp16 by weights
  * rounded to fp16; bf16 x bf16 for a bf16 cache (weights rounded to bf16); accumulated in fp32.
+ * Zero rows and pages of zeros are as any others (the mean of the values that a row sees).
  * workspace of at least tts_attn_decode_tree_workspace_bytes(...) bytes, as there.
  */
 size_t tts_attn_decode_tree_workspace_bytes(int32_t max_seqlen_q, int32_t num_heads_q,

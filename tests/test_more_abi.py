@@ -294,6 +294,22 @@ def test_chain_masks_are_causal():
         assert (got[base:] == (np.arange(base, 12) <= base + i)).all()
 
 
+def test_chain_masks_are_plain_decoding_where_the_window_holds_the_chain():
+    """In a shorter window plain decoding hides new tokens too, which a mask's bits do not."""
+    import gqa_ref as ref
+    other = 0
+    for n in range(1, 7):
+        for past in range(9):
+            for w in range(1, 10):
+                for s in range(3):
+                    for i in range(n):
+                        same = (ref.visible(past + i, past + n, w, s)
+                                == tree_ref.sees((1 << (i + 1)) - 1, n, past + n, w, s)).all()
+                        assert same or w < n
+                        other += not same
+    assert other > 0
+
+
 def test_masks_of_a_tree():
     assert tree_ref.masks_of([-1, 0, 0, 1]) == [1, 3, 5, 11]
     assert tree_ref.signed(1 << 63) == -(1 << 63) and tree_ref.signed(5) == 5

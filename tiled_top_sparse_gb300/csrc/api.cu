@@ -699,7 +699,9 @@ static tts_status attn_decode(bool tree, const void* q, int64_t total_q,
   if (tiles > 2e9) return TTS_ERR_UNSUPPORTED;
   if (total_q == 0) return TTS_OK;  // nothing to compute
   if (q == nullptr || k_cache == nullptr || v_cache == nullptr || page_tables == nullptr ||
-      kv_lens == nullptr || out == nullptr || (tree && (tree_mask == nullptr || (reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0)))
+      kv_lens == nullptr || out == nullptr)
+    return TTS_ERR_INVALID_ARG;
+  if (tree && (tree_mask == nullptr || (reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0))
     return TTS_ERR_INVALID_ARG;
   if (cache_dtype == TTS_E4M3 && (k_scale == nullptr || v_scale == nullptr))
     return TTS_ERR_INVALID_ARG;

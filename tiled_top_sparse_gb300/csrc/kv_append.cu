@@ -369,9 +369,8 @@ constexpr int kQHeads = 8;  // q heads that share one load of the table row
 // them: 220 to 250 bytes of spills at 48 registers, none at 64 and four blocks per SM (26,800 prompt tokens
 // into e4m3 pages of 64 123 -> 119 us, trees of 25 to 64 tokens 7.9 -> 7.2; pages of one pass 107 -> 112).
 template <int D, bool kF8, int kPasses, int kMost, bool kAxes>
-__global__ void __launch_bounds__(kMost, kMost == 256 ? (kAxes && kPasses == 2 ? 4 : 5) : 2) append_pages_kernel(const KvAppendArgs p,
-                                                           uint64_t q_share, int q_shift,
-                                                           int q_groups) {
+__global__ void __launch_bounds__(kMost, kMost == 256 ? (kAxes && kPasses == 2 ? 4 : 5) : 2)
+    append_pages_kernel(const KvAppendArgs p, uint64_t q_share, int q_shift, int q_groups) {
   constexpr int kTpr = D / 16;
   __shared__ float s_red[16];
   wait_for_prior_grids();
@@ -387,8 +386,9 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? (kAxes && kPasses == 2 ?
     const int hh = (int)(kb % heads);
     int b;
     const Req r = find_request<kAxes>(p, p.page_shift, u, &b, &first);
-    append_page<D, kF8, kPasses, false, kAxes>(p, b, r, (int)(u - first), hh >= p.hkv ? hh - p.hkv : hh,
-                                        hh >= p.hkv, threadIdx.x, blockDim.x, s_red);
+    append_page<D, kF8, kPasses, false, kAxes>(p, b, r, (int)(u - first),
+                                               hh >= p.hkv ? hh - p.hkv : hh, hh >= p.hkv,
+                                               threadIdx.x, blockDim.x, s_red);
     return;
   }
   const int64_t u = qb / (unsigned)q_groups;

@@ -23,15 +23,16 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 // A warp per (request, head, K or V) holds the rows in registers between all reads and the first
 // write: up to 16 pieces of 16 bytes a lane (64 rows of 128 bytes; longer bf16 paths go in two
 // batches, which is safe in order, since a later source lies behind every earlier destination).
-// Lane i looks up rows i and i + 32: lengths, path and tables are three rounds of loads
-// whatever the path's length, and there is no barrier but the warp's.
+// Lane i looks up rows i and i + 32: whatever the path's length, lengths and path are one round of
+// loads, table entries the second, rows (e4m3: the pages' scales, then rows) the last, and there is no
+// barrier but the warp's.
 //
 // e4m3: a page's scale holds for all of its slots. Where the rows moved into a page need a larger
 // one, it becomes the smallest power of two that holds them and every code of the page moves with it.
 //
-// Measured (CUDA graph): 8 requests of e4m3 4.7 us, 256 of bf16 (15 MB read and written) 6.3 us for 2.2 us of
-// bytes at the rate of a copy; the chain of dependent loads (lengths, path, table, rows) is what is
-// left.
+// Measured (CUDA graph): 8 requests of e4m3 4.8 us, 256 of bf16 (15 MB read and written) 6.3 us for 2.2 us of
+// bytes at the rate of a copy; those rounds, each of which waits for the one before, and the launch are
+// what is left.
 struct CompactParams {
   uint8_t* cache[2];  // K, V
   float* scale[2];
@@ -219,8 +220,8 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
 // A block per (new request, head) copies the used rows of a page's K and V, one more per request
 // writes the table row and the length.
 //
-// Bound: HBM for many beams (CUDA graph, 512 of them in bf16, 33 MB read and 33 written: 11.8 us for 9.8 at the rate of a copy),
-// a launch and one chain of loads for few (4 samples in e4m3: 2.3 us).
+// Bound: HBM for many beams (CUDA graph, 512 of them in bf16, 33 MB read and 33 written: 11.8 us for
+// 9.8 at the rate of a copy), a launch and one chain of loads for few (4 samples in e4m3: 2.3 us).
 struct ForkParams {
   uint4* cache[2];
   float* scale[2];  // null: bf16

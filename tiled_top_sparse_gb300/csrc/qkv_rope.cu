@@ -38,8 +38,13 @@
 // kAxes: a token has positions on up to four axes (row, column; time in front of them for video), and
 // every pair's axis chooses the one that it turns by. Only the fetch of a tile's cos/sin rows
 // differs, which runs while the tile's products do: 8547 patches of 1280 into 16 heads of 80 take
-// 57.1 us in a CUDA graph (1.47 PFLOP/s, 0.77 of a large bf16 product's rate), as without axes; 8500 of
-// 512 into 16 heads of 128 106 us (97 without axes; 160 with each pair's turn chosen by itself).
+// 57.1 us in a CUDA graph (1.47 PFLOP/s, 0.77 of a large bf16 product's rate), as without axes.
+//
+// Heads of 128 and 64 with many tokens are bound by the epilogue, far from the products' rate: 8500 of
+// 512 into 16 heads of 128 106 to 115 us (96 to 105 without axes; 160 with each pair's turn chosen by
+// itself) for 27.8 of products; 8500 of 1024 into 16 of 64 50 for 27.8. Staged rows lie 256 or 128
+// bytes apart there (160 for heads of 80), so that the 16-byte stores of a warp's lanes meet in the same
+// banks, four warps do 128 x 256 columns, and heads of 128 read the token's table row again for each head.
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
